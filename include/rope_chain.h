@@ -564,6 +564,220 @@ rc_status rc_qkv_front(const uint16_t *hidden, int32_t M, int32_t D, const uint1
                        uint16_t *cache, int32_t num_blocks, int32_t block_size, float eps,
                        uint16_t *out, uint16_t *raw_out, int32_t *err, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The drafted tokens' step over the caches above: rotary positions in any
+ * layout and scaling, attention of a tree of drafted tokens over the paged
+ * cache, and the adjustment of their logits.  The pages have no counterpart.
+ */
+
+/* Element types of the calls below. */
+typedef enum { RC_BF16 = 1, RC_F32 = 2 } rc_dtype;
+
+/* How the frequencies of a rotary table are scaled for contexts longer than
+   the trained ones. */
+typedef enum {
+    RC_ROPE_SCALE_NONE = 0,
+    RC_ROPE_SCALE_LINEAR = 1,  /* every frequency divided by factor */
+    RC_ROPE_SCALE_BASE = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) */
+    RC_ROPE_SCALE_PARTS = 3    /* frequencies that turn more than beta_fast times
+                                  over original_max_position kept, those that turn
+                                  less than beta_slow times divided by factor, a
+                                  linear ramp over the columns between */
+} rc_rope_scale;
+
+typedef struct {
+    int32_t kind;                   /* rc_rope_scale */
+    double factor;                  /* > 0 (not read with NONE) */
+    double original_max_position;   /* > 0 (PARTS) */
+    double beta_fast, beta_slow;    /* beta_fast > beta_slow > 0 (PARTS) */
+    double attention_factor;        /* multiplies every cos and sin */
+} rc_rope_scaling;
+
+/*
+ * rc_rope_table -- the cos|sin table that the store, the front and
+ * rc_rope_apply read: row p holds attention_factor * cos(p * inv_j) in columns
+ * j < rot_dim/2 and attention_factor * sin(p * inv_j) in rot_dim/2 + j, with
+ * inv_j = theta^(-2j/rot_dim), scaled.  PARTS: with
+ *   d(beta) = rot_dim * ln(original / (2 pi beta)) / (2 ln theta),
+ *   lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), rot_dim - 1),
+ *   ramp_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
+ *   inv_j * (1 - ramp_j) + inv_j / factor * ramp_j.
+ * Angles are reduced exactly (64-bit turns), so the values hold at any
+ * position to FP32 accuracy before their one rounding to `dtype`.
+ *
+ *   out          [max_position, rot_dim] of `dtype` (rc_dtype), contiguous,
+ *                16-byte aligned
+ *   max_position 0 <= max_position < 2^31 (0: nothing launched)
+ *   rot_dim      even, 2 <= rot_dim <= 512
+ *   theta        > 1
+ *   scaling      HOST pointer, or NULL (no scaling, factor 1)
+ */
+rc_status rc_rope_table(void *out, int32_t dtype, int64_t max_position, int32_t rot_dim,
+                        double theta, const rc_rope_scaling *scaling, cudaStream_t stream);
+
+typedef enum {
+    RC_ROPE_PAIRS = 0,    /* elements (2j, 2j+1) turn together (GPT-J) */
+    RC_ROPE_HALVES = 1    /* elements (j, rot_dim/2 + j) */
+} rc_rope_layout;
+
+/*
+ * rc_rope_apply -- rotary positions on any heads: for token t, head h and
+ * pair j of the first rot_dim elements, with c = cos_sin[positions[t], j] and
+ * s = cos_sin[positions[t], rot_dim/2 + j],
+ *   (a, b) -> (fma(a, c, -(b*s)), fma(b, c, a*s))
+ * in FP32, rounded once to the type of x; elements from rot_dim on are
+ * copied.  With `inverse` the transposed rotation ((a, b) -> (a c + b s,
+ * b c - a s)): the gradient with respect to x, given that of the output.
+ * A token whose position lies outside [0, max_position) passes through and
+ * adds one to *err.
+ *
+ *   x, out        `dtype` (rc_dtype) [T, heads, head_dim]: element (t, h, e) at
+ *                 t*row_stride + h*head_stride + e (strides in elements, >= 0,
+ *                 either order of tokens and heads; aligned to the element).
+ *                 out may be x with x's strides (in place), or else must not
+ *                 overlap x; its elements must be distinct
+ *   T, heads      T >= 0, heads >= 1, T*heads < 2^31 (T == 0: nothing launched)
+ *   rot_dim       even, 2 <= rot_dim <= min(head_dim, 512); PAIRS needs an even
+ *                 head_dim, which is at most 65536
+ *   positions     int64 [T], 8-byte aligned
+ *   cos_sin       `table_dtype` [max_position, rot_dim], contiguous, aligned to
+ *                 its element, max_position >= 1
+ *   err           optional device int32 counter
+ * 16-byte aligned pointers, strides, head_dim and rot_dim (half of it in
+ * HALVES) move 16 bytes at a time; anything else element by element.
+ */
+rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int64_t x_head_stride,
+                        int64_t T, int32_t heads, int32_t head_dim, const int64_t *positions,
+                        const void *cos_sin, int32_t table_dtype, int64_t max_position,
+                        int32_t rot_dim, int32_t layout, int32_t inverse, void *out,
+                        int64_t out_row_stride, int64_t out_head_stride, int32_t *err,
+                        cudaStream_t stream);
+
+/*
+ * rc_tree_attention -- attention of drafted tokens over a paged cache that the
+ * calls above fill.  Rows are the drafted tokens (nodes) of `seqs` sequences,
+ * row_start[b] .. row_start[b+1] - 1 those of sequence b (n_b of them, in tree
+ * or generation order).  Sequence b's logical keys are its context_len[b]
+ * cached tokens, then its nodes: node j's K and V are at logical key
+ * context_len[b] + j.  Logical key p lies in block
+ * block_table[b, p / block_size] at offset p % block_size.  Row i of the
+ * sequence sees every context key, and node j where bit j of its mask row is
+ * set (tree_mask NULL: every j <= i; one row: plain decoding).
+ *   out[i, h] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q[i, h].k_p)
+ * over the keys p that row i sees, h's KV head being h / (num_heads /
+ * num_kv_heads).  A row that sees nothing gives 0 (lse -infinity); what a row
+ * does not see never reaches it, be it infinite or NaN.  Scores, running
+ * maximum, sums and outputs are FP32; the weights are rounded to bf16 for the
+ * product with V (tensor cores), the output once to bf16.
+ *
+ *   q            bf16 [rows, num_heads, 64]: element (i, h, e) at
+ *                i*q_row_stride + 64*h + e (e.g. the Q columns of
+ *                rc_qkv_front's output), 16-byte aligned, q_row_stride a
+ *                multiple of 8
+ *   rows         0 <= rows, rows*num_heads < 2^31 (0: nothing launched)
+ *   num_heads    a multiple of num_kv_heads; num_kv_heads >= 1
+ *   row_start    device int32 [seqs + 1], non-decreasing, within [0, rows]
+ *                (values outside are clamped); rows of no sequence are left
+ *   seqs         1 <= seqs < 2^24
+ *   context_len  device int32 [seqs]
+ *   block_table  device int32 [seqs, table_width], row stride table_stride
+ *                elements.  Keys past table_width*block_size are not seen (one
+ *                is added to *err per such sequence), nor are those of a block
+ *                outside [0, num_blocks) (one per block that is needed)
+ *   tree_mask    device uint64 [rows, mask_words], or NULL: bit j%64 of word
+ *                j/64; nodes past the last word are not seen
+ *   cache        bf16 [num_blocks, num_kv_heads, block_size, 128] (K | V),
+ *                16-byte aligned; num_blocks*block_size < 2^31
+ *   scale        > 0, finite (1/8 for 64-wide heads)
+ *   out          bf16 [rows, num_heads, 64], as q with out_row_stride; 16-byte
+ *                aligned; must not overlap q or the cache
+ *   lse          optional FP32 [rows, num_heads]: log of the row's sum of
+ *                exp(scale * q.k), to join results over several caches
+ *   err          optional device int32 counter
+ *   workspace    device scratch, 16-byte aligned, of
+ *                rc_tree_attention_workspace_size() bytes, or NULL: then the
+ *                keys of a sequence's KV head are not split over the GPU
+ *                (slower for few rows over long contexts).  Calls sharing one
+ *                must not overlap on the GPU; its contents need no set-up
+ * Lengths stay on the device and the launches depend on the arguments alone,
+ * so a captured call may be replayed with other lengths.  Results depend on
+ * the arguments, not on timing.
+ */
+rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
+                            int32_t num_kv_heads, const int32_t *row_start, int32_t seqs,
+                            const int32_t *context_len, const int32_t *block_table,
+                            int64_t table_stride, int32_t table_width, const uint64_t *tree_mask,
+                            int32_t mask_words, const uint16_t *cache, int32_t num_blocks,
+                            int32_t block_size, float scale, uint16_t *out, int64_t out_row_stride,
+                            float *lse, int32_t *err, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* Workspace bytes of rc_tree_attention for these sizes on the current device
+   (0 for sizes it refuses). */
+size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_heads,
+                                        int32_t num_kv_heads);
+
+/*
+ * rc_logits_adjust -- penalties for repeated tokens, biases and grammar masks
+ * on the logits of drafted (or single) tokens.  Rows belong to sequences as in
+ * rc_tree_attention.  For row r of sequence b and token t, g counts t among
+ * the sequence's generated history (its history past the first prompt_len[b]
+ * tokens) and among the drafted tokens that the row's node sees (itself as the
+ * mask says; without a mask every node up to its own); `said` is whether t
+ * is in the prompt or g > 0.  In FP32, in this order:
+ *   x = logit;  if said: x = x > 0 ? x / repetition : x * repetition;
+ *   x = x - frequency * g;  if g > 0: x = x - presence;
+ *   x = x + bias of t;  if t is not allowed: x = -infinity
+ * rounded once to `dtype`.
+ *
+ *   logits       `dtype` (rc_dtype) [rows, vocab], row stride row_stride
+ *                elements, aligned to its element
+ *   out          as logits with out_row_stride; may be logits with its stride
+ *                (in place), else must not overlap it
+ *   rows         0 <= rows <= 2^30 (0: nothing launched); rows of no sequence
+ *                are left
+ *   vocab        1 <= vocab <= 2^30;  seqs: 1 .. 65535
+ *   row_start    device int32 [seqs + 1], as in rc_tree_attention
+ * Each of the following may be NULL, for none of it (repetition 1, frequency
+ * and presence 0, everything allowed):
+ *   history      device int32 [history_size], history_start[b] ..
+ *                history_start[b+1] - 1 that of sequence b (device int64
+ *                [seqs + 1]); history_size < 2^28
+ *   prompt_len   device int32 [seqs] (NULL: no prompt, all generated)
+ *   draft_tokens device int32 [rows], with tree_mask as in rc_tree_attention
+ *   repetition, frequency, presence    device FP32 [seqs]
+ *   bias_tokens, bias_values   device int32 and FP32 [bias_size],
+ *                bias_start[b] .. bias_start[b+1] - 1 those of sequence b
+ *                (device int32 [seqs + 1]); a token listed twice takes its last
+ *                entry; bias_size < 2^31
+ *   allowed      device uint32 words [rows, >= ceil(vocab / 32)], row stride
+ *                allowed_stride words: bit t%32 of word t/32 set where t may
+ *                come
+ *   err          device int32 counter: one per token outside [0, vocab) in
+ *                the history, the drafted tokens or the biases of a sequence
+ *                with rows (such tokens count for nothing)
+ */
+typedef struct {
+    const int32_t *history;
+    int64_t history_size;
+    const int64_t *history_start;
+    const int32_t *prompt_len;
+    const int32_t *draft_tokens;
+    const uint64_t *tree_mask;
+    int32_t mask_words;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_start, *bias_tokens;
+    const float *bias_values;
+    int64_t bias_size;
+    const uint32_t *allowed;
+    int64_t allowed_stride;
+} rc_logits_params;
+
+rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride, int64_t rows,
+                           int32_t vocab, const int32_t *row_start, int32_t seqs,
+                           const rc_logits_params *params, void *out, int64_t out_row_stride,
+                           int32_t *err, cudaStream_t stream);
+
 /* rc_device_address -- the address at which the current device reads p:
    p itself for device or managed memory; for page-locked host memory
    mapped into the device's address space (cudaHostAlloc, or

@@ -8,6 +8,9 @@ path: if the library is missing, every call raises.
     normed = context_norms(x, hidden_w, pre_w, L, eps)          # [L, T, 8192]
     kv     = kv_project(normed, W)                              # [L, T, 128*H]
     kv_store_from_projection(kv, H, positions, slots, cos_sin, caches, eps)
+
+and, for the tokens drafted over those caches: rope_table, rope_apply,
+tree_attention and logits_adjust.
 """
 from __future__ import annotations
 
@@ -118,6 +121,43 @@ SIGNATURES["rc_context_kv_chunked_workspace_size"] = ([_c.c_int32, _c.c_int64, _
                                                        _c.c_int32], _c.c_size_t)
 SIGNATURES["rc_context_kv_chunks"] = ([_c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32,
                                        _c.c_int32, _c.c_int32, _c.POINTER(_c.c_int64)], _c.c_int32)
+
+RC_BF16, RC_F32 = 1, 2
+RC_ROPE_PAIRS, RC_ROPE_HALVES = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+class RopeScaling(ctypes.Structure):
+    """rc_rope_scaling: how a rotary table's frequencies are scaled."""
+    _fields_ = [("kind", _c.c_int32), ("factor", _c.c_double), ("original_max_position", _c.c_double),
+                ("beta_fast", _c.c_double), ("beta_slow", _c.c_double),
+                ("attention_factor", _c.c_double)]
+
+
+class LogitsParams(ctypes.Structure):
+    """rc_logits_params: the optional operands of logits_adjust (device
+    pointers)."""
+    _fields_ = [("history", _vp), ("history_size", _c.c_int64), ("history_start", _vp),
+                ("prompt_len", _vp), ("draft_tokens", _vp), ("tree_mask", _vp),
+                ("mask_words", _c.c_int32), ("repetition", _vp), ("frequency", _vp),
+                ("presence", _vp), ("bias_start", _vp), ("bias_tokens", _vp), ("bias_values", _vp),
+                ("bias_size", _c.c_int64), ("allowed", _vp), ("allowed_stride", _c.c_int64)]
+
+
+SIGNATURES["rc_rope_table"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_double,
+                                _c.POINTER(RopeScaling), _vp], _c.c_int)
+SIGNATURES["rc_rope_apply"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32,
+                                _c.c_int32, _vp, _vp, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32,
+                                _c.c_int32, _vp, _c.c_int64, _c.c_int64, _vp, _vp], _c.c_int)
+SIGNATURES["rc_tree_attention"] = ([_vp, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _vp,
+                                    _c.c_int32, _vp, _vp, _c.c_int64, _c.c_int32, _vp, _c.c_int32,
+                                    _vp, _c.c_int32, _c.c_int32, _c.c_float, _vp, _c.c_int64, _vp,
+                                    _vp, _vp, _c.c_size_t, _vp], _c.c_int)
+SIGNATURES["rc_tree_attention_workspace_size"] = ([_c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32],
+                                                  _c.c_size_t)
+SIGNATURES["rc_logits_adjust"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int32, _vp,
+                                   _c.c_int32, _c.POINTER(LogitsParams), _vp, _c.c_int64, _vp, _vp],
+                                  _c.c_int)
 
 
 def lib():
@@ -709,3 +749,216 @@ def read_device_faults(clear: bool = True) -> int:
     f = ctypes.c_uint32(0)
     _check(lib().rc_read_device_faults(ctypes.byref(f), 1 if clear else 0))
     return int(f.value)
+
+
+# ------------------------------------------------- the drafted tokens' step
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return RC_BF16
+    if t.dtype == torch.float32:
+        return RC_F32
+    raise TypeError(f"{name} must be bfloat16 or float32")
+
+
+def _array(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, name: str) -> Optional[int]:
+    """The pointer of a contiguous CUDA array of at least ``numel`` elements
+    (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if t.numel() < numel:
+        raise ValueError(f"{name} needs {numel} elements, it has {t.numel()}")
+    return t.data_ptr()
+
+
+def _err_counter(err: Optional[torch.Tensor]) -> Optional[int]:
+    return _array(err, torch.int32, 1, "err")
+
+
+def rope_table(max_position: int, rot_dim: int = HEAD_DIM, *, theta: float = 10000.0,
+               scaling: str = "none", factor: float = 1.0, original_max_position: float = 1.0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, attention_factor: float = 1.0,
+               dtype: torch.dtype = torch.bfloat16, device=None,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The cos|sin table [max_position, rot_dim] (rc_rope_table): cos in the
+    first rot_dim / 2 columns, sin in the others, both times
+    ``attention_factor``; ``scaling`` "none", "linear", "base" or "parts".  A
+    bfloat16 table of 64 columns is what the store and the QKV front read."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}: one of {sorted(ROPE_SCALINGS)}")
+    if out is None:
+        out = torch.empty((max_position, rot_dim), dtype=dtype,
+                          device=torch.device("cuda") if device is None else device)
+    if tuple(out.shape) != (max_position, rot_dim) or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor [max_position, rot_dim]")
+    sc = RopeScaling(ROPE_SCALINGS[scaling], factor, original_max_position, beta_fast, beta_slow,
+                     attention_factor)
+    _check(lib().rc_rope_table(out.data_ptr(), _dtype(out, "out"), max_position, rot_dim, theta,
+                               ctypes.byref(sc), _stream(stream)))
+    return out
+
+
+def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *,
+               layout: int = RC_ROPE_PAIRS, inverse: bool = False,
+               out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """Rotary positions (rc_rope_apply): x bf16 or float32 [T, heads,
+    head_dim], a view with any strides but a contiguous last axis, turned by
+    the rows ``positions`` (int64 [T]) of ``cos_sin`` [max_position, rot_dim]
+    in the first rot_dim elements of each head; the rest is copied.
+    ``inverse``: the transposed rotation (the gradient with respect to x, given
+    that of the output).  ``out`` may be x (in place)."""
+    T, heads, head_dim = x.shape
+    if out is None:
+        out = torch.empty((T, heads, head_dim), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and dtype of x")
+    if not x.is_cuda or not out.is_cuda or not cos_sin.is_cuda:
+        raise TypeError("x, out and cos_sin must be CUDA tensors")
+    xs, os_ = x.stride(), out.stride()
+    if xs[2] != 1 or os_[2] != 1:
+        raise ValueError("the last axis of x and out must be contiguous")
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous [max_position, rot_dim]")
+    max_position, rot_dim = cos_sin.shape
+    _check(lib().rc_rope_apply(x.data_ptr(), _dtype(x, "x"), xs[0], xs[1], T, heads, head_dim,
+                               _array(positions, torch.int64, T, "positions"), cos_sin.data_ptr(),
+                               _dtype(cos_sin, "cos_sin"), max_position, rot_dim, layout,
+                               1 if inverse else 0, out.data_ptr(), os_[0], os_[1],
+                               _err_counter(err), _stream(stream)))
+    return out
+
+
+def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
+                             device) -> torch.Tensor:
+    """A workspace for tree_attention (rc_tree_attention_workspace_size bytes)."""
+    n = int(lib().rc_tree_attention_workspace_size(rows, seqs, num_heads, num_kv_heads))
+    if n == 0 and rows != 0:
+        raise RopeChainError(RC_ERR_INVALID_ARG, "no workspace size for these sizes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def tree_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.Tensor,
+                   block_table: torch.Tensor, cache: torch.Tensor, *,
+                   tree_mask: Optional[torch.Tensor] = None, scale: float = HEAD_DIM ** -0.5,
+                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   err: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over the paged cache (rc_tree_attention):
+    q bf16 [rows, num_heads, 64] (a view; heads side by side), sequence b's
+    nodes in rows row_start[b] .. row_start[b + 1] (int32 [seqs + 1]), its
+    context_len[b] (int32) cached tokens and then its nodes in the blocks of
+    block_table[b] (int32 [seqs, width]).  ``tree_mask`` int64 [rows, words]:
+    bit j of a row is set where it sees node j of its tree (None: every node up
+    to itself).  ``lse`` float32 [rows, num_heads] receives the log sums.
+    ``workspace``: tree_attention_workspace(); without one the keys are not
+    split over the GPU.  Returns out, bf16 [rows, num_heads, 64]."""
+    rows, heads, width = q.shape
+    if width != HEAD_DIM or q.dtype != torch.bfloat16 or not q.is_cuda:
+        raise ValueError("q must be a CUDA bfloat16 view [rows, num_heads, 64]")
+    if out is None:
+        out = torch.empty((rows, heads, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda:
+        raise ValueError("out must be CUDA bfloat16 of q's shape")
+    qs, os_ = q.stride(), out.stride()
+    if qs[2] != 1 or os_[2] != 1 or (heads > 1 and (qs[1] != HEAD_DIM or os_[1] != HEAD_DIM)):
+        raise ValueError("q and out need strides (*, 64, 1)")
+    if cache.dim() != 4 or cache.shape[3] != 2 * HEAD_DIM:
+        raise ValueError("cache must be [num_blocks, num_kv_heads, block_size, 128]")
+    _bf16(cache, "cache")
+    nb, kv_heads, bs, _ = cache.shape
+    seqs = context_len.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != seqs or block_table.dtype != torch.int32 or \
+            not block_table.is_cuda or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be CUDA int32 [seqs, width] with a contiguous last axis")
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != rows:
+            raise ValueError("tree_mask must be [rows, words]")
+        words = tree_mask.shape[1]
+    if lse is not None and tuple(lse.shape) != (rows, heads):
+        raise ValueError("lse must be [rows, num_heads]")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib().rc_tree_attention(q.data_ptr(), qs[0], rows, heads, kv_heads,
+                                   _array(row_start, torch.int32, seqs + 1, "row_start"), seqs,
+                                   _array(context_len, torch.int32, seqs, "context_len"),
+                                   block_table.data_ptr(), block_table.stride(0),
+                                   block_table.shape[1],
+                                   _array(tree_mask, torch.int64, rows * words, "tree_mask"), words,
+                                   cache.data_ptr(), nb, bs, scale, out.data_ptr(), os_[0],
+                                   _array(lse, torch.float32, rows * heads, "lse"),
+                                   _err_counter(err), ws_ptr, ws_bytes, _stream(stream)))
+    return out
+
+
+def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
+                  history: Optional[torch.Tensor] = None,
+                  history_start: Optional[torch.Tensor] = None,
+                  prompt_len: Optional[torch.Tensor] = None,
+                  draft_tokens: Optional[torch.Tensor] = None,
+                  tree_mask: Optional[torch.Tensor] = None,
+                  repetition: Optional[torch.Tensor] = None,
+                  frequency: Optional[torch.Tensor] = None,
+                  presence: Optional[torch.Tensor] = None,
+                  bias_start: Optional[torch.Tensor] = None,
+                  bias_tokens: Optional[torch.Tensor] = None,
+                  bias_values: Optional[torch.Tensor] = None,
+                  allowed: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties, biases and masks on logits (rc_logits_adjust): logits bf16
+    or float32 [rows, vocab] (a view; contiguous rows), sequence b's rows
+    row_start[b] .. row_start[b + 1] (int32 [seqs + 1]).  history int32 with
+    history_start int64 [seqs + 1], its first prompt_len[b] (int32) tokens the
+    prompt; draft_tokens int32 [rows] and tree_mask int64 [rows, words] as in
+    tree_attention; repetition, frequency, presence float32 [seqs]; bias_start
+    int32 [seqs + 1], bias_tokens int32, bias_values float32; allowed int32
+    bit words [rows, >= ceil(vocab / 32)].  ``out`` may be ``logits``."""
+    rows, vocab = logits.shape
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the shape and dtype of logits")
+    if not logits.is_cuda or not out.is_cuda:
+        raise TypeError("logits and out must be CUDA tensors")
+    if vocab > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+        raise ValueError("rows of logits and out must be contiguous")
+    seqs = row_start.shape[0] - 1
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != rows:
+            raise ValueError("tree_mask must be [rows, words]")
+        words = tree_mask.shape[1]
+    if (history is None) != (history_start is None):
+        raise ValueError("history and history_start go together")
+    if (bias_start is None) != (bias_tokens is None) or (bias_start is None) != (bias_values is None):
+        raise ValueError("bias_start, bias_tokens and bias_values go together")
+    bias_size = 0 if bias_tokens is None else bias_tokens.numel()
+    mask_ptr, mask_stride = None, 0
+    if allowed is not None:
+        if allowed.dtype != torch.int32 or not allowed.is_cuda or allowed.dim() != 2 or \
+                allowed.shape[0] != rows or allowed.shape[1] * 32 < vocab or allowed.stride(1) != 1:
+            raise ValueError("allowed must be CUDA int32 [rows, >= ceil(vocab / 32)], rows contiguous")
+        mask_ptr, mask_stride = allowed.data_ptr(), allowed.stride(0)
+    p = LogitsParams(
+        _array(history, torch.int32, 0, "history"), 0 if history is None else history.numel(),
+        _array(history_start, torch.int64, seqs + 1, "history_start"),
+        _array(prompt_len, torch.int32, seqs, "prompt_len"),
+        _array(draft_tokens, torch.int32, rows, "draft_tokens"),
+        _array(tree_mask, torch.int64, rows * words, "tree_mask"), words,
+        _array(repetition, torch.float32, seqs, "repetition"),
+        _array(frequency, torch.float32, seqs, "frequency"),
+        _array(presence, torch.float32, seqs, "presence"),
+        _array(bias_start, torch.int32, seqs + 1, "bias_start"),
+        _array(bias_tokens, torch.int32, bias_size, "bias_tokens"),
+        _array(bias_values, torch.float32, bias_size, "bias_values"), bias_size, mask_ptr, mask_stride)
+    _check(lib().rc_logits_adjust(logits.data_ptr(), _dtype(logits, "logits"), logits.stride(0), rows,
+                                  vocab, _array(row_start, torch.int32, seqs + 1, "row_start"), seqs,
+                                  ctypes.byref(p), out.data_ptr(), out.stride(0), _err_counter(err),
+                                  _stream(stream)))
+    return out

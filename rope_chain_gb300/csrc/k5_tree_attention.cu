@@ -1,0 +1,645 @@
+// K5: attention of a tree of drafted tokens over the paged context cache.
+//
+// Sequence b has context_len[b] cached tokens and n drafted ones (nodes); the
+// K | V row of context token p is logical key p, that of node j logical key
+// context_len[b] + j, and logical key p lives in block block_table[b, p / bs]
+// at offset p % bs.  Node i sees every context key and the nodes its mask row
+// names (without a mask: j <= i).  With t = scale * q.k in FP32,
+//   out = sum_j exp(t_j - m) v_j / sum_j exp(t_j - m),  m = max_j t_j
+// over the seen keys, in one pass: m, the sum and the output are running
+// values, rescaled when m grows (exponentials are powers of two: the scores
+// carry a factor log2 e).  A row that sees nothing gives zeros.
+//
+// Work split.  The query heads of one KV head and the nodes of one sequence
+// share its keys, so a unit is (sequence, KV head, tile of rows), its rows
+// being (node, query head of the group).  All units' key tiles, laid end to
+// end, are cut into equal ranges, one per CTA, from the lengths on the
+// device: the host needs no lengths, and a single long context fills the GPU
+// as a batch does.  A unit that crosses a cut leaves FP32 partials (output,
+// m, sum) in the workspace, which a second kernel joins in key order (no
+// atomics: the result does not depend on timing).
+#include "rc_internal.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace rc {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kKeyTile = 128;          // keys per step of a CTA
+
+struct Args : TreeAttentionLaunch {
+    float scale_log2;                  // scale * log2 e
+    int32_t min_tiles;                 // fewest key tiles a CTA is given
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- schedule
+
+struct Seq {
+    int32_t r0, n;                     // first row, nodes
+    int32_t ctx, keys;                 // context keys, all keys
+};
+
+__device__ __forceinline__ Seq seq_of(const Args &a, int b) {
+    Seq s;
+    s.r0 = (int32_t)max((int64_t)0, min((int64_t)__ldg(a.row_start + b), a.rows));
+    const int32_t r1 = (int32_t)max((int64_t)s.r0, min((int64_t)__ldg(a.row_start + b + 1), a.rows));
+    s.n = r1 - s.r0;
+    const int64_t ctx = max(__ldg(a.context_len + b), 0);
+    const int64_t room = (int64_t)a.table_width * a.block_size;
+    s.keys = (int32_t)min(ctx + s.n, room);
+    s.ctx = (int32_t)min(ctx, (int64_t)s.keys);
+    return s;
+}
+
+template <int kRows> __device__ __forceinline__ int row_tiles(const Args &a, const Seq &s) {
+    return (s.n * a.group + kRows - 1) / kRows;
+}
+__device__ __forceinline__ int key_tiles(const Seq &s) { return max(1, (s.keys + kKeyTile - 1) / kKeyTile); }
+
+template <int kRows> __device__ __forceinline__ int64_t tiles_of(const Args &a, int b) {
+    const Seq s = seq_of(a, b);
+    return (int64_t)row_tiles<kRows>(a, s) * a.kv_heads * key_tiles(s);
+}
+
+struct Place {
+    int64_t total;                     // key tiles of all units
+    int64_t lo, hi;                    // this CTA's range
+    int32_t b;                         // the sequence of `at`
+    int64_t off;                       // `at` within the sequence's tiles
+};
+
+// The range of CTA c of `ctas`, and where its first tile (or, with kLast, its
+// last one) lies.  Called by all kThreads threads; each takes a run of
+// sequences, and the thread whose run holds the tile walks it.
+template <int kRows, int kThreads, bool kLast>
+__device__ Place locate(const Args &a, int c, int ctas) {
+    __shared__ int64_t warp_sum[kThreads / 32];
+    __shared__ int64_t found_off;
+    __shared__ int32_t found_b;
+    const int per = (a.seqs + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.seqs), b1 = min(b0 + per, a.seqs);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += tiles_of<kRows>(a, b);
+    int64_t run = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o)
+            run += v;
+    }
+    if (lane == 31)
+        warp_sum[warp] = run;
+    __syncthreads();
+    Place p;
+    p.total = 0;
+    int64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp)
+            before += warp_sum[w];
+        p.total += warp_sum[w];
+    }
+    before += run - mine;
+    const int64_t used = max((int64_t)1, min((int64_t)ctas, p.total / a.min_tiles));
+    p.lo = c < used ? p.total * c / used : p.total;
+    p.hi = c < used ? p.total * (c + 1) / used : p.total;
+    p.b = 0;
+    p.off = 0;
+    if (p.lo >= p.hi)
+        return p;                      // uniform
+    const int64_t at = kLast ? p.hi - 1 : p.lo;
+    if (at >= before && at < before + mine) {
+        int64_t off = at - before;
+        int b = b0;
+        for (int64_t t; off >= (t = tiles_of<kRows>(a, b)); ++b)
+            off -= t;
+        found_b = b;
+        found_off = off;
+    }
+    __syncthreads();
+    p.b = found_b;
+    p.off = found_off;
+    return p;
+}
+
+// Where a unit's partial lies: per CTA one slot for the unit that an earlier
+// CTA began and one for a unit that it begins and a later CTA ends.
+template <int kRows> constexpr int kSlotFloats = kRows * (kHeadDim + 2) + 4;
+template <int kRows> __device__ __forceinline__ float *slot_of(const Args &a, int64_t slot) {
+    return a.partial + slot * kSlotFloats<kRows>;
+}
+
+__device__ __forceinline__ bool sees(const Args &a, const Seq &s, int i, int j) {
+    if (a.tree_mask == nullptr)
+        return j <= i;
+    return (j >> 6) < a.mask_words &&
+           ((__ldg(a.tree_mask + (int64_t)(s.r0 + i) * a.mask_words + (j >> 6)) >> (j & 63)) & 1u) != 0u;
+}
+
+// Element offset of logical key p's row in the cache, -1 without a valid block.
+__device__ __forceinline__ int64_t key_offset(const Args &a, int b, int h, int p) {
+    const uint32_t bs = (uint32_t)a.block_size, page = (uint32_t)p / bs;
+    const int32_t blk = __ldg(a.block_table + b * a.table_stride + page);
+    if (blk < 0 || blk >= a.num_blocks)
+        return -1;
+    return (((int64_t)blk * a.kv_heads + h) * bs + ((uint32_t)p - page * bs)) * (2 * kHeadDim);
+}
+
+// A drafted V row that is infinite or NaN must not reach rows that do not see
+// it (0 * inf in the matrix product), so the products take zeros in its place
+// and the rows that see it get it added here.  Rare: only where the flag of a
+// unit is set.
+__device__ __noinline__ float add_unfinite(const Args &a, const Seq &s, int b, int h, int i, int d, float x) {
+    for (int j = 0; j < min(s.n, s.keys - s.ctx); ++j) {
+        if (!sees(a, s, i, j))
+            continue;
+        const int64_t o = key_offset(a, b, h, s.ctx + j);
+        const uint32_t v = o < 0 ? 0u : (uint32_t)a.cache[o + kHeadDim + d] << 16;
+        if ((v & 0x7F800000u) == 0x7F800000u)
+            x += __uint_as_float(v);
+    }
+    return x;
+}
+
+// ------------------------------------------------- few rows: mma.sync tiles
+//
+// Up to 32 rows share a key (one drafted token of a group of 8, a small
+// tree): the kernel is bound by reading the cache, each K | V row of 256
+// bytes once.  Every warp of a CTA streams its own 16 of a tile's 128 keys
+// through its own ring of cp.async stages, with its own running maximum,
+// sum and output, so the warps never wait for one another until the unit's
+// end, where they are joined in shared memory.  Products are m16n8k16: rows x
+// keys for the scores, whose accumulator layout is the operand layout of the
+// second product, so the weights stay in registers (rounded to bf16 there,
+// which the tensor cores require; the sum takes them unrounded).
+
+constexpr int kWarps = 8, kSmallThreads = 32 * kWarps;
+constexpr int kChunk = 16;                                   // keys per warp and step
+constexpr uint32_t kChunkBytes = kChunk * 2 * kHeadDim * 2;  // 4 KiB
+
+template <int kTiles> constexpr int kRing = kTiles == 1 ? 3 : 5;
+// The rings; at a unit's end they hold the warps' outputs (32 KiB per row tile).
+template <int kTiles> constexpr uint32_t kSmallSmem = kWarps * kRing<kTiles> * kChunkBytes;
+
+__device__ __forceinline__ uint32_t smem_at(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void load4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void load4_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Zeros in place of infinite and NaN halves of a register of V whose two keys
+// are drafted ones (lo, hi); true if there was one.
+__device__ __forceinline__ bool finite_only(uint32_t &w, bool lo, bool hi) {
+    const bool x = lo && (w & 0x00007F80u) == 0x00007F80u, y = hi && (w & 0x7F800000u) == 0x7F800000u;
+    if (x)
+        w &= 0xFFFF0000u;
+    if (y)
+        w &= 0x0000FFFFu;
+    return x || y;
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(kSmallThreads, kTiles == 1 ? 2 : 1)
+k5_small(const __grid_constant__ Args a)
+{
+    constexpr int kRows = 16 * kTiles, kStages = kRing<kTiles>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_max[kWarps][kRows], s_sum[kWarps][kRows];
+    __shared__ uint32_t s_real[kWarps][kStages];       // which of a chunk's keys exist
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t ring = smem_at(smem) + (uint32_t)warp * (kStages * kChunkBytes);
+    pdl_trigger();
+    pdl_wait();
+
+    Place at = locate<kRows, kSmallThreads, false>(a, blockIdx.x, gridDim.x);
+    int64_t pos = at.lo, off = at.off;
+    int b = at.b;
+    while (pos < at.hi) {
+        const Seq s = seq_of(a, b);
+        const int kt = key_tiles(s), rt = row_tiles<kRows>(a, s);
+        const int64_t seq_tiles = (int64_t)rt * a.kv_heads * kt;
+        if (off >= seq_tiles) {                         // the next sequence with rows
+            off -= seq_tiles;
+            ++b;
+            continue;
+        }
+        const int unit = (int)(off / kt), k0 = (int)(off - (int64_t)unit * kt);
+        const int h = unit / rt, tile = unit - h * rt;
+        int count = (int)min((int64_t)(kt - k0), at.hi - pos);
+        const bool split_ok = a.partial != nullptr;
+        if (!split_ok) {
+            // without a workspace a unit belongs to the CTA of its first tile
+            if (k0 != 0) {
+                pos += count;
+                off += count;
+                continue;
+            }
+            count = kt;
+        }
+
+        // this thread's rows: lane / 4 and lane / 4 + 8 of each row tile
+        int node[kTiles][2];
+        uint32_t qf[kTiles][4][4];
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+            const uint32_t *src[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = tile * kRows + m * 16 + 8 * e + (lane >> 2);
+                const int i = r / a.group;
+                node[m][e] = i < s.n ? i : -1;
+                src[e] = reinterpret_cast<const uint32_t *>(
+                    a.q + (int64_t)(s.r0 + i) * a.q_row_stride + (h * a.group + r - i * a.group) * kHeadDim);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    qf[m][k][e] = node[m][e & 1] >= 0 ? __ldg(src[e & 1] + 8 * k + (lane & 3) + 4 * (e >> 1)) : 0u;
+            }
+        }
+        float o[kTiles][8][4], top[kTiles][2], sum[kTiles][2];
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[m][e] = -INFINITY;
+                sum[m][e] = 0.0f;
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[m][n][e] = 0.0f;
+        }
+        bool unfinite = false;
+
+        auto issue = [&](int j) {
+            const int st = j % kStages;
+            const int p = (k0 + j) * kKeyTile + warp * kChunk + (lane & 15);
+            int64_t src = -1;
+            if (p < s.keys) {
+                src = key_offset(a, b, h, p);
+                if (src < 0 && lane < 16 && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
+                    atomicAdd(a.err, 1);               // once per block: at its first key
+            }
+            const uint32_t real = __ballot_sync(0xFFFFFFFFu, src >= 0) & 0xFFFFu;
+            if (lane == 0)
+                s_real[warp][st] = real;
+#pragma unroll
+            for (int i = 0; i < kChunk / 2; ++i) {
+                const int row = 2 * i + (lane >> 4), c = lane & 15;
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, src, row);
+                copy16(ring + st * kChunkBytes + (c >> 3) * (kChunkBytes / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                       a.cache + (from >= 0 ? from + 8 * c : 0), from >= 0);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kStages - 1; ++j) {
+            if (j < count)
+                issue(j);
+            copy_commit();
+        }
+        for (int j = 0; j < count; ++j) {
+            copy_wait<kStages - 2>();
+            __syncwarp();
+            if (j + kStages - 1 < count)
+                issue(j + kStages - 1);
+            copy_commit();
+            const uint32_t k_at = ring + (j % kStages) * kChunkBytes, v_at = k_at + kChunkBytes / 2;
+            const int p0 = (k0 + j) * kKeyTile + warp * kChunk;
+            const uint32_t real = s_real[warp][j % kStages];
+            const bool drafted = p0 + kChunk > s.ctx;
+            float t[kTiles][2][4];
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        t[m][n][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t kf[4];
+                const int row = (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
+                load4(kf, k_at + row * 128 + ((c ^ (row & 7)) << 4));
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m) {
+                    mma16816(t[m][0], qf[m][k], kf[0], kf[1]);
+                    mma16816(t[m][1], qf[m][k], kf[2], kf[3]);
+                }
+            }
+            if (real != 0xFFFFu || drafted) {
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int in = 8 * n + 2 * (lane & 3) + (e & 1), i = node[m][e >> 1];
+                            const int p = p0 + in;
+                            if (!((real >> in) & 1u) || (p >= s.ctx && (i < 0 || !sees(a, s, i, p - s.ctx))))
+                                t[m][n][e] = -INFINITY;
+                        }
+            }
+            uint32_t pf[kTiles][4];
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(fmaxf(t[m][0][2 * e], t[m][0][2 * e + 1]),
+                                    fmaxf(t[m][1][2 * e], t[m][1][2 * e + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                    const float now = fmaxf(top[m][e], x * a.scale_log2);
+                    const float ref = now == -INFINITY ? 0.0f : now;
+                    const float shrink = ex2(top[m][e] - ref);
+                    top[m][e] = now;
+                    float part = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            float &w = t[m][n][2 * e + f];
+                            w = ex2(__fmaf_rn(w, a.scale_log2, -ref));
+                            part += w;
+                        }
+                    sum[m][e] = __fmaf_rn(sum[m][e], shrink, part);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        o[m][n][2 * e] *= shrink;
+                        o[m][n][2 * e + 1] *= shrink;
+                    }
+                }
+                pf[m][0] = pack_bf16x2(t[m][0][0], t[m][0][1]);
+                pf[m][1] = pack_bf16x2(t[m][0][2], t[m][0][3]);
+                pf[m][2] = pack_bf16x2(t[m][1][0], t[m][1][1]);
+                pf[m][3] = pack_bf16x2(t[m][1][2], t[m][1][3]);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; n += 2) {
+                uint32_t vf[4];
+                const int row = ((lane >> 3) & 1) * 8 + (lane & 7), c = n + (lane >> 4);
+                load4_t(vf, v_at + row * 128 + ((c ^ (row & 7)) << 4));
+                if (drafted) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int p = p0 + 8 * (q & 1) + 2 * (lane & 3);
+                        unfinite |= finite_only(vf[q], p >= s.ctx, p + 1 >= s.ctx);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m) {
+                    mma16816(o[m][n], pf[m], vf[0], vf[1]);
+                    mma16816(o[m][n + 1], pf[m], vf[2], vf[3]);
+                }
+            }
+            __syncwarp();
+        }
+        copy_wait<0>();
+
+        // The warps' parts, joined.
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = sum[m][e];
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+                if ((lane & 3) == 0) {
+                    const int r = m * 16 + 8 * e + (lane >> 2);
+                    s_max[warp][r] = top[m][e];
+                    s_sum[warp][r] = x;
+                }
+            }
+        unfinite = __syncthreads_or(unfinite) != 0;     // also: every ring is drained
+        float *outs = reinterpret_cast<float *>(smem) + warp * (16 * kHeadDim);
+        const bool whole = k0 == 0 && count == kt;
+        float *slot = whole ? nullptr : slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0));
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * e + (lane >> 2);
+                float now = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    now = fmaxf(now, s_max[w][m * 16 + r]);
+                const float f = ex2(top[m][e] - (now == -INFINITY ? 0.0f : now));
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    // two columns of row r; the column pairs of odd rows are
+                    // turned so that a warp's stores spread over the banks
+                    const int col = (8 * n + 2 * (lane & 3)) ^ ((r & 3) << 3);
+                    *reinterpret_cast<float2 *>(outs + r * kHeadDim + col) =
+                        make_float2(o[m][n][2 * e] * f, o[m][n][2 * e + 1] * f);
+                }
+            }
+            __syncthreads();
+            // 16 rows of 64: thread -> row threadIdx / 16, four columns
+            const int r = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float now = -INFINITY, total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                now = fmaxf(now, s_max[w][m * 16 + r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem) + w * (16 * kHeadDim) + r * kHeadDim + (col ^ ((r & 3) << 3)));
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+                total = __fmaf_rn(s_sum[w][m * 16 + r], ex2(s_max[w][m * 16 + r] - (now == -INFINITY ? 0.0f : now)), total);
+            }
+            const int row = tile * kRows + m * 16 + r, i = row / a.group;
+            if (!whole) {
+                *reinterpret_cast<float4 *>(slot + 4 + (m * 16 + r) * kHeadDim + col) = x;
+                if (col == 0) {
+                    slot[4 + kRows * kHeadDim + m * 16 + r] = now;
+                    slot[4 + kRows * (kHeadDim + 1) + m * 16 + r] = total;
+                }
+                if (threadIdx.x == 0 && m == 0)
+                    slot[0] = unfinite ? 1.0f : 0.0f;
+            } else if (i < s.n) {
+                const int head = h * a.group + row - i * a.group;
+                if (unfinite) {
+                    x.x = add_unfinite(a, s, b, h, i, col, x.x);
+                    x.y = add_unfinite(a, s, b, h, i, col + 1, x.y);
+                    x.z = add_unfinite(a, s, b, h, i, col + 2, x.z);
+                    x.w = add_unfinite(a, s, b, h, i, col + 3, x.w);
+                }
+                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+                *reinterpret_cast<uint2 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col) =
+                    make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+                if (col == 0 && a.lse != nullptr)
+                    a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
+                        total == 0.0f ? -INFINITY : __fmaf_rn(now, kLn2, logf(total));
+                if (threadIdx.x == 0 && m == 0 && unit == 0 && s.n > 0 && a.err != nullptr &&
+                    (int64_t)max(__ldg(a.context_len + b), 0) + s.n > s.keys)
+                    atomicAdd(a.err, 1);
+            }
+            __syncthreads();
+        }
+        pos += count;
+        off += count;
+    }
+}
+
+// ----------------------------------------------------------- joining parts
+//
+// Block c joins the unit that CTA c began and did not end: its own part and
+// those of the CTAs after it, in key order.
+constexpr int kJoinThreads = 256;
+
+template <int kRows>
+__global__ void __launch_bounds__(kJoinThreads)
+k5_join(const __grid_constant__ Args a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int c = blockIdx.x;
+    const Place p = locate<kRows, kJoinThreads, true>(a, c, gridDim.x);
+    if (p.lo >= p.hi)
+        return;
+    const Seq s = seq_of(a, p.b);
+    const int kt = key_tiles(s), rt = row_tiles<kRows>(a, s);
+    const int unit = (int)(p.off / kt), k = (int)(p.off - (int64_t)unit * kt);   // the range's last tile
+    const int64_t begin = p.hi - 1 - k, end = begin + kt;
+    if (begin < p.lo || end <= p.hi)
+        return;                                         // begun earlier, or ended here
+    const int64_t used = max((int64_t)1, min((int64_t)gridDim.x, p.total / a.min_tiles));
+    int last = c + 1;
+    while (last + 1 < used && p.total * (last + 1) / used < end)
+        ++last;
+    const int h = unit / rt, tile = unit - h * rt;
+    const float *own = slot_of<kRows>(a, 2 * (int64_t)c + 1);
+    bool unfinite = own[0] != 0.0f;
+    for (int d = c + 1; d <= last; ++d)
+        unfinite |= slot_of<kRows>(a, 2 * (int64_t)d)[0] != 0.0f;
+    for (int r = threadIdx.x >> 4; r < kRows; r += kJoinThreads / 16) {
+        const int row = tile * kRows + r, i = row / a.group;
+        if (i >= s.n)
+            continue;
+        const int col = (threadIdx.x & 15) * 4;
+        float now = own[4 + kRows * kHeadDim + r];
+        for (int d = c + 1; d <= last; ++d)
+            now = fmaxf(now, slot_of<kRows>(a, 2 * (int64_t)d)[4 + kRows * kHeadDim + r]);
+        const float ref = now == -INFINITY ? 0.0f : now;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float total = 0.0f;
+        for (int d = c; d <= last; ++d) {
+            const float *part = d == c ? own : slot_of<kRows>(a, 2 * (int64_t)d);
+            const float f = ex2(part[4 + kRows * kHeadDim + r] - ref);
+            const float4 y = *reinterpret_cast<const float4 *>(part + 4 + r * kHeadDim + col);
+            x.x = __fmaf_rn(y.x, f, x.x);
+            x.y = __fmaf_rn(y.y, f, x.y);
+            x.z = __fmaf_rn(y.z, f, x.z);
+            x.w = __fmaf_rn(y.w, f, x.w);
+            total = __fmaf_rn(part[4 + kRows * (kHeadDim + 1) + r], f, total);
+        }
+        const int head = h * a.group + row - i * a.group;
+        if (unfinite) {
+            x.x = add_unfinite(a, s, p.b, h, i, col, x.x);
+            x.y = add_unfinite(a, s, p.b, h, i, col + 1, x.y);
+            x.z = add_unfinite(a, s, p.b, h, i, col + 2, x.z);
+            x.w = add_unfinite(a, s, p.b, h, i, col + 3, x.w);
+        }
+        const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+        *reinterpret_cast<uint2 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col) =
+            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+        if (col == 0 && a.lse != nullptr)
+            a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
+                total == 0.0f ? -INFINITY : __fmaf_rn(now, kLn2, logf(total));
+    }
+    if (threadIdx.x == 0 && unit == 0 && a.err != nullptr &&
+        (int64_t)max(__ldg(a.context_len + p.b), 0) + s.n > s.keys)
+        atomicAdd(a.err, 1);
+}
+
+// Row tile of a call: 16 rows while the average unit fits them, else 32.
+int tiles_for(int64_t rows, int32_t seqs, int32_t group) {
+    const int64_t mean = (rows + seqs - 1) / seqs * group;
+    return mean <= 16 ? 1 : 2;
+}
+
+int ctas_for(int tiles, int num_sms) { return tiles == 1 ? 2 * num_sms : num_sms; }
+
+template <int kTiles>
+cudaError_t launch_small(const Args &a, int num_sms, cudaStream_t stream, const char **why)
+{
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(k5_small<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmallSmem<kTiles>);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            configured[dev] = true;
+    }
+    const int ctas = ctas_for(kTiles, num_sms);
+    *why = "tree attention launch";
+    e = launch_pdl(k5_small<kTiles>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
+    if (e != cudaSuccess || a.partial == nullptr)
+        return e;
+    *why = "tree attention join launch";
+    return launch_pdl(k5_join<16 * kTiles>, dim3((unsigned)ctas), dim3(kJoinThreads), 0, stream, 1, a);
+}
+
+}  // namespace
+
+size_t tree_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms)
+{
+    const int tiles = tiles_for(rows, seqs, group);
+    const size_t slot = tiles == 1 ? kSlotFloats<16> : kSlotFloats<32>;
+    return 2 * (size_t)ctas_for(tiles, num_sms) * slot * sizeof(float);
+}
+
+cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cudaStream_t stream,
+                                  const char **why)
+{
+    Args a{};
+    static_cast<TreeAttentionLaunch &>(a) = p;
+    a.scale_log2 = p.scale * kLog2e;
+    a.min_tiles = 4;
+    return tiles_for(p.rows, p.seqs, p.group) == 1 ? launch_small<1>(a, num_sms, stream, why)
+                                                   : launch_small<2>(a, num_sms, stream, why);
+}
+
+}  // namespace rc
