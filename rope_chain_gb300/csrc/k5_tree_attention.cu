@@ -71,16 +71,15 @@ template <int kRows> __device__ __forceinline__ int64_t tiles_of(const Args &a, 
 }
 
 struct Place {
-    int64_t total;                     // key tiles of all units
+    int64_t total, used;               // key tiles of all units; CTAs that have some
     int64_t lo, hi;                    // this CTA's range
     int32_t b;                         // the sequence of `at`
     int64_t off;                       // `at` within the sequence's tiles
 };
 
-// The range of CTA c of `ctas`, and where its first tile (or, with kLast, its
-// last one) lies.  Called by all kThreads threads; each takes a run of
+// The range of CTA c of `ctas`, and where its first tile lies.  Called by all kThreads threads; each takes a run of
 // sequences, and the thread whose run holds the tile walks it.
-template <int kRows, int kThreads, bool kLast>
+template <int kRows, int kThreads>
 __device__ Place locate(const Args &a, int c, int ctas) {
     __shared__ int64_t warp_sum[kThreads / 32];
     __shared__ int64_t found_off;
@@ -111,16 +110,15 @@ __device__ Place locate(const Args &a, int c, int ctas) {
         p.total += warp_sum[w];
     }
     before += run - mine;
-    const int64_t used = max((int64_t)1, min((int64_t)ctas, p.total / a.min_tiles));
-    p.lo = c < used ? p.total * c / used : p.total;
-    p.hi = c < used ? p.total * (c + 1) / used : p.total;
+    p.used = max((int64_t)1, min((int64_t)ctas, p.total / a.min_tiles));
+    p.lo = c < p.used ? p.total * c / p.used : p.total;
+    p.hi = c < p.used ? p.total * (c + 1) / p.used : p.total;
     p.b = 0;
     p.off = 0;
     if (p.lo >= p.hi)
         return p;                      // uniform
-    const int64_t at = kLast ? p.hi - 1 : p.lo;
-    if (at >= before && at < before + mine) {
-        int64_t off = at - before;
+    if (p.lo >= before && p.lo < before + mine) {
+        int64_t off = p.lo - before;
         int b = b0;
         for (int64_t t; off >= (t = tiles_of<kRows>(a, b)); ++b)
             off -= t;
@@ -133,12 +131,23 @@ __device__ Place locate(const Args &a, int c, int ctas) {
     return p;
 }
 
-// Where a unit's partial lies: per CTA one slot for the unit that an earlier
-// CTA began and one for a unit that it begins and a later CTA ends.
-template <int kRows> constexpr int kSlotFloats = kRows * (kHeadDim + 2) + 4;
+// A partial: a header, then kRows x 64 outputs (not divided by the sum), kRows
+// maxima and kRows sums.  Each CTA has two: slot 2c for the unit that an
+// earlier CTA began, slot 2c + 1 for one that it begins and a later CTA ends,
+// whose header names the unit and its last CTA (or says that there is none).
+struct Header {
+    int32_t last;                      // slot 2c + 1: last CTA of the unit, 0 without a unit
+    int32_t b, unit;
+    int32_t unfinite;
+};
+constexpr int kHeaderFloats = sizeof(Header) / sizeof(float);
+template <int kRows> constexpr int kSlotFloats = kHeaderFloats + kRows * (kHeadDim + 2);
 template <int kRows> __device__ __forceinline__ float *slot_of(const Args &a, int64_t slot) {
     return a.partial + slot * kSlotFloats<kRows>;
 }
+template <int kRows> constexpr int kSlotOut = kHeaderFloats;
+template <int kRows> constexpr int kSlotMax = kSlotOut<kRows> + kRows * kHeadDim;
+template <int kRows> constexpr int kSlotSum = kSlotMax<kRows> + kRows;
 
 __device__ __forceinline__ bool sees(const Args &a, const Seq &s, int i, int j) {
     if (a.tree_mask == nullptr)
@@ -154,6 +163,23 @@ __device__ __forceinline__ int64_t key_offset(const Args &a, int b, int h, int p
     if (blk < 0 || blk >= a.num_blocks)
         return -1;
     return (((int64_t)blk * a.kv_heads + h) * bs + ((uint32_t)p - page * bs)) * (2 * kHeadDim);
+}
+
+// The header of this CTA's part of a split unit: key tiles from k0 of kt, its
+// first tile at `begin` of all units' tiles laid end to end.
+template <int kRows>
+__device__ void write_header(const Args &a, const Place &p, int k0, int kt, int64_t begin, int b, int unit,
+                             bool unfinite) {
+    Header h{0, b, unit, unfinite ? 1 : 0};
+    if (k0 == 0) {
+        int64_t last = (begin + kt - 1) * p.used / p.total;      // its range holds the unit's last tile
+        while (p.total * (last + 1) / p.used < begin + kt)
+            ++last;
+        while (p.total * last / p.used >= begin + kt)
+            --last;
+        h.last = (int32_t)last;
+    }
+    *reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0))) = h;
 }
 
 // A drafted V row that is infinite or NaN must not reach rows that do not see
@@ -199,6 +225,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void copy16_real(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
@@ -242,7 +271,9 @@ k5_small(const __grid_constant__ Args a)
     pdl_trigger();
     pdl_wait();
 
-    Place at = locate<kRows, kSmallThreads, false>(a, blockIdx.x, gridDim.x);
+    const Place at = locate<kRows, kSmallThreads>(a, blockIdx.x, gridDim.x);
+    if (a.partial != nullptr && threadIdx.x == 0)
+        reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
     int64_t pos = at.lo, off = at.off;
     int b = at.b;
     while (pos < at.hi) {
@@ -305,25 +336,42 @@ k5_small(const __grid_constant__ Args a)
         }
         bool unfinite = false;
 
+        // Chunk j's key of this lane: its row's offset in the cache, -1 for
+        // none.  Looked up one chunk before the copies that use it.
+        auto look_up = [&](int j) -> int64_t {
+            const int p = (k0 + j) * kKeyTile + warp * kChunk + (lane & 15);
+            if (j >= count || p >= s.keys)
+                return -1;
+            const int64_t src = key_offset(a, b, h, p);
+            if (src < 0 && lane < 16 && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
+                atomicAdd(a.err, 1);                   // once per block: at its first key
+            return src;
+        };
+        int64_t from = look_up(0);
         auto issue = [&](int j) {
             const int st = j % kStages;
-            const int p = (k0 + j) * kKeyTile + warp * kChunk + (lane & 15);
-            int64_t src = -1;
-            if (p < s.keys) {
-                src = key_offset(a, b, h, p);
-                if (src < 0 && lane < 16 && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
-                    atomicAdd(a.err, 1);               // once per block: at its first key
-            }
-            const uint32_t real = __ballot_sync(0xFFFFFFFFu, src >= 0) & 0xFFFFu;
+            const uint32_t real = __ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu;
+            const int64_t first = __shfl_sync(0xFFFFFFFFu, from, 0);
+            // a chunk in one block is 4 KiB in a row (any block size where it
+            // happens to be; always with blocks of a multiple of 16)
+            const bool run = __all_sync(0xFFFFFFFFu, from == first + (lane & 15) * (2 * kHeadDim)) && first >= 0;
             if (lane == 0)
                 s_real[warp][st] = real;
+            const uint32_t at = ring + st * kChunkBytes + ((lane >> 3) & 1) * (kChunkBytes / 2) + (lane >> 4) * 128;
+            if (run) {
+                const uint16_t *src = a.cache + first + 8 * lane;
 #pragma unroll
-            for (int i = 0; i < kChunk / 2; ++i) {
-                const int row = 2 * i + (lane >> 4), c = lane & 15;
-                const int64_t from = __shfl_sync(0xFFFFFFFFu, src, row);
-                copy16(ring + st * kChunkBytes + (c >> 3) * (kChunkBytes / 2) + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                       a.cache + (from >= 0 ? from + 8 * c : 0), from >= 0);
+                for (int i = 0; i < kChunk / 2; ++i)
+                    copy16_real(at + i * 256 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) << 4), src + i * (4 * kHeadDim));
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk / 2; ++i) {
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, from, 2 * i + (lane >> 4));
+                    copy16(at + i * 256 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) << 4),
+                           a.cache + (row >= 0 ? row + 8 * (lane & 15) : 0), row >= 0);
+                }
             }
+            from = look_up(j + 1);
         };
 #pragma unroll
         for (int j = 0; j < kStages - 1; ++j) {
@@ -374,33 +422,49 @@ k5_small(const __grid_constant__ Args a)
                         }
             }
             uint32_t pf[kTiles][4];
+            float now[kTiles][2];
+            bool grew = false;
 #pragma unroll
-            for (int m = 0; m < kTiles; ++m) {
+            for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float x = fmaxf(fmaxf(t[m][0][2 * e], t[m][0][2 * e + 1]),
                                     fmaxf(t[m][1][2 * e], t[m][1][2 * e + 1]));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    const float now = fmaxf(top[m][e], x * a.scale_log2);
-                    const float ref = now == -INFINITY ? 0.0f : now;
-                    const float shrink = ex2(top[m][e] - ref);
-                    top[m][e] = now;
+                    now[m][e] = fmaxf(top[m][e], x * a.scale_log2);
+                    grew |= now[m][e] > top[m][e];
+                }
+            if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+                for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float shrink = now[m][e] == -INFINITY ? 1.0f : ex2(top[m][e] - now[m][e]);
+                        top[m][e] = now[m][e];
+                        sum[m][e] *= shrink;
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            o[m][n][2 * e] *= shrink;
+                            o[m][n][2 * e + 1] *= shrink;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = top[m][e] == -INFINITY ? 0.0f : -top[m][e];
                     float part = 0.0f;
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
                             float &w = t[m][n][2 * e + f];
-                            w = ex2(__fmaf_rn(w, a.scale_log2, -ref));
+                            w = ex2(__fmaf_rn(w, a.scale_log2, ref));
                             part += w;
                         }
-                    sum[m][e] = __fmaf_rn(sum[m][e], shrink, part);
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        o[m][n][2 * e] *= shrink;
-                        o[m][n][2 * e + 1] *= shrink;
-                    }
+                    sum[m][e] += part;
                 }
                 pf[m][0] = pack_bf16x2(t[m][0][0], t[m][0][1]);
                 pf[m][1] = pack_bf16x2(t[m][0][2], t[m][0][3]);
@@ -486,13 +550,13 @@ k5_small(const __grid_constant__ Args a)
             }
             const int row = tile * kRows + m * 16 + r, i = row / a.group;
             if (!whole) {
-                *reinterpret_cast<float4 *>(slot + 4 + (m * 16 + r) * kHeadDim + col) = x;
+                *reinterpret_cast<float4 *>(slot + kSlotOut<kRows> + (m * 16 + r) * kHeadDim + col) = x;
                 if (col == 0) {
-                    slot[4 + kRows * kHeadDim + m * 16 + r] = now;
-                    slot[4 + kRows * (kHeadDim + 1) + m * 16 + r] = total;
+                    slot[kSlotMax<kRows> + m * 16 + r] = now;
+                    slot[kSlotSum<kRows> + m * 16 + r] = total;
                 }
                 if (threadIdx.x == 0 && m == 0)
-                    slot[0] = unfinite ? 1.0f : 0.0f;
+                    write_header<kRows>(a, at, k0, kt, pos - k0, b, unit, unfinite);
             } else if (i < s.n) {
                 const int head = h * a.group + row - i * a.group;
                 if (unfinite) {
@@ -520,73 +584,120 @@ k5_small(const __grid_constant__ Args a)
 
 // ----------------------------------------------------------- joining parts
 //
-// Block c joins the unit that CTA c began and did not end: its own part and
-// those of the CTAs after it, in key order.
-constexpr int kJoinThreads = 256;
+// Block (c, y) joins kJoinRows rows of the unit that CTA c began and did not
+// end: its own part and those of the CTAs after it, in key order.  The parts'
+// weights are made first, one per thread, then four groups of 64 threads (16
+// columns of four, four rows) add every fourth part each, and the groups are
+// added in order.
+constexpr int kJoinThreads = 256, kJoinRows = 4, kJoinParts = 512;
 
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads)
 k5_join(const __grid_constant__ Args a)
 {
+    __shared__ float s_part[kJoinParts][kJoinRows];        // the part's maximum, then its weight
+    __shared__ float s_sum[kJoinParts][kJoinRows];
+    __shared__ float4 s_out[3][64];
+    __shared__ float s_top[kJoinRows], s_total[kJoinRows];
     pdl_trigger();
     pdl_wait();
     const int c = blockIdx.x;
-    const Place p = locate<kRows, kJoinThreads, true>(a, c, gridDim.x);
-    if (p.lo >= p.hi)
-        return;
-    const Seq s = seq_of(a, p.b);
-    const int kt = key_tiles(s), rt = row_tiles<kRows>(a, s);
-    const int unit = (int)(p.off / kt), k = (int)(p.off - (int64_t)unit * kt);   // the range's last tile
-    const int64_t begin = p.hi - 1 - k, end = begin + kt;
-    if (begin < p.lo || end <= p.hi)
-        return;                                         // begun earlier, or ended here
-    const int64_t used = max((int64_t)1, min((int64_t)gridDim.x, p.total / a.min_tiles));
-    int last = c + 1;
-    while (last + 1 < used && p.total * (last + 1) / used < end)
-        ++last;
-    const int h = unit / rt, tile = unit - h * rt;
     const float *own = slot_of<kRows>(a, 2 * (int64_t)c + 1);
-    bool unfinite = own[0] != 0.0f;
-    for (int d = c + 1; d <= last; ++d)
-        unfinite |= slot_of<kRows>(a, 2 * (int64_t)d)[0] != 0.0f;
-    for (int r = threadIdx.x >> 4; r < kRows; r += kJoinThreads / 16) {
-        const int row = tile * kRows + r, i = row / a.group;
-        if (i >= s.n)
-            continue;
-        const int col = (threadIdx.x & 15) * 4;
-        float now = own[4 + kRows * kHeadDim + r];
-        for (int d = c + 1; d <= last; ++d)
-            now = fmaxf(now, slot_of<kRows>(a, 2 * (int64_t)d)[4 + kRows * kHeadDim + r]);
-        const float ref = now == -INFINITY ? 0.0f : now;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float total = 0.0f;
-        for (int d = c; d <= last; ++d) {
-            const float *part = d == c ? own : slot_of<kRows>(a, 2 * (int64_t)d);
-            const float f = ex2(part[4 + kRows * kHeadDim + r] - ref);
-            const float4 y = *reinterpret_cast<const float4 *>(part + 4 + r * kHeadDim + col);
+    const Header hd = *reinterpret_cast<const Header *>(own);
+    if (hd.last == 0)
+        return;
+    const Seq s = seq_of(a, hd.b);
+    const int rt = row_tiles<kRows>(a, s);
+    const int h = hd.unit / rt, tile = hd.unit - h * rt;
+    const int r0 = blockIdx.y * kJoinRows, parts = hd.last - c + 1;
+    if (threadIdx.x == 0 && blockIdx.y == 0 && hd.unit == 0 && a.err != nullptr &&
+        (int64_t)max(__ldg(a.context_len + hd.b), 0) + s.n > s.keys)
+        atomicAdd(a.err, 1);
+    if (tile * kRows + r0 >= s.n * a.group)
+        return;
+    auto part_of = [&](int k) { return k == 0 ? own : slot_of<kRows>(a, 2 * (int64_t)(c + k)); };
+    const int group = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3, col = (threadIdx.x & 15) * 4;
+    bool unfinite = false;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -INFINITY, total = 0.0f;
+    // more parts than the table holds are joined in runs of kJoinParts
+    for (int k0 = 0; k0 < parts; k0 += kJoinParts) {
+        const int n = min(kJoinParts, parts - k0);
+        for (int i = threadIdx.x; i < n * kJoinRows; i += kJoinThreads) {
+            const float *part = part_of(k0 + i / kJoinRows);
+            s_part[i / kJoinRows][i % kJoinRows] = part[kSlotMax<kRows> + r0 + i % kJoinRows];
+            s_sum[i / kJoinRows][i % kJoinRows] = part[kSlotSum<kRows> + r0 + i % kJoinRows];
+            unfinite |= reinterpret_cast<const Header *>(part)->unfinite != 0;
+        }
+        unfinite = __syncthreads_or(unfinite) != 0;
+        if (threadIdx.x < kJoinRows * 32) {                // a warp per row
+            const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            float m = k0 == 0 ? -INFINITY : s_top[row];
+            const float before = m;
+            for (int k = lane; k < n; k += 32)
+                m = fmaxf(m, s_part[k][row]);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float ref = m == -INFINITY ? 0.0f : m;
+            float sum = 0.0f;
+            for (int k = lane; k < n; k += 32) {
+                const float f = ex2(s_part[k][row] - ref);
+                s_part[k][row] = f;
+                sum = __fmaf_rn(s_sum[k][row], f, sum);
+            }
+            sum = warp_butterfly_sum(sum);
+            if (lane == 0) {
+                s_total[row] = k0 == 0 ? sum : __fmaf_rn(s_total[row], ex2(before - ref), sum);
+                s_top[row] = m;
+            }
+        }
+        __syncthreads();
+        const float shrink = k0 == 0 ? 0.0f : ex2(top - (s_top[r] == -INFINITY ? 0.0f : s_top[r]));
+        top = s_top[r];
+        total = s_total[r];
+        x.x *= shrink;
+        x.y *= shrink;
+        x.z *= shrink;
+        x.w *= shrink;
+#pragma unroll 8
+        for (int k = group; k < n; k += 4) {
+            const float f = s_part[k][r];
+            const float4 y = *reinterpret_cast<const float4 *>(part_of(k0 + k) + kSlotOut<kRows> + (r0 + r) * kHeadDim + col);
             x.x = __fmaf_rn(y.x, f, x.x);
             x.y = __fmaf_rn(y.y, f, x.y);
             x.z = __fmaf_rn(y.z, f, x.z);
             x.w = __fmaf_rn(y.w, f, x.w);
-            total = __fmaf_rn(part[4 + kRows * (kHeadDim + 1) + r], f, total);
         }
-        const int head = h * a.group + row - i * a.group;
-        if (unfinite) {
-            x.x = add_unfinite(a, s, p.b, h, i, col, x.x);
-            x.y = add_unfinite(a, s, p.b, h, i, col + 1, x.y);
-            x.z = add_unfinite(a, s, p.b, h, i, col + 2, x.z);
-            x.w = add_unfinite(a, s, p.b, h, i, col + 3, x.w);
-        }
-        const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-        *reinterpret_cast<uint2 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col) =
-            make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-        if (col == 0 && a.lse != nullptr)
-            a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
-                total == 0.0f ? -INFINITY : __fmaf_rn(now, kLn2, logf(total));
+        __syncthreads();
     }
-    if (threadIdx.x == 0 && unit == 0 && a.err != nullptr &&
-        (int64_t)max(__ldg(a.context_len + p.b), 0) + s.n > s.keys)
-        atomicAdd(a.err, 1);
+    if (group > 0)
+        s_out[group - 1][threadIdx.x & 63] = x;
+    __syncthreads();
+    const int row = tile * kRows + r0 + r, i = row / a.group;
+    if (group > 0 || i >= s.n)
+        return;
+#pragma unroll
+    for (int g = 0; g < 3; ++g) {
+        const float4 y = s_out[g][threadIdx.x];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+    }
+    const int head = h * a.group + row - i * a.group;
+    if (unfinite) {
+        x.x = add_unfinite(a, s, hd.b, h, i, col, x.x);
+        x.y = add_unfinite(a, s, hd.b, h, i, col + 1, x.y);
+        x.z = add_unfinite(a, s, hd.b, h, i, col + 2, x.z);
+        x.w = add_unfinite(a, s, hd.b, h, i, col + 3, x.w);
+    }
+    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col) =
+        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+    if (col == 0 && a.lse != nullptr)
+        a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
+            total == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(total));
 }
 
 // Row tile of a call: 16 rows while the average unit fits them, else 32.
@@ -619,7 +730,7 @@ cudaError_t launch_small(const Args &a, int num_sms, cudaStream_t stream, const 
     if (e != cudaSuccess || a.partial == nullptr)
         return e;
     *why = "tree attention join launch";
-    return launch_pdl(k5_join<16 * kTiles>, dim3((unsigned)ctas), dim3(kJoinThreads), 0, stream, 1, a);
+    return launch_pdl(k5_join<16 * kTiles>, dim3((unsigned)ctas, 16 * kTiles / kJoinRows), dim3(kJoinThreads), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -638,6 +749,9 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
     a.min_tiles = 4;
+    // no unit has more tiles than a CTA takes at least: nothing to split or join
+    if ((int64_t)p.table_width * p.block_size <= a.min_tiles * kKeyTile)
+        a.partial = nullptr;
     return tiles_for(p.rows, p.seqs, p.group) == 1 ? launch_small<1>(a, num_sms, stream, why)
                                                    : launch_small<2>(a, num_sms, stream, why);
 }

@@ -18,46 +18,73 @@ namespace rc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kIter = 4;               // heads per thread: loads in flight
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<uint16_t>(uint16_t v) {
-    return __uint_as_float((uint32_t)v << 16);
-}
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ uint16_t from_f<uint16_t>(float v) {
-    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-
-// kN elements of T; kWideOf<T> of them are the 16 bytes of one access, and the
-// table's columns that go with them are 4 to 32 aligned bytes.
-template <typename T, int kN>
-struct alignas(sizeof(T) * kN < 16 ? sizeof(T) * kN : 16) Vec { T v[kN]; };
+// kN elements of T as 32-bit words (bf16 in pairs): 16 bytes at a time for
+// kOne accesses (4 or 8 for the table columns that go with fewer elements),
+// else element by element.
 template <typename T> constexpr int kWideOf = 16 / (int)sizeof(T);
 
-// kN consecutive elements, in one access (kOne) or one by one.
-template <bool kOne, typename T, int kN>
-__device__ __forceinline__ void get(Vec<T, kN> &d, const T *p) {
-    if (kOne) {
-        d = *reinterpret_cast<const Vec<T, kN> *>(p);
-    } else {
+template <typename T, int kN> struct Run {
+    static constexpr int kWords = (int)sizeof(T) * kN >= 4 ? (int)sizeof(T) * kN / 4 : 1;
+    uint32_t w[kWords];
+
+    template <bool kOne> __device__ __forceinline__ void get(const T *p) {
+        if (kOne && kWords % 4 == 0) {
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
-            d.v[j] = p[j];
-    }
-}
-template <bool kOne, typename T, int kN>
-__device__ __forceinline__ void put(T *p, const Vec<T, kN> &d) {
-    if (kOne) {
-        *reinterpret_cast<Vec<T, kN> *>(p) = d;
-    } else {
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x;
+                w[(4 * i + 1) % kWords] = v.y;
+                w[(4 * i + 2) % kWords] = v.z;
+                w[(4 * i + 3) % kWords] = v.w;
+            }
+        } else if (kOne && kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x;
+            w[kWords - 1] = v.y;
+        } else if (sizeof(T) == 4) {
 #pragma unroll
-        for (int j = 0; j < kN; ++j)
-            p[j] = d.v[j];
+            for (int i = 0; i < kN; ++i)
+                w[i % kWords] = reinterpret_cast<const uint32_t *>(p)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; i += 2)
+                w[i / 2] = (uint32_t)reinterpret_cast<const uint16_t *>(p)[i] |
+                           (i + 1 < kN ? (uint32_t)reinterpret_cast<const uint16_t *>(p)[i + 1] << 16 : 0u);
+        }
     }
-}
+    template <bool kOne> __device__ __forceinline__ void put(T *p) const {
+        if (kOne && kWords % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[(4 * i + 1) % kWords],
+                                                             w[(4 * i + 2) % kWords], w[(4 * i + 3) % kWords]);
+        } else if (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                reinterpret_cast<uint32_t *>(p)[i] = w[i % kWords];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+                reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if (sizeof(T) == 4)
+            return __uint_as_float(w[i % kWords]);
+        return (i & 1) ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    }
+    // Elements i and i + 1 (i even), or the only one.
+    __device__ __forceinline__ void set2(int i, float lo, float hi) {
+        if (sizeof(T) == 4) {
+            w[i % kWords] = __float_as_uint(lo);
+            if (kN > 1)
+                w[(i + 1) % kWords] = __float_as_uint(hi);
+        } else {
+            w[i / 2] = pack_bf16x2(lo, hi);
+        }
+    }
+};
 
 template <bool kInverse>
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
@@ -68,117 +95,119 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
     a = x;
 }
 
-// One thread: one unit of kIter (token, head) rows.  A unit is kVec
-// elements (pairs layout, and what is only copied) or kVec elements of each
-// half (halves layout).  Consecutive threads take the units of a head, then
-// the next head, so a warp reads whole rows.  kVec is 16 bytes' worth where
-// every pointer, stride, width and rot_dim allows it, else one pair, element
-// by element.  A narrow copied tail of odd width has kVec = 1 units, so pairs
-// heads whose tail is odd are refused on the host.
-template <typename T, typename C, bool kHalves, bool kInverse, int kVec>
-__global__ void __launch_bounds__(kThreads)
-k6_rope_apply(const RopeLaunch a)
+// One thread: one unit of kHeads consecutive heads of one token.  A unit is
+// kVec elements (pairs layout, and what is only copied) or kVec elements of
+// each half (halves layout), so its table columns are read once for all the
+// heads.  Consecutive threads take the units of a head, then the next group of
+// heads, then the next token.  kVec is 16 bytes' worth where every pointer,
+// stride, width and rot_dim allows it, else one pair, element by element (a
+// copied tail of odd width in the pairs layout is refused on the host).
+template <typename T, typename C, bool kHalves, bool kInverse, int kVec, int kHeads>
+__global__ void __launch_bounds__(kThreads, 4)
+k6_rope_apply(const __grid_constant__ RopeLaunch a)
 {
     pdl_trigger();
     pdl_wait();
     constexpr bool kOne = kVec == kWideOf<T>;
     const uint32_t rotated = kHalves ? (uint32_t)a.rot / (2 * kVec) : (uint32_t)a.rot / kVec;
     const uint32_t units = rotated + (uint32_t)(a.width - a.rot) / kVec;
+    const uint32_t groups = ((uint32_t)a.heads + kHeads - 1) / kHeads;
     const int half = a.rot / 2;
-    const int64_t all = a.T * a.heads;
-    const int64_t block0 = (int64_t)blockIdx.x * a.rows_per_block;
-    const uint32_t lanes = (uint32_t)a.rows_per_block / kIter;       // rows side by side
-    const T *x = static_cast<const T *>(a.x);
-    T *out = static_cast<T *>(a.out);
-    const C *table = static_cast<const C *>(a.table);
-    // units of a row beyond the block's threads (wide heads) are walked
-    for (uint32_t item = threadIdx.x; item < units * lanes; item += kThreads) {
-        const uint32_t u = item % units, lane_row = item / units;
+    // a block's threads are `units` wide (heads of more units than threads are
+    // walked) and take whole (token, group) items
+    const uint32_t side = max(1u, kThreads / units);
+    for (uint32_t i = threadIdx.x; i < units * side; i += kThreads) {
+        const uint32_t u = i % units;
+        const int64_t item = (int64_t)blockIdx.x * side + i / units;
+        if (item >= a.T * groups)
+            break;
+        // T * heads < 2^31 (checked on the host)
+        const uint32_t t = (uint32_t)item / groups, h0 = ((uint32_t)item - t * groups) * kHeads;
         const bool rot = u < rotated;
         const int at = rot ? (int)u * kVec : a.rot + (int)(u - rotated) * kVec;   // first element
         const int pair = kHalves ? at : at / 2;                                   // its table column
-        Vec<T, kVec> v0[kIter], v1[kIter];
-        int64_t pos[kIter], dst[kIter];
-        bool live[kIter];
+        const T *src = static_cast<const T *>(a.x) + t * a.x_row_stride + h0 * a.x_head_stride + at;
+        T *dst = static_cast<T *>(a.out) + t * a.out_row_stride + h0 * a.out_head_stride + at;
+        const int64_t pos = __ldg(a.positions + t);
+        Run<T, kVec> v0[kHeads], v1[kHeads];
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            const int64_t row = block0 + lane_row + (int64_t)i * lanes;
-            live[i] = row < all;
-            if (!live[i])
-                continue;
-            // T * heads < 2^31 (checked on the host)
-            const uint32_t t = (uint32_t)row / (uint32_t)a.heads, h = (uint32_t)row - t * (uint32_t)a.heads;
-            const T *src = x + t * a.x_row_stride + h * a.x_head_stride + at;
-            get<kOne>(v0[i], src);
-            if (kHalves && rot)
-                get<kOne>(v1[i], src + half);
-            pos[i] = __ldg(a.positions + t);
-            dst[i] = t * a.out_row_stride + h * a.out_head_stride + at;
-            if (u == 0 && h == 0 && a.err != nullptr && (pos[i] < 0 || pos[i] >= a.max_position))
-                atomicAdd(a.err, 1);
-        }
+        for (int k = 0; k < kHeads; ++k)
+            if (h0 + k < (uint32_t)a.heads) {
+                v0[k].template get<kOne>(src + k * a.x_head_stride);
+                if (kHalves && rot)
+                    v1[k].template get<kOne>(src + k * a.x_head_stride + half);
+            }
+        // a token without a table row passes through
+        const bool bad = pos < 0 || pos >= a.max_position;
+        if (bad && u == 0 && h0 == 0 && a.err != nullptr)
+            atomicAdd(a.err, 1);
+        if (rot && !bad) {
+            constexpr int kPairs = kHalves ? kVec : (kVec > 1 ? kVec / 2 : 1);
+            const C *cs = static_cast<const C *>(a.table) + pos * a.rot + pair;
+            Run<C, kPairs> c, s;
+            c.template get<kOne>(cs);
+            s.template get<kOne>(cs + half);
 #pragma unroll
-        for (int i = 0; i < kIter; ++i) {
-            if (!live[i])
-                continue;
-            // a token without a table row passes through
-            if (rot && pos[i] >= 0 && pos[i] < a.max_position) {
-                const C *cs = table + pos[i] * a.rot + pair;
+            for (int k = 0; k < kHeads; ++k) {
                 if (kHalves) {
-                    Vec<C, kVec> c, s;
-                    get<kOne>(c, cs);
-                    get<kOne>(s, cs + half);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        float p = to_f(v0[i].v[j]), q = to_f(v1[i].v[j]);
-                        turn<kInverse>(p, q, to_f(c.v[j]), to_f(s.v[j]));
-                        v0[i].v[j] = from_f<T>(p);
-                        v1[i].v[j] = from_f<T>(q);
+                    for (int j = 0; j < kVec; j += 2) {
+                        const int j1 = kVec > 1 ? j + 1 : j;
+                        float p0 = v0[k].at(j), q0 = v1[k].at(j), p1 = v0[k].at(j1), q1 = v1[k].at(j1);
+                        turn<kInverse>(p0, q0, c.at(j), s.at(j));
+                        turn<kInverse>(p1, q1, c.at(j1), s.at(j1));
+                        v0[k].set2(j, p0, p1);
+                        v1[k].set2(j, q0, q1);
                     }
                 } else {
-                    constexpr int kPairs = kVec > 1 ? kVec / 2 : 1;
-                    Vec<C, kPairs> c, s;
-                    get<kOne>(c, cs);
-                    get<kOne>(s, cs + half);
 #pragma unroll
                     for (int j = 0; j + 1 < kVec; j += 2) {
-                        float p = to_f(v0[i].v[j]), q = to_f(v0[i].v[j + 1]);
-                        turn<kInverse>(p, q, to_f(c.v[j / 2]), to_f(s.v[j / 2]));
-                        v0[i].v[j] = from_f<T>(p);
-                        v0[i].v[j + 1] = from_f<T>(q);
+                        float p = v0[k].at(j), q = v0[k].at(j + 1);
+                        turn<kInverse>(p, q, c.at(j / 2), s.at(j / 2));
+                        v0[k].set2(j, p, q);
                     }
                 }
             }
-            put<kOne>(out + dst[i], v0[i]);
-            if (kHalves && rot)
-                put<kOne>(out + dst[i] + half, v1[i]);
         }
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k)
+            if (h0 + k < (uint32_t)a.heads) {
+                v0[k].template put<kOne>(dst + k * a.out_head_stride);
+                if (kHalves && rot)
+                    v1[k].template put<kOne>(dst + k * a.out_head_stride + half);
+            }
     }
 }
 
 template <typename T, typename C, bool kHalves, bool kInverse>
-cudaError_t launch_vec(RopeLaunch &a, bool wide, cudaStream_t stream)
+cudaError_t launch_vec(const RopeLaunch &a, bool wide, int num_sms, cudaStream_t stream)
 {
     constexpr int kWide = kWideOf<T>;
     constexpr int kNarrow = kHalves ? 1 : 2;
     const int vec = wide ? kWide : kNarrow;
-    const int units = (kHalves ? a.rot / (2 * vec) : a.rot / vec) + (a.width - a.rot) / vec;
-    const int lanes = units >= kThreads ? 1 : kThreads / units;
-    a.rows_per_block = lanes * kIter;
-    const int64_t blocks = (a.T * a.heads + a.rows_per_block - 1) / a.rows_per_block;
-    auto kernel = wide ? k6_rope_apply<T, C, kHalves, kInverse, kWide>
-                       : k6_rope_apply<T, C, kHalves, kInverse, kNarrow>;
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, 1, a);
+    const int64_t units = (kHalves ? a.rot / (2 * vec) : a.rot / vec) + (a.width - a.rot) / vec;
+    // four loads in flight per thread (the heads that share them share the
+    // table's columns); with less work than fills the GPU that way, one head
+    // per thread
+    constexpr int kMany = kHalves ? 2 : 4;
+    const bool many = wide && a.heads >= kMany && a.T * a.heads * units >= (int64_t)kMany * num_sms * 1024;
+    const int64_t items = a.T * (many ? (a.heads + kMany - 1) / kMany : a.heads);
+    const int64_t side = std::max<int64_t>(1, kThreads / units);
+    auto kernel = many ? k6_rope_apply<T, C, kHalves, kInverse, kWide, kMany>
+                       : (wide ? k6_rope_apply<T, C, kHalves, kInverse, kWide, 1>
+                               : k6_rope_apply<T, C, kHalves, kInverse, kNarrow, 1>);
+    return launch_pdl(kernel, dim3((unsigned)((items + side - 1) / side)), dim3(kThreads), 0, stream, 1, a);
 }
 
 template <typename T, typename C>
-cudaError_t launch_types(RopeLaunch &a, bool halves, bool inverse, bool wide, cudaStream_t stream)
+cudaError_t launch_types(const RopeLaunch &a, bool halves, bool inverse, bool wide, int num_sms,
+                         cudaStream_t stream)
 {
     if (halves)
-        return inverse ? launch_vec<T, C, true, true>(a, wide, stream)
-                       : launch_vec<T, C, true, false>(a, wide, stream);
-    return inverse ? launch_vec<T, C, false, true>(a, wide, stream)
-                   : launch_vec<T, C, false, false>(a, wide, stream);
+        return inverse ? launch_vec<T, C, true, true>(a, wide, num_sms, stream)
+                       : launch_vec<T, C, true, false>(a, wide, num_sms, stream);
+    return inverse ? launch_vec<T, C, false, true>(a, wide, num_sms, stream)
+                   : launch_vec<T, C, false, false>(a, wide, num_sms, stream);
 }
 
 // ------------------------------------------------------------- the table
@@ -218,32 +247,34 @@ k6_rope_table(const __grid_constant__ TableArgs a)
             p = i / chunks;
             c = (uint32_t)(i - p * chunks);
         }
-        Vec<C, kVec> co, si;
+        Run<C, kVec> co, si;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const uint64_t turns = (uint64_t)p * a.step[c * kVec + j];
-            const float x = __fmul_rn((float)(int32_t)(turns >> 32), 0x1p-31f);    // half turns
-            float s, k;
-            sincospif(x, &s, &k);
-            co.v[j] = from_f<C>(__fmul_rn(k, a.gain));
-            si.v[j] = from_f<C>(__fmul_rn(s, a.gain));
+        for (int j = 0; j < kVec; j += 2) {
+            float s[2] = {0.0f, 0.0f}, k[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < (kVec > 1 ? 2 : 1); ++e) {
+                const uint64_t turns = (uint64_t)p * a.step[c * kVec + j + e];
+                sincospif(__fmul_rn((float)(int32_t)(turns >> 32), 0x1p-31f), &s[e], &k[e]);   // of half turns
+            }
+            co.set2(j, __fmul_rn(k[0], a.gain), __fmul_rn(k[1], a.gain));
+            si.set2(j, __fmul_rn(s[0], a.gain), __fmul_rn(s[1], a.gain));
         }
         C *row = static_cast<C *>(a.out) + p * 2 * a.half + c * kVec;
-        put<kVec == kWideOf<C>>(row, co);
-        put<kVec == kWideOf<C>>(row + a.half, si);
+        co.template put<kVec == kWideOf<C>>(row);
+        si.template put<kVec == kWideOf<C>>(row + a.half);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_rope_apply(RopeLaunch a, bool x_f32, bool table_f32, bool halves, bool inverse,
-                              bool wide, cudaStream_t stream)
+cudaError_t launch_rope_apply(const RopeLaunch &a, bool x_f32, bool table_f32, bool halves, bool inverse,
+                              bool wide, int num_sms, cudaStream_t stream)
 {
     if (x_f32)
-        return table_f32 ? launch_types<float, float>(a, halves, inverse, wide, stream)
-                         : launch_types<float, uint16_t>(a, halves, inverse, wide, stream);
-    return table_f32 ? launch_types<uint16_t, float>(a, halves, inverse, wide, stream)
-                     : launch_types<uint16_t, uint16_t>(a, halves, inverse, wide, stream);
+        return table_f32 ? launch_types<float, float>(a, halves, inverse, wide, num_sms, stream)
+                         : launch_types<float, uint16_t>(a, halves, inverse, wide, num_sms, stream);
+    return table_f32 ? launch_types<uint16_t, float>(a, halves, inverse, wide, num_sms, stream)
+                     : launch_types<uint16_t, uint16_t>(a, halves, inverse, wide, num_sms, stream);
 }
 
 cudaError_t launch_rope_table(void *out, bool f32, int64_t positions, int32_t rot, const double *inv,

@@ -10,11 +10,14 @@
 //
 // The floor is one read and one write of the logits.  A CTA owns a tile of
 // the vocabulary for the rows of one sequence: it scans the history once,
-// counts the tile's tokens in shared memory, and then streams its columns of
-// every row.  Most tokens occur nowhere, so a bit per token says whether its
-// count word has to be looked at: an access of 16 bytes of logits costs one
-// window of that bit map and one of the grammar mask.  Tokens drafted in the
-// tree are marked, and only their few words walk the tile's list of nodes.
+// counts the tile's tokens in shared memory, lists those that need arithmetic
+// and then streams its columns of every row, 16 bytes at a time.  Few tokens
+// are listed (what the history, the tree and the biases name), but they lie
+// scattered, so that computing them in place would make nearly every warp
+// walk the whole formula for a lane or two.  Instead the listed tokens of the
+// next row are computed side by side, one per thread, into shared memory while
+// the current row streams, and the stream only picks their values up where a
+// bit map says so.
 #include "rc_internal.cuh"
 
 #include <algorithm>
@@ -27,7 +30,7 @@ constexpr int kThreads = 256;
 constexpr int kPad = 32;                     // tokens kept before a tile (rows may start unaligned)
 constexpr int kNodes = 512;                  // drafted tokens a tile lists
 constexpr uint32_t kPrompt = 1u << 31;       // count word: in the prompt
-constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: see the list
+constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: the count changes by row
 constexpr uint32_t kBias = 1u << 29;         //   has a bias
 constexpr uint32_t kCount = kBias - 1;       //   occurrences in the generated history
 
@@ -55,12 +58,15 @@ __device__ __forceinline__ uint32_t window(const uint32_t *words, int at) {
 }
 
 template <int kTile> struct Smem {
-    uint32_t word[kTile + kPad];
-    uint32_t special[(kTile + kPad) / 32 + 2];       // bit: word != 0
-    uint32_t bias[kTile + kPad];                     // 1 + the entry that holds the token's bias
+    static constexpr int kWords = kTile + kPad;
+    uint32_t word[kWords];                           // count and flags of a token
+    uint32_t bias[kWords];                           // 1 + the entry of its bias, then the bias itself
+    float value[2][kWords];                          // a row's adjusted logits of the listed tokens
+    uint32_t special[kWords / 32 + 2];               // bit: word != 0
+    uint16_t list[kWords];                           // the tokens with word != 0
     int32_t node[kNodes];                            // the tile's drafted tokens: node index,
     int32_t token[kNodes];                           //   and place in the tile
-    int32_t nodes;
+    int32_t nodes, listed;
 };
 
 // kAligned: `logits` and `out` rows start at the same offset from a 16-byte
@@ -78,7 +84,7 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         s.bias[i] = 0u;
     }
     if (threadIdx.x == 0)
-        s.nodes = 0;
+        s.nodes = s.listed = 0;
     __syncthreads();
     pdl_wait();
 
@@ -92,6 +98,47 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     // counted by one CTA of the sequence
     const bool teller = blockIdx.x == 0 && blockIdx.z == 0 && a.err != nullptr;
     int bad = 0;
+
+    // Each row: its vectors and their mask bits are loaded while the row
+    // before it is worked on (the first while the history is counted).
+    struct alignas(kAligned ? 16 : sizeof(T)) Vec { T v[kVec]; };
+    constexpr int kPer = (kTile / kVec + kThreads - 1) / kThreads;
+    const int words = (a.V + 31) / 32;
+    auto shift_of = [&](int row) {
+        // vectors start on 16-byte boundaries: `shift` tokens before the tile
+        return kAligned ? (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
+                                                             (int64_t)row * a.row_stride) & 15u) / sizeof(T)) : 0;
+    };
+    auto load = [&](int row, Vec (&v)[kPer], uint32_t (&ok)[kPer]) {
+        const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
+        const uint32_t *mask = a.allowed != nullptr ? a.allowed + (int64_t)row * a.allowed_stride : nullptr;
+        const int shift = shift_of(row);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = (threadIdx.x + k * kThreads) * kVec, t = first - shift + i;
+            ok[k] = 0xFFFFFFFFu;
+            if (i >= kTile || t >= a.V)
+                continue;
+            if (t >= 0 && t + kVec <= a.V) {
+                v[k] = *reinterpret_cast<const Vec *>(src + t);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    v[k].v[j] = t + j >= 0 && t + j < a.V ? src[t + j] : T(0);
+            }
+            if (mask != nullptr) {
+                // the mask words around t; before token 0 and past the last word: not used
+                const int w0 = t >> 5;
+                const uint32_t lo = w0 >= 0 ? __ldg(mask + w0) : 0u;
+                const uint32_t hi = (t & 31) + kVec > 32 && w0 + 1 < words ? __ldg(mask + w0 + 1) : 0u;
+                ok[k] = __funnelshift_r(lo, hi, t & 31);
+            }
+        }
+    };
+    Vec next[kPer];
+    uint32_t next_ok[kPer];
+    int row = r0 + (int)blockIdx.z;
+    load(row, next, next_ok);
 
     // The history's tokens of this tile.
     if (a.history != nullptr) {
@@ -154,68 +201,97 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         atomicAdd(a.err, bad);
     __syncthreads();
     for (int i = threadIdx.x; i < kTile + kPad + 64; i += kThreads) {     // a whole number of warps
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, i < kTile + kPad && s.word[i] != 0u);
-        if ((threadIdx.x & 31) == 0)
+        const uint32_t w = i < kTile + kPad ? s.word[i] : 0u;
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, w != 0u);
+        const int lane = threadIdx.x & 31;
+        int at = 0;
+        if (lane == 0) {
             s.special[i >> 5] = bits;
+            at = bits != 0u ? atomicAdd(&s.listed, __popc(bits)) : 0;
+        }
+        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(bits & ((1u << lane) - 1u));
+        if (w != 0u)
+            s.list[at] = (uint16_t)i;
+        if (w & kBias)
+            s.bias[i] = __float_as_uint(__ldg(a.bias_values + (s.bias[i] - 1u)));
     }
     __syncthreads();
 
     const float rep = a.repetition != nullptr ? a.repetition[b] : 1.0f;
     const float freq = a.frequency != nullptr ? a.frequency[b] : 0.0f;
     const float pres = a.presence != nullptr ? a.presence[b] : 0.0f;
-    const int listed = s.nodes;
+    const int listed = s.listed, nodes = s.nodes;
 
-    // A token whose word is set, in row `row`.
-    auto adjust = [&](float x, int at, int row) -> float {
-        const uint32_t w = s.word[at];
-        uint32_t g = w & kCount;
-        if (w & kDraft) {
-            const uint64_t *see = a.tree_mask != nullptr ? a.tree_mask + (int64_t)row * a.mask_words : nullptr;
-            const int me = row - r0;
-            auto sees = [&](int j) {
-                if (see == nullptr)
-                    return j <= me;
-                return (j >> 6) < a.mask_words && ((see[j >> 6] >> (j & 63)) & 1u) != 0u;
-            };
-            if (listed <= kNodes) {
-                for (int k = 0; k < listed; ++k)
-                    g += s.token[k] == at && sees(s.node[k]);
-            } else {
-                for (int j = 0; j < r1 - r0; ++j)
-                    g += a.draft_tokens[r0 + j] == at + base && sees(j);
-            }
-        }
-        if (g != 0u || (w & kPrompt) != 0u)
-            x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-        x = __fsub_rn(x, __fmul_rn(freq, (float)g));
-        if (g != 0u)
-            x = __fsub_rn(x, pres);
-        if (w & kBias)
-            x = __fadd_rn(x, __ldg(a.bias_values + (s.bias[at] - 1u)));
-        return x;
-    };
-
-    struct alignas(kAligned ? 16 : sizeof(T)) Vec { T v[kVec]; };
-    constexpr int kPer = (kTile / kVec + kThreads - 1) / kThreads;
-    for (int row = r0 + (int)blockIdx.z; row < r1; row += (int)gridDim.z) {
+    // The logits of row `row`'s listed tokens: thread i takes entries i, i +
+    // kThreads, ...; the first kAhead of them are loaded before they are due.
+    constexpr int kAhead = 2;
+    auto fetch = [&](int row, float (&x)[kAhead]) {
         const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
-        T *dst = static_cast<T *>(a.out) + (int64_t)row * a.out_row_stride;
-        const uint32_t *ok = a.allowed != nullptr ? a.allowed + (int64_t)row * a.allowed_stride : nullptr;
-        // vectors start on 16-byte boundaries: `shift` tokens before the tile
-        const int shift = kAligned ? (int)((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T)) : 0;
-        const int words = (a.V + 31) / 32;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = threadIdx.x + k * kThreads;
+            const int t = e < listed ? base + s.list[e] : -1;
+            x[k] = t >= 0 && t < a.V ? Io<T>::load(src[t]) : 0.0f;
+        }
+    };
+    auto adjust = [&](int row, const float (&ahead)[kAhead], float *value) {
+        const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
+        const uint64_t *see = a.tree_mask != nullptr ? a.tree_mask + (int64_t)row * a.mask_words : nullptr;
+        auto sees = [&](int j) {
+            if (see == nullptr)
+                return j <= row - r0;
+            return (j >> 6) < a.mask_words && ((__ldg(see + (j >> 6)) >> (j & 63)) & 1u) != 0u;
+        };
+        auto one = [&](int e, float x) {
+            const int at = s.list[e];
+            const uint32_t w = s.word[at];
+            uint32_t g = w & kCount;
+            if (w & kDraft) {
+                if (nodes <= kNodes) {
+                    for (int k = 0; k < nodes; ++k)
+                        g += s.token[k] == at && sees(s.node[k]);
+                } else {
+                    for (int j = 0; j < r1 - r0; ++j)
+                        g += __ldg(a.draft_tokens + r0 + j) == at + base && sees(j);
+                }
+            }
+            if (g != 0u || (w & kPrompt) != 0u)
+                x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+            x = __fsub_rn(x, __fmul_rn(freq, (float)g));
+            if (g != 0u)
+                x = __fsub_rn(x, pres);
+            if (w & kBias)
+                x = __fadd_rn(x, __uint_as_float(s.bias[at]));
+            value[at] = x;
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (threadIdx.x + k * kThreads < listed)
+                one(threadIdx.x + k * kThreads, ahead[k]);
+        for (int e = threadIdx.x + kAhead * kThreads; e < listed; e += kThreads)
+            one(e, Io<T>::load(src[base + s.list[e]]));
+    };
+    float ahead[kAhead];
+    fetch(row, ahead);
+    adjust(row, ahead, s.value[0]);
+    int turn = 0;
+    for (; row < r1; row += (int)gridDim.z) {
+        __syncthreads();                                 // this row's values are there, the last row's are free
         Vec v[kPer];
+        uint32_t ok[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int t = first - shift + (threadIdx.x + k * kThreads) * kVec;
-            if (t >= 0 && t + kVec <= a.V) {
-                v[k] = *reinterpret_cast<const Vec *>(src + t);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    v[k].v[j] = t + j >= 0 && t + j < a.V ? src[t + j] : T(0);
-            }
+            v[k] = next[k];
+            ok[k] = next_ok[k];
         }
+        const bool more = row + (int)gridDim.z < r1;
+        if (more) {
+            load(row + (int)gridDim.z, next, next_ok);
+            fetch(row + (int)gridDim.z, ahead);
+        }
+        const float *value = s.value[turn];
+        T *dst = static_cast<T *>(a.out) + (int64_t)row * a.out_row_stride;
+        const int shift = shift_of(row);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const int i = (threadIdx.x + k * kThreads) * kVec;
@@ -223,30 +299,17 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             if (i >= kTile || t >= a.V)
                 continue;
             const int at = t - base;
-            uint32_t todo = window(s.special, at) & ((1u << kVec) - 1u);
-            while (todo != 0u) {
-                const int j = __ffs(todo) - 1;
-                todo &= todo - 1u;
-                T x = v[k].v[0];
-#pragma unroll
-                for (int q = 1; q < kVec; ++q)
-                    x = q == j ? v[k].v[q] : x;
-                x = Io<T>::store(adjust(Io<T>::load(x), at + j, row));
-#pragma unroll
-                for (int q = 0; q < kVec; ++q)
-                    v[k].v[q] = q == j ? x : v[k].v[q];
-            }
-            if (ok != nullptr) {
-                // the mask words around t; before token 0 and past the last word: not used
-                const int w0 = t >> 5;
-                const uint32_t lo = w0 >= 0 ? __ldg(ok + w0) : 0u;
-                const uint32_t hi = (t & 31) + kVec > 32 && w0 + 1 < words ? __ldg(ok + w0 + 1) : 0u;
-                const uint32_t bits = __funnelshift_r(lo, hi, t & 31);
+            const uint32_t todo = window(s.special, at) & ((1u << kVec) - 1u);
+            if (todo != 0u) {
 #pragma unroll
                 for (int j = 0; j < kVec; ++j)
-                    if (!((bits >> j) & 1u))
-                        v[k].v[j] = minus_inf<T>();
+                    if ((todo >> j) & 1u)
+                        v[k].v[j] = Io<T>::store(value[at + j]);
             }
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (!((ok[k] >> j) & 1u))
+                    v[k].v[j] = minus_inf<T>();
             if (t >= 0 && t + kVec <= a.V) {
                 *reinterpret_cast<Vec *>(dst + t) = v[k];
             } else {
@@ -256,6 +319,9 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
                         dst[t + j] = v[k].v[j];
             }
         }
+        turn ^= 1;
+        if (more)
+            adjust(row + (int)gridDim.z, ahead, s.value[turn]);
     }
 }
 
@@ -291,9 +357,9 @@ cudaError_t launch_type(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
     const uintptr_t src = reinterpret_cast<uintptr_t>(a.logits), dst = reinterpret_cast<uintptr_t>(a.out);
     const bool aligned = (src & 15u) == (dst & 15u) &&
                          (a.rows <= 1 || ((a.row_stride - a.out_row_stride) * (int64_t)sizeof(T)) % 16 == 0);
-    if ((int64_t)((a.V + 4095) / 4096) * a.seqs >= 2 * num_sms)
-        return aligned ? launch_one<T, 4096, true>(a, num_sms, stream)
-                       : launch_one<T, 4096, false>(a, num_sms, stream);
+    if ((int64_t)((a.V + 2047) / 2048) * a.seqs >= 2 * num_sms)
+        return aligned ? launch_one<T, 2048, true>(a, num_sms, stream)
+                       : launch_one<T, 2048, false>(a, num_sms, stream);
     return aligned ? launch_one<T, 1024, true>(a, num_sms, stream)
                    : launch_one<T, 1024, false>(a, num_sms, stream);
 }

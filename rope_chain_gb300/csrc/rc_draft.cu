@@ -197,8 +197,11 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
     a.width = head_dim;
     a.rot = rot_dim;
     a.err = err;
+    const int sms = num_sms_current();
+    if (sms <= 0)
+        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
     const cudaError_t e = rc::launch_rope_apply(a, dtype == RC_F32, table_dtype == RC_F32,
-                                                layout == RC_ROPE_HALVES, inverse != 0, wide, stream);
+                                                layout == RC_ROPE_HALVES, inverse != 0, wide, sms, stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, "rc_rope_apply launch");
 }
 

@@ -392,7 +392,7 @@ cudaError_t read_front_faults(uint32_t *flags, bool clear);
 constexpr int kMaxRotDim = 512;
 
 // Rotary application over T tokens of `heads` heads (strides in elements,
-// any order of token and head); the launcher fills rows_per_block.
+// any order of token and head).
 struct RopeLaunch {
     const void *x;
     void *out;
@@ -402,13 +402,12 @@ struct RopeLaunch {
     int64_t max_position;
     int64_t T;
     int32_t heads, width, rot;       // T * heads < 2^31
-    int32_t rows_per_block;
     int32_t *err;
 };
 
 // `wide`: 16-byte accesses (pointers, strides, width and rot allow them).
-cudaError_t launch_rope_apply(RopeLaunch a, bool x_f32, bool table_f32, bool halves, bool inverse,
-                              bool wide, cudaStream_t stream);
+cudaError_t launch_rope_apply(const RopeLaunch &a, bool x_f32, bool table_f32, bool halves, bool inverse,
+                              bool wide, int num_sms, cudaStream_t stream);
 
 // The table of `positions` rows from the rot / 2 angular frequencies inv.
 cudaError_t launch_rope_table(void *out, bool f32, int64_t positions, int32_t rot, const double *inv,
