@@ -791,8 +791,9 @@ rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride
 rc_status rc_device_address(const void *p, const void **dev);
 
 /* Sticky fault bits raised on the device when a bounded wait gives up: bits
-   0-3 by the projection kernels, bits 8-11 by the QKV front (per kernel:
-   load pipeline, tensor-core pipeline, accumulator, drain).  A kernel that
+   0-3 by the projection kernels, bits 8-11 by the QKV front, bits 16-19 by
+   the tree attention (per kernel: load pipeline, tensor-core pipeline,
+   accumulator, drain).  A kernel that
    sees a raised bit of its own kind skips its work, so after a fault its
    outputs are wrong until the bits are cleared.  Reads (and with clear != 0
    resets) the bits of the current device; synchronises the device.  No

@@ -19,11 +19,14 @@
 // m, sum) in the workspace, which a second kernel joins in key order (no
 // atomics: the result does not depend on timing).
 #include "rc_internal.cuh"
+#include "rc_tcgen05.cuh"
 
 #include <algorithm>
 #include <cmath>
 
 namespace rc {
+
+__device__ unsigned int g_attention_faults;
 
 namespace {
 
@@ -131,6 +134,52 @@ __device__ Place locate(const Args &a, int c, int ctas) {
     return p;
 }
 
+// One piece of a unit: key tiles k0 .. k0 + count - 1 of its kt.
+struct Piece {
+    Seq s;
+    int32_t b, unit, h, tile;          // sequence, unit within it, its KV head and row tile
+    int32_t k0, count, kt;
+    int64_t begin;                     // the unit's first tile among all units'
+    __device__ bool whole() const { return k0 == 0 && count == kt; }
+};
+
+// The pieces of a CTA's range, in order.
+template <int kRows> struct Walk {
+    int64_t pos, off, hi;
+    int32_t b;
+    __device__ explicit Walk(const Place &p) : pos(p.lo), off(p.off), hi(p.hi), b(p.b) {}
+    __device__ bool next(const Args &a, Piece &u) {
+        while (pos < hi) {
+            u.s = seq_of(a, b);
+            u.kt = key_tiles(u.s);
+            const int rt = row_tiles<kRows>(a, u.s);
+            const int64_t tiles = (int64_t)rt * a.kv_heads * u.kt;
+            if (off >= tiles) {                         // the next sequence with rows
+                off -= tiles;
+                ++b;
+                continue;
+            }
+            u.b = b;
+            u.unit = (int32_t)(off / u.kt);
+            u.k0 = (int32_t)(off - (int64_t)u.unit * u.kt);
+            u.h = u.unit / rt;
+            u.tile = u.unit - u.h * rt;
+            u.count = (int32_t)min((int64_t)(u.kt - u.k0), hi - pos);
+            u.begin = pos - u.k0;
+            pos += u.count;
+            off += u.count;
+            if (a.partial == nullptr) {
+                // without a workspace a unit belongs to the CTA of its first tile
+                if (u.k0 != 0)
+                    continue;
+                u.count = u.kt;
+            }
+            return true;
+        }
+        return false;
+    }
+};
+
 // A partial: a header, then kRows x 64 outputs (not divided by the sum), kRows
 // maxima and kRows sums.  Each CTA has two: slot 2c for the unit that an
 // earlier CTA began, slot 2c + 1 for one that it begins and a later CTA ends,
@@ -165,21 +214,20 @@ __device__ __forceinline__ int64_t key_offset(const Args &a, int b, int h, int p
     return (((int64_t)blk * a.kv_heads + h) * bs + ((uint32_t)p - page * bs)) * (2 * kHeadDim);
 }
 
-// The header of this CTA's part of a split unit: key tiles from k0 of kt, its
-// first tile at `begin` of all units' tiles laid end to end.
+// The header of this CTA's part of a split unit.
 template <int kRows>
-__device__ void write_header(const Args &a, const Place &p, int k0, int kt, int64_t begin, int b, int unit,
-                             bool unfinite) {
-    Header h{0, b, unit, unfinite ? 1 : 0};
-    if (k0 == 0) {
-        int64_t last = (begin + kt - 1) * p.used / p.total;      // its range holds the unit's last tile
-        while (p.total * (last + 1) / p.used < begin + kt)
+__device__ void write_header(const Args &a, const Place &p, const Piece &u, bool unfinite) {
+    Header h{0, u.b, u.unit, unfinite ? 1 : 0};
+    if (u.k0 == 0) {
+        const int64_t end = u.begin + u.kt;
+        int64_t last = (end - 1) * p.used / p.total;             // the CTA of the unit's last tile
+        while (p.total * (last + 1) / p.used < end)
             ++last;
-        while (p.total * last / p.used >= begin + kt)
+        while (p.total * last / p.used >= end)
             --last;
         h.last = (int32_t)last;
     }
-    *reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0))) = h;
+    *reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0))) = h;
 }
 
 // A drafted V row that is infinite or NaN must not reach rows that do not see
@@ -218,9 +266,6 @@ template <int kTiles> constexpr int kRing = kTiles == 1 ? 3 : 5;
 // The rings; at a unit's end they hold the warps' outputs (32 KiB per row tile).
 template <int kTiles> constexpr uint32_t kSmallSmem = kWarps * kRing<kTiles> * kChunkBytes;
 
-__device__ __forceinline__ uint32_t smem_at(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0)
                  : "memory");
@@ -267,37 +312,18 @@ k5_small(const __grid_constant__ Args a)
     __shared__ float s_max[kWarps][kRows], s_sum[kWarps][kRows];
     __shared__ uint32_t s_real[kWarps][kStages];       // which of a chunk's keys exist
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t ring = smem_at(smem) + (uint32_t)warp * (kStages * kChunkBytes);
+    const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (kStages * kChunkBytes);
     pdl_trigger();
     pdl_wait();
 
     const Place at = locate<kRows, kSmallThreads>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
-    int64_t pos = at.lo, off = at.off;
-    int b = at.b;
-    while (pos < at.hi) {
-        const Seq s = seq_of(a, b);
-        const int kt = key_tiles(s), rt = row_tiles<kRows>(a, s);
-        const int64_t seq_tiles = (int64_t)rt * a.kv_heads * kt;
-        if (off >= seq_tiles) {                         // the next sequence with rows
-            off -= seq_tiles;
-            ++b;
-            continue;
-        }
-        const int unit = (int)(off / kt), k0 = (int)(off - (int64_t)unit * kt);
-        const int h = unit / rt, tile = unit - h * rt;
-        int count = (int)min((int64_t)(kt - k0), at.hi - pos);
-        const bool split_ok = a.partial != nullptr;
-        if (!split_ok) {
-            // without a workspace a unit belongs to the CTA of its first tile
-            if (k0 != 0) {
-                pos += count;
-                off += count;
-                continue;
-            }
-            count = kt;
-        }
+    Walk<kRows> walk(at);
+    Piece u;
+    while (walk.next(a, u)) {
+        const Seq &s = u.s;
+        const int b = u.b, h = u.h, tile = u.tile, unit = u.unit, k0 = u.k0, count = u.count;
 
         // this thread's rows: lane / 4 and lane / 4 + 8 of each row tile
         int node[kTiles][2];
@@ -509,7 +535,7 @@ k5_small(const __grid_constant__ Args a)
             }
         unfinite = __syncthreads_or(unfinite) != 0;     // also: every ring is drained
         float *outs = reinterpret_cast<float *>(smem) + warp * (16 * kHeadDim);
-        const bool whole = k0 == 0 && count == kt;
+        const bool whole = u.whole();
         float *slot = whole ? nullptr : slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0));
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -556,7 +582,7 @@ k5_small(const __grid_constant__ Args a)
                     slot[kSlotSum<kRows> + m * 16 + r] = total;
                 }
                 if (threadIdx.x == 0 && m == 0)
-                    write_header<kRows>(a, at, k0, kt, pos - k0, b, unit, unfinite);
+                    write_header<kRows>(a, at, u, unfinite);
             } else if (i < s.n) {
                 const int head = h * a.group + row - i * a.group;
                 if (unfinite) {
@@ -577,8 +603,491 @@ k5_small(const __grid_constant__ Args a)
             }
             __syncthreads();
         }
-        pos += count;
-        off += count;
+    }
+}
+
+// ------------------------------------------------ many rows: tcgen05 tiles
+//
+// From 33 rows per unit on the tensor cores are the bound, and the work goes
+// to tcgen05: one 128-row tile of Q per group of four softmax warps (kQ of
+// them share each key tile), 128 keys per step.  S = Q K^T lands in TMEM (128
+// columns); a thread owns one row, so its maximum and sum need no shuffles;
+// the weights go back to TMEM as bf16 over the scores (64 columns), from where
+// they are the A operand of O += P V, and O stays in TMEM (64 columns).  O is
+// rescaled only when a row's maximum has grown by more than 2^8 since its last
+// reference (the weights then stay below 2^8, harmless in FP32 and bf16): by
+// the row's own thread, a rare path.
+//   loader warp   K and V tiles of 16 KiB by TMA, in boxes of the largest
+//                 power of two of keys that divides a block (8 to 128), each
+//                 box's block looked up in the table by its own lane
+//   MMA warp      S of tile t, then for each further step O of tile t followed
+//                 by the next S of tile t, so that one tile's products run
+//                 while the other tiles' softmax does
+//   softmax       4 warps per tile
+// Key tiles that hold drafted keys, or the end, take a masked path; there the
+// V rows past the end are zeroed and what is infinite or NaN in a drafted one
+// is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
+// fault bit is raised and all roles leave.
+
+enum : unsigned { kFaultLoad = 1u, kFaultMma = 2u, kFaultSoftmax = 4u, kFaultDrain = 8u };
+
+constexpr uint32_t kTileBytes = kKeyTile * kHeadDim * 2;           // K or V of a step, Q of a tile: 16 KiB
+template <int kQ> constexpr int kWideThreads = 128 * kQ + 128;
+template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
+template <int kQ> constexpr uint32_t kTmemCols = kQ == 1 ? 256u : 512u;
+template <int kQ> constexpr uint32_t kOCol = 128u * kQ;            // after the scores of all tiles
+template <int kQ> constexpr size_t kWideSmem = 1024 + kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
+constexpr float kGrow = 8.0f;                                      // log2: when O is rescaled
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int col, int off, int h, int blk,
+                                        uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(off), "r"(h), "r"(blk), "r"(bar)
+                 : "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem]
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
+}
+// 32 columns of this warp's 32 lanes; complete after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t at, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The values of a load, to be used no earlier than here (after the wait).
+__device__ __forceinline__ void loaded32(float *r) {
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                      "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
+                      "+f"(r[15]));
+    asm volatile("" : "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                      "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                      "+f"(r[30]), "+f"(r[31]));
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Which of the keys base .. base + 31 node i sees (bit k: key base + k);
+// i < 0: none of the drafted ones.
+__device__ uint32_t seen32(const Args &a, const Seq &s, int i, int base) {
+    auto below = [](int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); };
+    const uint32_t ctx = below(s.ctx - base);
+    uint32_t drafted = 0u;
+    if (i >= 0 && ctx != 0xFFFFFFFFu) {
+        if (a.tree_mask == nullptr) {
+            drafted = below(s.ctx + i + 1 - base);
+        } else {
+            const uint64_t *row = a.tree_mask + (int64_t)(s.r0 + i) * a.mask_words;
+            const int j0 = base - s.ctx;                // node of bit 0, negative inside the context
+            auto word = [&](int w) { return w >= 0 && w < a.mask_words ? __ldg(row + w) : (uint64_t)0; };
+            if (j0 < 0) {
+                drafted = (uint32_t)(word(0) << -j0);
+            } else {
+                const int w = j0 >> 6, sh = j0 & 63;
+                uint64_t v = word(w) >> sh;
+                if (sh > 32)
+                    v |= word(w + 1) << (64 - sh);
+                drafted = (uint32_t)v;
+            }
+        }
+    }
+    return (ctx | (drafted & ~ctx)) & below(s.keys - base);
+}
+
+template <int kQ>
+__global__ void __launch_bounds__(kWideThreads<kQ>, kQ == 1 ? 2 : 1)
+k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a, int box)
+{
+    constexpr int kRows = 128 * kQ, kStages = kWideStages<kQ>, kThreads = kWideThreads<kQ>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const uint32_t sQ = smem_u32(smem), sK = sQ + kQ * kTileBytes;     // a stage: K, then V
+    __shared__ uint64_t bars[2 * kStages + 4 * kQ + 2];
+    __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[2];
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kStages, q_ready0 = empty0 + 8u * kStages;
+    const uint32_t s_full0 = q_ready0 + 8u * kQ, p_ready0 = s_full0 + 8u * kQ, o_done0 = p_ready0 + 8u * kQ;
+    const uint32_t drain = o_done0 + 8u * kQ, v_fixed = drain + 8u;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    constexpr int kLoadWarp = 4 * kQ, kMmaWarp = 4 * kQ + 1;
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full0 + 8u * i, 1);
+            mbar_init(empty0 + 8u * i, 1);
+        }
+        for (int t = 0; t < kQ; ++t) {
+            mbar_init(q_ready0 + 8u * t, 128);
+            mbar_init(s_full0 + 8u * t, 1);
+            mbar_init(p_ready0 + 8u * t, 128);
+            mbar_init(o_done0 + 8u * t, 1);
+        }
+        mbar_init(drain, 1);
+        mbar_init(v_fixed, 128 * kQ);
+        s_unfinite[0] = s_unfinite[1] = 0u;
+        // one decision for the CTA: a raised fault skips the work
+        s_skip = *reinterpret_cast<volatile unsigned int *>(&g_attention_faults);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tensormap(&map);
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols<kQ>) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned fault) {
+        if (mbar_wait_flag(bar, parity, &g_attention_faults))
+            return true;
+        atomicOr(&g_attention_faults, fault);
+        return false;
+    };
+
+    const Place at = locate<kRows, kThreads>(a, blockIdx.x, gridDim.x);
+    if (a.partial != nullptr && threadIdx.x == 0)
+        reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
+    Walk<kRows> walk(at);
+    if (s_skip != 0u)
+        walk.hi = walk.pos;
+    Piece u;
+    uint32_t n = 0;                                     // key tiles of earlier pieces
+    uint32_t piece = 0;
+
+    if (warp >= 4 * kQ) {
+        if (kQ == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kLoadWarp) {
+            const int boxes = kKeyTile / box;           // <= 16
+            bool fine = true;
+            while (fine && walk.next(a, u)) {
+                const Seq &s = u.s;
+                // this lane's box of tile j: its block, or -1 for one that is not there
+                auto look_up = [&](int j) -> int {
+                    const int p = (u.k0 + j) * kKeyTile + lane * box;
+                    return j < u.count && lane < boxes && p < s.keys
+                               ? __ldg(a.block_table + u.b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size) : 0;
+                };
+                int blk = look_up(0);
+                for (int j = 0; j < u.count; ++j, ++n) {
+                    const uint32_t st = n % kStages, full = full0 + 8u * st;
+                    const int p = (u.k0 + j) * kKeyTile + lane * box;
+                    const bool mine = lane < boxes && p < s.keys;
+                    const int off = mine ? (int)((uint32_t)p % (uint32_t)a.block_size) : 0;
+                    const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
+                    if (bad && u.unit == 0 && off == 0 && a.err != nullptr)
+                        atomicAdd(a.err, 1);            // once per block: at its first key
+                    fine = wait(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
+                    fine = __all_sync(0xFFFFFFFFu, fine);
+                    if (!fine)
+                        break;
+                    const uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad), loads = __ballot_sync(0xFFFFFFFFu, mine);
+                    if (lane == 0) {
+                        s_bad[st] = bads;
+                        mbar_expect_tx(full, (uint32_t)__popc(loads) * box * 256u);
+                    }
+                    __syncwarp();
+                    if (mine) {
+                        // a block out of range reads zeros: one past the last
+                        const int from = bad ? a.num_blocks : blk;
+                        const uint32_t dst = sK + st * (2 * kTileBytes) + (uint32_t)(lane * box) * 128u;
+                        tma_box(dst, &map, 0, off, u.h, from, full);
+                        tma_box(dst + kTileBytes, &map, kHeadDim, off, u.h, from, full);
+                    }
+                    blk = look_up(j + 1);
+                }
+            }
+            // what was loaded has landed before shared memory is given back
+            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+                if (!mbar_wait_own(full0 + 8u * (i % kStages), (i / kStages) & 1u)) {
+                    atomicOr(&g_attention_faults, kFaultDrain);
+                    break;
+                }
+        } else if (warp == kMmaWarp) {
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = make_idesc(128, kKeyTile, false), idesc_o = make_idesc(128, kHeadDim, true);
+                auto scores = [&](int t, uint32_t st) {
+                    const uint32_t q = sQ + t * kTileBytes, k = sK + st * (2 * kTileBytes);
+#pragma unroll
+                    for (int kk = 0; kk < kHeadDim / 16; ++kk)
+                        mma_bf16(tmem + 128u * t, smem_desc_sw128(q + 32u * kk, 16u, 1024u),
+                                 smem_desc_sw128(k + 32u * kk, 16u, 1024u), idesc_s, kk != 0);
+                    mma_commit(s_full0 + 8u * t);
+                };
+                bool fine = true;
+                while (fine && walk.next(a, u)) {
+                    for (int t = 0; t < kQ && fine; ++t)
+                        fine = wait(q_ready0 + 8u * t, piece & 1u, kFaultMma);
+                    fine = fine && wait(full0 + 8u * (n % kStages), (n / kStages) & 1u, kFaultMma);
+                    if (!fine)
+                        break;
+                    tc_fence_after();
+                    for (int t = 0; t < kQ; ++t)
+                        scores(t, n % kStages);
+                    for (int j = 0; j < u.count && fine; ++j, ++n) {
+                        const uint32_t st = n % kStages, nx = (n + 1) % kStages;
+                        const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
+                        for (int t = 0; t < kQ; ++t) {
+                            fine = wait(p_ready0 + 8u * t, n & 1u, kFaultMma);
+                            if (!fine)
+                                break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < kKeyTile / 16; ++kk)
+                                mma_bf16_ta(tmem + kOCol<kQ> + 64u * t, tmem + 128u * t + 8u * kk,
+                                            smem_desc_sw128(v + 2048u * kk, 8192u, 1024u), idesc_o, (j | kk) != 0);
+                            mma_commit(o_done0 + 8u * t);
+                            if (t == kQ - 1)
+                                mma_commit(empty0 + 8u * st);
+                            if (j + 1 < u.count) {
+                                if (t == 0)
+                                    fine = wait(full0 + 8u * nx, ((n + 1) / kStages) & 1u, kFaultMma);
+                                if (!fine)
+                                    break;
+                                tc_fence_after();
+                                scores(t, nx);
+                            }
+                        }
+                    }
+                    ++piece;
+                }
+                mma_commit(drain);
+                if (!mbar_wait_own(drain, 0u))
+                    atomicOr(&g_attention_faults, kFaultDrain);
+            }
+            __syncwarp();
+        }
+    } else {
+        if (kQ == 1)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;                        // this group's row tile
+        const int r = threadIdx.x & 127;                // this thread's row of it, and its TMEM lane
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128u * t, tO = tmem + lanes + kOCol<kQ> + 64u * t;
+        const uint32_t q_at = sQ + t * kTileBytes + (uint32_t)r * 128u;
+        uint32_t fixes = 0;                             // tiles whose V was looked through
+        bool fine = true;
+        while (fine && walk.next(a, u)) {
+            const Seq &s = u.s;
+            const int row = u.tile * kRows + 128 * t + r, node = row / a.group, i = node < s.n ? node : -1;
+            const int head = u.h * a.group + row - node * a.group;
+            {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.r0 + node) * a.q_row_stride +
+                                                                   head * kHeadDim);
+                uint4 w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    w[c] = i >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    st_shared_v4(q_at + (uint32_t)((c ^ (r & 7)) << 4), w[c]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive_local(q_ready0 + 8u * t);
+            }
+            float top = -INFINITY, sum = 0.0f;          // reference (log2) and sum of the row
+            bool unfinite = false;
+            for (int j = 0; j < u.count; ++j, ++n) {
+                const int p0 = (u.k0 + j) * kKeyTile;
+                fine = wait(s_full0 + 8u * t, n & 1u, kFaultSoftmax);
+                fine = __all_sync(0xFFFFFFFFu, fine);
+                if (!fine)
+                    break;
+                tc_fence_after();
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32_async(tS + 32u * c, x + 32 * c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    loaded32(x + 32 * c);
+                const uint32_t st = n % kStages;
+                const bool last_keys = p0 + kKeyTile > s.ctx;
+                const uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
+                if (last_keys || bads != 0u) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t see = seen32(a, s, i, p0 + 32 * c);
+                        if (bads != 0u) {
+                            for (int k = 0; k < 32; ++k)
+                                if ((bads >> ((32 * c + k) / box)) & 1u)
+                                    see &= ~(1u << k);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            x[32 * c + k] = (see >> k) & 1u ? x[32 * c + k] : -INFINITY;
+                    }
+                }
+                if (last_keys) {
+                    // the tile's V: zeros past the end, and in place of what is
+                    // not finite in drafted keys.  The groups share the work and
+                    // wait for one another; a piece that met such a value leaves
+                    // its number (in the word of its parity: a group is never two
+                    // tiles ahead of one that has not read it).
+                    fine = wait(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
+                    const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
+                    bool found = false;
+                    for (int e = threadIdx.x; e < kKeyTile * 8; e += 128 * kQ) {
+                        const int key = p0 + (e >> 3);
+                        if (key < s.ctx)
+                            continue;
+                        const uint32_t chunk = v + 16u * e;
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        bool write = true;
+                        if (key < s.keys) {
+                            w = ld_shared_v4(chunk);
+                            write = finite_only(w.x, true, true);
+                            write |= finite_only(w.y, true, true);
+                            write |= finite_only(w.z, true, true);
+                            write |= finite_only(w.w, true, true);
+                            found |= write;
+                        }
+                        if (write)
+                            st_shared_v4(chunk, w);
+                    }
+                    if (found)
+                        *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 1u]) = piece + 1u;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive_local(v_fixed);
+                    fine = wait(v_fixed, fixes & 1u, kFaultSoftmax) && fine;
+                    ++fixes;
+                    unfinite |= *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 1u]) == piece + 1u;
+                }
+                float m = max3(x[0], x[1], x[2]);
+#pragma unroll
+                for (int k = 3; k + 1 < 128; k += 2)
+                    m = max3(m, x[k], x[k + 1]);
+                m = fmaxf(m, x[127]) * a.scale_log2;
+                const bool grew = m > top + kGrow || (top == -INFINITY && m > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, grew)) {
+                    const float shrink = grew ? ex2(top - m) : 1.0f;    // top -inf: 0
+                    if (j > 0) {
+                        fine = wait(o_done0 + 8u * t, (n - 1) & 1u, kFaultSoftmax);
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float o[32];
+                            uint32_t w[32];
+                            tmem_ld32_async(tO + 32u * c, o);
+                            tmem_wait_ld();
+                            loaded32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                w[k] = __float_as_uint(o[k] * shrink);
+                            tmem_st32(tO + 32u * c, w);
+                        }
+                        tmem_wait_st();
+                    }
+                    sum *= shrink;
+                    if (grew)
+                        top = m;
+                }
+                const float ref = top == -INFINITY ? 0.0f : -top;
+                float part[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        float x0 = x[64 * c + 2 * k], x1 = x[64 * c + 2 * k + 1];
+                        fma2_rn(x0, x1, a.scale_log2, a.scale_log2, ref, ref);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        add2_rn(part[0], part[1], x0, x1);
+                        w[k] = pack_bf16x2(x0, x1);
+                    }
+                    tmem_st32(tS + 32u * c, w);
+                }
+                tmem_wait_st();
+                sum += part[0] + part[1];
+                tc_fence_before();
+                mbar_arrive_local(p_ready0 + 8u * t);
+            }
+            if (!fine)
+                break;
+            // the row's output
+            fine = wait(o_done0 + 8u * t, (n - 1) & 1u, kFaultSoftmax);
+            fine = __all_sync(0xFFFFFFFFu, fine);
+            if (!fine)
+                break;
+            tc_fence_after();
+            float o[64];
+            tmem_ld32_async(tO, o);
+            tmem_ld32_async(tO + 32u, o + 32);
+            tmem_wait_ld();
+            loaded32(o);
+            loaded32(o + 32);
+            tc_fence_before();
+            if (!u.whole()) {
+                float *slot = slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0));
+                const int rr = 128 * t + r;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    *reinterpret_cast<float4 *>(slot + kSlotOut<kRows> + rr * kHeadDim + 4 * k) =
+                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                slot[kSlotMax<kRows> + rr] = top;
+                slot[kSlotSum<kRows> + rr] = sum;
+                if (threadIdx.x == 0)
+                    write_header<kRows>(a, at, u, unfinite);
+            } else if (i >= 0) {
+                if (unfinite) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        o[k] = add_unfinite(a, s, u.b, u.h, i, k, o[k]);
+                }
+                const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                        pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                        pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                if (a.lse != nullptr)
+                    a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
+                        sum == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(sum));
+                if (threadIdx.x == 0 && u.unit == 0 && a.err != nullptr &&
+                    (int64_t)max(__ldg(a.context_len + u.b), 0) + s.n > s.keys)
+                    atomicAdd(a.err, 1);
+            }
+            ++piece;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols<kQ>)
+                     : "memory");
     }
 }
 
@@ -700,46 +1209,100 @@ k5_join(const __grid_constant__ Args a)
             total == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(total));
 }
 
-// Row tile of a call: 16 rows while the average unit fits them, else 32.
-int tiles_for(int64_t rows, int32_t seqs, int32_t group) {
+// Which kernel takes a call, by the average rows of a unit (only the totals are
+// known on the host; any kernel is right for any unit):
+//   up to 16 rows  k5_small<1>;  up to 32  k5_small<2>: the cache's bytes bound
+//   beyond         k5_wide: 128 rows a CTA up to 128, else 256 (two row tiles
+//                  share each key tile); its TMA boxes need blocks of a
+//                  multiple of 8 keys, other block sizes stay with k5_small<2>
+enum Variant { kSmall16, kSmall32, kWide128, kWide256 };
+
+Variant variant_for(int64_t rows, int32_t seqs, int32_t group, int32_t block_size) {
     const int64_t mean = (rows + seqs - 1) / seqs * group;
-    return mean <= 16 ? 1 : 2;
+    if (mean <= 16)
+        return kSmall16;
+    if (mean <= 32 || block_size % 8 != 0)
+        return kSmall32;
+    return mean <= 128 ? kWide128 : kWide256;
 }
 
-int ctas_for(int tiles, int num_sms) { return tiles == 1 ? 2 * num_sms : num_sms; }
+// CTAs of a launch (all resident at once) and floats of a partial.
+int ctas_of(Variant v, int num_sms) { return v == kSmall16 || v == kWide128 ? 2 * num_sms : num_sms; }
+size_t slot_floats(Variant v) {
+    switch (v) {
+    case kSmall16: return kSlotFloats<16>;
+    case kSmall32: return kSlotFloats<32>;
+    case kWide128: return kSlotFloats<128>;
+    default: return kSlotFloats<256>;
+    }
+}
 
-template <int kTiles>
-cudaError_t launch_small(const Args &a, int num_sms, cudaStream_t stream, const char **why)
-{
-    static bool configured[64] = {};
+template <typename Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, bool (&configured)[64]) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && configured[dev]))
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64)
+        configured[dev] = true;
+    return e;
+}
+
+template <int kRows> cudaError_t launch_join(const Args &a, int ctas, cudaStream_t stream, const char **why) {
+    if (a.partial == nullptr)
+        return cudaSuccess;
+    *why = "tree attention join launch";
+    return launch_pdl(k5_join<kRows>, dim3((unsigned)ctas, kRows / kJoinRows), dim3(kJoinThreads), 0, stream, 1, a);
+}
+
+template <int kTiles>
+cudaError_t launch_small(const Args &a, int ctas, cudaStream_t stream, const char **why)
+{
+    static bool configured[64] = {};
+    cudaError_t e = allow_smem(k5_small<kTiles>, kSmallSmem<kTiles>, configured);
     if (e != cudaSuccess)
         return e;
-    if (dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(k5_small<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmallSmem<kTiles>);
-        if (e != cudaSuccess)
-            return e;
-        if (dev < 64)
-            configured[dev] = true;
-    }
-    const int ctas = ctas_for(kTiles, num_sms);
     *why = "tree attention launch";
     e = launch_pdl(k5_small<kTiles>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
-    if (e != cudaSuccess || a.partial == nullptr)
+    return e != cudaSuccess ? e : launch_join<16 * kTiles>(a, ctas, stream, why);
+}
+
+template <int kQ>
+cudaError_t launch_wide(const Args &a, int ctas, cudaStream_t stream, const char **why)
+{
+    static bool configured[64] = {};
+    cudaError_t e = allow_smem(k5_wide<kQ>, kWideSmem<kQ>, configured);
+    if (e != cudaSuccess)
         return e;
-    *why = "tree attention join launch";
-    return launch_pdl(k5_join<16 * kTiles>, dim3((unsigned)ctas, 16 * kTiles / kJoinRows), dim3(kJoinThreads), 0, stream, 1, a);
+    // the cache as [num_blocks, kv_heads, block_size, 128], boxes of 64 columns
+    // (K or V) and the largest power of two of keys, at most a tile, in a block
+    const int box = std::min(kKeyTile, a.block_size & -a.block_size);
+    const uint64_t row = 2 * kHeadDim * 2;
+    const cuuint64_t dims[4] = {2 * kHeadDim, (cuuint64_t)a.block_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_blocks};
+    const cuuint64_t strides[3] = {row, row * a.block_size, row * a.block_size * a.kv_heads};
+    const cuuint32_t boxes[4] = {kHeadDim, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    CUtensorMap map;
+    const EncodeTiledFn enc = encode_fn();
+    *why = "tensor map of the cache could not be encoded";
+    if (!enc || enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(a.cache), dims, strides, boxes,
+                    ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    *why = "tree attention launch";
+    e = launch_pdl(k5_wide<kQ>, dim3((unsigned)ctas), dim3(kWideThreads<kQ>), kWideSmem<kQ>, stream, 1, map, a, box);
+    return e != cudaSuccess ? e : launch_join<128 * kQ>(a, ctas, stream, why);
 }
 
 }  // namespace
 
 size_t tree_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms)
 {
-    const int tiles = tiles_for(rows, seqs, group);
-    const size_t slot = tiles == 1 ? kSlotFloats<16> : kSlotFloats<32>;
-    return 2 * (size_t)ctas_for(tiles, num_sms) * slot * sizeof(float);
+    size_t most = 0;
+    for (int32_t block_size : {8, 1}) {                 // whichever the cache has
+        const Variant v = variant_for(rows, seqs, group, block_size);
+        most = std::max(most, 2 * (size_t)ctas_of(v, num_sms) * slot_floats(v) * sizeof(float));
+    }
+    return most;
 }
 
 cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cudaStream_t stream,
@@ -752,8 +1315,31 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     // no unit has more tiles than a CTA takes at least: nothing to split or join
     if ((int64_t)p.table_width * p.block_size <= a.min_tiles * kKeyTile)
         a.partial = nullptr;
-    return tiles_for(p.rows, p.seqs, p.group) == 1 ? launch_small<1>(a, num_sms, stream, why)
-                                                   : launch_small<2>(a, num_sms, stream, why);
+    const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
+    const int ctas = ctas_of(v, num_sms);
+    switch (v) {
+    case kSmall16: return launch_small<1>(a, ctas, stream, why);
+    case kSmall32: return launch_small<2>(a, ctas, stream, why);
+    case kWide128: return launch_wide<1>(a, ctas, stream, why);
+    default: return launch_wide<2>(a, ctas, stream, why);
+    }
+}
+
+cudaError_t read_attention_faults(uint32_t *flags, bool clear)
+{
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess)
+        return e;
+    unsigned int v = 0;
+    e = cudaMemcpyFromSymbol(&v, g_attention_faults, sizeof v);
+    if (e != cudaSuccess)
+        return e;
+    *flags = v;
+    if (clear) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_attention_faults, &zero, sizeof zero);
+    }
+    return e;
 }
 
 }  // namespace rc

@@ -1106,13 +1106,15 @@ rc_status rc_read_device_faults(uint32_t *flags, int32_t clear)
 {
     if (!flags)
         return fail(RC_ERR_INVALID_ARG, "rc_read_device_faults: flags must not be NULL");
-    uint32_t project = 0, front = 0;
+    uint32_t project = 0, front = 0, attention = 0;
     cudaError_t e = rc::read_project_faults(&project, clear != 0);
     if (e == cudaSuccess)
         e = rc::read_front_faults(&front, clear != 0);
+    if (e == cudaSuccess)
+        e = rc::read_attention_faults(&attention, clear != 0);
     if (e != cudaSuccess)
         return cuda_fail(e, "rc_read_device_faults");
-    *flags = project | (front << 8);
+    *flags = project | (front << 8) | (attention << 16);
     return ok();
 }
 

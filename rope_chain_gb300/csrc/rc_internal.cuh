@@ -469,4 +469,7 @@ size_t tree_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int n
 cudaError_t launch_tree_attention(const TreeAttentionLaunch &a, int num_sms, cudaStream_t stream,
                                   const char **why);
 
+// Sticky device fault bits of the tree attention (current device).
+cudaError_t read_attention_faults(uint32_t *flags, bool clear);
+
 }  // namespace rc
