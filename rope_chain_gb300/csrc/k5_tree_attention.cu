@@ -609,21 +609,27 @@ k5_small(const __grid_constant__ Args a)
 // ------------------------------------------------ many rows: tcgen05 tiles
 //
 // From 33 rows per unit on the tensor cores are the bound, and the work goes
-// to tcgen05: one 128-row tile of Q per group of four softmax warps (kQ of
-// them share each key tile), 128 keys per step.  S = Q K^T lands in TMEM (128
-// columns); a thread owns one row, so its maximum and sum need no shuffles;
-// the weights go back to TMEM as bf16 over the scores (64 columns), from where
-// they are the A operand of O += P V, and O stays in TMEM (64 columns).  O is
-// rescaled only when a row's maximum has grown by more than 2^8 since its last
-// reference (the weights then stay below 2^8, harmless in FP32 and bf16): by
-// the row's own thread, a rare path.
-//   loader warp   K and V tiles of 16 KiB by TMA, in boxes of the largest
-//                 power of two of keys that divides a block (8 to 128), each
-//                 box's block looked up in the table by its own lane
-//   MMA warp      S of tile t, then for each further step O of tile t followed
-//                 by the next S of tile t, so that one tile's products run
-//                 while the other tiles' softmax does
-//   softmax       4 warps per tile
+// to tcgen05: kQ row tiles of 128 rows share each key tile of 128 keys.  A row
+// tile's S = Q K^T lands in TMEM (128 columns), the weights go back to TMEM as
+// bf16 (64 columns), from where they are the A operand of O += P V, and O stays
+// in TMEM (64 columns): 256 columns per row tile, two row tiles per SM (kQ = 2,
+// or two CTAs of kQ = 1).  Eight softmax warps per row tile, each with 16 of
+// its rows and whole key tiles (a quad of lanes per row, as in m16n8 tiles:
+// the maximum takes two shuffles): 16 warps per SM hide one another's
+// latencies, where 8 warps of a row per thread ran at a third of the issue
+// rate.  O is rescaled only when a row's maximum has grown by more than 2^8
+// since its last reference (the weights then stay below 2^8, harmless in FP32
+// and bf16): by the row's own quad, a rare path.
+//   loader warp      K and V tiles of 16 KiB by TMA, in boxes of the largest
+//                    power of two of keys that divides a block (8 to 128),
+//                    each box's block looked up in the table by its own lane
+//   kQ MMA warps     one per row tile: the next S as soon as the softmax has
+//                    the last one in registers, then O when the weights are
+//                    there.  One warp for both tiles was the bottleneck: some
+//                    100 cycles per product to issue, 1200 per tile and round
+// Per 256 rows x 128 keys the exponentials need 1024 cycles of an SM (32 per
+// cycle), the products as many at full rate; products of 64 columns (O) run at
+// about half of it.
 // Key tiles that hold drafted keys, or the end, take a masked path; there the
 // V rows past the end are zeroed and what is infinite or NaN in a drafted one
 // is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
@@ -632,12 +638,31 @@ k5_small(const __grid_constant__ Args a)
 enum : unsigned { kFaultLoad = 1u, kFaultMma = 2u, kFaultSoftmax = 4u, kFaultDrain = 8u };
 
 constexpr uint32_t kTileBytes = kKeyTile * kHeadDim * 2;           // K or V of a step, Q of a tile: 16 KiB
-template <int kQ> constexpr int kWideThreads = 128 * kQ + 128;
+template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
+template <int kQ> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + 1);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
-template <int kQ> constexpr uint32_t kTmemCols = kQ == 1 ? 256u : 512u;
-template <int kQ> constexpr uint32_t kOCol = 128u * kQ;            // after the scores of all tiles
-template <int kQ> constexpr size_t kWideSmem = 1024 + kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
+template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
+constexpr uint32_t kPCol = 128u, kOCol = 192u;
+template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
 constexpr float kGrow = 8.0f;                                      // log2: when O is rescaled
+
+// mbar_wait_flag for the many waits of softmax threads: the timer is read (a
+// slow access) and the fault word looked at only once a few tries, each of
+// which the hardware suspends for a while, have failed.
+__device__ __forceinline__ bool mbar_wait_patient(uint32_t bar, uint32_t parity, unsigned int *flag) {
+    unsigned long long t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try(bar, parity))
+            return true;
+        if ((it & 31u) == 31u) {
+            const unsigned long long now = globaltimer();
+            if (t0 == 0)
+                t0 = now;
+            if (*reinterpret_cast<volatile unsigned int *>(flag) != 0u || now - t0 > kWaitNs)
+                return false;
+        }
+    }
+}
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int col, int off, int h, int blk,
                                         uint32_t bar) {
@@ -646,17 +671,33 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(off), "r"(h), "r"(blk), "r"(bar)
                  : "memory");
 }
-// D[tmem] (+)= A[tmem] x B[smem]
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
+// Shared-memory descriptors (smem_desc_sw128) as their low words, so that the
+// next 16 columns or keys are one addition away; the high word is a constant.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
-// 32 columns of this warp's 32 lanes; complete after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t at, float *r) {
+// D[tmem] (+)= A[smem] x B[smem], and with A in TMEM
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alow, uint32_t blow, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+                 ::"r"(d), "r"(alow), "r"(blow), "r"(idesc), "r"(acc), "r"(kDescHigh) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blow, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 b, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(blow), "r"(idesc), "r"(acc), "r"(kDescHigh) : "memory");
+}
+// 64 columns of 16 lanes (FP32): lane l's values of rows l / 4 (r[4c], r[4c + 1])
+// and l / 4 + 8 (r[4c + 2], r[4c + 3]) are columns 8c + 2 (l % 4) and the next.
+// Complete after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t at, float *r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
@@ -665,29 +706,41 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t at, float *r) {
           "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// The values of a load, to be used no earlier than here (after the wait).
-__device__ __forceinline__ void loaded32(float *r) {
-    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
-                      "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
-                      "+f"(r[15]));
-    asm volatile("" : "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
-                      "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
-                      "+f"(r[30]), "+f"(r[31]));
+// 16 columns of the same kind, load and store.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t at, float *r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
+__device__ __forceinline__ void tmem_st_rows16(uint32_t at, const float *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+                 : "memory");
+}
+// 64 columns of 16 lanes: w[2c] row l / 4, w[2c + 1] row l / 4 + 8, column
+// 4c + l % 4 (pairs of bf16: columns 8c + 2 (l % 4) and the next of P).
+__device__ __forceinline__ void tmem_st_pairs(uint32_t at, const uint32_t *w) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
         "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
+        "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]),
+        "r"(w[16]), "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]),
+        "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
         : "memory");
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The values of a load, to be used no earlier than here (after the wait).
+__device__ __forceinline__ void loaded8(float *r) {
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Which of the keys base .. base + 31 node i sees (bit k: key base + k);
 // i < 0: none of the drafted ones.
@@ -721,32 +774,34 @@ __global__ void __launch_bounds__(kWideThreads<kQ>, kQ == 1 ? 2 : 1)
 k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a, int box)
 {
     constexpr int kRows = 128 * kQ, kStages = kWideStages<kQ>, kThreads = kWideThreads<kQ>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
-    const uint32_t sQ = smem_u32(smem), sK = sQ + kQ * kTileBytes;     // a stage: K, then V
-    __shared__ uint64_t bars[2 * kStages + 4 * kQ + 2];
-    __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[2];
+    constexpr int kMmaWarp = kSoftmaxWarps<kQ>, kLoadWarp = kMmaWarp + kQ;
+    extern __shared__ __align__(1024) uint8_t smem_wide[];
+    const uint32_t sQ = smem_u32(smem_wide), sK = sQ + kQ * kTileBytes;     // a stage: K, then V
+    __shared__ uint64_t bars[2 * kStages + 6 * kQ];
+    // by piece modulo 8: a row tile is never more than kStages + 1 pieces ahead
+    // of another, whose products free its stages
+    __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[8];
+    static_assert(kStages + 1 < 8, "pieces in flight");
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kStages, q_ready0 = empty0 + 8u * kStages;
-    const uint32_t s_full0 = q_ready0 + 8u * kQ, p_ready0 = s_full0 + 8u * kQ, o_done0 = p_ready0 + 8u * kQ;
-    const uint32_t drain = o_done0 + 8u * kQ, v_fixed = drain + 8u;
+    const uint32_t s_full0 = q_ready0 + 8u * kQ, s_free0 = s_full0 + 8u * kQ, p_ready0 = s_free0 + 8u * kQ;
+    const uint32_t o_done0 = p_ready0 + 8u * kQ, drain0 = o_done0 + 8u * kQ;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    constexpr int kLoadWarp = 4 * kQ, kMmaWarp = 4 * kQ + 1;
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full0 + 8u * i, 1);
-            mbar_init(empty0 + 8u * i, 1);
+            mbar_init(empty0 + 8u * i, kQ);
         }
         for (int t = 0; t < kQ; ++t) {
-            mbar_init(q_ready0 + 8u * t, 128);
+            mbar_init(q_ready0 + 8u * t, 256);
             mbar_init(s_full0 + 8u * t, 1);
-            mbar_init(p_ready0 + 8u * t, 128);
+            mbar_init(s_free0 + 8u * t, 8);
+            mbar_init(p_ready0 + 8u * t, 256);
             mbar_init(o_done0 + 8u * t, 1);
+            mbar_init(drain0 + 8u * t, 1);
         }
-        mbar_init(drain, 1);
-        mbar_init(v_fixed, 128 * kQ);
-        s_unfinite[0] = s_unfinite[1] = 0u;
+        for (int i = 0; i < 8; ++i)
+            s_unfinite[i] = 0u;
         // one decision for the CTA: a raised fault skips the work
         s_skip = *reinterpret_cast<volatile unsigned int *>(&g_attention_faults);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -760,10 +815,10 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
     pdl_wait();
     auto wait = [&](uint32_t bar, uint32_t parity, unsigned fault) {
-        if (mbar_wait_flag(bar, parity, &g_attention_faults))
+        if (mbar_wait_patient(bar, parity, &g_attention_faults))
             return true;
         atomicOr(&g_attention_faults, fault);
         return false;
@@ -779,188 +834,187 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     uint32_t n = 0;                                     // key tiles of earlier pieces
     uint32_t piece = 0;
 
-    if (warp >= 4 * kQ) {
-        if (kQ == 1)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        if (warp == kLoadWarp) {
-            const int boxes = kKeyTile / box;           // <= 16
-            bool fine = true;
-            while (fine && walk.next(a, u)) {
-                const Seq &s = u.s;
-                // this lane's box of tile j: its block, or -1 for one that is not there
-                auto look_up = [&](int j) -> int {
-                    const int p = (u.k0 + j) * kKeyTile + lane * box;
-                    return j < u.count && lane < boxes && p < s.keys
-                               ? __ldg(a.block_table + u.b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size) : 0;
-                };
-                int blk = look_up(0);
-                for (int j = 0; j < u.count; ++j, ++n) {
-                    const uint32_t st = n % kStages, full = full0 + 8u * st;
-                    const int p = (u.k0 + j) * kKeyTile + lane * box;
-                    const bool mine = lane < boxes && p < s.keys;
-                    const int off = mine ? (int)((uint32_t)p % (uint32_t)a.block_size) : 0;
-                    const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
-                    if (bad && u.unit == 0 && off == 0 && a.err != nullptr)
-                        atomicAdd(a.err, 1);            // once per block: at its first key
-                    fine = wait(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
-                    fine = __all_sync(0xFFFFFFFFu, fine);
-                    if (!fine)
-                        break;
-                    const uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad), loads = __ballot_sync(0xFFFFFFFFu, mine);
-                    if (lane == 0) {
-                        s_bad[st] = bads;
-                        mbar_expect_tx(full, (uint32_t)__popc(loads) * box * 256u);
-                    }
-                    __syncwarp();
-                    if (mine) {
-                        // a block out of range reads zeros: one past the last
-                        const int from = bad ? a.num_blocks : blk;
-                        const uint32_t dst = sK + st * (2 * kTileBytes) + (uint32_t)(lane * box) * 128u;
-                        tma_box(dst, &map, 0, off, u.h, from, full);
-                        tma_box(dst + kTileBytes, &map, kHeadDim, off, u.h, from, full);
-                    }
-                    blk = look_up(j + 1);
-                }
-            }
-            // what was loaded has landed before shared memory is given back
-            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
-                if (!mbar_wait_own(full0 + 8u * (i % kStages), (i / kStages) & 1u)) {
-                    atomicOr(&g_attention_faults, kFaultDrain);
-                    break;
-                }
-        } else if (warp == kMmaWarp) {
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = make_idesc(128, kKeyTile, false), idesc_o = make_idesc(128, kHeadDim, true);
-                auto scores = [&](int t, uint32_t st) {
-                    const uint32_t q = sQ + t * kTileBytes, k = sK + st * (2 * kTileBytes);
-#pragma unroll
-                    for (int kk = 0; kk < kHeadDim / 16; ++kk)
-                        mma_bf16(tmem + 128u * t, smem_desc_sw128(q + 32u * kk, 16u, 1024u),
-                                 smem_desc_sw128(k + 32u * kk, 16u, 1024u), idesc_s, kk != 0);
-                    mma_commit(s_full0 + 8u * t);
-                };
-                bool fine = true;
-                while (fine && walk.next(a, u)) {
-                    for (int t = 0; t < kQ && fine; ++t)
-                        fine = wait(q_ready0 + 8u * t, piece & 1u, kFaultMma);
-                    fine = fine && wait(full0 + 8u * (n % kStages), (n / kStages) & 1u, kFaultMma);
-                    if (!fine)
-                        break;
-                    tc_fence_after();
-                    for (int t = 0; t < kQ; ++t)
-                        scores(t, n % kStages);
-                    for (int j = 0; j < u.count && fine; ++j, ++n) {
-                        const uint32_t st = n % kStages, nx = (n + 1) % kStages;
-                        const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
-                        for (int t = 0; t < kQ; ++t) {
-                            fine = wait(p_ready0 + 8u * t, n & 1u, kFaultMma);
-                            if (!fine)
-                                break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < kKeyTile / 16; ++kk)
-                                mma_bf16_ta(tmem + kOCol<kQ> + 64u * t, tmem + 128u * t + 8u * kk,
-                                            smem_desc_sw128(v + 2048u * kk, 8192u, 1024u), idesc_o, (j | kk) != 0);
-                            mma_commit(o_done0 + 8u * t);
-                            if (t == kQ - 1)
-                                mma_commit(empty0 + 8u * st);
-                            if (j + 1 < u.count) {
-                                if (t == 0)
-                                    fine = wait(full0 + 8u * nx, ((n + 1) / kStages) & 1u, kFaultMma);
-                                if (!fine)
-                                    break;
-                                tc_fence_after();
-                                scores(t, nx);
-                            }
-                        }
-                    }
-                    ++piece;
-                }
-                mma_commit(drain);
-                if (!mbar_wait_own(drain, 0u))
-                    atomicOr(&g_attention_faults, kFaultDrain);
-            }
-            __syncwarp();
-        }
-    } else {
-        if (kQ == 1)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int t = warp >> 2;                        // this group's row tile
-        const int r = threadIdx.x & 127;                // this thread's row of it, and its TMEM lane
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + 128u * t, tO = tmem + lanes + kOCol<kQ> + 64u * t;
-        const uint32_t q_at = sQ + t * kTileBytes + (uint32_t)r * 128u;
-        uint32_t fixes = 0;                             // tiles whose V was looked through
+    if (warp == kLoadWarp) {
+        const int boxes = kKeyTile / box;               // <= 16
         bool fine = true;
         while (fine && walk.next(a, u)) {
             const Seq &s = u.s;
-            const int row = u.tile * kRows + 128 * t + r, node = row / a.group, i = node < s.n ? node : -1;
-            const int head = u.h * a.group + row - node * a.group;
+            // this lane's box of tile j: its block
+            auto look_up = [&](int j) -> int {
+                const int p = (u.k0 + j) * kKeyTile + lane * box;
+                return j < u.count && lane < boxes && p < s.keys
+                           ? __ldg(a.block_table + u.b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size) : 0;
+            };
+            int blk = look_up(0);
+            for (int j = 0; j < u.count; ++j, ++n) {
+                const uint32_t st = n % kStages, full = full0 + 8u * st;
+                const int p = (u.k0 + j) * kKeyTile + lane * box;
+                const bool mine = lane < boxes && p < s.keys;
+                const int off = mine ? (int)((uint32_t)p % (uint32_t)a.block_size) : 0;
+                const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
+                if (bad && u.unit == 0 && off == 0 && a.err != nullptr)
+                    atomicAdd(a.err, 1);                // once per block: at its first key
+                fine = wait(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
+                fine = __all_sync(0xFFFFFFFFu, fine);
+                if (!fine)
+                    break;
+                const uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad), loads = __ballot_sync(0xFFFFFFFFu, mine);
+                if (lane == 0) {
+                    s_bad[st] = bads;
+                    mbar_expect_tx(full, (uint32_t)__popc(loads) * box * 256u);
+                }
+                __syncwarp();
+                if (mine) {
+                    // a block out of range reads zeros: one past the last
+                    const int from = bad ? a.num_blocks : blk;
+                    const uint32_t dst = sK + st * (2 * kTileBytes) + (uint32_t)(lane * box) * 128u;
+                    tma_box(dst, &map, 0, off, u.h, from, full);
+                    tma_box(dst + kTileBytes, &map, kHeadDim, off, u.h, from, full);
+                }
+                blk = look_up(j + 1);
+            }
+        }
+        // what was loaded has landed before shared memory is given back
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+            if (!mbar_wait_own(full0 + 8u * (i % kStages), (i / kStages) & 1u)) {
+                atomicOr(&g_attention_faults, kFaultDrain);
+                break;
+            }
+    } else if (warp >= kMmaWarp) {
+        if (lane == 0) {
+            const int t = warp - kMmaWarp;
+            constexpr uint32_t idesc_s = make_idesc(128, kKeyTile, false), idesc_o = make_idesc(128, kHeadDim, true);
+            const uint32_t tS = tmem + 256u * t, tP = tS + kPCol, tO = tS + kOCol;
+            const uint32_t q = desc_low(sQ + t * kTileBytes, 16u);
+            const uint32_t k0 = desc_low(sK, 16u), v0 = desc_low(sK + kTileBytes, 8192u);
+            const uint32_t s_full = s_full0 + 8u * t, s_free = s_free0 + 8u * t, p_ready = p_ready0 + 8u * t;
+            const uint32_t o_done = o_done0 + 8u * t;
+            // the scores of key tile i, once their columns are free
+            auto scores = [&](uint32_t i) {
+                const uint32_t st = i % kStages;
+                if (!wait(full0 + 8u * st, (i / kStages) & 1u, kFaultMma) ||
+                    (i > 0 && !wait(s_free, (i - 1) & 1u, kFaultMma)))
+                    return false;
+                tc_fence_after();
+                const uint32_t k = k0 + st * (2 * kTileBytes >> 4);
+#pragma unroll
+                for (uint32_t kk = 0; kk < kHeadDim / 16; ++kk)
+                    mma_ss(tS, q + 2u * kk, k + 2u * kk, idesc_s, kk);
+                mma_commit(s_full);
+                return true;
+            };
+            bool fine = true;
+            while (fine && walk.next(a, u)) {
+                fine = wait(q_ready0 + 8u * t, piece & 1u, kFaultMma) && scores(n);
+                for (int j = 0; j < u.count && fine; ++j, ++n) {
+                    if (j + 1 < u.count)
+                        fine = scores(n + 1);
+                    fine = fine && wait(p_ready, n & 1u, kFaultMma);
+                    if (!fine)
+                        break;
+                    tc_fence_after();
+                    const uint32_t st = n % kStages, v = v0 + st * (2 * kTileBytes >> 4);
+                    mma_ts(tO, tP, v, idesc_o, j != 0);
+#pragma unroll
+                    for (uint32_t kk = 1; kk < kKeyTile / 16; ++kk)
+                        mma_ts(tO, tP + 8u * kk, v + kk * (2048u >> 4), idesc_o, 1u);
+                    mma_commit(o_done);
+                    mma_commit(empty0 + 8u * st);
+                }
+                ++piece;
+            }
+            mma_commit(drain0 + 8u * t);
+            if (!mbar_wait_own(drain0 + 8u * t, 0u))
+                atomicOr(&g_attention_faults, kFaultDrain);
+        }
+        __syncwarp();
+    } else {
+        // warp w of a row tile: rows 32 (w % 4) + 16 (w / 4) .. + 15 (a warp
+        // reaches the TMEM lanes of its number modulo 4); this lane's are
+        // l / 4 and l / 4 + 8 of them
+        const int t = warp >> 3, w8 = warp & 7;
+        const int first = 32 * (w8 & 3) + 16 * (w8 >> 2);
+        const uint32_t lanes = (uint32_t)first << 16;
+        const uint32_t tS = tmem + lanes + 256u * t, tP = tS + kPCol, tO = tS + kOCol;
+        const uint32_t s_full = s_full0 + 8u * t, p_ready = p_ready0 + 8u * t, o_done = o_done0 + 8u * t;
+        bool fine = true;
+        while (fine && walk.next(a, u)) {
+            const Seq &s = u.s;
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (int64_t)(s.r0 + node) * a.q_row_stride +
-                                                                   head * kHeadDim);
-                uint4 w[8];
+                // Q: thread i of the tile's 256 takes half of row i / 2
+                const int i = threadIdx.x & 255, r = i >> 1, half = i & 1;
+                const int row = u.tile * kRows + 128 * t + r, node = row / a.group;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (int64_t)(s.r0 + node) * a.q_row_stride + (u.h * a.group + row - node * a.group) * kHeadDim) + 4 * half;
+                const uint32_t dst = sQ + (uint32_t)t * kTileBytes + (uint32_t)r * 128u;
+                uint4 w[4];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    w[c] = i >= 0 ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < 4; ++c)
+                    w[c] = node < s.n ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    st_shared_v4(q_at + (uint32_t)((c ^ (r & 7)) << 4), w[c]);
+                for (int c = 0; c < 4; ++c)
+                    st_shared_v4(dst + (uint32_t)(((4 * half + c) ^ (r & 7)) << 4), w[c]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive_local(q_ready0 + 8u * t);
             }
-            float top = -INFINITY, sum = 0.0f;          // reference (log2) and sum of the row
-            bool unfinite = false;
+            int node[2];
+            float top[2], sum[2];                       // reference (log2) and this lane's sum
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = (u.tile * kRows + 128 * t + first + (lane >> 2) + 8 * e) / a.group;
+                node[e] = i < s.n ? i : -1;
+                top[e] = -INFINITY;
+                sum[e] = 0.0f;
+            }
             for (int j = 0; j < u.count; ++j, ++n) {
                 const int p0 = (u.k0 + j) * kKeyTile;
-                fine = wait(s_full0 + 8u * t, n & 1u, kFaultSoftmax);
+                fine = wait(s_full, n & 1u, kFaultSoftmax);
                 fine = __all_sync(0xFFFFFFFFu, fine);
                 if (!fine)
                     break;
                 tc_fence_after();
-                float x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32_async(tS + 32u * c, x + 32 * c);
+                float y[64];                            // y[4c + 2e + f]: row e, column 8c + 2 (l % 4) + f
+                tmem_ld_rows(tS, y);
+                tmem_ld_rows(tS + 64u, y + 32);
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    loaded32(x + 32 * c);
+                for (int c = 0; c < 8; ++c)
+                    loaded8(y + 8 * c);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_local(s_free0 + 8u * t);
                 const uint32_t st = n % kStages;
-                const bool last_keys = p0 + kKeyTile > s.ctx;
                 const uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
-                if (last_keys || bads != 0u) {
+                if (p0 + kKeyTile > s.ctx || bads != 0u) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t see = seen32(a, s, i, p0 + 32 * c);
-                        if (bads != 0u) {
-                            for (int k = 0; k < 32; ++k)
-                                if ((bads >> ((32 * c + k) / box)) & 1u)
-                                    see &= ~(1u << k);
-                        }
+                        uint32_t out = 0u;              // keys of blocks out of range
+                        for (int k = 0; bads != 0u && k < 32; ++k)
+                            out |= ((bads >> ((32 * c + k) / box)) & 1u) << k;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            x[32 * c + k] = (see >> k) & 1u ? x[32 * c + k] : -INFINITY;
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t see = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f)
+                                    if (!((see >> (8 * k + f)) & 1u))
+                                        y[4 * (4 * c + k) + 2 * e + f] = -INFINITY;
+                        }
                     }
-                }
-                if (last_keys) {
                     // the tile's V: zeros past the end, and in place of what is
-                    // not finite in drafted keys.  The groups share the work and
-                    // wait for one another; a piece that met such a value leaves
-                    // its number (in the word of its parity: a group is never two
-                    // tiles ahead of one that has not read it).
+                    // not finite in drafted keys.  Every row tile looks at all
+                    // of it; one that finds such a value says so (the number of
+                    // the piece) before it takes it out, so that the others,
+                    // who may see the zero, see the word too.
                     fine = wait(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
                     const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
-                    bool found = false;
-                    for (int e = threadIdx.x; e < kKeyTile * 8; e += 128 * kQ) {
-                        const int key = p0 + (e >> 3);
+                    for (int i = threadIdx.x & 255; i < kKeyTile * 8; i += 256) {
+                        const int key = p0 + (i >> 3);
                         if (key < s.ctx)
                             continue;
-                        const uint32_t chunk = v + 16u * e;
+                        const uint32_t chunk = v + 16u * i;
                         uint4 w = make_uint4(0, 0, 0, 0);
                         bool write = true;
                         if (key < s.keys) {
@@ -969,114 +1023,136 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                             write |= finite_only(w.y, true, true);
                             write |= finite_only(w.z, true, true);
                             write |= finite_only(w.w, true, true);
-                            found |= write;
+                            if (write) {
+                                *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) = piece + 1u;
+                                __threadfence_block();
+                            }
                         }
                         if (write)
                             st_shared_v4(chunk, w);
                     }
-                    if (found)
-                        *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 1u]) = piece + 1u;
+                    __threadfence_block();
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive_local(v_fixed);
-                    fine = wait(v_fixed, fixes & 1u, kFaultSoftmax) && fine;
-                    ++fixes;
-                    unfinite |= *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 1u]) == piece + 1u;
                 }
-                float m = max3(x[0], x[1], x[2]);
+                float m[2];
 #pragma unroll
-                for (int k = 3; k + 1 < 128; k += 2)
-                    m = max3(m, x[k], x[k + 1]);
-                m = fmaxf(m, x[127]) * a.scale_log2;
-                const bool grew = m > top + kGrow || (top == -INFINITY && m > -INFINITY);
-                if (__any_sync(0xFFFFFFFFu, grew)) {
-                    const float shrink = grew ? ex2(top - m) : 1.0f;    // top -inf: 0
+                for (int e = 0; e < 2; ++e) {
+                    float m0 = fmaxf(y[2 * e], y[2 * e + 1]), m1 = fmaxf(y[4 + 2 * e], y[5 + 2 * e]);
+#pragma unroll
+                    for (int c = 2; c < 16; c += 2) {
+                        m0 = max3(m0, y[4 * c + 2 * e], y[4 * c + 2 * e + 1]);
+                        m1 = max3(m1, y[4 * c + 4 + 2 * e], y[4 * c + 5 + 2 * e]);
+                    }
+                    m0 = fmaxf(m0, m1);
+                    m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
+                    m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
+                    m[e] = m0 * a.scale_log2;
+                }
+                // the products of the last tile have read P, and O holds them
+                if (n > 0)
+                    fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
+                tc_fence_after();
+                const bool grew[2] = {m[0] > top[0] + kGrow || (top[0] == -INFINITY && m[0] > -INFINITY),
+                                      m[1] > top[1] + kGrow || (top[1] == -INFINITY && m[1] > -INFINITY)};
+                if (__any_sync(0xFFFFFFFFu, grew[0] || grew[1])) {
+                    float shrink[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        shrink[e] = grew[e] ? ex2(top[e] - m[e]) : 1.0f;        // top -inf: 0
+                        sum[e] *= shrink[e];
+                        if (grew[e])
+                            top[e] = m[e];
+                    }
                     if (j > 0) {
-                        fine = wait(o_done0 + 8u * t, (n - 1) & 1u, kFaultSoftmax);
-                        tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float o[32];
-                            uint32_t w[32];
-                            tmem_ld32_async(tO + 32u * c, o);
+                        for (int c = 0; c < 4; ++c) {
+                            float o[8];
+                            tmem_ld_rows16(tO + 16u * c, o);
                             tmem_wait_ld();
-                            loaded32(o);
+                            loaded8(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                w[k] = __float_as_uint(o[k] * shrink);
-                            tmem_st32(tO + 32u * c, w);
+                            for (int k = 0; k < 8; ++k)
+                                o[k] *= shrink[(k >> 1) & 1];
+                            tmem_st_rows16(tO + 16u * c, o);
                         }
-                        tmem_wait_st();
                     }
-                    sum *= shrink;
-                    if (grew)
-                        top = m;
                 }
-                const float ref = top == -INFINITY ? 0.0f : -top;
-                float part[2] = {0.0f, 0.0f};
+                uint32_t w[32];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[32];
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = top[e] == -INFINITY ? 0.0f : -top[e];
+                    float part0 = 0.0f, part1 = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float x0 = x[64 * c + 2 * k], x1 = x[64 * c + 2 * k + 1];
-                        fma2_rn(x0, x1, a.scale_log2, a.scale_log2, ref, ref);
-                        x0 = ex2(x0);
-                        x1 = ex2(x1);
-                        add2_rn(part[0], part[1], x0, x1);
-                        w[k] = pack_bf16x2(x0, x1);
+                    for (int c = 0; c < 16; ++c) {
+                        float e0 = y[4 * c + 2 * e], e1 = y[4 * c + 2 * e + 1];
+                        fma2_rn(e0, e1, a.scale_log2, a.scale_log2, ref, ref);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        add2_rn(part0, part1, e0, e1);
+                        w[2 * c + e] = pack_bf16x2(e0, e1);
                     }
-                    tmem_st32(tS + 32u * c, w);
+                    sum[e] += part0 + part1;
                 }
+                tmem_st_pairs(tP, w);
                 tmem_wait_st();
-                sum += part[0] + part[1];
                 tc_fence_before();
-                mbar_arrive_local(p_ready0 + 8u * t);
+                mbar_arrive_local(p_ready);
             }
             if (!fine)
                 break;
-            // the row's output
-            fine = wait(o_done0 + 8u * t, (n - 1) & 1u, kFaultSoftmax);
+            // the rows' outputs
+            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax);
             fine = __all_sync(0xFFFFFFFFu, fine);
             if (!fine)
                 break;
             tc_fence_after();
-            float o[64];
-            tmem_ld32_async(tO, o);
-            tmem_ld32_async(tO + 32u, o + 32);
+            float o[32];                                // o[4c + 2e + f]: row e, column 8c + 2 (l % 4) + f
+            tmem_ld_rows(tO, o);
             tmem_wait_ld();
-            loaded32(o);
-            loaded32(o + 32);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                loaded8(o + 8 * c);
             tc_fence_before();
-            if (!u.whole()) {
-                float *slot = slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0));
-                const int rr = 128 * t + r;
+            const bool unfinite = *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) == piece + 1u;
+            const bool whole = u.whole();
+            float *slot = whole ? nullptr : slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0));
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    *reinterpret_cast<float4 *>(slot + kSlotOut<kRows> + rr * kHeadDim + 4 * k) =
-                        make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                slot[kSlotMax<kRows> + rr] = top;
-                slot[kSlotSum<kRows> + rr] = sum;
-                if (threadIdx.x == 0)
-                    write_header<kRows>(a, at, u, unfinite);
-            } else if (i >= 0) {
-                if (unfinite) {
+            for (int e = 0; e < 2; ++e) {
+                const int r = 128 * t + first + (lane >> 2) + 8 * e, row = u.tile * kRows + r, i = node[e];
+                float total = sum[e];
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, 1);
+                total += __shfl_xor_sync(0xFFFFFFFFu, total, 2);
+                if (!whole) {
+                    float *dst = slot + kSlotOut<kRows> + r * kHeadDim + 2 * (lane & 3);
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        o[k] = add_unfinite(a, s, u.b, u.h, i, k, o[k]);
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<float2 *>(dst + 8 * c) = make_float2(o[4 * c + 2 * e], o[4 * c + 2 * e + 1]);
+                    if ((lane & 3) == 0) {
+                        slot[kSlotMax<kRows> + r] = top[e];
+                        slot[kSlotSum<kRows> + r] = total;
+                    }
+                } else if (i >= 0) {
+                    const int head = u.h * a.group + row - i * a.group, col = 2 * (lane & 3);
+                    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+                    uint16_t *dst = a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float lo = o[4 * c + 2 * e], hi = o[4 * c + 2 * e + 1];
+                        if (unfinite) {
+                            lo = add_unfinite(a, s, u.b, u.h, i, 8 * c + col, lo);
+                            hi = add_unfinite(a, s, u.b, u.h, i, 8 * c + col + 1, hi);
+                        }
+                        *reinterpret_cast<uint32_t *>(dst + 8 * c) = pack_bf16x2(lo * inv, hi * inv);
+                    }
+                    if ((lane & 3) == 0 && a.lse != nullptr)
+                        a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
+                            total == 0.0f ? -INFINITY : __fmaf_rn(top[e], kLn2, logf(total));
                 }
-                const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-                uint4 *dst = reinterpret_cast<uint4 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                        pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                        pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                if (a.lse != nullptr)
-                    a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
-                        sum == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(sum));
-                if (threadIdx.x == 0 && u.unit == 0 && a.err != nullptr &&
-                    (int64_t)max(__ldg(a.context_len + u.b), 0) + s.n > s.keys)
+            }
+            if (threadIdx.x == 0) {
+                if (!whole)
+                    write_header<kRows>(a, at, u, unfinite);
+                else if (u.unit == 0 && a.err != nullptr && (int64_t)max(__ldg(a.context_len + u.b), 0) + s.n > s.keys)
                     atomicAdd(a.err, 1);
             }
             ++piece;
