@@ -617,9 +617,12 @@ k5_small(const __grid_constant__ Args a)
 // its rows and whole key tiles (a quad of lanes per row, as in m16n8 tiles:
 // the maximum takes two shuffles): 16 warps per SM hide one another's
 // latencies, where 8 warps of a row per thread ran at a third of the issue
-// rate.  O is rescaled only when a row's maximum has grown by more than 2^8
-// since its last reference (the weights then stay below 2^8, harmless in FP32
-// and bf16): by the row's own quad, a rare path.
+// rate.  A tile's weights are taken against the row's reference of the tiles
+// before it, without looking for the tile's own maximum: a sum above 2^8 makes
+// the next tile take a new reference (and rescale O), one above 2^64 this very
+// tile.  Until then weights above 1 are harmless, FP32 and bf16 having the
+// same range.  With the maximum first, all warps were in the exponentials at
+// the same time and out of them for the rest of it.
 //   loader warp      K and V tiles of 16 KiB by TMA, in boxes of the largest
 //                    power of two of keys that divides a block (8 to 128),
 //                    each box's block looked up in the table by its own lane
@@ -644,7 +647,8 @@ template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
 constexpr uint32_t kPCol = 128u, kOCol = 192u;
 template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
-constexpr float kGrow = 8.0f;                                      // log2: when O is rescaled
+constexpr float kGrow = 8.0f;                // log2: growth of a row's maximum at which O is rescaled
+constexpr float kMuch = 0x1p8f, kTooMuch = 0x1p64f;      // a lane's sum of a tile: see the kernel
 
 // mbar_wait_flag for the many waits of softmax threads: the timer is read (a
 // slow access) and the fault word looked at only once a few tries, each of
@@ -717,17 +721,14 @@ __device__ __forceinline__ void tmem_st_rows16(uint32_t at, const float *r) {
                  ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
                  : "memory");
 }
-// 64 columns of 16 lanes: w[2c] row l / 4, w[2c + 1] row l / 4 + 8, column
+// 32 columns of 16 lanes: w[2c] row l / 4, w[2c + 1] row l / 4 + 8, column
 // 4c + l % 4 (pairs of bf16: columns 8c + 2 (l % 4) and the next of P).
 __device__ __forceinline__ void tmem_st_pairs(uint32_t at, const uint32_t *w) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
         ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
-        "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]),
-        "r"(w[16]), "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]),
-        "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31])
+        "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -959,6 +960,12 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             }
             int node[2];
             float top[2], sum[2];                       // reference (log2) and this lane's sum
+            // A tile's weights are taken against the reference of the tiles
+            // before it, so that nothing waits for its maximum: `fresh` (a row
+            // has no reference yet, or has outgrown it: want) makes the tile
+            // look for its maxima first.
+            float want[2] = {-INFINITY, -INFINITY};
+            bool fresh = true;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = (u.tile * kRows + 128 * t + first + (lane >> 2) + 8 * e) / a.group;
@@ -973,35 +980,19 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 if (!fine)
                     break;
                 tc_fence_after();
-                float y[64];                            // y[4c + 2e + f]: row e, column 8c + 2 (l % 4) + f
-                tmem_ld_rows(tS, y);
-                tmem_ld_rows(tS + 64u, y + 32);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    loaded8(y + 8 * c);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_local(s_free0 + 8u * t);
                 const uint32_t st = n % kStages;
                 const uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
-                if (p0 + kKeyTile > s.ctx || bads != 0u) {
+                const bool edge = p0 + kKeyTile > s.ctx || bads != 0u;
+                uint32_t see[2][4];                     // edge: the keys that this lane's columns of each row see
+                if (edge) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
                         for (int k = 0; bads != 0u && k < 32; ++k)
                             out |= ((bads >> ((32 * c + k) / box)) & 1u) << k;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t see = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                                for (int f = 0; f < 2; ++f)
-                                    if (!((see >> (8 * k + f)) & 1u))
-                                        y[4 * (4 * c + k) + 2 * e + f] = -INFINITY;
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            see[e][c] = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
                     }
                     // the tile's V: zeros past the end, and in place of what is
                     // not finite in drafted keys.  Every row tile looks at all
@@ -1034,66 +1025,129 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                     __threadfence_block();
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                float m[2];
+                // half h of the scores: y[4c + 2e + f] is row e, key 64h + 8c + 2 (l % 4) + f
+                auto load = [&](int h, float (&y)[32]) {
+                    tmem_ld_rows(tS + 64u * h, y);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float m0 = fmaxf(y[2 * e], y[2 * e + 1]), m1 = fmaxf(y[4 + 2 * e], y[5 + 2 * e]);
+                    for (int c = 0; c < 4; ++c)
+                        loaded8(y + 8 * c);
+                    if (edge) {
 #pragma unroll
-                    for (int c = 2; c < 16; c += 2) {
-                        m0 = max3(m0, y[4 * c + 2 * e], y[4 * c + 2 * e + 1]);
-                        m1 = max3(m1, y[4 * c + 4 + 2 * e], y[4 * c + 5 + 2 * e]);
+                        for (int c = 0; c < 8; ++c)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f)
+                                    if (!((see[e][2 * h + (c >> 2)] >> (8 * (c & 3) + f)) & 1u))
+                                        y[4 * c + 2 * e + f] = -INFINITY;
                     }
-                    m0 = fmaxf(m0, m1);
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 1));
-                    m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, 2));
-                    m[e] = m0 * a.scale_log2;
-                }
-                // the products of the last tile have read P, and O holds them
-                if (n > 0)
-                    fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
-                tc_fence_after();
-                const bool grew[2] = {m[0] > top[0] + kGrow || (top[0] == -INFINITY && m[0] > -INFINITY),
-                                      m[1] > top[1] + kGrow || (top[1] == -INFINITY && m[1] > -INFINITY)};
-                if (__any_sync(0xFFFFFFFFu, grew[0] || grew[1])) {
-                    float shrink[2];
+                };
+                bool exact = edge || fresh;
+                float part[2][2];
+                for (;;) {
+                    if (exact) {
+                        // the tile's maxima (and what a tile before asked for)
+                        float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float y[32];
+                            load(h, y);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    m[e] = max3(m[e], y[4 * c + 2 * e], y[4 * c + 2 * e + 1]);
+                        }
+                        if (n > 0)                      // O holds the products of the tiles before
+                            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
+                        tc_fence_after();
+                        float shrink[2];
+                        bool grew = false;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 1));
+                            m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 2));
+                            m[e] = fmaxf(m[e] * a.scale_log2, want[e]);
+                            want[e] = -INFINITY;
+                            const bool g = m[e] > top[e] + kGrow || (top[e] == -INFINITY && m[e] > -INFINITY);
+                            shrink[e] = g ? ex2(top[e] - m[e]) : 1.0f;          // top -inf: 0
+                            sum[e] *= shrink[e];
+                            if (g)
+                                top[e] = m[e];
+                            grew |= g;
+                        }
+                        if (j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                float o[8];
+                                tmem_ld_rows16(tO + 16u * c, o);
+                                tmem_wait_ld();
+                                loaded8(o);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    o[k] *= shrink[(k >> 1) & 1];
+                                tmem_st_rows16(tO + 16u * c, o);
+                            }
+                        }
+                        fresh = __any_sync(0xFFFFFFFFu, top[0] == -INFINITY || top[1] == -INFINITY);
+                    }
+                    const float ref[2] = {top[0] == -INFINITY ? 0.0f : -top[0], top[1] == -INFINITY ? 0.0f : -top[1]};
+                    part[0][0] = part[0][1] = part[1][0] = part[1][1] = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float y[32];
+                        uint32_t w[16];
+                        load(h, y);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float e0 = y[4 * c + 2 * e], e1 = y[4 * c + 2 * e + 1];
+                                fma2_rn(e0, e1, a.scale_log2, a.scale_log2, ref[e], ref[e]);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                add2_rn(part[e][0], part[e][1], e0, e1);
+                                w[2 * c + e] = pack_bf16x2(e0, e1);
+                            }
+                        if (h == 0 && n > 0 && !exact) {
+                            // the products of the last tile have read P
+                            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
+                            tc_fence_after();
+                        }
+                        tmem_st_pairs(tP + 32u * h, w);
+                    }
+                    part[0][0] += part[0][1];
+                    part[1][0] += part[1][1];
+                    // Weights may pass 1 (the reference is that of earlier
+                    // tiles; FP32 and bf16 have the room), but past 2^8 the next
+                    // tile takes a new reference, and past 2^64 this one does.
+                    const bool much = !exact && (part[0][0] > kMuch || part[1][0] > kMuch);
+                    if (!__any_sync(0xFFFFFFFFu, much))
+                        break;
+                    bool again = false;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        shrink[e] = grew[e] ? ex2(top[e] - m[e]) : 1.0f;        // top -inf: 0
-                        sum[e] *= shrink[e];
-                        if (grew[e])
-                            top[e] = m[e];
+                        float x = part[e][0];
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                        again |= x > kTooMuch;
+                        if (x > kMuch)
+                            want[e] = top[e] + log2f(x);
                     }
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float o[8];
-                            tmem_ld_rows16(tO + 16u * c, o);
-                            tmem_wait_ld();
-                            loaded8(o);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                o[k] *= shrink[(k >> 1) & 1];
-                            tmem_st_rows16(tO + 16u * c, o);
-                        }
-                    }
+                    fresh = true;
+                    if (!__any_sync(0xFFFFFFFFu, again))
+                        break;
+                    want[0] = want[1] = -INFINITY;
+                    exact = true;
                 }
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = top[e] == -INFINITY ? 0.0f : -top[e];
-                    float part0 = 0.0f, part1 = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        float e0 = y[4 * c + 2 * e], e1 = y[4 * c + 2 * e + 1];
-                        fma2_rn(e0, e1, a.scale_log2, a.scale_log2, ref, ref);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        add2_rn(part0, part1, e0, e1);
-                        w[2 * c + e] = pack_bf16x2(e0, e1);
-                    }
-                    sum[e] += part0 + part1;
-                }
-                tmem_st_pairs(tP, w);
+                // the scores are read (and need no second look)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_local(s_free0 + 8u * t);
+                sum[0] += part[0][0];
+                sum[1] += part[1][0];
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive_local(p_ready);
