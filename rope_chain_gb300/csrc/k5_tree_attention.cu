@@ -617,12 +617,11 @@ k5_small(const __grid_constant__ Args a)
 // its rows and whole key tiles (a quad of lanes per row, as in m16n8 tiles:
 // the maximum takes two shuffles): 16 warps per SM hide one another's
 // latencies, where 8 warps of a row per thread ran at a third of the issue
-// rate.  A tile's weights are taken against the row's reference of the tiles
-// before it, without looking for the tile's own maximum: a sum above 2^8 makes
-// the next tile take a new reference (and rescale O), one above 2^64 this very
-// tile.  Until then weights above 1 are harmless, FP32 and bf16 having the
-// same range.  With the maximum first, all warps were in the exponentials at
-// the same time and out of them for the rest of it.
+// rate.  A row's reference (what its maximum is in a running softmax) is that of
+// an earlier tile until a score passes it by more than 2^8: weights above 1 are
+// harmless, FP32 and bf16 having the range.  So a tile's maximum needs no
+// shuffles, only a vote on whether a lane saw more, and O is rescaled rarely, by
+// the rows' own warp.
 //   loader warp      K and V tiles of 16 KiB by TMA, in boxes of the largest
 //                    power of two of keys that divides a block (8 to 128),
 //                    each box's block looked up in the table by its own lane
@@ -648,24 +647,37 @@ template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row ti
 constexpr uint32_t kPCol = 128u, kOCol = 192u;
 template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
 constexpr float kGrow = 8.0f;                // log2: growth of a row's maximum at which O is rescaled
-constexpr float kMuch = 0x1p8f, kTooMuch = 0x1p64f;      // a lane's sum of a tile: see the kernel
 
-// mbar_wait_flag for the many waits of softmax threads: the timer is read (a
-// slow access) and the fault word looked at only once a few tries, each of
-// which the hardware suspends for a while, have failed.
-__device__ __forceinline__ bool mbar_wait_patient(uint32_t bar, uint32_t parity, unsigned int *flag) {
-    unsigned long long t0 = 0;
+// The slow half of a wait: up to kWaitNs from its first look at the timer, or
+// until a fault has been raised; raises `fault` if the phase does not complete.
+__device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, unsigned fault) {
+    const unsigned long long t0 = globaltimer();
     for (uint32_t it = 0;; ++it) {
         if (mbar_try(bar, parity))
             return true;
-        if ((it & 31u) == 31u) {
-            const unsigned long long now = globaltimer();
-            if (t0 == 0)
-                t0 = now;
-            if (*reinterpret_cast<volatile unsigned int *>(flag) != 0u || now - t0 > kWaitNs)
-                return false;
+        if ((it & 31u) == 31u &&
+            (*reinterpret_cast<volatile unsigned int *>(&g_attention_faults) != 0u || globaltimer() - t0 > kWaitNs)) {
+            atomicOr(&g_attention_faults, fault);
+            return false;
         }
     }
+}
+// Wait for a phase: a few tries in line (each suspended by the hardware for a
+// while), then slowly; false once it has timed out or a fault has been raised.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned fault) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 i;\n\t"
+                 "mov.b32 i, 0;\n"
+                 "again_%=:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                 "@p bra done_%=;\n\t"
+                 "add.u32 i, i, 1;\n\t"
+                 "setp.lt.u32 q, i, 64;\n\t"
+                 "@q bra again_%=;\n"
+                 "done_%=:\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0u || wait_slowly(bar, parity, fault);
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int col, int off, int h, int blk,
@@ -818,13 +830,6 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     tc_fence_after();
     const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
     pdl_wait();
-    auto wait = [&](uint32_t bar, uint32_t parity, unsigned fault) {
-        if (mbar_wait_patient(bar, parity, &g_attention_faults))
-            return true;
-        atomicOr(&g_attention_faults, fault);
-        return false;
-    };
-
     const Place at = locate<kRows, kThreads>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
@@ -855,7 +860,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
                 if (bad && u.unit == 0 && off == 0 && a.err != nullptr)
                     atomicAdd(a.err, 1);                // once per block: at its first key
-                fine = wait(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
+                fine = wait_phase(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
                 fine = __all_sync(0xFFFFFFFFu, fine);
                 if (!fine)
                     break;
@@ -893,8 +898,8 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             // the scores of key tile i, once their columns are free
             auto scores = [&](uint32_t i) {
                 const uint32_t st = i % kStages;
-                if (!wait(full0 + 8u * st, (i / kStages) & 1u, kFaultMma) ||
-                    (i > 0 && !wait(s_free, (i - 1) & 1u, kFaultMma)))
+                if (!wait_phase(full0 + 8u * st, (i / kStages) & 1u, kFaultMma) ||
+                    (i > 0 && !wait_phase(s_free, (i - 1) & 1u, kFaultMma)))
                     return false;
                 tc_fence_after();
                 const uint32_t k = k0 + st * (2 * kTileBytes >> 4);
@@ -906,11 +911,11 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             };
             bool fine = true;
             while (fine && walk.next(a, u)) {
-                fine = wait(q_ready0 + 8u * t, piece & 1u, kFaultMma) && scores(n);
+                fine = wait_phase(q_ready0 + 8u * t, piece & 1u, kFaultMma) && scores(n);
                 for (int j = 0; j < u.count && fine; ++j, ++n) {
                     if (j + 1 < u.count)
                         fine = scores(n + 1);
-                    fine = fine && wait(p_ready, n & 1u, kFaultMma);
+                    fine = fine && wait_phase(p_ready, n & 1u, kFaultMma);
                     if (!fine)
                         break;
                     tc_fence_after();
@@ -938,8 +943,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         const uint32_t lanes = (uint32_t)first << 16;
         const uint32_t tS = tmem + lanes + 256u * t, tP = tS + kPCol, tO = tS + kOCol;
         const uint32_t s_full = s_full0 + 8u * t, p_ready = p_ready0 + 8u * t, o_done = o_done0 + 8u * t;
-        bool fine = true;
-        while (fine && walk.next(a, u)) {
+        // (a wait that fails has raised a fault: the tiles are gone through all
+        // the same, so that every barrier sees its arrivals)
+        while (walk.next(a, u)) {
             const Seq &s = u.s;
             {
                 // Q: thread i of the tile's 256 takes half of row i / 2
@@ -959,47 +965,58 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 mbar_arrive_local(q_ready0 + 8u * t);
             }
             int node[2];
-            float top[2], sum[2];                       // reference (log2) and this lane's sum
-            // A tile's weights are taken against the reference of the tiles
-            // before it, so that nothing waits for its maximum: `fresh` (a row
-            // has no reference yet, or has outgrown it: want) makes the tile
-            // look for its maxima first.
-            float want[2] = {-INFINITY, -INFINITY};
-            bool fresh = true;
+            // of each row: minus the reference (log2), the maximum that asks for
+            // another (-inf: none seen yet), this lane's sum
+            float ref[2], limit[2], sum[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = (u.tile * kRows + 128 * t + first + (lane >> 2) + 8 * e) / a.group;
                 node[e] = i < s.n ? i : -1;
-                top[e] = -INFINITY;
-                sum[e] = 0.0f;
+                ref[e] = sum[e] = 0.0f;
+                limit[e] = -INFINITY;
             }
             for (int j = 0; j < u.count; ++j, ++n) {
                 const int p0 = (u.k0 + j) * kKeyTile;
-                fine = wait(s_full, n & 1u, kFaultSoftmax);
-                fine = __all_sync(0xFFFFFFFFu, fine);
-                if (!fine)
-                    break;
+                wait_phase(s_full, n & 1u, kFaultSoftmax);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t st = n % kStages;
                 const uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
-                const bool edge = p0 + kKeyTile > s.ctx || bads != 0u;
-                uint32_t see[2][4];                     // edge: the keys that this lane's columns of each row see
-                if (edge) {
+                // y[32h + 4c + 2e + f]: row e, key 64h + 8c + 2 (l % 4) + f
+                float y[64];
+                tmem_ld_rows(tS, y);
+                tmem_ld_rows(tS + 64u, y + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    loaded8(y + 8 * c);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_local(s_free0 + 8u * t);
+                if (p0 + kKeyTile > s.ctx || bads != 0u) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
                         for (int k = 0; bads != 0u && k < 32; ++k)
                             out |= ((bads >> ((32 * c + k) / box)) & 1u) << k;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            see[e][c] = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t see = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f)
+                                    if (!((see >> (8 * k + f)) & 1u))
+                                        y[4 * (4 * c + k) + 2 * e + f] = -INFINITY;
+                        }
                     }
                     // the tile's V: zeros past the end, and in place of what is
                     // not finite in drafted keys.  Every row tile looks at all
                     // of it; one that finds such a value says so (the number of
                     // the piece) before it takes it out, so that the others,
                     // who may see the zero, see the word too.
-                    fine = wait(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
+                    wait_phase(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
                     const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
                     for (int i = threadIdx.x & 255; i < kKeyTile * 8; i += 256) {
                         const int key = p0 + (i >> 3);
@@ -1025,140 +1042,83 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                     __threadfence_block();
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                // half h of the scores: y[4c + 2e + f] is row e, key 64h + 8c + 2 (l % 4) + f
-                auto load = [&](int h, float (&y)[32]) {
-                    tmem_ld_rows(tS + 64u * h, y);
-                    tmem_wait_ld();
+                // this lane's maxima: past a row's reference by more than 2^8
+                // (or the first that it sees), the row takes a new one
+                float m[2];
+                bool grew = false;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        loaded8(y + 8 * c);
-                    if (edge) {
+                for (int e = 0; e < 2; ++e) {
+                    float m0 = fmaxf(y[2 * e], y[2 * e + 1]), m1 = fmaxf(y[4 + 2 * e], y[5 + 2 * e]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int f = 0; f < 2; ++f)
-                                    if (!((see[e][2 * h + (c >> 2)] >> (8 * (c & 3) + f)) & 1u))
-                                        y[4 * c + 2 * e + f] = -INFINITY;
+                    for (int c = 2; c < 16; c += 2) {
+                        m0 = max3(m0, y[4 * c + 2 * e], y[4 * c + 2 * e + 1]);
+                        m1 = max3(m1, y[4 * c + 4 + 2 * e], y[4 * c + 5 + 2 * e]);
                     }
-                };
-                bool exact = edge || fresh;
-                float part[2][2];
-                for (;;) {
-                    if (exact) {
-                        // the tile's maxima (and what a tile before asked for)
-                        float m[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float y[32];
-                            load(h, y);
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    m[e] = max3(m[e], y[4 * c + 2 * e], y[4 * c + 2 * e + 1]);
-                        }
-                        if (n > 0)                      // O holds the products of the tiles before
-                            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
-                        tc_fence_after();
-                        float shrink[2];
-                        bool grew = false;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 1));
-                            m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 2));
-                            m[e] = fmaxf(m[e] * a.scale_log2, want[e]);
-                            want[e] = -INFINITY;
-                            const bool g = m[e] > top[e] + kGrow || (top[e] == -INFINITY && m[e] > -INFINITY);
-                            shrink[e] = g ? ex2(top[e] - m[e]) : 1.0f;          // top -inf: 0
-                            sum[e] *= shrink[e];
-                            if (g)
-                                top[e] = m[e];
-                            grew |= g;
-                        }
-                        if (j > 0 && __any_sync(0xFFFFFFFFu, grew)) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                float o[8];
-                                tmem_ld_rows16(tO + 16u * c, o);
-                                tmem_wait_ld();
-                                loaded8(o);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    o[k] *= shrink[(k >> 1) & 1];
-                                tmem_st_rows16(tO + 16u * c, o);
-                            }
-                        }
-                        fresh = __any_sync(0xFFFFFFFFu, top[0] == -INFINITY || top[1] == -INFINITY);
-                    }
-                    const float ref[2] = {top[0] == -INFINITY ? 0.0f : -top[0], top[1] == -INFINITY ? 0.0f : -top[1]};
-                    part[0][0] = part[0][1] = part[1][0] = part[1][1] = 0.0f;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float y[32];
-                        uint32_t w[16];
-                        load(h, y);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float e0 = y[4 * c + 2 * e], e1 = y[4 * c + 2 * e + 1];
-                                fma2_rn(e0, e1, a.scale_log2, a.scale_log2, ref[e], ref[e]);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                                add2_rn(part[e][0], part[e][1], e0, e1);
-                                w[2 * c + e] = pack_bf16x2(e0, e1);
-                            }
-                        if (h == 0 && n > 0 && !exact) {
-                            // the products of the last tile have read P
-                            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax) && fine;
-                            tc_fence_after();
-                        }
-                        tmem_st_pairs(tP + 32u * h, w);
-                    }
-                    part[0][0] += part[0][1];
-                    part[1][0] += part[1][1];
-                    // Weights may pass 1 (the reference is that of earlier
-                    // tiles; FP32 and bf16 have the room), but past 2^8 the next
-                    // tile takes a new reference, and past 2^64 this one does.
-                    const bool much = !exact && (part[0][0] > kMuch || part[1][0] > kMuch);
-                    if (!__any_sync(0xFFFFFFFFu, much))
-                        break;
-                    bool again = false;
+                    m[e] = fmaxf(m0, m1) * a.scale_log2;
+                    grew |= m[e] > limit[e];
+                }
+                if (__any_sync(0xFFFFFFFFu, grew)) {
+                    if (n > 0)                          // O holds the products of the tiles before
+                        wait_phase(o_done, (n - 1) & 1u, kFaultSoftmax);
+                    tc_fence_after();
+                    float shrink[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = part[e][0];
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                        again |= x > kTooMuch;
-                        if (x > kMuch)
-                            want[e] = top[e] + log2f(x);
+                        m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 1));
+                        m[e] = fmaxf(m[e], __shfl_xor_sync(0xFFFFFFFFu, m[e], 2));
+                        shrink[e] = 1.0f;
+                        if (m[e] > limit[e]) {
+                            shrink[e] = limit[e] == -INFINITY ? 0.0f : ex2(-ref[e] - m[e]);
+                            sum[e] *= shrink[e];
+                            ref[e] = -m[e];
+                            limit[e] = m[e] + kGrow;
+                        }
                     }
-                    fresh = true;
-                    if (!__any_sync(0xFFFFFFFFu, again))
-                        break;
-                    want[0] = want[1] = -INFINITY;
-                    exact = true;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            float o[8];
+                            tmem_ld_rows16(tO + 16u * c, o);
+                            tmem_wait_ld();
+                            loaded8(o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                o[k] *= shrink[(k >> 1) & 1];
+                            tmem_st_rows16(tO + 16u * c, o);
+                        }
+                    }
                 }
-                // the scores are read (and need no second look)
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_local(s_free0 + 8u * t);
-                sum[0] += part[0][0];
-                sum[1] += part[1][0];
+                float part[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float e0 = y[32 * h + 4 * c + 2 * e], e1 = y[32 * h + 4 * c + 2 * e + 1];
+                            fma2_rn(e0, e1, a.scale_log2, a.scale_log2, ref[e], ref[e]);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            add2_rn(part[e][0], part[e][1], e0, e1);
+                            w[2 * c + e] = pack_bf16x2(e0, e1);
+                        }
+                    if (h == 0 && n > 0) {
+                        // the products of the last tile have read P
+                        wait_phase(o_done, (n - 1) & 1u, kFaultSoftmax);
+                        tc_fence_after();
+                    }
+                    tmem_st_pairs(tP + 32u * h, w);
+                }
+                sum[0] += part[0][0] + part[0][1];
+                sum[1] += part[1][0] + part[1][1];
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive_local(p_ready);
             }
-            if (!fine)
-                break;
             // the rows' outputs
-            fine = wait(o_done, (n - 1) & 1u, kFaultSoftmax);
-            fine = __all_sync(0xFFFFFFFFu, fine);
-            if (!fine)
-                break;
+            wait_phase(o_done, (n - 1) & 1u, kFaultSoftmax);
+            __syncwarp();
             tc_fence_after();
             float o[32];                                // o[4c + 2e + f]: row e, column 8c + 2 (l % 4) + f
             tmem_ld_rows(tO, o);
@@ -1176,13 +1136,14 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 float total = sum[e];
                 total += __shfl_xor_sync(0xFFFFFFFFu, total, 1);
                 total += __shfl_xor_sync(0xFFFFFFFFu, total, 2);
+                const float top = limit[e] == -INFINITY ? -INFINITY : -ref[e];
                 if (!whole) {
                     float *dst = slot + kSlotOut<kRows> + r * kHeadDim + 2 * (lane & 3);
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         *reinterpret_cast<float2 *>(dst + 8 * c) = make_float2(o[4 * c + 2 * e], o[4 * c + 2 * e + 1]);
                     if ((lane & 3) == 0) {
-                        slot[kSlotMax<kRows> + r] = top[e];
+                        slot[kSlotMax<kRows> + r] = top;
                         slot[kSlotSum<kRows> + r] = total;
                     }
                 } else if (i >= 0) {
@@ -1200,7 +1161,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                     }
                     if ((lane & 3) == 0 && a.lse != nullptr)
                         a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
-                            total == 0.0f ? -INFINITY : __fmaf_rn(top[e], kLn2, logf(total));
+                            total == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(total));
                 }
             }
             if (threadIdx.x == 0) {
