@@ -10,14 +10,13 @@
 //
 // The floor is one read and one write of the logits.  A CTA owns a tile of
 // the vocabulary for the rows of one sequence: it scans the history once,
-// counts the tile's tokens in shared memory, lists those that need arithmetic
-// and then streams its columns of every row, 16 bytes at a time.  Few tokens
-// are listed (what the history, the tree and the biases name), but they lie
-// scattered, so that computing them in place would make nearly every warp
-// walk the whole formula for a lane or two.  Instead the listed tokens of the
-// next row are computed side by side, one per thread, into shared memory while
-// the current row streams, and the stream only picks their values up where a
-// bit map says so.
+// counts the tile's tokens in shared memory, and then streams its columns of
+// every row, 16 bytes at a time, each warp by itself.  Few tokens need
+// arithmetic (what the history, the tree and the biases name); a bit map says
+// which, and a lane walks the set bits of its own few tokens, so that a warp
+// goes through the formula about once per 32 x 16 bytes however many lanes have
+// one.  The nodes that draft a token of the tile are a 64-bit set, so that a
+// row's count of it is a population count.
 #include "rc_internal.cuh"
 
 #include <algorithm>
@@ -28,9 +27,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPad = 32;                     // tokens kept before a tile (rows may start unaligned)
-constexpr int kNodes = 512;                  // drafted tokens a tile lists
+constexpr int kNodes = 256;                  // drafted tokens a tile lists
 constexpr uint32_t kPrompt = 1u << 31;       // count word: in the prompt
-constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: the count changes by row
+constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: the count differs by row
 constexpr uint32_t kBias = 1u << 29;         //   has a bias
 constexpr uint32_t kCount = kBias - 1;       //   occurrences in the generated history
 
@@ -59,23 +58,79 @@ __device__ __forceinline__ uint32_t window(const uint32_t *words, int at) {
 
 template <int kTile> struct Smem {
     static constexpr int kWords = kTile + kPad;
+    uint64_t set[kNodes];                            // the nodes that draft a listed token
     uint32_t word[kWords];                           // count and flags of a token
     uint32_t bias[kWords];                           // 1 + the entry of its bias, then the bias itself
-    float value[2][kWords];                          // a row's adjusted logits of the listed tokens
     uint32_t special[kWords / 32 + 2];               // bit: word != 0
-    uint16_t list[kWords];                           // the tokens with word != 0
-    int32_t node[kNodes];                            // the tile's drafted tokens: node index,
-    int32_t token[kNodes];                           //   and place in the tile
-    int32_t nodes, listed;
+    uint16_t listed[kWords];                         // where the drafted token's set is
+    int16_t node[kNodes], token[kNodes];             // a listed node, and its token's place in the tile
+    int32_t nodes;
 };
 
-// kAligned: `logits` and `out` rows start at the same offset from a 16-byte
-// boundary, so both move 16 bytes at a time; else element by element.
-template <typename T, int kTile, bool kAligned>
+// 16 bytes of logits, or one.
+template <typename T, int kVec> struct alignas(kVec > 1 ? 16 : sizeof(T)) Vec { T v[kVec]; };
+
+// A stretch of the history, four tokens a load where it is aligned: f(token).
+template <typename F>
+__device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
+    const int64_t lead = min(n, (int64_t)((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / 4);
+    if ((int64_t)threadIdx.x < lead)
+        f(__ldg(p + threadIdx.x));
+    const int64_t quads = (n - lead) / 4;
+    const int4 *q = reinterpret_cast<const int4 *>(p + lead);
+    for (int64_t i = threadIdx.x; i < quads; i += 4 * kThreads) {
+        int4 t[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * kThreads < quads)
+                t[j] = __ldg(q + i + j * kThreads);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j * kThreads < quads) {
+                f(t[j].x);
+                f(t[j].y);
+                f(t[j].z);
+                f(t[j].w);
+            }
+    }
+    const int64_t rest = n - lead - 4 * quads;
+    if ((int64_t)threadIdx.x < rest)
+        f(__ldg(p + n - rest + threadIdx.x));
+}
+
+// -inf where a token's bit of `ok` is not set.
+template <int kVec> __device__ __forceinline__ void mask_out(Vec<float, kVec> &v, uint32_t ok) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        v.v[j] = (ok >> j) & 1u ? v.v[j] : minus_inf<float>();
+}
+template <int kVec> __device__ __forceinline__ void mask_out(Vec<uint16_t, kVec> &v, uint32_t ok) {
+    if (kVec == 1) {
+        v.v[0] = ok & 1u ? v.v[0] : minus_inf<uint16_t>();
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; j += 2) {                  // two tokens a word
+        const uint32_t two = (ok >> j) & 3u;             // bits 0 and 1 to halves 0 and 1
+        const uint32_t keep = ((two | (two << 15)) & 0x00010001u) * 0xFFFFu;
+        uint32_t w = (uint32_t)v.v[j] | (uint32_t)v.v[j + 1 < kVec ? j + 1 : j] << 16;
+        w = (w & keep) | (0xFF80FF80u & ~keep);
+        v.v[j] = (uint16_t)w;
+        v.v[j + 1 < kVec ? j + 1 : j] = (uint16_t)(w >> 16);
+    }
+}
+
+// Rows move 16 bytes at a time where `logits` and `out` rows start at the same
+// offset from a 16-byte boundary (kVec > 1): a thread's vectors then start up
+// to kVec - 1 tokens (`shift`) before its place in the tile.  kSame: every row
+// has the same shift, so that where a thread's tokens lie, and which of them
+// are listed, is found once.  kR rows are in flight per thread.
+template <typename T, int kTile, int kVec, int kR, bool kSame>
 __global__ void __launch_bounds__(kThreads)
 k7_logits(const __grid_constant__ LogitsLaunch a)
 {
-    constexpr int kVec = kAligned ? Io<T>::kVec : 1;
+    constexpr int kPer = kTile / (kVec * kThreads);
+    using V = Vec<T, kVec>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Smem<kTile> &s = *reinterpret_cast<Smem<kTile> *>(smem_raw);
     pdl_trigger();
@@ -83,99 +138,121 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         s.word[i] = 0u;
         s.bias[i] = 0u;
     }
+    for (int i = threadIdx.x; i < kNodes; i += kThreads)
+        s.set[i] = 0u;
     if (threadIdx.x == 0)
-        s.nodes = s.listed = 0;
+        s.nodes = 0;
     __syncthreads();
     pdl_wait();
 
+    // (the sequence's scalars first: one latency for all of them)
     const int b = blockIdx.y;
-    const int first = blockIdx.x * kTile;            // the tile: tokens first - kPad + 1 on
+    const int64_t start0 = a.row_start[b], start1 = a.row_start[b + 1];
+    const int64_t hist0 = a.history != nullptr ? a.history_start[b] : 0;
+    const int64_t hist1 = a.history != nullptr ? a.history_start[b + 1] : 0;
+    const int32_t prompt = a.prompt_len != nullptr ? a.prompt_len[b] : 0;
+    const int32_t bias0 = a.bias_start != nullptr ? a.bias_start[b] : 0;
+    const int32_t bias1 = a.bias_start != nullptr ? a.bias_start[b + 1] : 0;
+    const float rep = a.repetition != nullptr ? a.repetition[b] : 1.0f;
+    const float freq = a.frequency != nullptr ? a.frequency[b] : 0.0f;
+    const float pres = a.presence != nullptr ? a.presence[b] : 0.0f;
+    const int first = blockIdx.x * kTile;            // the tile: tokens first - kVec + 1 on
     const int base = first - kPad;
-    const int r0 = (int)max((int64_t)0, min((int64_t)a.row_start[b], a.rows));
-    const int r1 = (int)max((int64_t)r0, min((int64_t)a.row_start[b + 1], a.rows));
+    const int r0 = (int)max((int64_t)0, min(start0, a.rows));
+    const int r1 = (int)max((int64_t)r0, min(start1, a.rows));
+    const int step = (int)gridDim.z;                 // this CTA's rows: r0 + blockIdx.z, + step, ...
     if (r0 + (int)blockIdx.z >= r1)
         return;
-    // counted by one CTA of the sequence
-    const bool teller = blockIdx.x == 0 && blockIdx.z == 0 && a.err != nullptr;
-    int bad = 0;
 
-    // Each row: its vectors and their mask bits are loaded while the row
-    // before it is worked on (the first while the history is counted).
-    struct alignas(kAligned ? 16 : sizeof(T)) Vec { T v[kVec]; };
-    constexpr int kPer = (kTile / kVec + kThreads - 1) / kThreads;
+    // A thread's vector k of a row: its first token, whether all of it is in
+    // the vocabulary, whether any is, and the shift of its bits in a mask word.
     const int words = (a.V + 31) / 32;
     auto shift_of = [&](int row) {
-        // vectors start on 16-byte boundaries: `shift` tokens before the tile
-        return kAligned ? (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
+        return kVec > 1 ? (int)((reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
                                                              (int64_t)row * a.row_stride) & 15u) / sizeof(T)) : 0;
     };
-    auto load = [&](int row, Vec (&v)[kPer], uint32_t (&ok)[kPer]) {
+    const int shift0 = shift_of(r0 + (int)blockIdx.z);
+    auto token = [&](int row, int k) {
+        return first - (kSame ? shift0 : shift_of(row)) + ((int)threadIdx.x + k * kThreads) * kVec;
+    };
+    // The rows of a turn: their vectors and mask words are loaded while those of
+    // the turn before are worked on (the first while the history is counted).
+    // Nothing here looks at what it loads: a thread that did would wait for
+    // each load in turn (measured: 6000 cycles a turn instead of 1000).
+    struct Words { uint32_t lo, hi; };               // around a vector's first token
+    auto load = [&](int row, V (&v)[kPer], Words (&ok)[kPer], uint64_t &see) {
+        see = a.tree_mask != nullptr ? __ldg(a.tree_mask + (int64_t)row * a.mask_words) : 0u;
         const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
         const uint32_t *mask = a.allowed != nullptr ? a.allowed + (int64_t)row * a.allowed_stride : nullptr;
-        const int shift = shift_of(row);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = (threadIdx.x + k * kThreads) * kVec, t = first - shift + i;
-            ok[k] = 0xFFFFFFFFu;
-            if (i >= kTile || t >= a.V)
+            const int t = token(row, k);
+            ok[k].lo = ok[k].hi = 0xFFFFFFFFu;
+            if (t + kVec <= 0 || t >= a.V)
                 continue;
             if (t >= 0 && t + kVec <= a.V) {
-                v[k] = *reinterpret_cast<const Vec *>(src + t);
+                v[k] = *reinterpret_cast<const V *>(src + t);
             } else {
+                // an end of the row
 #pragma unroll
                 for (int j = 0; j < kVec; ++j)
                     v[k].v[j] = t + j >= 0 && t + j < a.V ? src[t + j] : T(0);
             }
             if (mask != nullptr) {
-                // the mask words around t; before token 0 and past the last word: not used
-                const int w0 = t >> 5;
-                const uint32_t lo = w0 >= 0 ? __ldg(mask + w0) : 0u;
-                const uint32_t hi = (t & 31) + kVec > 32 && w0 + 1 < words ? __ldg(mask + w0 + 1) : 0u;
-                ok[k] = __funnelshift_r(lo, hi, t & 31);
+                const int w = t >> 5;                // (the word before token 0's is not there)
+                if (w >= 0)
+                    ok[k].lo = __ldg(mask + w);
+                if (kVec > 1 && (t & 31) + kVec > 32 && w + 1 < words)      // (only with a shift)
+                    ok[k].hi = __ldg(mask + w + 1);
             }
         }
     };
-    Vec next[kPer];
-    uint32_t next_ok[kPer];
+    V next[kR][kPer];
+    Words next_ok[kR][kPer];
+    uint64_t next_see[kR];
     int row = r0 + (int)blockIdx.z;
-    load(row, next, next_ok);
+#pragma unroll
+    for (int q = 0; q < kR; ++q)
+        if (row + q * step < r1)
+            load(row + q * step, next[q], next_ok[q], next_see[q]);
 
-    // The history's tokens of this tile.
+    // (so are this thread's first bias and drafted token)
+    const int64_t e0 = max((int64_t)0, min((int64_t)bias0, a.bias_size));
+    const int64_t e1 = max(e0, min((int64_t)bias1, a.bias_size));
+    const int32_t bias_token = e0 + threadIdx.x < e1 ? __ldg(a.bias_tokens + e0 + threadIdx.x) : 0;
+    const int32_t draft_token = a.draft_tokens != nullptr && r0 + (int)threadIdx.x < r1
+                                    ? __ldg(a.draft_tokens + r0 + threadIdx.x) : 0;
+
+    // The history's tokens of this tile (what lies outside the vocabulary may
+    // land beside it, where nothing is read): the prompt's marked, then the
+    // generated ones counted.
+    const bool teller = blockIdx.x == 0 && blockIdx.z == 0 && a.err != nullptr;
+    int bad = 0;                                     // counted by one CTA of the sequence
     if (a.history != nullptr) {
-        const int64_t h0 = max((int64_t)0, min(a.history_start[b], a.history_size));
-        const int64_t h1 = max(h0, min(a.history_start[b + 1], a.history_size));
-        const int64_t made = h0 + (a.prompt_len != nullptr ? max(a.prompt_len[b], 0) : 0);
-        for (int64_t i0 = h0 + threadIdx.x; i0 < h1; i0 += 8 * kThreads) {
-            int32_t t[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                t[j] = i0 + j * kThreads < h1 ? __ldg(a.history + i0 + j * kThreads) : 0x7FFFFFFF;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t i = i0 + j * kThreads;
-                if (i >= h1)
-                    break;
-                bad += t[j] < 0 || t[j] >= a.V;
-                const uint32_t at = (uint32_t)t[j] - (uint32_t)base;
-                if (t[j] >= 0 && t[j] < a.V && at < (uint32_t)(kTile + kPad)) {
-                    if (i < made)
-                        atomicOr(&s.word[at], kPrompt);
-                    else
-                        atomicAdd(&s.word[at], 1u);
-                }
-            }
-        }
+        const int64_t h0 = max((int64_t)0, min(hist0, a.history_size));
+        const int64_t h1 = max(h0, min(hist1, a.history_size));
+        const int64_t made = min(h1, h0 + max(prompt, 0));
+        each_token(a.history + h0, made - h0, [&](int32_t t) {
+            const uint32_t at = (uint32_t)t - (uint32_t)base;
+            if (at < (uint32_t)(kTile + kPad))
+                s.word[at] = kPrompt;
+            bad += teller && (t < 0 || t >= a.V);
+        });
+        __syncthreads();
+        each_token(a.history + made, h1 - made, [&](int32_t t) {
+            const uint32_t at = (uint32_t)t - (uint32_t)base;
+            if (at < (uint32_t)(kTile + kPad))
+                atomicAdd(&s.word[at], 1u);
+            bad += teller && (t < 0 || t >= a.V);
+        });
     }
-    __syncthreads();
     // The biases: a token listed twice takes its last entry.
     if (a.bias_start != nullptr) {
-        const int64_t e0 = max((int64_t)0, min((int64_t)a.bias_start[b], a.bias_size));
-        const int64_t e1 = max(e0, min((int64_t)a.bias_start[b + 1], a.bias_size));
         for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-            const int32_t t = __ldg(a.bias_tokens + e);
-            bad += t < 0 || t >= a.V;
+            const int32_t t = e < e0 + kThreads ? bias_token : __ldg(a.bias_tokens + e);
+            bad += teller && (t < 0 || t >= a.V);
             const uint32_t at = (uint32_t)t - (uint32_t)base;
-            if (t >= 0 && t < a.V && at < (uint32_t)(kTile + kPad)) {
+            if (at < (uint32_t)(kTile + kPad)) {
                 atomicOr(&s.word[at], kBias);
                 atomicMax(&s.bias[at], (uint32_t)(e + 1));
             }
@@ -184,169 +261,179 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     // The tokens drafted in this tree.
     if (a.draft_tokens != nullptr) {
         for (int r = r0 + threadIdx.x; r < r1; r += kThreads) {
-            const int32_t t = __ldg(a.draft_tokens + r);
-            bad += t < 0 || t >= a.V;
+            const int32_t t = r < r0 + kThreads ? draft_token : __ldg(a.draft_tokens + r);
+            bad += teller && (t < 0 || t >= a.V);
             const uint32_t at = (uint32_t)t - (uint32_t)base;
-            if (t >= 0 && t < a.V && at < (uint32_t)(kTile + kPad)) {
+            if (at < (uint32_t)(kTile + kPad)) {
                 atomicOr(&s.word[at], kDraft);
                 const int k = atomicAdd(&s.nodes, 1);
-                if (k < kNodes) {
-                    s.node[k] = r - r0;
-                    s.token[k] = (int32_t)at;
+                if (k < kNodes && r - r0 < 64) {
+                    s.node[k] = (int16_t)(r - r0);
+                    s.token[k] = (int16_t)at;
+                    s.listed[at] = (uint16_t)k;          // any one of a token's entries
                 }
             }
         }
     }
-    if (teller && bad)
+    if (bad)
         atomicAdd(a.err, bad);
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile + kPad + 64; i += kThreads) {     // a whole number of warps
-        const uint32_t w = i < kTile + kPad ? s.word[i] : 0u;
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, w != 0u);
-        const int lane = threadIdx.x & 31;
-        int at = 0;
-        if (lane == 0) {
-            s.special[i >> 5] = bits;
-            at = bits != 0u ? atomicAdd(&s.listed, __popc(bits)) : 0;
+    // Trees of more than 64 nodes, or that draft more of the tile than is
+    // listed, are walked node by node for each of their tokens.
+    const int nodes = s.nodes;
+    const bool few = r1 - r0 <= 64 && nodes <= kNodes;
+    if (few && threadIdx.x < nodes)
+        atomicOr(reinterpret_cast<unsigned long long *>(&s.set[s.listed[s.token[threadIdx.x]]]),
+                 1ull << s.node[threadIdx.x]);
+    {
+        constexpr int kGroups = (kTile + kPad + 64) / 32, kTurns = (kGroups + kThreads / 32 - 1) / (kThreads / 32);
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+        for (int g = 0; g < kTurns; ++g) {
+            const int at = warp + g * (kThreads / 32), i = at * 32 + lane;
+            const uint32_t w = i < kTile + kPad ? s.word[i] : 0u;
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, w != 0u);
+            if (lane == 0 && at < kGroups)
+                s.special[at] = bits;
+            if (w & kBias)
+                s.bias[i] = __float_as_uint(__ldg(a.bias_values + (s.bias[i] - 1u)));
         }
-        at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(bits & ((1u << lane) - 1u));
-        if (w != 0u)
-            s.list[at] = (uint16_t)i;
-        if (w & kBias)
-            s.bias[i] = __float_as_uint(__ldg(a.bias_values + (s.bias[i] - 1u)));
     }
     __syncthreads();
 
-    const float rep = a.repetition != nullptr ? a.repetition[b] : 1.0f;
-    const float freq = a.frequency != nullptr ? a.frequency[b] : 0.0f;
-    const float pres = a.presence != nullptr ? a.presence[b] : 0.0f;
-    const int listed = s.listed, nodes = s.nodes;
-
-    // The logits of row `row`'s listed tokens: thread i takes entries i, i +
-    // kThreads, ...; the first kAhead of them are loaded before they are due.
-    constexpr int kAhead = 2;
-    auto fetch = [&](int row, float (&x)[kAhead]) {
-        const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int e = threadIdx.x + k * kThreads;
-            const int t = e < listed ? base + s.list[e] : -1;
-            x[k] = t >= 0 && t < a.V ? Io<T>::load(src[t]) : 0.0f;
-        }
-    };
-    auto adjust = [&](int row, const float (&ahead)[kAhead], float *value) {
-        const T *src = static_cast<const T *>(a.logits) + (int64_t)row * a.row_stride;
-        const uint64_t *see = a.tree_mask != nullptr ? a.tree_mask + (int64_t)row * a.mask_words : nullptr;
-        auto sees = [&](int j) {
-            if (see == nullptr)
-                return j <= row - r0;
-            return (j >> 6) < a.mask_words && ((__ldg(see + (j >> 6)) >> (j & 63)) & 1u) != 0u;
-        };
-        auto one = [&](int e, float x) {
-            const int at = s.list[e];
-            const uint32_t w = s.word[at];
-            uint32_t g = w & kCount;
-            if (w & kDraft) {
-                if (nodes <= kNodes) {
-                    for (int k = 0; k < nodes; ++k)
-                        g += s.token[k] == at && sees(s.node[k]);
-                } else {
-                    for (int j = 0; j < r1 - r0; ++j)
-                        g += __ldg(a.draft_tokens + r0 + j) == at + base && sees(j);
+    // The logit of a token whose word is set, in row r, whose node sees `see`
+    // (its first 64 nodes).
+    auto adjusted = [&](int r, uint64_t see, int at, float x) {
+        const uint32_t w = s.word[at];
+        uint32_t g = w & kCount;
+        if (w & kDraft) {
+            if (few) {
+                g += __popcll(see & s.set[s.listed[at]]);
+            } else {
+                const uint64_t *all = a.tree_mask != nullptr ? a.tree_mask + (int64_t)r * a.mask_words : nullptr;
+                for (int j = 0; j < r1 - r0; ++j) {
+                    const bool sees = all == nullptr ? j <= r - r0
+                                                     : (j >> 6) < a.mask_words && ((__ldg(all + (j >> 6)) >> (j & 63)) & 1u);
+                    g += sees && __ldg(a.draft_tokens + r0 + j) == at + base;
                 }
             }
-            if (g != 0u || (w & kPrompt) != 0u)
-                x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-            x = __fsub_rn(x, __fmul_rn(freq, (float)g));
-            if (g != 0u)
-                x = __fsub_rn(x, pres);
-            if (w & kBias)
-                x = __fadd_rn(x, __uint_as_float(s.bias[at]));
-            value[at] = x;
-        };
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (threadIdx.x + k * kThreads < listed)
-                one(threadIdx.x + k * kThreads, ahead[k]);
-        for (int e = threadIdx.x + kAhead * kThreads; e < listed; e += kThreads)
-            one(e, Io<T>::load(src[base + s.list[e]]));
+        }
+        if (g != 0u || (w & kPrompt) != 0u)
+            x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+        x = __fsub_rn(x, __fmul_rn(freq, (float)g));
+        if (g != 0u)
+            x = __fsub_rn(x, pres);
+        if (w & kBias)
+            x = __fadd_rn(x, __uint_as_float(s.bias[at]));
+        return x;
     };
-    float ahead[kAhead];
-    fetch(row, ahead);
-    adjust(row, ahead, s.value[0]);
-    int turn = 0;
-    for (; row < r1; row += (int)gridDim.z) {
-        __syncthreads();                                 // this row's values are there, the last row's are free
-        Vec v[kPer];
-        uint32_t ok[kPer];
+    // which of a vector's tokens have their word set
+    auto special_in = [&](int t) { return window(s.special, max(t, first - kVec) - base) & ((1u << kVec) - 1u); };
+    uint32_t todo[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            v[k] = next[k];
-            ok[k] = next_ok[k];
-        }
-        const bool more = row + (int)gridDim.z < r1;
-        if (more) {
-            load(row + (int)gridDim.z, next, next_ok);
-            fetch(row + (int)gridDim.z, ahead);
-        }
-        const float *value = s.value[turn];
-        T *dst = static_cast<T *>(a.out) + (int64_t)row * a.out_row_stride;
-        const int shift = shift_of(row);
+    for (int k = 0; k < kPer; ++k)
+        todo[k] = special_in(token(row, k));
+    while (row < r1) {
+        V v[kR][kPer];
+        Words ok[kR][kPer];
+        uint64_t see[kR];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = (threadIdx.x + k * kThreads) * kVec;
-            const int t = first - shift + i;
-            if (i >= kTile || t >= a.V)
-                continue;
-            const int at = t - base;
-            const uint32_t todo = window(s.special, at) & ((1u << kVec) - 1u);
-            if (todo != 0u) {
+        for (int q = 0; q < kR; ++q) {
+            const int me = row + q * step - r0;
+            see[q] = a.tree_mask != nullptr ? next_see[q] : (me < 63 ? (2ull << me) - 1u : ~0ull);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    if ((todo >> j) & 1u)
-                        v[k].v[j] = Io<T>::store(value[at + j]);
-            }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                if (!((ok[k] >> j) & 1u))
-                    v[k].v[j] = minus_inf<T>();
-            if (t >= 0 && t + kVec <= a.V) {
-                *reinterpret_cast<Vec *>(dst + t) = v[k];
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    if (t + j >= 0 && t + j < a.V)
-                        dst[t + j] = v[k].v[j];
+            for (int k = 0; k < kPer; ++k) {
+                v[q][k] = next[q][k];
+                ok[q][k] = next_ok[q][k];
             }
         }
-        turn ^= 1;
-        if (more)
-            adjust(row + (int)gridDim.z, ahead, s.value[turn]);
+        const int coming = row + kR * step;
+#pragma unroll
+        for (int q = 0; q < kR; ++q)
+            if (coming + q * step < r1)
+                load(coming + q * step, next[q], next_ok[q], next_see[q]);
+#pragma unroll
+        for (int q = 0; q < kR; ++q) {
+            const int r = row + q * step;
+            if (r >= r1)
+                break;
+            T *dst = static_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int t = token(r, k);
+                uint32_t bits = kSame ? todo[k] : special_in(t);
+                while (bits != 0u) {
+                    const int j = __ffs(bits) - 1;
+                    bits &= bits - 1u;
+                    T x = v[q][k].v[0];
+#pragma unroll
+                    for (int i = 1; i < kVec; ++i)
+                        x = i == j ? v[q][k].v[i] : x;
+                    x = Io<T>::store(adjusted(r, see[q], t + j - base, Io<T>::load(x)));
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        v[q][k].v[i] = i == j ? x : v[q][k].v[i];
+                }
+                mask_out(v[q][k], __funnelshift_r(ok[q][k].lo, ok[q][k].hi, t & 31));
+                if (t >= 0 && t + kVec <= a.V) {
+                    *reinterpret_cast<V *>(dst + t) = v[q][k];
+                } else if (t + kVec > 0 && t < a.V) {
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j)
+                        if (t + j >= 0 && t + j < a.V)
+                            dst[t + j] = v[q][k].v[j];
+                }
+            }
+        }
+        row = coming;
     }
 }
 
-template <typename T, int kTile, bool kAligned>
+template <typename T, int kTile, int kVec, int kR, bool kSame>
 cudaError_t launch_one(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 {
     const size_t smem = sizeof(Smem<kTile>);
     static bool configured[64] = {};
+    static int resident[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    auto kernel = k7_logits<T, kTile, kAligned>;
-    if (dev >= 64 || !configured[dev]) {
+    auto kernel = k7_logits<T, kTile, kVec, kR, kSame>;
+    int per_sm = dev < 64 && configured[dev] ? resident[dev] : 0;
+    if (per_sm == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
         if (e != cudaSuccess)
             return e;
-        if (dev < 64)
+        per_sm = std::max(per_sm, 1);
+        if (dev < 64) {
+            resident[dev] = per_sm;
             configured[dev] = true;
+        }
     }
     // a row's vectors start up to kVec - 1 tokens before its first token
-    const int64_t tiles = ((int64_t)a.V + (kAligned ? Io<T>::kVec - 1 : 0) + kTile - 1) / kTile;
-    // a sequence's rows are shared out to as many CTAs as fill the GPU
-    const int64_t rows = std::max<int64_t>(1, a.rows / a.seqs);
-    const int64_t chunks = std::min<int64_t>(rows, std::max<int64_t>(1, 4LL * num_sms / (tiles * a.seqs)));
+    const int64_t tiles = ((int64_t)a.V + kVec - 1 + kTile - 1) / kTile;
+    // A sequence's rows are shared out to as many CTAs as finish soonest.  A CTA's
+    // start (the scan of the history and the list) takes as long as some
+    // eight rows.
+    constexpr int64_t kLeast = 8;
+    const int64_t rows = std::max<int64_t>(1, (a.rows + a.seqs - 1) / a.seqs), units = tiles * a.seqs;
+    const int64_t wave = (int64_t)per_sm * num_sms;
+    int64_t chunks = 1;
+    double best = 0.0;
+    for (int64_t c = 1; c <= std::max<int64_t>(1, std::min<int64_t>(rows / kLeast, 64)); ++c) {
+        const int64_t waves = (units * c + wave - 1) / wave;
+        const double rate = 1.0 / (waves * ((rows + c - 1) / c + (double)kLeast));
+        if (rate > best * 1.02) {
+            best = rate;
+            chunks = c;
+        }
+    }
+    // too few to fill the GPU once: as many as fill it
+    if (units * chunks < wave)
+        chunks = std::max(chunks, std::min<int64_t>(rows, wave / units));
     return launch_pdl(kernel, dim3((unsigned)tiles, (unsigned)a.seqs, (unsigned)chunks), dim3(kThreads),
                       smem, stream, 1, a);
 }
@@ -354,14 +441,20 @@ cudaError_t launch_one(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 template <typename T>
 cudaError_t launch_type(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 {
+    constexpr int kVec = Io<T>::kVec;
     const uintptr_t src = reinterpret_cast<uintptr_t>(a.logits), dst = reinterpret_cast<uintptr_t>(a.out);
-    const bool aligned = (src & 15u) == (dst & 15u) &&
-                         (a.rows <= 1 || ((a.row_stride - a.out_row_stride) * (int64_t)sizeof(T)) % 16 == 0);
-    if ((int64_t)((a.V + 2047) / 2048) * a.seqs >= 2 * num_sms)
-        return aligned ? launch_one<T, 2048, true>(a, num_sms, stream)
-                       : launch_one<T, 2048, false>(a, num_sms, stream);
-    return aligned ? launch_one<T, 1024, true>(a, num_sms, stream)
-                   : launch_one<T, 1024, false>(a, num_sms, stream);
+    const bool one = a.rows <= 1;
+    if ((src & 15u) != (dst & 15u) || (!one && ((a.row_stride - a.out_row_stride) * (int64_t)sizeof(T)) % 16 != 0))
+        return launch_one<T, 1024, 1, 1, true>(a, num_sms, stream);
+    const bool same = one || (a.row_stride * (int64_t)sizeof(T)) % 16 == 0;
+    // wide tiles (two accesses per thread and row) scan the history half as
+    // often; narrow ones give twice the CTAs where there are few
+    constexpr int kNarrow = kThreads * kVec, kWide = 2 * kNarrow;
+    if ((int64_t)((a.V + kWide - 1) / kWide) * a.seqs >= 2 * num_sms)
+        return same ? launch_one<T, kWide, kVec, 2, true>(a, num_sms, stream)
+                    : launch_one<T, kWide, kVec, 2, false>(a, num_sms, stream);
+    return same ? launch_one<T, kNarrow, kVec, 2, true>(a, num_sms, stream)
+                : launch_one<T, kNarrow, kVec, 2, false>(a, num_sms, stream);
 }
 
 }  // namespace
