@@ -33,23 +33,73 @@ constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: the count
 constexpr uint32_t kBias = 1u << 29;         //   has a bias
 constexpr uint32_t kCount = kBias - 1;       //   occurrences in the generated history
 
-template <typename T> struct Io;
-template <> struct Io<float> {
-    static constexpr int kVec = 4;
-    static __device__ __forceinline__ float load(float v) { return v; }
-    static __device__ __forceinline__ float store(float v) { return v; }
-};
-template <> struct Io<uint16_t> {
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ float load(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-    static __device__ __forceinline__ uint16_t store(float v) {
-        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// kVec logits of one access as 32-bit words: FP32 values, or bf16 in pairs (a
+// single one alone).
+template <typename T, int kVec> struct Vec;
+template <int kVec> struct alignas(kVec > 1 ? 16 : 4) Vec<float, kVec> {
+    float w[kVec];
+    __device__ __forceinline__ void load(const float *p) { *this = *reinterpret_cast<const Vec *>(p); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<Vec *>(p) = *this; }
+    __device__ __forceinline__ float get(int j) const {
+        float x = w[0];
+#pragma unroll
+        for (int i = 1; i < kVec; ++i)
+            x = i == j ? w[i] : x;
+        return x;
+    }
+    __device__ __forceinline__ void set(int j, float x) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            w[i] = i == j ? x : w[i];
+    }
+    // -inf where a token's bit of `ok` is not set
+    __device__ __forceinline__ void mask(uint32_t ok) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            w[i] = (ok >> i) & 1u ? w[i] : __int_as_float((int)0xFF800000);
     }
 };
-
-template <typename T> __device__ __forceinline__ T minus_inf();
-template <> __device__ __forceinline__ float minus_inf<float>() { return __int_as_float((int)0xFF800000); }
-template <> __device__ __forceinline__ uint16_t minus_inf<uint16_t>() { return 0xFF80u; }
+template <> struct alignas(16) Vec<uint16_t, 8> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ float get(int j) const {
+        const uint32_t lo = j & 2 ? w[1] : w[0], hi = j & 2 ? w[3] : w[2], x = j & 4 ? hi : lo;
+        return __uint_as_float(j & 1 ? x & 0xFFFF0000u : x << 16);
+    }
+    __device__ __forceinline__ void set(int j, float x) {
+        const uint32_t v = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t with = j & 1 ? (w[i] & 0xFFFFu) | (v << 16) : (w[i] & 0xFFFF0000u) | v;
+            w[i] = i == j >> 1 ? with : w[i];
+        }
+    }
+    __device__ __forceinline__ void mask(uint32_t ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t two = (ok >> (2 * i)) & 3u;       // bits 0 and 1 to halves 0 and 1
+            const uint32_t keep = ((two | (two << 15)) & 0x00010001u) * 0xFFFFu;
+            w[i] = (w[i] & keep) | (0xFF80FF80u & ~keep);
+        }
+    }
+};
+template <> struct Vec<uint16_t, 1> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *p; }
+    __device__ __forceinline__ void store(uint16_t *p) const { *p = (uint16_t)w; }
+    __device__ __forceinline__ float get(int) const { return __uint_as_float(w << 16); }
+    __device__ __forceinline__ void set(int, float x) { w = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+    __device__ __forceinline__ void mask(uint32_t ok) { w = ok & 1u ? w : 0xFF80u; }
+};
 
 // 32 bits of a bit map (words 32 bits wide) from bit `at` on.
 __device__ __forceinline__ uint32_t window(const uint32_t *words, int at) {
@@ -66,9 +116,6 @@ template <int kTile> struct Smem {
     int16_t node[kNodes], token[kNodes];             // a listed node, and its token's place in the tile
     int32_t nodes;
 };
-
-// 16 bytes of logits, or one.
-template <typename T, int kVec> struct alignas(kVec > 1 ? 16 : sizeof(T)) Vec { T v[kVec]; };
 
 // A stretch of the history, four tokens a load where it is aligned: f(token).
 template <typename F>
@@ -96,28 +143,6 @@ __device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
     const int64_t rest = n - lead - 4 * quads;
     if ((int64_t)threadIdx.x < rest)
         f(__ldg(p + n - rest + threadIdx.x));
-}
-
-// -inf where a token's bit of `ok` is not set.
-template <int kVec> __device__ __forceinline__ void mask_out(Vec<float, kVec> &v, uint32_t ok) {
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-        v.v[j] = (ok >> j) & 1u ? v.v[j] : minus_inf<float>();
-}
-template <int kVec> __device__ __forceinline__ void mask_out(Vec<uint16_t, kVec> &v, uint32_t ok) {
-    if (kVec == 1) {
-        v.v[0] = ok & 1u ? v.v[0] : minus_inf<uint16_t>();
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < kVec; j += 2) {                  // two tokens a word
-        const uint32_t two = (ok >> j) & 3u;             // bits 0 and 1 to halves 0 and 1
-        const uint32_t keep = ((two | (two << 15)) & 0x00010001u) * 0xFFFFu;
-        uint32_t w = (uint32_t)v.v[j] | (uint32_t)v.v[j + 1 < kVec ? j + 1 : j] << 16;
-        w = (w & keep) | (0xFF80FF80u & ~keep);
-        v.v[j] = (uint16_t)w;
-        v.v[j + 1 < kVec ? j + 1 : j] = (uint16_t)(w >> 16);
-    }
 }
 
 // Rows move 16 bytes at a time where `logits` and `out` rows start at the same
@@ -191,12 +216,15 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             if (t + kVec <= 0 || t >= a.V)
                 continue;
             if (t >= 0 && t + kVec <= a.V) {
-                v[k] = *reinterpret_cast<const V *>(src + t);
+                v[k].load(src + t);
             } else {
                 // an end of the row
-#pragma unroll
                 for (int j = 0; j < kVec; ++j)
-                    v[k].v[j] = t + j >= 0 && t + j < a.V ? src[t + j] : T(0);
+                    if (t + j >= 0 && t + j < a.V) {
+                        Vec<T, 1> one;
+                        one.load(src + t + j);
+                        v[k].set(j, one.get(0));
+                    }
             }
             if (mask != nullptr) {
                 const int w = t >> 5;                // (the word before token 0's is not there)
@@ -224,8 +252,8 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
                                     ? __ldg(a.draft_tokens + r0 + threadIdx.x) : 0;
 
     // The history's tokens of this tile (what lies outside the vocabulary may
-    // land beside it, where nothing is read): the prompt's marked, then the
-    // generated ones counted.
+    // land beside it, where nothing is read): the prompt's marked, the generated
+    // ones counted.
     const bool teller = blockIdx.x == 0 && blockIdx.z == 0 && a.err != nullptr;
     int bad = 0;                                     // counted by one CTA of the sequence
     if (a.history != nullptr) {
@@ -235,10 +263,9 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         each_token(a.history + h0, made - h0, [&](int32_t t) {
             const uint32_t at = (uint32_t)t - (uint32_t)base;
             if (at < (uint32_t)(kTile + kPad))
-                s.word[at] = kPrompt;
+                atomicOr(&s.word[at], kPrompt);
             bad += teller && (t < 0 || t >= a.V);
         });
-        __syncthreads();
         each_token(a.history + made, h1 - made, [&](int32_t t) {
             const uint32_t at = (uint32_t)t - (uint32_t)base;
             if (at < (uint32_t)(kTile + kPad))
@@ -365,23 +392,18 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
                 while (bits != 0u) {
                     const int j = __ffs(bits) - 1;
                     bits &= bits - 1u;
-                    T x = v[q][k].v[0];
-#pragma unroll
-                    for (int i = 1; i < kVec; ++i)
-                        x = i == j ? v[q][k].v[i] : x;
-                    x = Io<T>::store(adjusted(r, see[q], t + j - base, Io<T>::load(x)));
-#pragma unroll
-                    for (int i = 0; i < kVec; ++i)
-                        v[q][k].v[i] = i == j ? x : v[q][k].v[i];
+                    v[q][k].set(j, adjusted(r, see[q], t + j - base, v[q][k].get(j)));
                 }
-                mask_out(v[q][k], __funnelshift_r(ok[q][k].lo, ok[q][k].hi, t & 31));
+                v[q][k].mask(__funnelshift_r(ok[q][k].lo, ok[q][k].hi, t & 31));
                 if (t >= 0 && t + kVec <= a.V) {
-                    *reinterpret_cast<V *>(dst + t) = v[q][k];
+                    v[q][k].store(dst + t);
                 } else if (t + kVec > 0 && t < a.V) {
-#pragma unroll
                     for (int j = 0; j < kVec; ++j)
-                        if (t + j >= 0 && t + j < a.V)
-                            dst[t + j] = v[q][k].v[j];
+                        if (t + j >= 0 && t + j < a.V) {
+                            Vec<T, 1> one;
+                            one.set(0, v[q][k].get(j));
+                            one.store(dst + t + j);
+                        }
                 }
             }
         }
@@ -441,15 +463,19 @@ cudaError_t launch_one(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 template <typename T>
 cudaError_t launch_type(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 {
-    constexpr int kVec = Io<T>::kVec;
+    constexpr int kVec = 16 / (int)sizeof(T);
     const uintptr_t src = reinterpret_cast<uintptr_t>(a.logits), dst = reinterpret_cast<uintptr_t>(a.out);
     const bool one = a.rows <= 1;
     if ((src & 15u) != (dst & 15u) || (!one && ((a.row_stride - a.out_row_stride) * (int64_t)sizeof(T)) % 16 != 0))
         return launch_one<T, 1024, 1, 1, true>(a, num_sms, stream);
     const bool same = one || (a.row_stride * (int64_t)sizeof(T)) % 16 == 0;
     // wide tiles (two accesses per thread and row) scan the history half as
-    // often; narrow ones give twice the CTAs where there are few
-    constexpr int kNarrow = kThreads * kVec, kWide = 2 * kNarrow;
+    // often, very wide ones (four) where a CTA has a row or two, so that its
+    // start is shared by more; narrow ones give twice the CTAs where there are
+    // few
+    constexpr int kNarrow = kThreads * kVec, kWide = 2 * kNarrow, kVery = 4 * kNarrow;
+    if (same && a.rows <= 2LL * a.seqs && (int64_t)((a.V + kVery - 1) / kVery) * a.seqs >= 4 * num_sms)
+        return launch_one<T, kVery, kVec, 1, true>(a, num_sms, stream);
     if ((int64_t)((a.V + kWide - 1) / kWide) * a.seqs >= 2 * num_sms)
         return same ? launch_one<T, kWide, kVec, 2, true>(a, num_sms, stream)
                     : launch_one<T, kWide, kVec, 2, false>(a, num_sms, stream);
