@@ -1184,21 +1184,22 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 
 // ----------------------------------------------------------- joining parts
 //
-// Block (c, y) joins kJoinRows rows of the unit that CTA c began and did not
-// end: its own part and those of the CTAs after it, in key order.  The parts'
-// weights are made first, one per thread, then four groups of 64 threads (16
-// columns of four, four rows) add every fourth part each, and the groups are
-// added in order.
-constexpr int kJoinThreads = 256, kJoinRows = 4, kJoinParts = 512;
+// Block (c, y) joins rows of the unit that CTA c began and did not end: its own
+// part and those of the CTAs after it, in key order.  A thread has four columns
+// of a row; with few rows (kRows <= 32: units cut into many parts) four groups
+// of threads take every fourth part each and are joined in order at the end.  A
+// thread loads eight parts' maxima, sums and columns at once, so that the few
+// parts of a unit of many rows cost one latency.
+constexpr int kJoinThreads = 256;
+template <int kRows> constexpr int kJoinRows = kRows <= 32 ? 4 : 16;
 
 template <int kRows>
 __global__ void __launch_bounds__(kJoinThreads)
 k5_join(const __grid_constant__ Args a)
 {
-    __shared__ float s_part[kJoinParts][kJoinRows];        // the part's maximum, then its weight
-    __shared__ float s_sum[kJoinParts][kJoinRows];
-    __shared__ float4 s_out[3][64];
-    __shared__ float s_top[kJoinRows], s_total[kJoinRows];
+    constexpr int kGroups = kJoinThreads / (16 * kJoinRows<kRows>), kBatch = 8;
+    __shared__ float4 s_out[kGroups][16 * kJoinRows<kRows>];
+    __shared__ float s_top[kGroups][kJoinRows<kRows>], s_sum[kGroups][kJoinRows<kRows>];
     pdl_trigger();
     pdl_wait();
     const int c = blockIdx.x;
@@ -1209,82 +1210,91 @@ k5_join(const __grid_constant__ Args a)
     const Seq s = seq_of(a, hd.b);
     const int rt = row_tiles<kRows>(a, s);
     const int h = hd.unit / rt, tile = hd.unit - h * rt;
-    const int r0 = blockIdx.y * kJoinRows, parts = hd.last - c + 1;
+    const int r0 = blockIdx.y * kJoinRows<kRows>, parts = hd.last - c + 1;
     if (threadIdx.x == 0 && blockIdx.y == 0 && hd.unit == 0 && a.err != nullptr &&
         (int64_t)max(__ldg(a.context_len + hd.b), 0) + s.n > s.keys)
         atomicAdd(a.err, 1);
     if (tile * kRows + r0 >= s.n * a.group)
         return;
-    auto part_of = [&](int k) { return k == 0 ? own : slot_of<kRows>(a, 2 * (int64_t)(c + k)); };
-    const int group = threadIdx.x >> 6, r = (threadIdx.x >> 4) & 3, col = (threadIdx.x & 15) * 4;
-    bool unfinite = false;
+    const int group = threadIdx.x / (16 * kJoinRows<kRows>), col = (threadIdx.x & 15) * 4;
+    const int r = (threadIdx.x >> 4) % kJoinRows<kRows>;
+    int unfinite = 0;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float top = -INFINITY, total = 0.0f;
-    // more parts than the table holds are joined in runs of kJoinParts
-    for (int k0 = 0; k0 < parts; k0 += kJoinParts) {
-        const int n = min(kJoinParts, parts - k0);
-        for (int i = threadIdx.x; i < n * kJoinRows; i += kJoinThreads) {
-            const float *part = part_of(k0 + i / kJoinRows);
-            s_part[i / kJoinRows][i % kJoinRows] = part[kSlotMax<kRows> + r0 + i % kJoinRows];
-            s_sum[i / kJoinRows][i % kJoinRows] = part[kSlotSum<kRows> + r0 + i % kJoinRows];
-            unfinite |= reinterpret_cast<const Header *>(part)->unfinite != 0;
-        }
-        unfinite = __syncthreads_or(unfinite) != 0;
-        if (threadIdx.x < kJoinRows * 32) {                // a warp per row
-            const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-            float m = k0 == 0 ? -INFINITY : s_top[row];
-            const float before = m;
-            for (int k = lane; k < n; k += 32)
-                m = fmaxf(m, s_part[k][row]);
+    for (int k0 = group; k0 < parts; k0 += kBatch * kGroups) {
+        float m[kBatch], l[kBatch];
+        float4 y[kBatch];
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const float ref = m == -INFINITY ? 0.0f : m;
-            float sum = 0.0f;
-            for (int k = lane; k < n; k += 32) {
-                const float f = ex2(s_part[k][row] - ref);
-                s_part[k][row] = f;
-                sum = __fmaf_rn(s_sum[k][row], f, sum);
-            }
-            sum = warp_butterfly_sum(sum);
-            if (lane == 0) {
-                s_total[row] = k0 == 0 ? sum : __fmaf_rn(s_total[row], ex2(before - ref), sum);
-                s_top[row] = m;
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = k0 + i * kGroups;
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+            y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k < parts) {
+                const float *part = k == 0 ? own : slot_of<kRows>(a, 2 * (int64_t)(c + k));
+                m[i] = part[kSlotMax<kRows> + r0 + r];
+                l[i] = part[kSlotSum<kRows> + r0 + r];
+                y[i] = *reinterpret_cast<const float4 *>(part + kSlotOut<kRows> + (r0 + r) * kHeadDim + col);
+                unfinite |= reinterpret_cast<const Header *>(part)->unfinite;
             }
         }
-        __syncthreads();
-        const float shrink = k0 == 0 ? 0.0f : ex2(top - (s_top[r] == -INFINITY ? 0.0f : s_top[r]));
-        top = s_top[r];
-        total = s_total[r];
+        float now = top;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            now = fmaxf(now, m[i]);
+        const float ref = now == -INFINITY ? 0.0f : now, shrink = ex2(top - ref);
+        top = now;
+        total *= shrink;
         x.x *= shrink;
         x.y *= shrink;
         x.z *= shrink;
         x.w *= shrink;
-#pragma unroll 8
-        for (int k = group; k < n; k += 4) {
-            const float f = s_part[k][r];
-            const float4 y = *reinterpret_cast<const float4 *>(part_of(k0 + k) + kSlotOut<kRows> + (r0 + r) * kHeadDim + col);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (k0 + i * kGroups >= parts)
+                break;
+            const float f = ex2(m[i] - ref);
+            total = __fmaf_rn(l[i], f, total);
+            x.x = __fmaf_rn(y[i].x, f, x.x);
+            x.y = __fmaf_rn(y[i].y, f, x.y);
+            x.z = __fmaf_rn(y[i].z, f, x.z);
+            x.w = __fmaf_rn(y[i].w, f, x.w);
+        }
+    }
+    if (kGroups > 1) {
+        s_out[group][threadIdx.x % (16 * kJoinRows<kRows>)] = x;
+        if (col == 0) {
+            s_top[group][r] = top;
+            s_sum[group][r] = total;
+        }
+        unfinite = __syncthreads_or(unfinite);
+        if (group > 0)
+            return;
+        float now = top;
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g)
+            now = fmaxf(now, s_top[g][r]);
+        const float ref = now == -INFINITY ? 0.0f : now, f0 = ex2(top - ref);
+        top = now;
+        total *= f0;
+        x.x *= f0;
+        x.y *= f0;
+        x.z *= f0;
+        x.w *= f0;
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+            const float f = ex2(s_top[g][r] - ref);
+            const float4 y = s_out[g][threadIdx.x];
+            total = __fmaf_rn(s_sum[g][r], f, total);
             x.x = __fmaf_rn(y.x, f, x.x);
             x.y = __fmaf_rn(y.y, f, x.y);
             x.z = __fmaf_rn(y.z, f, x.z);
             x.w = __fmaf_rn(y.w, f, x.w);
         }
-        __syncthreads();
     }
-    if (group > 0)
-        s_out[group - 1][threadIdx.x & 63] = x;
-    __syncthreads();
     const int row = tile * kRows + r0 + r, i = row / a.group;
-    if (group > 0 || i >= s.n)
+    if (i >= s.n)
         return;
-#pragma unroll
-    for (int g = 0; g < 3; ++g) {
-        const float4 y = s_out[g][threadIdx.x];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-    }
     const int head = h * a.group + row - i * a.group;
     if (unfinite) {
         x.x = add_unfinite(a, s, hd.b, h, i, col, x.x);
@@ -1343,7 +1353,7 @@ template <int kRows> cudaError_t launch_join(const Args &a, int ctas, cudaStream
     if (a.partial == nullptr)
         return cudaSuccess;
     *why = "tree attention join launch";
-    return launch_pdl(k5_join<kRows>, dim3((unsigned)ctas, kRows / kJoinRows), dim3(kJoinThreads), 0, stream, 1, a);
+    return launch_pdl(k5_join<kRows>, dim3((unsigned)ctas, kRows / kJoinRows<kRows>), dim3(kJoinThreads), 0, stream, 1, a);
 }
 
 template <int kTiles>
@@ -1407,7 +1417,11 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     if ((int64_t)p.table_width * p.block_size <= a.min_tiles * kKeyTile)
         a.partial = nullptr;
     const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
-    const int ctas = ctas_of(v, num_sms);
+    // as many CTAs as fill the GPU, or as the block table lets have work
+    const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
+    const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)p.table_width * p.block_size + kKeyTile - 1) / kKeyTile);
+    const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, units * tiles / a.min_tiles));
     switch (v) {
     case kSmall16: return launch_small<1>(a, ctas, stream, why);
     case kSmall32: return launch_small<2>(a, ctas, stream, why);
