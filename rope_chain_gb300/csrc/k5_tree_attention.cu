@@ -32,6 +32,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kKeyTile = 128;          // keys per step of a CTA
+constexpr float kGrow = 8.0f;          // log2: growth of a row's maximum at which its output is rescaled
 
 struct Args : TreeAttentionLaunch {
     float scale_log2;                  // scale * log2 e
@@ -205,13 +206,16 @@ __device__ __forceinline__ bool sees(const Args &a, const Seq &s, int i, int j) 
            ((__ldg(a.tree_mask + (int64_t)(s.r0 + i) * a.mask_words + (j >> 6)) >> (j & 63)) & 1u) != 0u;
 }
 
-// Element offset of logical key p's row in the cache, -1 without a valid block.
-__device__ __forceinline__ int64_t key_offset(const Args &a, int b, int h, int p) {
-    const uint32_t bs = (uint32_t)a.block_size, page = (uint32_t)p / bs;
-    const int32_t blk = __ldg(a.block_table + b * a.table_stride + page);
+// Logical key p's block, as the table has it, and with it the element offset of
+// the key's row in the cache (-1 without a valid block).
+__device__ __forceinline__ int32_t block_of(const Args &a, int b, int p) {
+    return __ldg(a.block_table + b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size);
+}
+__device__ __forceinline__ int64_t offset_in(const Args &a, int32_t blk, int h, int p) {
+    const uint32_t bs = (uint32_t)a.block_size;
     if (blk < 0 || blk >= a.num_blocks)
         return -1;
-    return (((int64_t)blk * a.kv_heads + h) * bs + ((uint32_t)p - page * bs)) * (2 * kHeadDim);
+    return (((int64_t)blk * a.kv_heads + h) * bs + (uint32_t)p % bs) * (2 * kHeadDim);
 }
 
 // The header of this CTA's part of a split unit.
@@ -238,7 +242,7 @@ __device__ __noinline__ float add_unfinite(const Args &a, const Seq &s, int b, i
     for (int j = 0; j < min(s.n, s.keys - s.ctx); ++j) {
         if (!sees(a, s, i, j))
             continue;
-        const int64_t o = key_offset(a, b, h, s.ctx + j);
+        const int64_t o = offset_in(a, block_of(a, b, s.ctx + j), h, s.ctx + j);
         const uint32_t v = o < 0 ? 0u : (uint32_t)a.cache[o + kHeadDim + d] << 16;
         if ((v & 0x7F800000u) == 0x7F800000u)
             x += __uint_as_float(v);
@@ -303,7 +307,8 @@ __device__ __forceinline__ bool finite_only(uint32_t &w, bool lo, bool hi) {
     return x || y;
 }
 
-template <int kTiles>
+// kRuns: blocks hold a multiple of 16 keys, so a chunk is 4 KiB in a row.
+template <int kTiles, bool kRuns>
 __global__ void __launch_bounds__(kSmallThreads, kTiles == 1 ? 2 : 1)
 k5_small(const __grid_constant__ Args a)
 {
@@ -346,13 +351,15 @@ k5_small(const __grid_constant__ Args a)
                     qf[m][k][e] = node[m][e & 1] >= 0 ? __ldg(src[e & 1] + 8 * k + (lane & 3) + 4 * (e >> 1)) : 0u;
             }
         }
-        float o[kTiles][8][4], top[kTiles][2], sum[kTiles][2];
+        // ref, limit: as in the wide kernel (a row's reference moves when a score
+        // passes it by 2^8)
+        float o[kTiles][8][4], ref[kTiles][2], limit[kTiles][2], sum[kTiles][2];
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                top[m][e] = -INFINITY;
-                sum[m][e] = 0.0f;
+                limit[m][e] = -INFINITY;
+                ref[m][e] = sum[m][e] = 0.0f;
             }
 #pragma unroll
             for (int n = 0; n < 8; ++n)
@@ -362,58 +369,92 @@ k5_small(const __grid_constant__ Args a)
         }
         bool unfinite = false;
 
-        // Chunk j's key of this lane: its row's offset in the cache, -1 for
-        // none.  Looked up one chunk before the copies that use it.
-        auto look_up = [&](int j) -> int64_t {
-            const int p = (k0 + j) * kKeyTile + warp * kChunk + (lane & 15);
-            if (j >= count || p >= s.keys)
-                return -1;
-            const int64_t src = key_offset(a, b, h, p);
-            if (src < 0 && lane < 16 && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
-                atomicAdd(a.err, 1);                   // once per block: at its first key
-            return src;
+        // Where chunks lie.  Block numbers are loaded well before they are looked
+        // at (a warp that looks waits): with kRuns a lane has chunk j & ~31 +
+        // lane, 32 chunks ahead, else a key of the next chunk.
+        const int lane_key = kRuns ? lane * kKeyTile : lane & 15;
+        auto first_key = [&](int j) { return (k0 + j) * kKeyTile + warp * kChunk; };
+        auto table_entry = [&](int j) -> int32_t {          // for this lane's key at or after chunk j
+            const int p = first_key(j) + lane_key;
+            return j + (kRuns ? lane : 0) < count && p < s.keys ? block_of(a, b, p) : -1;
         };
-        int64_t from = look_up(0);
-        auto issue = [&](int j) {
-            const int st = j % kStages;
-            const uint32_t real = __ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu;
-            const int64_t first = __shfl_sync(0xFFFFFFFFu, from, 0);
-            // a chunk in one block is 4 KiB in a row (any block size where it
-            // happens to be; always with blocks of a multiple of 16)
-            const bool run = __all_sync(0xFFFFFFFFu, from == first + (lane & 15) * (2 * kHeadDim)) && first >= 0;
-            if (lane == 0)
-                s_real[warp][st] = real;
-            const uint32_t at = ring + st * kChunkBytes + ((lane >> 3) & 1) * (kChunkBytes / 2) + (lane >> 4) * 128;
-            if (run) {
-                const uint16_t *src = a.cache + first + 8 * lane;
+        int32_t entry = table_entry(0);
+        int64_t from = -1;
+        auto place = [&](int j) {                           // this lane's row from `entry`
+            const int p = first_key(j) + lane_key;
+            const bool there = j + (kRuns ? lane : 0) < count && p < s.keys;
+            from = there ? offset_in(a, entry, h, p) : -1;
+            // once per block that is out of range: at its first key
+            if (there && from < 0 && (kRuns || lane < 16) && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
+                atomicAdd(a.err, 1);
+        };
+        const uint32_t lane_at = ((lane >> 3) & 1) * (kChunkBytes / 2) + (lane >> 4) * 128;
+        uint32_t swizzled[4];
 #pragma unroll
-                for (int i = 0; i < kChunk / 2; ++i)
-                    copy16_real(at + i * 256 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) << 4), src + i * (4 * kHeadDim));
+        for (int i = 0; i < 4; ++i)
+            swizzled[i] = lane_at + i * 256 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) << 4);
+        auto issue = [&](int j, int st) {
+            const uint32_t at = ring + st * kChunkBytes;
+            if (kRuns) {
+                if ((j & 31) == 0) {
+                    place(j);
+                    entry = table_entry(j + 32);
+                }
+                const int64_t first = __shfl_sync(0xFFFFFFFFu, from, j & 31);
+                const int keys = first < 0 ? 0 : min(kChunk, s.keys - first_key(j));
+                if (lane == 0)
+                    s_real[warp][st] = (1u << keys) - 1u;
+                const uint16_t *src = a.cache + (first < 0 ? 0 : first) + 8 * lane;
+                if (keys == kChunk) {
+#pragma unroll
+                    for (int i = 0; i < kChunk / 2; ++i)
+                        copy16_real(at + swizzled[i & 3] + (i >> 2) * 1024, src + i * (4 * kHeadDim));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kChunk / 2; ++i)
+                        copy16(at + swizzled[i & 3] + (i >> 2) * 1024, src + i * (4 * kHeadDim),
+                               2 * i + (lane >> 4) < keys);
+                }
             } else {
+                place(j);
+                entry = table_entry(j + 1);
+                const uint32_t real = __ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu;
+                if (lane == 0)
+                    s_real[warp][st] = real;
 #pragma unroll
                 for (int i = 0; i < kChunk / 2; ++i) {
                     const int64_t row = __shfl_sync(0xFFFFFFFFu, from, 2 * i + (lane >> 4));
-                    copy16(at + i * 256 + (((lane & 7) ^ ((2 * i + (lane >> 4)) & 7)) << 4),
+                    copy16(at + swizzled[i & 3] + (i >> 2) * 1024,
                            a.cache + (row >= 0 ? row + 8 * (lane & 15) : 0), row >= 0);
                 }
             }
-            from = look_up(j + 1);
         };
+        // ldmatrix addresses within a stage: K by halves of 8 keys, V transposed
+        uint32_t k_lane[4], v_lane[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int kr = (lane >> 4) * 8 + (lane & 7), vr = ((lane >> 3) & 1) * 8 + (lane & 7);
+            k_lane[k] = ring + kr * 128 + (((2 * k + ((lane >> 3) & 1)) ^ (kr & 7)) << 4);
+            v_lane[k] = ring + kChunkBytes / 2 + vr * 128 + (((2 * k + (lane >> 4)) ^ (vr & 7)) << 4);
+        }
 #pragma unroll
         for (int j = 0; j < kStages - 1; ++j) {
             if (j < count)
-                issue(j);
+                issue(j, j);
             copy_commit();
         }
+        int st = 0, st_in = kStages - 1;                    // stages of chunks j and j + kStages - 1
         for (int j = 0; j < count; ++j) {
             copy_wait<kStages - 2>();
             __syncwarp();
             if (j + kStages - 1 < count)
-                issue(j + kStages - 1);
+                issue(j + kStages - 1, st_in);
             copy_commit();
-            const uint32_t k_at = ring + (j % kStages) * kChunkBytes, v_at = k_at + kChunkBytes / 2;
-            const int p0 = (k0 + j) * kKeyTile + warp * kChunk;
-            const uint32_t real = s_real[warp][j % kStages];
+            st_in = st;
+            const uint32_t at = st * kChunkBytes;
+            const int p0 = first_key(j);
+            const uint32_t real = s_real[warp][st];
+            st = st + 1 == kStages ? 0 : st + 1;
             const bool drafted = p0 + kChunk > s.ctx;
             float t[kTiles][2][4];
 #pragma unroll
@@ -426,8 +467,7 @@ k5_small(const __grid_constant__ Args a)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t kf[4];
-                const int row = (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
-                load4(kf, k_at + row * 128 + ((c ^ (row & 7)) << 4));
+                load4(kf, k_lane[k] + at);
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m) {
                     mma16816(t[m][0], qf[m][k], kf[0], kf[1]);
@@ -454,25 +494,28 @@ k5_small(const __grid_constant__ Args a)
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(fmaxf(t[m][0][2 * e], t[m][0][2 * e + 1]),
-                                    fmaxf(t[m][1][2 * e], t[m][1][2 * e + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-                    now[m][e] = fmaxf(top[m][e], x * a.scale_log2);
-                    grew |= now[m][e] > top[m][e];
+                    now[m][e] = fmaxf(fmaxf(t[m][0][2 * e], t[m][0][2 * e + 1]),
+                                      fmaxf(t[m][1][2 * e], t[m][1][2 * e + 1])) * a.scale_log2;
+                    grew |= now[m][e] > limit[m][e];
                 }
             if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float shrink = now[m][e] == -INFINITY ? 1.0f : ex2(top[m][e] - now[m][e]);
-                        top[m][e] = now[m][e];
-                        sum[m][e] *= shrink;
+                        float x = now[m][e];
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+                        if (x > limit[m][e]) {
+                            const float shrink = limit[m][e] == -INFINITY ? 0.0f : ex2(-ref[m][e] - x);
+                            ref[m][e] = -x;
+                            limit[m][e] = x + kGrow;
+                            sum[m][e] *= shrink;
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
-                            o[m][n][2 * e] *= shrink;
-                            o[m][n][2 * e + 1] *= shrink;
+                            for (int n = 0; n < 8; ++n) {
+                                o[m][n][2 * e] *= shrink;
+                                o[m][n][2 * e + 1] *= shrink;
+                            }
                         }
                     }
             }
@@ -480,17 +523,16 @@ k5_small(const __grid_constant__ Args a)
             for (int m = 0; m < kTiles; ++m) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float ref = top[m][e] == -INFINITY ? 0.0f : -top[m][e];
-                    float part = 0.0f;
+                    float part0 = 0.0f, part1 = 0.0f;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            float &w = t[m][n][2 * e + f];
-                            w = ex2(__fmaf_rn(w, a.scale_log2, ref));
-                            part += w;
-                        }
-                    sum[m][e] += part;
+                    for (int n = 0; n < 2; ++n) {
+                        float &x0 = t[m][n][2 * e], &x1 = t[m][n][2 * e + 1];
+                        fma2_rn(x0, x1, a.scale_log2, a.scale_log2, ref[m][e], ref[m][e]);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        add2_rn(part0, part1, x0, x1);
+                    }
+                    sum[m][e] += part0 + part1;
                 }
                 pf[m][0] = pack_bf16x2(t[m][0][0], t[m][0][1]);
                 pf[m][1] = pack_bf16x2(t[m][0][2], t[m][0][3]);
@@ -500,8 +542,7 @@ k5_small(const __grid_constant__ Args a)
 #pragma unroll
             for (int n = 0; n < 8; n += 2) {
                 uint32_t vf[4];
-                const int row = ((lane >> 3) & 1) * 8 + (lane & 7), c = n + (lane >> 4);
-                load4_t(vf, v_at + row * 128 + ((c ^ (row & 7)) << 4));
+                load4_t(vf, v_lane[n / 2] + at);
                 if (drafted) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -529,7 +570,7 @@ k5_small(const __grid_constant__ Args a)
                 x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
                 if ((lane & 3) == 0) {
                     const int r = m * 16 + 8 * e + (lane >> 2);
-                    s_max[warp][r] = top[m][e];
+                    s_max[warp][r] = limit[m][e] == -INFINITY ? -INFINITY : -ref[m][e];
                     s_sum[warp][r] = x;
                 }
             }
@@ -546,7 +587,7 @@ k5_small(const __grid_constant__ Args a)
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     now = fmaxf(now, s_max[w][m * 16 + r]);
-                const float f = ex2(top[m][e] - (now == -INFINITY ? 0.0f : now));
+                const float f = limit[m][e] == -INFINITY ? 0.0f : ex2(-ref[m][e] - now);
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     // two columns of row r; the column pairs of odd rows are
@@ -646,7 +687,6 @@ template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
 constexpr uint32_t kPCol = 128u, kOCol = 192u;
 template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
-constexpr float kGrow = 8.0f;                // log2: growth of a row's maximum at which O is rescaled
 
 // The slow half of a wait: up to kWaitNs from its first look at the timer, or
 // until a fault has been raised; raises `fault` if the phase does not complete.
@@ -849,7 +889,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             auto look_up = [&](int j) -> int {
                 const int p = (u.k0 + j) * kKeyTile + lane * box;
                 return j < u.count && lane < boxes && p < s.keys
-                           ? __ldg(a.block_table + u.b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size) : 0;
+                           ? block_of(a, u.b, p) : 0;
             };
             int blk = look_up(0);
             for (int j = 0; j < u.count; ++j, ++n) {
@@ -1356,15 +1396,15 @@ template <int kRows> cudaError_t launch_join(const Args &a, int ctas, cudaStream
     return launch_pdl(k5_join<kRows>, dim3((unsigned)ctas, kRows / kJoinRows<kRows>), dim3(kJoinThreads), 0, stream, 1, a);
 }
 
-template <int kTiles>
+template <int kTiles, bool kRuns>
 cudaError_t launch_small(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     static bool configured[64] = {};
-    cudaError_t e = allow_smem(k5_small<kTiles>, kSmallSmem<kTiles>, configured);
+    cudaError_t e = allow_smem(k5_small<kTiles, kRuns>, kSmallSmem<kTiles>, configured);
     if (e != cudaSuccess)
         return e;
     *why = "tree attention launch";
-    e = launch_pdl(k5_small<kTiles>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
+    e = launch_pdl(k5_small<kTiles, kRuns>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
     return e != cudaSuccess ? e : launch_join<16 * kTiles>(a, ctas, stream, why);
 }
 
@@ -1423,8 +1463,10 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)p.table_width * p.block_size + kKeyTile - 1) / kKeyTile);
     const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, units * tiles / a.min_tiles));
     switch (v) {
-    case kSmall16: return launch_small<1>(a, ctas, stream, why);
-    case kSmall32: return launch_small<2>(a, ctas, stream, why);
+    case kSmall16: return p.block_size % kChunk == 0 ? launch_small<1, true>(a, ctas, stream, why)
+                                                     : launch_small<1, false>(a, ctas, stream, why);
+    case kSmall32: return p.block_size % kChunk == 0 ? launch_small<2, true>(a, ctas, stream, why)
+                                                     : launch_small<2, false>(a, ctas, stream, why);
     case kWide128: return launch_wide<1>(a, ctas, stream, why);
     default: return launch_wide<2>(a, ctas, stream, why);
     }
