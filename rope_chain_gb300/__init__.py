@@ -15,6 +15,7 @@ tree_attention and logits_adjust.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -185,18 +186,6 @@ def _check(status: int) -> None:
 def _stream(stream) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
-
-
-# torch.cuda.current_stream().cuda_stream without its objects (2.9 us a call
-# on the GB300's host, this 0.2 us: the drafted tokens' calls take a few us).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_raw_device = getattr(torch._C, "_cuda_getDevice", None)
-
-
-def _fast_stream(stream) -> int:
-    if stream is not None or _raw_stream is None or _raw_device is None:
-        return _stream(stream)
-    return _raw_stream(_raw_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -765,40 +754,29 @@ def read_device_faults(clear: bool = True) -> int:
 
 # ------------------------------------------------- the drafted tokens' step
 #
-# These calls take a few us on the GPU, so their host side counts: each
-# attribute of a tensor is read once, and what is wrong is found out apart.
+# These calls take a few us on the GPU, so they go through a module of their own
+# (csrc/py_draft.cpp) instead of ctypes: it checks the tensors, makes the output
+# and calls the same C ABI.
 
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_fn = {}
-
-
-def _bound(name: str):
-    """The library's function, looked up once."""
-    f = _fn.get(name)
-    if f is None:
-        f = _fn[name] = getattr(lib(), name)
-    return f
+_draft_module = None
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    d = t.dtype
-    if d is _BF16:
-        return RC_BF16
-    if d is _F32:
-        return RC_F32
-    raise TypeError(f"{name} must be bfloat16 or float32")
-
-
-def _array(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, name: str) -> Optional[int]:
-    """The pointer of a contiguous CUDA array of at least ``numel`` elements
-    (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
-        return t.data_ptr()
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    raise ValueError(f"{name} needs {numel} elements, it has {t.numel()}")
+def _draft():
+    """The module, loaded on first use; raises if it has not been built."""
+    global _draft_module
+    if _draft_module is None:
+        lib()
+        path = os.path.join(_HERE, "_draft.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is missing: build it first "
+                "(python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_file_location(__name__ + "._draft", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(RopeChainError)
+        _draft_module = module
+    return _draft_module
 
 
 def rope_table(max_position: int, rot_dim: int = HEAD_DIM, *, theta: float = 10000.0,
@@ -813,19 +791,14 @@ def rope_table(max_position: int, rot_dim: int = HEAD_DIM, *, theta: float = 100
     kind = ROPE_SCALINGS.get(scaling)
     if kind is None:
         raise ValueError(f"unknown scaling {scaling!r}: one of {sorted(ROPE_SCALINGS)}")
-    if out is None:
-        out = torch.empty((max_position, rot_dim), dtype=dtype,
-                          device="cuda" if device is None else device)
-        if not out.is_cuda:
-            raise ValueError("the table is made on a CUDA device")
-    elif out.shape != (max_position, rot_dim) or not out.is_cuda or not out.is_contiguous():
-        raise ValueError("out must be a contiguous CUDA tensor [max_position, rot_dim]")
-    sc = RopeScaling(kind, factor, original_max_position, beta_fast, beta_slow, attention_factor)
-    st = _bound("rc_rope_table")(out.data_ptr(), _dtype(out, "out"), max_position, rot_dim, theta,
-                                 sc, _fast_stream(stream))
-    if st:
-        _check(st)
-    return out
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError("dtype must be bfloat16 or float32")
+    if device is not None and not isinstance(device, torch.device):
+        device = torch.device(device)
+    return (_draft_module or _draft()).rope_table(
+        max_position, rot_dim, theta, kind, factor, original_max_position, beta_fast, beta_slow,
+        attention_factor, dtype is torch.float32, device, out,
+        None if stream is None else stream.cuda_stream)
 
 
 def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *,
@@ -838,36 +811,8 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
     in the first rot_dim elements of each head; the rest is copied.
     ``inverse``: the transposed rotation (the gradient with respect to x, given
     that of the output).  ``out`` may be x (in place)."""
-    T, heads, head_dim = shape = x.shape
-    dtype = x.dtype
-    x_row, x_head, x_last = x.stride()
-    if out is None:
-        if not x.is_cuda:
-            raise TypeError("x must be a CUDA tensor")
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-        out_head = head_dim
-        out_row = heads * head_dim
-    else:
-        if out.shape != shape or out.dtype is not dtype:
-            raise ValueError("out must have the shape and dtype of x")
-        if not x.is_cuda or not out.is_cuda:
-            raise TypeError("x and out must be CUDA tensors")
-        out_row, out_head, out_last = out.stride()
-        if out_last != 1:
-            raise ValueError("the last axis of out must be contiguous")
-    if x_last != 1:
-        raise ValueError("the last axis of x must be contiguous")
-    max_position, rot_dim = cos_sin.shape
-    if not cos_sin.is_cuda or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous CUDA tensor [max_position, rot_dim]")
-    st = _bound("rc_rope_apply")(
-        x.data_ptr(), _dtype(x, "x"), x_row, x_head, T, heads, head_dim,
-        _array(positions, _I64, T, "positions"), cos_sin.data_ptr(), _dtype(cos_sin, "cos_sin"),
-        max_position, rot_dim, layout, 1 if inverse else 0, out.data_ptr(), out_row, out_head,
-        None if err is None else _array(err, _I32, 1, "err"), _fast_stream(stream))
-    if st:
-        _check(st)
-    return out
+    return (_draft_module or _draft()).rope_apply(x, positions, cos_sin, layout, inverse, out, err,
+                                                  None if stream is None else stream.cuda_stream)
 
 
 def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
@@ -894,55 +839,9 @@ def tree_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.
     to itself).  ``lse`` float32 [rows, num_heads] receives the log sums.
     ``workspace``: tree_attention_workspace(); without one the keys are not
     split over the GPU.  Returns out, bf16 [rows, num_heads, 64]."""
-    rows, heads, width = shape = q.shape
-    if width != HEAD_DIM or q.dtype is not _BF16 or not q.is_cuda:
-        raise ValueError("q must be a CUDA bfloat16 view [rows, num_heads, 64]")
-    q_row, q_head, q_last = q.stride()
-    if q_last != 1 or (q_head != HEAD_DIM and heads > 1):
-        raise ValueError("q needs strides (*, 64, 1)")
-    if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
-        out_row = heads * HEAD_DIM
-    else:
-        if out.shape != shape or out.dtype is not _BF16 or not out.is_cuda:
-            raise ValueError("out must be CUDA bfloat16 of q's shape")
-        out_row, out_head, out_last = out.stride()
-        if out_last != 1 or (out_head != HEAD_DIM and heads > 1):
-            raise ValueError("out needs strides (*, 64, 1)")
-    nb, kv_heads, bs, kv_width = cache.shape
-    if kv_width != 2 * HEAD_DIM or cache.dtype is not _BF16 or not cache.is_cuda or \
-            not cache.is_contiguous():
-        raise ValueError("cache must be contiguous CUDA bfloat16 [num_blocks, num_kv_heads, "
-                         "block_size, 128]")
-    seqs, table_width = block_table.shape
-    table_stride, table_last = block_table.stride()
-    if block_table.dtype is not _I32 or not block_table.is_cuda or (table_last != 1 and table_width > 1):
-        raise ValueError("block_table must be CUDA int32 [seqs, width] with a contiguous last axis")
-    mask_ptr, words = None, 0
-    if tree_mask is not None:
-        mask_rows, words = tree_mask.shape
-        if mask_rows != rows:
-            raise ValueError("tree_mask must be [rows, words]")
-        mask_ptr = _array(tree_mask, _I64, 0, "tree_mask")
-    lse_ptr = None
-    if lse is not None:
-        if lse.shape != (rows, heads):
-            raise ValueError("lse must be [rows, num_heads]")
-        lse_ptr = _array(lse, _F32, 0, "lse")
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        if not (workspace.is_cuda and workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    st = _bound("rc_tree_attention")(
-        q.data_ptr(), q_row, rows, heads, kv_heads, _array(row_start, _I32, seqs + 1, "row_start"),
-        seqs, _array(context_len, _I32, seqs, "context_len"), block_table.data_ptr(), table_stride,
-        table_width, mask_ptr, words, cache.data_ptr(), nb, bs, scale, out.data_ptr(), out_row,
-        lse_ptr, None if err is None else _array(err, _I32, 1, "err"), ws_ptr, ws_bytes,
-        _fast_stream(stream))
-    if st:
-        _check(st)
-    return out
+    return (_draft_module or _draft()).tree_attention(
+        q, row_start, context_len, block_table, cache, tree_mask, scale, out, lse, err, workspace,
+        None if stream is None else stream.cuda_stream)
 
 
 def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
@@ -967,70 +866,7 @@ def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
     tree_attention; repetition, frequency, presence float32 [seqs]; bias_start
     int32 [seqs + 1], bias_tokens int32, bias_values float32; allowed int32
     bit words [rows, >= ceil(vocab / 32)].  ``out`` may be ``logits``."""
-    rows, vocab = shape = logits.shape
-    dtype = logits.dtype
-    row, last = logits.stride()
-    if not logits.is_cuda:
-        raise TypeError("logits must be a CUDA tensor")
-    if last != 1 and vocab > 1:
-        raise ValueError("rows of logits must be contiguous")
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=logits.device)
-        out_row = vocab
-    else:
-        if out.shape != shape or out.dtype is not dtype or not out.is_cuda:
-            raise ValueError("out must be a CUDA tensor of the shape and dtype of logits")
-        out_row, out_last = out.stride()
-        if out_last != 1 and vocab > 1:
-            raise ValueError("rows of out must be contiguous")
-    seqs = row_start.shape[0] - 1
-    p = LogitsParams()
-    if history is not None:
-        if history_start is None:
-            raise ValueError("history and history_start go together")
-        p.history = _array(history, _I32, 0, "history")
-        p.history_size = history.numel()
-        p.history_start = _array(history_start, _I64, seqs + 1, "history_start")
-        if prompt_len is not None:
-            p.prompt_len = _array(prompt_len, _I32, seqs, "prompt_len")
-    elif history_start is not None:
-        raise ValueError("history and history_start go together")
-    if draft_tokens is not None:
-        p.draft_tokens = _array(draft_tokens, _I32, rows, "draft_tokens")
-        if tree_mask is not None:
-            mask_rows, words = tree_mask.shape
-            if mask_rows != rows:
-                raise ValueError("tree_mask must be [rows, words]")
-            p.tree_mask = _array(tree_mask, _I64, 0, "tree_mask")
-            p.mask_words = words
-    if repetition is not None:
-        p.repetition = _array(repetition, _F32, seqs, "repetition")
-    if frequency is not None:
-        p.frequency = _array(frequency, _F32, seqs, "frequency")
-    if presence is not None:
-        p.presence = _array(presence, _F32, seqs, "presence")
-    if bias_start is not None:
-        if bias_tokens is None or bias_values is None:
-            raise ValueError("bias_start, bias_tokens and bias_values go together")
-        n = bias_tokens.numel()
-        p.bias_start = _array(bias_start, _I32, seqs + 1, "bias_start")
-        p.bias_tokens = _array(bias_tokens, _I32, 0, "bias_tokens")
-        p.bias_values = _array(bias_values, _F32, n, "bias_values")
-        p.bias_size = n
-    elif bias_tokens is not None or bias_values is not None:
-        raise ValueError("bias_start, bias_tokens and bias_values go together")
-    if allowed is not None:
-        mask_rows, mask_words = allowed.shape
-        mask_row, mask_last = allowed.stride()
-        if allowed.dtype is not _I32 or not allowed.is_cuda or mask_rows != rows or \
-                mask_words * 32 < vocab or (mask_last != 1 and mask_words > 1):
-            raise ValueError("allowed must be CUDA int32 [rows, >= ceil(vocab / 32)], rows contiguous")
-        p.allowed = allowed.data_ptr()
-        p.allowed_stride = mask_row
-    st = _bound("rc_logits_adjust")(
-        logits.data_ptr(), _dtype(logits, "logits"), row, rows, vocab,
-        _array(row_start, _I32, seqs + 1, "row_start"), seqs, p, out.data_ptr(), out_row,
-        None if err is None else _array(err, _I32, 1, "err"), _fast_stream(stream))
-    if st:
-        _check(st)
-    return out
+    return (_draft_module or _draft()).logits_adjust(
+        logits, row_start, history, history_start, prompt_len, draft_tokens, tree_mask, repetition,
+        frequency, presence, bias_start, bias_tokens, bias_values, allowed, out, err,
+        None if stream is None else stream.cuda_stream)
