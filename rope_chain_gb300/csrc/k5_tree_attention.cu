@@ -1452,11 +1452,14 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     Args a{};
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
-    a.min_tiles = 4;
-    // no unit has more tiles than a CTA takes at least: nothing to split or join
-    if ((int64_t)p.table_width * p.block_size <= a.min_tiles * kKeyTile)
-        a.partial = nullptr;
     const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
+    a.min_tiles = 2;
+    // units of at most so many tiles are not worth a join
+    constexpr int kWhole = 4;
+    if ((int64_t)p.table_width * p.block_size <= kWhole * kKeyTile) {
+        a.partial = nullptr;
+        a.min_tiles = kWhole;
+    }
     // as many CTAs as fill the GPU, or as the block table lets have work
     const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
     const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;
