@@ -226,9 +226,15 @@ struct TableArgs {
     uint64_t step[kMaxRotDim / 2];      // inv_j / 2 pi mod 1, times 2^64
 };
 
-template <typename C, int kVec>
+// cos and sin of p times column j's angle.
+__device__ __forceinline__ void cos_sin_at(uint64_t step, uint64_t p, float &c, float &s) {
+    sincospif(__fmul_rn((float)(int32_t)((p * step) >> 32), 0x1p-31f), &s, &c);     // of half turns
+}
+
+// FP32 tables: every entry from its own angle.
+template <int kVec>
 __global__ void __launch_bounds__(kThreads)
-k6_rope_table(const __grid_constant__ TableArgs a)
+k6_rope_table_f32(const __grid_constant__ TableArgs a)
 {
     pdl_trigger();
     pdl_wait();
@@ -236,32 +242,76 @@ k6_rope_table(const __grid_constant__ TableArgs a)
     const int64_t n = a.positions * chunks;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
          i += (int64_t)gridDim.x * kThreads) {
-        // positions * half < 2^31 * 256: the quotient by 64-bit division is
-        // only needed past 2^32
-        int64_t p;
-        uint32_t c;
-        if (n <= 0xFFFFFFFFll) {
-            p = (uint32_t)i / chunks;
-            c = (uint32_t)i - (uint32_t)p * chunks;
-        } else {
-            p = i / chunks;
-            c = (uint32_t)(i - p * chunks);
+        const int64_t p = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / chunks) : i / chunks;
+        const uint32_t c = (uint32_t)(i - p * chunks);
+        Run<float, kVec> co, si;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            float k, s;
+            cos_sin_at(a.step[c * kVec + j], (uint64_t)p, k, s);
+            co.w[j] = __float_as_uint(__fmul_rn(k, a.gain));
+            si.w[j] = __float_as_uint(__fmul_rn(s, a.gain));
         }
-        Run<C, kVec> co, si;
+        float *row = static_cast<float *>(a.out) + p * 2 * a.half + c * kVec;
+        co.template put<kVec == kWideOf<float>>(row);
+        si.template put<kVec == kWideOf<float>>(row + a.half);
+    }
+}
+
+// bf16 tables: a sine and cosine of its own take a thread some 40 instructions,
+// four times what the stores allow, so a thread makes them for one of kStep
+// positions and turns that one by the block's table of the first kStep - 1
+// steps (cos(x + y) = cos x cos y - sin x sin y): two more FP32 roundings,
+// 2^-22 at most, against bf16's 2^-9.
+constexpr int kStep = 4;
+template <int kVec>
+__global__ void __launch_bounds__(kThreads)
+k6_rope_table_bf16(const __grid_constant__ TableArgs a)
+{
+    extern __shared__ float s_turn[];                   // [kStep][2][half]: cos and sin of k steps, without the gain
+    for (int i = threadIdx.x; i < a.half * kStep; i += kThreads) {
+        const int k = i / a.half, j = i - k * a.half;
+        cos_sin_at(a.step[j], (uint64_t)k, s_turn[2 * k * a.half + j], s_turn[(2 * k + 1) * a.half + j]);
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t chunks = (uint32_t)a.half / kVec;
+    const int64_t groups = (a.positions + kStep - 1) / kStep, n = groups * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
+         i += (int64_t)gridDim.x * kThreads) {
+        const int64_t g = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / chunks) : i / chunks;
+        const uint32_t c = (uint32_t)(i - g * chunks);
+        const int64_t p0 = g * kStep;
+        float c0[kVec], s0[kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; j += 2) {
-            float s[2] = {0.0f, 0.0f}, k[2] = {0.0f, 0.0f};
+        for (int j = 0; j < kVec; ++j) {
+            cos_sin_at(a.step[c * kVec + j], (uint64_t)p0, c0[j], s0[j]);
+            c0[j] = __fmul_rn(c0[j], a.gain);
+            s0[j] = __fmul_rn(s0[j], a.gain);
+        }
+        uint16_t *row = static_cast<uint16_t *>(a.out) + p0 * 2 * a.half + c * kVec;
 #pragma unroll
-            for (int e = 0; e < (kVec > 1 ? 2 : 1); ++e) {
-                const uint64_t turns = (uint64_t)p * a.step[c * kVec + j + e];
-                sincospif(__fmul_rn((float)(int32_t)(turns >> 32), 0x1p-31f), &s[e], &k[e]);   // of half turns
+        for (int k = 0; k < kStep; ++k) {
+            if (p0 + k >= a.positions)
+                break;
+            Run<uint16_t, kVec> co, si;
+#pragma unroll
+            for (int j = 0; j < kVec; j += 2) {
+                float x[2] = {0.0f, 0.0f}, y[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int e = 0; e < (kVec > 1 ? 2 : 1); ++e) {
+                    const float *t = s_turn + 2 * k * a.half + c * kVec + j + e;
+                    x[e] = __fmaf_rn(c0[j + e], t[0], -__fmul_rn(s0[j + e], t[a.half]));
+                    y[e] = __fmaf_rn(s0[j + e], t[0], __fmul_rn(c0[j + e], t[a.half]));
+                }
+                co.set2(j, x[0], x[1]);
+                si.set2(j, y[0], y[1]);
             }
-            co.set2(j, __fmul_rn(k[0], a.gain), __fmul_rn(k[1], a.gain));
-            si.set2(j, __fmul_rn(s[0], a.gain), __fmul_rn(s[1], a.gain));
+            co.template put<kVec == kWideOf<uint16_t>>(row);
+            si.template put<kVec == kWideOf<uint16_t>>(row + a.half);
+            row += 2 * a.half;
         }
-        C *row = static_cast<C *>(a.out) + p * 2 * a.half + c * kVec;
-        co.template put<kVec == kWideOf<C>>(row);
-        si.template put<kVec == kWideOf<C>>(row + a.half);
     }
 }
 
@@ -298,13 +348,13 @@ cudaError_t launch_rope_table(void *out, bool f32, int64_t positions, int32_t ro
         a.step[j] += (uint64_t)(int64_t)std::llround(std::ldexp(low, 12) + std::ldexp(rest, 64));
     }
     const int half = rot / 2;
-    const int size = f32 ? 4 : 2;
-    const int vec = half * size % 16 == 0 ? 16 / size : 1;
-    const int64_t n = positions * (half / vec);
+    const int vec = half % (f32 ? 4 : 8) == 0 ? (f32 ? 4 : 8) : 1;
+    const int64_t n = (f32 ? positions : (positions + kStep - 1) / kStep) * (half / vec);
     const int64_t blocks = std::min<int64_t>((n + kThreads - 1) / kThreads, (int64_t)num_sms * 64);
-    auto kernel = f32 ? (vec > 1 ? k6_rope_table<float, 4> : k6_rope_table<float, 1>)
-                      : (vec > 1 ? k6_rope_table<uint16_t, 8> : k6_rope_table<uint16_t, 1>);
-    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, 1, a);
+    auto kernel = f32 ? (vec > 1 ? k6_rope_table_f32<4> : k6_rope_table_f32<1>)
+                      : (vec > 1 ? k6_rope_table_bf16<8> : k6_rope_table_bf16<1>);
+    const size_t smem = f32 ? 0 : (size_t)half * kStep * 2 * sizeof(float);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, stream, 1, a);
 }
 
 }  // namespace rc
