@@ -724,7 +724,8 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
  * the sequence's generated history (its history past the first prompt_len[b]
  * tokens) and among the drafted tokens that the row's node sees (itself as the
  * mask says; without a mask every node up to its own); `said` is whether t
- * is in the prompt or g > 0.  In FP32, in this order:
+ * is in the prompt or g > 0.  In FP32, in this order (the quotient as a product
+ * with the rounded 1 / repetition):
  *   x = logit;  if said: x = x > 0 ? x / repetition : x * repetition;
  *   x = x - frequency * g;  if g > 0: x = x - presence;
  *   x = x + bias of t;  if t is not allowed: x = -infinity

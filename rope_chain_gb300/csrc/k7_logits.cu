@@ -6,7 +6,8 @@
 // itself among them) and `seen` = g > 0 or t is in the prompt:
 //   x = logit;  x = seen ? (x > 0 ? x / rep : x * rep) : x
 //   x = x - freq * g - (g > 0 ? pres : 0);  x = x + bias;  disallowed -> -inf
-// in FP32 in this order, rounded once to the logits' type.
+// in FP32 in this order (x / rep as x times the rounded 1 / rep, freq * g fused
+// into its difference), rounded once to the logits' type.
 //
 // The floor is one read and one write of the logits.  A CTA owns a tile of
 // the vocabulary for the rows of one sequence: it scans the history once,
@@ -125,14 +126,15 @@ __device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
         f(__ldg(p + threadIdx.x));
     const int64_t quads = (n - lead) / 4;
     const int4 *q = reinterpret_cast<const int4 *>(p + lead);
-    for (int64_t i = threadIdx.x; i < quads; i += 4 * kThreads) {
-        int4 t[4];
+    constexpr int kLoads = 4;
+    for (int64_t i = threadIdx.x; i < quads; i += kLoads * kThreads) {
+        int4 t[kLoads];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kLoads; ++j)
             if (i + j * kThreads < quads)
                 t[j] = __ldg(q + i + j * kThreads);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kLoads; ++j)
             if (i + j * kThreads < quads) {
                 f(t[j].x);
                 f(t[j].y);
@@ -151,7 +153,7 @@ __device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
 // has the same shift, so that where a thread's tokens lie, and which of them
 // are listed, is found once.  kR rows are in flight per thread.
 template <typename T, int kTile, int kVec, int kR, bool kSame>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kVec * kR * kTile >= 4096 * 8 ? 3 : 4)
 k7_logits(const __grid_constant__ LogitsLaunch a)
 {
     constexpr int kPer = kTile / (kVec * kThreads);
@@ -328,6 +330,7 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     }
     __syncthreads();
 
+    const float less = __fdiv_rn(1.0f, rep);
     // The logit of a token whose word is set, in row r, whose node sees `see`
     // (its first 64 nodes).
     auto adjusted = [&](int r, uint64_t see, int at, float x) {
@@ -346,8 +349,8 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             }
         }
         if (g != 0u || (w & kPrompt) != 0u)
-            x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-        x = __fsub_rn(x, __fmul_rn(freq, (float)g));
+            x = __fmul_rn(x, x > 0.0f ? less : rep);
+        x = __fmaf_rn(-freq, (float)g, x);
         if (g != 0u)
             x = __fsub_rn(x, pres);
         if (w & kBias)
