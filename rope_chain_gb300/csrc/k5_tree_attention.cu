@@ -663,7 +663,7 @@ k5_small(const __grid_constant__ Args a)
 // harmless, FP32 and bf16 having the range.  So a tile's maximum needs no
 // shuffles, only a vote on whether a lane saw more, and O is rescaled rarely, by
 // the rows' own warp.
-//   loader warp      K and V tiles of 16 KiB by TMA, in boxes of the largest
+//   kQ loader warps  K and V tiles of 16 KiB by TMA, in boxes of the largest
 //                    power of two of keys that divides a block (8 to 128),
 //                    each box's block looked up in the table by its own lane
 //   kQ MMA warps     one per row tile: the next S as soon as the softmax has
@@ -682,11 +682,24 @@ enum : unsigned { kFaultLoad = 1u, kFaultMma = 2u, kFaultSoftmax = 4u, kFaultDra
 
 constexpr uint32_t kTileBytes = kKeyTile * kHeadDim * 2;           // K or V of a step, Q of a tile: 16 KiB
 template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
-template <int kQ> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + 1);
+// A warp's boxes are issued one by one, at some 130 cycles each.  With two row
+// tiles one warp loads K and another V: 293 us instead of 323 for 8 trees of 64
+// tokens over 32768 keys (512 rows a KV head, blocks of 16).  With one row tile a
+// single warp loads both, as an eleventh warp would cost the SM its second CTA:
+// 16 trees of 16 over 8192 keys take 73 us, with two loaders 84.
+template <int kQ> constexpr int kLoaders = kQ;
+template <int kQ> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ>);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
 constexpr uint32_t kPCol = 128u, kOCol = 192u;
 template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ> * 2 * kTileBytes;
+
+// Keeps x in local memory: what is read at a piece's ends only would otherwise
+// crowd the scores out of the registers.  Used with two row tiles (8 trees of 64
+// tokens over 32768 keys in blocks of 128: 273 us, without 291; in blocks of 16,
+// where the loads bound, 293 either way), not with one (16 trees of 16 over 8192
+// keys: 73 us, with it 76).
+template <typename T> __device__ __forceinline__ void in_memory(T &x) { asm volatile("" ::"l"(&x) : "memory"); }
 
 // The slow half of a wait: up to kWaitNs from its first look at the timer, or
 // until a fault has been raised; raises `fault` if the phase does not complete.
@@ -842,7 +855,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full0 + 8u * i, 1);
+            mbar_init(full0 + 8u * i, kLoaders<kQ>);
             mbar_init(empty0 + 8u * i, kQ);
         }
         for (int t = 0; t < kQ; ++t) {
@@ -870,17 +883,23 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     tc_fence_after();
     const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
     pdl_wait();
-    const Place at = locate<kRows, kThreads>(a, blockIdx.x, gridDim.x);
+    Place at = locate<kRows, kThreads>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
     Walk<kRows> walk(at);
     if (s_skip != 0u)
         walk.hi = walk.pos;
     Piece u;
+    if constexpr (kQ == 2) {
+        in_memory(at);
+        in_memory(walk);
+        in_memory(u);
+    }
     uint32_t n = 0;                                     // key tiles of earlier pieces
     uint32_t piece = 0;
 
-    if (warp == kLoadWarp) {
+    if (warp >= kLoadWarp) {
+        const bool keys = warp == kLoadWarp, values = kLoaders<kQ> == 1 || !keys;
         const int boxes = kKeyTile / box;               // <= 16
         bool fine = true;
         while (fine && walk.next(a, u)) {
@@ -898,7 +917,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 const bool mine = lane < boxes && p < s.keys;
                 const int off = mine ? (int)((uint32_t)p % (uint32_t)a.block_size) : 0;
                 const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
-                if (bad && u.unit == 0 && off == 0 && a.err != nullptr)
+                if (bad && keys && u.unit == 0 && off == 0 && a.err != nullptr)
                     atomicAdd(a.err, 1);                // once per block: at its first key
                 fine = wait_phase(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
                 fine = __all_sync(0xFFFFFFFFu, fine);
@@ -906,16 +925,19 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                     break;
                 const uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad), loads = __ballot_sync(0xFFFFFFFFu, mine);
                 if (lane == 0) {
-                    s_bad[st] = bads;
-                    mbar_expect_tx(full, (uint32_t)__popc(loads) * box * 256u);
+                    if (keys)
+                        s_bad[st] = bads;
+                    mbar_expect_tx(full, (uint32_t)__popc(loads) * box * (256u / kLoaders<kQ>));
                 }
                 __syncwarp();
                 if (mine) {
                     // a block out of range reads zeros: one past the last
                     const int from = bad ? a.num_blocks : blk;
                     const uint32_t dst = sK + st * (2 * kTileBytes) + (uint32_t)(lane * box) * 128u;
-                    tma_box(dst, &map, 0, off, u.h, from, full);
-                    tma_box(dst + kTileBytes, &map, kHeadDim, off, u.h, from, full);
+                    if (keys)
+                        tma_box(dst, &map, 0, off, u.h, from, full);
+                    if (values)
+                        tma_box(dst + kTileBytes, &map, kHeadDim, off, u.h, from, full);
                 }
                 blk = look_up(j + 1);
             }
@@ -1015,8 +1037,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 ref[e] = sum[e] = 0.0f;
                 limit[e] = -INFINITY;
             }
-            for (int j = 0; j < u.count; ++j, ++n) {
-                const int p0 = (u.k0 + j) * kKeyTile;
+            const int count = u.count, ctx = s.ctx;
+            int p0 = u.k0 * kKeyTile;
+            for (int j = 0; j < count; ++j, ++n, p0 += kKeyTile) {
                 wait_phase(s_full, n & 1u, kFaultSoftmax);
                 __syncwarp();
                 tc_fence_after();
@@ -1034,7 +1057,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_local(s_free0 + 8u * t);
-                if (p0 + kKeyTile > s.ctx || bads != 0u) {
+                if (p0 + kKeyTile > ctx || bads != 0u) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
