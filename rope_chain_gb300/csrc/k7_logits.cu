@@ -118,16 +118,23 @@ template <int kTile> struct Smem {
     int32_t nodes;
 };
 
-// A stretch of the history, four tokens a load where it is aligned: f(token).
+// The history, four tokens a load where it is aligned: f(token, whether it is
+// one of the first `made`).  A thread's first kLoads accesses and the unaligned
+// ends are on their way before any of it is looked at (prompt and generated part
+// one after the other, ends apart: 32000 logits with 600 tokens of history
+// 4.5 us instead of 3.8).
 template <typename F>
-__device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
-    const int64_t lead = min(n, (int64_t)((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / 4);
-    if ((int64_t)threadIdx.x < lead)
-        f(__ldg(p + threadIdx.x));
-    const int64_t quads = (n - lead) / 4;
+__device__ __forceinline__ void each_token(const int32_t *p, int n, int made, F f) {
+    const int me = (int)threadIdx.x;
+    const int lead = min(n, (int)((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / 4);
+    const int quads = (n - lead) / 4, rest = n - lead - 4 * quads;
     const int4 *q = reinterpret_cast<const int4 *>(p + lead);
-    constexpr int kLoads = 4;
-    for (int64_t i = threadIdx.x; i < quads; i += kLoads * kThreads) {
+    constexpr int kLoads = 5;
+    // the ends: up to three tokens each, by threads 0 .. 2 and 4 .. 6
+    const int end = me < 4 ? me : n - rest + me - 4;
+    const bool has = me < 4 ? me < lead : me - 4 < rest;
+    const int32_t lone = has ? __ldg(p + end) : 0;
+    for (int i = me; i < quads; i += kLoads * kThreads) {
         int4 t[kLoads];
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
@@ -136,15 +143,15 @@ __device__ __forceinline__ void each_token(const int32_t *p, int64_t n, F f) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
             if (i + j * kThreads < quads) {
-                f(t[j].x);
-                f(t[j].y);
-                f(t[j].z);
-                f(t[j].w);
+                const int at = lead + 4 * (i + j * kThreads);
+                f(t[j].x, at < made);
+                f(t[j].y, at + 1 < made);
+                f(t[j].z, at + 2 < made);
+                f(t[j].w, at + 3 < made);
             }
     }
-    const int64_t rest = n - lead - 4 * quads;
-    if ((int64_t)threadIdx.x < rest)
-        f(__ldg(p + n - rest + threadIdx.x));
+    if (has)
+        f(lone, end < made);
 }
 
 // Rows move 16 bytes at a time where `logits` and `out` rows start at the same
@@ -261,17 +268,14 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     if (a.history != nullptr) {
         const int64_t h0 = max((int64_t)0, min(hist0, a.history_size));
         const int64_t h1 = max(h0, min(hist1, a.history_size));
-        const int64_t made = min(h1, h0 + max(prompt, 0));
-        each_token(a.history + h0, made - h0, [&](int32_t t) {
+        each_token(a.history + h0, (int)(h1 - h0), max(prompt, 0), [&](int32_t t, bool prompted) {
             const uint32_t at = (uint32_t)t - (uint32_t)base;
-            if (at < (uint32_t)(kTile + kPad))
-                atomicOr(&s.word[at], kPrompt);
-            bad += teller && (t < 0 || t >= a.V);
-        });
-        each_token(a.history + made, h1 - made, [&](int32_t t) {
-            const uint32_t at = (uint32_t)t - (uint32_t)base;
-            if (at < (uint32_t)(kTile + kPad))
-                atomicAdd(&s.word[at], 1u);
+            if (at < (uint32_t)(kTile + kPad)) {
+                if (prompted)
+                    atomicOr(&s.word[at], kPrompt);
+                else
+                    atomicAdd(&s.word[at], 1u);
+            }
             bad += teller && (t < 0 || t >= a.V);
         });
     }
