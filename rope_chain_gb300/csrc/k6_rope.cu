@@ -28,11 +28,11 @@ template <typename T, int kN> struct Run {
     static constexpr int kWords = (int)sizeof(T) * kN >= 4 ? (int)sizeof(T) * kN / 4 : 1;
     uint32_t w[kWords];
 
-    template <bool kOne> __device__ __forceinline__ void get(const T *p) {
+    template <bool kOne, bool kStream = false> __device__ __forceinline__ void get(const T *p) {
         if (kOne && kWords % 4 == 0) {
 #pragma unroll
             for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                const uint4 *q = reinterpret_cast<const uint4 *>(p) + i, v = kStream ? __ldcs(q) : *q;
                 w[4 * i] = v.x;
                 w[(4 * i + 1) % kWords] = v.y;
                 w[(4 * i + 2) % kWords] = v.z;
@@ -53,12 +53,17 @@ template <typename T, int kN> struct Run {
                            (i + 1 < kN ? (uint32_t)reinterpret_cast<const uint16_t *>(p)[i + 1] << 16 : 0u);
         }
     }
-    template <bool kOne> __device__ __forceinline__ void put(T *p) const {
+    template <bool kOne, bool kStream = false> __device__ __forceinline__ void put(T *p) const {
         if (kOne && kWords % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i)
-                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[(4 * i + 1) % kWords],
-                                                             w[(4 * i + 2) % kWords], w[(4 * i + 3) % kWords]);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = make_uint4(w[4 * i], w[(4 * i + 1) % kWords], w[(4 * i + 2) % kWords],
+                                           w[(4 * i + 3) % kWords]);
+                if (kStream)
+                    __stcs(reinterpret_cast<uint4 *>(p) + i, v);
+                else
+                    reinterpret_cast<uint4 *>(p)[i] = v;
+            }
         } else if (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < kN; ++i)
@@ -99,16 +104,21 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
 // kVec elements (pairs layout, and what is only copied) or kVec elements of
 // each half (halves layout), so its table columns are read once for all the
 // heads.  Consecutive threads take the units of a head, then the next group of
-// heads, then the next token.  kVec is 16 bytes' worth where every pointer,
+// heads, then the next token.  Work of several heads per thread is larger than a
+// few MB and passes the caches by (evict first), or it would drive its own table
+// out: 32768 x 16 heads of 128, halves, forward and transposed, 105 us without
+// the hints, 93 with them, 88 with five blocks on an SM instead of four (6.1 TB/s;
+// the pairs' four loads per thread want the registers of four: 17.2 us for
+// 32768 x 16 heads of 64, with five 18.3).  kVec is 16 bytes' worth where every pointer,
 // stride, width and rot_dim allows it, else one pair, element by element (a
 // copied tail of odd width in the pairs layout is refused on the host).
 template <typename T, typename C, bool kHalves, bool kInverse, int kVec, int kHeads>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, kHalves && kHeads > 1 ? 5 : 4)
 k6_rope_apply(const __grid_constant__ RopeLaunch a)
 {
     pdl_trigger();
     pdl_wait();
-    constexpr bool kOne = kVec == kWideOf<T>;
+    constexpr bool kOne = kVec == kWideOf<T>, kStream = kHeads > 1;
     const uint32_t rotated = kHalves ? (uint32_t)a.rot / (2 * kVec) : (uint32_t)a.rot / kVec;
     const uint32_t units = rotated + (uint32_t)(a.width - a.rot) / kVec;
     const uint32_t groups = ((uint32_t)a.heads + kHeads - 1) / kHeads;
@@ -133,9 +143,9 @@ k6_rope_apply(const __grid_constant__ RopeLaunch a)
 #pragma unroll
         for (int k = 0; k < kHeads; ++k)
             if (h0 + k < (uint32_t)a.heads) {
-                v0[k].template get<kOne>(src + k * a.x_head_stride);
+                v0[k].template get<kOne, kStream>(src + k * a.x_head_stride);
                 if (kHalves && rot)
-                    v1[k].template get<kOne>(src + k * a.x_head_stride + half);
+                    v1[k].template get<kOne, kStream>(src + k * a.x_head_stride + half);
             }
         // a token without a table row passes through
         const bool bad = pos < 0 || pos >= a.max_position;
@@ -172,9 +182,9 @@ k6_rope_apply(const __grid_constant__ RopeLaunch a)
 #pragma unroll
         for (int k = 0; k < kHeads; ++k)
             if (h0 + k < (uint32_t)a.heads) {
-                v0[k].template put<kOne>(dst + k * a.out_head_stride);
+                v0[k].template put<kOne, kStream>(dst + k * a.out_head_stride);
                 if (kHalves && rot)
-                    v1[k].template put<kOne>(dst + k * a.out_head_stride + half);
+                    v1[k].template put<kOne, kStream>(dst + k * a.out_head_stride + half);
             }
     }
 }
@@ -187,7 +197,8 @@ cudaError_t launch_vec(const RopeLaunch &a, bool wide, int num_sms, cudaStream_t
     const int vec = wide ? kWide : kNarrow;
     const int64_t units = (kHalves ? a.rot / (2 * vec) : a.rot / vec) + (a.width - a.rot) / vec;
     // four loads in flight per thread (the heads that share them share the
-    // table's columns); with less work than fills the GPU that way, one head
+    // table's columns; eight for halves, in either number of blocks: 94 and 118
+    // us in place of 88); with less work than fills the GPU that way, one head
     // per thread
     constexpr int kMany = kHalves ? 2 : 4;
     const bool many = wide && a.heads >= kMany && a.T * a.heads * units >= (int64_t)kMany * num_sms * 1024;
@@ -262,7 +273,7 @@ k6_rope_table_f32(const __grid_constant__ TableArgs a)
 // four times what the stores allow, so a thread makes them for one of kStep
 // positions and turns that one by the block's table of the first kStep - 1
 // steps (cos(x + y) = cos x cos y - sin x sin y): two more FP32 roundings,
-// 2^-22 at most, against bf16's 2^-9.
+// 2^-22 at most, against bf16's 2^-8.
 constexpr int kStep = 4;
 template <int kVec>
 __global__ void __launch_bounds__(kThreads)
