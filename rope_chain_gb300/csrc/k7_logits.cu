@@ -13,14 +13,20 @@
 // the vocabulary for the rows of one sequence: it scans the history once,
 // counts the tile's tokens in shared memory, and then streams its columns of
 // every row, 16 bytes at a time, each warp by itself.  Few tokens need
-// arithmetic (what the history, the tree and the biases name); a bit map says
-// which, and a lane walks the set bits of its own few tokens, so that a warp
-// goes through the formula about once per 32 x 16 bytes however many lanes have
-// one.  The nodes that draft a token of the tile are a 64-bit set, so that a
-// row's count of it is a population count.
+// arithmetic (what the history, the tree and the biases name).  Each warp lists
+// those of its columns once; with every row its logits go through shared memory,
+// where the lanes take the listed ones 32 at a time.  (Lanes that walked what
+// was listed in their own 16 bytes were bound by instructions, as long as the
+// fullest of 32: 16 x 64 rows of 131072, history 4096, 221 us FP32 and 178 bf16;
+// now 193, 5.6 TB/s, bound by memory, and 125, 4.4 TB/s.)  The nodes that draft
+// a token of the tile are a 64-bit set, so that a row's count of it is a
+// population count.  Small calls are latency: one row of 32000 takes 3.9 us, 39
+// rows of 100003 bf16 with skewed histories of 9001 15.6 us, of which the tile
+// with the most frequent tokens makes 5 and the scan of the history 2.
 #include "rc_internal.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace rc {
 
@@ -107,8 +113,10 @@ __device__ __forceinline__ uint32_t window(const uint32_t *words, int at) {
     return __funnelshift_r(words[at >> 5], words[(at >> 5) + 1], at & 31);
 }
 
-template <int kTile> struct Smem {
-    static constexpr int kWords = kTile + kPad;
+template <typename T, int kTile, int kVec, int kR, bool kSame> struct Smem {
+    static constexpr int kWords = kTile + kPad, kWarps = kThreads / 32;
+    static constexpr int kWindow = 32 * kVec;        // tokens of a warp's access
+    T stage[kWarps][kR][kWindow];                    // a warp's logits while its listed ones are worked on
     uint64_t set[kNodes];                            // the nodes that draft a listed token
     uint32_t word[kWords];                           // count and flags of a token
     uint32_t bias[kWords];                           // 1 + the entry of its bias, then the bias itself
@@ -116,6 +124,10 @@ template <int kTile> struct Smem {
     uint16_t listed[kWords];                         // where the drafted token's set is
     int16_t node[kNodes], token[kNodes];             // a listed node, and its token's place in the tile
     int32_t nodes;
+    // per access of a warp, the places of what is listed (kSame: within the 256
+    // tokens at most; else of the rows' windows together)
+    using Place = typename std::conditional<kSame, uint8_t, uint16_t>::type;
+    Place order[kWarps][kTile / (kVec * kThreads)][kWindow + (kSame ? 0 : kVec - 1)];
 };
 
 // The history, four tokens a load where it is aligned: f(token, whether it is
@@ -158,15 +170,18 @@ __device__ __forceinline__ void each_token(const int32_t *p, int n, int made, F 
 // offset from a 16-byte boundary (kVec > 1): a thread's vectors then start up
 // to kVec - 1 tokens (`shift`) before its place in the tile.  kSame: every row
 // has the same shift, so that where a thread's tokens lie, and which of them
-// are listed, is found once.  kR rows are in flight per thread.
+// are listed, is found once.  kR rows are in flight per thread.  bf16 vectors
+// want 80 registers, three blocks on an SM (16 x 64 rows of 131072 125 us, with
+// four blocks 172); FP32 fits the 64 of four.
 template <typename T, int kTile, int kVec, int kR, bool kSame>
-__global__ void __launch_bounds__(kThreads, kVec * kR * kTile >= 4096 * 8 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && kVec > 1 ? 3 : 4)
 k7_logits(const __grid_constant__ LogitsLaunch a)
 {
     constexpr int kPer = kTile / (kVec * kThreads);
     using V = Vec<T, kVec>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<kTile> &s = *reinterpret_cast<Smem<kTile> *>(smem_raw);
+    using S = Smem<T, kTile, kVec, kR, kSame>;
+    S &s = *reinterpret_cast<S *>(smem_raw);
     pdl_trigger();
     for (int i = threadIdx.x; i < kTile + kPad; i += kThreads) {
         s.word[i] = 0u;
@@ -334,11 +349,34 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     }
     __syncthreads();
 
+    // What is listed among the tokens that this warp's access k reaches, in
+    // order, as places from start_of(k) on.
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto start_of = [&](int k) {
+        return first - (kSame ? shift0 : kVec - 1) + (warp * 32 + k * kThreads) * kVec - base;
+    };
+    int listed[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int from = start_of(k) + lane * kVec, own = kSame || lane < 31 ? kVec : 2 * kVec - 1;
+        uint32_t bits = window(s.special, from) & ((1u << own) - 1u);
+        int at = __popc(bits);
+        const int mine = at;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int other = __shfl_up_sync(0xFFFFFFFFu, at, d);
+            at += lane >= d ? other : 0;
+        }
+        listed[k] = __shfl_sync(0xFFFFFFFFu, at, 31);
+        for (at -= mine; bits != 0u; bits &= bits - 1u)
+            s.order[warp][k][at++] = (typename S::Place)(lane * kVec + __ffs(bits) - 1);
+    }
+    __syncwarp();
+
     const float less = __fdiv_rn(1.0f, rep);
-    // The logit of a token whose word is set, in row r, whose node sees `see`
+    // The logit of a token whose word w is set, in row r, whose node sees `see`
     // (its first 64 nodes).
-    auto adjusted = [&](int r, uint64_t see, int at, float x) {
-        const uint32_t w = s.word[at];
+    auto adjusted = [&](int r, uint64_t see, int at, uint32_t w, float x) {
         uint32_t g = w & kCount;
         if (w & kDraft) {
             if (few) {
@@ -361,12 +399,6 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             x = __fadd_rn(x, __uint_as_float(s.bias[at]));
         return x;
     };
-    // which of a vector's tokens have their word set
-    auto special_in = [&](int t) { return window(s.special, max(t, first - kVec) - base) & ((1u << kVec) - 1u); };
-    uint32_t todo[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-        todo[k] = special_in(token(row, k));
     while (row < r1) {
         V v[kR][kPer];
         Words ok[kR][kPer];
@@ -387,20 +419,41 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             if (coming + q * step < r1)
                 load(coming + q * step, next[q], next_ok[q], next_see[q]);
 #pragma unroll
-        for (int q = 0; q < kR; ++q) {
-            const int r = row + q * step;
-            if (r >= r1)
-                break;
-            T *dst = static_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
+        for (int k = 0; k < kPer; ++k) {
+            if (listed[k] != 0) {
+                // through shared memory, so that a lane takes a listed logit
+                // wherever it lies
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int t = token(r, k);
-                uint32_t bits = kSame ? todo[k] : special_in(t);
-                while (bits != 0u) {
-                    const int j = __ffs(bits) - 1;
-                    bits &= bits - 1u;
-                    v[q][k].set(j, adjusted(r, see[q], t + j - base, v[q][k].get(j)));
+                for (int q = 0; q < kR; ++q)
+                    v[q][k].store(&s.stage[warp][q][lane * kVec]);
+                __syncwarp();
+                for (int e = lane; e < listed[k]; e += 32) {
+                    const int i = s.order[warp][k][e], at = start_of(k) + i;
+                    const uint32_t w = s.word[at];
+#pragma unroll
+                    for (int q = 0; q < kR; ++q) {
+                        const int r = row + q * step;
+                        const int j = kSame ? i : i + shift_of(r) - (kVec - 1);
+                        if (r < r1 && (kSame || (uint32_t)j < (uint32_t)S::kWindow)) {
+                            Vec<T, 1> x;
+                            x.load(&s.stage[warp][q][j]);
+                            x.set(0, adjusted(r, see[q], at, w, x.get(0)));
+                            x.store(&s.stage[warp][q][j]);
+                        }
+                    }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < kR; ++q)
+                    v[q][k].load(&s.stage[warp][q][lane * kVec]);
+            }
+#pragma unroll
+            for (int q = 0; q < kR; ++q) {
+                const int r = row + q * step;
+                if (r >= r1)
+                    break;
+                const int t = token(r, k);
+                T *dst = static_cast<T *>(a.out) + (int64_t)r * a.out_row_stride;
                 v[q][k].mask(__funnelshift_r(ok[q][k].lo, ok[q][k].hi, t & 31));
                 if (t >= 0 && t + kVec <= a.V) {
                     v[q][k].store(dst + t);
@@ -421,7 +474,7 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
 template <typename T, int kTile, int kVec, int kR, bool kSame>
 cudaError_t launch_one(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
 {
-    const size_t smem = sizeof(Smem<kTile>);
+    const size_t smem = sizeof(Smem<T, kTile, kVec, kR, kSame>);
     static bool configured[64] = {};
     static int resident[64] = {};
     int dev = 0;
@@ -445,16 +498,17 @@ cudaError_t launch_one(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
     // a row's vectors start up to kVec - 1 tokens before its first token
     const int64_t tiles = ((int64_t)a.V + kVec - 1 + kTile - 1) / kTile;
     // A sequence's rows are shared out to as many CTAs as finish soonest.  A CTA's
-    // start (the scan of the history and the list) takes as long as some
-    // eight rows.
-    constexpr int64_t kLeast = 8;
+    // start takes as long as some two rows, and the scan as one per 4096 tokens
+    // (16 x 64 rows of 131072, FP32: with history 4096 193 us, 199 for eight rows
+    // flat; with 65536 257 us, 321 for two rows flat).
+    const int64_t start = 2 + (a.history != nullptr ? a.history_size / a.seqs / 4096 : 0);
     const int64_t rows = std::max<int64_t>(1, (a.rows + a.seqs - 1) / a.seqs), units = tiles * a.seqs;
     const int64_t wave = (int64_t)per_sm * num_sms;
     int64_t chunks = 1;
     double best = 0.0;
-    for (int64_t c = 1; c <= std::max<int64_t>(1, std::min<int64_t>(rows / kLeast, 64)); ++c) {
+    for (int64_t c = 1; c <= std::max<int64_t>(1, std::min<int64_t>(rows / start, 64)); ++c) {
         const int64_t waves = (units * c + wave - 1) / wave;
-        const double rate = 1.0 / (waves * ((rows + c - 1) / c + (double)kLeast));
+        const double rate = 1.0 / (waves * ((rows + c - 1) / c + (double)start));
         if (rate > best * 1.02) {
             best = rate;
             chunks = c;
@@ -479,13 +533,14 @@ cudaError_t launch_type(const LogitsLaunch &a, int num_sms, cudaStream_t stream)
     // wide tiles (two accesses per thread and row) scan the history half as
     // often, very wide ones (four) where a CTA has a row or two, so that its
     // start is shared by more; narrow ones give twice the CTAs where there are
-    // few
+    // few.  One bf16 row in flight leaves more of a CTA's registers to the lists
+    // (two: 16 x 64 rows of 131072 132 us, one 125); FP32 wants two (193, 206).
     constexpr int kNarrow = kThreads * kVec, kWide = 2 * kNarrow, kVery = 4 * kNarrow;
     if (same && a.rows <= 2LL * a.seqs && (int64_t)((a.V + kVery - 1) / kVery) * a.seqs >= 4 * num_sms)
         return launch_one<T, kVery, kVec, 1, true>(a, num_sms, stream);
     if ((int64_t)((a.V + kWide - 1) / kWide) * a.seqs >= 2 * num_sms)
-        return same ? launch_one<T, kWide, kVec, 2, true>(a, num_sms, stream)
-                    : launch_one<T, kWide, kVec, 2, false>(a, num_sms, stream);
+        return same ? launch_one<T, kWide, kVec, sizeof(T) == 2 ? 1 : 2, true>(a, num_sms, stream)
+                    : launch_one<T, kWide, kVec, sizeof(T) == 2 ? 1 : 2, false>(a, num_sms, stream);
     return same ? launch_one<T, kNarrow, kVec, 2, true>(a, num_sms, stream)
                 : launch_one<T, kNarrow, kVec, 2, false>(a, num_sms, stream);
 }

@@ -113,6 +113,14 @@ def test_parts(parts):
     check(logits, start, kw, sees, rc.logits_adjust(logits, start, **kw))
 
 
+# two and four accesses a row and thread: many sequences over large vocabularies, rows on and off 16-byte boundaries
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("counts,V,hist", [([3] * 40, 40000, 3000), ([3] * 40, 40001, 3000), ([1] * 130, 40000, 200), ([1, 2] * 30, 40003, 20)])
+def test_wide_tiles(counts, V, hist, dtype):
+    logits, start, kw, sees = make(V + len(counts), counts, V, hist, dtype=dtype)
+    check(logits, start, kw, sees, rc.logits_adjust(logits, start, **kw))
+
+
 def test_many_drafted_tokens_in_one_tile():
     """More nodes than a tile lists, all of few tokens."""
     logits, start, kw, sees = make(12, [700], 40, 30)
