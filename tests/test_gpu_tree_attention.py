@@ -320,6 +320,21 @@ def test_offsets_past_32_bits(n):
     check(case, out, lse)
 
 
+@pytest.mark.parametrize("counts,ctx,G", [
+    ([1] * 40, [700 + 37 * i for i in range(40)], 8),           # two CTAs an SM, few rows
+    ([3, 4] * 20, [2100 - 41 * i for i in range(40)], 7),       # one
+    ([16, 15] * 6, [3000 - 201 * i for i in range(12)], 8),     # one row tile
+    ([64, 0, 63] * 3, [2500, 3, 777, 2048, 10, 1300, 0, 1, 2176], 8),
+])
+@pytest.mark.parametrize("ws", [True, False])
+def test_units_that_end_inside_a_cta(counts, ctx, G, ws):
+    """Many units of uneven lengths, so that most CTAs go through ends and beginnings of several."""
+    case = Case(31 + G + len(counts), counts, ctx, 8, G, 16)
+    out, lse, err = case.run(ws)
+    assert err == 0
+    check(case, out, lse)
+
+
 def test_reads_what_the_store_wrote():
     """Through the store's own slot mapping: keys inserted by rc_kv_store, attended by block table."""
     H, T, bs = 8, 70, 16
