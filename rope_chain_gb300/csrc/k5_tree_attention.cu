@@ -15,9 +15,13 @@
 // being (node, query head of the group).  All units' key tiles, laid end to
 // end, are cut into equal ranges, one per CTA, from the lengths on the
 // device: the host needs no lengths, and a single long context fills the GPU
-// as a batch does.  A unit that crosses a cut leaves FP32 partials (output,
-// m, sum) in the workspace, which a second kernel joins in key order (no
-// atomics: the result does not depend on timing).
+// as a batch does.  Where units are fewer than CTAs and that is no longer, each
+// is cut into equal parts instead, so that no CTA has to go from one to another
+// (6 trees of 8 over 700 to 1405 keys: 20.8 us, cut anywhere 23.3; 9 of 6 with 16
+// heads a KV head over 1900 to 3855: 21.0, 24.8), and short ones are not cut (36
+// trees of 12 over 136 keys: 15.6 us, in equal ranges 34.6).  A unit that is cut
+// leaves FP32 partials (output, m, sum) in the workspace, which a second kernel
+// joins in key order (no atomics: the result does not depend on timing).
 #include "rc_internal.cuh"
 #include "rc_tcgen05.cuh"
 
@@ -37,6 +41,7 @@ constexpr float kGrow = 8.0f;          // log2: growth of a row's maximum at whi
 struct Args : TreeAttentionLaunch {
     float scale_log2;                  // scale * log2 e
     int32_t min_tiles;                 // fewest key tiles a CTA is given
+    bool whole;                        // units are not cut
     int32_t change;                    // going to another unit, in key tiles' time
 };
 
@@ -70,10 +75,15 @@ template <int kRows> __device__ __forceinline__ int row_tiles(const Args &a, con
 }
 __device__ __forceinline__ int key_tiles(const Seq &s) { return max(1, (s.keys + kKeyTile - 1) / kKeyTile); }
 
-// A unit's slots are its key tiles and then `change` empty ones.
-template <int kRows> __device__ __forceinline__ int64_t slots_of(const Args &a, int b) {
+// How the units are cut.  Their slots, laid end to end, are shared out evenly.
+//   most >= 1: a slot is a part of at most so many key tiles, and a CTA gets one
+//              (or, uncut, as many units as another)
+//   most == 0: a unit's slots are its key tiles and then `change` empty ones, for
+//              the time that the change to it takes
+template <int kRows> __device__ __forceinline__ int64_t slots_of(const Args &a, int b, int32_t most) {
     const Seq s = seq_of(a, b);
-    return (int64_t)row_tiles<kRows>(a, s) * a.kv_heads * (key_tiles(s) + a.change);
+    const int kt = key_tiles(s);
+    return (int64_t)row_tiles<kRows>(a, s) * a.kv_heads * (most > 0 ? (kt - 1) / most + 1 : kt + a.change);
 }
 
 // A quotient; division of 64 bits is some 100 instructions, of 32 bits 20.
@@ -82,6 +92,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int32_t y) {
 }
 
 struct Place {
+    int32_t most;                      // see slots_of
     int64_t total;                     // slots of all units
     int32_t used;                      // CTAs that have some
     int64_t each;                      // total / used and the remainder
@@ -95,40 +106,88 @@ struct Place {
     int64_t off;                       // `at` within the sequence's slots
 };
 
-// The range of CTA c of `ctas`, and where its first tile lies.  Called by all kThreads threads; each takes a run of
-// sequences, and the thread whose run holds the tile walks it.
-template <int kRows, int kThreads>
+// How many key tiles a part has at most, 0: a cut wherever it falls (slots_of).
+// Parts of `most` tiles are at most tiles / most + units.  They are taken where a
+// CTA gets fewer tiles so than slots otherwise, or hardly more than a change.
+__device__ __forceinline__ int32_t most_of(const Args &a, int64_t tiles, int64_t units, int ctas) {
+    if (units >= ctas)
+        return 0;
+    const int32_t room = ctas - (int32_t)units;
+    const int64_t most = max((int64_t)a.min_tiles, quotient(tiles + room - 1, room));
+    return most <= a.change + 2 || most * ctas <= tiles + a.change * units ? (int32_t)min(most, (int64_t)INT32_MAX) : 0;
+}
+
+// The range of CTA c of `ctas`, and where its first slot lies.  Called by all
+// kThreads threads.  kParts: cut into parts where that is better (else only
+// where all units are whole).  Up to 32 sequences a lane takes one, and each warp
+// finds the range by itself; beyond, a thread takes a run of sequences, and the
+// one whose run holds the slot walks it.
+template <int kRows, int kThreads, bool kParts>
 __device__ Place locate(const Args &a, int c, int ctas) {
+    __shared__ int64_t warp_tiles[kParts ? kThreads / 32 : 1], warp_units[kParts ? kThreads / 32 : 1];
     __shared__ int64_t warp_sum[kThreads / 32];
     __shared__ int64_t found_off;
     __shared__ int32_t found_b;
-    const int per = (a.seqs + kThreads - 1) / kThreads;
-    const int b0 = min((int)threadIdx.x * per, a.seqs), b1 = min(b0 + per, a.seqs);
+    const bool alone = kParts && a.seqs <= 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int threads = alone ? 32 : kThreads, me = alone ? lane : (int)threadIdx.x;
+    const int per = (a.seqs + threads - 1) / threads;
+    const int b0 = min(me * per, a.seqs), b1 = min(b0 + per, a.seqs);
+    Place p;
+    p.most = a.whole ? INT32_MAX : 0;
+    if (kParts && !a.whole && a.partial != nullptr) {
+        int64_t tiles = 0, units = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = seq_of(a, b);
+            const int n = row_tiles<kRows>(a, s) * a.kv_heads;
+            units += n;
+            tiles += (int64_t)n * key_tiles(s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
+            units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
+        }
+        if (!alone) {
+            if (lane == 0) {
+                warp_tiles[kParts ? warp : 0] = tiles;
+                warp_units[kParts ? warp : 0] = units;
+            }
+            __syncthreads();
+            tiles = units = 0;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                tiles += warp_tiles[kParts ? w : 0];
+                units += warp_units[kParts ? w : 0];
+            }
+        }
+        p.most = most_of(a, tiles, units, ctas);
+    }
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b)
-        mine += slots_of<kRows>(a, b);
+        mine += slots_of<kRows>(a, b, p.most);
     int64_t run = mine;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, run, o);
         if (lane >= o)
             run += v;
     }
-    if (lane == 31)
-        warp_sum[warp] = run;
-    __syncthreads();
-    Place p;
-    p.total = 0;
-    int64_t before = 0;
+    int64_t before = run - mine;
+    if (alone) {
+        p.total = __shfl_sync(0xFFFFFFFFu, run, 31);
+    } else {
+        if (lane == 31)
+            warp_sum[warp] = run;
+        __syncthreads();
+        p.total = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp)
-            before += warp_sum[w];
-        p.total += warp_sum[w];
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp)
+                before += warp_sum[w];
+            p.total += warp_sum[w];
+        }
     }
-    before += run - mine;
-    p.used = (int32_t)max((int64_t)1, min((int64_t)ctas, quotient(p.total, a.min_tiles)));
+    p.used = (int32_t)max((int64_t)1, min((int64_t)ctas, p.most > 0 ? p.total : quotient(p.total, a.min_tiles)));
     p.each = quotient(p.total, p.used);
     p.rest = (int32_t)(p.total - p.each * p.used);               // rest * c < used^2 < 2^32
     p.lo = c < p.used ? p.begin_of(c) : p.total;
@@ -137,10 +196,17 @@ __device__ Place locate(const Args &a, int c, int ctas) {
     p.off = 0;
     if (p.lo >= p.hi)
         return p;                      // uniform
-    if (p.lo >= before && p.lo < before + mine) {
+    const bool here = p.lo >= before && p.lo < before + mine;
+    if (alone) {
+        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+        p.b = src;
+        p.off = p.lo - __shfl_sync(0xFFFFFFFFu, before, src);
+        return p;
+    }
+    if (here) {
         int64_t off = p.lo - before;
         int b = b0;
-        for (int64_t t; off >= (t = slots_of<kRows>(a, b)); ++b)
+        for (int64_t t; off >= (t = slots_of<kRows>(a, b, p.most)); ++b)
             off -= t;
         found_b = b;
         found_off = off;
@@ -156,6 +222,7 @@ struct Piece {
     Seq s;
     int32_t b, unit, h, tile;          // sequence, unit within it, its KV head and row tile
     int32_t k0, count, kt;
+    int32_t parts;                     // of the unit, where it is cut into such
     int64_t begin;                     // the unit's first slot
     __device__ bool whole() const { return k0 == 0 && count == kt; }
 };
@@ -163,14 +230,15 @@ struct Piece {
 // The pieces of a CTA's range, in order.
 template <int kRows> struct Walk {
     int64_t pos, off, hi;
-    int32_t b;
-    __device__ explicit Walk(const Place &p) : pos(p.lo), off(p.off), hi(p.hi), b(p.b) {}
+    int32_t b, most;
+    __device__ explicit Walk(const Place &p) : pos(p.lo), off(p.off), hi(p.hi), b(p.b), most(p.most) {}
     __device__ bool next(const Args &a, Piece &u) {
         while (pos < hi) {
             u.s = seq_of(a, b);
             u.kt = key_tiles(u.s);
             const int rt = row_tiles<kRows>(a, u.s);
-            const int32_t slots = u.kt + a.change;
+            u.parts = most > 0 ? (u.kt - 1) / most + 1 : 0;
+            const int32_t slots = most > 0 ? u.parts : u.kt + a.change;
             const int64_t all = (int64_t)rt * a.kv_heads * slots;
             if (off >= all) {                           // the next sequence with rows
                 off -= all;
@@ -179,12 +247,20 @@ template <int kRows> struct Walk {
             }
             u.b = b;
             u.unit = (int32_t)quotient(off, slots);
-            u.k0 = (int32_t)(off - (int64_t)u.unit * slots);
+            const int32_t slot = (int32_t)(off - (int64_t)u.unit * slots);
             u.h = u.unit / rt;
             u.tile = u.unit - u.h * rt;
-            const int32_t here = (int32_t)min((int64_t)(slots - u.k0), hi - pos);
-            u.count = min(u.kt - u.k0, here);
-            u.begin = pos - u.k0;
+            u.begin = pos - slot;
+            if (most > 0) {
+                u.k0 = (int32_t)quotient((int64_t)u.kt * slot, u.parts);
+                u.count = (int32_t)quotient((int64_t)u.kt * (slot + 1), u.parts) - u.k0;
+                ++pos;
+                ++off;
+                return true;
+            }
+            const int32_t here = (int32_t)min((int64_t)(slots - slot), hi - pos);
+            u.k0 = slot;
+            u.count = min(u.kt - slot, here);
             pos += here;
             off += here;
             if (u.count <= 0)
@@ -242,7 +318,9 @@ __device__ __forceinline__ int64_t offset_in(const Args &a, int32_t blk, int h, 
 template <int kRows>
 __device__ void write_header(const Args &a, const Place &p, const Piece &u, bool unfinite) {
     Header h{0, u.b, u.unit, unfinite ? 1 : 0};
-    if (u.k0 == 0) {
+    if (u.k0 == 0 && p.most > 0) {
+        h.last = (int32_t)blockIdx.x + u.parts - 1;
+    } else if (u.k0 == 0) {
         const int64_t end = u.begin + u.kt;
         // the CTA of the unit's last tile, from an estimate
         int32_t last = min(p.used - 1, (int32_t)__fdividef((float)end * (float)p.used, (float)p.total));
@@ -342,7 +420,7 @@ k5_small(const __grid_constant__ Args a)
     pdl_trigger();
     pdl_wait();
 
-    const Place at = locate<kRows, kSmallThreads>(a, blockIdx.x, gridDim.x);
+    const Place at = locate<kRows, kSmallThreads, false>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
     Walk<kRows> walk(at);
@@ -904,7 +982,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     tc_fence_after();
     const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
     pdl_wait();
-    Place at = locate<kRows, kThreads>(a, blockIdx.x, gridDim.x);
+    Place at = locate<kRows, kThreads, true>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
     Walk<kRows> walk(at);
@@ -1502,18 +1580,20 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     constexpr int kWhole = 4;
     if ((int64_t)p.table_width * p.block_size <= kWhole * kKeyTile) {
         a.partial = nullptr;
-        a.min_tiles = kWhole;
+        a.whole = true;
     }
     // as many CTAs as fill the GPU, or as the block table lets have work
     const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
     const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)p.table_width * p.block_size + kKeyTile - 1) / kKeyTile);
-    const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, units * tiles / a.min_tiles));
+    const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, a.whole ? units : units * tiles / a.min_tiles));
     // A CTA that goes from one unit to another loses some 10 us while the cache is
     // streamed, six key tiles' time; counted as such, 64 sequences of 1025 to 2050
-    // keys take 42.4 us instead of 45.9, 16 trees of 16 over 8192 71.2, 74.5.  With
-    // few tiles a CTA the ranges had better begin with the units.
-    a.change = units * tiles >= 8 * ctas ? 6 : 0;
+    // keys take 42.4 us instead of 45.9, 16 trees of 16 over 8192 71.2, 74.5.  In
+    // the small kernel, with few tiles a CTA, the ranges had better begin with the
+    // units.
+    const bool wide = v == kWide128 || v == kWide256;
+    a.change = wide || units * tiles >= 8 * ctas ? 6 : 0;
     switch (v) {
     case kSmall16: return p.block_size % kChunk == 0 ? launch_small<1, true>(a, ctas, stream, why)
                                                      : launch_small<1, false>(a, ctas, stream, why);

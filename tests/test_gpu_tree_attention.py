@@ -335,6 +335,19 @@ def test_units_that_end_inside_a_cta(counts, ctx, G, ws):
     check(case, out, lse)
 
 
+@pytest.mark.parametrize("counts,ctx,H,G", [
+    ([12, 11] * 18, [136 + 3 * i for i in range(36)], 8, 4),    # whole units, about one a CTA
+    ([25, 24, 0, 25], [90, 1, 50, 0], 1, 64),                   # several row tiles each
+    ([8, 7] * 3, [1405, 703, 0, 90, 1000, 1311], 8, 8),         # parts of two tiles
+    ([33, 32], [4339, 2100], 2, 16), ([1] * 33 + [50], [600] * 34, 2, 16),
+])
+def test_parts_of_units(counts, ctx, H, G):
+    case = Case(77 + H + G + len(counts), counts, ctx, H, G, 16)
+    out, lse, err = case.run()
+    assert err == 0
+    check(case, out, lse)
+
+
 def test_reads_what_the_store_wrote():
     """Through the store's own slot mapping: keys inserted by rc_kv_store, attended by block table."""
     H, T, bs = 8, 70, 16
