@@ -360,6 +360,12 @@ __device__ __noinline__ float add_unfinite(const Args &a, const Seq &s, int b, i
 // keys for the scores, whose accumulator layout is the operand layout of the
 // second product, so the weights stay in registers (rounded to bf16 there,
 // which the tensor cores require; the sum takes them unrounded).
+// Measured: one token over 131071 keys (8 KV heads, 268 MB) 51 us with the join,
+// 5.2 TB/s; 64 tokens over 1025 to 2049 keys (204 MB) 43 us, 4.7 TB/s; the
+// loads alone, without the products, 50 and 44 us before the changes of unit
+// were counted.  One token over 500 keys 7.3 us: launch, lengths, Q and block
+// numbers, then four tiles, one after the other.  Eight warps and two CTAs an SM
+// (one token of 131071 keys 52.1 us; four warps and four CTAs 55.2).
 
 constexpr int kWarps = 8, kSmallThreads = 32 * kWarps;
 constexpr int kChunk = 16;                                   // keys per warp and step
@@ -748,7 +754,7 @@ k5_small(const __grid_constant__ Args a)
 
 // ------------------------------------------------ many rows: tcgen05 tiles
 //
-// From 33 rows per unit on the tensor cores are the bound, and the work goes
+// From 33 rows per unit on the products are the bound, and the work goes
 // to tcgen05: kQ row tiles of 128 rows share each key tile of 128 keys.  A row
 // tile's S = Q K^T lands in TMEM (128 columns), the weights go back to TMEM as
 // bf16 (64 columns), from where they are the A operand of O += P V, and O stays
@@ -771,7 +777,13 @@ k5_small(const __grid_constant__ Args a)
 //                    100 cycles per product to issue, 1200 per tile and round
 // Per 256 rows x 128 keys the exponentials need 1024 cycles of an SM (32 per
 // cycle), the products as many at full rate; products of 64 columns (O) run at
-// about half of it.
+// about half of it, 1536 in all.
+// Measured: 8 trees of 64 tokens over 32768 keys (64 query and 8 KV heads, 273
+// GFLOP) 292 us, 0.93 PFLOP/s, 2700 cycles per 256 x 128 (in blocks of 16 keys;
+// 273 us in blocks of 128): the steps of the two row tiles, products, softmax and
+// weights, one after the other; tensor pipe 42 %, issue slots 60 %.  16 trees of 16
+// over 8192 keys (273 MB) 71 us, 3.8 TB/s: 44 us at 6.2 TB/s between a start of
+// 9 us (launch, lengths, Q, first tile) and changes of unit and the join of 18.
 // Key tiles that hold drafted keys, or the end, take a masked path; there the
 // V rows past the end are zeroed and what is infinite or NaN in a drafted one
 // is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
@@ -1351,7 +1363,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 // of a row; with few rows (kRows <= 32: units cut into many parts) four groups
 // of threads take every fourth part each and are joined in order at the end.  A
 // thread loads eight parts' maxima, sums and columns at once, so that the few
-// parts of a unit of many rows cost one latency.
+// parts of a unit of many rows cost one latency (one part at a time: 27 us for 16
+// trees of 16 tokens, 42 for 8 of 64; now about 5 behind the kernel that wrote
+// them, of which launch and headers are 1.3).
 constexpr int kJoinThreads = 256;
 template <int kRows> constexpr int kJoinRows = kRows <= 32 ? 4 : 16;
 
@@ -1473,11 +1487,14 @@ k5_join(const __grid_constant__ Args a)
 }
 
 // Which kernel takes a call, by the average rows of a unit (only the totals are
-// known on the host; any kernel is right for any unit):
-//   up to 16 rows  k5_small<1>;  up to 32  k5_small<2>: the cache's bytes bound
-//   beyond         k5_wide: 128 rows a CTA up to 128, else 256 (two row tiles
-//                  share each key tile); its TMA boxes need blocks of a
-//                  multiple of 8 keys, other block sizes stay with k5_small<2>
+// known on the host; any kernel is right for any unit).  8 sequences over 4096
+// keys, us:
+//   up to 16 rows   k5_small<1>: 21.2 at 16 rows, k5_small<2> 23.5
+//   up to 32        k5_small<2>: 26.5 at 32, k5_wide<1> 29.6; at 40 31.3 and 29.5
+//   up to 128       k5_wide<1>: 32.5 at 128, k5_wide<2> 38.5; at 160 44.1 and 40.1
+//   beyond          k5_wide<2>: two row tiles share each key tile
+// The wide kernel's TMA boxes need blocks of a multiple of 8 keys; other block
+// sizes stay with k5_small<2>.
 enum Variant { kSmall16, kSmall32, kWide128, kWide256 };
 
 Variant variant_for(int64_t rows, int32_t seqs, int32_t group, int32_t block_size) {
@@ -1575,10 +1592,16 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
     const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
+    // (3 trees of 13 over 1500 keys, in equal ranges: 15.3 us with two tiles a CTA at
+    // least, 19.9 with four, 18.3 with one)
     a.min_tiles = 2;
-    // units of at most so many tiles are not worth a join
-    constexpr int kWhole = 4;
-    if ((int64_t)p.table_width * p.block_size <= kWhole * kKeyTile) {
+    // Units of at most so many tiles are not worth a cut and a join: one token over
+    // 300 keys 6.9 us (cut 11.2), 8 trees of 4 over 900 13.5 (19.1); a tile of many
+    // rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of 13 over 900
+    // 17.6 whole and 16.1 cut.
+    const bool wide = v == kWide128 || v == kWide256;
+    const int whole = wide ? 4 : 8;
+    if ((int64_t)p.table_width * p.block_size <= whole * kKeyTile) {
         a.partial = nullptr;
         a.whole = true;
     }
@@ -1589,10 +1612,9 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, a.whole ? units : units * tiles / a.min_tiles));
     // A CTA that goes from one unit to another loses some 10 us while the cache is
     // streamed, six key tiles' time; counted as such, 64 sequences of 1025 to 2050
-    // keys take 42.4 us instead of 45.9, 16 trees of 16 over 8192 71.2, 74.5.  In
+    // keys take 43 us instead of 46, 16 trees of 16 over 8192 71.2, 74.5.  In
     // the small kernel, with few tiles a CTA, the ranges had better begin with the
     // units.
-    const bool wide = v == kWide128 || v == kWide256;
     a.change = wide || units * tiles >= 8 * ctas ? 6 : 0;
     switch (v) {
     case kSmall16: return p.block_size % kChunk == 0 ? launch_small<1, true>(a, ctas, stream, why)

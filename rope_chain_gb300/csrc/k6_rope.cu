@@ -273,7 +273,8 @@ k6_rope_table_f32(const __grid_constant__ TableArgs a)
 // four times what the stores allow, so a thread makes them for one of kStep
 // positions and turns that one by the block's table of the first kStep - 1
 // steps (cos(x + y) = cos x cos y - sin x sin y): two more FP32 roundings,
-// 2^-22 at most, against bf16's 2^-8.
+// 2^-22 at most, against bf16's 2^-8.  131072 positions of 64 columns (17 MB):
+// 5.0 us, 3.3 TB/s with the launch, every entry from its own angle 7.4.
 constexpr int kStep = 4;
 template <int kVec>
 __global__ void __launch_bounds__(kThreads)
