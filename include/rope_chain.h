@@ -607,7 +607,7 @@ typedef struct {
  *
  *   out          [max_position, rot_dim] of `dtype` (rc_dtype), contiguous,
  *                16-byte aligned
- *   max_position 0 <= max_position < 2^31 (0: nothing launched)
+ *   max_position 0 <= max_position < 2^31 (0: nothing launched, out may be NULL)
  *   rot_dim      even, 2 <= rot_dim <= 512
  *   theta        > 1
  *   scaling      HOST pointer, or NULL (no scaling, factor 1)
@@ -636,7 +636,8 @@ typedef enum {
  *                 either order of tokens and heads; aligned to the element).
  *                 out may be x with x's strides (in place), or else must not
  *                 overlap x; its elements must be distinct
- *   T, heads      T >= 0, heads >= 1, T*heads < 2^31 (T == 0: nothing launched)
+ *   T, heads      T >= 0, heads >= 1, T*heads < 2^31 (T == 0: nothing launched, and x,
+ *                 out and positions may be NULL)
  *   rot_dim       even, 2 <= rot_dim <= min(head_dim, 512); PAIRS needs an even
  *                 head_dim, which is at most 65536
  *   positions     int64 [T], 8-byte aligned
@@ -674,7 +675,8 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
  *                i*q_row_stride + 64*h + e (e.g. the Q columns of
  *                rc_qkv_front's output), 16-byte aligned, q_row_stride a
  *                multiple of 8
- *   rows         0 <= rows, rows*num_heads < 2^31 (0: nothing launched)
+ *   rows         0 <= rows, rows*num_heads < 2^31 (0: nothing launched, q and out
+ *                may be NULL)
  *   num_heads    a multiple of num_kv_heads; num_kv_heads >= 1
  *   row_start    device int32 [seqs + 1], non-decreasing, within [0, rows]
  *                (values outside are clamped); rows of no sequence are left
@@ -735,7 +737,8 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
  *                elements, aligned to its element
  *   out          as logits with out_row_stride; may be logits with its stride
  *                (in place), else must not overlap it
- *   rows         0 <= rows <= 2^30 (0: nothing launched); rows of no sequence
+ *   rows         0 <= rows <= 2^30 (0: nothing launched, logits and out may be
+ *                NULL); rows of no sequence
  *                are left
  *   vocab        1 <= vocab <= 2^30;  seqs: 1 .. 65535
  *   row_start    device int32 [seqs + 1], as in rc_tree_attention

@@ -172,6 +172,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const Tensor &mask = tensor(args[5], "tree_mask");
         TORCH_CHECK_VALUE(mask.dim() == 2 && mask.size(0) == rows, "tree_mask must be [rows, words]");
         words = mask.size(1);
+        TORCH_CHECK_VALUE(words > 0 || rows == 0, "tree_mask needs a word per row at least");
     }
     float *lse = nullptr;
     if (args[8] != Py_None) {
@@ -231,6 +232,7 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
         TORCH_CHECK_VALUE(mask.dim() == 2 && mask.size(0) == rows, "tree_mask must be [rows, words]");
         p.tree_mask = reinterpret_cast<const uint64_t *>(array<int64_t>(args[6], at::kLong, 0, "tree_mask"));
         p.mask_words = narrow<int32_t>(mask.size(1), "words of tree_mask");
+        TORCH_CHECK_VALUE(p.mask_words > 0 || rows == 0, "tree_mask needs a word per row at least");
     }
     p.repetition = array<float>(args[7], at::kFloat, seqs, "repetition");
     p.frequency = array<float>(args[8], at::kFloat, seqs, "frequency");
@@ -242,6 +244,8 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
         p.bias_start = array<int32_t>(args[10], at::kInt, seqs + 1, "bias_start");
         p.bias_tokens = array<int32_t>(args[11], at::kInt, 0, "bias_tokens");
         p.bias_values = array<float>(args[12], at::kFloat, p.bias_size, "bias_values");
+        if (p.bias_size == 0)                // none for any sequence: an empty tensor has no address
+            p.bias_start = p.bias_tokens = nullptr, p.bias_values = nullptr;
     }
     if (args[13] != Py_None) {
         const Tensor &allowed = tensor(args[13], "allowed");

@@ -92,7 +92,7 @@ rc_status rc_rope_table(void *out, int32_t dtype, int64_t max_position, int32_t 
          !(sc.beta_slow > 0.0) || !(sc.beta_fast > sc.beta_slow) || !std::isfinite(sc.beta_fast)))
         return fail(RC_ERR_INVALID_ARG, "%s: scaling by parts needs original_max_position > 0 and "
                     "beta_fast > beta_slow > 0", fn);
-    if (!out || !aligned(out, 16))
+    if ((max_position > 0 && !out) || !aligned(out, 16))
         return fail(RC_ERR_INVALID_ARG, "%s: out must be a 16-byte aligned pointer", fn);
     if (max_position == 0)
         return ok();
@@ -154,9 +154,10 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
         std::max(std::max(x_row_stride, x_head_stride), std::max(out_row_stride, out_head_stride)) > kMaxStride)
         return fail(RC_ERR_INVALID_ARG, "%s: strides outside [0, 2^40]", fn);
     const int size = size_of(dtype), table_size = size_of(table_dtype);
-    if (!x || !out || !aligned(x, size) || !aligned(out, size))
+    // (an empty tensor may have no address)
+    if ((T > 0 && (!x || !out)) || !aligned(x, size) || !aligned(out, size))
         return fail(RC_ERR_INVALID_ARG, "%s: x and out must be pointers aligned to their element", fn);
-    if (!positions || !aligned(positions, 8))
+    if ((T > 0 && !positions) || !aligned(positions, 8))
         return fail(RC_ERR_INVALID_ARG, "%s: positions must be an 8-byte aligned pointer", fn);
     if (!cos_sin || !aligned(cos_sin, table_size) || max_position < 1)
         return fail(RC_ERR_INVALID_ARG, "%s: cos_sin must be an aligned pointer with max_position >= 1", fn);
@@ -242,7 +243,7 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
                     "< 2^31 - 4096", fn);
     if (!(scale > 0.0f) || !std::isfinite(scale))
         return fail(RC_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
-    if (!q || !out || !cache || !aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16))
+    if ((rows > 0 && (!q || !out)) || !cache || !aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16))
         return fail(RC_ERR_INVALID_ARG, "%s: q, out and cache must be 16-byte aligned pointers", fn);
     if (!row_start || !context_len || !aligned(row_start, 4) || !aligned(context_len, 4) ||
         (table_width > 0 && (!block_table || !aligned(block_table, 4))))
@@ -321,7 +322,7 @@ rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride
     if (seqs < 1 || seqs > 65535)
         return fail(RC_ERR_INVALID_ARG, "%s: seqs=%d outside [1, 65535]", fn, seqs);
     const int size = size_of(dtype);
-    if (!logits || !out || !row_start || !params)
+    if ((rows > 0 && (!logits || !out)) || !row_start || !params)
         return fail(RC_ERR_INVALID_ARG, "%s: logits, out, row_start and params must not be NULL", fn);
     if (!aligned(logits, size) || !aligned(out, size) || !aligned(row_start, 4))
         return fail(RC_ERR_INVALID_ARG, "%s: logits, out and row_start must be aligned to their element", fn);

@@ -126,6 +126,13 @@ def test_logits_refusals(lib):
     assert adjust(lib, rows=0) == rc.RC_OK
 
 
+def test_empty_calls_need_no_addresses(lib):
+    assert table(lib, n=0, out=None) == rc.RC_OK
+    assert apply(lib, T=0, x=None, out=None, pos=None) == rc.RC_OK
+    assert attend(lib, rows=0, q=None, out=None, tm=None, bt=None, tw=0) == rc.RC_OK
+    assert adjust(lib, rows=0, x=None, out=None) == rc.RC_OK
+
+
 def test_python_checks_shapes_and_types():
     cpu = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
     with pytest.raises((TypeError, ValueError)):

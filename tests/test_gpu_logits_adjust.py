@@ -121,6 +121,19 @@ def test_wide_tiles(counts, V, hist, dtype):
     check(logits, start, kw, sees, rc.logits_adjust(logits, start, **kw))
 
 
+def test_empty_tensors_and_masks_without_words():
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    empty = torch.zeros(0, dtype=torch.int32, device=DEV)
+    assert rc.logits_adjust(torch.zeros(0, 9, device=DEV), i32(0, 0), draft_tokens=empty).shape == (0, 9)
+    x = torch.arange(9.0, device=DEV)[None]
+    got = rc.logits_adjust(x, i32(0, 1), history=empty, history_start=torch.zeros(2, dtype=torch.int64, device=DEV),
+                           bias_start=i32(0, 0), bias_tokens=empty, bias_values=empty.float(),
+                           repetition=torch.full((1,), 2.0, device=DEV))
+    assert torch.equal(got, x)
+    with pytest.raises(ValueError, match="word"):
+        rc.logits_adjust(x, i32(0, 1), draft_tokens=i32(3), tree_mask=torch.zeros(1, 0, dtype=torch.int64, device=DEV))
+
+
 def test_many_drafted_tokens_in_one_tile():
     """More nodes than a tile lists, all of few tokens."""
     logits, start, kw, sees = make(12, [700], 40, 30)

@@ -158,6 +158,13 @@ def test_inverse_is_the_gradient(layout):
             assert abs(float((up - down) / 0.25) - float(grad[t, 0, e])) <= 2.0 ** -24 * 8 * 64 / 0.25
 
 
+def test_empty_tensors():
+    cs = rc.rope_table(5, device=DEV)
+    x = torch.zeros(0, 3, 64, dtype=BF, device=DEV)
+    assert rc.rope_apply(x, torch.zeros(0, dtype=torch.int64, device=DEV), cs).shape == x.shape
+    assert rc.rope_table(0, device=DEV).shape == (0, 64)
+
+
 def test_the_fronts_rotation():
     """Pairs, all 64 columns, bf16: what the store does to keys after their norm (norm switched off by unit keys)."""
     H, T = 2, 40

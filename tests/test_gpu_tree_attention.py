@@ -348,6 +348,15 @@ def test_parts_of_units(counts, ctx, H, G):
     check(case, out, lse)
 
 
+def test_empty_tensors_and_masks_without_words():
+    case = Case(5, [2], [40], 2, 2, 16)
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    out = rc.tree_attention(case.q[:0], none, case.context, case.table, case.cache, tree_mask=case.mask[:0])
+    assert out.shape == (0, 4, 64)
+    with pytest.raises(ValueError, match="word"):
+        rc.tree_attention(case.q, case.row_start, case.context, case.table, case.cache, tree_mask=case.mask[:, :0].contiguous())
+
+
 def test_reads_what_the_store_wrote():
     """Through the store's own slot mapping: keys inserted by rc_kv_store, attended by block table."""
     H, T, bs = 8, 70, 16
