@@ -1595,19 +1595,20 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     // (3 trees of 13 over 1500 keys, in equal ranges: 15.3 us with two tiles a CTA at
     // least, 19.9 with four, 18.3 with one)
     a.min_tiles = 2;
+    const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
+    const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;      // at most
     // Units of at most so many tiles are not worth a cut and a join: one token over
-    // 300 keys 6.9 us (cut 11.2), 8 trees of 4 over 900 13.5 (19.1); a tile of many
-    // rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of 13 over 900
-    // 17.6 whole and 16.1 cut.
-    const bool wide = v == kWide128 || v == kWide256;
-    const int whole = wide ? 4 : 8;
+    // 300 keys 6.9 us (cut 11.2), 30 single tokens over 450 to 900 15.0 (19.2); a
+    // tile of many rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of
+    // 13 over 900 17.6 whole and 16.1 cut.  With several units a CTA equal ranges
+    // of tiles spread ragged lengths better (256 tokens over 450 to 900: 77.4 whole,
+    // 73.5 cut; 64 25.9 and 27.8).
+    const int whole = v == kWide128 || v == kWide256 || units > 3 * ctas_of(v, num_sms) ? 4 : 8;
     if ((int64_t)p.table_width * p.block_size <= whole * kKeyTile) {
         a.partial = nullptr;
         a.whole = true;
     }
     // as many CTAs as fill the GPU, or as the block table lets have work
-    const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
-    const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;
     const int64_t tiles = std::max<int64_t>(1, ((int64_t)p.table_width * p.block_size + kKeyTile - 1) / kKeyTile);
     const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, a.whole ? units : units * tiles / a.min_tiles));
     // A CTA that goes from one unit to another loses some 10 us while the cache is
@@ -1615,6 +1616,7 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     // keys take 43 us instead of 46, 16 trees of 16 over 8192 71.2, 74.5.  In
     // the small kernel, with few tiles a CTA, the ranges had better begin with the
     // units.
+    const bool wide = v == kWide128 || v == kWide256;
     a.change = wide || units * tiles >= 8 * ctas ? 6 : 0;
     switch (v) {
     case kSmall16: return p.block_size % kChunk == 0 ? launch_small<1, true>(a, ctas, stream, why)
