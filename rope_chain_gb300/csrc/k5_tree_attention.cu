@@ -118,10 +118,12 @@ __device__ __forceinline__ int32_t most_of(const Args &a, int64_t tiles, int64_t
 }
 
 // The range of CTA c of `ctas`, and where its first slot lies.  Called by all
-// kThreads threads.  kParts: cut into parts where that is better (else only
-// where all units are whole).  Up to 32 sequences a lane takes one, and each warp
-// finds the range by itself; beyond, a thread takes a run of sequences, and the
-// one whose run holds the slot walks it.
+// kThreads threads.  kParts: cut into parts where that is better (not in the small
+// kernel: its start would take 0.7 us longer, one token over 500 keys 7.9 instead
+// of 7.2 us, and few calls have fewer units than CTAs, 4 tokens over 3000 keys 14.0
+// and 12.4).  Up to 32 sequences a lane takes one, and each warp finds the range
+// by itself (3 trees of 13: 16.6 us, by the block 17.0); beyond, a thread takes a
+// run of sequences, and the one whose run holds the slot walks it.
 template <int kRows, int kThreads, bool kParts>
 __device__ Place locate(const Args &a, int c, int ctas) {
     __shared__ int64_t warp_tiles[kParts ? kThreads / 32 : 1], warp_units[kParts ? kThreads / 32 : 1];
