@@ -817,8 +817,10 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
 
 def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
                              device) -> torch.Tensor:
-    """A workspace for tree_attention (rc_tree_attention_workspace_size bytes)."""
-    n = int(lib().rc_tree_attention_workspace_size(rows, seqs, num_heads, num_kv_heads))
+    """A workspace for tree_attention (rc_tree_attention_workspace_size bytes on
+    ``device``)."""
+    with torch.cuda.device(device):
+        n = int(lib().rc_tree_attention_workspace_size(rows, seqs, num_heads, num_kv_heads))
     if n == 0 and rows != 0:
         raise RopeChainError(RC_ERR_INVALID_ARG, "no workspace size for these sizes")
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)

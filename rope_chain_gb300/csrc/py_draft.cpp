@@ -8,10 +8,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Device.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
 
 namespace {
 
@@ -61,23 +64,32 @@ int32_t dtype_of(const Tensor &t, const char *name) {
     return RC_F32;
 }
 
-// The data of a contiguous CUDA array of at least `numel` elements (NULL for None).
+// Every operand lies on one device, that of the call's first tensor: a kernel of
+// one GPU must not get another's addresses.
+void beside(const Tensor &t, at::Device device, const char *name) {
+    TORCH_CHECK_VALUE(t.device() == device, name, " is on device ", t.device(), ", other operands on ", device);
+}
+
+// The data of a contiguous CUDA array of at least `numel` elements on `device`
+// (NULL for None).
 template <typename T>
-const T *array(PyObject *o, at::ScalarType type, int64_t numel, const char *name) {
+const T *array(PyObject *o, at::Device device, at::ScalarType type, int64_t numel, const char *name) {
     if (o == Py_None)
         return nullptr;
     const Tensor &t = tensor(o, name);
     TORCH_CHECK_TYPE(t.scalar_type() == type && t.is_cuda() && t.is_contiguous(), name,
                      " must be a contiguous CUDA ", at::toString(type), " tensor");
+    beside(t, device, name);
     TORCH_CHECK_VALUE(t.numel() >= numel, name, " needs ", numel, " elements, it has ", t.numel());
     return static_cast<const T *>(t.const_data_ptr());
 }
 
-int32_t *counter(PyObject *o) {
-    return const_cast<int32_t *>(array<int32_t>(o, at::kInt, 1, "err"));
+int32_t *counter(PyObject *o, at::Device device) {
+    return const_cast<int32_t *>(array<int32_t>(o, device, at::kInt, 1, "err"));
 }
 
-// `stream` is None (the current stream) or a stream's handle.
+// `stream` is None (the current stream of the current device, which a
+// CUDAGuard has made the operands') or a stream's handle.
 cudaStream_t stream_of(PyObject *o) {
     if (o != Py_None)
         return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(o)));
@@ -93,6 +105,7 @@ Tensor output(PyObject *o, const Tensor &t, const char *what) {
     const Tensor &out = tensor(o, "out");
     TORCH_CHECK_VALUE(out.sizes() == t.sizes() && out.scalar_type() == t.scalar_type() && out.is_cuda(),
                       "out must be a CUDA tensor of the shape and dtype of ", what);
+    beside(out, t.device(), "out");
     return out;
 }
 
@@ -105,20 +118,26 @@ PyObject *rope_table(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const rc_rope_scaling sc = {narrow<int32_t>(integer(args[3]), "scaling"), number(args[4]), number(args[5]),
                                 number(args[6]), number(args[7]), number(args[8])};
     Tensor out;
+    std::optional<at::Device> device;
+    if (args[10] != Py_None) {
+        TORCH_CHECK_TYPE(THPDevice_Check(args[10]), "device must be a torch.device");
+        device = reinterpret_cast<THPDevice *>(args[10])->device;
+        TORCH_CHECK_VALUE(device->is_cuda(), "the table is made on a CUDA device");
+    }
     if (args[11] != Py_None) {
         out = tensor(args[11], "out");
         TORCH_CHECK_VALUE(out.dim() == 2 && out.size(0) == positions && out.size(1) == rot_dim && out.is_cuda() &&
                               out.is_contiguous(), "out must be a contiguous CUDA tensor [max_position, rot_dim]");
+        if (device && device->has_index())
+            beside(out, *device, "out");
+        device = out.device();
     } else {
         TORCH_CHECK_VALUE(positions >= 0 && rot_dim > 0, "max_position must not be negative, rot_dim positive");
-        at::Device device(at::kCUDA, -1);
-        if (args[10] != Py_None) {
-            TORCH_CHECK_TYPE(THPDevice_Check(args[10]), "device must be a torch.device");
-            device = reinterpret_cast<THPDevice *>(args[10])->device;
-            TORCH_CHECK_VALUE(device.is_cuda(), "the table is made on a CUDA device");
-        }
-        out = at::empty({positions, rot_dim}, at::TensorOptions(integer(args[9]) ? at::kFloat : at::kBFloat16).device(device));
     }
+    const c10::cuda::OptionalCUDAGuard guard(device);
+    if (!out.defined())
+        out = at::empty({positions, rot_dim},
+                        at::TensorOptions(integer(args[9]) ? at::kFloat : at::kBFloat16).device(at::kCUDA));
     const rc_status s = rc_rope_table(out.data_ptr(), dtype_of(out, "out"), positions,
                                       narrow<int32_t>(rot_dim, "rot_dim"), number(args[2]), &sc, stream_of(args[12]));
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
@@ -134,16 +153,19 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     TORCH_CHECK_VALUE(x.dim() == 3 && x.stride(2) == 1, "x must be [T, heads, head_dim] with a contiguous last axis");
     TORCH_CHECK_VALUE(table.dim() == 2 && table.is_cuda() && table.is_contiguous(),
                       "cos_sin must be a contiguous CUDA tensor [max_position, rot_dim]");
+    beside(table, x.device(), "cos_sin");
     const int32_t type = dtype_of(x, "x");
+    TORCH_CHECK_TYPE(args[1] != Py_None, "positions must be a tensor");
+    const int64_t *positions = array<int64_t>(args[1], x.device(), at::kLong, x.size(0), "positions");
+    int32_t *err = counter(args[6], x.device());
     const Tensor out = output(args[5], x, "x");
     TORCH_CHECK_VALUE(out.stride(2) == 1, "the last axis of out must be contiguous");
-    TORCH_CHECK_TYPE(args[1] != Py_None, "positions must be a tensor");
+    const c10::cuda::CUDAGuard guard(x.device());
     const rc_status s = rc_rope_apply(
         x.const_data_ptr(), type, x.stride(0), x.stride(1), x.size(0), narrow<int32_t>(x.size(1), "heads"),
-        narrow<int32_t>(x.size(2), "head_dim"), array<int64_t>(args[1], at::kLong, x.size(0), "positions"),
-        table.const_data_ptr(), dtype_of(table, "cos_sin"), table.size(0), narrow<int32_t>(table.size(1), "rot_dim"),
+        narrow<int32_t>(x.size(2), "head_dim"), positions, table.const_data_ptr(), dtype_of(table, "cos_sin"), table.size(0), narrow<int32_t>(table.size(1), "rot_dim"),
         narrow<int32_t>(integer(args[3]), "layout"), PyObject_IsTrue(args[4]), out.data_ptr(), out.stride(0),
-        out.stride(1), counter(args[6]), stream_of(args[7]));
+        out.stride(1), err, stream_of(args[7]));
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -165,8 +187,9 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
                           (table.size(1) <= 1 || table.stride(1) == 1),
                       "block_table must be CUDA int32 [seqs, width] with a contiguous last axis");
     const int64_t seqs = table.size(0);
-    const Tensor out = output(args[7], q, "q");
-    TORCH_CHECK_VALUE(out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64), "out needs strides (*, 64, 1)");
+    const at::Device device = q.device();
+    beside(cache, device, "cache");
+    beside(table, device, "block_table");
     int64_t words = 0;
     if (args[5] != Py_None) {
         const Tensor &mask = tensor(args[5], "tree_mask");
@@ -178,27 +201,33 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (args[8] != Py_None) {
         const Tensor &t = tensor(args[8], "lse");
         TORCH_CHECK_VALUE(t.dim() == 2 && t.size(0) == rows && t.size(1) == heads, "lse must be [rows, num_heads]");
-        lse = const_cast<float *>(array<float>(args[8], at::kFloat, 0, "lse"));
+        lse = const_cast<float *>(array<float>(args[8], device, at::kFloat, 0, "lse"));
     }
     void *workspace = nullptr;
     size_t workspace_bytes = 0;
     if (args[10] != Py_None) {
         const Tensor &t = tensor(args[10], "workspace");
         TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+        beside(t, device, "workspace");
         workspace = t.data_ptr();
         workspace_bytes = t.nbytes();
     }
     TORCH_CHECK_TYPE(args[1] != Py_None && args[2] != Py_None, "row_start and context_len must be tensors");
+    const int32_t *row_start = array<int32_t>(args[1], device, at::kInt, seqs + 1, "row_start");
+    const int32_t *context_len = array<int32_t>(args[2], device, at::kInt, seqs, "context_len");
+    const int64_t *tree_mask = array<int64_t>(args[5], device, at::kLong, 0, "tree_mask");
+    int32_t *err = counter(args[9], device);
+    const Tensor out = output(args[7], q, "q");
+    TORCH_CHECK_VALUE(out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64), "out needs strides (*, 64, 1)");
+    const c10::cuda::CUDAGuard guard(device);
     const rc_status s = rc_tree_attention(
         static_cast<const uint16_t *>(q.const_data_ptr()), q.stride(0), rows, narrow<int32_t>(heads, "num_heads"),
-        narrow<int32_t>(cache.size(1), "num_kv_heads"), array<int32_t>(args[1], at::kInt, seqs + 1, "row_start"),
-        narrow<int32_t>(seqs, "seqs"), array<int32_t>(args[2], at::kInt, seqs, "context_len"),
+        narrow<int32_t>(cache.size(1), "num_kv_heads"), row_start, narrow<int32_t>(seqs, "seqs"), context_len,
         static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0),
-        narrow<int32_t>(table.size(1), "width of block_table"),
-        reinterpret_cast<const uint64_t *>(array<int64_t>(args[5], at::kLong, 0, "tree_mask")),
+        narrow<int32_t>(table.size(1), "width of block_table"), reinterpret_cast<const uint64_t *>(tree_mask),
         narrow<int32_t>(words, "words of tree_mask"), static_cast<const uint16_t *>(cache.const_data_ptr()),
         narrow<int32_t>(cache.size(0), "num_blocks"), narrow<int32_t>(cache.size(2), "block_size"),
-        (float)number(args[6]), static_cast<uint16_t *>(out.data_ptr()), out.stride(0), lse, counter(args[9]),
+        (float)number(args[6]), static_cast<uint16_t *>(out.data_ptr()), out.stride(0), lse, err,
         workspace, workspace_bytes, stream_of(args[11]));
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
@@ -216,34 +245,33 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t rows = logits.size(0), vocab = logits.size(1), seqs = start.numel() - 1;
     TORCH_CHECK_VALUE(vocab <= 1 || logits.stride(1) == 1, "rows of logits must be contiguous");
     const int32_t type = dtype_of(logits, "logits");
-    const Tensor out = output(args[14], logits, "logits");
-    TORCH_CHECK_VALUE(vocab <= 1 || out.stride(1) == 1, "rows of out must be contiguous");
+    const at::Device device = logits.device();
     rc_logits_params p = {};
     TORCH_CHECK_VALUE((args[2] == Py_None) == (args[3] == Py_None), "history and history_start go together");
     if (args[2] != Py_None) {
-        p.history = array<int32_t>(args[2], at::kInt, 0, "history");
+        p.history = array<int32_t>(args[2], device, at::kInt, 0, "history");
         p.history_size = tensor(args[2], "history").numel();
-        p.history_start = array<int64_t>(args[3], at::kLong, seqs + 1, "history_start");
-        p.prompt_len = array<int32_t>(args[4], at::kInt, seqs, "prompt_len");
+        p.history_start = array<int64_t>(args[3], device, at::kLong, seqs + 1, "history_start");
+        p.prompt_len = array<int32_t>(args[4], device, at::kInt, seqs, "prompt_len");
     }
-    p.draft_tokens = array<int32_t>(args[5], at::kInt, rows, "draft_tokens");
+    p.draft_tokens = array<int32_t>(args[5], device, at::kInt, rows, "draft_tokens");
     if (args[6] != Py_None) {
         const Tensor &mask = tensor(args[6], "tree_mask");
         TORCH_CHECK_VALUE(mask.dim() == 2 && mask.size(0) == rows, "tree_mask must be [rows, words]");
-        p.tree_mask = reinterpret_cast<const uint64_t *>(array<int64_t>(args[6], at::kLong, 0, "tree_mask"));
+        p.tree_mask = reinterpret_cast<const uint64_t *>(array<int64_t>(args[6], device, at::kLong, 0, "tree_mask"));
         p.mask_words = narrow<int32_t>(mask.size(1), "words of tree_mask");
         TORCH_CHECK_VALUE(p.mask_words > 0 || rows == 0, "tree_mask needs a word per row at least");
     }
-    p.repetition = array<float>(args[7], at::kFloat, seqs, "repetition");
-    p.frequency = array<float>(args[8], at::kFloat, seqs, "frequency");
-    p.presence = array<float>(args[9], at::kFloat, seqs, "presence");
+    p.repetition = array<float>(args[7], device, at::kFloat, seqs, "repetition");
+    p.frequency = array<float>(args[8], device, at::kFloat, seqs, "frequency");
+    p.presence = array<float>(args[9], device, at::kFloat, seqs, "presence");
     TORCH_CHECK_VALUE((args[10] == Py_None) == (args[11] == Py_None) && (args[10] == Py_None) == (args[12] == Py_None),
                       "bias_start, bias_tokens and bias_values go together");
     if (args[10] != Py_None) {
         p.bias_size = tensor(args[11], "bias_tokens").numel();
-        p.bias_start = array<int32_t>(args[10], at::kInt, seqs + 1, "bias_start");
-        p.bias_tokens = array<int32_t>(args[11], at::kInt, 0, "bias_tokens");
-        p.bias_values = array<float>(args[12], at::kFloat, p.bias_size, "bias_values");
+        p.bias_start = array<int32_t>(args[10], device, at::kInt, seqs + 1, "bias_start");
+        p.bias_tokens = array<int32_t>(args[11], device, at::kInt, 0, "bias_tokens");
+        p.bias_values = array<float>(args[12], device, at::kFloat, p.bias_size, "bias_values");
         if (p.bias_size == 0)                // none for any sequence: an empty tensor has no address
             p.bias_start = p.bias_tokens = nullptr, p.bias_values = nullptr;
     }
@@ -253,14 +281,19 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
                               allowed.size(0) == rows && allowed.size(1) >= (vocab + 31) / 32 &&
                               (allowed.size(1) <= 1 || allowed.stride(1) == 1),
                           "allowed must be CUDA int32 [rows, >= ceil(vocab / 32)], rows contiguous");
+        beside(allowed, device, "allowed");
         p.allowed = static_cast<const uint32_t *>(allowed.const_data_ptr());
         p.allowed_stride = allowed.stride(0);
     }
+    const int32_t *row_start = array<int32_t>(args[1], device, at::kInt, 0, "row_start");
+    int32_t *err = counter(args[15], device);
+    const Tensor out = output(args[14], logits, "logits");
+    TORCH_CHECK_VALUE(vocab <= 1 || out.stride(1) == 1, "rows of out must be contiguous");
+    const c10::cuda::CUDAGuard guard(device);
     const rc_status s = rc_logits_adjust(logits.const_data_ptr(), type, logits.stride(0), rows,
-                                         narrow<int32_t>(vocab, "vocab"),
-                                         array<int32_t>(args[1], at::kInt, 0, "row_start"),
-                                         narrow<int32_t>(seqs, "seqs"), &p, out.data_ptr(), out.stride(0),
-                                         counter(args[15]), stream_of(args[16]));
+                                         narrow<int32_t>(vocab, "vocab"), row_start,
+                                         narrow<int32_t>(seqs, "seqs"), &p, out.data_ptr(), out.stride(0), err,
+                                         stream_of(args[16]));
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }

@@ -1,0 +1,63 @@
+"""Refusals of the drafted tokens' calls in their Python module (no GPU
+needed): the operands are tensors with a device, a shape and a type but no
+memory, and every refusal comes before a data pointer or CUDA is asked for."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import rope_chain_gb300 as rc
+
+BF, F32, I32, I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from rope_chain_gb300 import _build
+    _build.build()
+
+
+def fake(*shape, dtype=BF, device="cuda:0", **kw):
+    with FakeTensorMode():
+        return torch.empty(*shape, dtype=dtype, device=device, **kw)
+
+
+def rope_operands():
+    return dict(x=fake(4, 8, 64), positions=fake(4, dtype=I64), cos_sin=fake(16, 64), out=fake(4, 8, 64),
+                err=fake(1, dtype=I32))
+
+
+def attention_operands():
+    return dict(q=fake(4, 8, 64), row_start=fake(3, dtype=I32), context_len=fake(2, dtype=I32),
+                block_table=fake(2, 5, dtype=I32), cache=fake(9, 2, 16, 128), tree_mask=fake(4, 1, dtype=I64),
+                out=fake(4, 8, 64), lse=fake(4, 8, dtype=F32), err=fake(1, dtype=I32),
+                workspace=fake(1 << 24, dtype=torch.uint8))
+
+
+def logits_operands():
+    return dict(logits=fake(4, 100, dtype=F32), row_start=fake(3, dtype=I32), history=fake(50, dtype=I32),
+                history_start=fake(3, dtype=I64), prompt_len=fake(2, dtype=I32), draft_tokens=fake(4, dtype=I32),
+                tree_mask=fake(4, 1, dtype=I64), repetition=fake(2, dtype=F32), frequency=fake(2, dtype=F32),
+                presence=fake(2, dtype=F32), bias_start=fake(3, dtype=I32), bias_tokens=fake(6, dtype=I32),
+                bias_values=fake(6, dtype=F32), allowed=fake(4, 4, dtype=I32), out=fake(4, 100, dtype=F32),
+                err=fake(1, dtype=I32))
+
+
+# (a tensor without memory sets up the context of its GPU where there are any)
+two_gpus = pytest.mark.skipif(torch.cuda.device_count() == 1, reason="no GPU or two")
+CALLS = {"rope_apply": rope_operands, "tree_attention": attention_operands, "logits_adjust": logits_operands}
+
+
+@two_gpus
+@pytest.mark.parametrize("call,name", [(c, n) for c, make in CALLS.items() for n in make()])
+def test_operands_of_two_gpus_are_refused(call, name):
+    args = CALLS[call]()
+    with FakeTensorMode():
+        args[name] = torch.empty_strided(args[name].shape, args[name].stride(), dtype=args[name].dtype, device="cuda:1")
+    with pytest.raises(ValueError, match="is on device cuda:"):
+        getattr(rc, call)(**args)
+
+
+@two_gpus
+def test_a_table_on_another_gpu_than_its_output_is_refused():
+    with pytest.raises(ValueError, match="is on device cuda:"):
+        rc.rope_table(16, 64, device="cuda:0", out=fake(16, 64, device="cuda:1"))
