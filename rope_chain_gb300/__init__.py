@@ -756,7 +756,10 @@ def read_device_faults(clear: bool = True) -> int:
 #
 # These calls take a few us on the GPU, so they go through a module of their own
 # (csrc/py_draft.cpp) instead of ctypes: it checks the tensors, makes the output
-# and calls the same C ABI.
+# and calls the same C ABI.  With `stream` the call, and the memory of an output
+# that it makes, are as if made under torch.cuda.stream(stream): another stream
+# that uses the operands or the result waits for it (and calls record_stream on
+# what it drops).
 
 _draft_module = None
 

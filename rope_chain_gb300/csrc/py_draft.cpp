@@ -88,25 +88,45 @@ int32_t *counter(PyObject *o, at::Device device) {
     return const_cast<int32_t *>(array<int32_t>(o, device, at::kInt, 1, "err"));
 }
 
-// `stream` is None (the current stream of the current device, which a
-// CUDAGuard has made the operands') or a stream's handle.
-cudaStream_t stream_of(PyObject *o) {
-    if (o != Py_None)
-        return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(o)));
-    return c10::cuda::getCurrentCUDAStream().stream();
-}
+// The device and stream of a call, current while it lasts: the operands' device
+// and `stream`, a stream's handle or None (the device's current stream).  What is
+// allocated meanwhile comes from that stream's memory: on the caller's it could
+// still be in use by work queued there, which the call's stream does not wait for.
+class On {
+public:
+    On(std::optional<at::Device> device, PyObject *stream) : device_(device) {
+        if (stream != Py_None) {
+            handle_ = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(integer(stream)));
+            stream_.reset_stream(c10::cuda::getStreamFromExternal(handle_, c10::cuda::current_device()));
+        } else {
+            handle_ = c10::cuda::getCurrentCUDAStream().stream();
+        }
+    }
+    cudaStream_t stream() const { return handle_; }
+
+private:
+    c10::cuda::OptionalCUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard stream_;
+    cudaStream_t handle_;
+};
 
 void need(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n); }
 
-// The output: `o`, checked to be like `t`, or a new contiguous tensor.
+// The output: `o`, checked to be like `t`, or (undefined) one to be made by made().
 Tensor output(PyObject *o, const Tensor &t, const char *what) {
     if (o == Py_None)
-        return at::empty(t.sizes(), t.options(), at::MemoryFormat::Contiguous);
+        return Tensor();
     const Tensor &out = tensor(o, "out");
     TORCH_CHECK_VALUE(out.sizes() == t.sizes() && out.scalar_type() == t.scalar_type() && out.is_cuda(),
                       "out must be a CUDA tensor of the shape and dtype of ", what);
     beside(out, t.device(), "out");
     return out;
+}
+
+// A new contiguous output like `t` where there is none yet (within an On).
+void made(Tensor &out, const Tensor &t) {
+    if (!out.defined())
+        out = at::empty(t.sizes(), t.options(), at::MemoryFormat::Contiguous);
 }
 
 PyObject *rope_table(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -134,12 +154,12 @@ PyObject *rope_table(PyObject *, PyObject *const *args, Py_ssize_t n) {
     } else {
         TORCH_CHECK_VALUE(positions >= 0 && rot_dim > 0, "max_position must not be negative, rot_dim positive");
     }
-    const c10::cuda::OptionalCUDAGuard guard(device);
+    const On on(device, args[12]);
     if (!out.defined())
         out = at::empty({positions, rot_dim},
                         at::TensorOptions(integer(args[9]) ? at::kFloat : at::kBFloat16).device(at::kCUDA));
     const rc_status s = rc_rope_table(out.data_ptr(), dtype_of(out, "out"), positions,
-                                      narrow<int32_t>(rot_dim, "rot_dim"), number(args[2]), &sc, stream_of(args[12]));
+                                      narrow<int32_t>(rot_dim, "rot_dim"), number(args[2]), &sc, on.stream());
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -158,14 +178,15 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     TORCH_CHECK_TYPE(args[1] != Py_None, "positions must be a tensor");
     const int64_t *positions = array<int64_t>(args[1], x.device(), at::kLong, x.size(0), "positions");
     int32_t *err = counter(args[6], x.device());
-    const Tensor out = output(args[5], x, "x");
-    TORCH_CHECK_VALUE(out.stride(2) == 1, "the last axis of out must be contiguous");
-    const c10::cuda::CUDAGuard guard(x.device());
+    Tensor out = output(args[5], x, "x");
+    TORCH_CHECK_VALUE(!out.defined() || out.stride(2) == 1, "the last axis of out must be contiguous");
+    const On on(x.device(), args[7]);
+    made(out, x);
     const rc_status s = rc_rope_apply(
         x.const_data_ptr(), type, x.stride(0), x.stride(1), x.size(0), narrow<int32_t>(x.size(1), "heads"),
         narrow<int32_t>(x.size(2), "head_dim"), positions, table.const_data_ptr(), dtype_of(table, "cos_sin"), table.size(0), narrow<int32_t>(table.size(1), "rot_dim"),
         narrow<int32_t>(integer(args[3]), "layout"), PyObject_IsTrue(args[4]), out.data_ptr(), out.stride(0),
-        out.stride(1), err, stream_of(args[7]));
+        out.stride(1), err, on.stream());
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -217,9 +238,11 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int32_t *context_len = array<int32_t>(args[2], device, at::kInt, seqs, "context_len");
     const int64_t *tree_mask = array<int64_t>(args[5], device, at::kLong, 0, "tree_mask");
     int32_t *err = counter(args[9], device);
-    const Tensor out = output(args[7], q, "q");
-    TORCH_CHECK_VALUE(out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64), "out needs strides (*, 64, 1)");
-    const c10::cuda::CUDAGuard guard(device);
+    Tensor out = output(args[7], q, "q");
+    TORCH_CHECK_VALUE(!out.defined() || (out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64)),
+                      "out needs strides (*, 64, 1)");
+    const On on(device, args[11]);
+    made(out, q);
     const rc_status s = rc_tree_attention(
         static_cast<const uint16_t *>(q.const_data_ptr()), q.stride(0), rows, narrow<int32_t>(heads, "num_heads"),
         narrow<int32_t>(cache.size(1), "num_kv_heads"), row_start, narrow<int32_t>(seqs, "seqs"), context_len,
@@ -228,7 +251,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(words, "words of tree_mask"), static_cast<const uint16_t *>(cache.const_data_ptr()),
         narrow<int32_t>(cache.size(0), "num_blocks"), narrow<int32_t>(cache.size(2), "block_size"),
         (float)number(args[6]), static_cast<uint16_t *>(out.data_ptr()), out.stride(0), lse, err,
-        workspace, workspace_bytes, stream_of(args[11]));
+        workspace, workspace_bytes, on.stream());
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }
@@ -287,13 +310,14 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
     const int32_t *row_start = array<int32_t>(args[1], device, at::kInt, 0, "row_start");
     int32_t *err = counter(args[15], device);
-    const Tensor out = output(args[14], logits, "logits");
-    TORCH_CHECK_VALUE(vocab <= 1 || out.stride(1) == 1, "rows of out must be contiguous");
-    const c10::cuda::CUDAGuard guard(device);
+    Tensor out = output(args[14], logits, "logits");
+    TORCH_CHECK_VALUE(!out.defined() || vocab <= 1 || out.stride(1) == 1, "rows of out must be contiguous");
+    const On on(device, args[16]);
+    made(out, logits);
     const rc_status s = rc_logits_adjust(logits.const_data_ptr(), type, logits.stride(0), rows,
                                          narrow<int32_t>(vocab, "vocab"), row_start,
                                          narrow<int32_t>(seqs, "seqs"), &p, out.data_ptr(), out.stride(0), err,
-                                         stream_of(args[16]));
+                                         on.stream());
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }

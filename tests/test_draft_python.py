@@ -1,6 +1,6 @@
 """Refusals of the drafted tokens' calls in their Python module (no GPU
 needed): the operands are tensors with a device, a shape and a type but no
-memory, and every refusal comes before a data pointer or CUDA is asked for."""
+memory, and every refusal comes before CUDA is asked for anything."""
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
