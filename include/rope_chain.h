@@ -715,7 +715,10 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
                             cudaStream_t stream);
 
 /* Workspace bytes of rc_tree_attention for these sizes on the current device
-   (0 for sizes it refuses). */
+   (0 for sizes it refuses).  They never shrink with more rows, fewer sequences or
+   more heads per KV head, so a workspace for the most rows, the fewest sequences
+   that have them (one serves any) and the largest num_heads / num_kv_heads
+   serves every call up to those. */
 size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_heads,
                                         int32_t num_kv_heads);
 

@@ -821,7 +821,7 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
 def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
                              device) -> torch.Tensor:
     """A workspace for tree_attention (rc_tree_attention_workspace_size bytes on
-    ``device``)."""
+    ``device``): it also serves calls of fewer rows and of more sequences."""
     with torch.cuda.device(device):
         n = int(lib().rc_tree_attention_workspace_size(rows, seqs, num_heads, num_kv_heads))
     if n == 0 and rows != 0:

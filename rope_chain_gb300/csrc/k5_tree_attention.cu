@@ -1579,11 +1579,14 @@ cudaError_t launch_wide(const Args &a, int ctas, cudaStream_t stream, const char
 
 size_t tree_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms)
 {
+    // For whichever block size the cache has (a multiple of 8 gives the variant of
+    // most rows) and for any call of fewer rows or more sequences: the variants of
+    // smaller tiles have twice the CTAs, and so may take a few headers more.
+    const Variant last = variant_for(rows, seqs, group, 8);
     size_t most = 0;
-    for (int32_t block_size : {8, 1}) {                 // whichever the cache has
-        const Variant v = variant_for(rows, seqs, group, block_size);
-        most = std::max(most, 2 * (size_t)ctas_of(v, num_sms) * slot_floats(v) * sizeof(float));
-    }
+    for (const Variant v : {kSmall16, kSmall32, kWide128, kWide256})
+        if (v <= last)
+            most = std::max(most, 2 * (size_t)ctas_of(v, num_sms) * slot_floats(v) * sizeof(float));
     return most;
 }
 

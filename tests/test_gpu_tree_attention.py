@@ -379,3 +379,26 @@ def test_reads_what_the_store_wrote():
     ref = torch.einsum("nhgp,phd->nhgd", w, v).reshape(2, 16, 64)
     mag = torch.einsum("nhgp,phd->nhgd", w, v.abs()).reshape(2, 16, 64)
     assert bool(((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -30).all())
+
+
+@pytest.mark.parametrize("group", [1, 3, 8, 16, 64])
+def test_workspace_of_the_largest_call_serves_smaller_ones(group):
+    size = lambda rows, seqs: rc.lib().rc_tree_attention_workspace_size(rows, seqs, 2 * group, 2)
+    rows = [1, 2, 3, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 1000]
+    for seqs in (1, 2, 7):
+        sizes = [size(r, seqs) for r in rows]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    for r in rows:
+        sizes = [size(r, seqs) for seqs in (400, 64, 9, 3, 2, 1)]
+        assert sizes == sorted(sizes)
+        assert size(r, 1) <= rc.lib().rc_tree_attention_workspace_size(r, 1, 4 * group, 2)
+
+
+@pytest.mark.parametrize("small,large", [([2], 4), ([16], 64), ([4, 1], 64)])
+def test_small_call_with_a_large_calls_workspace(small, large):
+    case = Case(19, small, [3000] * len(small), 2, 8, 16)
+    ws = rc.tree_attention_workspace(large, 1, 16, 2, DEV)
+    lse = torch.empty(case.rows, 16, device=DEV)
+    out = rc.tree_attention(case.q, case.row_start, case.context, case.table, case.cache, tree_mask=case.mask, lse=lse,
+                            workspace=ws)
+    check(case, out, lse)
