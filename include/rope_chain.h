@@ -635,7 +635,8 @@ typedef enum {
  *                 t*row_stride + h*head_stride + e (strides in elements, >= 0,
  *                 either order of tokens and heads; aligned to the element).
  *                 out may be x with x's strides (in place), or else must not
- *                 overlap x; its elements must be distinct
+ *                 overlap it; it overlaps no other operand, and its elements are
+ *                 distinct
  *   T, heads      T >= 0, heads >= 1, T*heads < 2^31 (T == 0: nothing launched, and x,
  *                 out and positions may be NULL)
  *   rot_dim       even, 2 <= rot_dim <= min(head_dim, 512); PAIRS needs an even
@@ -692,7 +693,7 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
  *                16-byte aligned; num_blocks*block_size < 2^31
  *   scale        > 0, finite (1/8 for 64-wide heads)
  *   out          bf16 [rows, num_heads, 64], as q with out_row_stride; 16-byte
- *                aligned; must not overlap q or the cache
+ *                aligned; out, lse and the workspace overlap no other operand
  *   lse          optional FP32 [rows, num_heads]: log of the row's sum of
  *                exp(scale * q.k), to join results over several caches
  *   err          optional device int32 counter
@@ -739,7 +740,7 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
  *   logits       `dtype` (rc_dtype) [rows, vocab], row stride row_stride
  *                elements, aligned to its element
  *   out          as logits with out_row_stride; may be logits with its stride
- *                (in place), else must not overlap it
+ *                (in place), else must not overlap it; overlaps no other operand
  *   rows         0 <= rows <= 2^30 (0: nothing launched, logits and out may be
  *                NULL); rows of no sequence
  *                are left

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 namespace {
 
@@ -36,6 +37,19 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
+}
+
+// Bytes that a call touches (none without an address).
+struct Span {
+    const void *p;
+    size_t n;
+};
+
+bool overlap(const Span &written, std::initializer_list<Span> others) {
+    for (const Span &o : others)
+        if (written.p && o.p && written.n > 0 && o.n > 0 && overlap(written.p, written.n, o.p, o.n))
+            return true;
+    return false;
 }
 
 int num_sms_current() {
@@ -179,6 +193,10 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
     const bool in_place = x == out && x_row_stride == out_row_stride && x_head_stride == out_head_stride;
     if (!in_place && overlap(x, x_span, out, out_span))
         return fail(RC_ERR_INVALID_ARG, "%s: out overlaps x and is not x itself", fn);
+    if (!aligned(err, 4) ||
+        overlap({out, out_span}, {{positions, (size_t)T * 8}, {cos_sin, (size_t)max_position * rot_dim * table_size},
+                                  {err, 4}}))
+        return fail(RC_ERR_INVALID_ARG, "%s: out overlaps positions, cos_sin or err, or err is not 4-byte aligned", fn);
     const int vec = 16 / size;
     const bool wide = aligned(x, 16) && aligned(out, 16) && aligned(cos_sin, 16) &&
                       (x_row_stride | x_head_stride | out_row_stride | out_head_stride | (int64_t)head_dim) % vec == 0 &&
@@ -261,11 +279,17 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
     if (rows == 0)
         return ok();
     const size_t out_bytes = ((rows - 1) * out_row_stride + width) * 2;
-    const size_t cache_bytes = (size_t)num_blocks * num_kv_heads * block_size * 128 * 2;
-    if (overlap(out, out_bytes, q, ((rows - 1) * q_row_stride + width) * 2) ||
-        overlap(out, out_bytes, cache, cache_bytes) ||
-        (lse && overlap(lse, (size_t)rows * num_heads * 4, out, out_bytes)))
-        return fail(RC_ERR_INVALID_ARG, "%s: out overlaps q, the cache or lse", fn);
+    const Span out_span = {out, out_bytes}, lse_span = {lse, (size_t)rows * num_heads * 4};
+    const Span q_span = {q, (size_t)((rows - 1) * q_row_stride + width) * 2};
+    const Span cache_span = {cache, (size_t)num_blocks * num_kv_heads * block_size * 128 * 2};
+    const Span start_span = {row_start, ((size_t)seqs + 1) * 4}, len_span = {context_len, (size_t)seqs * 4};
+    const Span table_span = {block_table, table_width > 0 ? (size_t)((seqs - 1) * table_stride + table_width) * 4 : (size_t)0};
+    const Span mask_span = {tree_mask, (size_t)rows * mask_words * 8}, err_span = {err, 4};
+    auto reads = [&](const Span &written) {
+        return overlap(written, {q_span, cache_span, start_span, len_span, table_span, mask_span, err_span});
+    };
+    if (reads(out_span) || reads(lse_span) || overlap(lse_span, {out_span}) || !aligned(err, 4))
+        return fail(RC_ERR_INVALID_ARG, "%s: out or lse overlaps another operand, or err is not 4-byte aligned", fn);
     const int sms = num_sms_current();
     if (sms <= 0)
         return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
@@ -275,9 +299,7 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
         if (workspace_bytes < need)
             return fail(RC_ERR_INVALID_ARG, "%s: the workspace holds %zu bytes, these sizes take %zu", fn,
                         workspace_bytes, need);
-        if (overlap(workspace, need, out, out_bytes) || overlap(workspace, need, cache, cache_bytes) ||
-            overlap(workspace, need, q, ((rows - 1) * q_row_stride + width) * 2) ||
-            (lse && overlap(workspace, need, lse, (size_t)rows * num_heads * 4)))
+        if (reads({workspace, need}) || overlap({workspace, need}, {out_span, lse_span}))
             return fail(RC_ERR_INVALID_ARG, "%s: the workspace overlaps an operand", fn);
     }
     rc::TreeAttentionLaunch a{};
@@ -355,6 +377,19 @@ rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride
     const bool in_place = logits == out && (rows == 1 || row_stride == out_row_stride);
     if (!in_place && overlap(logits, in_bytes, out, out_bytes))
         return fail(RC_ERR_INVALID_ARG, "%s: out overlaps logits and is not logits itself", fn);
+    // (what other CTAs still read while one writes)
+    const size_t per_seq = (size_t)seqs * 4, starts = ((size_t)seqs + 1) * 4;
+    if (!aligned(err, 4) ||
+        overlap({out, out_bytes},
+                {{row_start, starts}, {p.history, p.history ? (size_t)p.history_size * 4 : (size_t)0},
+                 {p.history ? p.history_start : nullptr, 2 * starts}, {p.prompt_len, per_seq},
+                 {p.draft_tokens, (size_t)rows * 4}, {p.tree_mask, (size_t)rows * p.mask_words * 8},
+                 {p.repetition, per_seq}, {p.frequency, per_seq}, {p.presence, per_seq},
+                 {p.bias_start, starts}, {p.bias_tokens, (size_t)p.bias_size * 4},
+                 {p.bias_values, (size_t)p.bias_size * 4},
+                 {p.allowed, (size_t)((rows - 1) * p.allowed_stride + (vocab + 31) / 32) * 4}, {err, 4}}))
+        return fail(RC_ERR_INVALID_ARG, "%s: out overlaps a history, a mask or another operand that is read, or err "
+                    "is not 4-byte aligned", fn);
     const int sms = num_sms_current();
     if (sms <= 0)
         return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);

@@ -143,3 +143,31 @@ def test_python_checks_shapes_and_types():
         rc.logits_adjust(torch.zeros(4, 100), torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="scaling"):
         rc.rope_table(16, scaling="other")
+
+
+def test_outputs_over_what_is_still_read(lib):
+    """Other CTAs read positions, tables, lists and masks while one writes its outputs."""
+    bad = rc.RC_ERR_INVALID_ARG
+    end = OUT + 2 * 4 * 512                            # of out: [4, 8, 64] bf16
+    for at in (OUT, OUT + 512, end - 16):
+        for name in ("pos", "tab"):
+            assert apply(lib, **{name: at}) == bad, (name, at)
+        for name in ("rs", "cl", "bt", "tm"):
+            assert attend(lib, **{name: at}) == bad, (name, at)
+    assert attend(lib, tm=OUT - 24) == bad             # the mask's last row
+    assert attend(lib, bt=OUT - 28) == bad             # the table's last
+    lse = 0x5000000
+    for name in ("q", "ca", "rs", "cl", "bt", "tm"):
+        assert attend(lib, lse=lse, **{name: lse}) == bad, name
+    last = OUT + 4 * 399                               # of out: [4, 100] FP32
+    assert adjust(lib, rs=last) == bad
+    for at in (OUT & ~7, last & ~7):
+        for params in (dict(history=at, history_size=1, history_start=0x2000),
+                       dict(history=0x1000, history_size=1, history_start=at), dict(prompt_len=at),
+                       dict(draft_tokens=at), dict(tree_mask=at, mask_words=1), dict(repetition=at),
+                       dict(frequency=at), dict(presence=at), dict(allowed=at, allowed_stride=4),
+                       dict(bias_start=at, bias_tokens=0x1000, bias_values=0x2000, bias_size=2),
+                       dict(bias_start=0x1000, bias_tokens=at, bias_values=0x2000, bias_size=2),
+                       dict(bias_start=0x1000, bias_tokens=0x2000, bias_values=at, bias_size=2)):
+            assert adjust(lib, params=params) == bad, params
+    assert adjust(lib, params=dict(allowed=OUT - 48, allowed_stride=4)) == bad

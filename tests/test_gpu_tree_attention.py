@@ -402,3 +402,16 @@ def test_small_call_with_a_large_calls_workspace(small, large):
     out = rc.tree_attention(case.q, case.row_start, case.context, case.table, case.cache, tree_mask=case.mask, lse=lse,
                             workspace=ws)
     check(case, out, lse)
+
+
+def test_workspace_over_another_operand_is_refused():
+    case = Case(23, [2, 3], [300, 40], 2, 4, 16)
+    ws = rc.tree_attention_workspace(case.rows, 2, 8, 2, DEV)
+    ws[64:64 + 12].view(torch.int32).copy_(case.row_start)
+    lists = dict(tree_mask=case.mask, workspace=ws)
+    with pytest.raises(rc.RopeChainError, match="workspace"):
+        rc.tree_attention(case.q, ws[64:64 + 12].view(torch.int32), case.context, case.table, case.cache, **lists)
+    with pytest.raises(rc.RopeChainError, match="workspace"):
+        rc.tree_attention(case.q, case.row_start, ws[64:64 + 8].view(torch.int32), case.table, case.cache, **lists)
+    with pytest.raises(rc.RopeChainError, match="workspace"):
+        rc.tree_attention(case.q, case.row_start, case.context, case.table, case.cache, err=ws[:4].view(torch.int32), **lists)
