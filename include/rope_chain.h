@@ -733,7 +733,7 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
  * is in the prompt or g > 0.  In FP32, in this order (the quotient as a product
  * with the rounded 1 / repetition):
  *   x = logit;  if said: x = x > 0 ? x / repetition : x * repetition;
- *   x = x - frequency * g;  if g > 0: x = x - presence;
+ *   if g > 0: x = x - frequency * g (fused), x = x - presence;
  *   x = x + bias of t;  if t is not allowed: x = -infinity
  * rounded once to `dtype`.
  *

@@ -5,7 +5,7 @@
 // history past the prompt, and the drafted tokens that the row's node sees,
 // itself among them) and `seen` = g > 0 or t is in the prompt:
 //   x = logit;  x = seen ? (x > 0 ? x / rep : x * rep) : x
-//   x = x - freq * g - (g > 0 ? pres : 0);  x = x + bias;  disallowed -> -inf
+//   x = g > 0 ? x - freq * g - pres : x;  x = x + bias;  disallowed -> -inf
 // in FP32 in this order (x / rep as x times the rounded 1 / rep, freq * g fused
 // into its difference), rounded once to the logits' type.
 //
@@ -392,9 +392,10 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         }
         if (g != 0u || (w & kPrompt) != 0u)
             x = __fmul_rn(x, x > 0.0f ? less : rep);
-        x = __fmaf_rn(-freq, (float)g, x);
+        // (without an occurrence there is nothing to subtract: an infinite penalty
+        // times zero would be NaN)
         if (g != 0u)
-            x = __fsub_rn(x, pres);
+            x = __fsub_rn(__fmaf_rn(-freq, (float)g, x), pres);
         if (w & kBias)
             x = __fadd_rn(x, __uint_as_float(s.bias[at]));
         return x;

@@ -193,3 +193,25 @@ def test_rows_without_a_sequence_and_stream():
     torch.cuda.synchronize()
     check(logits, start, kw, sees, out[:7])
     assert bool((out[7:] == 4).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_infinite_penalties_touch_what_was_generated_only(dtype):
+    """A frequency or presence of infinity forbids what was generated; what the prompt, a bias or another node of
+    the tree names, but the row's own past does not (g = 0), has no penalty to multiply."""
+    logits, start, kw, sees = make(21, [6, 5], 900, 200, dtype=dtype, parts="hrdmb")
+    plain = rc.logits_adjust(logits, start, **kw)
+    ref, tol = reference(logits, start, kw, sees)
+    host = {k: v.cpu().numpy() for k, v in kw.items()}
+    made = np.zeros(ref.shape, bool)
+    for b in range(2):
+        h = host["history"][host["history_start"][b]:host["history_start"][b + 1]][host["prompt_len"][b]:]
+        for i in range(*start.cpu().numpy()[b:b + 2]):
+            made[i, h] = True
+            r0 = int(start[b])
+            made[i, host["draft_tokens"][r0:int(start[b + 1])][sees[b][i - r0]]] = True
+    assert made.any() and not made.all()
+    for name in ("frequency", "presence"):
+        got = rc.logits_adjust(logits, start, **kw, **{name: torch.full((2,), float("inf"), device=DEV)}).double().cpu().numpy()
+        assert np.isneginf(got[made]).all(), name
+        assert np.array_equal(got[~made], plain.double().cpu().numpy()[~made]), name
