@@ -783,17 +783,24 @@ def _draft():
 
 
 def rope_table(max_position: int, rot_dim: int = HEAD_DIM, *, theta: float = 10000.0,
-               scaling: str = "none", factor: float = 1.0, original_max_position: float = 1.0,
+               scaling: str = "none", factor: float = 1.0,
+               original_max_position: Optional[float] = None,
                beta_fast: float = 32.0, beta_slow: float = 1.0, attention_factor: float = 1.0,
                dtype: torch.dtype = torch.bfloat16, device=None,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The cos|sin table [max_position, rot_dim] (rc_rope_table): cos in the
     first rot_dim / 2 columns, sin in the others, both times
-    ``attention_factor``; ``scaling`` "none", "linear", "base" or "parts".  A
-    bfloat16 table of 64 columns is what the store and the QKV front read."""
+    ``attention_factor``; ``scaling`` "none", "linear", "base" or "parts", which
+    needs ``original_max_position``, the positions trained on, and is usually
+    given with attention_factor = 0.1 * ln(factor) + 1.  A bfloat16 table of 64
+    columns is what the store and the QKV front read."""
     kind = ROPE_SCALINGS.get(scaling)
     if kind is None:
         raise ValueError(f"unknown scaling {scaling!r}: one of {sorted(ROPE_SCALINGS)}")
+    if original_max_position is None:
+        if scaling == "parts":
+            raise ValueError("scaling by parts needs original_max_position")
+        original_max_position = 1.0
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("dtype must be bfloat16 or float32")
     if device is not None and not isinstance(device, torch.device):

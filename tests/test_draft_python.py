@@ -61,3 +61,9 @@ def test_operands_of_two_gpus_are_refused(call, name):
 def test_a_table_on_another_gpu_than_its_output_is_refused():
     with pytest.raises(ValueError, match="is on device cuda:"):
         rc.rope_table(16, 64, device="cuda:0", out=fake(16, 64, device="cuda:1"))
+
+
+def test_scaling_by_parts_needs_the_trained_positions():
+    """Without them every column but the first would be divided by the factor."""
+    with pytest.raises(ValueError, match="original_max_position"):
+        rc.rope_table(16, 64, scaling="parts", factor=4.0, out=fake(16, 64))
