@@ -811,6 +811,24 @@ def rope_table(max_position: int, rot_dim: int = HEAD_DIM, *, theta: float = 100
         None if stream is None else stream.cuda_stream)
 
 
+class _Turned(torch.autograd.Function):
+    """rope_apply of an x that requires a gradient: linear, so the gradient is
+    the transposed rotation of the output's."""
+
+    @staticmethod
+    def forward(ctx, x, positions, cos_sin, layout, inverse, err):
+        ctx.save_for_backward(positions, cos_sin)
+        ctx.how = layout, inverse
+        return _draft().rope_apply(x, positions, cos_sin, layout, inverse, None, err, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        layout, inverse = ctx.how
+        if grad.stride(2) != 1:
+            grad = grad.contiguous()
+        return (rope_apply(grad, *ctx.saved_tensors, layout=layout, inverse=not inverse),) + (None,) * 5
+
+
 def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *,
                layout: int = RC_ROPE_PAIRS, inverse: bool = False,
                out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
@@ -820,7 +838,12 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
     the rows ``positions`` (int64 [T]) of ``cos_sin`` [max_position, rot_dim]
     in the first rot_dim elements of each head; the rest is copied.
     ``inverse``: the transposed rotation (the gradient with respect to x, given
-    that of the output).  ``out`` may be x (in place)."""
+    that of the output; autograd takes it where x requires one, without
+    ``out``).  ``out`` may be x (in place)."""
+    if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad and out is None \
+            and not cos_sin.requires_grad:
+        with torch.cuda.stream(stream):
+            return _Turned.apply(x, positions, cos_sin, layout, inverse, err)
     return (_draft_module or _draft()).rope_apply(x, positions, cos_sin, layout, inverse, out, err,
                                                   None if stream is None else stream.cuda_stream)
 
@@ -850,7 +873,8 @@ def tree_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.
     bit j of a row is set where it sees node j of its tree (None: every node up
     to itself).  ``lse`` float32 [rows, num_heads] receives the log sums.
     ``workspace``: tree_attention_workspace(); without one the keys are not
-    split over the GPU.  Returns out, bf16 [rows, num_heads, 64]."""
+    split over the GPU.  Returns out, bf16 [rows, num_heads, 64].  It has no
+    gradient: operands that require one are refused outside torch.no_grad()."""
     return (_draft_module or _draft()).tree_attention(
         q, row_start, context_len, block_table, cache, tree_mask, scale, out, lse, err, workspace,
         None if stream is None else stream.cuda_stream)
@@ -877,7 +901,8 @@ def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
     prompt; draft_tokens int32 [rows] and tree_mask int64 [rows, words] as in
     tree_attention; repetition, frequency, presence float32 [seqs]; bias_start
     int32 [seqs + 1], bias_tokens int32, bias_values float32; allowed int32
-    bit words [rows, >= ceil(vocab / 32)].  ``out`` may be ``logits``."""
+    bit words [rows, >= ceil(vocab / 32)].  ``out`` may be ``logits``.  It has
+    no gradient: operands that require one are refused outside torch.no_grad()."""
     return (_draft_module or _draft()).logits_adjust(
         logits, row_start, history, history_start, prompt_len, draft_tokens, tree_mask, repetition,
         frequency, presence, bias_start, bias_tokens, bias_values, allowed, out, err,

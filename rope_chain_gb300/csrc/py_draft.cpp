@@ -7,6 +7,7 @@
 #include "rope_chain.h"
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -70,6 +71,12 @@ void beside(const Tensor &t, at::Device device, const char *name) {
     TORCH_CHECK_VALUE(t.device() == device, name, " is on device ", t.device(), ", other operands on ", device);
 }
 
+// The calls record nothing for autograd (rope_apply does so in Python).
+void no_gradient(const Tensor &t, const char *name) {
+    TORCH_CHECK_VALUE(!t.requires_grad() || !at::GradMode::is_enabled(), name, " requires a gradient, which this call "
+                      "does not give: detach it or call under torch.no_grad()");
+}
+
 // The data of a contiguous CUDA array of at least `numel` elements on `device`
 // (NULL for None).
 template <typename T>
@@ -80,6 +87,7 @@ const T *array(PyObject *o, at::Device device, at::ScalarType type, int64_t nume
     TORCH_CHECK_TYPE(t.scalar_type() == type && t.is_cuda() && t.is_contiguous(), name,
                      " must be a contiguous CUDA ", at::toString(type), " tensor");
     beside(t, device, name);
+    no_gradient(t, name);
     TORCH_CHECK_VALUE(t.numel() >= numel, name, " needs ", numel, " elements, it has ", t.numel());
     return static_cast<const T *>(t.const_data_ptr());
 }
@@ -120,6 +128,7 @@ Tensor output(PyObject *o, const Tensor &t, const char *what) {
     TORCH_CHECK_VALUE(out.sizes() == t.sizes() && out.scalar_type() == t.scalar_type() && out.is_cuda(),
                       "out must be a CUDA tensor of the shape and dtype of ", what);
     beside(out, t.device(), "out");
+    no_gradient(out, "out");
     return out;
 }
 
@@ -148,6 +157,7 @@ PyObject *rope_table(PyObject *, PyObject *const *args, Py_ssize_t n) {
         out = tensor(args[11], "out");
         TORCH_CHECK_VALUE(out.dim() == 2 && out.size(0) == positions && out.size(1) == rot_dim && out.is_cuda() &&
                               out.is_contiguous(), "out must be a contiguous CUDA tensor [max_position, rot_dim]");
+        no_gradient(out, "out");
         if (device && device->has_index())
             beside(out, *device, "out");
         device = out.device();
@@ -174,6 +184,8 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     TORCH_CHECK_VALUE(table.dim() == 2 && table.is_cuda() && table.is_contiguous(),
                       "cos_sin must be a contiguous CUDA tensor [max_position, rot_dim]");
     beside(table, x.device(), "cos_sin");
+    no_gradient(x, "x");
+    no_gradient(table, "cos_sin");
     const int32_t type = dtype_of(x, "x");
     TORCH_CHECK_TYPE(args[1] != Py_None, "positions must be a tensor");
     const int64_t *positions = array<int64_t>(args[1], x.device(), at::kLong, x.size(0), "positions");
@@ -211,6 +223,8 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const at::Device device = q.device();
     beside(cache, device, "cache");
     beside(table, device, "block_table");
+    no_gradient(q, "q");
+    no_gradient(cache, "cache");
     int64_t words = 0;
     if (args[5] != Py_None) {
         const Tensor &mask = tensor(args[5], "tree_mask");
@@ -269,6 +283,7 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
     TORCH_CHECK_VALUE(vocab <= 1 || logits.stride(1) == 1, "rows of logits must be contiguous");
     const int32_t type = dtype_of(logits, "logits");
     const at::Device device = logits.device();
+    no_gradient(logits, "logits");
     rc_logits_params p = {};
     TORCH_CHECK_VALUE((args[2] == Py_None) == (args[3] == Py_None), "history and history_start go together");
     if (args[2] != Py_None) {

@@ -67,3 +67,16 @@ def test_scaling_by_parts_needs_the_trained_positions():
     """Without them every column but the first would be divided by the factor."""
     with pytest.raises(ValueError, match="original_max_position"):
         rc.rope_table(16, 64, scaling="parts", factor=4.0, out=fake(16, 64))
+
+
+FLOATS = [("rope_apply", n) for n in ("x", "cos_sin", "out")] + [("tree_attention", n) for n in ("q", "cache", "out", "lse")] + \
+    [("logits_adjust", n) for n in ("logits", "repetition", "frequency", "presence", "bias_values", "out")]
+
+
+@pytest.mark.parametrize("call,name", FLOATS)
+def test_gradients_are_not_dropped_silently(call, name):
+    """What requires a gradient, where the call gives none, is refused while gradients are recorded."""
+    args = CALLS[call]()
+    args[name] = fake(*args[name].shape, dtype=args[name].dtype, requires_grad=True)
+    with pytest.raises(ValueError, match=f"{name} requires a gradient"):
+        getattr(rc, call)(**args)

@@ -178,3 +178,29 @@ def test_the_fronts_rotation():
     rc.kv_store_from_projection(kv, H, pos, [slots], cs, [turned], 1e-6)
     keys = plain[slots // 16, :, slots % 16, :64]
     assert torch.equal(rc.rope_apply(keys, pos, cs), turned[slots // 16, :, slots % 16, :64])
+
+
+@pytest.mark.parametrize("layout", [rc.RC_ROPE_PAIRS, rc.RC_ROPE_HALVES])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("side", [False, True])
+def test_autograd_takes_the_transposed_rotation(layout, inverse, side):
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.randn(9, 3, 96, generator=gen, device=DEV).to(BF).requires_grad_()
+    w = torch.randn(9, 3, 96, generator=gen, device=DEV).to(BF)
+    cs, pos = rc.rope_table(64, 48, device=DEV), torch.randint(0, 64, (9,), generator=gen, device=DEV)
+    stream = torch.cuda.Stream() if side else None
+    torch.cuda.synchronize()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = rc.rope_apply(x, pos, cs, layout=layout, inverse=inverse, stream=stream, err=err)
+    torch.cuda.synchronize()
+    y.backward(w)
+    torch.cuda.synchronize()
+    with torch.no_grad():
+        assert torch.equal(y, rc.rope_apply(x, pos, cs, layout=layout, inverse=inverse))
+        assert torch.equal(x.grad, rc.rope_apply(w, pos, cs, layout=layout, inverse=not inverse))
+    # a gradient that is broadcast along the heads' elements
+    x.grad = None
+    rc.rope_apply(x, pos, cs, layout=layout, inverse=inverse).sum().backward()
+    with torch.no_grad():
+        assert torch.equal(x.grad, rc.rope_apply(torch.ones_like(w), pos, cs, layout=layout, inverse=not inverse))
+    assert not rc.rope_apply(x.detach(), pos, cs, layout=layout).requires_grad
