@@ -19,6 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "librope_chain.so")
 MODULE = os.path.join(HERE, "_draft.so")
+MODULE_SOURCE = "py_draft.cpp"
+MODULE_STAMP = os.path.join(BUILD, "module.txt")      # the torch and Python that MODULE was made for
+HEADER = os.path.join(ROOT, "include", "rope_chain.h")
 SOURCES = ["rc_api.cu", "k1_norms.cu", "k2_gemm.cu", "k3_store.cu", "k4_qkv_front.cu",
            "rc_project_static.cu", "k5_tree_attention.cu", "k6_rope.cu", "k7_logits.cu", "rc_draft.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,7 +47,8 @@ def _torch_flags():
     include = os.path.join(root, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     lib = os.path.join(root, "lib")
-    compile_flags = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I", include,
+    # (the version: a torch put in place of another of the same path)
+    compile_flags = [f'-DRC_TORCH_VERSION="{torch.__version__}"', "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", include,
                      "-I", os.path.join(include, "torch", "csrc", "api", "include"),
                      "-I", sysconfig.get_paths()["include"], "-I", cuda,
                      "-I", os.path.join(ROOT, "include"),
@@ -54,60 +58,85 @@ def _torch_flags():
     return compile_flags, link_flags
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MODULE):
+def _run(cmd, what: str) -> str:
+    """Runs a compiler; what it printed, or RuntimeError."""
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr + r.stdout
+
+
+def _link(cmd, target: str) -> None:
+    """Links `target` beside its place, then moves it there."""
+    tmp = f"{target}.{os.getpid()}.tmp"
+    _run([*cmd, "-o", tmp], f"link of {os.path.basename(target)}")
+    os.replace(tmp, target)
+
+
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
+def _library_stale() -> bool:
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != MODULE_SOURCE]
+    return _older(LIB, deps + [HEADER, os.path.abspath(__file__)])
+
+
+def _module_stale(made_for: str) -> bool:
+    if _older(MODULE, [os.path.join(CSRC, MODULE_SOURCE), HEADER, os.path.abspath(__file__)]):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MODULE))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(ROOT, "include", "rope_chain.h"))
-    deps.append(os.path.abspath(__file__))
-    return any(os.path.getmtime(d) > t for d in deps)
+    try:
+        with open(MODULE_STAMP) as f:
+            return f.read() != made_for
+    except OSError:
+        return True
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_library() -> None:
     cc = nvcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [cc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr + r.stdout
+        return obj, _run([cc, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj], f"nvcc on {src}")
 
-    cxx = shutil.which("g++") or "c++"
-    compile_flags, link_flags = _torch_flags()
-
-    def compile_module():
-        obj = os.path.join(BUILD, "py_draft.o")
-        cmd = [cxx, *compile_flags, "-c", os.path.join(CSRC, "py_draft.cpp"), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on py_draft.cpp:\n{r.stdout}\n{r.stderr}")
-        return obj
-
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(compile_module)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        module_obj = module.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = MODULE + f".{os.getpid()}.tmp"
-    cmd = [cxx, "-shared", "-o", tmp, module_obj, "-L" + HERE, "-lrope_chain", *link_flags]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the module failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MODULE)
+    _link([cc, *ARCH, "-shared", *(o for o, _ in results)], LIB)
+
+
+def _compile_module(compile_flags) -> str:
+    obj = os.path.join(BUILD, MODULE_SOURCE.replace(".cpp", ".o"))
+    cxx = shutil.which("g++") or "c++"
+    _run([cxx, *compile_flags, "-c", os.path.join(CSRC, MODULE_SOURCE), "-o", obj], f"g++ on {MODULE_SOURCE}")
+    return obj
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is missing or older than its sources.  The library wants
+    nothing of torch and is in place before a failure of the module is raised."""
+    os.makedirs(BUILD, exist_ok=True)
+
+    def module_object():
+        """(object or None, linker flags, what it was made for)."""
+        compile_flags, link_flags = _torch_flags()
+        made_for = " ".join(compile_flags + link_flags)
+        if not force and not _module_stale(made_for):
+            return None, link_flags, made_for
+        return _compile_module(compile_flags), link_flags, made_for
+
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(module_object)
+        if force or _library_stale():
+            _build_library()
+    obj, link_flags, made_for = module.result()
+    if obj is not None:
+        _link([shutil.which("g++") or "c++", "-shared", obj, "-L" + os.path.dirname(LIB), "-lrope_chain", *link_flags],
+              MODULE)
+        with open(MODULE_STAMP, "w") as f:
+            f.write(made_for)
     if verbose:
         print(open(os.path.join(BUILD, "ptxas.log")).read())
     return LIB
