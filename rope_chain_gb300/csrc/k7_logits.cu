@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPad = 32;                     // tokens kept before a tile (rows may start unaligned)
-constexpr int kNodes = 256;                  // drafted tokens a tile lists
+constexpr int kNodes = 64;                   // nodes of a tree whose drafted tokens a tile lists
 constexpr uint32_t kPrompt = 1u << 31;       // count word: in the prompt
 constexpr uint32_t kDraft = 1u << 30;        //   drafted in the tree: the count differs by row
 constexpr uint32_t kBias = 1u << 29;         //   has a bias
@@ -187,8 +187,8 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
         s.word[i] = 0u;
         s.bias[i] = 0u;
     }
-    for (int i = threadIdx.x; i < kNodes; i += kThreads)
-        s.set[i] = 0u;
+    if (threadIdx.x < kNodes)
+        s.set[threadIdx.x] = 0u;
     if (threadIdx.x == 0)
         s.nodes = 0;
     __syncthreads();
@@ -315,7 +315,7 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
             if (at < (uint32_t)(kTile + kPad)) {
                 atomicOr(&s.word[at], kDraft);
                 const int k = atomicAdd(&s.nodes, 1);
-                if (k < kNodes && r - r0 < 64) {
+                if (k < kNodes && r - r0 < kNodes) {
                     s.node[k] = (int16_t)(r - r0);
                     s.token[k] = (int16_t)at;
                     s.listed[at] = (uint16_t)k;          // any one of a token's entries
@@ -326,11 +326,10 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     if (bad)
         atomicAdd(a.err, bad);
     __syncthreads();
-    // Trees of more than 64 nodes, or that draft more of the tile than is
-    // listed, are walked node by node for each of their tokens.
-    const int nodes = s.nodes;
-    const bool few = r1 - r0 <= 64 && nodes <= kNodes;
-    if (few && threadIdx.x < nodes)
+    // Trees of more nodes than are listed are walked node by node for each of their
+    // tokens.
+    const bool few = r1 - r0 <= kNodes;
+    if (few && (int)threadIdx.x < s.nodes)
         atomicOr(reinterpret_cast<unsigned long long *>(&s.set[s.listed[s.token[threadIdx.x]]]),
                  1ull << s.node[threadIdx.x]);
     {

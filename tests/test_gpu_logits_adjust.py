@@ -215,3 +215,11 @@ def test_infinite_penalties_touch_what_was_generated_only(dtype):
         got = rc.logits_adjust(logits, start, **kw, **{name: torch.full((2,), float("inf"), device=DEV)}).double().cpu().numpy()
         assert np.isneginf(got[made]).all(), name
         assert np.array_equal(got[~made], plain.double().cpu().numpy()[~made]), name
+
+
+@pytest.mark.parametrize("n", [63, 64, 65])
+@pytest.mark.parametrize("V,skew", [(40, 1), (40, 30), (9000, 1)])
+def test_trees_as_large_as_the_listed_ones(n, V, skew):
+    """64 nodes is the largest tree whose tokens are listed; one more is walked node by node."""
+    logits, start, kw, sees = make(n, [n, 2, n], V, 30, skew=skew)
+    check(logits, start, kw, sees, rc.logits_adjust(logits, start, **kw))
