@@ -676,8 +676,8 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
  *                i*q_row_stride + 64*h + e (e.g. the Q columns of
  *                rc_qkv_front's output), 16-byte aligned, q_row_stride a
  *                multiple of 8
- *   rows         0 <= rows, rows*num_heads < 2^31 (0: nothing launched, q and out
- *                may be NULL)
+ *   rows         0 <= rows, rows*num_heads < 2^31 - 256 (0: nothing launched, q and
+ *                out may be NULL)
  *   num_heads    a multiple of num_kv_heads; num_kv_heads >= 1
  *   row_start    device int32 [seqs + 1], non-decreasing, within [0, rows]
  *                (values outside are clamped); rows of no sequence are left

@@ -72,6 +72,9 @@ int size_of(int32_t dtype) { return dtype == RC_F32 ? 4 : 2; }
 // Strides are kept below 2^40 elements and counts below 2^31, so that byte
 // spans stay far from overflowing.
 constexpr int64_t kMaxStride = 1LL << 40;
+// Rows times heads of an attention: a row's index is 32 bits, that of the last
+// row tile's end (up to 256 rows) included.
+constexpr int64_t kMaxAttentionRows = 0x7FFFFFFFLL - 256;
 
 }  // namespace
 
@@ -228,7 +231,7 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
                                         int32_t num_kv_heads)
 {
     if (rows < 1 || seqs < 1 || num_kv_heads < 1 || num_heads < num_kv_heads ||
-        num_heads % num_kv_heads != 0 || rows > 0x7FFFFFFFLL / num_heads)
+        num_heads % num_kv_heads != 0 || rows > kMaxAttentionRows / num_heads)
         return 0;
     const int sms = num_sms_current();
     return sms > 0 ? rc::tree_attention_workspace(rows, seqs, num_heads / num_kv_heads, sms) : 0;
@@ -247,8 +250,8 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
     if (num_kv_heads < 1 || num_heads < num_kv_heads || num_heads % num_kv_heads != 0)
         return fail(RC_ERR_INVALID_ARG, "%s: num_heads=%d is not a positive multiple of num_kv_heads=%d",
                     fn, num_heads, num_kv_heads);
-    if (rows < 0 || rows > 0x7FFFFFFFLL / num_heads)
-        return fail(RC_ERR_INVALID_ARG, "%s: need rows >= 0 and rows*num_heads < 2^31", fn);
+    if (rows < 0 || rows > kMaxAttentionRows / num_heads)
+        return fail(RC_ERR_INVALID_ARG, "%s: need rows >= 0 and rows*num_heads < 2^31 - 256", fn);
     if (seqs < 1 || seqs >= (1 << 24))
         return fail(RC_ERR_INVALID_ARG, "%s: seqs=%d outside [1, 2^24)", fn, seqs);
     if (num_blocks < 1 || block_size < 1 || (int64_t)num_blocks * block_size >= (1LL << 31))

@@ -171,3 +171,13 @@ def test_outputs_over_what_is_still_read(lib):
                        dict(bias_start=0x1000, bias_tokens=0x2000, bias_values=at, bias_size=2)):
             assert adjust(lib, params=params) == bad, params
     assert adjust(lib, params=dict(allowed=OUT - 48, allowed_stride=4)) == bad
+
+
+def test_rows_whose_last_tile_ends_past_32_bits(lib):
+    """2^31 - 1 rows of a KV head: the last tile of 16 to 256 rows would end past 2^31."""
+    rows = (1 << 31) - 1
+    far = 1 << 60
+    for n in (rows, rows - 15, rows - 255):
+        assert attend(lib, rows=n, heads=1, kv=1, seqs=1, qs=0, os=64, out=far, tm=None) == rc.RC_ERR_INVALID_ARG, n
+        assert lib.rc_last_error().decode().find("2^31") > 0
+        assert lib.rc_tree_attention_workspace_size(n, 1, 1, 1) == 0
