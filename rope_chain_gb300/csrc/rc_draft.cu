@@ -273,6 +273,8 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
     if (tree_mask && (!aligned(tree_mask, 8) || mask_words < 1))
         return fail(RC_ERR_INVALID_ARG, "%s: tree_mask must be 8-byte aligned with mask_words >= 1", fn);
     const int64_t width = 64LL * num_heads;
+    if (rows <= 1)                      // the stride of an axis of length one is never used
+        q_row_stride = out_row_stride = 0;
     if (q_row_stride % 8 != 0 || out_row_stride % 8 != 0 || q_row_stride < 0 || q_row_stride > kMaxStride ||
         out_row_stride > kMaxStride || (rows > 1 && out_row_stride < width) || out_row_stride < 0)
         return fail(RC_ERR_INVALID_ARG, "%s: row strides must be non-negative multiples of 8, and out's "

@@ -181,3 +181,9 @@ def test_rows_whose_last_tile_ends_past_32_bits(lib):
         assert attend(lib, rows=n, heads=1, kv=1, seqs=1, qs=0, os=64, out=far, tm=None) == rc.RC_ERR_INVALID_ARG, n
         assert lib.rc_last_error().decode().find("2^31") > 0
         assert lib.rc_tree_attention_workspace_size(n, 1, 1, 1) == 0
+
+
+def test_the_stride_of_one_row_is_not_looked_at(lib):
+    for over in (dict(qs=516), dict(qs=-512), dict(os=448), dict(os=516)):
+        assert attend(lib, rows=0, **over) == rc.RC_OK, over
+        assert attend(lib, rows=2, **over) == rc.RC_ERR_INVALID_ARG, over

@@ -415,3 +415,13 @@ def test_workspace_over_another_operand_is_refused():
         rc.tree_attention(case.q, case.row_start, ws[64:64 + 8].view(torch.int32), case.table, case.cache, **lists)
     with pytest.raises(rc.RopeChainError, match="workspace"):
         rc.tree_attention(case.q, case.row_start, case.context, case.table, case.cache, err=ws[:4].view(torch.int32), **lists)
+
+
+def test_one_row_of_any_stride():
+    case = Case(29, [1], [700], 2, 4, 16)
+    out, lse, _ = case.run()
+    q = torch.empty(3, 517, dtype=torch.bfloat16, device=DEV)[:1, :512].as_strided((1, 8, 64), (517, 64, 1)).copy_(case.q)
+    into = torch.empty(3, 517, dtype=torch.bfloat16, device=DEV).as_strided((1, 8, 64), (517, 64, 1))
+    case.q = q
+    again, _, _ = case.run(out=into)
+    assert torch.equal(again, out)
