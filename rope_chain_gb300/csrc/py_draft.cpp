@@ -52,6 +52,13 @@ double number(PyObject *o) {
     return v;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();
+    return v != 0;
+}
+
 template <typename T> T narrow(int64_t v, const char *name) {
     TORCH_CHECK_VALUE(v >= std::numeric_limits<T>::min() && v <= std::numeric_limits<T>::max(), name, " = ", v,
                       " is out of range");
@@ -188,6 +195,7 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     no_gradient(table, "cos_sin");
     const int32_t type = dtype_of(x, "x");
     TORCH_CHECK_TYPE(args[1] != Py_None, "positions must be a tensor");
+    const bool inverse = truth(args[4]);
     const int64_t *positions = array<int64_t>(args[1], x.device(), at::kLong, x.size(0), "positions");
     int32_t *err = counter(args[6], x.device());
     Tensor out = output(args[5], x, "x");
@@ -196,9 +204,9 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     made(out, x);
     const rc_status s = rc_rope_apply(
         x.const_data_ptr(), type, x.stride(0), x.stride(1), x.size(0), narrow<int32_t>(x.size(1), "heads"),
-        narrow<int32_t>(x.size(2), "head_dim"), positions, table.const_data_ptr(), dtype_of(table, "cos_sin"), table.size(0), narrow<int32_t>(table.size(1), "rot_dim"),
-        narrow<int32_t>(integer(args[3]), "layout"), PyObject_IsTrue(args[4]), out.data_ptr(), out.stride(0),
-        out.stride(1), err, on.stream());
+        narrow<int32_t>(x.size(2), "head_dim"), positions, table.const_data_ptr(), dtype_of(table, "cos_sin"),
+        table.size(0), narrow<int32_t>(table.size(1), "rot_dim"), narrow<int32_t>(integer(args[3]), "layout"),
+        inverse, out.data_ptr(), out.stride(0), out.stride(1), err, on.stream());
     return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }

@@ -80,3 +80,12 @@ def test_gradients_are_not_dropped_silently(call, name):
     args[name] = fake(*args[name].shape, dtype=args[name].dtype, requires_grad=True)
     with pytest.raises(ValueError, match=f"{name} requires a gradient"):
         getattr(rc, call)(**args)
+
+
+def test_an_inverse_without_a_truth_value_is_refused():
+    class Neither:
+        def __bool__(self):
+            raise ArithmeticError("neither")
+    args = rope_operands()
+    with pytest.raises(ArithmeticError, match="neither"):
+        rc.rope_apply(**args, inverse=Neither())
