@@ -986,17 +986,20 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tensormap(&map);
     }
+    pdl_wait();
+    // TMEM only now: two CTAs (kQ = 1) fit on an SM, and one that held its columns
+    // while it waited for the previous kernel could keep them from a CTA of that
+    // kernel which has still to allocate.  (The lengths are read meanwhile.)
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols<kQ>) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    Place at = locate<kRows, kThreads, true>(a, blockIdx.x, gridDim.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
-    pdl_wait();
-    Place at = locate<kRows, kThreads, true>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
     Walk<kRows> walk(at);
