@@ -204,3 +204,30 @@ def test_autograd_takes_the_transposed_rotation(layout, inverse, side):
     with torch.no_grad():
         assert torch.equal(x.grad, rc.rope_apply(torch.ones_like(w), pos, cs, layout=layout, inverse=not inverse))
     assert not rc.rope_apply(x.detach(), pos, cs, layout=layout).requires_grad
+
+
+# much work: several heads a thread, from 2 * 1024 units an SM on in halves and 4 * 1024 in pairs (heads that are no
+# multiple of either, a copied tail, rows of a wider tensor)
+@pytest.mark.parametrize("T,heads,dim,rot,row", [(11201, 7, 64, 64, 7 * 64), (9001, 9, 128, 64, 9 * 128 + 64), (3001, 30, 96, 96, 30 * 96),
+                                                 (9999, 5, 256, 64, 6 * 256)])
+@pytest.mark.parametrize("layout", [rc.RC_ROPE_PAIRS, rc.RC_ROPE_HALVES])
+@pytest.mark.parametrize("xt,tt", [(BF, BF), (BF, F32), (F32, F32)])
+def test_apply_much_work(T, heads, dim, rot, row, layout, xt, tt):
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    whole = torch.randn(T, row, generator=gen, device=DEV).to(xt)
+    x = whole.as_strided((T, heads, dim), (row, dim, 1))
+    cs, pos = rc.rope_table(700, rot, dtype=tt, device=DEV), torch.randint(0, 700, (T,), generator=gen, device=DEV)
+    pos[5] = -1
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for inverse in (False, True):
+        ref, tol = rotate(x, cs, pos.clamp(min=0), layout, inverse)
+        ref[5], tol[5] = x[5].double(), 0
+        got = rc.rope_apply(x, pos, cs, layout=layout, inverse=inverse, err=err)
+        turned = torch.empty(heads, T, dim, dtype=xt, device=DEV).transpose(0, 1)      # heads outermost
+        rc.rope_apply(x, pos, cs, layout=layout, inverse=inverse, out=turned)
+        assert torch.equal(got, turned) and bool(((got.double() - ref).abs() <= tol).all())
+        assert torch.equal(got[..., rot:], x[..., rot:])
+    assert int(err.item()) == 2
+    before = whole.clone()
+    rc.rope_apply(x, pos, cs, layout=layout, inverse=True, out=x)
+    assert torch.equal(x, got) and torch.equal(whole[:, heads * dim:], before[:, heads * dim:])

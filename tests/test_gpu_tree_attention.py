@@ -425,3 +425,75 @@ def test_one_row_of_any_stride():
     case.q = q
     again, _, _ = case.run(out=into)
     assert torch.equal(again, out)
+
+
+# one batch for each kernel: up to 16 rows a unit, 32, 128, more
+KERNELS = [([1, 2], 8), ([4, 3], 8), ([13, 12], 8), ([40, 33], 8)]
+
+
+@pytest.mark.parametrize("bs", [8, 24, 40, 48, 136])
+@pytest.mark.parametrize("counts,G", KERNELS[2:])
+@pytest.mark.parametrize("ws", [True, False])
+def test_blocks_that_end_inside_a_tile(bs, counts, G, ws):
+    """Boxes of 8 and 16 keys, blocks that are no power of two, some of them out of range."""
+    case = Case(bs, counts, [1000, 391], 2, G, bs)
+    out, lse, err = case.run(ws)
+    assert err == 0
+    check(case, out, lse)
+    gone = [2, 200 // bs]                                       # of the first sequence: that block, of the second: another
+    case.table[0, gone[0]] = -7
+    case.table[1, gone[1]] = case.cache.shape[0]
+    out, lse, err = case.run(ws)
+    assert err == 2
+    for b, page in enumerate(gone):
+        keep = torch.ones(case.kv[b].shape[0], dtype=torch.bool, device=DEV)
+        keep[page * bs:(page + 1) * bs] = False
+        case.kv[b] = case.kv[b][keep]
+        case.ctx[b] -= bs
+    check(case, out, lse)
+
+
+@pytest.mark.parametrize("bs", [16, 24, 1])
+@pytest.mark.parametrize("counts,G", KERNELS)
+@pytest.mark.parametrize("ws", [True, False])
+@pytest.mark.parametrize("width", [0, 7, 300])
+def test_table_that_ends_inside_the_context(bs, counts, G, ws, width):
+    """Keys past the table's end are not seen, context or drafted, and each such sequence counts once."""
+    case = Case(width + bs, counts, [2500, 90], 2, G, bs)
+    width = min(width, case.table.shape[1] - 1)
+    case.table = case.table[:, :width]
+    out, lse, err = case.run(ws)
+    lost = 0
+    for b in range(2):
+        room, ctx, n = width * bs, case.ctx[b], counts[b]
+        lost += ctx + n > room
+        kept = min(room, ctx + n)
+        case.ctx[b] = min(ctx, room)
+        case.sees[b][:, max(0, kept - ctx):] = False
+        case.kv[b] = torch.cat([case.kv[b][:kept], torch.zeros(case.ctx[b] + n - kept, 2, 128, dtype=torch.bfloat16, device=DEV)])
+    assert err == lost >= 1
+    check(case, out, lse)
+
+
+@pytest.mark.parametrize("counts,G", KERNELS)
+def test_scores_in_the_thousands(counts, G):
+    """As test_large_scores_and_scale, for each kernel, and with keys that raise the maximum by hundreds again and again."""
+    case = Case(9, counts, [900, 64], 2, G, 16, sigma=6.0)
+    for b in range(2):
+        grow = torch.linspace(0.1, 3.0, case.kv[b].shape[0], device=DEV)[:, None, None]
+        case.kv[b][..., :64] = (case.kv[b][..., :64].float() * grow).to(torch.bfloat16)
+        p = torch.arange(case.kv[b].shape[0], device=DEV)
+        case.cache[case.table[b].long()[p // 16], :, p % 16] = case.kv[b]
+    out, lse, _ = case.run(scale=1.0)
+    ref, rlse, tol, ltol = case.ref(1.0)
+    assert bool(((lse.double() - rlse).abs() <= ltol).all())
+    assert bool(((out.double() - ref).abs() <= tol + 4 * ltol.amax() * 36).all())
+
+
+@pytest.mark.parametrize("ws", [True, False])
+def test_single_tokens_beside_a_wide_tree(ws):
+    """63 single tokens and a tree of 64: the mean says 16 rows a unit, the tree has 512."""
+    case = Case(41, [1] * 40 + [64] + [1] * 23, [10 + 53 * i for i in range(64)], 2, 8, 16)
+    out, lse, err = case.run(ws)
+    assert err == 0
+    check(case, out, lse)
