@@ -51,26 +51,26 @@ CALL_SOURCES = {
 NCU_TRAFFIC = {
     # rc_kv_project_store at workload 5 over all rows (the breakdown's call,
     # the one the roofline times): one k2_project_pair_persistent launch
-    # (dynamic tile order), 4,861,931,520 B read + 527,136,512 B written
+    # (dynamic tile order), 4,638,700,544 B read + 526,106,368 B written
     # (profiles/k2_pair_persistent_workload5.md)
-    (5, "store", "project_store"): (5_389_068_032, "8bb10d3211a5d91f",
+    (5, "store", "project_store"): (5_164_806_912, "c9b6c5b63943c528",
                                     "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, "
                                     "one launch at full size (one pass)"),
     # rc_context_norms at workload 5: one k1_context_norms2 launch,
-    # 537,302,016 B read + 4,233,134,336 B written
-    (5, "unfused", "norms"): (4_770_436_352, "2655d675e990d059",
+    # 537,376,256 B read + 4,230,468,352 B written
+    (5, "unfused", "norms"): (4_767_844_608, "403d2ebda9fd3f31",
                               "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, "
                               "one launch at full size (one pass)"),
     # rc_kv_store at workload 5: one k3_kv_store_heads launch (8 layers),
-    # 574,425,600 B read + 482,196,992 B written
-    (5, "unfused", "store"): (1_056_622_592, "b4f44c2c856746c9",
+    # 574,445,824 B read + 479,392,256 B written
+    (5, "unfused", "store"): (1_053_838_080, "8f296a58154fd27c",
                               "ncu --metrics dram__bytes_read.sum,dram__bytes_write.sum, "
                               "one launch at full size (one pass)"),
-    # rc_kv_project_store at workload 2: k2_project_pair (52,795,648 B read,
-    # 19,434,752 B written) then k3_reduce_store (82,688 B read, 1,630,976 B
+    # rc_kv_project_store at workload 2: k2_project_pair (54,690,816 B read,
+    # 33,224,192 B written) then k3_reduce_store (82,944 B read, 2,258,944 B
     # written), captured in sequence without ncu's cache flush between them
     # (the split-K partials are read back from L2, as in the step)
-    (2, "store", "project_store"): (73_944_064, "8bb10d3211a5d91f",
+    (2, "store", "project_store"): (90_256_896, "c9b6c5b63943c528",
                                     "ncu --cache-control none --metrics dram__bytes_read.sum,"
                                     "dram__bytes_write.sum, the call's two launches in sequence"),
 }

@@ -22,7 +22,7 @@
 // trees of 12 over 136 keys: 15.6 us, in equal ranges 34.6).  A unit that is cut
 // leaves FP32 partials (output, m, sum) in the workspace, which a second kernel
 // joins in key order (no atomics: the result does not depend on timing).
-#include "rc_internal.cuh"
+#include "rc_draft.cuh"
 #include "rc_tcgen05.cuh"
 
 #include <algorithm>

@@ -8,7 +8,7 @@
 //
 // Both kernels are bound by memory: one read and one write of every element
 // (the table rows, shared by a token's heads, come from L1 and L2).
-#include "rc_internal.cuh"
+#include "rc_draft.cuh"
 
 #include <algorithm>
 #include <cmath>

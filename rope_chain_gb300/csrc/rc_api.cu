@@ -3,6 +3,7 @@
 // allocates device memory or synchronises, except rc_read_device_faults.
 #include "rope_chain.h"
 #include "rc_internal.cuh"
+#include "rc_draft.cuh"
 
 #include <algorithm>
 #include <numeric>

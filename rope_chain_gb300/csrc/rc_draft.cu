@@ -3,7 +3,7 @@
 // Arguments are checked on the host, then the kernels go on the caller's
 // stream; nothing here allocates device memory or synchronises.
 #include "rope_chain.h"
-#include "rc_internal.cuh"
+#include "rc_draft.cuh"
 
 #include <algorithm>
 #include <cmath>

@@ -156,3 +156,15 @@ def test_traffic_figures_expire_with_their_sources(tmp_path, monkeypatch):
         else:
             assert nbytes == bench.NCU_TRAFFIC[k][0]
     assert bench.ncu_traffic((9, "store", "project_store"))[0] is None
+
+
+def test_traffic_figures_do_not_expire_with_other_operators():
+    """The digest's sources are the chain's and the front's alone: what the drafted tokens' operators declare has a
+    header of its own, so that a change of theirs does not void a traffic figure of the chain."""
+    import os
+    src = os.path.join(bench.ROOT, "rope_chain_gb300", "csrc")
+    for name in {n for names in bench.CALL_SOURCES.values() for n in names}:
+        text = open(os.path.join(src, name)).read()
+        for other in ("RopeLaunch", "LogitsLaunch", "TreeAttentionLaunch"):
+            assert other not in text, (name, other)
+    assert any(bench.ncu_traffic(k)[0] is not None for k in bench.NCU_TRAFFIC)
