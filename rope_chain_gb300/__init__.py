@@ -840,12 +840,12 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
     ``inverse``: the transposed rotation (the gradient with respect to x, given
     that of the output; autograd takes it where x requires one, without
     ``out``).  ``out`` may be x (in place)."""
-    if torch.is_grad_enabled() and isinstance(x, torch.Tensor) and x.requires_grad and out is None \
-            and not cos_sin.requires_grad:
+    y = (_draft_module or _draft()).rope_apply(x, positions, cos_sin, layout, inverse, out, err,
+                                               None if stream is None else stream.cuda_stream)
+    if y is None:                        # x requires a gradient
         with torch.cuda.stream(stream):
-            return _Turned.apply(x, positions, cos_sin, layout, inverse, err)
-    return (_draft_module or _draft()).rope_apply(x, positions, cos_sin, layout, inverse, out, err,
-                                                  None if stream is None else stream.cuda_stream)
+            y = _Turned.apply(x, positions, cos_sin, layout, inverse, err)
+    return y
 
 
 def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
