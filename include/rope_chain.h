@@ -602,8 +602,9 @@ typedef struct {
  *   lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), rot_dim - 1),
  *   ramp_j = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
  *   inv_j * (1 - ramp_j) + inv_j / factor * ramp_j.
- * Angles are reduced exactly (64-bit turns), so the values hold at any
- * position to FP32 accuracy before their one rounding to `dtype`.
+ * Angles are reduced in 64-bit turns, so the values hold alike at any position:
+ * before their rounding to `dtype` they are within 2^-21 (RC_F32) or 2^-20
+ * (RC_BF16) of the formula's, times attention_factor.
  *
  *   out          [max_position, rot_dim] of `dtype` (rc_dtype), contiguous,
  *                16-byte aligned

@@ -781,11 +781,13 @@ k5_small(const __grid_constant__ Args a)
 // cycle), the products as many at full rate; products of 64 columns (O) run at
 // about half of it, 1536 in all.
 // Measured: 8 trees of 64 tokens over 32768 keys (64 query and 8 KV heads, 273
-// GFLOP) 292 us, 0.93 PFLOP/s, 2700 cycles per 256 x 128 (in blocks of 16 keys;
-// 273 us in blocks of 128): the steps of the two row tiles, products, softmax and
-// weights, one after the other; tensor pipe 42 %, issue slots 60 %.  16 trees of 16
-// over 8192 keys (273 MB) 71 us, 3.8 TB/s: 44 us at 6.2 TB/s between a start of
-// 9 us (launch, lengths, Q, first tile) and changes of unit and the join of 18.
+// GFLOP) 290 to 307 us by the box, 0.89 to 0.94 PFLOP/s, 2700 cycles per 256 x 128
+// (in blocks of 16 keys; 273 us in blocks of 128): the steps of the two row tiles,
+// products, softmax and weights, one after the other; tensor pipe 42 %, issue slots
+// 60 %.  16 trees of 16 over 8192 keys (273 MB) 71 us, 3.8 TB/s: 44 us at 6.2 TB/s
+// between a start of 9 us (launch, lengths, Q, first tile) and changes of unit and
+// the join of 18.  Two CTAs an SM leave kQ = 1 96 registers a thread, of which it
+// spills 51 (204 bytes stored, 572 loaded); kQ = 2 spills three.
 // Key tiles that hold drafted keys, or the end, take a masked path; there the
 // V rows past the end are zeroed and what is infinite or NaN in a drafted one
 // is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
@@ -1498,6 +1500,8 @@ k5_join(const __grid_constant__ Args a)
 //   up to 32        k5_small<2>: 26.5 at 32, k5_wide<1> 29.6; at 40 31.3 and 29.5
 //   up to 128       k5_wide<1>: 32.5 at 128, k5_wide<2> 38.5; at 160 44.1 and 40.1
 //   beyond          k5_wide<2>: two row tiles share each key tile
+// Batches that mix them: 63 single tokens and a tree of 64 over 2000 keys 57 us (64
+// single tokens 51, the tree alone 25).
 // The wide kernel's TMA boxes need blocks of a multiple of 8 keys; other block
 // sizes stay with k5_small<2>.
 enum Variant { kSmall16, kSmall32, kWide128, kWide256 };

@@ -109,7 +109,8 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
 // out: 32768 x 16 heads of 128, halves, forward and transposed, 105 us without
 // the hints, 93 with them, 88 with five blocks on an SM instead of four (6.1 TB/s;
 // the pairs' four loads per thread want the registers of four: 17.2 us for
-// 32768 x 16 heads of 64, with five 18.3).  kVec is 16 bytes' worth where every pointer,
+// 32768 x 16 heads of 64, with five 18.3; FP32, 32768 x 16 heads of 128: 76.5 us a
+// direction in either layout, 7.0 TB/s).  kVec is 16 bytes' worth where every pointer,
 // stride, width and rot_dim allows it, else one pair, element by element (a
 // copied tail of odd width in the pairs layout is refused on the host).
 template <typename T, typename C, bool kHalves, bool kInverse, int kVec, int kHeads>
@@ -228,7 +229,9 @@ cudaError_t launch_types(const RopeLaunch &a, bool halves, bool inverse, bool wi
 // fixed-point fraction and p times it modulo 2^64 is exact integer
 // arithmetic: its top 32 bits give the angle to 2^-32 turns at any position
 // (the fraction's own rounding, 2^-65 turns times p < 2^31, stays below
-// that), with no FP64 arithmetic on the GPU.
+// that), with no FP64 arithmetic on the GPU.  As an FP32 number the angle is off
+// by up to 2^-26 turns, 1.6 * 2^-24 of cos and sin: absolute, so near a zero of
+// theirs the relative error is larger.
 struct TableArgs {
     void *out;
     int64_t positions;
@@ -242,7 +245,8 @@ __device__ __forceinline__ void cos_sin_at(uint64_t step, uint64_t p, float &c, 
     sincospif(__fmul_rn((float)(int32_t)((p * step) >> 32), 0x1p-31f), &s, &c);     // of half turns
 }
 
-// FP32 tables: every entry from its own angle.
+// FP32 tables: every entry from its own angle (131072 positions of 64 columns, 34
+// MB: 10.9 us, 3.1 TB/s, bound by that arithmetic), within 2^-21 times the gain.
 template <int kVec>
 __global__ void __launch_bounds__(kThreads)
 k6_rope_table_f32(const __grid_constant__ TableArgs a)
@@ -272,8 +276,9 @@ k6_rope_table_f32(const __grid_constant__ TableArgs a)
 // bf16 tables: a sine and cosine of its own take a thread some 40 instructions,
 // four times what the stores allow, so a thread makes them for one of kStep
 // positions and turns that one by the block's table of the first kStep - 1
-// steps (cos(x + y) = cos x cos y - sin x sin y): two more FP32 roundings,
-// 2^-22 at most, against bf16's 2^-8.  131072 positions of 64 columns (17 MB):
+// steps (cos(x + y) = cos x cos y - sin x sin y): each entry has two angles' errors
+// and two more FP32 roundings, within 2^-20 times the gain together, against
+// bf16's 2^-8 of the entry.  131072 positions of 64 columns (17 MB):
 // 5.0 us, 3.3 TB/s with the launch, every entry from its own angle 7.4.
 constexpr int kStep = 4;
 template <int kVec>

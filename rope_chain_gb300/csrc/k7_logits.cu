@@ -18,11 +18,13 @@
 // where the lanes take the listed ones 32 at a time.  (Lanes that walked what
 // was listed in their own 16 bytes were bound by instructions, as long as the
 // fullest of 32: 16 x 64 rows of 131072, history 4096, 221 us FP32 and 178 bf16;
-// now 193, 5.6 TB/s, bound by memory, and 125, 4.4 TB/s.)  The nodes that draft
+// now 192 to 195, 5.6 TB/s, bound by memory, and 125 to 128, 4.3 TB/s.)  The nodes that draft
 // a token of the tile are a 64-bit set, so that a row's count of it is a
-// population count.  Small calls are latency: one row of 32000 takes 3.9 us, 39
-// rows of 100003 bf16 with skewed histories of 9001 15.6 us, of which the tile
-// with the most frequent tokens makes 5 and the scan of the history 2.
+// population count.  Trees of more than 64 nodes are walked node by node instead,
+// for each listed token of each row: 4 x 64 rows of 131072 73 us, 4 x 65 1390.
+// Small calls are latency: one row of 32000 takes 4.0 us, 39 rows of 100003 bf16
+// with skewed histories of 9001 15.8 us, of which the tile with the most frequent
+// tokens makes 5 and the scan of the history 2.
 #include "rc_draft.cuh"
 
 #include <algorithm>
@@ -372,6 +374,9 @@ k7_logits(const __grid_constant__ LogitsLaunch a)
     }
     __syncwarp();
 
+    // The quotient as a product: at most 1.5 ulp, where the division has half a one.
+    // 16 x 64 rows of 131072: 193 us; with the product corrected by its remainder
+    // 203, with the division 210.
     const float less = __fdiv_rn(1.0f, rep);
     // The logit of a token whose word w is set, in row r, whose node sees `see`
     // (its first 64 nodes).

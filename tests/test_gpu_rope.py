@@ -231,3 +231,13 @@ def test_apply_much_work(T, heads, dim, rot, row, layout, xt, tt):
     before = whole.clone()
     rc.rope_apply(x, pos, cs, layout=layout, inverse=True, out=x)
     assert torch.equal(x, got) and torch.equal(whole[:, heads * dim:], before[:, heads * dim:])
+
+
+@pytest.mark.parametrize("dtype,bound", [(F32, 2.0 ** -21), (BF, 2.0 ** -20)])
+@pytest.mark.parametrize("n,rot,gain", [(1 << 20, 8, 1.0), (70001, 66, 1.25), (4099, 512, 0.5)])
+def test_table_within_the_stated_bounds(dtype, bound, n, rot, gain):
+    """Before its rounding an entry is within 2^-21 (FP32) or 2^-20 (bf16) of the formula's, times the gain."""
+    got = rc.rope_table(n, rot, theta=10000.0, attention_factor=gain, dtype=dtype, device=DEV).double().cpu().numpy()
+    a = angles(n, rot, 10000.0, "none", 1.0, 1.0)
+    ref = gain * np.concatenate([np.cos(a), np.sin(a)], 1)
+    assert (np.abs(got - ref) <= ROUND[dtype] * (np.abs(ref) + bound * gain) + bound * gain + n * 2.0 ** -50).all()
