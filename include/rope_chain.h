@@ -787,6 +787,76 @@ rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride
                            const rc_logits_params *params, void *out, int64_t out_row_stride,
                            int32_t *err, cudaStream_t stream);
 
+/*
+ * rc_head_norm_rope -- the RMS norm of each query and key head with its rotary
+ * position in one pass: for token t and head h, over its head_dim elements,
+ *   r = 1 / sqrt(mean(x^2) + eps),   y = rotated(x * r * w)
+ * with w = q_weight for the first q_heads heads and k_weight for the others
+ * (NULL: ones), and the rotation of rc_rope_apply at positions[t] in the first
+ * rot_dim elements.  All in FP32, rounded once to the type of x (the context
+ * chain and rc_qkv_front round the normed key to bf16 before they turn it; this
+ * call does not).  A token whose position lies outside [0, max_position) is
+ * normed but not turned, and adds one to *err.
+ *
+ *   x, out       as rc_rope_apply's (views of `dtype`; out may be x, in place)
+ *   T, heads     as rc_rope_apply's
+ *   head_dim     2 .. 512 (PAIRS: even)
+ *   params       HOST pointer:
+ *     q_heads    0 .. heads
+ *     q_weight, k_weight   `weight_dtype` [head_dim], aligned to their element,
+ *                or NULL
+ *     eps        >= 0, finite
+ *   positions ... layout, err    as rc_rope_apply's
+ * 16-byte aligned pointers, strides, head_dim and rot_dim (half of it in
+ * HALVES) move 16 bytes at a time; anything else element by element.
+ */
+typedef struct {
+    int32_t q_heads;
+    const void *q_weight, *k_weight;
+    int32_t weight_dtype;               /* rc_dtype; not read without weights */
+    float eps;
+} rc_head_norm_params;
+
+rc_status rc_head_norm_rope(const void *x, int32_t dtype, int64_t x_row_stride, int64_t x_head_stride,
+                            int64_t T, int32_t heads, int32_t head_dim, const rc_head_norm_params *params,
+                            const int64_t *positions, const void *cos_sin, int32_t table_dtype,
+                            int64_t max_position, int32_t rot_dim, int32_t layout, void *out,
+                            int64_t out_row_stride, int64_t out_head_stride, int32_t *err,
+                            cudaStream_t stream);
+
+/*
+ * rc_head_norm_rope_grad -- its gradients.  With g the transposed rotation of dy
+ * and n = x * r (r as above, made again from x):
+ *   dw = sum over tokens and the weight's heads of g * n          (FP32)
+ *   dx = r * (g * w - n * mean(g * w * n))                        (rounded once)
+ *
+ *   dy           as x, with strides of its own
+ *   x ... layout as rc_head_norm_rope's
+ *   dx           as out; may be dy or x with its strides (in place)
+ *   dq_weight, dk_weight   FP32 [head_dim], or NULL where not wanted; they are
+ *                overwritten (zeros where T is 0 or no head has that weight), and
+ *                a weight that is NULL has the gradient at ones
+ *   workspace    device scratch, 16-byte aligned, of
+ *                rc_head_norm_rope_grad_workspace_size() bytes where a weight's
+ *                gradient is wanted (else NULL).  Calls sharing one must not
+ *                overlap on the GPU; its contents need no set-up
+ * The sums over tokens are taken in an order that depends on the sizes alone: two
+ * calls give the same bits.
+ */
+rc_status rc_head_norm_rope_grad(const void *dy, int64_t dy_row_stride, int64_t dy_head_stride,
+                                 const void *x, int32_t dtype, int64_t x_row_stride,
+                                 int64_t x_head_stride, int64_t T, int32_t heads, int32_t head_dim,
+                                 const rc_head_norm_params *params, const int64_t *positions,
+                                 const void *cos_sin, int32_t table_dtype, int64_t max_position,
+                                 int32_t rot_dim, int32_t layout, void *dx, int64_t dx_row_stride,
+                                 int64_t dx_head_stride, float *dq_weight, float *dk_weight,
+                                 void *workspace, size_t workspace_bytes, int32_t *err,
+                                 cudaStream_t stream);
+
+/* Workspace bytes of rc_head_norm_rope_grad on the current device, for any number
+   of tokens and heads (0 for a head_dim that it refuses). */
+size_t rc_head_norm_rope_grad_workspace_size(int32_t head_dim);
+
 /* rc_device_address -- the address at which the current device reads p:
    p itself for device or managed memory; for page-locked host memory
    mapped into the device's address space (cudaHostAlloc, or

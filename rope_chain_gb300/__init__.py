@@ -145,6 +145,20 @@ class LogitsParams(ctypes.Structure):
                 ("bias_size", _c.c_int64), ("allowed", _vp), ("allowed_stride", _c.c_int64)]
 
 
+class HeadNormParams(ctypes.Structure):
+    """rc_head_norm_params: the weights (device pointers) and eps of head_norm_rope."""
+    _fields_ = [("q_heads", _c.c_int32), ("q_weight", _vp), ("k_weight", _vp), ("weight_dtype", _c.c_int32),
+                ("eps", _c.c_float)]
+
+
+SIGNATURES["rc_head_norm_rope"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32,
+                                    _c.POINTER(HeadNormParams), _vp, _vp, _c.c_int32, _c.c_int64, _c.c_int32,
+                                    _c.c_int32, _vp, _c.c_int64, _c.c_int64, _vp, _vp], _c.c_int)
+SIGNATURES["rc_head_norm_rope_grad"] = ([_vp, _c.c_int64, _c.c_int64, _vp, _c.c_int32, _c.c_int64, _c.c_int64,
+                                         _c.c_int64, _c.c_int32, _c.c_int32, _c.POINTER(HeadNormParams), _vp, _vp,
+                                         _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _vp, _c.c_int64, _c.c_int64,
+                                         _vp, _vp, _vp, _c.c_size_t, _vp, _vp], _c.c_int)
+SIGNATURES["rc_head_norm_rope_grad_workspace_size"] = ([_c.c_int32], _c.c_size_t)
 SIGNATURES["rc_rope_table"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_double,
                                 _c.POINTER(RopeScaling), _vp], _c.c_int)
 SIGNATURES["rc_rope_apply"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32,
@@ -846,6 +860,75 @@ def rope_apply(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, 
         with torch.cuda.stream(stream):
             y = _Turned.apply(x, positions, cos_sin, layout, inverse, err)
     return y
+
+
+class _NormTurned(torch.autograd.Function):
+    """head_norm_rope where x or a weight requires a gradient."""
+
+    @staticmethod
+    def forward(ctx, x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, err):
+        ctx.save_for_backward(x, positions, cos_sin, q_weight, k_weight)
+        ctx.how = eps, q_heads, layout
+        return _draft().head_norm_rope(x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, None, err, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        x, positions, cos_sin, q_weight, k_weight = ctx.saved_tensors
+        eps, q_heads, layout = ctx.how
+        if grad.stride(2) != 1:
+            grad = grad.contiguous()
+        wanted = ctx.needs_input_grad
+        dx, dq, dk = _draft().head_norm_rope_grad(grad, x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout,
+                                                  wanted[4] or wanted[5], None, None, None, None)
+        return (dx if wanted[0] else None, None, None, None, dq.to(q_weight.dtype) if wanted[4] else None,
+                dk.to(k_weight.dtype) if wanted[5] else None, None, None, None)
+
+
+def head_norm_rope(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *, eps: float,
+                   q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                   q_heads: Optional[int] = None, layout: int = RC_ROPE_PAIRS,
+                   out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The RMS norm of each query and key head and its rotary position in one pass
+    (rc_head_norm_rope): x bf16 or float32 [T, heads, head_dim], a view as
+    rope_apply takes it, e.g. the Q and K columns of a projection's rows.  The first
+    ``q_heads`` heads (None: all) take ``q_weight``, the others ``k_weight``
+    (bf16 or float32 [head_dim]; None: ones).  Rounded once; ``out`` may be x (in
+    place).  autograd takes the gradients where x or a weight requires one, without
+    ``out``."""
+    y = (_draft_module or _draft()).head_norm_rope(x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, out,
+                                                   err, None if stream is None else stream.cuda_stream)
+    if y is None:                        # something requires a gradient
+        with torch.cuda.stream(stream):
+            y = _NormTurned.apply(x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, err)
+    return y
+
+
+def head_norm_rope_grad(grad: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, *,
+                        eps: float, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, q_heads: Optional[int] = None,
+                        layout: int = RC_ROPE_PAIRS, weight_grads: bool = True,
+                        out: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of head_norm_rope (rc_head_norm_rope_grad), given that of its
+    output: (dx, dq_weight, dk_weight), the weights' in float32 (None for a weight
+    that is None, or without ``weight_grads``).  ``out`` (dx) may be ``grad`` or x
+    (in place); ``workspace``: head_norm_rope_grad_workspace() (None: made by the
+    call)."""
+    return (_draft_module or _draft()).head_norm_rope_grad(
+        grad, x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, weight_grads, out, err, workspace,
+        None if stream is None else stream.cuda_stream)
+
+
+def head_norm_rope_grad_workspace(head_dim: int, device) -> torch.Tensor:
+    """A workspace for head_norm_rope_grad (rc_head_norm_rope_grad_workspace_size
+    bytes on ``device``), for any number of tokens and heads."""
+    with torch.cuda.device(device):
+        n = int(lib().rc_head_norm_rope_grad_workspace_size(head_dim))
+    if n == 0:
+        raise RopeChainError(RC_ERR_UNSUPPORTED, "no workspace size for this head_dim")
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def tree_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,

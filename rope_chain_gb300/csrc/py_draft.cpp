@@ -1,6 +1,7 @@
 // Python side of the drafted tokens' calls (rc_rope_table, rc_rope_apply,
-// rc_tree_attention, rc_logits_adjust): checks torch tensors, makes the output
-// and calls the C ABI.  The other calls of the package go through ctypes, whose
+// rc_tree_attention, rc_logits_adjust) and of those around them
+// (rc_head_norm_rope, rc_head_norm_rope_grad): checks torch tensors, makes the
+// output and calls the C ABI.  The other calls of the package go through ctypes, whose
 // 6 to 12 us a call these cannot afford: their kernels take 2 to 20 us.
 // Arguments come by position (rope_chain_gb300/__init__.py has the signatures
 // and their documentation).
@@ -353,6 +354,143 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// What both directions of the head norm take beside x: positions, cos_sin, eps,
+// q_weight, k_weight, q_heads, layout (as args[0] to args[6]).
+struct NormOperands {
+    rc_head_norm_params params = {};
+    const int64_t *positions;
+    const Tensor *table;
+    int32_t layout;
+
+    NormOperands(const Tensor &x, PyObject *const *args) {
+        TORCH_CHECK_TYPE(args[0] != Py_None, "positions must be a tensor");
+        positions = array<int64_t>(args[0], x.device(), at::kLong, x.size(0), "positions");
+        table = &tensor(args[1], "cos_sin");
+        TORCH_CHECK_VALUE(table->dim() == 2 && table->is_cuda() && table->is_contiguous(),
+                          "cos_sin must be a contiguous CUDA tensor [max_position, rot_dim]");
+        beside(*table, x.device(), "cos_sin");
+        no_gradient(*table, "cos_sin");
+        params.eps = (float)number(args[2]);
+        params.q_heads = narrow<int32_t>(args[5] == Py_None ? x.size(1) : integer(args[5]), "q_heads");
+        params.weight_dtype = RC_BF16;
+        TORCH_CHECK_VALUE(args[5] != Py_None || args[4] == Py_None, "k_weight needs q_heads, the number of the query heads");
+        params.q_weight = weight(args[3], x, "q_weight");
+        params.k_weight = weight(args[4], x, "k_weight");
+        if (args[3] != Py_None && args[4] != Py_None)
+            TORCH_CHECK_TYPE(tensor(args[3], "q_weight").scalar_type() == tensor(args[4], "k_weight").scalar_type(),
+                             "q_weight and k_weight must have one dtype");
+        layout = narrow<int32_t>(integer(args[6]), "layout");
+    }
+
+private:
+    const void *weight(PyObject *o, const Tensor &x, const char *name) {
+        if (o == Py_None)
+            return nullptr;
+        const Tensor &w = tensor(o, name);
+        TORCH_CHECK_VALUE(w.dim() == 1 && w.size(0) == x.size(2) && w.is_cuda() && w.is_contiguous(), name,
+                          " must be a contiguous CUDA tensor [head_dim]");
+        params.weight_dtype = dtype_of(w, name);
+        beside(w, x.device(), name);
+        return w.const_data_ptr();
+    }
+};
+
+void heads_view(const Tensor &t, const char *name) {
+    TORCH_CHECK_TYPE(t.is_cuda(), name, " must be a CUDA tensor");
+    TORCH_CHECK_VALUE(t.dim() == 3 && (t.size(2) <= 1 || t.stride(2) == 1), name,
+                      " must be [T, heads, head_dim] with a contiguous last axis");
+}
+
+bool wants_gradient(PyObject *o) { return o != Py_None && THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad(); }
+
+PyObject *head_norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, out, err, stream
+    need(n, 11);
+    const Tensor &x = tensor(args[0], "x");
+    heads_view(x, "x");
+    const int32_t type = dtype_of(x, "x");
+    const NormOperands o(x, args + 1);
+    if (at::GradMode::is_enabled() && (x.requires_grad() || wants_gradient(args[4]) || wants_gradient(args[5]))) {
+        if (args[8] == Py_None)
+            Py_RETURN_NONE;              // to be recorded: the caller does
+        no_gradient(x, "x");
+        for (const int i : {4, 5})
+            if (args[i] != Py_None)
+                no_gradient(tensor(args[i], "weight"), i == 4 ? "q_weight" : "k_weight");
+    }
+    int32_t *err = counter(args[9], x.device());
+    Tensor out = output(args[8], x, "x");
+    TORCH_CHECK_VALUE(!out.defined() || out.size(2) <= 1 || out.stride(2) == 1, "the last axis of out must be contiguous");
+    const On on(x.device(), args[10]);
+    made(out, x);
+    const rc_status s = rc_head_norm_rope(
+        x.const_data_ptr(), type, x.stride(0), x.stride(1), x.size(0), narrow<int32_t>(x.size(1), "heads"),
+        narrow<int32_t>(x.size(2), "head_dim"), &o.params, o.positions, o.table->const_data_ptr(),
+        dtype_of(*o.table, "cos_sin"), o.table->size(0), narrow<int32_t>(o.table->size(1), "rot_dim"), o.layout,
+        out.data_ptr(), out.stride(0), out.stride(1), err, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *head_norm_rope_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // grad, x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout,
+    // weight_grads, out, err, workspace, stream
+    need(n, 14);
+    const Tensor &dy = tensor(args[0], "grad"), &x = tensor(args[1], "x");
+    heads_view(x, "x");
+    heads_view(dy, "grad");
+    TORCH_CHECK_VALUE(dy.sizes() == x.sizes() && dy.scalar_type() == x.scalar_type(),
+                      "grad must have the shape and dtype of x");
+    beside(dy, x.device(), "grad");
+    no_gradient(dy, "grad");
+    no_gradient(x, "x");
+    const int32_t type = dtype_of(x, "x");
+    const NormOperands o(x, args + 2);
+    for (const int i : {5, 6})
+        if (args[i] != Py_None)
+            no_gradient(tensor(args[i], "weight"), i == 5 ? "q_weight" : "k_weight");
+    int32_t *err = counter(args[11], x.device());
+    Tensor dx = output(args[10], x, "x");
+    TORCH_CHECK_VALUE(!dx.defined() || dx.size(2) <= 1 || dx.stride(2) == 1, "the last axis of out must be contiguous");
+    const int32_t dim = narrow<int32_t>(x.size(2), "head_dim");
+    const bool weights = truth(args[9]);
+    const bool q = weights && args[5] != Py_None, k = weights && args[6] != Py_None;
+    Tensor workspace;
+    if (args[12] != Py_None) {
+        workspace = tensor(args[12], "workspace");
+        TORCH_CHECK_VALUE(workspace.is_cuda() && workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+        beside(workspace, x.device(), "workspace");
+    }
+    const On on(x.device(), args[13]);
+    made(dx, x);
+    const auto floats = x.options().dtype(at::kFloat);
+    Tensor dq, dk;
+    if (q)
+        dq = at::empty({dim}, floats);
+    if (k)
+        dk = at::empty({dim}, floats);
+    if ((q || k) && !workspace.defined())
+        workspace = at::empty({(int64_t)rc_head_norm_rope_grad_workspace_size(dim)}, x.options().dtype(at::kByte));
+    const rc_status s = rc_head_norm_rope_grad(
+        dy.const_data_ptr(), dy.stride(0), dy.stride(1), x.const_data_ptr(), type, x.stride(0), x.stride(1), x.size(0),
+        narrow<int32_t>(x.size(1), "heads"), dim, &o.params, o.positions, o.table->const_data_ptr(),
+        dtype_of(*o.table, "cos_sin"), o.table->size(0), narrow<int32_t>(o.table->size(1), "rot_dim"), o.layout,
+        dx.data_ptr(), dx.stride(0), dx.stride(1), q ? dq.data_ptr<float>() : nullptr, k ? dk.data_ptr<float>() : nullptr,
+        workspace.defined() ? workspace.data_ptr() : nullptr, workspace.defined() ? workspace.nbytes() : 0, err, on.stream());
+    if (s != RC_OK)
+        return raise_status(s);
+    auto wrapped = [](bool is, Tensor &t) {
+        if (is)
+            return THPVariable_Wrap(t);
+        Py_INCREF(Py_None);
+        return Py_None;
+    };
+    return Py_BuildValue("NNN", THPVariable_Wrap(dx), wrapped(q, dq), wrapped(k, dk));
+    END_HANDLE_TH_ERRORS
+}
+
 // The exception class that an error status raises.
 PyObject *set_error(PyObject *, PyObject *cls) {
     Py_INCREF(cls);
@@ -365,6 +503,9 @@ PyMethodDef g_methods[] = {
     {"rope_apply", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(rope_apply)), METH_FASTCALL, nullptr},
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(tree_attention)), METH_FASTCALL, nullptr},
     {"logits_adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(logits_adjust)), METH_FASTCALL, nullptr},
+    {"head_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope)), METH_FASTCALL, nullptr},
+    {"head_norm_rope_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope_grad)), METH_FASTCALL,
+     nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

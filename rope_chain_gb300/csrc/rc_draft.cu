@@ -4,74 +4,15 @@
 // stream; nothing here allocates device memory or synchronises.
 #include "rope_chain.h"
 #include "rc_draft.cuh"
+#include "rc_checks.cuh"
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <initializer_list>
+
+using namespace rc;
 
 namespace {
 
-rc_status fail(rc_status s, const char *fmt, ...) {
-    char msg[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(msg, sizeof msg, fmt, ap);
-    va_end(ap);
-    rc::set_last_error(msg);
-    return s;
-}
-
-rc_status ok() {
-    rc::set_last_error("");
-    return RC_OK;
-}
-
-rc_status cuda_fail(cudaError_t e, const char *what) {
-    return fail(RC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-// Bytes that a call touches (none without an address).
-struct Span {
-    const void *p;
-    size_t n;
-};
-
-bool overlap(const Span &written, std::initializer_list<Span> others) {
-    for (const Span &o : others)
-        if (written.p && o.p && written.n > 0 && o.n > 0 && overlap(written.p, written.n, o.p, o.n))
-            return true;
-    return false;
-}
-
-int num_sms_current() {
-    static int cache[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return 0;
-    if (dev < 64 && cache[dev])
-        return cache[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    if (dev < 64)
-        cache[dev] = n;
-    return n;
-}
-
-int size_of(int32_t dtype) { return dtype == RC_F32 ? 4 : 2; }
-
-// Strides are kept below 2^40 elements and counts below 2^31, so that byte
-// spans stay far from overflowing.
-constexpr int64_t kMaxStride = 1LL << 40;
 // Rows times heads of an attention: a row's index is 32 bits, that of the last
 // row tile's end (up to 256 rows) included.
 constexpr int64_t kMaxAttentionRows = 0x7FFFFFFFLL - 256;
