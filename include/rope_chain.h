@@ -857,6 +857,89 @@ rc_status rc_head_norm_rope_grad(const void *dy, int64_t dy_row_stride, int64_t 
    of tokens and heads (0 for a head_dim that it refuses). */
 size_t rc_head_norm_rope_grad_workspace_size(int32_t head_dim);
 
+/*
+ * A paged cache in 4 bits: `cache4` bytes [num_blocks, num_kv_heads, block_size, 64],
+ * the K of a row in its first 32 bytes and the V in the others, element 2i in the
+ * low half of byte i and element 2i + 1 in the high half; `scales` bf16
+ * [num_blocks, num_kv_heads, block_size, 4], those of K's elements 0 to 31 and 32
+ * to 63, then of V's.  A half-byte c stands for (c - 8) * scale, which is a bf16
+ * number for the scales that rc_kv4_store writes (four significant bits); a scale
+ * that is not finite, or above 2^100 in size, counts as 0.  72 bytes a row, where
+ * the bf16 caches have 256.  A cache of zero bytes and scales holds zeros.
+ */
+
+/*
+ * rc_kv4_store -- inserts K and V rows into a cache in 4 bits, as rc_kv_store does
+ * into a bf16 cache: K comes normed and turned (rc_head_norm_rope, or
+ * rc_qkv_front's output rows).  For each row, head and group of 32 elements, with
+ * m the largest size of its elements:
+ *   scale = m / 7 rounded to four significant bits (nearest, ties to even),
+ *           0 where that is below 2^-100
+ *   c = 8 + x / scale rounded to the nearest whole number, ties toward zero
+ *       (8 where the scale is 0)
+ * A NaN counts as 0, and sizes above 7 * 2^100 (infinities too) as that; a row's
+ * head with an element that is not finite adds one to *err.
+ *
+ *   k, v         bf16 [T, num_kv_heads, 64]: element (t, h, e) at t*row_stride +
+ *                h*head_stride + e, 16-byte aligned, strides multiples of 8
+ *   slots        int64 [T], 8-byte aligned: block*block_size + offset of the row, or
+ *                negative: skipped.  A slot past the cache adds one to *err and is
+ *                skipped; rows of one call must not share a slot
+ *   cache4       16-byte aligned, scales 8-byte aligned; num_blocks*block_size < 2^31
+ *   err          optional device int32 counter
+ */
+rc_status rc_kv4_store(const uint16_t *k, int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v,
+                       int64_t v_row_stride, int64_t v_head_stride, int64_t T, int32_t num_kv_heads,
+                       const int64_t *slots, uint8_t *cache4, uint16_t *scales, int32_t num_blocks,
+                       int32_t block_size, int32_t *err, cudaStream_t stream);
+
+/*
+ * rc_kv4_load -- the rows at `slots` as what they stand for, K | V in bf16 (to go
+ * on in a bf16 cache, or to look at).
+ *
+ *   out          bf16 [T, num_kv_heads, 128] contiguous, 16-byte aligned; zeros for
+ *                a slot that is negative or past the cache (which adds one to *err)
+ *   slots ... err   as rc_kv4_store's
+ */
+rc_status rc_kv4_load(const int64_t *slots, int64_t T, int32_t num_kv_heads, const uint8_t *cache4,
+                      const uint16_t *scales, int32_t num_blocks, int32_t block_size, uint16_t *out,
+                      int32_t *err, cudaStream_t stream);
+
+/*
+ * rc_kv_compact -- after a tree of drafted tokens was verified: the accepted nodes'
+ * rows follow the context, in every cache of the list, in one launch.  For sequence
+ * b and k < path_len[b], as if every row were read before one is written:
+ *   row at logical key context_len[b] + k  <-  row at context_len[b] + path[b, k]
+ * with logical keys as rc_tree_attention has them (node j at context_len[b] + j, key
+ * p in block block_table[b, p / block_size]).
+ *
+ *   caches       HOST array of `count` device pointers (1 <= count <= 64): caches
+ *                [num_blocks, num_kv_heads, block_size] of rows of row_bytes[i]
+ *                bytes (HOST array, multiples of 8 up to 4096; 256 for a bf16 cache,
+ *                64 and 8 for one in 4 bits and its scales), 16-byte aligned (8-byte
+ *                where row_bytes[i] is no multiple of 16), none overlapping another
+ *   block_table, table_stride, table_width, context_len, row_start, seqs
+ *                as rc_tree_attention's (row_start gives a sequence's node count;
+ *                its values are clamped to [0, rows])
+ *   rows         the nodes of all sequences, 0 <= rows < 2^31
+ *   path         device int32 [seqs, path_stride]: nodes in increasing order
+ *   path_width   entries of a row of path that may be used, >= 0
+ *   path_len     device int32 [seqs] (clamped to [0, path_width])
+ *   new_len      optional device int32 [seqs]: context_len[b] + the rows that are in
+ *                place; it overlaps nothing that is read (context_len included)
+ *   err          optional device int32 counter
+ * A path ends before a node that is not in the tree or not past the one before it,
+ * and before a row whose block is outside [0, num_blocks) or past the table: that
+ * adds one to *err.  Blocks must not be shared by two sequences of the call at the
+ * keys that are written.
+ */
+rc_status rc_kv_compact(void *const *caches, const int32_t *row_bytes, int32_t count, int32_t num_blocks,
+                        int32_t num_kv_heads, int32_t block_size, const int32_t *block_table,
+                        int64_t table_stride, int32_t table_width, const int32_t *context_len,
+                        const int32_t *row_start, int32_t seqs, int64_t rows, const int32_t *path,
+                        int64_t path_stride, int32_t path_width, const int32_t *path_len, int32_t *new_len,
+                        int32_t *err, cudaStream_t stream);
+
 /* rc_device_address -- the address at which the current device reads p:
    p itself for device or managed memory; for page-locked host memory
    mapped into the device's address space (cudaHostAlloc, or

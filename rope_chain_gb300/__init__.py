@@ -159,6 +159,12 @@ SIGNATURES["rc_head_norm_rope_grad"] = ([_vp, _c.c_int64, _c.c_int64, _vp, _c.c_
                                          _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _vp, _c.c_int64, _c.c_int64,
                                          _vp, _vp, _vp, _c.c_size_t, _vp, _vp], _c.c_int)
 SIGNATURES["rc_head_norm_rope_grad_workspace_size"] = ([_c.c_int32], _c.c_size_t)
+SIGNATURES["rc_kv4_store"] = ([_vp, _c.c_int64, _c.c_int64, _vp, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _vp,
+                               _vp, _vp, _c.c_int32, _c.c_int32, _vp, _vp], _c.c_int)
+SIGNATURES["rc_kv4_load"] = ([_vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32, _c.c_int32, _vp, _vp, _vp], _c.c_int)
+SIGNATURES["rc_kv_compact"] = ([_c.POINTER(_vp), _c.POINTER(_c.c_int32), _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32,
+                                _vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32, _c.c_int64, _vp, _c.c_int64,
+                                _c.c_int32, _vp, _vp, _vp, _vp], _c.c_int)
 SIGNATURES["rc_rope_table"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_double,
                                 _c.POINTER(RopeScaling), _vp], _c.c_int)
 SIGNATURES["rc_rope_apply"] = ([_vp, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32,
@@ -990,3 +996,44 @@ def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
         logits, row_start, history, history_start, prompt_len, draft_tokens, tree_mask, repetition,
         frequency, presence, bias_start, bias_tokens, bias_values, allowed, out, err,
         None if stream is None else stream.cuda_stream)
+
+
+# --------------------------------------------- caches in 4 bits, accepted rows
+
+def new_kv4_cache(num_blocks: int, num_kv_heads: int, block_size: int, device):
+    """A cache in 4 bits, of zeros: (cache uint8 [num_blocks, num_kv_heads,
+    block_size, 64], scales bf16 [num_blocks, num_kv_heads, block_size, 4])."""
+    shape = (num_blocks, num_kv_heads, block_size)
+    return (torch.zeros(*shape, HEAD_DIM, dtype=torch.uint8, device=device),
+            torch.zeros(*shape, 4, dtype=torch.bfloat16, device=device))
+
+
+def kv4_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *,
+              err: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Inserts K and V rows into a cache in 4 bits (rc_kv4_store): k and v bf16
+    [T, num_kv_heads, 64] (views; K normed and turned), slots int64 [T] (negative:
+    skipped), cache and scales as new_kv4_cache() makes them."""
+    (_draft_module or _draft()).kv4_store(k, v, slots, cache, scales, err, None if stream is None else stream.cuda_stream)
+
+
+def kv4_load(slots: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+             err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The rows at ``slots`` of a cache in 4 bits (rc_kv4_load): bf16
+    [T, num_kv_heads, 128], K | V, exactly what they stand for (zeros for a negative
+    slot)."""
+    return (_draft_module or _draft()).kv4_load(slots, cache, scales, out, err,
+                                                None if stream is None else stream.cuda_stream)
+
+
+def kv_compact(caches: Sequence[torch.Tensor], block_table: torch.Tensor, context_len: torch.Tensor,
+               row_start: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor, *,
+               new_len: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """Moves accepted nodes' rows to follow the context, in every cache
+    (rc_kv_compact): ``caches`` bf16 ones and, for those in 4 bits, cache and scales
+    both; block_table, context_len and row_start as tree_attention had them; path
+    int32 [seqs, most], sequence b's first path_len[b] (int32 [seqs]) entries its
+    accepted nodes in increasing order.  Returns the new context lengths, int32
+    [seqs]."""
+    return (_draft_module or _draft()).kv_compact(caches, block_table, context_len, row_start, path, path_len, new_len, err,
+                                                  None if stream is None else stream.cuda_stream)

@@ -1,6 +1,7 @@
 // Python side of the drafted tokens' calls (rc_rope_table, rc_rope_apply,
 // rc_tree_attention, rc_logits_adjust) and of those around them
-// (rc_head_norm_rope, rc_head_norm_rope_grad): checks torch tensors, makes the
+// (rc_head_norm_rope, rc_head_norm_rope_grad, rc_kv4_store, rc_kv4_load,
+// rc_kv_compact): checks torch tensors, makes the
 // output and calls the C ABI.  The other calls of the package go through ctypes, whose
 // 6 to 12 us a call these cannot afford: their kernels take 2 to 20 us.
 // Arguments come by position (rope_chain_gb300/__init__.py has the signatures
@@ -15,6 +16,7 @@
 #include <torch/csrc/Device.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <optional>
 
@@ -491,6 +493,146 @@ PyObject *head_norm_rope_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A cache in 4 bits and its scales.
+struct Kv4 {
+    uint8_t *cache4;
+    uint16_t *scales;
+    int32_t blocks, heads, block_size;
+
+    Kv4(PyObject *c, PyObject *s, at::Device device) {
+        const Tensor &cache = tensor(c, "cache"), &scale = tensor(s, "scales");
+        TORCH_CHECK_VALUE(cache.dim() == 4 && cache.size(3) == 64 && cache.scalar_type() == at::kByte && cache.is_cuda() &&
+                              cache.is_contiguous(), "cache must be contiguous CUDA uint8 [num_blocks, num_kv_heads, block_size, 64]");
+        TORCH_CHECK_VALUE(scale.dim() == 4 && scale.size(0) == cache.size(0) && scale.size(1) == cache.size(1) &&
+                              scale.size(2) == cache.size(2) && scale.size(3) == 4 && scale.scalar_type() == at::kBFloat16 &&
+                              scale.is_cuda() && scale.is_contiguous(),
+                          "scales must be contiguous CUDA bfloat16 [num_blocks, num_kv_heads, block_size, 4]");
+        beside(cache, device, "cache");
+        beside(scale, device, "scales");
+        no_gradient(scale, "scales");
+        cache4 = static_cast<uint8_t *>(cache.data_ptr());
+        scales = static_cast<uint16_t *>(scale.data_ptr());
+        blocks = narrow<int32_t>(cache.size(0), "num_blocks");
+        heads = narrow<int32_t>(cache.size(1), "num_kv_heads");
+        block_size = narrow<int32_t>(cache.size(2), "block_size");
+    }
+};
+
+PyObject *kv4_store(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // k, v, slots, cache, scales, err, stream
+    need(n, 7);
+    const Tensor &k = tensor(args[0], "k"), &v = tensor(args[1], "v");
+    for (const Tensor *t : {&k, &v}) {
+        const char *name = t == &k ? "k" : "v";
+        heads_view(*t, name);
+        TORCH_CHECK_TYPE(t->scalar_type() == at::kBFloat16, name, " must be bfloat16");
+        no_gradient(*t, name);
+    }
+    TORCH_CHECK_VALUE(k.sizes() == v.sizes() && k.size(2) == 64, "k and v must be [T, num_kv_heads, 64]");
+    beside(v, k.device(), "v");
+    const Kv4 c(args[3], args[4], k.device());
+    TORCH_CHECK_VALUE(c.heads == k.size(1), "k has ", k.size(1), " heads, the cache ", c.heads);
+    TORCH_CHECK_TYPE(args[2] != Py_None, "slots must be a tensor");
+    const int64_t *slots = array<int64_t>(args[2], k.device(), at::kLong, k.size(0), "slots");
+    int32_t *err = counter(args[5], k.device());
+    const On on(k.device(), args[6]);
+    const rc_status s = rc_kv4_store(static_cast<const uint16_t *>(k.const_data_ptr()), k.stride(0), k.stride(1),
+                                     static_cast<const uint16_t *>(v.const_data_ptr()), v.stride(0), v.stride(1), k.size(0),
+                                     c.heads, slots, c.cache4, c.scales, c.blocks, c.block_size, err, on.stream());
+    if (s != RC_OK)
+        return raise_status(s);
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *kv4_load(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // slots, cache, scales, out, err, stream
+    need(n, 6);
+    const Tensor &slot = tensor(args[0], "slots");
+    TORCH_CHECK_VALUE(slot.dim() == 1, "slots must be [T]");
+    const at::Device device = slot.device();
+    const int64_t *slots = array<int64_t>(args[0], device, at::kLong, 0, "slots");
+    const Kv4 c(args[1], args[2], device);
+    Tensor out;
+    if (args[3] != Py_None) {
+        out = tensor(args[3], "out");
+        TORCH_CHECK_VALUE(out.dim() == 3 && out.size(0) == slot.size(0) && out.size(1) == c.heads && out.size(2) == 128 &&
+                              out.scalar_type() == at::kBFloat16 && out.is_cuda() && out.is_contiguous(),
+                          "out must be contiguous CUDA bfloat16 [T, num_kv_heads, 128]");
+        beside(out, device, "out");
+        no_gradient(out, "out");
+    }
+    int32_t *err = counter(args[4], device);
+    const On on(device, args[5]);
+    if (!out.defined())
+        out = at::empty({slot.size(0), c.heads, 128}, slot.options().dtype(at::kBFloat16));
+    const rc_status s = rc_kv4_load(slots, slot.size(0), c.heads, c.cache4, c.scales, c.blocks, c.block_size,
+                                    static_cast<uint16_t *>(out.data_ptr()), err, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *kv_compact(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // caches, block_table, context_len, row_start, path, path_len, new_len, err, stream
+    need(n, 9);
+    constexpr Py_ssize_t kMost = 64;
+    const THPObjectPtr list(PySequence_Fast(args[0], "caches must be a sequence of tensors"));
+    if (!list)
+        throw python_error();
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(list.get());
+    TORCH_CHECK_VALUE(count >= 1 && count <= kMost, "need 1 to ", kMost, " caches, not ", count);
+    const Tensor &table = tensor(args[1], "block_table"), &path = tensor(args[4], "path");
+    TORCH_CHECK_VALUE(table.dim() == 2 && table.scalar_type() == at::kInt && table.is_cuda() &&
+                          (table.size(1) <= 1 || table.stride(1) == 1),
+                      "block_table must be CUDA int32 [seqs, width] with a contiguous last axis");
+    const at::Device device = table.device();
+    const int64_t seqs = table.size(0);
+    TORCH_CHECK_VALUE(path.dim() == 2 && path.size(0) == seqs && path.scalar_type() == at::kInt && path.is_cuda() &&
+                          (path.size(1) <= 1 || path.stride(1) == 1),
+                      "path must be CUDA int32 [seqs, most] with a contiguous last axis");
+    beside(path, device, "path");
+    void *caches[kMost];
+    int32_t row_bytes[kMost];
+    const Tensor &first = tensor(PySequence_Fast_GET_ITEM(list.get(), 0), "caches");
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const Tensor &c = tensor(PySequence_Fast_GET_ITEM(list.get(), i), "caches");
+        TORCH_CHECK_VALUE(c.dim() == 4 && c.is_cuda() && c.is_contiguous(),
+                          "caches must be contiguous CUDA tensors [num_blocks, num_kv_heads, block_size, width]");
+        TORCH_CHECK_VALUE(c.size(0) == first.size(0) && c.size(1) == first.size(1) && c.size(2) == first.size(2),
+                          "caches must agree in num_blocks, num_kv_heads and block_size");
+        beside(c, device, "a cache");
+        no_gradient(c, "a cache");
+        caches[i] = c.data_ptr();
+        row_bytes[i] = narrow<int32_t>(c.size(3) * c.element_size(), "bytes of a cache's row");
+    }
+    TORCH_CHECK_TYPE(args[2] != Py_None && args[3] != Py_None && args[5] != Py_None,
+                     "context_len, row_start and path_len must be tensors");
+    const int32_t *context_len = array<int32_t>(args[2], device, at::kInt, seqs, "context_len");
+    const int32_t *row_start = array<int32_t>(args[3], device, at::kInt, seqs + 1, "row_start");
+    const int32_t *path_len = array<int32_t>(args[5], device, at::kInt, seqs, "path_len");
+    Tensor new_len;
+    if (args[6] != Py_None) {
+        array<int32_t>(args[6], device, at::kInt, seqs, "new_len");
+        new_len = tensor(args[6], "new_len");
+    }
+    int32_t *err = counter(args[7], device);
+    const On on(device, args[8]);
+    if (!new_len.defined())
+        new_len = at::empty({seqs}, table.options());
+    // (the nodes of all sequences are not known here: row_start's own numbers count)
+    const rc_status s = rc_kv_compact(
+        caches, row_bytes, (int32_t)count, narrow<int32_t>(first.size(0), "num_blocks"),
+        narrow<int32_t>(first.size(1), "num_kv_heads"), narrow<int32_t>(first.size(2), "block_size"),
+        static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0), narrow<int32_t>(table.size(1), "width of block_table"),
+        context_len, row_start, narrow<int32_t>(seqs, "seqs"), 0x7FFFFFFF, static_cast<const int32_t *>(path.const_data_ptr()),
+        path.stride(0), narrow<int32_t>(path.size(1), "width of path"), path_len, new_len.data_ptr<int32_t>(), err, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(new_len) : raise_status(s);
+    END_HANDLE_TH_ERRORS
+}
+
 // The exception class that an error status raises.
 PyObject *set_error(PyObject *, PyObject *cls) {
     Py_INCREF(cls);
@@ -506,6 +648,9 @@ PyMethodDef g_methods[] = {
     {"head_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope)), METH_FASTCALL, nullptr},
     {"head_norm_rope_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope_grad)), METH_FASTCALL,
      nullptr},
+    {"kv4_store", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv4_store)), METH_FASTCALL, nullptr},
+    {"kv4_load", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv4_load)), METH_FASTCALL, nullptr},
+    {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_compact)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -1,7 +1,7 @@
 // C ABI of the operators around the drafted tokens' step (declared in
-// include/rope_chain.h): head norms with their rotation.  Arguments are checked on
-// the host, then the kernels go on the caller's stream; nothing here allocates
-// device memory or synchronises.
+// include/rope_chain.h): head norms with their rotation, rows of a cache in 4 bits,
+// accepted rows moved.  Arguments are checked on the host, then the kernels go on the
+// caller's stream; nothing here allocates device memory or synchronises.
 #include "rope_chain.h"
 #include "rc_checks.cuh"
 #include "rc_paged.cuh"
@@ -236,6 +236,167 @@ rc_status rc_head_norm_rope_grad(const void *dy, int64_t dy_row_stride, int64_t 
                                                 norm_wide(dtype, head_dim, rot_dim, layout, *params, cos_sin, {dy, x, dx},
                                                           {vd, vx, vo}), sms, stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, "rc_head_norm_rope_grad launch");
+}
+
+// A cache in 4 bits: sizes and addresses.
+static rc_status check_kv4(const char *fn, int64_t T, int32_t heads, const int64_t *slots, const uint8_t *cache4,
+                           const uint16_t *scales, int32_t num_blocks, int32_t block_size, const int32_t *err)
+{
+    if (heads < 1 || T < 0 || T > 0x7FFFFFFFLL || T * heads > 0x7FFFFFFFLL)
+        return fail(RC_ERR_INVALID_ARG, "%s: need T >= 0, num_kv_heads >= 1 and T*num_kv_heads < 2^31", fn);
+    if (num_blocks < 1 || block_size < 1 || (int64_t)num_blocks * block_size >= (1LL << 31))
+        return fail(RC_ERR_INVALID_ARG, "%s: need num_blocks, block_size >= 1 and num_blocks*block_size < 2^31", fn);
+    if ((T > 0 && !slots) || !aligned(slots, 8))
+        return fail(RC_ERR_INVALID_ARG, "%s: slots must be an 8-byte aligned pointer", fn);
+    if (!cache4 || !aligned(cache4, 16) || !scales || !aligned(scales, 8))
+        return fail(RC_ERR_INVALID_ARG, "%s: cache4 must be a 16-byte and scales an 8-byte aligned pointer", fn);
+    if (!aligned(err, 4))
+        return fail(RC_ERR_INVALID_ARG, "%s: err must be 4-byte aligned", fn);
+    return RC_OK;
+}
+
+static Span kv4_span(const void *p, int32_t num_blocks, int32_t heads, int32_t block_size, size_t row) {
+    return {p, (size_t)num_blocks * heads * block_size * row};
+}
+
+rc_status rc_kv4_store(const uint16_t *k, int64_t k_row_stride, int64_t k_head_stride, const uint16_t *v,
+                       int64_t v_row_stride, int64_t v_head_stride, int64_t T, int32_t num_kv_heads,
+                       const int64_t *slots, uint8_t *cache4, uint16_t *scales, int32_t num_blocks,
+                       int32_t block_size, int32_t *err, cudaStream_t stream)
+{
+    const char *fn = "rc_kv4_store";
+    const rc_status s = check_kv4(fn, T, num_kv_heads, slots, cache4, scales, num_blocks, block_size, err);
+    if (s != RC_OK)
+        return s;
+    const HeadsView vk = heads_view(std::max<int64_t>(T, 1), k_row_stride, k_head_stride, num_kv_heads, kHeadDim);
+    const HeadsView vv = heads_view(std::max<int64_t>(T, 1), v_row_stride, v_head_stride, num_kv_heads, kHeadDim);
+    for (const int64_t x : {vk.row_stride, vk.head_stride, vv.row_stride, vv.head_stride})
+        if (x < 0 || x > kMaxStride || x % 8 != 0)
+            return fail(RC_ERR_INVALID_ARG, "%s: strides of k and v must be multiples of 8 in [0, 2^40]", fn);
+    if ((T > 0 && (!k || !v)) || !aligned(k, 16) || !aligned(v, 16))
+        return fail(RC_ERR_INVALID_ARG, "%s: k and v must be 16-byte aligned pointers", fn);
+    if (T == 0)
+        return ok();
+    const Span cs = kv4_span(cache4, num_blocks, num_kv_heads, block_size, 64), ss = kv4_span(scales, num_blocks, num_kv_heads, block_size, 8);
+    const Span ks = {k, (size_t)vk.elements() * 2}, vs = {v, (size_t)vv.elements() * 2}, at = {slots, (size_t)T * 8}, es = {err, 4};
+    if (overlap(cs, {ss, ks, vs, at, es}) || overlap(ss, {ks, vs, at, es}))
+        return fail(RC_ERR_INVALID_ARG, "%s: cache4 or scales overlaps another operand", fn);
+    Kv4StoreLaunch a{};
+    a.k = k;
+    a.v = v;
+    a.k_row_stride = vk.row_stride;
+    a.k_head_stride = vk.head_stride;
+    a.v_row_stride = vv.row_stride;
+    a.v_head_stride = vv.head_stride;
+    a.T = T;
+    a.slots = slots;
+    a.cache4 = cache4;
+    a.scales = scales;
+    a.capacity = (int64_t)num_blocks * block_size;
+    a.heads = num_kv_heads;
+    a.block_size = block_size;
+    a.err = err;
+    const int sms = num_sms_current();
+    if (sms <= 0)
+        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
+    const cudaError_t e = launch_kv4_store(a, sms, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rc_kv4_store launch");
+}
+
+rc_status rc_kv4_load(const int64_t *slots, int64_t T, int32_t num_kv_heads, const uint8_t *cache4,
+                      const uint16_t *scales, int32_t num_blocks, int32_t block_size, uint16_t *out,
+                      int32_t *err, cudaStream_t stream)
+{
+    const char *fn = "rc_kv4_load";
+    const rc_status s = check_kv4(fn, T, num_kv_heads, slots, cache4, scales, num_blocks, block_size, err);
+    if (s != RC_OK)
+        return s;
+    if ((T > 0 && !out) || !aligned(out, 16))
+        return fail(RC_ERR_INVALID_ARG, "%s: out must be a 16-byte aligned pointer", fn);
+    if (T == 0)
+        return ok();
+    if (overlap({out, (size_t)T * num_kv_heads * 256},
+                {kv4_span(cache4, num_blocks, num_kv_heads, block_size, 64),
+                 kv4_span(scales, num_blocks, num_kv_heads, block_size, 8), {slots, (size_t)T * 8}, {err, 4}}))
+        return fail(RC_ERR_INVALID_ARG, "%s: out overlaps another operand", fn);
+    const Kv4LoadLaunch a = {slots, T, cache4, scales, (int64_t)num_blocks * block_size, num_kv_heads, block_size, out, err};
+    const int sms = num_sms_current();
+    if (sms <= 0)
+        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
+    const cudaError_t e = launch_kv4_load(a, sms, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rc_kv4_load launch");
+}
+
+rc_status rc_kv_compact(void *const *caches, const int32_t *row_bytes, int32_t count, int32_t num_blocks,
+                        int32_t num_kv_heads, int32_t block_size, const int32_t *block_table,
+                        int64_t table_stride, int32_t table_width, const int32_t *context_len,
+                        const int32_t *row_start, int32_t seqs, int64_t rows, const int32_t *path,
+                        int64_t path_stride, int32_t path_width, const int32_t *path_len, int32_t *new_len,
+                        int32_t *err, cudaStream_t stream)
+{
+    const char *fn = "rc_kv_compact";
+    if (count < 1 || count > kMaxCompactCaches || !caches || !row_bytes)
+        return fail(RC_ERR_INVALID_ARG, "%s: need 1 to %d caches with their row_bytes, not %d", fn, kMaxCompactCaches, count);
+    if (num_kv_heads < 1 || num_kv_heads > 65536 || num_blocks < 1 || block_size < 1 ||
+        (int64_t)num_blocks * block_size >= (1LL << 31))
+        return fail(RC_ERR_INVALID_ARG, "%s: need num_kv_heads in [1, 65536], num_blocks, block_size >= 1 and "
+                    "num_blocks*block_size < 2^31", fn);
+    if (seqs < 1 || seqs >= (1 << 24) || rows < 0 || rows > 0x7FFFFFFFLL)
+        return fail(RC_ERR_INVALID_ARG, "%s: need 1 <= seqs < 2^24 and 0 <= rows < 2^31", fn);
+    if (table_width < 0 || table_stride < 0 || table_stride > kMaxStride || (int64_t)table_width * block_size >= (1LL << 31) ||
+        path_width < 0 || path_stride < 0 || path_stride > kMaxStride)
+        return fail(RC_ERR_INVALID_ARG, "%s: need table_width, table_stride, path_width, path_stride >= 0 and "
+                    "table_width*block_size < 2^31", fn);
+    if (!row_start || !context_len || !path_len || (path_width > 0 && !path) || (table_width > 0 && !block_table) ||
+        !aligned(row_start, 4) || !aligned(context_len, 4) || !aligned(path_len, 4) || !aligned(path, 4) ||
+        !aligned(block_table, 4) || !aligned(new_len, 4) || !aligned(err, 4))
+        return fail(RC_ERR_INVALID_ARG, "%s: row_start, context_len, block_table, path and path_len must be 4-byte aligned "
+                    "pointers, new_len and err 4-byte aligned", fn);
+    CompactLaunch a{};
+    Span spans[kMaxCompactCaches];
+    for (int i = 0; i < count; ++i) {
+        const int32_t n = row_bytes[i];
+        if (n < 8 || n % 8 != 0 || n > 4096)
+            return fail(RC_ERR_INVALID_ARG, "%s: row_bytes[%d]=%d is not a multiple of 8 in [8, 4096]", fn, i, n);
+        if (!caches[i] || !aligned(caches[i], n % 16 == 0 ? 16 : 8))
+            return fail(RC_ERR_INVALID_ARG, "%s: caches[%d] must be a 16-byte aligned pointer (8 where its row_bytes are no "
+                        "multiple of 16)", fn, i);
+        spans[i] = {caches[i], (size_t)num_blocks * num_kv_heads * block_size * n};
+        a.caches[i] = caches[i];
+        a.row_bytes[i] = n;
+    }
+    const Span table_span = {block_table, table_width > 0 ? (size_t)((seqs - 1) * table_stride + table_width) * 4 : (size_t)0};
+    const Span path_span = {path, path_width > 0 ? (size_t)((seqs - 1) * path_stride + path_width) * 4 : (size_t)0};
+    const Span start_span = {row_start, ((size_t)seqs + 1) * 4}, len_span = {context_len, (size_t)seqs * 4};
+    const Span count_span = {path_len, (size_t)seqs * 4}, new_span = {new_len, (size_t)seqs * 4}, err_span = {err, 4};
+    for (int i = 0; i < count; ++i) {
+        if (overlap(spans[i], {table_span, path_span, start_span, len_span, count_span, new_span, err_span}))
+            return fail(RC_ERR_INVALID_ARG, "%s: caches[%d] overlaps another operand", fn, i);
+        for (int j = 0; j < i; ++j)
+            if (overlap(spans[i], {spans[j]}))
+                return fail(RC_ERR_INVALID_ARG, "%s: caches[%d] and caches[%d] overlap", fn, j, i);
+    }
+    if (overlap(new_span, {table_span, path_span, start_span, len_span, count_span, err_span}))
+        return fail(RC_ERR_INVALID_ARG, "%s: new_len overlaps an operand that is read, or err", fn);
+    a.count = count;
+    a.num_blocks = num_blocks;
+    a.heads = num_kv_heads;
+    a.block_size = block_size;
+    a.seqs = seqs;
+    a.block_table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.context_len = context_len;
+    a.row_start = row_start;
+    a.rows = rows;
+    a.path = path;
+    a.path_stride = path_stride;
+    a.path_width = path_width;
+    a.path_len = path_len;
+    a.new_len = new_len;
+    a.err = err;
+    const cudaError_t e = launch_kv_compact(a, stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rc_kv_compact launch");
 }
 
 }  // extern "C"

@@ -30,7 +30,24 @@ def norm_grad_operands():
     return dict(norm_operands(), grad=fake(4, 8, 64), workspace=fake(1 << 24, dtype=U8))
 
 
-CALLS = {"head_norm_rope": norm_operands, "head_norm_rope_grad": norm_grad_operands}
+def store_operands():
+    return dict(k=fake(4, 8, 64), v=fake(4, 8, 64), slots=fake(4, dtype=I64), cache=fake(9, 8, 16, 64, dtype=U8),
+                scales=fake(9, 8, 16, 4), err=fake(1, dtype=I32))
+
+
+def load_operands():
+    return dict(slots=fake(4, dtype=I64), cache=fake(9, 8, 16, 64, dtype=U8), scales=fake(9, 8, 16, 4), out=fake(4, 8, 128),
+                err=fake(1, dtype=I32))
+
+
+def compact_operands():
+    return dict(block_table=fake(2, 5, dtype=I32), caches=[fake(9, 8, 16, 128)], context_len=fake(2, dtype=I32),
+                row_start=fake(3, dtype=I32), path=fake(2, 4, dtype=I32), path_len=fake(2, dtype=I32), new_len=fake(2, dtype=I32),
+                err=fake(1, dtype=I32))
+
+
+CALLS = {"head_norm_rope": norm_operands, "head_norm_rope_grad": norm_grad_operands, "kv4_store": store_operands,
+         "kv4_load": load_operands, "kv_compact": compact_operands}
 TENSORS = [(c, n) for c, make in CALLS.items() for n, t in make().items() if isinstance(t, torch.Tensor)]
 # (a tensor without memory sets up the context of its GPU where there are any)
 two_gpus = pytest.mark.skipif(torch.cuda.device_count() == 1, reason="no GPU or two")
@@ -82,3 +99,39 @@ def test_head_norm_gradient_like_x():
     for grad in (fake(4, 8, 32), fake(4, 8, 64, dtype=F32), fake(4, 64, 8).transpose(1, 2), fake(3, 8, 64)):
         with pytest.raises((TypeError, ValueError)):
             rc.head_norm_rope_grad(**dict(norm_grad_operands(), grad=grad))
+
+
+@pytest.mark.parametrize("call", ["kv4_store", "kv4_load"])
+@pytest.mark.parametrize("change", [
+    dict(cache=fake(9, 8, 16, 128, dtype=U8)), dict(cache=fake(9, 8, 16, 64)), dict(cache=fake(9, 8, 64, 16, dtype=U8).transpose(2, 3)),
+    dict(scales=fake(9, 8, 16, 4, dtype=F32)), dict(scales=fake(9, 8, 16, 2)), dict(scales=fake(8, 8, 16, 4)), dict(slots=None),
+    dict(slots=fake(4, dtype=I32)), dict(slots=fake(8, dtype=I64)[::2]), dict(err=fake(0, dtype=I32))])
+def test_kv4_shapes_and_types(call, change):
+    with pytest.raises((TypeError, ValueError)):
+        getattr(rc, call)(**{**CALLS[call](), **change})
+
+
+@pytest.mark.parametrize("change", [dict(k=fake(4, 7, 64)), dict(k=fake(4, 8, 32)), dict(v=fake(3, 8, 64)), dict(v=fake(4, 8, 64, dtype=F32)),
+                                    dict(k=fake(4, 64, 8).transpose(1, 2)), dict(slots=fake(3, dtype=I64)),
+                                    dict(k=fake(4, 2, 64), v=fake(4, 2, 64))])
+def test_kv4_rows(change):
+    with pytest.raises((TypeError, ValueError)):
+        rc.kv4_store(**{**store_operands(), **change})
+
+
+@pytest.mark.parametrize("change", [dict(out=fake(4, 8, 64)), dict(out=fake(3, 8, 128)), dict(out=fake(4, 8, 128, dtype=F32))])
+def test_kv4_output(change):
+    with pytest.raises((TypeError, ValueError)):
+        rc.kv4_load(**{**load_operands(), **change})
+
+
+@pytest.mark.parametrize("change", [
+    dict(caches=[]), dict(caches=3), dict(caches=[None]), dict(caches=[fake(9, 8, 16, 128)] * 65), dict(caches=[fake(9, 8, 16)]),
+    dict(caches=[fake(9, 8, 16, 128), fake(9, 8, 15, 4)]), dict(caches=[fake(9, 8, 128, 16).transpose(2, 3)]),
+    dict(caches=[fake(9, 8, 16, 128, requires_grad=True)]), dict(caches=[fake(9, 8, 16, 128, device="cpu")]),
+    dict(block_table=fake(2, 5, dtype=I64)), dict(block_table=fake(2, 10, dtype=I32)[:, ::2]), dict(path=fake(3, 4, dtype=I32)),
+    dict(path=fake(2, 4, dtype=I64)), dict(path=fake(4, 2, dtype=I32).t()), dict(context_len=fake(1, dtype=I32)),
+    dict(row_start=fake(2, dtype=I32)), dict(path_len=None), dict(path_len=fake(2, dtype=I64)), dict(new_len=fake(1, dtype=I32))])
+def test_compact_shapes_and_types(change):
+    with pytest.raises((TypeError, ValueError)):
+        rc.kv_compact(**{**compact_operands(), **change})

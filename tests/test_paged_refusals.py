@@ -75,3 +75,62 @@ def test_empty_head_norms(lib):
     assert lib.rc_last_error() == b""
     for dim in (0, 1, 513):
         assert lib.rc_head_norm_rope_grad_workspace_size(dim) == 0
+
+
+K, V, SLOTS, C4, SC = 0x100000, 0x180000, 0x200000, 0x8000000, 0x9000000
+KV4 = dict(k=K, kr=512, kh=64, v=V, vr=512, vh=64, T=4, heads=8, slots=SLOTS, cache=C4, scales=SC, nb=8, bs=16, err=ERR, out=OUT + 0x4000000)
+
+
+def kv4_store(lib, **over):
+    a = {**KV4, **over}
+    return lib.rc_kv4_store(A(a["k"]), a["kr"], a["kh"], A(a["v"]), a["vr"], a["vh"], a["T"], a["heads"], A(a["slots"]),
+                            A(a["cache"]), A(a["scales"]), a["nb"], a["bs"], A(a["err"]), None)
+
+
+def kv4_load(lib, **over):
+    a = {**KV4, **over}
+    return lib.rc_kv4_load(A(a["slots"]), a["T"], a["heads"], A(a["cache"]), A(a["scales"]), a["nb"], a["bs"], A(a["out"]),
+                           A(a["err"]), None)
+
+
+COMMON4 = [dict(T=-1), dict(T=1 << 28), dict(heads=0), dict(nb=0), dict(bs=0), dict(nb=1 << 20, bs=1 << 11), dict(slots=None),
+           dict(slots=SLOTS + 4), dict(cache=None), dict(cache=C4 + 8), dict(scales=None), dict(scales=SC + 4), dict(err=ERR + 2)]
+
+
+def test_kv4_refusals(lib):
+    for over in COMMON4 + [dict(k=None), dict(v=None), dict(k=K + 8), dict(v=V + 2), dict(kr=516), dict(vh=60), dict(kr=-512),
+                           dict(vr=1 << 41), dict(cache=K), dict(scales=V), dict(scales=C4 + 64), dict(slots=C4), dict(err=SC)]:
+        assert kv4_store(lib, **over) == BAD, over
+    for over in COMMON4 + [dict(out=None), dict(out=KV4["out"] + 8), dict(out=C4), dict(out=SC), dict(slots=KV4["out"]), dict(err=KV4["out"])]:
+        assert kv4_load(lib, **over) == BAD, over
+    assert kv4_store(lib, T=0, k=None, v=None, slots=None) == OK and kv4_load(lib, T=0, out=None, slots=None) == OK
+
+
+TABLE, LENS, START, PATH, COUNT, NEW = 0x30000, 0x20000, 0x10000, 0x40000, 0x50000, 0x60000
+MOVE = dict(caches=(0x10000000, 0x20000000), bytes=(256, 8), nb=8, heads=4, bs=16, bt=TABLE, ts=4, tw=4, ctx=LENS, rs=START, seqs=2,
+            rows=26, path=PATH, ps=5, pw=5, count=COUNT, new=NEW, err=ERR)
+
+
+def compact(lib, **over):
+    a = {**MOVE, **over}
+    n = len(a["caches"]) if a["caches"] else 0
+    caches = (ctypes.c_void_p * n)(*a["caches"]) if n else None
+    sizes = (ctypes.c_int32 * len(a["bytes"]))(*a["bytes"]) if a["bytes"] else None
+    return lib.rc_kv_compact(caches, sizes, n, a["nb"], a["heads"], a["bs"], A(a["bt"]), a["ts"], a["tw"], A(a["ctx"]), A(a["rs"]),
+                             a["seqs"], a["rows"], A(a["path"]), a["ps"], a["pw"], A(a["count"]), A(a["new"]), A(a["err"]), None)
+
+
+def test_compact_refusals(lib):
+    first = MOVE["caches"][0]
+    size = 8 * 4 * 16 * 256
+    for over in (dict(caches=()), dict(bytes=()), dict(caches=(first,) * 65, bytes=(256,) * 65), dict(nb=0), dict(bs=0), dict(heads=0),
+                 dict(heads=65537), dict(nb=1 << 20, bs=1 << 11), dict(seqs=0), dict(seqs=1 << 24), dict(rows=-1), dict(rows=1 << 31),
+                 dict(tw=-1), dict(ts=-1), dict(tw=1 << 20, bs=1 << 11), dict(pw=-1), dict(ps=-1), dict(ps=1 << 41), dict(rs=None),
+                 dict(ctx=None), dict(count=None), dict(path=None), dict(bt=None), dict(rs=START + 2), dict(ctx=LENS + 1),
+                 dict(count=COUNT + 2), dict(path=PATH + 2), dict(bt=TABLE + 2), dict(new=NEW + 2), dict(err=ERR + 2),
+                 dict(bytes=(12, 8)), dict(bytes=(0, 8)), dict(bytes=(256, 4104)), dict(bytes=(-8, 8)), dict(caches=(None, 0x20000000)),
+                 dict(caches=(first + 8, 0x20000000)), dict(caches=(first, 0x20000004)), dict(caches=(first, first + size - 8)),
+                 dict(caches=(first, first)), dict(bt=first), dict(path=first + size - 4), dict(ctx=first), dict(rs=first), dict(count=first),
+                 dict(new=first), dict(err=first), dict(new=LENS), dict(new=PATH), dict(new=START), dict(new=COUNT), dict(new=TABLE),
+                 dict(new=ERR)):
+        assert compact(lib, **over) == BAD, over
