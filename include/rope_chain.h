@@ -725,6 +725,55 @@ size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_
                                         int32_t num_kv_heads);
 
 /*
+ * rc_window_attention -- rc_tree_attention with a sliding window and a few first
+ * keys that stay visible: of the keys that a row sees, in order (the context, then
+ * the nodes that its mask row names), the first `sinks` and the last `window` count.
+ * For a chain, or a tree whose nodes stand at their depth, that is the window over
+ * positions.  Key tiles that no row of a sequence sees are not read.
+ *
+ *   window       >= 1;  sinks  >= 0
+ *   block_table  entries of blocks without a key that counts are not looked at (such
+ *                blocks may have been given away): those whose keys all lie at or
+ *                past `sinks` and below context_len[b] + 1 - window (without the 1
+ *                where a row sees no node).  Keys of a block that is out of range keep
+ *                their place in a row's order
+ *   other arguments, the workspace and its size, and the errors as rc_tree_attention's
+ */
+rc_status rc_window_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
+                              int32_t num_kv_heads, const int32_t *row_start, int32_t seqs,
+                              const int32_t *context_len, const int32_t *block_table,
+                              int64_t table_stride, int32_t table_width, const uint64_t *tree_mask,
+                              int32_t mask_words, const uint16_t *cache, int32_t num_blocks,
+                              int32_t block_size, int32_t window, int32_t sinks, float scale,
+                              uint16_t *out, int64_t out_row_stride, float *lse, int32_t *err,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * rc_kv4_attention -- rc_tree_attention, or with a window rc_window_attention, over a
+ * cache in 4 bits (below).  K and V enter the products as exactly what they stand
+ * for; scores, running maximum, sums and outputs are FP32, the weights are rounded to
+ * bf16 for the product with V, the output once to bf16.
+ *
+ *   cache4, scales   as rc_kv4_store's
+ *   window       >= 1, or 0: none (sinks 0 then)
+ *   workspace    of rc_kv4_attention_workspace_size() bytes, or NULL
+ *   other arguments and errors as rc_window_attention's
+ */
+rc_status rc_kv4_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
+                           int32_t num_kv_heads, const int32_t *row_start, int32_t seqs,
+                           const int32_t *context_len, const int32_t *block_table, int64_t table_stride,
+                           int32_t table_width, const uint64_t *tree_mask, int32_t mask_words,
+                           const uint8_t *cache4, const uint16_t *scales, int32_t num_blocks,
+                           int32_t block_size, int32_t window, int32_t sinks, float scale,
+                           uint16_t *out, int64_t out_row_stride, float *lse, int32_t *err,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of rc_kv4_attention for these sizes on the current device, with the
+   promises of rc_tree_attention_workspace_size. */
+size_t rc_kv4_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_heads,
+                                       int32_t num_kv_heads);
+
+/*
  * rc_logits_adjust -- penalties for repeated tokens, biases and grammar masks
  * on the logits of drafted (or single) tokens.  Rows belong to sequences as in
  * rc_tree_attention.  For row r of sequence b and token t, g counts t among

@@ -159,6 +159,15 @@ SIGNATURES["rc_head_norm_rope_grad"] = ([_vp, _c.c_int64, _c.c_int64, _vp, _c.c_
                                          _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _vp, _c.c_int64, _c.c_int64,
                                          _vp, _vp, _vp, _c.c_size_t, _vp, _vp], _c.c_int)
 SIGNATURES["rc_head_norm_rope_grad_workspace_size"] = ([_c.c_int32], _c.c_size_t)
+SIGNATURES["rc_window_attention"] = ([_vp, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _vp, _c.c_int32, _vp, _vp,
+                                      _c.c_int64, _c.c_int32, _vp, _c.c_int32, _vp, _c.c_int32, _c.c_int32,
+                                      _c.c_int32, _c.c_int32, _c.c_float, _vp, _c.c_int64, _vp, _vp, _vp, _c.c_size_t,
+                                      _vp], _c.c_int)
+SIGNATURES["rc_kv4_attention"] = ([_vp, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _vp, _c.c_int32, _vp, _vp,
+                                   _c.c_int64, _c.c_int32, _vp, _c.c_int32, _vp, _vp, _c.c_int32, _c.c_int32,
+                                   _c.c_int32, _c.c_int32, _c.c_float, _vp, _c.c_int64, _vp, _vp, _vp, _c.c_size_t,
+                                   _vp], _c.c_int)
+SIGNATURES["rc_kv4_attention_workspace_size"] = ([_c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32], _c.c_size_t)
 SIGNATURES["rc_kv4_store"] = ([_vp, _c.c_int64, _c.c_int64, _vp, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _vp,
                                _vp, _vp, _c.c_int32, _c.c_int32, _vp, _vp], _c.c_int)
 SIGNATURES["rc_kv4_load"] = ([_vp, _c.c_int64, _c.c_int32, _vp, _vp, _c.c_int32, _c.c_int32, _vp, _vp, _vp], _c.c_int)
@@ -969,6 +978,22 @@ def tree_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.
         None if stream is None else stream.cuda_stream)
 
 
+def window_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.Tensor,
+                     block_table: torch.Tensor, cache: torch.Tensor, *, window: int, sinks: int = 0,
+                     tree_mask: Optional[torch.Tensor] = None, scale: float = HEAD_DIM ** -0.5,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     err: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """tree_attention with a sliding window (rc_window_attention): of the keys that a
+    row sees, in order (the context, then the nodes that its mask row names), the
+    first ``sinks`` and the last ``window`` count.  Blocks without such a key are not
+    looked at, so they may have been given away.  ``workspace``:
+    tree_attention_workspace()."""
+    return (_draft_module or _draft()).window_attention(
+        q, row_start, context_len, block_table, cache, tree_mask, scale, out, lse, err, workspace,
+        None if stream is None else stream.cuda_stream, window, sinks)
+
+
 def logits_adjust(logits: torch.Tensor, row_start: torch.Tensor, *,
                   history: Optional[torch.Tensor] = None,
                   history_start: Optional[torch.Tensor] = None,
@@ -1023,6 +1048,32 @@ def kv4_load(slots: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, *, 
     slot)."""
     return (_draft_module or _draft()).kv4_load(slots, cache, scales, out, err,
                                                 None if stream is None else stream.cuda_stream)
+
+
+def kv4_attention_workspace(rows: int, seqs: int, num_heads: int, num_kv_heads: int,
+                            device) -> torch.Tensor:
+    """A workspace for kv4_attention (rc_kv4_attention_workspace_size bytes on
+    ``device``): it also serves calls of fewer rows and of more sequences."""
+    with torch.cuda.device(device):
+        n = int(lib().rc_kv4_attention_workspace_size(rows, seqs, num_heads, num_kv_heads))
+    if n == 0 and rows != 0:
+        raise RopeChainError(RC_ERR_INVALID_ARG, "no workspace size for these sizes")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def kv4_attention(q: torch.Tensor, row_start: torch.Tensor, context_len: torch.Tensor, block_table: torch.Tensor,
+                  cache: torch.Tensor, scales: torch.Tensor, *, window: Optional[int] = None, sinks: int = 0,
+                  tree_mask: Optional[torch.Tensor] = None, scale: float = HEAD_DIM ** -0.5,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  err: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """tree_attention, or with ``window`` window_attention, over a cache in 4 bits
+    (rc_kv4_attention): cache and scales as new_kv4_cache() makes and kv4_store()
+    fills them, the other operands as tree_attention's; ``workspace``:
+    kv4_attention_workspace()."""
+    return (_draft_module or _draft()).kv4_attention(
+        q, row_start, context_len, block_table, cache, scales, tree_mask, scale, out, lse, err, workspace,
+        None if stream is None else stream.cuda_stream, window, sinks)
 
 
 def kv_compact(caches: Sequence[torch.Tensor], block_table: torch.Tensor, context_len: torch.Tensor,

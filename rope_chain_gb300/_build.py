@@ -24,7 +24,8 @@ MODULE_STAMP = os.path.join(BUILD, "module.txt")      # the torch and Python tha
 HEADER = os.path.join(ROOT, "include", "rope_chain.h")
 SOURCES = ["rc_api.cu", "k1_norms.cu", "k2_gemm.cu", "k3_store.cu", "k4_qkv_front.cu",
            "rc_project_static.cu", "k5_tree_attention.cu", "k6_rope.cu", "k7_logits.cu", "rc_draft.cu",
-           "k8_head_norm.cu", "k9_kv4.cu", "k10_compact.cu", "rc_paged.cu"]
+           "k8_head_norm.cu", "k9_kv4.cu", "k10_compact.cu", "k11_kv4_attention.cu",
+           "rc_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # --fmad=false: no multiply-add is fused unless the source asks for it.
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC",

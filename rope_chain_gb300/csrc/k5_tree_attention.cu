@@ -22,10 +22,9 @@
 // trees of 12 over 136 keys: 15.6 us, in equal ranges 34.6).  A unit that is cut
 // leaves FP32 partials (output, m, sum) in the workspace, which a second kernel
 // joins in key order (no atomics: the result does not depend on timing).
-#include "rc_draft.cuh"
+#include "rc_attention.cuh"
 #include "rc_tcgen05.cuh"
 
-#include <algorithm>
 #include <cmath>
 
 namespace rc {
@@ -33,323 +32,6 @@ namespace rc {
 __device__ unsigned int g_attention_faults;
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kKeyTile = 128;          // keys per step of a CTA
-constexpr float kGrow = 8.0f;          // log2: growth of a row's maximum at which its output is rescaled
-
-struct Args : TreeAttentionLaunch {
-    float scale_log2;                  // scale * log2 e
-    int32_t min_tiles;                 // fewest key tiles a CTA is given
-    bool whole;                        // units are not cut
-    int32_t change;                    // going to another unit, in key tiles' time
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// ---------------------------------------------------------------- schedule
-
-struct Seq {
-    int32_t r0, n;                     // first row, nodes
-    int32_t ctx, keys;                 // context keys, all keys
-};
-
-__device__ __forceinline__ Seq seq_of(const Args &a, int b) {
-    Seq s;
-    s.r0 = (int32_t)max((int64_t)0, min((int64_t)__ldg(a.row_start + b), a.rows));
-    const int32_t r1 = (int32_t)max((int64_t)s.r0, min((int64_t)__ldg(a.row_start + b + 1), a.rows));
-    s.n = r1 - s.r0;
-    const int64_t ctx = max(__ldg(a.context_len + b), 0);
-    const int64_t room = (int64_t)a.table_width * a.block_size;
-    s.keys = (int32_t)min(ctx + s.n, room);
-    s.ctx = (int32_t)min(ctx, (int64_t)s.keys);
-    return s;
-}
-
-template <int kRows> __device__ __forceinline__ int row_tiles(const Args &a, const Seq &s) {
-    return (s.n * a.group + kRows - 1) / kRows;
-}
-__device__ __forceinline__ int key_tiles(const Seq &s) { return max(1, (s.keys + kKeyTile - 1) / kKeyTile); }
-
-// How the units are cut.  Their slots, laid end to end, are shared out evenly.
-//   most >= 1: a slot is a part of at most so many key tiles, and a CTA gets one
-//              (or, uncut, as many units as another)
-//   most == 0: a unit's slots are its key tiles and then `change` empty ones, for
-//              the time that the change to it takes
-template <int kRows> __device__ __forceinline__ int64_t slots_of(const Args &a, int b, int32_t most) {
-    const Seq s = seq_of(a, b);
-    const int kt = key_tiles(s);
-    return (int64_t)row_tiles<kRows>(a, s) * a.kv_heads * (most > 0 ? (kt - 1) / most + 1 : kt + a.change);
-}
-
-// A quotient; division of 64 bits is some 100 instructions, of 32 bits 20.
-__device__ __forceinline__ int64_t quotient(int64_t x, int32_t y) {
-    return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
-struct Place {
-    int32_t most;                      // see slots_of
-    int64_t total;                     // slots of all units
-    int32_t used;                      // CTAs that have some
-    int64_t each;                      // total / used and the remainder
-    int32_t rest;
-    int64_t lo, hi;                    // this CTA's range
-    // where CTA c's range begins: total * c / used
-    __device__ __forceinline__ int64_t begin_of(int32_t c) const {
-        return each * c + (uint32_t)((uint32_t)rest * (uint32_t)c) / (uint32_t)used;
-    }
-    int32_t b;                         // the sequence of `at`
-    int64_t off;                       // `at` within the sequence's slots
-};
-
-// How many key tiles a part has at most, 0: a cut wherever it falls (slots_of).
-// Parts of `most` tiles are at most tiles / most + units.  They are taken where a
-// CTA gets fewer tiles so than slots otherwise, or hardly more than a change.
-__device__ __forceinline__ int32_t most_of(const Args &a, int64_t tiles, int64_t units, int ctas) {
-    if (units >= ctas)
-        return 0;
-    const int32_t room = ctas - (int32_t)units;
-    const int64_t most = max((int64_t)a.min_tiles, quotient(tiles + room - 1, room));
-    return most <= a.change + 2 || most * ctas <= tiles + a.change * units ? (int32_t)min(most, (int64_t)INT32_MAX) : 0;
-}
-
-// The range of CTA c of `ctas`, and where its first slot lies.  Called by all
-// kThreads threads.  kParts: cut into parts where that is better (not in the small
-// kernel: its start would take 0.7 us longer, one token over 500 keys 7.9 instead
-// of 7.2 us, and few calls have fewer units than CTAs, 4 tokens over 3000 keys 14.0
-// and 12.4).  Up to 32 sequences a lane takes one, and each warp finds the range
-// by itself (3 trees of 13: 16.6 us, by the block 17.0); beyond, a thread takes a
-// run of sequences, and the one whose run holds the slot walks it.
-template <int kRows, int kThreads, bool kParts>
-__device__ Place locate(const Args &a, int c, int ctas) {
-    __shared__ int64_t warp_tiles[kParts ? kThreads / 32 : 1], warp_units[kParts ? kThreads / 32 : 1];
-    __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ int64_t found_off;
-    __shared__ int32_t found_b;
-    const bool alone = kParts && a.seqs <= 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int threads = alone ? 32 : kThreads, me = alone ? lane : (int)threadIdx.x;
-    const int per = (a.seqs + threads - 1) / threads;
-    const int b0 = min(me * per, a.seqs), b1 = min(b0 + per, a.seqs);
-    Place p;
-    p.most = a.whole ? INT32_MAX : 0;
-    if (kParts && !a.whole && a.partial != nullptr) {
-        int64_t tiles = 0, units = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(a, b);
-            const int n = row_tiles<kRows>(a, s) * a.kv_heads;
-            units += n;
-            tiles += (int64_t)n * key_tiles(s);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
-            units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
-        }
-        if (!alone) {
-            if (lane == 0) {
-                warp_tiles[kParts ? warp : 0] = tiles;
-                warp_units[kParts ? warp : 0] = units;
-            }
-            __syncthreads();
-            tiles = units = 0;
-            for (int w = 0; w < kThreads / 32; ++w) {
-                tiles += warp_tiles[kParts ? w : 0];
-                units += warp_units[kParts ? w : 0];
-            }
-        }
-        p.most = most_of(a, tiles, units, ctas);
-    }
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += slots_of<kRows>(a, b, p.most);
-    int64_t run = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, run, o);
-        if (lane >= o)
-            run += v;
-    }
-    int64_t before = run - mine;
-    if (alone) {
-        p.total = __shfl_sync(0xFFFFFFFFu, run, 31);
-    } else {
-        if (lane == 31)
-            warp_sum[warp] = run;
-        __syncthreads();
-        p.total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp)
-                before += warp_sum[w];
-            p.total += warp_sum[w];
-        }
-    }
-    p.used = (int32_t)max((int64_t)1, min((int64_t)ctas, p.most > 0 ? p.total : quotient(p.total, a.min_tiles)));
-    p.each = quotient(p.total, p.used);
-    p.rest = (int32_t)(p.total - p.each * p.used);               // rest * c < used^2 < 2^32
-    p.lo = c < p.used ? p.begin_of(c) : p.total;
-    p.hi = c < p.used ? p.begin_of(c + 1) : p.total;
-    p.b = 0;
-    p.off = 0;
-    if (p.lo >= p.hi)
-        return p;                      // uniform
-    const bool here = p.lo >= before && p.lo < before + mine;
-    if (alone) {
-        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
-        p.b = src;
-        p.off = p.lo - __shfl_sync(0xFFFFFFFFu, before, src);
-        return p;
-    }
-    if (here) {
-        int64_t off = p.lo - before;
-        int b = b0;
-        for (int64_t t; off >= (t = slots_of<kRows>(a, b, p.most)); ++b)
-            off -= t;
-        found_b = b;
-        found_off = off;
-    }
-    __syncthreads();
-    p.b = found_b;
-    p.off = found_off;
-    return p;
-}
-
-// One piece of a unit: key tiles k0 .. k0 + count - 1 of its kt.
-struct Piece {
-    Seq s;
-    int32_t b, unit, h, tile;          // sequence, unit within it, its KV head and row tile
-    int32_t k0, count, kt;
-    int32_t parts;                     // of the unit, where it is cut into such
-    int64_t begin;                     // the unit's first slot
-    __device__ bool whole() const { return k0 == 0 && count == kt; }
-};
-
-// The pieces of a CTA's range, in order.
-template <int kRows> struct Walk {
-    int64_t pos, off, hi;
-    int32_t b, most;
-    __device__ explicit Walk(const Place &p) : pos(p.lo), off(p.off), hi(p.hi), b(p.b), most(p.most) {}
-    __device__ bool next(const Args &a, Piece &u) {
-        while (pos < hi) {
-            u.s = seq_of(a, b);
-            u.kt = key_tiles(u.s);
-            const int rt = row_tiles<kRows>(a, u.s);
-            u.parts = most > 0 ? (u.kt - 1) / most + 1 : 0;
-            const int32_t slots = most > 0 ? u.parts : u.kt + a.change;
-            const int64_t all = (int64_t)rt * a.kv_heads * slots;
-            if (off >= all) {                           // the next sequence with rows
-                off -= all;
-                ++b;
-                continue;
-            }
-            u.b = b;
-            u.unit = (int32_t)quotient(off, slots);
-            const int32_t slot = (int32_t)(off - (int64_t)u.unit * slots);
-            u.h = u.unit / rt;
-            u.tile = u.unit - u.h * rt;
-            u.begin = pos - slot;
-            if (most > 0) {
-                u.k0 = (int32_t)quotient((int64_t)u.kt * slot, u.parts);
-                u.count = (int32_t)quotient((int64_t)u.kt * (slot + 1), u.parts) - u.k0;
-                ++pos;
-                ++off;
-                return true;
-            }
-            const int32_t here = (int32_t)min((int64_t)(slots - slot), hi - pos);
-            u.k0 = slot;
-            u.count = min(u.kt - slot, here);
-            pos += here;
-            off += here;
-            if (u.count <= 0)
-                continue;                               // empty slots only
-            if (a.partial == nullptr) {
-                // without a workspace a unit belongs to the CTA of its first tile
-                if (u.k0 != 0)
-                    continue;
-                u.count = u.kt;
-            }
-            return true;
-        }
-        return false;
-    }
-};
-
-// A partial: a header, then kRows x 64 outputs (not divided by the sum), kRows
-// maxima and kRows sums.  Each CTA has two: slot 2c for the unit that an
-// earlier CTA began, slot 2c + 1 for one that it begins and a later CTA ends,
-// whose header names the unit and its last CTA (or says that there is none).
-struct Header {
-    int32_t last;                      // slot 2c + 1: last CTA of the unit, 0 without a unit
-    int32_t b, unit;
-    int32_t unfinite;
-};
-constexpr int kHeaderFloats = sizeof(Header) / sizeof(float);
-template <int kRows> constexpr int kSlotFloats = kHeaderFloats + kRows * (kHeadDim + 2);
-template <int kRows> __device__ __forceinline__ float *slot_of(const Args &a, int64_t slot) {
-    return a.partial + slot * kSlotFloats<kRows>;
-}
-template <int kRows> constexpr int kSlotOut = kHeaderFloats;
-template <int kRows> constexpr int kSlotMax = kSlotOut<kRows> + kRows * kHeadDim;
-template <int kRows> constexpr int kSlotSum = kSlotMax<kRows> + kRows;
-
-__device__ __forceinline__ bool sees(const Args &a, const Seq &s, int i, int j) {
-    if (a.tree_mask == nullptr)
-        return j <= i;
-    return (j >> 6) < a.mask_words &&
-           ((__ldg(a.tree_mask + (int64_t)(s.r0 + i) * a.mask_words + (j >> 6)) >> (j & 63)) & 1u) != 0u;
-}
-
-// Logical key p's block, as the table has it, and with it the element offset of
-// the key's row in the cache (-1 without a valid block).
-__device__ __forceinline__ int32_t block_of(const Args &a, int b, int p) {
-    return __ldg(a.block_table + b * a.table_stride + (uint32_t)p / (uint32_t)a.block_size);
-}
-__device__ __forceinline__ int64_t offset_in(const Args &a, int32_t blk, int h, int p) {
-    const uint32_t bs = (uint32_t)a.block_size;
-    if (blk < 0 || blk >= a.num_blocks)
-        return -1;
-    return (((int64_t)blk * a.kv_heads + h) * bs + (uint32_t)p % bs) * (2 * kHeadDim);
-}
-
-// The header of this CTA's part of a split unit.
-template <int kRows>
-__device__ void write_header(const Args &a, const Place &p, const Piece &u, bool unfinite) {
-    Header h{0, u.b, u.unit, unfinite ? 1 : 0};
-    if (u.k0 == 0 && p.most > 0) {
-        h.last = (int32_t)blockIdx.x + u.parts - 1;
-    } else if (u.k0 == 0) {
-        const int64_t end = u.begin + u.kt;
-        // the CTA of the unit's last tile, from an estimate
-        int32_t last = min(p.used - 1, (int32_t)__fdividef((float)end * (float)p.used, (float)p.total));
-        while (last + 1 < p.used && p.begin_of(last + 1) < end)
-            ++last;
-        while (p.begin_of(last) >= end)
-            --last;
-        h.last = last;
-    }
-    *reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0))) = h;
-}
-
-// A drafted V row that is infinite or NaN must not reach rows that do not see
-// it (0 * inf in the matrix product), so the products take zeros in its place
-// and the rows that see it get it added here.  Rare: only where the flag of a
-// unit is set.
-__device__ __noinline__ float add_unfinite(const Args &a, const Seq &s, int b, int h, int i, int d, float x) {
-    for (int j = 0; j < min(s.n, s.keys - s.ctx); ++j) {
-        if (!sees(a, s, i, j))
-            continue;
-        const int64_t o = offset_in(a, block_of(a, b, s.ctx + j), h, s.ctx + j);
-        const uint32_t v = o < 0 ? 0u : (uint32_t)a.cache[o + kHeadDim + d] << 16;
-        if ((v & 0x7F800000u) == 0x7F800000u)
-            x += __uint_as_float(v);
-    }
-    return x;
-}
 
 // ------------------------------------------------- few rows: mma.sync tiles
 //
@@ -404,7 +86,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // Zeros in place of infinite and NaN halves of a register of V whose two keys
-// are drafted ones (lo, hi); true if there was one.
+// are such as a row may not see (lo, hi); true if there was one.
 __device__ __forceinline__ bool finite_only(uint32_t &w, bool lo, bool hi) {
     const bool x = lo && (w & 0x00007F80u) == 0x00007F80u, y = hi && (w & 0x7F800000u) == 0x7F800000u;
     if (x)
@@ -415,7 +97,7 @@ __device__ __forceinline__ bool finite_only(uint32_t &w, bool lo, bool hi) {
 }
 
 // kRuns: blocks hold a multiple of 16 keys, so a chunk is 4 KiB in a row.
-template <int kTiles, bool kRuns>
+template <int kTiles, bool kRuns, bool kWindow>
 __global__ void __launch_bounds__(kSmallThreads, kTiles == 1 ? 2 : 1)
 k5_small(const __grid_constant__ Args a)
 {
@@ -428,13 +110,13 @@ k5_small(const __grid_constant__ Args a)
     pdl_trigger();
     pdl_wait();
 
-    const Place at = locate<kRows, kSmallThreads, false>(a, blockIdx.x, gridDim.x);
+    const Place at = locate<kRows, kSmallThreads, false, kWindow>(a, blockIdx.x, gridDim.x);
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
-    Walk<kRows> walk(at);
-    Piece u;
+    Walk<kRows, kWindow> walk(at);
+    Piece<kWindow> u;
     while (walk.next(a, u)) {
-        const Seq &s = u.s;
+        const SeqOf<kWindow> &s = u.s;
         const int b = u.b, h = u.h, tile = u.tile, unit = u.unit, k0 = u.k0, count = u.count;
 
         // this thread's rows: lane / 4 and lane / 4 + 8 of each row tile
@@ -458,6 +140,14 @@ k5_small(const __grid_constant__ Args a)
                     qf[m][k][e] = node[m][e & 1] >= 0 ? __ldg(src[e & 1] + 8 * k + (lane & 3) + 4 * (e >> 1)) : 0u;
             }
         }
+        int32_t begin[kTiles][2];                       // of the rows' windows
+        if constexpr (kWindow) {
+#pragma unroll
+            for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    begin[m][e] = begin_of_window(a, s, node[m][e]);
+        }
         // ref, limit: as in the wide kernel (a row's reference moves when a score
         // passes it by 2^8)
         float o[kTiles][8][4], ref[kTiles][2], limit[kTiles][2], sum[kTiles][2];
@@ -479,20 +169,22 @@ k5_small(const __grid_constant__ Args a)
         // Where chunks lie.  Block numbers are loaded well before they are looked
         // at (a warp that looks waits): with kRuns a lane has chunk j & ~31 +
         // lane, 32 chunks ahead, else a key of the next chunk.
-        const int lane_key = kRuns ? lane * kKeyTile : lane & 15;
-        auto first_key = [&](int j) { return (k0 + j) * kKeyTile + warp * kChunk; };
+        auto first_key = [&](int j) { return tile_at(s, k0 + j) * kKeyTile + warp * kChunk; };
+        auto lane_key = [&](int j) { return kRuns ? first_key(j + lane) : first_key(j) + (lane & 15); };
         auto table_entry = [&](int j) -> int32_t {          // for this lane's key at or after chunk j
-            const int p = first_key(j) + lane_key;
+            const int p = lane_key(j);
             return j + (kRuns ? lane : 0) < count && p < s.keys ? block_of(a, b, p) : -1;
         };
         int32_t entry = table_entry(0);
         int64_t from = -1;
         auto place = [&](int j) {                           // this lane's row from `entry`
-            const int p = first_key(j) + lane_key;
+            const int p = lane_key(j);
             const bool there = j + (kRuns ? lane : 0) < count && p < s.keys;
-            from = there ? offset_in(a, entry, h, p) : -1;
-            // once per block that is out of range: at its first key
-            if (there && from < 0 && (kRuns || lane < 16) && unit == 0 && p % a.block_size == 0 && a.err != nullptr)
+            const bool wanted = there && some_seen(a, s, p, kRuns ? kChunk : 1);
+            from = wanted ? offset_in(a, entry, h, p) : -1;
+            // once per block that is out of range: at the first of its keys that is needed
+            if (wanted && from < 0 && (kRuns || lane < 16) && unit == 0 && a.err != nullptr &&
+                first_needed(a, s, p, kRuns ? min(kChunk, s.keys - p) : 1))
                 atomicAdd(a.err, 1);
         };
         const uint32_t lane_at = ((lane >> 3) & 1) * (kChunkBytes / 2) + (lane >> 4) * 128;
@@ -562,7 +254,7 @@ k5_small(const __grid_constant__ Args a)
             const int p0 = first_key(j);
             const uint32_t real = s_real[warp][st];
             st = st + 1 == kStages ? 0 : st + 1;
-            const bool drafted = p0 + kChunk > s.ctx;
+            const bool partly = some_partly_seen(a, s, p0, kChunk);
             float t[kTiles][2][4];
 #pragma unroll
             for (int m = 0; m < kTiles; ++m)
@@ -581,16 +273,16 @@ k5_small(const __grid_constant__ Args a)
                     mma16816(t[m][1], qf[m][k], kf[2], kf[3]);
                 }
             }
-            if (real != 0xFFFFu || drafted) {
+            if (real != 0xFFFFu || partly) {
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int in = 8 * n + 2 * (lane & 3) + (e & 1), i = node[m][e >> 1];
-                            const int p = p0 + in;
-                            if (!((real >> in) & 1u) || (p >= s.ctx && (i < 0 || !sees(a, s, i, p - s.ctx))))
+                            const int in = 8 * n + 2 * (lane & 3) + (e & 1);
+                            if (!((real >> in) & 1u) ||
+                                !sees_key(a, s, node[m][e >> 1], p0 + in, kWindow ? begin[m][e >> 1] : 0))
                                 t[m][n][e] = -INFINITY;
                         }
             }
@@ -650,11 +342,11 @@ k5_small(const __grid_constant__ Args a)
             for (int n = 0; n < 8; n += 2) {
                 uint32_t vf[4];
                 load4_t(vf, v_lane[n / 2] + at);
-                if (drafted) {
+                if (partly) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int p = p0 + 8 * (q & 1) + 2 * (lane & 3);
-                        unfinite |= finite_only(vf[q], p >= s.ctx, p + 1 >= s.ctx);
+                        unfinite |= finite_only(vf[q], partly_seen(a, s, p), partly_seen(a, s, p + 1));
                     }
                 }
 #pragma unroll
@@ -730,7 +422,7 @@ k5_small(const __grid_constant__ Args a)
                     slot[kSlotSum<kRows> + m * 16 + r] = total;
                 }
                 if (threadIdx.x == 0 && m == 0)
-                    write_header<kRows>(a, at, u, unfinite);
+                    write_header<kRows, kWindow>(a, at, u, unfinite);
             } else if (i < s.n) {
                 const int head = h * a.group + row - i * a.group;
                 if (unfinite) {
@@ -924,8 +616,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Which of the keys base .. base + 31 node i sees (bit k: key base + k);
-// i < 0: none of the drafted ones.
-__device__ uint32_t seen32(const Args &a, const Seq &s, int i, int base) {
+// i < 0: none of the drafted ones.  `begin`: of the row's window.
+template <bool kWindow> __device__ uint32_t seen32(const Args &a, const SeqOf<kWindow> &s, int i, int base, int32_t begin) {
     auto below = [](int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); };
     const uint32_t ctx = below(s.ctx - base);
     uint32_t drafted = 0u;
@@ -947,10 +639,21 @@ __device__ uint32_t seen32(const Args &a, const Seq &s, int i, int base) {
             }
         }
     }
+    if constexpr (kWindow) {
+        uint32_t seen = (ctx & (below(a.sinks - base) | ~below(begin - base))) | (drafted & ~ctx);
+        if (i >= 0 && begin > s.ctx && base + 32 > s.ctx) {
+            // nodes that the window has left behind, by their place in the row's order
+            int place = s.ctx + seen_before(a, s, i, max(0, base - s.ctx));
+            for (uint32_t rest = drafted & ~ctx; rest != 0u && place < begin; rest &= rest - 1u, ++place)
+                if (place >= a.sinks)
+                    seen &= ~(rest & (0u - rest));
+        }
+        return seen & below(s.keys - base);
+    }
     return (ctx | (drafted & ~ctx)) & below(s.keys - base);
 }
 
-template <int kQ>
+template <int kQ, bool kWindow>
 __global__ void __launch_bounds__(kWideThreads<kQ>, kQ == 1 ? 2 : 1)
 k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a, int box)
 {
@@ -997,17 +700,17 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                      ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols<kQ>) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    Place at = locate<kRows, kThreads, true>(a, blockIdx.x, gridDim.x);
+    Place at = locate<kRows, kThreads, true, kWindow>(a, blockIdx.x, gridDim.x);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;                       // row tile t: S, P, O from column 256 t
     if (a.partial != nullptr && threadIdx.x == 0)
         reinterpret_cast<Header *>(slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + 1))->last = 0;
-    Walk<kRows> walk(at);
+    Walk<kRows, kWindow> walk(at);
     if (s_skip != 0u)
         walk.hi = walk.pos;
-    Piece u;
+    Piece<kWindow> u;
     if constexpr (kQ == 2) {
         in_memory(at);
         in_memory(walk);
@@ -1021,22 +724,23 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         const int boxes = kKeyTile / box;               // <= 16
         bool fine = true;
         while (fine && walk.next(a, u)) {
-            const Seq &s = u.s;
+            const SeqOf<kWindow> &s = u.s;
             // this lane's box of tile j: its block
             auto look_up = [&](int j) -> int {
-                const int p = (u.k0 + j) * kKeyTile + lane * box;
+                const int p = tile_at(s, u.k0 + j) * kKeyTile + lane * box;
                 return j < u.count && lane < boxes && p < s.keys
                            ? block_of(a, u.b, p) : 0;
             };
             int blk = look_up(0);
             for (int j = 0; j < u.count; ++j, ++n) {
                 const uint32_t st = n % kStages, full = full0 + 8u * st;
-                const int p = (u.k0 + j) * kKeyTile + lane * box;
+                const int p = tile_at(s, u.k0 + j) * kKeyTile + lane * box;
                 const bool mine = lane < boxes && p < s.keys;
                 const int off = mine ? (int)((uint32_t)p % (uint32_t)a.block_size) : 0;
-                const bool bad = mine && (blk < 0 || blk >= a.num_blocks);
-                if (bad && keys && u.unit == 0 && off == 0 && a.err != nullptr)
-                    atomicAdd(a.err, 1);                // once per block: at its first key
+                const bool lost = mine && (blk < 0 || blk >= a.num_blocks);
+                const bool bad = lost || (mine && !some_seen(a, s, p, box));
+                if (lost && keys && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(box, s.keys - p)))
+                    atomicAdd(a.err, 1);                // once per block: at the first key that is needed
                 fine = wait_phase(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
                 fine = __all_sync(0xFFFFFFFFu, fine);
                 if (!fine)
@@ -1049,7 +753,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 }
                 __syncwarp();
                 if (mine) {
-                    // a block out of range reads zeros: one past the last
+                    // a block out of range, or of no row, reads zeros: one past the last
                     const int from = bad ? a.num_blocks : blk;
                     const uint32_t dst = sK + st * (2 * kTileBytes) + (uint32_t)(lane * box) * 128u;
                     if (keys)
@@ -1126,7 +830,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         // (a wait that fails has raised a fault: the tiles are gone through all
         // the same, so that every barrier sees its arrivals)
         while (walk.next(a, u)) {
-            const Seq &s = u.s;
+            const SeqOf<kWindow> &s = u.s;
             {
                 // Q: thread i of the tile's 256 takes half of row i / 2
                 const int i = threadIdx.x & 255, r = i >> 1, half = i & 1;
@@ -1145,6 +849,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 mbar_arrive_local(q_ready0 + 8u * t);
             }
             int node[2];
+            int32_t begin[2];                           // of the rows' windows
             // of each row: minus the reference (log2), the maximum that asks for
             // another (-inf: none seen yet), this lane's sum
             float ref[2], limit[2], sum[2];
@@ -1152,12 +857,16 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             for (int e = 0; e < 2; ++e) {
                 const int i = (u.tile * kRows + 128 * t + first + (lane >> 2) + 8 * e) / a.group;
                 node[e] = i < s.n ? i : -1;
+                if constexpr (kWindow)
+                    begin[e] = begin_of_window(a, s, node[e]);
                 ref[e] = sum[e] = 0.0f;
                 limit[e] = -INFINITY;
             }
             const int count = u.count, ctx = s.ctx;
             int p0 = u.k0 * kKeyTile;
             for (int j = 0; j < count; ++j, ++n, p0 += kKeyTile) {
+                if constexpr (kWindow)
+                    p0 = tile_at(s, u.k0 + j) * kKeyTile;
                 wait_phase(s_full, n & 1u, kFaultSoftmax);
                 __syncwarp();
                 tc_fence_after();
@@ -1175,7 +884,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_local(s_free0 + 8u * t);
-                if (p0 + kKeyTile > ctx || bads != 0u) {
+                if ((kWindow ? some_partly_seen(a, s, p0, kKeyTile) : p0 + kKeyTile > ctx) || bads != 0u) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
@@ -1183,7 +892,8 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                             out |= ((bads >> ((32 * c + k) / box)) & 1u) << k;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const uint32_t see = (seen32(a, s, node[e], p0 + 32 * c) & ~out) >> (2 * (lane & 3));
+                            const uint32_t see =
+                                (seen32<kWindow>(a, s, node[e], p0 + 32 * c, kWindow ? begin[e] : 0) & ~out) >> (2 * (lane & 3));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -1193,7 +903,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                         }
                     }
                     // the tile's V: zeros past the end, and in place of what is
-                    // not finite in drafted keys.  Every row tile looks at all
+                    // not finite in keys that a row may not see.  Every row tile looks at all
                     // of it; one that finds such a value says so (the number of
                     // the piece) before it takes it out, so that the others,
                     // who may see the zero, see the word too.
@@ -1201,7 +911,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                     const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
                     for (int i = threadIdx.x & 255; i < kKeyTile * 8; i += 256) {
                         const int key = p0 + (i >> 3);
-                        if (key < s.ctx)
+                        if (!partly_seen(a, s, key))
                             continue;
                         const uint32_t chunk = v + 16u * i;
                         uint4 w = make_uint4(0, 0, 0, 0);
@@ -1347,7 +1057,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             }
             if (threadIdx.x == 0) {
                 if (!whole)
-                    write_header<kRows>(a, at, u, unfinite);
+                    write_header<kRows, kWindow>(a, at, u, unfinite);
                 else if (u.unit == 0 && a.err != nullptr && (int64_t)max(__ldg(a.context_len + u.b), 0) + s.n > s.keys)
                     atomicAdd(a.err, 1);
             }
@@ -1361,136 +1071,6 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols<kQ>)
                      : "memory");
     }
-}
-
-// ----------------------------------------------------------- joining parts
-//
-// Block (c, y) joins rows of the unit that CTA c began and did not end: its own
-// part and those of the CTAs after it, in key order.  A thread has four columns
-// of a row; with few rows (kRows <= 32: units cut into many parts) four groups
-// of threads take every fourth part each and are joined in order at the end.  A
-// thread loads eight parts' maxima, sums and columns at once, so that the few
-// parts of a unit of many rows cost one latency (one part at a time: 27 us for 16
-// trees of 16 tokens, 42 for 8 of 64; now about 5 behind the kernel that wrote
-// them, of which launch and headers are 1.3).
-constexpr int kJoinThreads = 256;
-template <int kRows> constexpr int kJoinRows = kRows <= 32 ? 4 : 16;
-
-template <int kRows>
-__global__ void __launch_bounds__(kJoinThreads)
-k5_join(const __grid_constant__ Args a)
-{
-    constexpr int kGroups = kJoinThreads / (16 * kJoinRows<kRows>), kBatch = 8;
-    __shared__ float4 s_out[kGroups][16 * kJoinRows<kRows>];
-    __shared__ float s_top[kGroups][kJoinRows<kRows>], s_sum[kGroups][kJoinRows<kRows>];
-    pdl_trigger();
-    pdl_wait();
-    const int c = blockIdx.x;
-    const float *own = slot_of<kRows>(a, 2 * (int64_t)c + 1);
-    const Header hd = *reinterpret_cast<const Header *>(own);
-    if (hd.last == 0)
-        return;
-    const Seq s = seq_of(a, hd.b);
-    const int rt = row_tiles<kRows>(a, s);
-    const int h = hd.unit / rt, tile = hd.unit - h * rt;
-    const int r0 = blockIdx.y * kJoinRows<kRows>, parts = hd.last - c + 1;
-    if (threadIdx.x == 0 && blockIdx.y == 0 && hd.unit == 0 && a.err != nullptr &&
-        (int64_t)max(__ldg(a.context_len + hd.b), 0) + s.n > s.keys)
-        atomicAdd(a.err, 1);
-    if (tile * kRows + r0 >= s.n * a.group)
-        return;
-    const int group = threadIdx.x / (16 * kJoinRows<kRows>), col = (threadIdx.x & 15) * 4;
-    const int r = (threadIdx.x >> 4) % kJoinRows<kRows>;
-    int unfinite = 0;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float top = -INFINITY, total = 0.0f;
-    for (int k0 = group; k0 < parts; k0 += kBatch * kGroups) {
-        float m[kBatch], l[kBatch];
-        float4 y[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int k = k0 + i * kGroups;
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
-            y[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k < parts) {
-                const float *part = k == 0 ? own : slot_of<kRows>(a, 2 * (int64_t)(c + k));
-                m[i] = part[kSlotMax<kRows> + r0 + r];
-                l[i] = part[kSlotSum<kRows> + r0 + r];
-                y[i] = *reinterpret_cast<const float4 *>(part + kSlotOut<kRows> + (r0 + r) * kHeadDim + col);
-                unfinite |= reinterpret_cast<const Header *>(part)->unfinite;
-            }
-        }
-        float now = top;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            now = fmaxf(now, m[i]);
-        const float ref = now == -INFINITY ? 0.0f : now, shrink = ex2(top - ref);
-        top = now;
-        total *= shrink;
-        x.x *= shrink;
-        x.y *= shrink;
-        x.z *= shrink;
-        x.w *= shrink;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (k0 + i * kGroups >= parts)
-                break;
-            const float f = ex2(m[i] - ref);
-            total = __fmaf_rn(l[i], f, total);
-            x.x = __fmaf_rn(y[i].x, f, x.x);
-            x.y = __fmaf_rn(y[i].y, f, x.y);
-            x.z = __fmaf_rn(y[i].z, f, x.z);
-            x.w = __fmaf_rn(y[i].w, f, x.w);
-        }
-    }
-    if (kGroups > 1) {
-        s_out[group][threadIdx.x % (16 * kJoinRows<kRows>)] = x;
-        if (col == 0) {
-            s_top[group][r] = top;
-            s_sum[group][r] = total;
-        }
-        unfinite = __syncthreads_or(unfinite);
-        if (group > 0)
-            return;
-        float now = top;
-#pragma unroll
-        for (int g = 1; g < kGroups; ++g)
-            now = fmaxf(now, s_top[g][r]);
-        const float ref = now == -INFINITY ? 0.0f : now, f0 = ex2(top - ref);
-        top = now;
-        total *= f0;
-        x.x *= f0;
-        x.y *= f0;
-        x.z *= f0;
-        x.w *= f0;
-#pragma unroll
-        for (int g = 1; g < kGroups; ++g) {
-            const float f = ex2(s_top[g][r] - ref);
-            const float4 y = s_out[g][threadIdx.x];
-            total = __fmaf_rn(s_sum[g][r], f, total);
-            x.x = __fmaf_rn(y.x, f, x.x);
-            x.y = __fmaf_rn(y.y, f, x.y);
-            x.z = __fmaf_rn(y.z, f, x.z);
-            x.w = __fmaf_rn(y.w, f, x.w);
-        }
-    }
-    const int row = tile * kRows + r0 + r, i = row / a.group;
-    if (i >= s.n)
-        return;
-    const int head = h * a.group + row - i * a.group;
-    if (unfinite) {
-        x.x = add_unfinite(a, s, hd.b, h, i, col, x.x);
-        x.y = add_unfinite(a, s, hd.b, h, i, col + 1, x.y);
-        x.z = add_unfinite(a, s, hd.b, h, i, col + 2, x.z);
-        x.w = add_unfinite(a, s, hd.b, h, i, col + 3, x.w);
-    }
-    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    *reinterpret_cast<uint2 *>(a.out + (int64_t)(s.r0 + i) * a.out_row_stride + head * kHeadDim + col) =
-        make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-    if (col == 0 && a.lse != nullptr)
-        a.lse[(int64_t)(s.r0 + i) * (a.kv_heads * a.group) + head] =
-            total == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(total));
 }
 
 // Which kernel takes a call, by the average rows of a unit (only the totals are
@@ -1526,41 +1106,23 @@ size_t slot_floats(Variant v) {
     }
 }
 
-template <typename Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, bool (&configured)[64]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && configured[dev]))
-        return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64)
-        configured[dev] = true;
-    return e;
-}
-
-template <int kRows> cudaError_t launch_join(const Args &a, int ctas, cudaStream_t stream, const char **why) {
-    if (a.partial == nullptr)
-        return cudaSuccess;
-    *why = "tree attention join launch";
-    return launch_pdl(k5_join<kRows>, dim3((unsigned)ctas, kRows / kJoinRows<kRows>), dim3(kJoinThreads), 0, stream, 1, a);
-}
-
-template <int kTiles, bool kRuns>
+template <int kTiles, bool kRuns, bool kWindow>
 cudaError_t launch_small(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     static bool configured[64] = {};
-    cudaError_t e = allow_smem(k5_small<kTiles, kRuns>, kSmallSmem<kTiles>, configured);
+    cudaError_t e = allow_smem(k5_small<kTiles, kRuns, kWindow>, kSmallSmem<kTiles>, configured);
     if (e != cudaSuccess)
         return e;
-    *why = "tree attention launch";
-    e = launch_pdl(k5_small<kTiles, kRuns>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
-    return e != cudaSuccess ? e : launch_join<16 * kTiles>(a, ctas, stream, why);
+    *why = "attention launch";
+    e = launch_pdl(k5_small<kTiles, kRuns, kWindow>, dim3((unsigned)ctas), dim3(kSmallThreads), kSmallSmem<kTiles>, stream, 1, a);
+    return e != cudaSuccess ? e : launch_join<16 * kTiles, kWindow, false>(a, ctas, stream, why);
 }
 
-template <int kQ>
+template <int kQ, bool kWindow>
 cudaError_t launch_wide(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     static bool configured[64] = {};
-    cudaError_t e = allow_smem(k5_wide<kQ>, kWideSmem<kQ>, configured);
+    cudaError_t e = allow_smem(k5_wide<kQ, kWindow>, kWideSmem<kQ>, configured);
     if (e != cudaSuccess)
         return e;
     // the cache as [num_blocks, kv_heads, block_size, 128], boxes of 64 columns
@@ -1577,9 +1139,23 @@ cudaError_t launch_wide(const Args &a, int ctas, cudaStream_t stream, const char
                     ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    *why = "tree attention launch";
-    e = launch_pdl(k5_wide<kQ>, dim3((unsigned)ctas), dim3(kWideThreads<kQ>), kWideSmem<kQ>, stream, 1, map, a, box);
-    return e != cudaSuccess ? e : launch_join<128 * kQ>(a, ctas, stream, why);
+    *why = "attention launch";
+    e = launch_pdl(k5_wide<kQ, kWindow>, dim3((unsigned)ctas), dim3(kWideThreads<kQ>), kWideSmem<kQ>, stream, 1, map, a, box);
+    return e != cudaSuccess ? e : launch_join<128 * kQ, kWindow, false>(a, ctas, stream, why);
+}
+
+template <bool kWindow>
+cudaError_t launch_variant(Variant v, const Args &a, int ctas, cudaStream_t stream, const char **why)
+{
+    const bool runs = a.block_size % kChunk == 0;
+    switch (v) {
+    case kSmall16: return runs ? launch_small<1, true, kWindow>(a, ctas, stream, why)
+                               : launch_small<1, false, kWindow>(a, ctas, stream, why);
+    case kSmall32: return runs ? launch_small<2, true, kWindow>(a, ctas, stream, why)
+                               : launch_small<2, false, kWindow>(a, ctas, stream, why);
+    case kWide128: return launch_wide<1, kWindow>(a, ctas, stream, why);
+    default: return launch_wide<2, kWindow>(a, ctas, stream, why);
+    }
 }
 
 }  // namespace
@@ -1604,40 +1180,10 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
     const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
-    // (3 trees of 13 over 1500 keys, in equal ranges: 15.3 us with two tiles a CTA at
-    // least, 19.9 with four, 18.3 with one)
-    a.min_tiles = 2;
-    const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
-    const int64_t units = (p.rows * p.group / unit_rows + p.seqs) * p.kv_heads;      // at most
-    // Units of at most so many tiles are not worth a cut and a join: one token over
-    // 300 keys 6.9 us (cut 11.2), 30 single tokens over 450 to 900 15.0 (19.2); a
-    // tile of many rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of
-    // 13 over 900 17.6 whole and 16.1 cut.  With several units a CTA equal ranges
-    // of tiles spread ragged lengths better (256 tokens over 450 to 900: 77.4 whole,
-    // 73.5 cut; 64 25.9 and 27.8).
-    const int whole = v == kWide128 || v == kWide256 || units > 3 * ctas_of(v, num_sms) ? 4 : 8;
-    if ((int64_t)p.table_width * p.block_size <= whole * kKeyTile) {
-        a.partial = nullptr;
-        a.whole = true;
-    }
-    // as many CTAs as fill the GPU, or as the block table lets have work
-    const int64_t tiles = std::max<int64_t>(1, ((int64_t)p.table_width * p.block_size + kKeyTile - 1) / kKeyTile);
-    const int ctas = (int)std::min<int64_t>(ctas_of(v, num_sms), std::max<int64_t>(1, a.whole ? units : units * tiles / a.min_tiles));
-    // A CTA that goes from one unit to another loses some 10 us while the cache is
-    // streamed, six key tiles' time; counted as such, 64 sequences of 1025 to 2050
-    // keys take 43 us instead of 46, 16 trees of 16 over 8192 71.2, 74.5.  In
-    // the small kernel, with few tiles a CTA, the ranges had better begin with the
-    // units.
     const bool wide = v == kWide128 || v == kWide256;
-    a.change = wide || units * tiles >= 8 * ctas ? 6 : 0;
-    switch (v) {
-    case kSmall16: return p.block_size % kChunk == 0 ? launch_small<1, true>(a, ctas, stream, why)
-                                                     : launch_small<1, false>(a, ctas, stream, why);
-    case kSmall32: return p.block_size % kChunk == 0 ? launch_small<2, true>(a, ctas, stream, why)
-                                                     : launch_small<2, false>(a, ctas, stream, why);
-    case kWide128: return launch_wide<1>(a, ctas, stream, why);
-    default: return launch_wide<2>(a, ctas, stream, why);
-    }
+    const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
+    const int ctas = plan(a, unit_rows, wide, ctas_of(v, num_sms));
+    return p.window > 0 ? launch_variant<true>(v, a, ctas, stream, why) : launch_variant<false>(v, a, ctas, stream, why);
 }
 
 cudaError_t read_attention_faults(uint32_t *flags, bool clear)

@@ -1,7 +1,7 @@
 // Python side of the drafted tokens' calls (rc_rope_table, rc_rope_apply,
 // rc_tree_attention, rc_logits_adjust) and of those around them
-// (rc_head_norm_rope, rc_head_norm_rope_grad, rc_kv4_store, rc_kv4_load,
-// rc_kv_compact): checks torch tensors, makes the
+// (rc_window_attention, rc_kv4_attention, rc_head_norm_rope,
+// rc_head_norm_rope_grad, rc_kv4_store, rc_kv4_load, rc_kv_compact): checks torch tensors, makes the
 // output and calls the C ABI.  The other calls of the package go through ctypes, whose
 // 6 to 12 us a call these cannot afford: their kernels take 2 to 20 us.
 // Arguments come by position (rope_chain_gb300/__init__.py has the signatures
@@ -222,70 +222,123 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// What the attention calls have in common: q, row_start, context_len, block_table
+// and, beside the cache, tree_mask, scale, out, lse, err, workspace, stream (as
+// args[0] to args[3] and rest[0] to rest[6]).
+struct AttentionOperands {
+    const Tensor &q, &table;
+    const at::Device device;
+    const int64_t rows, heads, seqs;
+    int64_t words = 0;
+    const int32_t *row_start, *context_len;
+    const uint64_t *tree_mask;
+    float scale, *lse = nullptr;
+    int32_t *err;
+    void *workspace = nullptr;
+    size_t workspace_bytes = 0;
+    Tensor out;
+
+    // `cache_checked`: looks at the cache, once q and the table have been looked at.
+    template <typename Check>
+    AttentionOperands(PyObject *const *args, PyObject *const *rest, const Check &cache_checked)
+        : q(tensor(args[0], "q")), table(tensor(args[3], "block_table")), device(q.device()), rows(q.dim() == 3 ? q.size(0) : 0),
+          heads(q.dim() == 3 ? q.size(1) : 0), seqs(table.dim() == 2 ? table.size(0) : 0) {
+        TORCH_CHECK_VALUE(q.dim() == 3 && q.size(2) == 64 && q.scalar_type() == at::kBFloat16 && q.is_cuda(),
+                          "q must be a CUDA bfloat16 view [rows, num_heads, 64]");
+        TORCH_CHECK_VALUE(q.stride(2) == 1 && (heads == 1 || q.stride(1) == 64), "q needs strides (*, 64, 1)");
+        cache_checked(device);
+        TORCH_CHECK_VALUE(table.dim() == 2 && table.scalar_type() == at::kInt && table.is_cuda() &&
+                              (table.size(1) <= 1 || table.stride(1) == 1),
+                          "block_table must be CUDA int32 [seqs, width] with a contiguous last axis");
+        beside(table, device, "block_table");
+        no_gradient(q, "q");
+        if (rest[0] != Py_None) {
+            const Tensor &mask = tensor(rest[0], "tree_mask");
+            TORCH_CHECK_VALUE(mask.dim() == 2 && mask.size(0) == rows, "tree_mask must be [rows, words]");
+            words = mask.size(1);
+            TORCH_CHECK_VALUE(words > 0 || rows == 0, "tree_mask needs a word per row at least");
+        }
+        if (rest[3] != Py_None) {
+            const Tensor &t = tensor(rest[3], "lse");
+            TORCH_CHECK_VALUE(t.dim() == 2 && t.size(0) == rows && t.size(1) == heads, "lse must be [rows, num_heads]");
+            lse = const_cast<float *>(array<float>(rest[3], device, at::kFloat, 0, "lse"));
+        }
+        if (rest[5] != Py_None) {
+            const Tensor &t = tensor(rest[5], "workspace");
+            TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+            beside(t, device, "workspace");
+            workspace = t.data_ptr();
+            workspace_bytes = t.nbytes();
+        }
+        TORCH_CHECK_TYPE(args[1] != Py_None && args[2] != Py_None, "row_start and context_len must be tensors");
+        row_start = array<int32_t>(args[1], device, at::kInt, seqs + 1, "row_start");
+        context_len = array<int32_t>(args[2], device, at::kInt, seqs, "context_len");
+        tree_mask = reinterpret_cast<const uint64_t *>(array<int64_t>(rest[0], device, at::kLong, 0, "tree_mask"));
+        err = counter(rest[4], device);
+        out = output(rest[2], q, "q");
+        TORCH_CHECK_VALUE(!out.defined() || (out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64)),
+                          "out needs strides (*, 64, 1)");
+        scale = (float)number(rest[1]);
+    }
+    const int32_t *blocks() const { return static_cast<const int32_t *>(table.const_data_ptr()); }
+    int32_t table_width() const { return narrow<int32_t>(table.size(1), "width of block_table"); }
+    const uint16_t *queries() const { return static_cast<const uint16_t *>(q.const_data_ptr()); }
+    uint16_t *outputs() const { return static_cast<uint16_t *>(out.data_ptr()); }
+};
+
+// A bf16 cache.
+struct Cache {
+    const uint16_t *data;
+    int32_t blocks, heads, block_size;
+    void check(PyObject *o, at::Device device) {
+        const Tensor &cache = tensor(o, "cache");
+        TORCH_CHECK_VALUE(cache.dim() == 4 && cache.size(3) == 128 && cache.scalar_type() == at::kBFloat16 &&
+                              cache.is_cuda() && cache.is_contiguous(),
+                          "cache must be contiguous CUDA bfloat16 [num_blocks, num_kv_heads, block_size, 128]");
+        beside(cache, device, "cache");
+        no_gradient(cache, "cache");
+        data = static_cast<const uint16_t *>(cache.const_data_ptr());
+        blocks = narrow<int32_t>(cache.size(0), "num_blocks");
+        heads = narrow<int32_t>(cache.size(1), "num_kv_heads");
+        block_size = narrow<int32_t>(cache.size(2), "block_size");
+    }
+};
+
 PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     // q, row_start, context_len, block_table, cache, tree_mask, scale, out, lse,
     // err, workspace, stream
     need(n, 12);
-    const Tensor &q = tensor(args[0], "q"), &table = tensor(args[3], "block_table"), &cache = tensor(args[4], "cache");
-    TORCH_CHECK_VALUE(q.dim() == 3 && q.size(2) == 64 && q.scalar_type() == at::kBFloat16 && q.is_cuda(),
-                      "q must be a CUDA bfloat16 view [rows, num_heads, 64]");
-    const int64_t rows = q.size(0), heads = q.size(1);
-    TORCH_CHECK_VALUE(q.stride(2) == 1 && (heads == 1 || q.stride(1) == 64), "q needs strides (*, 64, 1)");
-    TORCH_CHECK_VALUE(cache.dim() == 4 && cache.size(3) == 128 && cache.scalar_type() == at::kBFloat16 &&
-                          cache.is_cuda() && cache.is_contiguous(),
-                      "cache must be contiguous CUDA bfloat16 [num_blocks, num_kv_heads, block_size, 128]");
-    TORCH_CHECK_VALUE(table.dim() == 2 && table.scalar_type() == at::kInt && table.is_cuda() &&
-                          (table.size(1) <= 1 || table.stride(1) == 1),
-                      "block_table must be CUDA int32 [seqs, width] with a contiguous last axis");
-    const int64_t seqs = table.size(0);
-    const at::Device device = q.device();
-    beside(cache, device, "cache");
-    beside(table, device, "block_table");
-    no_gradient(q, "q");
-    no_gradient(cache, "cache");
-    int64_t words = 0;
-    if (args[5] != Py_None) {
-        const Tensor &mask = tensor(args[5], "tree_mask");
-        TORCH_CHECK_VALUE(mask.dim() == 2 && mask.size(0) == rows, "tree_mask must be [rows, words]");
-        words = mask.size(1);
-        TORCH_CHECK_VALUE(words > 0 || rows == 0, "tree_mask needs a word per row at least");
-    }
-    float *lse = nullptr;
-    if (args[8] != Py_None) {
-        const Tensor &t = tensor(args[8], "lse");
-        TORCH_CHECK_VALUE(t.dim() == 2 && t.size(0) == rows && t.size(1) == heads, "lse must be [rows, num_heads]");
-        lse = const_cast<float *>(array<float>(args[8], device, at::kFloat, 0, "lse"));
-    }
-    void *workspace = nullptr;
-    size_t workspace_bytes = 0;
-    if (args[10] != Py_None) {
-        const Tensor &t = tensor(args[10], "workspace");
-        TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous(), "workspace must be a contiguous CUDA tensor");
-        beside(t, device, "workspace");
-        workspace = t.data_ptr();
-        workspace_bytes = t.nbytes();
-    }
-    TORCH_CHECK_TYPE(args[1] != Py_None && args[2] != Py_None, "row_start and context_len must be tensors");
-    const int32_t *row_start = array<int32_t>(args[1], device, at::kInt, seqs + 1, "row_start");
-    const int32_t *context_len = array<int32_t>(args[2], device, at::kInt, seqs, "context_len");
-    const int64_t *tree_mask = array<int64_t>(args[5], device, at::kLong, 0, "tree_mask");
-    int32_t *err = counter(args[9], device);
-    Tensor out = output(args[7], q, "q");
-    TORCH_CHECK_VALUE(!out.defined() || (out.stride(2) == 1 && (heads == 1 || out.stride(1) == 64)),
-                      "out needs strides (*, 64, 1)");
-    const On on(device, args[11]);
-    made(out, q);
+    Cache c;
+    AttentionOperands o(args, args + 5, [&](at::Device device) { c.check(args[4], device); });
+    const On on(o.device, args[11]);
+    made(o.out, o.q);
     const rc_status s = rc_tree_attention(
-        static_cast<const uint16_t *>(q.const_data_ptr()), q.stride(0), rows, narrow<int32_t>(heads, "num_heads"),
-        narrow<int32_t>(cache.size(1), "num_kv_heads"), row_start, narrow<int32_t>(seqs, "seqs"), context_len,
-        static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0),
-        narrow<int32_t>(table.size(1), "width of block_table"), reinterpret_cast<const uint64_t *>(tree_mask),
-        narrow<int32_t>(words, "words of tree_mask"), static_cast<const uint16_t *>(cache.const_data_ptr()),
-        narrow<int32_t>(cache.size(0), "num_blocks"), narrow<int32_t>(cache.size(2), "block_size"),
-        (float)number(args[6]), static_cast<uint16_t *>(out.data_ptr()), out.stride(0), lse, err,
-        workspace, workspace_bytes, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+        o.queries(), o.q.stride(0), o.rows, narrow<int32_t>(o.heads, "num_heads"), c.heads, o.row_start,
+        narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
+        narrow<int32_t>(o.words, "words of tree_mask"), c.data, c.blocks, c.block_size, o.scale, o.outputs(),
+        o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // q, row_start, context_len, block_table, cache, tree_mask, scale, out, lse,
+    // err, workspace, stream, window, sinks
+    need(n, 14);
+    Cache c;
+    AttentionOperands o(args, args + 5, [&](at::Device device) { c.check(args[4], device); });
+    const int32_t window = narrow<int32_t>(integer(args[12]), "window"), sinks = narrow<int32_t>(integer(args[13]), "sinks");
+    TORCH_CHECK_VALUE(window > 0 && sinks >= 0, "window must be positive, sinks not negative");
+    const On on(o.device, args[11]);
+    made(o.out, o.q);
+    const rc_status s = rc_window_attention(
+        o.queries(), o.q.stride(0), o.rows, narrow<int32_t>(o.heads, "num_heads"), c.heads, o.row_start,
+        narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
+        narrow<int32_t>(o.words, "words of tree_mask"), c.data, c.blocks, c.block_size, window, sinks, o.scale,
+        o.outputs(), o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
     END_HANDLE_TH_ERRORS
 }
 
@@ -518,6 +571,28 @@ struct Kv4 {
     }
 };
 
+PyObject *kv4_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    // q, row_start, context_len, block_table, cache, scales, tree_mask, scale, out,
+    // lse, err, workspace, stream, window, sinks
+    need(n, 15);
+    std::optional<Kv4> c;
+    AttentionOperands o(args, args + 6, [&](at::Device device) { c.emplace(args[4], args[5], device); });
+    const int32_t window = args[13] == Py_None ? 0 : narrow<int32_t>(integer(args[13]), "window");
+    const int32_t sinks = narrow<int32_t>(integer(args[14]), "sinks");
+    TORCH_CHECK_VALUE((args[13] == Py_None || window > 0) && sinks >= 0 && (window > 0 || sinks == 0),
+                      "window must be positive, or None without sinks; sinks not negative");
+    const On on(o.device, args[12]);
+    made(o.out, o.q);
+    const rc_status s = rc_kv4_attention(
+        o.queries(), o.q.stride(0), o.rows, narrow<int32_t>(o.heads, "num_heads"), c->heads, o.row_start,
+        narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
+        narrow<int32_t>(o.words, "words of tree_mask"), c->cache4, c->scales, c->blocks, c->block_size, window, sinks,
+        o.scale, o.outputs(), o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
+    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *kv4_store(PyObject *, PyObject *const *args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     // k, v, slots, cache, scales, err, stream
@@ -648,6 +723,8 @@ PyMethodDef g_methods[] = {
     {"head_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope)), METH_FASTCALL, nullptr},
     {"head_norm_rope_grad", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(head_norm_rope_grad)), METH_FASTCALL,
      nullptr},
+    {"window_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(window_attention)), METH_FASTCALL, nullptr},
+    {"kv4_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv4_attention)), METH_FASTCALL, nullptr},
     {"kv4_store", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv4_store)), METH_FASTCALL, nullptr},
     {"kv4_load", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv4_load)), METH_FASTCALL, nullptr},
     {"kv_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(kv_compact)), METH_FASTCALL, nullptr},

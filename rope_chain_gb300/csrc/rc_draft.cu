@@ -1,5 +1,5 @@
 // C ABI of the drafted tokens' operators (declared in include/rope_chain.h):
-// rotary positions, tree attention over the paged cache, logits adjustment.
+// rotary positions, attention over the paged caches, logits adjustment.
 // Arguments are checked on the host, then the kernels go on the caller's
 // stream; nothing here allocates device memory or synchronises.
 #include "rope_chain.h"
@@ -16,6 +16,120 @@ namespace {
 // Rows times heads of an attention: a row's index is 32 bits, that of the last
 // row tile's end (up to 256 rows) included.
 constexpr int64_t kMaxAttentionRows = 0x7FFFFFFFLL - 256;
+
+// The attention calls: `a` as the entry points fill it in (group and partial apart).
+rc_status attend(const char *fn, TreeAttentionLaunch a, int32_t num_heads, void *workspace, size_t workspace_bytes,
+                 cudaStream_t stream)
+{
+    const bool four = a.cache4 != nullptr;
+    if (a.kv_heads < 1 || num_heads < a.kv_heads || num_heads % a.kv_heads != 0)
+        return fail(RC_ERR_INVALID_ARG, "%s: num_heads=%d is not a positive multiple of num_kv_heads=%d",
+                    fn, num_heads, a.kv_heads);
+    if (a.rows < 0 || a.rows > kMaxAttentionRows / num_heads)
+        return fail(RC_ERR_INVALID_ARG, "%s: need rows >= 0 and rows*num_heads < 2^31 - 256", fn);
+    if (a.seqs < 1 || a.seqs >= (1 << 24))
+        return fail(RC_ERR_INVALID_ARG, "%s: seqs=%d outside [1, 2^24)", fn, a.seqs);
+    if (a.num_blocks < 1 || a.block_size < 1 || (int64_t)a.num_blocks * a.block_size >= (1LL << 31))
+        return fail(RC_ERR_INVALID_ARG,
+                    "%s: need num_blocks, block_size >= 1 and num_blocks*block_size < 2^31", fn);
+    // a logical key is a 32-bit index, a tile's end included
+    if (a.table_width < 0 || a.table_stride < 0 || a.table_stride > kMaxStride ||
+        (int64_t)a.table_width * a.block_size >= (1LL << 31) - 4096)
+        return fail(RC_ERR_INVALID_ARG, "%s: need table_width, table_stride >= 0 and table_width*block_size "
+                    "< 2^31 - 4096", fn);
+    if (!(a.scale > 0.0f) || !std::isfinite(a.scale))
+        return fail(RC_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+    const void *cache = four ? static_cast<const void *>(a.cache4) : a.cache;
+    if ((a.rows > 0 && (!a.q || !a.out)) || !cache || !aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(cache, 16))
+        return fail(RC_ERR_INVALID_ARG, "%s: q, out and the cache must be 16-byte aligned pointers", fn);
+    if (four && (!a.scales || !aligned(a.scales, 8)))
+        return fail(RC_ERR_INVALID_ARG, "%s: scales must be an 8-byte aligned pointer", fn);
+    if (!a.row_start || !a.context_len || !aligned(a.row_start, 4) || !aligned(a.context_len, 4) ||
+        (a.table_width > 0 && (!a.block_table || !aligned(a.block_table, 4))))
+        return fail(RC_ERR_INVALID_ARG, "%s: row_start, context_len and block_table must be 4-byte "
+                    "aligned pointers", fn);
+    if (a.tree_mask && (!aligned(a.tree_mask, 8) || a.mask_words < 1))
+        return fail(RC_ERR_INVALID_ARG, "%s: tree_mask must be 8-byte aligned with mask_words >= 1", fn);
+    const int64_t width = 64LL * num_heads;
+    if (a.rows <= 1)                    // the stride of an axis of length one is never used
+        a.q_row_stride = a.out_row_stride = 0;
+    if (a.q_row_stride % 8 != 0 || a.out_row_stride % 8 != 0 || a.q_row_stride < 0 || a.q_row_stride > kMaxStride ||
+        a.out_row_stride > kMaxStride || (a.rows > 1 && a.out_row_stride < width) || a.out_row_stride < 0)
+        return fail(RC_ERR_INVALID_ARG, "%s: row strides must be non-negative multiples of 8, and out's "
+                    "at least 64*num_heads", fn);
+    if ((a.lse && !aligned(a.lse, 4)) || (workspace && !aligned(workspace, 16)))
+        return fail(RC_ERR_INVALID_ARG, "%s: lse must be 4-byte and the workspace 16-byte aligned", fn);
+    if (a.rows == 0)
+        return ok();
+    const size_t out_bytes = ((a.rows - 1) * a.out_row_stride + width) * 2;
+    const Span out_span = {a.out, out_bytes}, lse_span = {a.lse, (size_t)a.rows * num_heads * 4};
+    const Span q_span = {a.q, (size_t)((a.rows - 1) * a.q_row_stride + width) * 2};
+    const size_t keys = (size_t)a.num_blocks * a.kv_heads * a.block_size;
+    const Span cache_span = {cache, keys * (four ? 64 : 256)}, scales_span = {a.scales, keys * 8};
+    const Span start_span = {a.row_start, ((size_t)a.seqs + 1) * 4}, len_span = {a.context_len, (size_t)a.seqs * 4};
+    const Span table_span = {a.block_table,
+                             a.table_width > 0 ? (size_t)((a.seqs - 1) * a.table_stride + a.table_width) * 4 : (size_t)0};
+    const Span mask_span = {a.tree_mask, (size_t)a.rows * a.mask_words * 8}, err_span = {a.err, 4};
+    auto reads = [&](const Span &written) {
+        return overlap(written, {q_span, cache_span, scales_span, start_span, len_span, table_span, mask_span, err_span});
+    };
+    if (reads(out_span) || reads(lse_span) || overlap(lse_span, {out_span}) || !aligned(a.err, 4))
+        return fail(RC_ERR_INVALID_ARG, "%s: out or lse overlaps another operand, or err is not 4-byte aligned", fn);
+    const int sms = num_sms_current();
+    if (sms <= 0)
+        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
+    a.group = num_heads / a.kv_heads;
+    if (workspace) {
+        const size_t need = four ? kv4_attention_workspace(a.rows, a.seqs, a.group, sms)
+                                 : tree_attention_workspace(a.rows, a.seqs, a.group, sms);
+        if (workspace_bytes < need)
+            return fail(RC_ERR_INVALID_ARG, "%s: the workspace holds %zu bytes, these sizes take %zu", fn,
+                        workspace_bytes, need);
+        if (reads({workspace, need}) || overlap({workspace, need}, {out_span, lse_span}))
+            return fail(RC_ERR_INVALID_ARG, "%s: the workspace overlaps an operand", fn);
+    }
+    a.partial = static_cast<float *>(workspace);
+    const char *why = "launch";
+    const cudaError_t e = four ? launch_kv4_attention(a, sms, stream, &why) : launch_tree_attention(a, sms, stream, &why);
+    return e == cudaSuccess ? ok() : cuda_fail(e, why);
+}
+
+// The operands that the attention calls have in common.
+TreeAttentionLaunch attention_launch(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_kv_heads,
+                                     const int32_t *row_start, int32_t seqs, const int32_t *context_len,
+                                     const int32_t *block_table, int64_t table_stride, int32_t table_width,
+                                     const uint64_t *tree_mask, int32_t mask_words, int32_t num_blocks,
+                                     int32_t block_size, float scale, uint16_t *out, int64_t out_row_stride, float *lse,
+                                     int32_t *err)
+{
+    TreeAttentionLaunch a{};
+    a.q = q;
+    a.q_row_stride = q_row_stride;
+    a.rows = rows;
+    a.kv_heads = num_kv_heads;
+    a.seqs = seqs;
+    a.row_start = row_start;
+    a.context_len = context_len;
+    a.block_table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.tree_mask = tree_mask;
+    a.mask_words = mask_words;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.scale = scale;
+    a.out = out;
+    a.out_row_stride = out_row_stride;
+    a.lse = lse;
+    a.err = err;
+    return a;
+}
+
+// Sizes for which an attention has a workspace.
+bool attention_sizes(int64_t rows, int32_t seqs, int32_t num_heads, int32_t num_kv_heads) {
+    return rows >= 1 && seqs >= 1 && num_kv_heads >= 1 && num_heads >= num_kv_heads && num_heads % num_kv_heads == 0 &&
+           rows <= kMaxAttentionRows / num_heads;
+}
 
 }  // namespace
 
@@ -171,11 +285,10 @@ rc_status rc_rope_apply(const void *x, int32_t dtype, int64_t x_row_stride, int6
 size_t rc_tree_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_heads,
                                         int32_t num_kv_heads)
 {
-    if (rows < 1 || seqs < 1 || num_kv_heads < 1 || num_heads < num_kv_heads ||
-        num_heads % num_kv_heads != 0 || rows > kMaxAttentionRows / num_heads)
+    if (!attention_sizes(rows, seqs, num_heads, num_kv_heads))
         return 0;
     const int sms = num_sms_current();
-    return sms > 0 ? rc::tree_attention_workspace(rows, seqs, num_heads / num_kv_heads, sms) : 0;
+    return sms > 0 ? tree_attention_workspace(rows, seqs, num_heads / num_kv_heads, sms) : 0;
 }
 
 rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
@@ -187,93 +300,64 @@ rc_status rc_tree_attention(const uint16_t *q, int64_t q_row_stride, int64_t row
                             float *lse, int32_t *err, void *workspace, size_t workspace_bytes,
                             cudaStream_t stream)
 {
-    const char *fn = "rc_tree_attention";
-    if (num_kv_heads < 1 || num_heads < num_kv_heads || num_heads % num_kv_heads != 0)
-        return fail(RC_ERR_INVALID_ARG, "%s: num_heads=%d is not a positive multiple of num_kv_heads=%d",
-                    fn, num_heads, num_kv_heads);
-    if (rows < 0 || rows > kMaxAttentionRows / num_heads)
-        return fail(RC_ERR_INVALID_ARG, "%s: need rows >= 0 and rows*num_heads < 2^31 - 256", fn);
-    if (seqs < 1 || seqs >= (1 << 24))
-        return fail(RC_ERR_INVALID_ARG, "%s: seqs=%d outside [1, 2^24)", fn, seqs);
-    if (num_blocks < 1 || block_size < 1 || (int64_t)num_blocks * block_size >= (1LL << 31))
-        return fail(RC_ERR_INVALID_ARG,
-                    "%s: need num_blocks, block_size >= 1 and num_blocks*block_size < 2^31", fn);
-    // a logical key is a 32-bit index, a tile's end included
-    if (table_width < 0 || table_stride < 0 || table_stride > kMaxStride ||
-        (int64_t)table_width * block_size >= (1LL << 31) - 4096)
-        return fail(RC_ERR_INVALID_ARG, "%s: need table_width, table_stride >= 0 and table_width*block_size "
-                    "< 2^31 - 4096", fn);
-    if (!(scale > 0.0f) || !std::isfinite(scale))
-        return fail(RC_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
-    if ((rows > 0 && (!q || !out)) || !cache || !aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16))
-        return fail(RC_ERR_INVALID_ARG, "%s: q, out and cache must be 16-byte aligned pointers", fn);
-    if (!row_start || !context_len || !aligned(row_start, 4) || !aligned(context_len, 4) ||
-        (table_width > 0 && (!block_table || !aligned(block_table, 4))))
-        return fail(RC_ERR_INVALID_ARG, "%s: row_start, context_len and block_table must be 4-byte "
-                    "aligned pointers", fn);
-    if (tree_mask && (!aligned(tree_mask, 8) || mask_words < 1))
-        return fail(RC_ERR_INVALID_ARG, "%s: tree_mask must be 8-byte aligned with mask_words >= 1", fn);
-    const int64_t width = 64LL * num_heads;
-    if (rows <= 1)                      // the stride of an axis of length one is never used
-        q_row_stride = out_row_stride = 0;
-    if (q_row_stride % 8 != 0 || out_row_stride % 8 != 0 || q_row_stride < 0 || q_row_stride > kMaxStride ||
-        out_row_stride > kMaxStride || (rows > 1 && out_row_stride < width) || out_row_stride < 0)
-        return fail(RC_ERR_INVALID_ARG, "%s: row strides must be non-negative multiples of 8, and out's "
-                    "at least 64*num_heads", fn);
-    if ((lse && !aligned(lse, 4)) || (workspace && !aligned(workspace, 16)))
-        return fail(RC_ERR_INVALID_ARG, "%s: lse must be 4-byte and the workspace 16-byte aligned", fn);
-    if (rows == 0)
-        return ok();
-    const size_t out_bytes = ((rows - 1) * out_row_stride + width) * 2;
-    const Span out_span = {out, out_bytes}, lse_span = {lse, (size_t)rows * num_heads * 4};
-    const Span q_span = {q, (size_t)((rows - 1) * q_row_stride + width) * 2};
-    const Span cache_span = {cache, (size_t)num_blocks * num_kv_heads * block_size * 128 * 2};
-    const Span start_span = {row_start, ((size_t)seqs + 1) * 4}, len_span = {context_len, (size_t)seqs * 4};
-    const Span table_span = {block_table, table_width > 0 ? (size_t)((seqs - 1) * table_stride + table_width) * 4 : (size_t)0};
-    const Span mask_span = {tree_mask, (size_t)rows * mask_words * 8}, err_span = {err, 4};
-    auto reads = [&](const Span &written) {
-        return overlap(written, {q_span, cache_span, start_span, len_span, table_span, mask_span, err_span});
-    };
-    if (reads(out_span) || reads(lse_span) || overlap(lse_span, {out_span}) || !aligned(err, 4))
-        return fail(RC_ERR_INVALID_ARG, "%s: out or lse overlaps another operand, or err is not 4-byte aligned", fn);
-    const int sms = num_sms_current();
-    if (sms <= 0)
-        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
-    const int32_t group = num_heads / num_kv_heads;
-    if (workspace) {
-        const size_t need = rc::tree_attention_workspace(rows, seqs, group, sms);
-        if (workspace_bytes < need)
-            return fail(RC_ERR_INVALID_ARG, "%s: the workspace holds %zu bytes, these sizes take %zu", fn,
-                        workspace_bytes, need);
-        if (reads({workspace, need}) || overlap({workspace, need}, {out_span, lse_span}))
-            return fail(RC_ERR_INVALID_ARG, "%s: the workspace overlaps an operand", fn);
-    }
-    rc::TreeAttentionLaunch a{};
-    a.q = q;
-    a.q_row_stride = q_row_stride;
-    a.rows = rows;
-    a.kv_heads = num_kv_heads;
-    a.group = group;
-    a.seqs = seqs;
-    a.row_start = row_start;
-    a.context_len = context_len;
-    a.block_table = block_table;
-    a.table_stride = table_stride;
-    a.table_width = table_width;
-    a.tree_mask = tree_mask;
-    a.mask_words = mask_words;
+    TreeAttentionLaunch a = attention_launch(q, q_row_stride, rows, num_kv_heads, row_start, seqs, context_len, block_table,
+                                             table_stride, table_width, tree_mask, mask_words, num_blocks, block_size, scale,
+                                             out, out_row_stride, lse, err);
     a.cache = cache;
-    a.num_blocks = num_blocks;
-    a.block_size = block_size;
-    a.scale = scale;
-    a.out = out;
-    a.out_row_stride = out_row_stride;
-    a.lse = lse;
-    a.err = err;
-    a.partial = static_cast<float *>(workspace);
-    const char *why = "launch";
-    const cudaError_t e = rc::launch_tree_attention(a, sms, stream, &why);
-    return e == cudaSuccess ? ok() : cuda_fail(e, why);
+    return attend("rc_tree_attention", a, num_heads, workspace, workspace_bytes, stream);
+}
+
+rc_status rc_window_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
+                              int32_t num_kv_heads, const int32_t *row_start, int32_t seqs,
+                              const int32_t *context_len, const int32_t *block_table,
+                              int64_t table_stride, int32_t table_width, const uint64_t *tree_mask,
+                              int32_t mask_words, const uint16_t *cache, int32_t num_blocks,
+                              int32_t block_size, int32_t window, int32_t sinks, float scale,
+                              uint16_t *out, int64_t out_row_stride, float *lse, int32_t *err,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const char *fn = "rc_window_attention";
+    if (window < 1 || sinks < 0)
+        return fail(RC_ERR_INVALID_ARG, "%s: need window >= 1 and sinks >= 0", fn);
+    TreeAttentionLaunch a = attention_launch(q, q_row_stride, rows, num_kv_heads, row_start, seqs, context_len, block_table,
+                                             table_stride, table_width, tree_mask, mask_words, num_blocks, block_size, scale,
+                                             out, out_row_stride, lse, err);
+    a.cache = cache;
+    a.window = window;
+    a.sinks = sinks;
+    return attend(fn, a, num_heads, workspace, workspace_bytes, stream);
+}
+
+size_t rc_kv4_attention_workspace_size(int64_t rows, int32_t seqs, int32_t num_heads, int32_t num_kv_heads)
+{
+    if (!attention_sizes(rows, seqs, num_heads, num_kv_heads))
+        return 0;
+    const int sms = num_sms_current();
+    return sms > 0 ? kv4_attention_workspace(rows, seqs, num_heads / num_kv_heads, sms) : 0;
+}
+
+rc_status rc_kv4_attention(const uint16_t *q, int64_t q_row_stride, int64_t rows, int32_t num_heads,
+                           int32_t num_kv_heads, const int32_t *row_start, int32_t seqs,
+                           const int32_t *context_len, const int32_t *block_table, int64_t table_stride,
+                           int32_t table_width, const uint64_t *tree_mask, int32_t mask_words,
+                           const uint8_t *cache4, const uint16_t *scales, int32_t num_blocks,
+                           int32_t block_size, int32_t window, int32_t sinks, float scale,
+                           uint16_t *out, int64_t out_row_stride, float *lse, int32_t *err,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const char *fn = "rc_kv4_attention";
+    if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
+        return fail(RC_ERR_INVALID_ARG, "%s: need window >= 0 (0: none) and sinks >= 0 (0 without a window)", fn);
+    if (!cache4)
+        return fail(RC_ERR_INVALID_ARG, "%s: cache4 must not be NULL", fn);
+    TreeAttentionLaunch a = attention_launch(q, q_row_stride, rows, num_kv_heads, row_start, seqs, context_len, block_table,
+                                             table_stride, table_width, tree_mask, mask_words, num_blocks, block_size, scale,
+                                             out, out_row_stride, lse, err);
+    a.cache4 = cache4;
+    a.scales = scales;
+    a.window = window;
+    a.sinks = sinks;
+    return attend(fn, a, num_heads, workspace, workspace_bytes, stream);
 }
 
 rc_status rc_logits_adjust(const void *logits, int32_t dtype, int64_t row_stride, int64_t rows,

@@ -71,6 +71,8 @@ struct TreeAttentionLaunch {
     const uint64_t *tree_mask;               // [rows, mask_words] or NULL (chain)
     int32_t mask_words;
     const uint16_t *cache;                   // bf16 [num_blocks, kv_heads, block_size, 128]
+    const uint8_t *cache4;                   // or in 4 bits, [num_blocks, kv_heads, block_size, 64]
+    const uint16_t *scales;                  // with its scales, bf16 [num_blocks, kv_heads, block_size, 4]
     int32_t num_blocks, block_size;
     float scale;
     uint16_t *out;                           // bf16 [rows, heads, 64], head stride 64
@@ -78,6 +80,7 @@ struct TreeAttentionLaunch {
     float *lse;                              // [rows, heads] or NULL
     int32_t *err;
     float *partial;                          // workspace, or NULL: no split
+    int32_t window, sinks;                   // keys that count, the last and the first (window 0: all)
 };
 
 // Workspace bytes with which the keys are split over the GPU.
@@ -85,6 +88,10 @@ size_t tree_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int n
 
 cudaError_t launch_tree_attention(const TreeAttentionLaunch &a, int num_sms, cudaStream_t stream,
                                   const char **why);
+
+// The same over a cache in 4 bits.
+size_t kv4_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms);
+cudaError_t launch_kv4_attention(const TreeAttentionLaunch &a, int num_sms, cudaStream_t stream, const char **why);
 
 // Sticky device fault bits of the tree attention (current device).
 cudaError_t read_attention_faults(uint32_t *flags, bool clear);

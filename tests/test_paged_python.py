@@ -46,7 +46,17 @@ def compact_operands():
                 err=fake(1, dtype=I32))
 
 
-CALLS = {"head_norm_rope": norm_operands, "head_norm_rope_grad": norm_grad_operands, "kv4_store": store_operands,
+def window_operands():
+    return dict(q=fake(4, 8, 64), row_start=fake(3, dtype=I32), context_len=fake(2, dtype=I32), block_table=fake(2, 5, dtype=I32),
+                cache=fake(9, 2, 16, 128), tree_mask=fake(4, 1, dtype=I64), out=fake(4, 8, 64), lse=fake(4, 8, dtype=F32),
+                err=fake(1, dtype=I32), workspace=fake(1 << 24, dtype=U8), window=5, sinks=1)
+
+
+def kv4_attention_operands():
+    return dict(window_operands(), cache=fake(9, 2, 16, 64, dtype=U8), scales=fake(9, 2, 16, 4))
+
+
+CALLS = {"window_attention": window_operands, "kv4_attention": kv4_attention_operands, "head_norm_rope": norm_operands, "head_norm_rope_grad": norm_grad_operands, "kv4_store": store_operands,
          "kv4_load": load_operands, "kv_compact": compact_operands}
 TENSORS = [(c, n) for c, make in CALLS.items() for n, t in make().items() if isinstance(t, torch.Tensor)]
 # (a tensor without memory sets up the context of its GPU where there are any)
@@ -135,3 +145,29 @@ def test_kv4_output(change):
 def test_compact_shapes_and_types(change):
     with pytest.raises((TypeError, ValueError)):
         rc.kv_compact(**{**compact_operands(), **change})
+
+
+@pytest.mark.parametrize("call", ["window_attention", "kv4_attention"])
+@pytest.mark.parametrize("change", [
+    dict(q=fake(4, 8, 32)), dict(q=fake(4, 8, 64, dtype=F32)), dict(q=fake(4, 512)), dict(q=fake(8, 4, 64).transpose(0, 1)),
+    dict(row_start=fake(2, dtype=I32)), dict(row_start=None), dict(context_len=fake(2, dtype=I64)), dict(block_table=fake(2, 5, dtype=I64)),
+    dict(block_table=fake(2, 10, dtype=I32)[:, ::2]), dict(cache=fake(9, 2, 16, 32)), dict(cache=fake(9, 2, 16)),
+    dict(tree_mask=fake(3, 1, dtype=I64)), dict(tree_mask=fake(4, 0, dtype=I64)), dict(tree_mask=fake(4, 1, dtype=I32)),
+    dict(out=fake(4, 8, 32)), dict(out=fake(8, 4, 64).transpose(0, 1)), dict(lse=fake(4, 7, dtype=F32)), dict(lse=fake(4, 8)),
+    dict(workspace=fake(64, 2, dtype=U8).t()), dict(window="wide"), dict(window=2 ** 31), dict(sinks=2 ** 31), dict(sinks=None)])
+def test_attention_shapes_and_types(call, change):
+    with pytest.raises((TypeError, ValueError)):
+        getattr(rc, call)(**{**CALLS[call](), **change})
+
+
+@pytest.mark.parametrize("change", [dict(scales=fake(9, 2, 16, 2)), dict(scales=fake(9, 2, 16, 4, dtype=F32)), dict(scales=fake(9, 2, 15, 4)),
+                                    dict(window=0), dict(window=-1), dict(sinks=-1), dict(window=None)])
+def test_kv4_attention_operands(change):
+    with pytest.raises((TypeError, ValueError)):
+        rc.kv4_attention(**{**kv4_attention_operands(), **change})
+
+
+@pytest.mark.parametrize("change", [dict(window=0), dict(window=-3), dict(sinks=-1)])
+def test_windows(change):
+    with pytest.raises(ValueError):
+        rc.window_attention(**{**window_operands(), **change})

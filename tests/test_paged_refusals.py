@@ -134,3 +134,46 @@ def test_compact_refusals(lib):
                  dict(new=first), dict(err=first), dict(new=LENS), dict(new=PATH), dict(new=START), dict(new=COUNT), dict(new=TABLE),
                  dict(new=ERR)):
         assert compact(lib, **over) == BAD, over
+
+
+Q, RS, CL, BT, TM, CA, S4 = 0x1000000, 0x10000, 0x20000, 0x30000, 0x40000, 0x2000000, 0x3000000
+ATTEND = dict(q=Q, qs=512, rows=4, heads=8, kv=2, rs=RS, seqs=2, cl=CL, bt=BT, ts=4, tw=4, tm=TM, mw=1, ca=CA, sc=S4, nb=8, bs=16,
+              window=5, sinks=1, scale=0.125, out=OUT, os=512, lse=None, ws=None, wb=0)
+
+
+def window(lib, **over):
+    a = {**ATTEND, **over}
+    return lib.rc_window_attention(A(a["q"]), a["qs"], a["rows"], a["heads"], a["kv"], A(a["rs"]), a["seqs"], A(a["cl"]), A(a["bt"]),
+                                   a["ts"], a["tw"], A(a["tm"]), a["mw"], A(a["ca"]), a["nb"], a["bs"], a["window"], a["sinks"],
+                                   a["scale"], A(a["out"]), a["os"], A(a["lse"]), None, A(a["ws"]), a["wb"], None)
+
+
+def attend4(lib, **over):
+    a = {**ATTEND, **over}
+    return lib.rc_kv4_attention(A(a["q"]), a["qs"], a["rows"], a["heads"], a["kv"], A(a["rs"]), a["seqs"], A(a["cl"]), A(a["bt"]),
+                                a["ts"], a["tw"], A(a["tm"]), a["mw"], A(a["ca"]), A(a["sc"]), a["nb"], a["bs"], a["window"],
+                                a["sinks"], a["scale"], A(a["out"]), a["os"], A(a["lse"]), None, A(a["ws"]), a["wb"], None)
+
+
+@pytest.mark.parametrize("call", [window, attend4])
+def test_attention_refusals(lib, call):
+    for over in (dict(heads=7), dict(kv=0), dict(heads=1, kv=2), dict(rows=-1), dict(rows=1 << 29), dict(seqs=0), dict(seqs=1 << 24),
+                 dict(nb=0), dict(bs=0), dict(nb=1 << 20, bs=1 << 11), dict(tw=-1), dict(ts=-1), dict(tw=1 << 20, bs=1 << 11),
+                 dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(q=Q + 8),
+                 dict(out=None), dict(out=OUT + 2), dict(ca=None), dict(ca=CA + 4), dict(rs=None), dict(cl=None), dict(bt=None),
+                 dict(tm=TM + 4), dict(mw=0), dict(qs=516), dict(qs=-512), dict(os=448), dict(os=516), dict(lse=0x50002),
+                 dict(ws=WS + 8, wb=1 << 30), dict(out=Q), dict(out=Q + 512), dict(out=CA), dict(lse=OUT), dict(window=-1),
+                 dict(sinks=-1), dict(window=0, sinks=1), dict(out=CL & ~15), dict(lse=TM)):
+        assert call(lib, **over) == BAD, over
+    assert call(lib, rows=0, q=None, out=None, tm=None, bt=None, tw=0) == OK
+    rows = (1 << 31) - 1
+    assert call(lib, rows=rows, heads=1, kv=1, seqs=1, qs=0, os=64, out=1 << 60, tm=None) == BAD
+
+
+def test_attention_of_each_format(lib):
+    assert window(lib, window=0, sinks=0) == BAD
+    for over in (dict(sc=None), dict(sc=S4 + 4), dict(out=S4), dict(lse=S4)):
+        assert attend4(lib, **over) == BAD, over
+    assert attend4(lib, rows=0, window=0, sinks=0) == OK
+    for sizes in ((0, 1, 8, 8), (4, 0, 8, 8), (4, 1, 8, 3), (4, 1, 0, 0), (1 << 30, 1, 8, 8)):
+        assert lib.rc_kv4_attention_workspace_size(*sizes) == 0
