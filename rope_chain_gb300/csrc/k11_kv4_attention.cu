@@ -21,7 +21,7 @@
 // no value is infinite or NaN, and what a row does not see stays away by a weight of 0.
 //
 // Every warp streams its own 16 of a tile's 128 keys from the cache into registers,
-// kStages chunks ahead, with a running maximum, sum and output of its own; the warps'
+// kAhead chunks ahead, with a running maximum, sum and output of its own; the warps'
 // parts are joined at a unit's end.
 #include "rc_attention.cuh"
 #include "rc_kv4.cuh"
@@ -52,11 +52,11 @@ struct Chunk {
     uint2 k[2];                        // keys g, g + 8
     uint32_t v[4];                     // keys 2c, 2c + 1, 2c + 8, 2c + 9
     uint2 scale;                       // lanes 0 to 15: of key `lane`, K's two and V's two
-    uint32_t real;                     // which keys exist
+    int32_t at;                        // kRuns: its number in the cache, -1 without a block; else which keys exist
 };
 
-// Chunks in flight, and CTAs on an SM.
-template <int kTiles> constexpr int kStages = kTiles == 4 ? 2 : 3;
+// Chunks in flight beside the one that is worked on, and CTAs on an SM.
+template <int kTiles> constexpr int kAhead = kTiles == 4 ? 2 : 3;
 template <int kTiles> constexpr int kPerSm = kTiles == 1 ? 2 : 1;
 
 // kTiles: tiles of eight rows.  kRuns: blocks hold a multiple of 16 keys, so a chunk
@@ -107,7 +107,8 @@ k11_attention(const __grid_constant__ Args a)
                     begin[m][f] = begin_of_window(a, s, node[m][f]);
             }
         }
-        // o[m][t][2e + f]: row 2c + f, element 8g + 2t + e
+        // o[m][t][2e + f]: row 2c + f, element 8g + 2t + e.  ref as in k5_small; limit is of
+        // the scores before their factor
         float o[kTiles][4][4], ref[kTiles][2], limit[kTiles][2], sum[kTiles][2];
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -132,41 +133,45 @@ k11_attention(const __grid_constant__ Args a)
             return j + (kRuns ? lane : 0) < count && p < s.keys ? block_of(a, b, p) : -1;
         };
         int32_t entry = table_entry(0);
-        int64_t from = -1;                              // the row of this lane's chunk or key
+        // kRuns: the number of this lane's chunk of 16 rows (a cache holds fewer than
+        // 2^31 of them: it would be 2 TB); else the row of its key
+        using Where = std::conditional_t<kRuns, int32_t, int64_t>;
+        Where from = -1;
         auto place = [&](int j) {
             const int p = lane_key(j);
             const bool wanted = j + (kRuns ? lane : 0) < count && p < s.keys && some_seen(a, s, p, kRuns ? kChunk : 1);
             const bool there = wanted && entry >= 0 && entry < a.num_blocks;
             const uint32_t bs = (uint32_t)a.block_size;
-            from = there ? ((int64_t)entry * a.kv_heads + h) * bs + (uint32_t)p % bs : -1;
+            const int64_t row = ((int64_t)entry * a.kv_heads + h) * bs + (uint32_t)p % bs;
+            from = there ? (Where)(kRuns ? row / kChunk : row) : (Where)-1;
             if (wanted && !there && (kRuns || lane < 16) && unit == 0 && a.err != nullptr &&
                 first_needed(a, s, p, kRuns ? min(kChunk, s.keys - p) : 1))
                 atomicAdd(a.err, 1);
         };
         // (rows that do not exist are read from row 0, or lie in a block that does:
         // their values are finite whatever is there, their weights 0)
+        const uint8_t *const k_at = a.cache4 + g * kKv4Row + 8 * c, *const v_at = a.cache4 + 2 * c * kKv4Row + 32 + 4 * g;
+        const uint16_t *const scale_at = a.scales + (lane & 15) * kKv4Scales;
         auto load = [&](int j, Chunk &x) {
-            if (kRuns) {
+            if constexpr (kRuns) {
                 if ((j & 31) == 0) {
                     place(j);
                     entry = table_entry(j + 32);
                 }
-                const int64_t first = __shfl_sync(0xFFFFFFFFu, from, j & 31);
-                const int keys = first < 0 ? 0 : min(kChunk, s.keys - first_key(j));
-                x.real = (1u << keys) - 1u;
-                const int64_t row = max(first, (int64_t)0);
-                const uint8_t *p = a.cache4 + row * kKv4Row;
+                x.at = __shfl_sync(0xFFFFFFFFu, from, j & 31);
+                const uint32_t i = (uint32_t)max(x.at, 0);
+                const uint8_t *const k = k_at + (uint64_t)i * (kChunk * kKv4Row), *const v = v_at + (uint64_t)i * (kChunk * kKv4Row);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    x.k[e] = __ldg(reinterpret_cast<const uint2 *>(p + (g + 8 * e) * kKv4Row) + c);
+                    x.k[e] = __ldg(reinterpret_cast<const uint2 *>(k + 8 * e * kKv4Row));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x.v[e] = __ldg(reinterpret_cast<const uint32_t *>(p + (2 * c + (e & 1) + 8 * (e >> 1)) * kKv4Row) + 8 + g);
-                x.scale = __ldg(reinterpret_cast<const uint2 *>(a.scales + row * kKv4Scales) + (lane & 15));
+                    x.v[e] = __ldg(reinterpret_cast<const uint32_t *>(v + ((e & 1) + 8 * (e >> 1)) * kKv4Row));
+                x.scale = __ldg(reinterpret_cast<const uint2 *>(scale_at + (uint64_t)i * (kChunk * kKv4Scales)));
             } else {
                 place(j);
                 entry = table_entry(j + 1);
-                x.real = __ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu;
+                x.at = (int32_t)(__ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu);
                 const int64_t row = max(from, (int64_t)0);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
@@ -182,7 +187,12 @@ k11_attention(const __grid_constant__ Args a)
         auto work = [&](int j, const Chunk &x) {
             const int p0 = first_key(j);
             // scales: of this lane's two keys of K, twice each; of its pairs of keys of V
-            const uint32_t ks = kv4_scales(x.scale.x), vs = kv4_scales(x.scale.y);
+            uint32_t ks = x.scale.x & 0xFFF0FFF0u, vs = x.scale.y & 0xFFF0FFF0u;
+            constexpr uint32_t kMost = kKv4MostScale | kKv4MostScale << 16;
+            if (__any_sync(0xFFFFFFFFu, __vmaxu2(__vmaxu2(ks & 0x7FFF7FFFu, vs & 0x7FFF7FFFu), kMost) != kMost)) {
+                ks = kv4_scales(ks);
+                vs = kv4_scales(vs);
+            }
             uint32_t k_scale[2], v_scale[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -207,13 +217,14 @@ k11_attention(const __grid_constant__ Args a)
                 for (int m = 0; m < kTiles; ++m)
                     mma16816(t[m], kf, qf[m][k][0], qf[m][k][1]);
             }
-            if (x.real != 0xFFFFu || some_partly_seen(a, s, p0, kChunk)) {
+            if ((kRuns ? x.at < 0 : x.at != 0xFFFF) || some_partly_seen(a, s, p0, kChunk)) {
+                const uint32_t real = !kRuns ? (uint32_t)x.at : x.at < 0 ? 0u : (1u << max(0, min(kChunk, s.keys - p0))) - 1u;
 #pragma unroll
                 for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int in = g + 8 * (e >> 1);
-                        if (!((x.real >> in) & 1u) || !sees_key(a, s, node[m][e & 1], p0 + in, kWindow ? begin[m][e & 1] : 0))
+                        if (!((real >> in) & 1u) || !sees_key(a, s, node[m][e & 1], p0 + in, kWindow ? begin[m][e & 1] : 0))
                             t[m][e] = -INFINITY;
                     }
             }
@@ -223,7 +234,7 @@ k11_attention(const __grid_constant__ Args a)
             for (int m = 0; m < kTiles; ++m)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    now[m][f] = fmaxf(t[m][f], t[m][2 + f]) * a.scale_log2;
+                    now[m][f] = fmaxf(t[m][f], t[m][2 + f]);
                     grew |= now[m][f] > limit[m][f];
                 }
             if (__any_sync(0xFFFFFFFFu, grew)) {
@@ -236,9 +247,10 @@ k11_attention(const __grid_constant__ Args a)
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
                         if (y > limit[m][f]) {
-                            const float shrink = limit[m][f] == -INFINITY ? 0.0f : ex2(-ref[m][f] - y);
-                            ref[m][f] = -y;
-                            limit[m][f] = y + kGrow;
+                            const float shrink =
+                                limit[m][f] == -INFINITY ? 0.0f : ex2(__fmaf_rn(-y, a.scale_log2, -ref[m][f]));
+                            ref[m][f] = -(y * a.scale_log2);
+                            limit[m][f] = y + a.grow;
                             sum[m][f] *= shrink;
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
@@ -278,20 +290,20 @@ k11_attention(const __grid_constant__ Args a)
                     mma16816(o[m][n], vf, pf[m][0], pf[m][1]);
             }
         };
-        Chunk ring[kStages<kTiles>];
+        constexpr int kBuffers = kAhead<kTiles> + 1;
+        Chunk ring[kBuffers];
 #pragma unroll
-        for (int i = 0; i < kStages<kTiles>; ++i)
+        for (int i = 0; i < kAhead<kTiles>; ++i)
             if (i < count)
                 load(i, ring[i]);
-        for (int j = 0; j < count; j += kStages<kTiles>) {
+        for (int j = 0; j < count; j += kBuffers) {
 #pragma unroll
-            for (int i = 0; i < kStages<kTiles>; ++i) {
+            for (int i = 0; i < kBuffers; ++i) {
                 if (j + i >= count)
                     break;
-                const Chunk now = ring[i];
-                if (j + i + kStages<kTiles> < count)
-                    load(j + i + kStages<kTiles>, ring[i]);
-                work(j + i, now);
+                if (j + i + kAhead<kTiles> < count)
+                    load(j + i + kAhead<kTiles>, ring[(i + kAhead<kTiles>) % kBuffers]);
+                work(j + i, ring[i]);
             }
         }
 
@@ -416,6 +428,7 @@ cudaError_t launch_kv4_attention(const TreeAttentionLaunch &p, int num_sms, cuda
     Args a{};
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
+    a.grow = kGrow / a.scale_log2;
     const Variant v = variant_for(p.rows, p.seqs, p.group);
     const int ctas = plan(a, 8 * tiles_of(v), false, ctas_of(v, num_sms));
     if (p.block_size % kChunk == 0)

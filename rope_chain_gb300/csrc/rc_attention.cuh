@@ -16,6 +16,7 @@ constexpr float kGrow = 8.0f;          // log2: growth of a row's maximum at whi
 
 struct Args : TreeAttentionLaunch {
     float scale_log2;                  // scale * log2 e
+    float grow;                        // kGrow / scale_log2: in scores before that factor
     int32_t min_tiles;                 // fewest key tiles a CTA is given
     bool whole;                        // units are not cut
     int32_t change;                    // going to another unit, in key tiles' time
