@@ -39,6 +39,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// D = A B
+__device__ __forceinline__ void mma16816_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // The transpose of an 8 x 8 matrix of 16-bit elements (lane l: row l / 4, columns
 // 2 (l % 4) and the next).
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -201,11 +208,6 @@ k11_attention(const __grid_constant__ Args a)
                                          g < 4 ? 0x5410 : 0x7632);
             }
             float t[kTiles][4];                         // keys g, g, g + 8, g + 8; rows 2c, 2c + 1
-#pragma unroll
-            for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    t[m][e] = 0.0f;
             const uint32_t ko[2] = {kv4_offsets(k_scale[0]), kv4_offsets(k_scale[1])};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -214,8 +216,12 @@ k11_attention(const __grid_constant__ Args a)
                 for (int e = 0; e < 4; ++e)
                     kf[e] = fma_bf16x2(kv4_pair(k < 2 ? x.k[e & 1].x : x.k[e & 1].y, 2 * (k & 1) + (e >> 1)), k_scale[e & 1], ko[e & 1]);
 #pragma unroll
-                for (int m = 0; m < kTiles; ++m)
-                    mma16816(t[m], kf, qf[m][k][0], qf[m][k][1]);
+                for (int m = 0; m < kTiles; ++m) {
+                    if (k == 0)
+                        mma16816_new(t[m], kf, qf[m][k][0], qf[m][k][1]);
+                    else
+                        mma16816(t[m], kf, qf[m][k][0], qf[m][k][1]);
+                }
             }
             if ((kRuns ? x.at < 0 : x.at != 0xFFFF) || some_partly_seen(a, s, p0, kChunk)) {
                 const uint32_t real = !kRuns ? (uint32_t)x.at : x.at < 0 ? 0u : (1u << max(0, min(kChunk, s.keys - p0))) - 1u;
@@ -378,18 +384,27 @@ k11_attention(const __grid_constant__ Args a)
     }
 }
 
-// By the average rows of a unit; any kernel is right for any unit.
-enum Variant { kRows8, kRows16, kRows32 };
-Variant variant_for(int64_t rows, int32_t seqs, int32_t group) {
+// By the average rows of a unit; any kernel is right for any unit.  From 33 rows on
+// the products are the bound, and k5_wide takes the call (blocks of a multiple of 8
+// keys; other block sizes stay here).
+enum Variant { kRows8, kRows16, kRows32, kRows128, kRows256 };
+Variant variant_for(int64_t rows, int32_t seqs, int32_t group, int32_t block_size) {
     const int64_t mean = (rows + seqs - 1) / seqs * group;
-    return mean <= 8 ? kRows8 : mean <= 16 ? kRows16 : kRows32;
+    if (mean <= 16)
+        return mean <= 8 ? kRows8 : kRows16;
+    if (mean <= 32 || block_size % 8 != 0)
+        return kRows32;
+    return mean <= 128 ? kRows128 : kRows256;
 }
 int tiles_of(Variant v) { return v == kRows8 ? 1 : v == kRows16 ? 2 : 4; }
 int ctas_of(Variant v, int num_sms) {
     return num_sms * (v == kRows8 ? kPerSm<1> : v == kRows16 ? kPerSm<2> : kPerSm<4>);
 }
-size_t slot_floats(Variant v) {
-    return v == kRows8 ? kSlotFloats<8> : v == kRows16 ? kSlotFloats<16> : kSlotFloats<32>;
+size_t workspace_of(Variant v, int num_sms) {
+    if (v >= kRows128)
+        return kv4_wide_workspace(v == kRows256, num_sms);
+    const size_t floats = v == kRows8 ? kSlotFloats<8> : v == kRows16 ? kSlotFloats<16> : kSlotFloats<32>;
+    return 2 * (size_t)ctas_of(v, num_sms) * floats * sizeof(float);
 }
 
 template <int kTiles, bool kRuns, bool kWindow>
@@ -414,12 +429,12 @@ cudaError_t launch_variant(Variant v, const Args &a, int ctas, cudaStream_t stre
 
 size_t kv4_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms)
 {
-    // for any call of fewer rows or more sequences too
-    const Variant last = variant_for(rows, seqs, group);
+    // for whichever block size, and for any call of fewer rows or more sequences too
+    const Variant last = variant_for(rows, seqs, group, 8);
     size_t most = 0;
-    for (const Variant v : {kRows8, kRows16, kRows32})
+    for (const Variant v : {kRows8, kRows16, kRows32, kRows128, kRows256})
         if (v <= last)
-            most = std::max(most, 2 * (size_t)ctas_of(v, num_sms) * slot_floats(v) * sizeof(float));
+            most = std::max(most, workspace_of(v, num_sms));
     return most;
 }
 
@@ -429,7 +444,9 @@ cudaError_t launch_kv4_attention(const TreeAttentionLaunch &p, int num_sms, cuda
     static_cast<TreeAttentionLaunch &>(a) = p;
     a.scale_log2 = p.scale * kLog2e;
     a.grow = kGrow / a.scale_log2;
-    const Variant v = variant_for(p.rows, p.seqs, p.group);
+    const Variant v = variant_for(p.rows, p.seqs, p.group, p.block_size);
+    if (v >= kRows128)
+        return launch_kv4_wide(p, v == kRows256, num_sms, stream, why);
     const int ctas = plan(a, 8 * tiles_of(v), false, ctas_of(v, num_sms));
     if (p.block_size % kChunk == 0)
         return p.window > 0 ? launch_variant<true, true>(v, a, ctas, stream, why)

@@ -23,6 +23,7 @@
 // leaves FP32 partials (output, m, sum) in the workspace, which a second kernel
 // joins in key order (no atomics: the result does not depend on timing).
 #include "rc_attention.cuh"
+#include "rc_kv4.cuh"
 #include "rc_tcgen05.cuh"
 
 #include <cmath>
@@ -494,8 +495,11 @@ template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 // tokens over 32768 keys (512 rows a KV head, blocks of 16).  With one row tile a
 // single warp loads both, as an eleventh warp would cost the SM its second CTA:
 // 16 trees of 16 over 8192 keys take 73 us, with two loaders 84.
-template <int kQ> constexpr int kLoaders = kQ;
-template <int kQ> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ>);
+//
+// kFour: over a cache in 4 bits two warps load rows and make bf16 numbers of them in
+// shared memory, in place of the boxes: 32 elements and their scale to a lane.
+template <int kQ, bool kFour> constexpr int kLoaders = kFour ? 2 : kQ;
+template <int kQ, bool kFour> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ, kFour>);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
 constexpr uint32_t kPCol = 128u, kOCol = 192u;
@@ -653,11 +657,11 @@ template <bool kWindow> __device__ uint32_t seen32(const Args &a, const SeqOf<kW
     return (ctx | (drafted & ~ctx)) & below(s.keys - base);
 }
 
-template <int kQ, bool kWindow>
-__global__ void __launch_bounds__(kWideThreads<kQ>, kQ == 1 ? 2 : 1)
+template <int kQ, bool kWindow, bool kFour>
+__global__ void __launch_bounds__(kWideThreads<kQ, kFour>, kQ == 1 ? 2 : 1)
 k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a, int box)
 {
-    constexpr int kRows = 128 * kQ, kStages = kWideStages<kQ>, kThreads = kWideThreads<kQ>;
+    constexpr int kRows = 128 * kQ, kStages = kWideStages<kQ>, kThreads = kWideThreads<kQ, kFour>;
     constexpr int kMmaWarp = kSoftmaxWarps<kQ>, kLoadWarp = kMmaWarp + kQ;
     extern __shared__ __align__(1024) uint8_t smem_wide[];
     const uint32_t sQ = smem_u32(smem_wide), sK = sQ + kQ * kTileBytes;     // a stage: K, then V
@@ -665,6 +669,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     // by piece modulo 8: a row tile is never more than kStages + 1 pieces ahead
     // of another, whose products free its stages
     __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[8];
+    __shared__ uint32_t s_bad_high[kFour ? kStages : 1];       // of the second half's boxes, with kFour
     static_assert(kStages + 1 < 8, "pieces in flight");
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kStages, q_ready0 = empty0 + 8u * kStages;
     const uint32_t s_full0 = q_ready0 + 8u * kQ, s_free0 = s_full0 + 8u * kQ, p_ready0 = s_free0 + 8u * kQ;
@@ -673,7 +678,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full0 + 8u * i, kLoaders<kQ>);
+            mbar_init(full0 + 8u * i, kLoaders<kQ, kFour>);
             mbar_init(empty0 + 8u * i, kQ);
         }
         for (int t = 0; t < kQ; ++t) {
@@ -689,7 +694,8 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         // one decision for the CTA: a raised fault skips the work
         s_skip = *reinterpret_cast<volatile unsigned int *>(&g_attention_faults);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_tensormap(&map);
+        if (!kFour)
+            prefetch_tensormap(&map);
     }
     pdl_wait();
     // TMEM only now: two CTAs (kQ = 1) fit on an SM, and one that held its columns
@@ -719,8 +725,88 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     uint32_t n = 0;                                     // key tiles of earlier pieces
     uint32_t piece = 0;
 
-    if (warp >= kLoadWarp) {
-        const bool keys = warp == kLoadWarp, values = kLoaders<kQ> == 1 || !keys;
+    if (kFour && warp >= kLoadWarp) {
+        // Boxes of eight keys, eight to a warp.  Lane 4r + q has key r of each and of its
+        // 64 bytes the q-th 16, K's two halves and V's two: a group of 32 elements with
+        // one scale.  A box's registers are loaded again for the next tile as soon as
+        // they are used.  In a word the elements come apart as (i, i + 4): the heads'
+        // elements are in that order in shared memory, Q's too, and O's columns are put
+        // back at the end.  V's lanes take their words in the order 2 3 0 1, so that the
+        // eight lanes of a store's phase write to all banks.
+        constexpr int kBoxes = 8;
+        const int half = warp - kLoadWarp, r = lane >> 2, q = lane & 3;
+        const uint32_t first_word = (q & 2) ? 2u : 0u;
+        bool fine = true;
+        while (fine && walk.next(a, u)) {
+            const SeqOf<kWindow> &s = u.s;
+            uint2 word[kBoxes][2];
+            uint32_t scale[kBoxes];
+            // lane l < 8: its box of tile j, as the number of its eight rows in the cache
+            // (-1: no block); its table entry is loaded before
+            auto key_of = [&](int j) { return tile_at(s, u.k0 + j) * kKeyTile + (half * kBoxes + (lane & 7)) * 8; };
+            auto look_up = [&](int j) -> int {
+                const int p = key_of(j);
+                return j < u.count && p < s.keys ? block_of(a, u.b, p) : 0;
+            };
+            auto place = [&](int j, int blk) -> int32_t {
+                const int p = key_of(j);
+                const bool mine = j < u.count && p < s.keys && some_seen(a, s, p, 8);
+                const bool lost = mine && (blk < 0 || blk >= a.num_blocks);
+                if (lost && lane < kBoxes && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(8, s.keys - p)))
+                    atomicAdd(a.err, 1);
+                if (!mine || lost)
+                    return -1;
+                const uint32_t bs = (uint32_t)a.block_size;
+                return (int32_t)((((int64_t)blk * a.kv_heads + u.h) * bs + (uint32_t)p % bs) / 8);
+            };
+            auto load = [&](int32_t at, int k) {
+                const int64_t row = (int64_t)max(__shfl_sync(0xFFFFFFFFu, at, k), 0) * 8 + r;
+                const uint2 *src = reinterpret_cast<const uint2 *>(a.cache4 + row * kKv4Row + 16 * q);
+                word[k][0] = __ldg(src + first_word / 2);
+                word[k][1] = __ldg(src + 1 - first_word / 2);
+                scale[k] = __ldg(a.scales + row * kKv4Scales + q);
+            };
+            int blk = look_up(0);
+            int32_t at = place(0, blk);
+            blk = look_up(1);
+#pragma unroll
+            for (int k = 0; k < kBoxes; ++k)
+                load(at, k);
+            for (int j = 0; j < u.count; ++j, ++n) {
+                const uint32_t st = n % kStages;
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, at < 0) & 0xFFu;
+                at = place(j + 1, blk);
+                blk = look_up(j + 2);
+                fine = wait_phase(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
+                fine = __all_sync(0xFFFFFFFFu, fine);
+                if (!fine)
+                    break;
+                if (lane == 0)
+                    (half == 0 ? s_bad[st] : s_bad_high[kFour ? st : 0]) = gone << (half * kBoxes);
+                const uint32_t tile = sK + st * (2 * kTileBytes) + (q >> 1) * kTileBytes;
+#pragma unroll
+                for (int k = 0; k < kBoxes; ++k) {
+                    const uint32_t sc = kv4_scales(scale[k] | scale[k] << 16), off = kv4_offsets(sc);
+                    const uint32_t row = (uint32_t)(half * kBoxes + k) * 8u + r;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = i & 1 ? word[k][i >> 1].y : word[k][i >> 1].x;
+                        const uint32_t chunk = (4u * (q & 1) + (i ^ first_word)) ^ (uint32_t)r;
+                        st_shared_v4(tile + row * 128u + (chunk << 4),
+                                     make_uint4(fma_bf16x2(kv4_pair(w, 0), sc, off), fma_bf16x2(kv4_pair(w, 1), sc, off),
+                                                fma_bf16x2(kv4_pair(w, 2), sc, off), fma_bf16x2(kv4_pair(w, 3), sc, off)));
+                    }
+                    if (j + 1 < u.count)
+                        load(at, k);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_local(full0 + 8u * st);
+            }
+        }
+    } else if (warp >= kLoadWarp) {
+        const bool keys = warp == kLoadWarp, values = kLoaders<kQ, kFour> == 1 || !keys;
         const int boxes = kKeyTile / box;               // <= 16
         bool fine = true;
         while (fine && walk.next(a, u)) {
@@ -749,7 +835,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 if (lane == 0) {
                     if (keys)
                         s_bad[st] = bads;
-                    mbar_expect_tx(full, (uint32_t)__popc(loads) * box * (256u / kLoaders<kQ>));
+                    mbar_expect_tx(full, (uint32_t)__popc(loads) * box * (256u / kLoaders<kQ, kFour>));
                 }
                 __syncwarp();
                 if (mine) {
@@ -843,8 +929,12 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 for (int c = 0; c < 4; ++c)
                     w[c] = node < s.n ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    if constexpr (kFour)                // elements in the order of the loaders
+                        w[c] = make_uint4(__byte_perm(w[c].x, w[c].z, 0x5410), __byte_perm(w[c].x, w[c].z, 0x7632),
+                                          __byte_perm(w[c].y, w[c].w, 0x5410), __byte_perm(w[c].y, w[c].w, 0x7632));
                     st_shared_v4(dst + (uint32_t)(((4 * half + c) ^ (r & 7)) << 4), w[c]);
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive_local(q_ready0 + 8u * t);
             }
@@ -871,7 +961,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t st = n % kStages;
-                const uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
+                uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
+                if constexpr (kFour)
+                    bads |= *reinterpret_cast<volatile uint32_t *>(&s_bad_high[st]);
                 // y[32h + 4c + 2e + f]: row e, key 64h + 8c + 2 (l % 4) + f
                 float y[64];
                 tmem_ld_rows(tS, y);
@@ -902,36 +994,39 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                                         y[4 * (4 * c + k) + 2 * e + f] = -INFINITY;
                         }
                     }
-                    // the tile's V: zeros past the end, and in place of what is
-                    // not finite in keys that a row may not see.  Every row tile looks at all
-                    // of it; one that finds such a value says so (the number of
-                    // the piece) before it takes it out, so that the others,
-                    // who may see the zero, see the word too.
-                    wait_phase(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
-                    const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
-                    for (int i = threadIdx.x & 255; i < kKeyTile * 8; i += 256) {
-                        const int key = p0 + (i >> 3);
-                        if (!partly_seen(a, s, key))
-                            continue;
-                        const uint32_t chunk = v + 16u * i;
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        bool write = true;
-                        if (key < s.keys) {
-                            w = ld_shared_v4(chunk);
-                            write = finite_only(w.x, true, true);
-                            write |= finite_only(w.y, true, true);
-                            write |= finite_only(w.z, true, true);
-                            write |= finite_only(w.w, true, true);
-                            if (write) {
-                                *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) = piece + 1u;
-                                __threadfence_block();
+                    // (in 4 bits no value is infinite or NaN, nor is what lies past the end)
+                    if constexpr (!kFour) {
+                        // the tile's V: zeros past the end, and in place of what is
+                        // not finite in keys that a row may not see.  Every row tile looks at all
+                        // of it; one that finds such a value says so (the number of
+                        // the piece) before it takes it out, so that the others,
+                        // who may see the zero, see the word too.
+                        wait_phase(full0 + 8u * st, (n / kStages) & 1u, kFaultSoftmax);    // complete: seen through S
+                        const uint32_t v = sK + st * (2 * kTileBytes) + kTileBytes;
+                        for (int i = threadIdx.x & 255; i < kKeyTile * 8; i += 256) {
+                            const int key = p0 + (i >> 3);
+                            if (!partly_seen(a, s, key))
+                                continue;
+                            const uint32_t chunk = v + 16u * i;
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            bool write = true;
+                            if (key < s.keys) {
+                                w = ld_shared_v4(chunk);
+                                write = finite_only(w.x, true, true);
+                                write |= finite_only(w.y, true, true);
+                                write |= finite_only(w.z, true, true);
+                                write |= finite_only(w.w, true, true);
+                                if (write) {
+                                    *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) = piece + 1u;
+                                    __threadfence_block();
+                                }
                             }
+                            if (write)
+                                st_shared_v4(chunk, w);
                         }
-                        if (write)
-                            st_shared_v4(chunk, w);
+                        __threadfence_block();
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    __threadfence_block();
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 // this lane's maxima: past a row's reference by more than 2^8
                 // (or the first that it sees), the row takes a new one
@@ -1018,7 +1113,18 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             for (int c = 0; c < 4; ++c)
                 loaded8(o + 8 * c);
             tc_fence_before();
-            const bool unfinite = *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) == piece + 1u;
+            if constexpr (kFour) {
+                // columns 2i and 2i + 1 of eight are elements i and i + 4
+                const int from = (lane & 28) | ((2 * lane) & 3);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float a0 = __shfl_sync(0xFFFFFFFFu, o[k], from), a1 = __shfl_sync(0xFFFFFFFFu, o[k + 1], from);
+                    const float b0 = __shfl_sync(0xFFFFFFFFu, o[k], from + 1), b1 = __shfl_sync(0xFFFFFFFFu, o[k + 1], from + 1);
+                    o[k] = (lane & 2) ? a1 : a0;
+                    o[k + 1] = (lane & 2) ? b1 : b0;
+                }
+            }
+            const bool unfinite = !kFour && *reinterpret_cast<volatile uint32_t *>(&s_unfinite[piece & 7u]) == piece + 1u;
             const bool whole = u.whole();
             float *slot = whole ? nullptr : slot_of<kRows>(a, 2 * (int64_t)blockIdx.x + (u.k0 == 0 ? 1 : 0));
 #pragma unroll
@@ -1044,7 +1150,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         float lo = o[4 * c + 2 * e], hi = o[4 * c + 2 * e + 1];
-                        if (unfinite) {
+                        if (!kFour && unfinite) {
                             lo = add_unfinite(a, s, u.b, u.h, i, 8 * c + col, lo);
                             hi = add_unfinite(a, s, u.b, u.h, i, 8 * c + col + 1, hi);
                         }
@@ -1118,30 +1224,33 @@ cudaError_t launch_small(const Args &a, int ctas, cudaStream_t stream, const cha
     return e != cudaSuccess ? e : launch_join<16 * kTiles, kWindow, false>(a, ctas, stream, why);
 }
 
-template <int kQ, bool kWindow>
+template <int kQ, bool kWindow, bool kFour>
 cudaError_t launch_wide(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     static bool configured[64] = {};
-    cudaError_t e = allow_smem(k5_wide<kQ, kWindow>, kWideSmem<kQ>, configured);
+    cudaError_t e = allow_smem(k5_wide<kQ, kWindow, kFour>, kWideSmem<kQ>, configured);
     if (e != cudaSuccess)
         return e;
     // the cache as [num_blocks, kv_heads, block_size, 128], boxes of 64 columns
     // (K or V) and the largest power of two of keys, at most a tile, in a block
-    const int box = std::min(kKeyTile, a.block_size & -a.block_size);
-    const uint64_t row = 2 * kHeadDim * 2;
-    const cuuint64_t dims[4] = {2 * kHeadDim, (cuuint64_t)a.block_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_blocks};
-    const cuuint64_t strides[3] = {row, row * a.block_size, row * a.block_size * a.kv_heads};
-    const cuuint32_t boxes[4] = {kHeadDim, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    CUtensorMap map;
-    const EncodeTiledFn enc = encode_fn();
-    *why = "tensor map of the cache could not be encoded";
-    if (!enc || enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(a.cache), dims, strides, boxes,
-                    ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    const int box = kFour ? 8 : std::min(kKeyTile, a.block_size & -a.block_size);
+    CUtensorMap map = {};
+    if (!kFour) {
+        const uint64_t row = 2 * kHeadDim * 2;
+        const cuuint64_t dims[4] = {2 * kHeadDim, (cuuint64_t)a.block_size, (cuuint64_t)a.kv_heads, (cuuint64_t)a.num_blocks};
+        const cuuint64_t strides[3] = {row, row * a.block_size, row * a.block_size * a.kv_heads};
+        const cuuint32_t boxes[4] = {kHeadDim, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+        const EncodeTiledFn enc = encode_fn();
+        *why = "tensor map of the cache could not be encoded";
+        if (!enc || enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(a.cache), dims, strides, boxes,
+                        ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     *why = "attention launch";
-    e = launch_pdl(k5_wide<kQ, kWindow>, dim3((unsigned)ctas), dim3(kWideThreads<kQ>), kWideSmem<kQ>, stream, 1, map, a, box);
-    return e != cudaSuccess ? e : launch_join<128 * kQ, kWindow, false>(a, ctas, stream, why);
+    e = launch_pdl(k5_wide<kQ, kWindow, kFour>, dim3((unsigned)ctas), dim3(kWideThreads<kQ, kFour>), kWideSmem<kQ>, stream,
+                   1, map, a, box);
+    return e != cudaSuccess ? e : launch_join<128 * kQ, kWindow, kFour>(a, ctas, stream, why);
 }
 
 template <bool kWindow>
@@ -1153,8 +1262,8 @@ cudaError_t launch_variant(Variant v, const Args &a, int ctas, cudaStream_t stre
                                : launch_small<1, false, kWindow>(a, ctas, stream, why);
     case kSmall32: return runs ? launch_small<2, true, kWindow>(a, ctas, stream, why)
                                : launch_small<2, false, kWindow>(a, ctas, stream, why);
-    case kWide128: return launch_wide<1, kWindow>(a, ctas, stream, why);
-    default: return launch_wide<2, kWindow>(a, ctas, stream, why);
+    case kWide128: return launch_wide<1, kWindow, false>(a, ctas, stream, why);
+    default: return launch_wide<2, kWindow, false>(a, ctas, stream, why);
     }
 }
 
@@ -1184,6 +1293,23 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &p, int num_sms, cud
     const int64_t unit_rows = v == kSmall16 ? 16 : v == kSmall32 ? 32 : v == kWide128 ? 128 : 256;
     const int ctas = plan(a, unit_rows, wide, ctas_of(v, num_sms));
     return p.window > 0 ? launch_variant<true>(v, a, ctas, stream, why) : launch_variant<false>(v, a, ctas, stream, why);
+}
+
+size_t kv4_wide_workspace(bool two, int num_sms)
+{
+    const Variant v = two ? kWide256 : kWide128;
+    return 2 * (size_t)ctas_of(v, num_sms) * slot_floats(v) * sizeof(float);
+}
+
+cudaError_t launch_kv4_wide(const TreeAttentionLaunch &p, bool two, int num_sms, cudaStream_t stream, const char **why)
+{
+    Args a{};
+    static_cast<TreeAttentionLaunch &>(a) = p;
+    a.scale_log2 = p.scale * kLog2e;
+    const int ctas = plan(a, two ? 256 : 128, true, ctas_of(two ? kWide256 : kWide128, num_sms));
+    if (two)
+        return p.window > 0 ? launch_wide<2, true, true>(a, ctas, stream, why) : launch_wide<2, false, true>(a, ctas, stream, why);
+    return p.window > 0 ? launch_wide<1, true, true>(a, ctas, stream, why) : launch_wide<1, false, true>(a, ctas, stream, why);
 }
 
 cudaError_t read_attention_faults(uint32_t *flags, bool clear)

@@ -93,6 +93,10 @@ cudaError_t launch_tree_attention(const TreeAttentionLaunch &a, int num_sms, cud
 size_t kv4_attention_workspace(int64_t rows, int32_t seqs, int32_t group, int num_sms);
 cudaError_t launch_kv4_attention(const TreeAttentionLaunch &a, int num_sms, cudaStream_t stream, const char **why);
 
+// Its tiles of 128 rows (two: 256) on tcgen05, and their workspace.
+size_t kv4_wide_workspace(bool two, int num_sms);
+cudaError_t launch_kv4_wide(const TreeAttentionLaunch &a, bool two, int num_sms, cudaStream_t stream, const char **why);
+
 // Sticky device fault bits of the tree attention (current device).
 cudaError_t read_attention_faults(uint32_t *flags, bool clear);
 
