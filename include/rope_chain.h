@@ -912,8 +912,8 @@ size_t rc_head_norm_rope_grad_workspace_size(int32_t head_dim);
  * low half of byte i and element 2i + 1 in the high half; `scales` bf16
  * [num_blocks, num_kv_heads, block_size, 4], those of K's elements 0 to 31 and 32
  * to 63, then of V's.  A half-byte c stands for (c - 8) * scale, which is a bf16
- * number for the scales that rc_kv4_store writes (four significant bits); a scale
- * that is not finite, or above 2^100 in size, counts as 0.  72 bytes a row, where
+ * number: of a scale four significant bits count, not its sign, and at most 2^100
+ * (infinities and NaN, too, count as that), so every value is finite.  72 bytes a row, where
  * the bf16 caches have 256.  A cache of zero bytes and scales holds zeros.
  */
 

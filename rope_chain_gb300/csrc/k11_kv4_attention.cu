@@ -17,8 +17,8 @@
 //   V: keys 2c, 2c + 1, 2c + 8 and 2c + 9, elements 8g to 8g + 7, a word each; the low
 //      halves of two keys' words in one register come apart into pairs of keys
 // Every value is an exact bf16 number, so nothing is rounded but the weights (to bf16,
-// for the products with V) and the output.  Scales that are not finite count as 0, so
-// no value is infinite or NaN, and what a row does not see stays away by a weight of 0.
+// for the products with V) and the output.  No value is infinite or NaN, so what a row
+// does not see stays away by a weight of 0.
 //
 // Every warp streams its own 16 of a tile's 128 keys from the cache into registers,
 // kAhead chunks ahead, with a running maximum, sum and output of its own; the warps'
@@ -194,12 +194,7 @@ k11_attention(const __grid_constant__ Args a)
         auto work = [&](int j, const Chunk &x) {
             const int p0 = first_key(j);
             // scales: of this lane's two keys of K, twice each; of its pairs of keys of V
-            uint32_t ks = x.scale.x & 0xFFF0FFF0u, vs = x.scale.y & 0xFFF0FFF0u;
-            constexpr uint32_t kMost = kKv4MostScale | kKv4MostScale << 16;
-            if (__any_sync(0xFFFFFFFFu, __vmaxu2(__vmaxu2(ks & 0x7FFF7FFFu, vs & 0x7FFF7FFFu), kMost) != kMost)) {
-                ks = kv4_scales(ks);
-                vs = kv4_scales(vs);
-            }
+            const uint32_t ks = kv4_scales(x.scale.x), vs = kv4_scales(x.scale.y);
             uint32_t k_scale[2], v_scale[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

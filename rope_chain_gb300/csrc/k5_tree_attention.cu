@@ -496,9 +496,11 @@ template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 // single warp loads both, as an eleventh warp would cost the SM its second CTA:
 // 16 trees of 16 over 8192 keys take 73 us, with two loaders 84.
 //
-// kFour: over a cache in 4 bits two warps load rows and make bf16 numbers of them in
-// shared memory, in place of the boxes: 32 elements and their scale to a lane.
-template <int kQ, bool kFour> constexpr int kLoaders = kFour ? 2 : kQ;
+//
+// kFour: over a cache in 4 bits the loaders make bf16 numbers of the rows in shared
+// memory, in place of the boxes: 32 elements and their scale to a lane.
+constexpr int kTileBoxes = 16;         // of eight keys
+template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 1 : 2) : kQ;
 template <int kQ, bool kFour> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ, kFour>);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
@@ -613,6 +615,11 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void loaded8(float *r) {
     asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
 }
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t at) {
+    uint2 x;
+    asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
+    return x;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -669,7 +676,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     // by piece modulo 8: a row tile is never more than kStages + 1 pieces ahead
     // of another, whose products free its stages
     __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[8];
-    __shared__ uint32_t s_bad_high[kFour ? kStages : 1];       // of the second half's boxes, with kFour
+    __shared__ __align__(8) uint16_t s_gone[kFour ? kStages : 1][4];  // kFour: of each loader's boxes
     static_assert(kStages + 1 < 8, "pieces in flight");
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kStages, q_ready0 = empty0 + 8u * kStages;
     const uint32_t s_full0 = q_ready0 + 8u * kQ, s_free0 = s_full0 + 8u * kQ, p_ready0 = s_free0 + 8u * kQ;
@@ -691,6 +698,8 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         }
         for (int i = 0; i < 8; ++i)
             s_unfinite[i] = 0u;
+        for (int i = 0; kFour && i < 4 * kStages; ++i)
+            s_gone[i / 4][i % 4] = 0;
         // one decision for the CTA: a raised fault skips the work
         s_skip = *reinterpret_cast<volatile unsigned int *>(&g_attention_faults);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -717,7 +726,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     if (s_skip != 0u)
         walk.hi = walk.pos;
     Piece<kWindow> u;
-    if constexpr (kQ == 2) {
+    if constexpr (kQ == 2 && !kFour) {
         in_memory(at);
         in_memory(walk);
         in_memory(u);
@@ -725,79 +734,103 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     uint32_t n = 0;                                     // key tiles of earlier pieces
     uint32_t piece = 0;
 
+    if constexpr (kFour) {
+        in_memory(at);
+        in_memory(walk);
+        in_memory(u);
+    }
     if (kFour && warp >= kLoadWarp) {
-        // Boxes of eight keys, eight to a warp.  Lane 4r + q has key r of each and of its
-        // 64 bytes the q-th 16, K's two halves and V's two: a group of 32 elements with
-        // one scale.  A box's registers are loaded again for the next tile as soon as
-        // they are used.  In a word the elements come apart as (i, i + 4): the heads'
-        // elements are in that order in shared memory, Q's too, and O's columns are put
-        // back at the end.  V's lanes take their words in the order 2 3 0 1, so that the
-        // eight lanes of a store's phase write to all banks.
-        constexpr int kBoxes = 8;
-        const int half = warp - kLoadWarp, r = lane >> 2, q = lane & 3;
+        // A tile's 16 boxes of eight keys, kOwn to a warp.  Lane 4r + q has key r of a box
+        // and of its 64 bytes the q-th 16, K's two halves and V's two: a group of 32
+        // elements with one scale.  A box's registers are loaded again, for the next
+        // kGroup boxes, as soon as they are used.  In a word the elements come apart as
+        // (i, i + 4): the heads' elements are in that order in shared memory, Q's too, and
+        // O's columns are put back at the end.  V's lanes take their words in the order
+        // 2 3 0 1, so that the eight lanes of a store's phase write to all banks.
+        constexpr int kOwn = kTileBoxes / kLoaders<kQ, kFour>, kGroup = kOwn < 8 ? kOwn : 8, kRounds = kOwn / kGroup;
+        constexpr int kAtOnce = 32 / kOwn;              // tiles whose boxes are looked up at once, a lane each
+        const int first_box = (warp - kLoadWarp) * kOwn, r = lane >> 2, q = lane & 3;
         const uint32_t first_word = (q & 2) ? 2u : 0u;
+        // where this lane's words of box 0 go: word i, chunk 4 (q % 2) + i of the row
+        const uint32_t row_at = sK + (q >> 1) * kTileBytes + (uint32_t)(8 * first_box + r) * 128u;
+        uint32_t chunk_at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            chunk_at[i] = row_at + (((4u * (q & 1) + (i ^ first_word)) ^ (uint32_t)r) << 4);
+        const uint8_t *const from4 = a.cache4 + r * kKv4Row + 16 * q + 4 * first_word;
+        const int other = first_word != 0u ? -1 : 1;    // from the first two words to the others
+        const uint16_t *const from_scales = a.scales + r * kKv4Scales + q;
         bool fine = true;
         while (fine && walk.next(a, u)) {
             const SeqOf<kWindow> &s = u.s;
-            uint2 word[kBoxes][2];
-            uint32_t scale[kBoxes];
-            // lane l < 8: its box of tile j, as the number of its eight rows in the cache
-            // (-1: no block); its table entry is loaded before
-            auto key_of = [&](int j) { return tile_at(s, u.k0 + j) * kKeyTile + (half * kBoxes + (lane & 7)) * 8; };
+            uint2 word[kGroup][2];
+            uint32_t scale[kGroup];
+            // this lane's box, of tile j + lane / kOwn: its table entry, then the number of
+            // its eight rows in the cache (-1: no block)
+            auto key_of = [&](int j) { return tile_at(s, u.k0 + j + lane / kOwn) * kKeyTile + (first_box + lane % kOwn) * 8; };
             auto look_up = [&](int j) -> int {
                 const int p = key_of(j);
-                return j < u.count && p < s.keys ? block_of(a, u.b, p) : 0;
+                return j + lane / kOwn < u.count && p < s.keys ? block_of(a, u.b, p) : 0;
             };
             auto place = [&](int j, int blk) -> int32_t {
                 const int p = key_of(j);
-                const bool mine = j < u.count && p < s.keys && some_seen(a, s, p, 8);
+                const bool mine = j + lane / kOwn < u.count && p < s.keys && some_seen(a, s, p, 8);
                 const bool lost = mine && (blk < 0 || blk >= a.num_blocks);
-                if (lost && lane < kBoxes && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(8, s.keys - p)))
+                if (lost && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(8, s.keys - p)))
                     atomicAdd(a.err, 1);
                 if (!mine || lost)
                     return -1;
                 const uint32_t bs = (uint32_t)a.block_size;
                 return (int32_t)((((int64_t)blk * a.kv_heads + u.h) * bs + (uint32_t)p % bs) / 8);
             };
-            auto load = [&](int32_t at, int k) {
-                const int64_t row = (int64_t)max(__shfl_sync(0xFFFFFFFFu, at, k), 0) * 8 + r;
-                const uint2 *src = reinterpret_cast<const uint2 *>(a.cache4 + row * kKv4Row + 16 * q);
-                word[k][0] = __ldg(src + first_word / 2);
-                word[k][1] = __ldg(src + 1 - first_word / 2);
-                scale[k] = __ldg(a.scales + row * kKv4Scales + q);
+            auto load = [&](int32_t at, int lane_of, int k) {
+                const uint64_t i = (uint32_t)max(__shfl_sync(0xFFFFFFFFu, at, lane_of), 0);
+                const uint2 *src = reinterpret_cast<const uint2 *>(from4 + i * (8 * kKv4Row));
+                word[k][0] = __ldg(src);
+                word[k][1] = __ldg(src + other);
+                scale[k] = __ldg(from_scales + i * (8 * kKv4Scales));
             };
-            int blk = look_up(0);
-            int32_t at = place(0, blk);
-            blk = look_up(1);
+            int32_t at = place(0, look_up(0));
+            int blk = look_up(kAtOnce);
+            uint32_t gone = __ballot_sync(0xFFFFFFFFu, at < 0);     // of the tiles that are worked on
+            uint32_t gone_next = gone;
+            int next_lane = 0;                          // of the boxes that are loaded next
 #pragma unroll
-            for (int k = 0; k < kBoxes; ++k)
-                load(at, k);
+            for (int k = 0; k < kGroup; ++k)
+                load(at, next_lane + k, k);
+            next_lane += kGroup;
             for (int j = 0; j < u.count; ++j, ++n) {
                 const uint32_t st = n % kStages;
-                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, at < 0) & 0xFFu;
-                at = place(j + 1, blk);
-                blk = look_up(j + 2);
+                if (j % kAtOnce == 0)
+                    gone = gone_next;
                 fine = wait_phase(empty0 + 8u * st, ((n / kStages) & 1u) ^ 1u, kFaultLoad);
                 fine = __all_sync(0xFFFFFFFFu, fine);
                 if (!fine)
                     break;
                 if (lane == 0)
-                    (half == 0 ? s_bad[st] : s_bad_high[kFour ? st : 0]) = gone << (half * kBoxes);
-                const uint32_t tile = sK + st * (2 * kTileBytes) + (q >> 1) * kTileBytes;
+                    s_gone[kFour ? st : 0][warp - kLoadWarp] = (uint16_t)(gone >> (j % kAtOnce * kOwn) & ((1u << kOwn) - 1u));
+                const uint32_t to = st * (2 * kTileBytes);
 #pragma unroll
-                for (int k = 0; k < kBoxes; ++k) {
-                    const uint32_t sc = kv4_scales(scale[k] | scale[k] << 16), off = kv4_offsets(sc);
-                    const uint32_t row = (uint32_t)(half * kBoxes + k) * 8u + r;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = i & 1 ? word[k][i >> 1].y : word[k][i >> 1].x;
-                        const uint32_t chunk = (4u * (q & 1) + (i ^ first_word)) ^ (uint32_t)r;
-                        st_shared_v4(tile + row * 128u + (chunk << 4),
-                                     make_uint4(fma_bf16x2(kv4_pair(w, 0), sc, off), fma_bf16x2(kv4_pair(w, 1), sc, off),
-                                                fma_bf16x2(kv4_pair(w, 2), sc, off), fma_bf16x2(kv4_pair(w, 3), sc, off)));
+                for (int h = 0; h < kRounds; ++h) {
+                    if (next_lane == kAtOnce * kOwn) {  // the next boxes are those of tile j + 1
+                        next_lane = 0;
+                        at = place(j + 1, blk);
+                        blk = look_up(j + 1 + kAtOnce);
+                        gone_next = __ballot_sync(0xFFFFFFFFu, at < 0);
                     }
-                    if (j + 1 < u.count)
-                        load(at, k);
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        const uint32_t sc = kv4_scales(scale[k] * 0x10001u), off = kv4_offsets(sc);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t w = c & 1 ? word[k][c >> 1].y : word[k][c >> 1].x;
+                            st_shared_v4(chunk_at[c] + to + 1024u * (h * kGroup + k),
+                                         make_uint4(fma_bf16x2(kv4_pair(w, 0), sc, off), fma_bf16x2(kv4_pair(w, 1), sc, off),
+                                                    fma_bf16x2(kv4_pair(w, 2), sc, off), fma_bf16x2(kv4_pair(w, 3), sc, off)));
+                        }
+                        load(at, next_lane + k, k);     // (past the last tile: row 0)
+                    }
+                    next_lane += kGroup;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -961,9 +994,18 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t st = n % kStages;
-                uint32_t bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
-                if constexpr (kFour)
-                    bads |= *reinterpret_cast<volatile uint32_t *>(&s_bad_high[st]);
+                uint32_t bads;                          // boxes without keys
+                if constexpr (kFour) {
+                    constexpr int kWarps4 = kLoaders<kQ, kFour>, kOwn = kTileBoxes / kWarps4;
+                    const uint2 gone = ld_shared_v2(smem_u32(s_gone[st]));
+                    bads = gone.x & 0xFFFFu;
+                    if constexpr (kWarps4 > 1)
+                        bads |= gone.x >> 16 << kOwn;
+                    if constexpr (kWarps4 > 2)
+                        bads |= (gone.y & 0xFFFFu) << 2 * kOwn | gone.y >> 16 << 3 * kOwn;
+                } else {
+                    bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
+                }
                 // y[32h + 4c + 2e + f]: row e, key 64h + 8c + 2 (l % 4) + f
                 float y[64];
                 tmem_ld_rows(tS, y);

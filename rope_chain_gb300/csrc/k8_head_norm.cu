@@ -158,7 +158,6 @@ template <typename T, bool kHalves, int kVec, int kU, int kHeads> struct Lane {
     static constexpr bool kOne = kVec * sizeof(T) == 16;
     static constexpr int kParts = kHalves ? 2 : 1;          // runs of kVec elements of a unit
     static constexpr int kPairs = kHalves ? kVec : (kVec > 1 ? kVec / 2 : 1);
-    static constexpr int kValues = kParts * kVec;
 
     // the unit's first element, or -1 past the last unit; whether it is turned
     static __device__ __forceinline__ int place(const NormArgs &a, int i, bool &rot) {

@@ -14,16 +14,12 @@ namespace rc {
 
 constexpr int kKv4Row = 64;            // bytes of K and V of a row
 constexpr int kKv4Scales = 4;          // their scales
-constexpr uint32_t kKv4MostScale = 0x7180u;     // 2^100 as bf16: scales past it, or not finite, count as 0
+constexpr uint32_t kKv4MostScale = 0x7180u;     // 2^100 as bf16
 
-// A pair of scales as they count.
+// A pair of scales as they count: without a sign, of four significant bits, and at
+// most 2^100 (which takes infinities and NaN in, so that no value is either).
 __device__ __forceinline__ uint32_t kv4_scales(uint32_t two) {
-    two &= 0xFFF0FFF0u;
-    if ((two & 0x7FFFu) > kKv4MostScale)
-        two &= 0xFFFF0000u;
-    if ((two & 0x7FFF0000u) > (kKv4MostScale << 16))
-        two &= 0x0000FFFFu;
-    return two;
+    return __vminu2(two & 0x7FF07FF0u, kKv4MostScale | kKv4MostScale << 16);
 }
 
 // (a0 * b0 + c0, a1 * b1 + c1) of bf16 pairs, and their product

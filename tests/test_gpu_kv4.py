@@ -133,10 +133,10 @@ def test_scales_that_the_store_does_not_write():
     scales[0, 0, 4, 2] = float("nan")
     got = rc.kv4_load(torch.arange(8, device=DEV), cache, scales)[:, 0].double()
     n = torch.stack((cache[0, 0] % 16, cache[0, 0] // 16), -1).flatten(-2).double() - 8
-    s = (scales[0, 0].view(torch.int16) & -16).view(BF).double()      # four significant bits
-    s = torch.where(s.abs() <= 2.0 ** 100, s, torch.zeros_like(s)).repeat_interleave(32, -1)
-    assert torch.equal(got, n * s)
-    assert not bool(got[0].any()) and not bool(got[1].any()) and not bool(got[2].any()) and bool(got[3].any())
+    # four significant bits, no sign, at most 2^100
+    s = (scales[0, 0].view(torch.int16) & 0x7FF0).view(BF).double()
+    s = torch.where(s <= 2.0 ** 100, s, 2.0 ** 100).repeat_interleave(32, -1)
+    assert torch.equal(got, n * s) and bool(torch.isfinite(got).all())
 
 
 def test_slots_past_the_cache_are_counted():
