@@ -500,7 +500,7 @@ template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 // kFour: over a cache in 4 bits the loaders make bf16 numbers of the rows in shared
 // memory, in place of the boxes: 32 elements and their scale to a lane.
 constexpr int kTileBoxes = 16;         // of eight keys
-template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 1 : 2) : kQ;
+template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 2 : 4) : kQ;
 template <int kQ, bool kFour> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ, kFour>);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
@@ -726,7 +726,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     if (s_skip != 0u)
         walk.hi = walk.pos;
     Piece<kWindow> u;
-    if constexpr (kQ == 2 && !kFour) {
+    if constexpr ((kQ == 2 || kWindow) && !kFour) {
         in_memory(at);
         in_memory(walk);
         in_memory(u);
@@ -766,7 +766,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             uint2 word[kGroup][2];
             uint32_t scale[kGroup];
             // this lane's box, of tile j + lane / kOwn: its table entry, then the number of
-            // its eight rows in the cache (-1: no block)
+            // its eight rows in the cache (negative: none)
             auto key_of = [&](int j) { return tile_at(s, u.k0 + j + lane / kOwn) * kKeyTile + (first_box + lane % kOwn) * 8; };
             auto look_up = [&](int j) -> int {
                 const int p = key_of(j);
@@ -779,7 +779,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 if (lost && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(8, s.keys - p)))
                     atomicAdd(a.err, 1);
                 if (!mine || lost)
-                    return -1;
+                    return lost ? -1 : -2;              // (-2: hidden by the rows' masks anyway)
                 const uint32_t bs = (uint32_t)a.block_size;
                 return (int32_t)((((int64_t)blk * a.kv_heads + u.h) * bs + (uint32_t)p % bs) / 8);
             };
@@ -792,7 +792,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             };
             int32_t at = place(0, look_up(0));
             int blk = look_up(kAtOnce);
-            uint32_t gone = __ballot_sync(0xFFFFFFFFu, at < 0);     // of the tiles that are worked on
+            uint32_t gone = __ballot_sync(0xFFFFFFFFu, at == -1);   // of the tiles that are worked on
             uint32_t gone_next = gone;
             int next_lane = 0;                          // of the boxes that are loaded next
 #pragma unroll
@@ -816,7 +816,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                         next_lane = 0;
                         at = place(j + 1, blk);
                         blk = look_up(j + 1 + kAtOnce);
-                        gone_next = __ballot_sync(0xFFFFFFFFu, at < 0);
+                        gone_next = __ballot_sync(0xFFFFFFFFu, at == -1);
                     }
 #pragma unroll
                     for (int k = 0; k < kGroup; ++k) {
@@ -864,7 +864,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 fine = __all_sync(0xFFFFFFFFu, fine);
                 if (!fine)
                     break;
-                const uint32_t bads = __ballot_sync(0xFFFFFFFFu, bad), loads = __ballot_sync(0xFFFFFFFFu, mine);
+                const uint32_t bads = __ballot_sync(0xFFFFFFFFu, lost), loads = __ballot_sync(0xFFFFFFFFu, mine);
                 if (lane == 0) {
                     if (keys)
                         s_bad[st] = bads;
@@ -985,6 +985,10 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 ref[e] = sum[e] = 0.0f;
                 limit[e] = -INFINITY;
             }
+            if constexpr (kWindow || kFour) {
+                in_memory(node);
+                in_memory(begin);
+            }
             const int count = u.count, ctx = s.ctx;
             int p0 = u.k0 * kKeyTile;
             for (int j = 0; j < count; ++j, ++n, p0 += kKeyTile) {
@@ -1022,8 +1026,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
-                        for (int k = 0; bads != 0u && k < 32; ++k)
-                            out |= ((bads >> ((32 * c + k) / box)) & 1u) << k;
+#pragma unroll 1
+                        for (int k = 0; bads != 0u && k < 32; k += 8)   // (boxes of 8 keys at least)
+                            out |= ((bads >> ((32 * c + k) / box)) & 1u ? 0xFFu : 0u) << k;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const uint32_t see =
