@@ -128,15 +128,6 @@ __device__ __forceinline__ void values(const void *p, bool f32, int64_t at, floa
     }
 }
 
-// The rotation of pair (a, b), or (kBack) its transpose.
-template <bool kBack> __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
-    if (kBack)
-        s = -s;
-    const float x = __fmaf_rn(a, c, -__fmul_rn(b, s));
-    b = __fmaf_rn(b, c, __fmul_rn(a, s));
-    a = x;
-}
-
 // The sum over the `lanes` (a power of two) lanes of a head, in every one of them.
 __device__ __forceinline__ float head_sum(float v, int lanes) {
     for (int o = lanes >> 1; o >= 1; o >>= 1)
@@ -145,19 +136,21 @@ __device__ __forceinline__ float head_sum(float v, int lanes) {
 }
 
 struct NormArgs : HeadNormLaunch {
-    int32_t lanes;                       // lanes of a head: a power of two <= 32
-    int32_t groups[2];                   // groups of kHeads heads of the queries and of the keys
+    int32_t lanes, lanes_log2;           // lanes of a head: a power of two <= 32
+    int32_t per;                         // heads of an item at most
+    int32_t groups[2];                   // items of the queries and of the keys of a token
     float inv_width;
     int32_t blocks;                      // of a kind (gradient)
 };
 
 // A head's units of kVec elements (HALVES: kVec of each half; past rot_dim kVec) go
-// to consecutive lanes, kU to a lane.  What a lane has of kHeads heads of one kind
-// (queries or keys) of one token, whose table columns and weights are read once.
-template <typename T, bool kHalves, int kVec, int kU, int kHeads> struct Lane {
+// to consecutive lanes, kU to a lane.  In FP32 a unit is kPairs pairs (p, q): the
+// pairs that turn, or two elements that do not.
+template <typename T, bool kHalves, int kVec, int kU> struct Lane {
     static constexpr bool kOne = kVec * sizeof(T) == 16;
     static constexpr int kParts = kHalves ? 2 : 1;          // runs of kVec elements of a unit
-    static constexpr int kPairs = kHalves ? kVec : (kVec > 1 ? kVec / 2 : 1);
+    static constexpr int kPairs = kHalves ? kVec : kVec / 2;
+    using Raw = Run<T, kVec>[kU][kParts];
 
     // the unit's first element, or -1 past the last unit; whether it is turned
     static __device__ __forceinline__ int place(const NormArgs &a, int i, bool &rot) {
@@ -167,7 +160,8 @@ template <typename T, bool kHalves, int kVec, int kU, int kHeads> struct Lane {
         const int at = rot ? u * kVec : a.rot + (u - rotated) * kVec;
         return at < a.width ? at : -1;
     }
-    static __device__ __forceinline__ void load(const NormArgs &a, const T *head, Run<T, kVec> (&v)[kU][kParts]) {
+    // what a lane has of the head at `head` (NULL: zeros)
+    static __device__ __forceinline__ void load(const NormArgs &a, const T *head, Raw &v) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
             bool rot;
@@ -175,40 +169,123 @@ template <typename T, bool kHalves, int kVec, int kU, int kHeads> struct Lane {
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
                 v[i][p].clear();
-            if (at >= 0) {
+            if (head != nullptr && at >= 0) {
                 v[i][0].template get<kOne>(head + at);
                 if (kHalves && rot)
                     v[i][kParts - 1].template get<kOne>(head + at + a.rot / 2);
             }
         }
     }
-    static __device__ __forceinline__ void table(const NormArgs &a, int64_t pos, int at, bool rot, float (&c)[kPairs],
-                                                 float (&s)[kPairs]) {
-        if (rot) {
+    static __device__ __forceinline__ void store(const NormArgs &a, T *head, int i, const float (&p)[kPairs], const float (&q)[kPairs]) {
+        bool rot;
+        const int at = place(a, i, rot);
+        if (at < 0)
+            return;
+        Run<T, kVec> o;
+        if constexpr (kHalves) {
+            o.set(p);
+            o.template put<kOne>(head + at);
+            if (rot) {
+                o.set(q);
+                o.template put<kOne>(head + at + a.rot / 2);
+            }
+        } else {
+            float both[kVec];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                both[2 * j] = p[j];
+                both[2 * j + 1] = q[j];
+            }
+            o.set(both);
+            o.template put<kOne>(head + at);
+        }
+    }
+    static __device__ __forceinline__ void pairs(const Run<T, kVec> (&v)[kParts], float (&p)[kPairs], float (&q)[kPairs]) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            p[j] = v[0].at(kHalves ? j : 2 * j);
+            q[j] = kHalves ? v[kParts - 1].at(j) : v[0].at(2 * j + 1);
+        }
+    }
+    // the table's columns of unit i (1 and 0 where it is not turned)
+    static __device__ __forceinline__ void table(const NormArgs &a, int64_t pos, bool bad, int i, float (&c)[kPairs], float (&s)[kPairs]) {
+        bool rot;
+        const int at = place(a, i, rot);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            c[j] = 1.0f;
+            s[j] = 0.0f;
+        }
+        if (at >= 0 && rot && !bad) {
             const int64_t from = pos * a.rot + (kHalves ? at : at / 2);
             values<kPairs, kOne>(a.table, a.table_f32 != 0, from, c);
             values<kPairs, kOne>(a.table, a.table_f32 != 0, from + a.rot / 2, s);
         }
     }
-    // a unit's values, turned by (c, s)
-    template <bool kBack>
-    static __device__ __forceinline__ void rotate(float (&y)[kParts][kVec], const float (&c)[kPairs], const float (&s)[kPairs]) {
+    static __device__ __forceinline__ void weights(const NormArgs &a, int kind, int i, float (&p)[kPairs], float (&q)[kPairs]) {
+        bool rot;
+        const int at = place(a, i, rot);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j)
+            p[j] = q[j] = 1.0f;
+        if (a.weight[kind] == nullptr || at < 0)
+            return;
         if constexpr (kHalves) {
+            values<kPairs, kOne>(a.weight[kind], a.weight_f32 != 0, at, p);
+            if (rot)
+                values<kPairs, kOne>(a.weight[kind], a.weight_f32 != 0, at + a.rot / 2, q);
+        } else {
+            float both[kVec];
+            values<kVec, kOne>(a.weight[kind], a.weight_f32 != 0, at, both);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                turn<kBack>(y[0][j], y[1][j], c[j], s[j]);
-        } else if constexpr (kVec > 1) {
-#pragma unroll
-            for (int j = 0; j < kVec; j += 2)
-                turn<kBack>(y[0][j], y[0][j + 1], c[j / 2], s[j / 2]);
+            for (int j = 0; j < kPairs; ++j) {
+                p[j] = both[2 * j];
+                q[j] = both[2 * j + 1];
+            }
         }
     }
 };
 
-// Items are (token, group of heads); a group holds heads of one kind.
-template <int kHeads> struct Item {
+// Two at a time where there are two: (a, b) <- f(a, b), FP32 pairs.
+template <int kN> __device__ __forceinline__ void scale(float (&v)[kN], float r) {
+#pragma unroll
+    for (int j = 0; j + 1 < kN; j += 2)
+        mul2_rn(v[j], v[j + 1], r, r);
+    if (kN % 2)
+        v[kN - 1] *= r;
+}
+// v * w
+template <int kN> __device__ __forceinline__ void times(float (&v)[kN], const float (&w)[kN]) {
+#pragma unroll
+    for (int j = 0; j + 1 < kN; j += 2)
+        mul2_rn(v[j], v[j + 1], w[j], w[j + 1]);
+    if (kN % 2)
+        v[kN - 1] *= w[kN - 1];
+}
+// d <- v * w + d
+template <int kN> __device__ __forceinline__ void add_product(float (&d)[kN], const float (&v)[kN], const float (&w)[kN]) {
+#pragma unroll
+    for (int j = 0; j + 1 < kN; j += 2) {
+        float x = v[j], y = v[j + 1];
+        fma2_rn(x, y, w[j], w[j + 1], d[j], d[j + 1]);
+        d[j] = x;
+        d[j + 1] = y;
+    }
+    if (kN % 2)
+        d[kN - 1] = __fmaf_rn(v[kN - 1], w[kN - 1], d[kN - 1]);
+}
+template <int kN> __device__ __forceinline__ float sum_of(const float (&v)[kN]) {
+    float x = v[0];
+#pragma unroll
+    for (int j = 1; j < kN; ++j)
+        x += v[j];
+    return x;
+}
+
+// Items are (token, up to `per` heads of one kind), of consecutive lanes.
+struct Item {
     int64_t t;
-    int kind, h0, heads;                 // heads: how many of the group exist
+    int kind, h0, heads;                 // heads: how many of them exist
     __device__ __forceinline__ Item(const NormArgs &a, int64_t item, int groups, int only) {
         const uint32_t token = (uint32_t)item / (uint32_t)groups;
         int g = (int)((uint32_t)item - token * (uint32_t)groups);
@@ -217,90 +294,97 @@ template <int kHeads> struct Item {
         if (only < 0 && kind == 1)
             g -= a.groups[0];
         const int first = kind == 0 ? 0 : a.q_heads, last = kind == 0 ? a.q_heads : a.heads;
-        h0 = first + g * kHeads;
-        heads = min(kHeads, last - h0);
+        h0 = first + g * a.per;
+        heads = min(a.per, last - h0);
     }
 };
 
+// What a token and a weight make of a pair's turn is the same for all heads of an
+// item: y_p = r (p w_p c - q w_q s), y_q = r (q w_q c + p w_p s), four factors a pair.
+// The next kHeads heads are loaded before the present ones are worked on.
 template <typename T, bool kHalves, int kVec, int kU, int kHeads>
 __global__ void __launch_bounds__(kThreads)
 k8_head_norm(const __grid_constant__ NormArgs a)
 {
-    using L = Lane<T, kHalves, kVec, kU, kHeads>;
+    using L = Lane<T, kHalves, kVec, kU>;
+    constexpr int kP = L::kPairs;
     pdl_trigger();
     pdl_wait();
     const int groups = a.groups[0] + a.groups[1];
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / a.lanes;
+    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> a.lanes_log2;
     const bool live = item < a.T * groups;               // (all lanes stay for the sums)
-    const Item<kHeads> it(a, live ? item : 0, groups, -1);
-    const int64_t pos = __ldg(a.positions + it.t);
-    const bool bad = pos < 0 || pos >= a.max_position;
+    const Item it(a, live ? item : 0, groups, -1);
+    const int heads = live ? it.heads : 0;
     const T *src = static_cast<const T *>(a.x) + it.t * a.x_row_stride + it.h0 * a.x_head_stride;
-    Run<T, kVec> v[kHeads][kU][L::kParts];
+    T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
+    typename L::Raw next[kHeads];
 #pragma unroll
     for (int k = 0; k < kHeads; ++k)
-        if (live && k < it.heads)
-            L::load(a, src + k * a.x_head_stride, v[k]);
-        else
+        L::load(a, k < heads ? src + k * a.x_head_stride : nullptr, next[k]);
+    const int64_t pos = __ldg(a.positions + it.t);
+    const bool bad = pos < 0 || pos >= a.max_position;
+    if (live && bad && it.h0 == 0 && (threadIdx.x & (a.lanes - 1)) == 0 && a.err != nullptr)
+        atomicAdd(a.err, 1);
+    float pp[kU][kP], pq[kU][kP], qp[kU][kP], qq[kU][kP];    // to p from p and from q, to q from p and from q
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+        float wp[kP], wq[kP];
+        L::table(a, pos, bad, i, pp[i], pq[i]);
+        L::weights(a, it.kind, i, wp, wq);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+            const float c = pp[i][j], s = pq[i][j];
+            pp[i][j] = wp[j] * c;
+            pq[i][j] = -(wq[j] * s);
+            qp[i][j] = wp[j] * s;
+            qq[i][j] = wq[j] * c;
+        }
+    }
+    for (int h = 0; h < a.per; h += kHeads) {
+        typename L::Raw now[kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k)
 #pragma unroll
             for (int i = 0; i < kU; ++i)
 #pragma unroll
                 for (int p = 0; p < L::kParts; ++p)
-                    v[k][i][p].clear();
-    if (live && bad && it.h0 == 0 && (threadIdx.x & (a.lanes - 1)) == 0 && a.err != nullptr)
-        atomicAdd(a.err, 1);
-    float r[kHeads];
+                    now[k][i][p] = next[k][i][p];
+        if (h + kHeads < a.per) {
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kU; ++i)
-#pragma unroll
-            for (int p = 0; p < L::kParts; ++p)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    sum = __fmaf_rn(v[k][i][p].at(j), v[k][i][p].at(j), sum);
-        r[k] = rsqrtf(__fmaf_rn(head_sum(sum, a.lanes), a.inv_width, a.eps));
-    }
-    if (!live)
-        return;
-    T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
-    const void *weight = a.weight[it.kind];
-#pragma unroll
-    for (int i = 0; i < kU; ++i) {
-        bool rot;
-        const int at = L::place(a, i, rot);
-        if (at < 0)
-            continue;
-        float c[L::kPairs], s[L::kPairs], w[L::kParts][kVec];
-        L::table(a, pos, at, rot && !bad, c, s);
-#pragma unroll
-        for (int p = 0; p < L::kParts; ++p) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                w[p][j] = 1.0f;
-            if (weight != nullptr && (p == 0 || rot))
-                values<kVec, L::kOne>(weight, a.weight_f32 != 0, at + p * (a.rot / 2), w[p]);
+            for (int k = 0; k < kHeads; ++k)
+                L::load(a, h + kHeads + k < heads ? src + (h + kHeads + k) * a.x_head_stride : nullptr, next[k]);
         }
 #pragma unroll
         for (int k = 0; k < kHeads; ++k) {
-            if (k >= it.heads)
-                break;
-            float y[L::kParts][kVec];
+            float p[kU][kP], q[kU][kP], squares[kP];
 #pragma unroll
-            for (int p = 0; p < L::kParts; ++p)
+            for (int j = 0; j < kP; ++j)
+                squares[j] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                    y[p][j] = v[k][i][p].at(j) * r[k] * w[p][j];
-            if (rot && !bad)
-                L::template rotate<false>(y, c, s);
+            for (int i = 0; i < kU; ++i) {
+                L::pairs(now[k][i], p[i], q[i]);
+                add_product(squares, p[i], p[i]);
+                add_product(squares, q[i], q[i]);
+            }
+            const float r = rsqrtf(__fmaf_rn(head_sum(sum_of(squares), a.lanes), a.inv_width, a.eps));
+            if (h + k >= heads)
+                continue;
+            T *head = dst + (h + k) * a.out_head_stride;
 #pragma unroll
-            for (int p = 0; p < L::kParts; ++p) {
-                if (p > 0 && !rot)
-                    continue;
-                Run<T, kVec> o;
-                o.set(y[p]);
-                o.template put<L::kOne>(dst + k * a.out_head_stride + at + p * (a.rot / 2));
+            for (int i = 0; i < kU; ++i) {
+                scale(p[i], r);
+                scale(q[i], r);
+                float y[kP], z[kP];
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    y[j] = p[i][j];
+                    z[j] = p[i][j];
+                }
+                times(y, pp[i]);
+                add_product(y, q[i], pq[i]);
+                times(z, qp[i]);
+                add_product(z, q[i], qq[i]);
+                L::store(a, head, i, y, z);
             }
         }
     }
@@ -310,119 +394,112 @@ k8_head_norm(const __grid_constant__ NormArgs a)
 // of dw is of one weight and of the same elements throughout; a kind's blocks take
 // its items in turn, and leave their sums, joined over the block's heads, in the
 // workspace, which k8_weight_grad adds up in the order of the blocks.
-template <typename T, bool kHalves, int kVec, int kU, int kHeads>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, bool kHalves, int kVec, int kU>
+__global__ void __launch_bounds__(kThreads, kU == 1 ? 2 : 1)
 k8_head_norm_grad(const __grid_constant__ NormArgs a)
 {
-    using L = Lane<T, kHalves, kVec, kU, kHeads>;
+    using L = Lane<T, kHalves, kVec, kU>;
+    constexpr int kP = L::kPairs;
     __shared__ float s_sum[kThreads / 32][kMaxNormDim];
     pdl_trigger();
     pdl_wait();
     const int kind = blockIdx.y, groups = a.groups[kind];
     const int64_t items = a.T * groups;
-    const int side = kThreads / a.lanes;                  // heads side by side in a block
-    const void *weight = a.weight[kind];
+    const int side = kThreads >> a.lanes_log2;            // heads side by side in a block
     const bool wanted = a.dweight[kind] != nullptr;
-    float w[kU][L::kParts][kVec], dw[kU][L::kParts][kVec];
+    float wp[kU][kP], wq[kU][kP], dp[kU][kP], dq[kU][kP];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-        bool rot;
-        const int at = L::place(a, i, rot);
+        L::weights(a, kind, i, wp[i], wq[i]);
 #pragma unroll
-        for (int p = 0; p < L::kParts; ++p) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                w[i][p][j] = 1.0f;
-                dw[i][p][j] = 0.0f;
-            }
-            if (weight != nullptr && at >= 0 && (p == 0 || rot))
-                values<kVec, L::kOne>(weight, a.weight_f32 != 0, at + p * (a.rot / 2), w[i][p]);
-        }
+        for (int j = 0; j < kP; ++j)
+            dp[i][j] = dq[i][j] = 0.0f;
     }
     // uniform over the block: all lanes stay for the sums
     for (int64_t base = (int64_t)blockIdx.x * side; base < items; base += (int64_t)gridDim.x * side) {
-        const int64_t item = base + threadIdx.x / a.lanes;
+        const int64_t item = base + (threadIdx.x >> a.lanes_log2);
         const bool live = item < items;
-        const Item<kHeads> it(a, live ? item : 0, groups, kind);
-        const int64_t pos = __ldg(a.positions + it.t);
-        const bool bad = pos < 0 || pos >= a.max_position;
+        const Item it(a, live ? item : 0, groups, kind);
+        const int heads = live ? it.heads : 0;
         const T *src = static_cast<const T *>(a.x) + it.t * a.x_row_stride + it.h0 * a.x_head_stride;
         const T *dsrc = static_cast<const T *>(a.dy) + it.t * a.dy_row_stride + it.h0 * a.dy_head_stride;
-        Run<T, kVec> v[kHeads][kU][L::kParts], d[kHeads][kU][L::kParts];
-#pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-            if (live && k < it.heads) {
-                L::load(a, src + k * a.x_head_stride, v[k]);
-                L::load(a, dsrc + k * a.dy_head_stride, d[k]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kU; ++i)
-#pragma unroll
-                    for (int p = 0; p < L::kParts; ++p) {
-                        v[k][i][p].clear();
-                        d[k][i][p].clear();
-                    }
-            }
-        }
+        T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
+        typename L::Raw vnext, dnext;
+        L::load(a, heads > 0 ? src : nullptr, vnext);
+        L::load(a, heads > 0 ? dsrc : nullptr, dnext);
+        const int64_t pos = __ldg(a.positions + it.t);
+        const bool bad = pos < 0 || pos >= a.max_position;
         if (live && bad && it.h0 == 0 && (threadIdx.x & (a.lanes - 1)) == 0 && a.err != nullptr)
             atomicAdd(a.err, 1);
-        float c[kU][L::kPairs], s[kU][L::kPairs];
+        float c[kU][kP], s[kU][kP];
 #pragma unroll
-        for (int i = 0; i < kU; ++i) {
-            bool rot;
-            const int at = L::place(a, i, rot);
-            L::table(a, pos, at, at >= 0 && rot && !bad, c[i], s[i]);
-        }
-        T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
+        for (int i = 0; i < kU; ++i)
+            L::table(a, pos, bad, i, c[i], s[i]);
+        for (int h = 0; h < a.per; ++h) {
+            typename L::Raw v, d;
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-            float g[kU][L::kParts][kVec], sum = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-                bool rot;
-                const int at = L::place(a, i, rot);
-#pragma unroll
-                for (int p = 0; p < L::kParts; ++p)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j)
-                        g[i][p][j] = d[k][i][p].at(j);
-                if (at >= 0 && rot && !bad)
-                    L::template rotate<true>(g[i], c[i], s[i]);
-#pragma unroll
-                for (int p = 0; p < L::kParts; ++p)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        const float x = v[k][i][p].at(j);
-                        sum = __fmaf_rn(x, x, sum);
-                        dot = __fmaf_rn(g[i][p][j] * w[i][p][j], x, dot);
-                    }
-            }
-            const float r = rsqrtf(__fmaf_rn(head_sum(sum, a.lanes), a.inv_width, a.eps));
-            const float along = head_sum(dot, a.lanes) * r * a.inv_width;        // mean(g w n)
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-                bool rot;
-                const int at = L::place(a, i, rot);
-                float y[L::kParts][kVec];
-#pragma unroll
-                for (int p = 0; p < L::kParts; ++p)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        const float n = v[k][i][p].at(j) * r;
-                        if (live && k < it.heads)         // (else r may be infinite)
-                            dw[i][p][j] = __fmaf_rn(g[i][p][j], n, dw[i][p][j]);
-                        y[p][j] = r * __fmaf_rn(g[i][p][j], w[i][p][j], -(n * along));
-                    }
-                if (!live || at < 0 || k >= it.heads)
-                    continue;
+            for (int i = 0; i < kU; ++i)
 #pragma unroll
                 for (int p = 0; p < L::kParts; ++p) {
-                    if (p > 0 && !rot)
-                        continue;
-                    Run<T, kVec> o;
-                    o.set(y[p]);
-                    o.template put<L::kOne>(dst + k * a.out_head_stride + at + p * (a.rot / 2));
+                    v[i][p] = vnext[i][p];
+                    d[i][p] = dnext[i][p];
                 }
+            if (h + 1 < a.per) {
+                L::load(a, h + 1 < heads ? src + (h + 1) * a.x_head_stride : nullptr, vnext);
+                L::load(a, h + 1 < heads ? dsrc + (h + 1) * a.dy_head_stride : nullptr, dnext);
+            }
+            float p[kU][kP], q[kU][kP], g[kU][kP], k[kU][kP], squares[kP], dots[kP];   // x, the gradient of n w
+#pragma unroll
+            for (int j = 0; j < kP; ++j)
+                squares[j] = dots[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                L::pairs(v[i], p[i], q[i]);
+                float e[kP], f[kP];                       // dy, turned back
+                L::pairs(d[i], e, f);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    g[i][j] = e[j];
+                    k[i][j] = -e[j];
+                }
+                times(g[i], c[i]);
+                add_product(g[i], f, s[i]);
+                times(k[i], s[i]);
+                add_product(k[i], f, c[i]);
+                add_product(squares, p[i], p[i]);
+                add_product(squares, q[i], q[i]);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    e[j] = g[i][j];
+                    f[j] = k[i][j];
+                }
+                times(e, wp[i]);
+                times(f, wq[i]);
+                add_product(dots, e, p[i]);
+                add_product(dots, f, q[i]);
+            }
+            const float r = rsqrtf(__fmaf_rn(head_sum(sum_of(squares), a.lanes), a.inv_width, a.eps));
+            const float along = -(head_sum(sum_of(dots), a.lanes) * r * a.inv_width);   // -mean(g w n)
+            if (h >= heads)                               // (then r may be infinite)
+                continue;
+            T *head = dst + h * a.out_head_stride;
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                scale(p[i], r);                           // n
+                scale(q[i], r);
+                add_product(dp[i], g[i], p[i]);
+                add_product(dq[i], k[i], q[i]);
+                times(g[i], wp[i]);
+                times(k[i], wq[i]);
+                float m[kP];
+#pragma unroll
+                for (int j = 0; j < kP; ++j)
+                    m[j] = along;
+                add_product(g[i], p[i], m);
+                add_product(k[i], q[i], m);
+                scale(g[i], r);
+                scale(k[i], r);
+                L::store(a, head, i, g[i], k[i]);
             }
         }
     }
@@ -435,15 +512,18 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
         bool rot;
         const int at = L::place(a, i, rot);
 #pragma unroll
-        for (int p = 0; p < L::kParts; ++p)
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                float x = dw[i][p][j];
-                for (int o = 16; o >= a.lanes; o >>= 1)
-                    x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-                if (at >= 0 && lane < a.lanes && (p == 0 || rot))
-                    s_sum[warp][at + p * (a.rot / 2) + j] = x;
+        for (int j = 0; j < kP; ++j) {
+            float x = dp[i][j], y = dq[i][j];
+            for (int o = 16; o >= a.lanes; o >>= 1) {
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+                y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
             }
+            if (at >= 0 && lane < a.lanes) {
+                s_sum[warp][kHalves ? at + j : at + 2 * j] = x;
+                if (!kHalves || rot)
+                    s_sum[warp][kHalves ? at + a.rot / 2 + j : at + 2 * j + 1] = y;
+            }
+        }
     }
     __syncthreads();
     float *part = a.partial + ((int64_t)kind * a.blocks + blockIdx.x) * a.width;
@@ -485,16 +565,30 @@ k8_weight_grad(const __grid_constant__ NormArgs a)
 
 constexpr int kGradBlocksPerSm = 4;
 
+// Heads of an item: the most, up to `most`, with which hardly a place stays empty.
+int heads_of_item(int q_heads, int k_heads, int most)
+{
+    const int heads = q_heads + k_heads;
+    for (int per = most; per > 1; --per)
+        if (((q_heads + per - 1) / per + (k_heads + per - 1) / per) * per - heads <= heads / 16)
+            return per;
+    return 1;
+}
+
 template <typename T, bool kHalves, int kVec, int kU, int kHeads>
-cudaError_t launch_kind(const HeadNormLaunch &p, int units, int num_sms, cudaStream_t stream)
+cudaError_t launch_kind(const HeadNormLaunch &p, int units, int most, int num_sms, cudaStream_t stream)
 {
     NormArgs a{};
     static_cast<HeadNormLaunch &>(a) = p;
     a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < units)
+    while (a.lanes < 32 && a.lanes < units) {
         a.lanes *= 2;
-    a.groups[0] = (p.q_heads + kHeads - 1) / kHeads;
-    a.groups[1] = (p.heads - p.q_heads + kHeads - 1) / kHeads;
+        ++a.lanes_log2;
+    }
+    const int k_heads = p.heads - p.q_heads;
+    a.per = heads_of_item(p.q_heads, k_heads, most);
+    a.groups[0] = (p.q_heads + a.per - 1) / a.per;
+    a.groups[1] = (k_heads + a.per - 1) / a.per;
     a.inv_width = 1.0f / (float)p.width;
     if (p.dy == nullptr) {
         const int64_t threads = p.T * (a.groups[0] + a.groups[1]) * a.lanes;
@@ -507,8 +601,7 @@ cudaError_t launch_kind(const HeadNormLaunch &p, int units, int num_sms, cudaStr
     a.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((items + side - 1) / side, (int64_t)num_sms * kGradBlocksPerSm));
     cudaError_t e = cudaSuccess;
     if (p.T > 0)
-        e = launch_pdl(k8_head_norm_grad<T, kHalves, kVec, kU, kHeads>, dim3((unsigned)a.blocks, 2), dim3(kThreads), 0,
-                       stream, 1, a);
+        e = launch_pdl(k8_head_norm_grad<T, kHalves, kVec, kU>, dim3((unsigned)a.blocks, 2), dim3(kThreads), 0, stream, 1, a);
     if (e == cudaSuccess && weights)
         e = launch_pdl(k8_weight_grad, dim3((unsigned)((p.width + 31) / 32), 2), dim3(kThreads), 0, stream, 1, a);
     return e;
@@ -520,16 +613,16 @@ cudaError_t launch_type(const HeadNormLaunch &a, bool wide, int num_sms, cudaStr
     constexpr int kWide = 16 / (int)sizeof(T), kNarrow = kHalves ? 1 : 2;
     const int vec = wide ? kWide : kNarrow;
     const int units = (kHalves ? a.rot / (2 * vec) : a.rot / vec) + (a.width - a.rot) / vec;
+    // Several heads an item, whose table columns and weights are read once, where
+    // there is work to fill the GPU that way.
+    const int64_t threads = a.T * a.heads * units;
+    const int most = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads / ((int64_t)num_sms * 2048)));
     if (!wide)                              // up to 511 units of an element or two
-        return launch_kind<T, kHalves, kNarrow, 16, 1>(a, units, num_sms, stream);
+        return launch_kind<T, kHalves, kNarrow, 16, 1>(a, units, 1, num_sms, stream);
     if (units > 32)                         // up to 128
-        return launch_kind<T, kHalves, kWide, 4, 1>(a, units, num_sms, stream);
-    // Several heads a thread, whose table columns are read once, where there is
-    // work to fill the GPU that way.
-    constexpr int kMany = 2;
-    const bool many = a.T * a.heads * units >= (int64_t)kMany * num_sms * 2048;
-    return many ? launch_kind<T, kHalves, kWide, 1, kMany>(a, units, num_sms, stream)
-                : launch_kind<T, kHalves, kWide, 1, 1>(a, units, num_sms, stream);
+        return launch_kind<T, kHalves, kWide, 4, 1>(a, units, most, num_sms, stream);
+    return most > 1 ? launch_kind<T, kHalves, kWide, 1, 2>(a, units, most, num_sms, stream)
+                    : launch_kind<T, kHalves, kWide, 1, 1>(a, units, 1, num_sms, stream);
 }
 
 }  // namespace
