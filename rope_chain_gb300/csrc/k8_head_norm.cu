@@ -9,6 +9,7 @@
 // Bound by memory: forward one read and one write of every element, backward two
 // reads (r is made again from x, which the gradient needs anyway) and one write.
 #include "rc_paged.cuh"
+#include "rc_tcgen05.cuh"
 
 #include <algorithm>
 
@@ -55,6 +56,10 @@ template <typename T, int kN> struct Run {
                 reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
         }
     }
+    __device__ __forceinline__ void from_shared(uint32_t at) {      // 16 bytes
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1 % kWords]), "=r"(w[2 % kWords]), "=r"(w[3 % kWords]) : "r"(at) : "memory");
+    }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
@@ -75,6 +80,14 @@ template <typename T, int kN> struct Run {
         }
     }
 };
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 // kN values at element `at` of a bf16 or FP32 array; kOne: it is aligned to the
 // bytes of kN of its elements (at most 16).
@@ -173,6 +186,34 @@ template <typename T, bool kHalves, int kVec, int kU> struct Lane {
                 v[i][0].template get<kOne>(head + at);
                 if (kHalves && rot)
                     v[i][kParts - 1].template get<kOne>(head + at + a.rot / 2);
+            }
+        }
+    }
+    // The same through shared memory (16-byte accesses): copied there ahead, into the
+    // lane's own places from `to` on, kThreads * 16 bytes apart, and read by it alone.
+    static constexpr uint32_t kBytes = kU * kParts * kThreads * 16;
+    static __device__ __forceinline__ void copy(const NormArgs &a, const T *head, uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            bool rot;
+            const int at = place(a, i, rot);
+            if (head == nullptr || at < 0)
+                continue;
+            copy16(to + (i * kParts) * (kThreads * 16), head + at);
+            if (kHalves && rot)
+                copy16(to + (i * kParts + 1) * (kThreads * 16), head + at + a.rot / 2);
+        }
+    }
+    static __device__ __forceinline__ void copied(const NormArgs &a, bool there, uint32_t from, Raw &v) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i) {
+            bool rot;
+            const int at = place(a, i, rot);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                v[i][p].clear();
+                if (there && at >= 0 && (p == 0 || rot))
+                    v[i][p].from_shared(from + (i * kParts + p) * (kThreads * 16));
             }
         }
     }
@@ -301,13 +342,17 @@ struct Item {
 
 // What a token and a weight make of a pair's turn is the same for all heads of an
 // item: y_p = r (p w_p c - q w_q s), y_q = r (q w_q c + p w_p s), four factors a pair.
-// The next kHeads heads are loaded before the present ones are worked on.
-template <typename T, bool kHalves, int kVec, int kU, int kHeads>
-__global__ void __launch_bounds__(kThreads)
+// Heads come through a ring of kStages copies per lane in shared memory (kRing), which
+// no other lane reads, so nothing is waited for but the copy; or, with an item of one
+// head or in narrow accesses, straight into registers.
+constexpr int kStages = 4;
+template <typename T, bool kHalves, int kVec, int kU, bool kRing>
+__global__ void __launch_bounds__(kThreads, kRing ? 3 : 1)
 k8_head_norm(const __grid_constant__ NormArgs a)
 {
     using L = Lane<T, kHalves, kVec, kU>;
     constexpr int kP = L::kPairs;
+    extern __shared__ __align__(16) uint8_t s_ring[];
     pdl_trigger();
     pdl_wait();
     const int groups = a.groups[0] + a.groups[1];
@@ -317,10 +362,17 @@ k8_head_norm(const __grid_constant__ NormArgs a)
     const int heads = live ? it.heads : 0;
     const T *src = static_cast<const T *>(a.x) + it.t * a.x_row_stride + it.h0 * a.x_head_stride;
     T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
-    typename L::Raw next[kHeads];
+    typename L::Raw v;
+    const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+    if constexpr (kRing) {
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k)
-        L::load(a, k < heads ? src + k * a.x_head_stride : nullptr, next[k]);
+        for (int h = 0; h < kStages - 1; ++h) {
+            L::copy(a, h < heads ? src + h * a.x_head_stride : nullptr, ring + h * L::kBytes);
+            copy_commit();
+        }
+    } else {
+        L::load(a, heads > 0 ? src : nullptr, v);
+    }
     const int64_t pos = __ldg(a.positions + it.t);
     const bool bad = pos < 0 || pos >= a.max_position;
     if (live && bad && it.h0 == 0 && (threadIdx.x & (a.lanes - 1)) == 0 && a.err != nullptr)
@@ -340,52 +392,49 @@ k8_head_norm(const __grid_constant__ NormArgs a)
             qq[i][j] = wq[j] * c;
         }
     }
-    for (int h = 0; h < a.per; h += kHeads) {
-        typename L::Raw now[kHeads];
-#pragma unroll
-        for (int k = 0; k < kHeads; ++k)
-#pragma unroll
-            for (int i = 0; i < kU; ++i)
-#pragma unroll
-                for (int p = 0; p < L::kParts; ++p)
-                    now[k][i][p] = next[k][i][p];
-        if (h + kHeads < a.per) {
-#pragma unroll
-            for (int k = 0; k < kHeads; ++k)
-                L::load(a, h + kHeads + k < heads ? src + (h + kHeads + k) * a.x_head_stride : nullptr, next[k]);
+    int st = 0;
+    for (int h = 0; h < (kRing ? a.per : 1); ++h) {
+        if constexpr (kRing) {
+            copy_wait<kStages - 2>();
+            L::copied(a, h < heads, ring + st * L::kBytes, v);
         }
+        float p[kU][kP], q[kU][kP], squares[kP];
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-            float p[kU][kP], q[kU][kP], squares[kP];
+        for (int j = 0; j < kP; ++j)
+            squares[j] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kP; ++j)
-                squares[j] = 0.0f;
+        for (int i = 0; i < kU; ++i) {
+            L::pairs(v[i], p[i], q[i]);
+            add_product(squares, p[i], p[i]);
+            add_product(squares, q[i], q[i]);
+        }
+        const float sum = head_sum(sum_of(squares), a.lanes);
+        if constexpr (kRing) {
+            // into the place of the head before, long read
+            const int next = h + kStages - 1;
+            L::copy(a, next < heads ? src + next * a.x_head_stride : nullptr, ring + ((st + kStages - 1) % kStages) * L::kBytes);
+            copy_commit();
+            st = st + 1 == kStages ? 0 : st + 1;
+        }
+        const float r = rsqrtf(__fmaf_rn(sum, a.inv_width, a.eps));
+        if (h >= heads)
+            continue;
+        T *head = dst + h * a.out_head_stride;
 #pragma unroll
-            for (int i = 0; i < kU; ++i) {
-                L::pairs(now[k][i], p[i], q[i]);
-                add_product(squares, p[i], p[i]);
-                add_product(squares, q[i], q[i]);
+        for (int i = 0; i < kU; ++i) {
+            scale(p[i], r);
+            scale(q[i], r);
+            float y[kP], z[kP];
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+                y[j] = p[i][j];
+                z[j] = p[i][j];
             }
-            const float r = rsqrtf(__fmaf_rn(head_sum(sum_of(squares), a.lanes), a.inv_width, a.eps));
-            if (h + k >= heads)
-                continue;
-            T *head = dst + (h + k) * a.out_head_stride;
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-                scale(p[i], r);
-                scale(q[i], r);
-                float y[kP], z[kP];
-#pragma unroll
-                for (int j = 0; j < kP; ++j) {
-                    y[j] = p[i][j];
-                    z[j] = p[i][j];
-                }
-                times(y, pp[i]);
-                add_product(y, q[i], pq[i]);
-                times(z, qp[i]);
-                add_product(z, q[i], qq[i]);
-                L::store(a, head, i, y, z);
-            }
+            times(y, pp[i]);
+            add_product(y, q[i], pq[i]);
+            times(z, qp[i]);
+            add_product(z, q[i], qq[i]);
+            L::store(a, head, i, y, z);
         }
     }
 }
@@ -394,12 +443,18 @@ k8_head_norm(const __grid_constant__ NormArgs a)
 // of dw is of one weight and of the same elements throughout; a kind's blocks take
 // its items in turn, and leave their sums, joined over the block's heads, in the
 // workspace, which k8_weight_grad adds up in the order of the blocks.
-template <typename T, bool kHalves, int kVec, int kU>
-__global__ void __launch_bounds__(kThreads, kU == 1 ? 2 : 1)
+// The heads' x and dy come through the ring, which runs on from item to item.
+// Blocks that an SM holds, and as many of a kind are launched: more of them only begin
+// and end more often.
+constexpr int kMaxGradPerSm = 2;
+template <typename T, bool kHalves, int kU> constexpr int kGradPerSm = kU > 2 ? 1 : kMaxGradPerSm;
+template <typename T, bool kHalves, int kVec, int kU, bool kRing>
+__global__ void __launch_bounds__(kThreads, kGradPerSm<T, kHalves, kU>)
 k8_head_norm_grad(const __grid_constant__ NormArgs a)
 {
     using L = Lane<T, kHalves, kVec, kU>;
     constexpr int kP = L::kPairs;
+    extern __shared__ __align__(16) uint8_t s_ring[];
     __shared__ float s_sum[kThreads / 32][kMaxNormDim];
     pdl_trigger();
     pdl_wait();
@@ -415,8 +470,41 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
         for (int j = 0; j < kP; ++j)
             dp[i][j] = dq[i][j] = 0.0f;
     }
+    const uint32_t ring = smem_u32(s_ring) + threadIdx.x * 16;
+    const int64_t stride = (int64_t)gridDim.x * side, mine = (int64_t)blockIdx.x * side + (threadIdx.x >> a.lanes_log2);
+    // the head that is copied next: item `ahead`, head h_ahead of it
+    int64_t ahead = mine;
+    int h_ahead = 0, heads_ahead = 0;
+    const T *x_ahead = nullptr, *dy_ahead = nullptr;
+    auto copy_next = [&](int st) {
+        if (h_ahead == 0) {
+            heads_ahead = 0;
+            if (ahead < items) {
+                const Item it(a, ahead, groups, kind);
+                heads_ahead = it.heads;
+                x_ahead = static_cast<const T *>(a.x) + it.t * a.x_row_stride + it.h0 * a.x_head_stride;
+                dy_ahead = static_cast<const T *>(a.dy) + it.t * a.dy_row_stride + it.h0 * a.dy_head_stride;
+            }
+        }
+        const bool there = h_ahead < heads_ahead;
+        L::copy(a, there ? x_ahead : nullptr, ring + (2 * st) * L::kBytes);
+        L::copy(a, there ? dy_ahead : nullptr, ring + (2 * st + 1) * L::kBytes);
+        copy_commit();
+        x_ahead += a.x_head_stride;
+        dy_ahead += a.dy_head_stride;
+        if (++h_ahead == a.per) {
+            h_ahead = 0;
+            ahead += stride;
+        }
+    };
+    if constexpr (kRing) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i)
+            copy_next(i);
+    }
+    int st = 0;
     // uniform over the block: all lanes stay for the sums
-    for (int64_t base = (int64_t)blockIdx.x * side; base < items; base += (int64_t)gridDim.x * side) {
+    for (int64_t base = (int64_t)blockIdx.x * side; base < items; base += stride) {
         const int64_t item = base + (threadIdx.x >> a.lanes_log2);
         const bool live = item < items;
         const Item it(a, live ? item : 0, groups, kind);
@@ -424,9 +512,6 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
         const T *src = static_cast<const T *>(a.x) + it.t * a.x_row_stride + it.h0 * a.x_head_stride;
         const T *dsrc = static_cast<const T *>(a.dy) + it.t * a.dy_row_stride + it.h0 * a.dy_head_stride;
         T *dst = static_cast<T *>(a.out) + it.t * a.out_row_stride + it.h0 * a.out_head_stride;
-        typename L::Raw vnext, dnext;
-        L::load(a, heads > 0 ? src : nullptr, vnext);
-        L::load(a, heads > 0 ? dsrc : nullptr, dnext);
         const int64_t pos = __ldg(a.positions + it.t);
         const bool bad = pos < 0 || pos >= a.max_position;
         if (live && bad && it.h0 == 0 && (threadIdx.x & (a.lanes - 1)) == 0 && a.err != nullptr)
@@ -437,16 +522,13 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
             L::table(a, pos, bad, i, c[i], s[i]);
         for (int h = 0; h < a.per; ++h) {
             typename L::Raw v, d;
-#pragma unroll
-            for (int i = 0; i < kU; ++i)
-#pragma unroll
-                for (int p = 0; p < L::kParts; ++p) {
-                    v[i][p] = vnext[i][p];
-                    d[i][p] = dnext[i][p];
-                }
-            if (h + 1 < a.per) {
-                L::load(a, h + 1 < heads ? src + (h + 1) * a.x_head_stride : nullptr, vnext);
-                L::load(a, h + 1 < heads ? dsrc + (h + 1) * a.dy_head_stride : nullptr, dnext);
+            if constexpr (kRing) {
+                copy_wait<kStages - 2>();
+                L::copied(a, h < heads, ring + (2 * st) * L::kBytes, v);
+                L::copied(a, h < heads, ring + (2 * st + 1) * L::kBytes, d);
+            } else {
+                L::load(a, h < heads ? src + h * a.x_head_stride : nullptr, v);
+                L::load(a, h < heads ? dsrc + h * a.dy_head_stride : nullptr, d);
             }
             float p[kU][kP], q[kU][kP], g[kU][kP], k[kU][kP], squares[kP], dots[kP];   // x, the gradient of n w
 #pragma unroll
@@ -480,6 +562,10 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
             }
             const float r = rsqrtf(__fmaf_rn(head_sum(sum_of(squares), a.lanes), a.inv_width, a.eps));
             const float along = -(head_sum(sum_of(dots), a.lanes) * r * a.inv_width);   // -mean(g w n)
+            if constexpr (kRing) {
+                copy_next((st + kStages - 1) % kStages);  // into the place of the head before, long read
+                st = st + 1 == kStages ? 0 : st + 1;
+            }
             if (h >= heads)                               // (then r may be infinite)
                 continue;
             T *head = dst + h * a.out_head_stride;
@@ -536,12 +622,13 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
     }
 }
 
-// dw from the blocks' sums: a block has 32 columns, its warps take every eighth
-// part each and are joined in order.
-__global__ void __launch_bounds__(kThreads)
+// dw from the blocks' sums: a block has 32 columns, its warps take every 32nd part
+// each, several at once, and are joined in order.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
 k8_weight_grad(const __grid_constant__ NormArgs a)
 {
-    __shared__ float s_sum[kThreads / 32][32];
+    __shared__ float s_sum[kJoinWarps][32];
     pdl_trigger();
     pdl_wait();
     const int kind = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
@@ -550,20 +637,21 @@ k8_weight_grad(const __grid_constant__ NormArgs a)
     float x = 0.0f;
     // (no block of a kind without heads has left any)
     const int blocks = a.groups[kind] > 0 && a.T > 0 ? a.blocks : 0;
-    if (e < a.width)
-        for (int b = warp; b < blocks; b += kThreads / 32)
-            x += a.partial[((int64_t)kind * a.blocks + b) * a.width + e];
+    const float *part = a.partial + (int64_t)kind * a.blocks * a.width + e;
+    if (e < a.width) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kJoinWarps)
+            x += part[(int64_t)b * a.width];
+    }
     s_sum[warp][lane] = x;
     __syncthreads();
     if (warp == 0 && e < a.width) {
 #pragma unroll
-        for (int k = 1; k < kThreads / 32; ++k)
+        for (int k = 1; k < kJoinWarps; ++k)
             x += s_sum[k][lane];
         a.dweight[kind][e] = x;
     }
 }
-
-constexpr int kGradBlocksPerSm = 4;
 
 // Heads of an item: the most, up to `most`, with which hardly a place stays empty.
 int heads_of_item(int q_heads, int k_heads, int most)
@@ -575,35 +663,44 @@ int heads_of_item(int q_heads, int k_heads, int most)
     return 1;
 }
 
-template <typename T, bool kHalves, int kVec, int kU, int kHeads>
+template <typename T, bool kHalves, int kVec, int kU, bool kRing>
 cudaError_t launch_kind(const HeadNormLaunch &p, int units, int most, int num_sms, cudaStream_t stream)
 {
     NormArgs a{};
     static_cast<HeadNormLaunch &>(a) = p;
     a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < units) {
+    while (a.lanes < 32 && a.lanes * (kU == 2 ? 2 : 1) < units) {
         a.lanes *= 2;
         ++a.lanes_log2;
     }
     const int k_heads = p.heads - p.q_heads;
-    a.per = heads_of_item(p.q_heads, k_heads, most);
+    a.per = kRing ? heads_of_item(p.q_heads, k_heads, most) : 1;
     a.groups[0] = (p.q_heads + a.per - 1) / a.per;
     a.groups[1] = (k_heads + a.per - 1) / a.per;
     a.inv_width = 1.0f / (float)p.width;
+    constexpr size_t kSmem = kRing ? kStages * Lane<T, kHalves, kVec, kU>::kBytes : 0;
+    static bool configured[2][64] = {};
     if (p.dy == nullptr) {
+        const auto kernel = k8_head_norm<T, kHalves, kVec, kU, kRing>;
+        const cudaError_t e = kRing ? allow_smem(kernel, kSmem, configured[0]) : cudaSuccess;
+        if (e != cudaSuccess)
+            return e;
         const int64_t threads = p.T * (a.groups[0] + a.groups[1]) * a.lanes;
-        return launch_pdl(k8_head_norm<T, kHalves, kVec, kU, kHeads>, dim3((unsigned)((threads + kThreads - 1) / kThreads)),
-                          dim3(kThreads), 0, stream, 1, a);
+        return launch_pdl(kernel, dim3((unsigned)((threads + kThreads - 1) / kThreads)), dim3(kThreads), kSmem, stream, 1, a);
     }
     const bool weights = a.dweight[0] != nullptr || a.dweight[1] != nullptr;
     const int side = kThreads / a.lanes;
     const int64_t items = p.T * std::max(a.groups[0], a.groups[1]);
-    a.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((items + side - 1) / side, (int64_t)num_sms * kGradBlocksPerSm));
+    a.blocks = (int)std::max<int64_t>(1, std::min<int64_t>((items + side - 1) / side, (int64_t)num_sms * kGradPerSm<T, kHalves, kU>));
     cudaError_t e = cudaSuccess;
-    if (p.T > 0)
-        e = launch_pdl(k8_head_norm_grad<T, kHalves, kVec, kU>, dim3((unsigned)a.blocks, 2), dim3(kThreads), 0, stream, 1, a);
+    if (p.T > 0) {
+        const auto kernel = k8_head_norm_grad<T, kHalves, kVec, kU, kRing>;
+        e = kRing ? allow_smem(kernel, 2 * kSmem, configured[1]) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = launch_pdl(kernel, dim3((unsigned)a.blocks, 2), dim3(kThreads), 2 * kSmem, stream, 1, a);
+    }
     if (e == cudaSuccess && weights)
-        e = launch_pdl(k8_weight_grad, dim3((unsigned)((p.width + 31) / 32), 2), dim3(kThreads), 0, stream, 1, a);
+        e = launch_pdl(k8_weight_grad, dim3((unsigned)((p.width + 31) / 32), 2), dim3(32 * kJoinWarps), 0, stream, 1, a);
     return e;
 }
 
@@ -618,18 +715,21 @@ cudaError_t launch_type(const HeadNormLaunch &a, bool wide, int num_sms, cudaStr
     const int64_t threads = a.T * a.heads * units;
     const int most = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads / ((int64_t)num_sms * 2048)));
     if (!wide)                              // up to 511 units of an element or two
-        return launch_kind<T, kHalves, kNarrow, 16, 1>(a, units, 1, num_sms, stream);
+        return launch_kind<T, kHalves, kNarrow, 16, false>(a, units, 1, num_sms, stream);
     if (units > 32)                         // up to 128
-        return launch_kind<T, kHalves, kWide, 4, 1>(a, units, most, num_sms, stream);
-    return most > 1 ? launch_kind<T, kHalves, kWide, 1, 2>(a, units, most, num_sms, stream)
-                    : launch_kind<T, kHalves, kWide, 1, 1>(a, units, 1, num_sms, stream);
+        return launch_kind<T, kHalves, kWide, 4, false>(a, units, 1, num_sms, stream);
+    // (the gradient in pairs: two units a lane)
+    if (most > 1 && !kHalves && a.dy != nullptr && units > 1)
+        return launch_kind<T, kHalves, kWide, kHalves ? 1 : 2, true>(a, units, most, num_sms, stream);
+    return most > 1 ? launch_kind<T, kHalves, kWide, 1, true>(a, units, most, num_sms, stream)
+                    : launch_kind<T, kHalves, kWide, 1, false>(a, units, 1, num_sms, stream);
 }
 
 }  // namespace
 
 size_t head_norm_grad_workspace(int32_t width, int num_sms)
 {
-    return (size_t)2 * num_sms * kGradBlocksPerSm * width * sizeof(float);
+    return (size_t)2 * num_sms * kMaxGradPerSm * width * sizeof(float);
 }
 
 cudaError_t launch_head_norm_rope(const HeadNormLaunch &a, bool f32, bool halves, bool wide, int num_sms,

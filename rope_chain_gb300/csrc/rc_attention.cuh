@@ -548,17 +548,6 @@ k5_join(const __grid_constant__ Args a)
             total == 0.0f ? -INFINITY : __fmaf_rn(top, kLn2, logf(total));
 }
 
-template <typename Kernel> cudaError_t allow_smem(Kernel kernel, size_t bytes, bool (&configured)[64]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && configured[dev]))
-        return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64)
-        configured[dev] = true;
-    return e;
-}
-
 template <int kRows, bool kWindow, bool kCache4>
 cudaError_t launch_join(const Args &a, int ctas, cudaStream_t stream, const char **why) {
     if (a.partial == nullptr)

@@ -5,6 +5,18 @@
 
 namespace rc {
 
+// Dynamic shared memory of `bytes` allowed for a kernel, once per device.
+template <typename Kernel> inline cudaError_t allow_smem(Kernel kernel, size_t bytes, bool (&configured)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && configured[dev]))
+        return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64)
+        configured[dev] = true;
+    return e;
+}
+
 constexpr int kMaxNormDim = 512;
 
 // Norm and rotation of T tokens of `heads` heads (strides in elements), and with
