@@ -152,6 +152,18 @@ def test_slots_past_the_cache_are_counted():
     assert int(err) == 4 and not bool(got[[1, 3, 4]].any()) and bool(got[[0, 2, 5]].any())
 
 
+@pytest.mark.parametrize("T", [5, 40000])
+def test_outputs_aligned_to_16_bytes(T):
+    cache, scales = fresh(2500, 4, 16)
+    slots = torch.randint(0, 40000, (T,), device=DEV)
+    want = rc.kv4_load(slots, cache, scales)
+    flat = torch.zeros(T * 512 + 8, dtype=BF, device=DEV)
+    out = flat[8:].view(T, 4, 128)
+    assert out.data_ptr() % 32 == 16
+    assert rc.kv4_load(slots, cache, scales, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want) and not bool(flat[:8].any())
+
+
 def test_nothing_to_store_or_load():
     cache, scales = fresh(2, 3, 4)
     none = torch.empty(0, dtype=I64, device=DEV)
