@@ -347,7 +347,7 @@ struct Item {
 // head or in narrow accesses, straight into registers.
 constexpr int kStages = 4;
 template <typename T, bool kHalves, int kVec, int kU, bool kRing>
-__global__ void __launch_bounds__(kThreads, kRing ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, kRing && kU == 1 ? 3 : 1)
 k8_head_norm(const __grid_constant__ NormArgs a)
 {
     using L = Lane<T, kHalves, kVec, kU>;
@@ -447,7 +447,7 @@ k8_head_norm(const __grid_constant__ NormArgs a)
 // Blocks that an SM holds, and as many of a kind are launched: more of them only begin
 // and end more often.
 constexpr int kMaxGradPerSm = 2;
-template <typename T, bool kHalves, int kU> constexpr int kGradPerSm = kU > 2 ? 1 : kMaxGradPerSm;
+template <typename T, bool kHalves, int kU> constexpr int kGradPerSm = kU > 2 || (kHalves && kU == 2) ? 1 : kMaxGradPerSm;
 template <typename T, bool kHalves, int kVec, int kU, bool kRing>
 __global__ void __launch_bounds__(kThreads, kGradPerSm<T, kHalves, kU>)
 k8_head_norm_grad(const __grid_constant__ NormArgs a)
@@ -716,11 +716,11 @@ cudaError_t launch_type(const HeadNormLaunch &a, bool wide, int num_sms, cudaStr
     const int most = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads / ((int64_t)num_sms * 2048)));
     if (!wide)                              // up to 511 units of an element or two
         return launch_kind<T, kHalves, kNarrow, 16, false>(a, units, 1, num_sms, stream);
-    if (units > 32)                         // up to 128
+    if (units > 64)                         // up to 128
         return launch_kind<T, kHalves, kWide, 4, false>(a, units, 1, num_sms, stream);
-    // (the gradient in pairs: two units a lane)
-    if (most > 1 && !kHalves && a.dy != nullptr && units > 1)
-        return launch_kind<T, kHalves, kWide, kHalves ? 1 : 2, true>(a, units, most, num_sms, stream);
+    if (units > 32 || (most > 1 && !kHalves && a.dy != nullptr && units > 1))    // (the gradient in pairs: two units a lane)
+        return most > 1 ? launch_kind<T, kHalves, kWide, 2, true>(a, units, most, num_sms, stream)
+                        : launch_kind<T, kHalves, kWide, 2, false>(a, units, 1, num_sms, stream);
     return most > 1 ? launch_kind<T, kHalves, kWide, 1, true>(a, units, most, num_sms, stream)
                     : launch_kind<T, kHalves, kWide, 1, false>(a, units, 1, num_sms, stream);
 }

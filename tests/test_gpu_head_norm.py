@@ -168,11 +168,13 @@ def test_strides_and_alignment(kw, layout, dtype):
     assert bool((out[:, :, 0] == 7).all()) and bool((out[:, :, 65:] == 7).all())
 
 
-@pytest.mark.parametrize("T,heads,d", [(3000, 40, 128), (9000, 16, 64), (2500, 33, 96)])
+@pytest.mark.parametrize("T,heads,d,dtype", [(3000, 40, 128, BF), (9000, 16, 64, BF), (2500, 33, 96, BF), (1500, 20, 256, F32), (900, 24, 512, BF),
+                                             (2000, 17, 128, F32)])
 @pytest.mark.parametrize("layout", [PAIRS, HALVES])
-def test_much_work(T, heads, d, layout):
-    """Several heads a thread, of odd numbers of query and key heads."""
-    c = Case(T, heads, d, d, BF, layout, weight=BF, q_heads=heads - 7)
+@pytest.mark.parametrize("rot", [64, 0])
+def test_much_work(T, heads, d, layout, dtype, rot):
+    """Several heads an item, of odd numbers of query and key heads."""
+    c = Case(T, heads, d, rot or d, dtype, layout, weight=dtype, q_heads=heads - 7)
     c.check_forward(c.run())
     dx, dq, dk = c.grad()
     c.check_grad(dx, dq, dk)
@@ -293,6 +295,32 @@ def test_captured_with_its_gradients():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want[0]) and all(torch.equal(a, b) for a, b in zip(grads, want[1]))
+
+
+def test_captured_backward_pass():
+    """autograd's own, once the warm-up's graphs are gone."""
+    c = Case(64, 6, 64, 64, BF, PAIRS, weight=BF, q_heads=4)
+    x, qw, kw = (t.detach().clone().requires_grad_() for t in (c.x, c.qw, c.kw))
+    how = dict(c.how, q_weight=qw, k_weight=kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        rc.head_norm_rope(x, c.pos, c.table, **how).backward(c.dy)
+    torch.cuda.current_stream().wait_stream(side)
+    x.grad = qw.grad = kw.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rc.head_norm_rope(x, c.pos, c.table, **how).backward(c.dy)
+    with torch.no_grad():
+        x.mul_(2).add_(c.dy)
+        c.dy.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    c.x = x.detach()
+    dx, dq, dk = rc.head_norm_rope_grad(c.dy, c.x, c.pos, c.table, **c.how)
+    c.check_grad(x.grad, dq, dk)
+    assert torch.equal(x.grad, dx)
+    assert torch.equal(qw.grad, dq.to(BF)) and torch.equal(kw.grad, dk.to(BF))
 
 
 @pytest.mark.parametrize("which", ["forward", "grad"])
