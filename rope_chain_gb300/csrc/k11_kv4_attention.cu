@@ -23,6 +23,16 @@
 // Every warp streams its own 16 of a tile's 128 keys from the cache into registers,
 // kAhead chunks ahead, with a running maximum, sum and output of its own; the warps'
 // parts are joined at a unit's end.
+// Measured: 64 tokens over 4100 to 8200 keys (8 query heads a KV head, 229 MB) 77 us,
+// 3.0 TB/s (tree attention over bf16 reads 3.6 times as much); one token over 131071 keys
+// (75 MB) 29 us with the join; 32 trees of 2 over 4000 to 8000 58, 16 of 4 47; one token
+// over 500 keys 6.5.  From L2 alone the first takes 74, so it is not memory that bounds
+// it: 206 instructions of a warp per chunk, 111 of them on the integer pipe, at 2.3 an
+// SM's cycle, and some 20 us of starts, changes of unit and the join.  Tried and no
+// faster: chunks in pairs (80), through shared memory with more warps (80 to 91; with two
+// blocks an SM 74, but 56 where 256 tokens over 350 to 700 keys take 52), four-warp blocks
+// (85 to 96), shifts as products on the other pipe (79 to 81), the scores' products in 8
+// bits (80).
 #include "rc_attention.cuh"
 #include "rc_kv4.cuh"
 
@@ -62,7 +72,9 @@ struct Chunk {
     int32_t at;                        // kRuns: its number in the cache, -1 without a block; else which keys exist
 };
 
-// Chunks in flight beside the one that is worked on, and CTAs on an SM.
+// Chunks in flight beside the one that is worked on (64 tokens over 4100 to 8200 keys: 82
+// us with two, 78 with three), and CTAs on an SM (three, at 80 registers a thread: 93 us;
+// two with tiles of 16 rows, 32 trees of 2 over 4000 to 8000 keys: 65 us, with one 58).
 template <int kTiles> constexpr int kAhead = kTiles == 4 ? 2 : 3;
 template <int kTiles> constexpr int kPerSm = kTiles == 1 ? 2 : 1;
 
@@ -381,7 +393,9 @@ k11_attention(const __grid_constant__ Args a)
 
 // By the average rows of a unit; any kernel is right for any unit.  From 33 rows on
 // the products are the bound, and k5_wide takes the call (blocks of a multiple of 8
-// keys; other block sizes stay here).
+// keys; other block sizes stay here): 16 trees of 16 over a window of 6000 keys, 128 rows
+// a unit, 79 us, in tiles of 32 rows here 170; at 32 rows (16 trees of 4 over 4000 to 8000
+// keys) 47 here.
 enum Variant { kRows8, kRows16, kRows32, kRows128, kRows256 };
 Variant variant_for(int64_t rows, int32_t seqs, int32_t group, int32_t block_size) {
     const int64_t mean = (rows + seqs - 1) / seqs * group;

@@ -45,6 +45,9 @@ namespace {
 // keys for the scores, whose accumulator layout is the operand layout of the
 // second product, so the weights stay in registers (rounded to bf16 there,
 // which the tensor cores require; the sum takes them unrounded).
+// With a window (kWindow) only the key tiles that some row may see are gone through: 64
+// tokens over a window of 4096 + 16 of 8192 to 16384 keys (537 MB) 95 us, 5.7 TB/s; one
+// token over one of 1024 + 4 of 131071 keys 12, where ten tiles are cut and joined.
 // Measured: one token over 131071 keys (8 KV heads, 268 MB) 51 us with the join,
 // 5.2 TB/s; 64 tokens over 1025 to 2049 keys (204 MB) 43 us, 4.7 TB/s; the
 // loads alone, without the products, 50 and 44 us before the changes of unit
@@ -481,7 +484,7 @@ k5_small(const __grid_constant__ Args a)
 // between a start of 9 us (launch, lengths, Q, first tile) and changes of unit and
 // the join of 18.  Two CTAs an SM leave kQ = 1 96 registers a thread, of which it
 // spills 51 (204 bytes stored, 572 loaded); kQ = 2 spills three.
-// Key tiles that hold drafted keys, or the end, take a masked path; there the
+// Key tiles that hold drafted keys, the end, or a window's begin, take a masked path; there the
 // V rows past the end are zeroed and what is infinite or NaN in a drafted one
 // is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
 // fault bit is raised and all roles leave.
@@ -498,7 +501,11 @@ template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 //
 //
 // kFour: over a cache in 4 bits the loaders make bf16 numbers of the rows in shared
-// memory, in place of the boxes: 32 elements and their scale to a lane.
+// memory, in place of the boxes: 32 elements and their scale to a lane.  That is some
+// 1000 instructions a tile, more than one warp (or two for two row tiles) issues beside
+// the softmax: 16 trees of 16 over a window of 6000 keys 103 us with one loader, with two
+// 79; 8 trees of 64 over 32768 keys 538 with two, with four 380 (bf16: 69 and 278).  The
+// loaders cost the softmax warps registers, 80 a thread instead of 96.
 constexpr int kTileBoxes = 16;         // of eight keys
 template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 2 : 4) : kQ;
 template <int kQ, bool kFour> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ, kFour>);

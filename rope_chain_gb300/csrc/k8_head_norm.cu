@@ -7,7 +7,13 @@
 // row of the token, each result rounded once.
 //
 // Bound by memory: forward one read and one write of every element, backward two
-// reads (r is made again from x, which the gradient needs anyway) and one write.
+// reads (r is made again from x, which the gradient needs anyway) and one write.  To be
+// there the work of an element must stay small, so a lane takes 16 bytes or two times
+// 16 of a head, up to eight heads one after another, whose table columns and weights it
+// loads once, and FP32 arithmetic goes in pairs.  Measured, 16384 tokens of 32 + 8 heads
+// of 128: bf16 halves 52 us forward (6.4 TB/s) and 88 backward (5.7), pairs 53 and 90,
+// FP32 halves 100 and 156; one head at a time straight into registers 67 and 107.
+// Heads of 96 leave four lanes of 16 idle (49 and 94 us for 40 of them).
 #include "rc_paged.cuh"
 #include "rc_tcgen05.cuh"
 
