@@ -25,7 +25,7 @@
 // parts are joined at a unit's end.
 // Measured: 64 tokens over 4100 to 8200 keys (8 query heads a KV head, 229 MB) 77 us,
 // 3.0 TB/s (tree attention over bf16 reads 3.6 times as much); one token over 131071 keys
-// (75 MB) 29 us with the join; 32 trees of 2 over 4000 to 8000 58, 16 of 4 47; one token
+// (75 MB) 29 us with the join; 32 trees of 2 over 4000 to 8000 52, 16 of 4 47; one token
 // over 500 keys 6.5.  From L2 alone the first takes 74, so it is not memory that bounds
 // it: 206 instructions of a warp per chunk, 111 of them on the integer pipe, at 2.3 an
 // SM's cycle, and some 20 us of starts, changes of unit and the join.  Tried and no
@@ -35,6 +35,7 @@
 // bits (80).
 #include "rc_attention.cuh"
 #include "rc_kv4.cuh"
+#include "rc_tcgen05.cuh"
 
 namespace rc {
 
@@ -72,11 +73,30 @@ struct Chunk {
     int32_t at;                        // kRuns: its number in the cache, -1 without a block; else which keys exist
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+// With two row tiles the chunks come through a ring in shared memory instead, which
+// leaves the registers for two blocks an SM (32 trees of 2 over 4000 to 8000 keys: 52 us
+// for 58).  There a chunk is the K of its rows, 32 bytes each; their V, the rows in the
+// order 0 2 4 6 1 3 5 7, so that what a warp reads at once lies in all banks; their
+// scales.
+template <int kTiles> constexpr bool kShared = kTiles == 2;
+constexpr int kRing = 4;               // stages
+constexpr uint32_t kChunkV = 512, kChunkScales = 1024, kChunkBytes = 1024 + 128;
+template <int kTiles> constexpr uint32_t kSmem = kShared<kTiles> ? kWarps * kRing * kChunkBytes : 0;
+
 // Chunks in flight beside the one that is worked on (64 tokens over 4100 to 8200 keys: 82
-// us with two, 78 with three), and CTAs on an SM (three, at 80 registers a thread: 93 us;
-// two with tiles of 16 rows, 32 trees of 2 over 4000 to 8000 keys: 65 us, with one 58).
+// us with two, 78 with three), and CTAs on an SM (three, at 80 registers a thread: 93 us).
 template <int kTiles> constexpr int kAhead = kTiles == 4 ? 2 : 3;
-template <int kTiles> constexpr int kPerSm = kTiles == 1 ? 2 : 1;
+template <int kTiles> constexpr int kPerSm = kTiles <= 2 ? 2 : 1;
 
 // kTiles: tiles of eight rows.  kRuns: blocks hold a multiple of 16 keys, so a chunk
 // is 1 KiB in a row.
@@ -87,6 +107,7 @@ k11_attention(const __grid_constant__ Args a)
     constexpr int kRows = 8 * kTiles;
     __shared__ float s_max[kWarps][kRows], s_sum[kWarps][kRows];
     __shared__ __align__(16) float s_out[kWarps][8 * kStride];
+    extern __shared__ __align__(128) uint8_t s_ring[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_trigger();
     pdl_wait();
@@ -203,7 +224,8 @@ k11_attention(const __grid_constant__ Args a)
                 x.scale = __ldg(reinterpret_cast<const uint2 *>(a.scales + row * kKv4Scales));
             }
         };
-        auto work = [&](int j, const Chunk &x) {
+        // (v_word(e): x.v[e], asked for late)
+        auto work = [&](int j, const Chunk &x, const auto &v_word) {
             const int p0 = first_key(j);
             // scales: of this lane's two keys of K, twice each; of its pairs of keys of V
             const uint32_t ks = kv4_scales(x.scale.x), vs = kv4_scales(x.scale.y);
@@ -260,9 +282,9 @@ k11_attention(const __grid_constant__ Args a)
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
                         if (y > limit[m][f]) {
-                            const float shrink =
-                                limit[m][f] == -INFINITY ? 0.0f : ex2(__fmaf_rn(-y, a.scale_log2, -ref[m][f]));
-                            ref[m][f] = -(y * a.scale_log2);
+                            const float top = y * a.scale_log2;
+                            const float shrink = limit[m][f] == -INFINITY ? 0.0f : ex2(-ref[m][f] - top);
+                            ref[m][f] = -top;
                             limit[m][f] = y + a.grow;
                             sum[m][f] *= shrink;
 #pragma unroll
@@ -287,6 +309,10 @@ k11_attention(const __grid_constant__ Args a)
                 add2_rn(t[m][0], t[m][1], t[m][2], t[m][3]);
                 add2_rn(sum[m][0], sum[m][1], t[m][0], t[m][1]);
             }
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = v_word(e);
             const uint32_t vo[2] = {kv4_offsets(v_scale[0]), kv4_offsets(v_scale[1])};
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -295,7 +321,7 @@ k11_attention(const __grid_constant__ Args a)
                 for (int e = 0; e < 4; ++e) {
                     // element 2n + (e & 1) of keys 2c, 2c + 1 (and + 8): from the low or
                     // the high halves of their words
-                    const uint32_t two = __byte_perm(x.v[2 * (e >> 1)], x.v[2 * (e >> 1) + 1], n < 2 ? 0x5410 : 0x7632);
+                    const uint32_t two = __byte_perm(v[2 * (e >> 1)], v[2 * (e >> 1) + 1], n < 2 ? 0x5410 : 0x7632);
                     vf[e] = fma_bf16x2(kv4_pair(two, 2 * (n & 1) + (e & 1)), v_scale[e >> 1], vo[e >> 1]);
                 }
 #pragma unroll
@@ -303,20 +329,95 @@ k11_attention(const __grid_constant__ Args a)
                     mma16816(o[m][n], vf, pf[m][0], pf[m][1]);
             }
         };
+        if constexpr (kShared<kTiles>) {
+            const uint32_t ring = smem_u32(s_ring) + (uint32_t)warp * (kRing * kChunkBytes);
+            const int row_of = lane >> 1, half = 16 * (lane & 1);
+            const uint32_t to_k = ring + 16u * lane;
+            const uint32_t to_v = ring + kChunkV + 32u * (((row_of >> 1) & 3) | (row_of & 1) << 2 | (row_of & 8)) + half;
+            const uint32_t to_scales = ring + kChunkScales + 4u * lane;
+            const uint8_t *const from4 = a.cache4 + row_of * kKv4Row + half;
+            const uint16_t *const from_scales = a.scales + 2 * lane;
+            // kRuns: which of the 32 chunks that `from` is of, and of the 32 before, are not
+            // there; else which keys of a stage's chunk are
+            uint32_t lost = 0u, lost_before = 0u, there[kRing];
+#pragma unroll
+            for (int i = 0; i < kRing; ++i)
+                there[i] = 0u;
+            auto issue = [&](int j, int st) {
+                const uint32_t at = st * kChunkBytes;
+                if constexpr (kRuns) {
+                    if ((j & 31) == 0) {
+                        place(j);
+                        entry = table_entry(j + 32);
+                        lost_before = lost;
+                        lost = __ballot_sync(0xFFFFFFFFu, from < 0);
+                    }
+                    const uint64_t i = (uint32_t)max(__shfl_sync(0xFFFFFFFFu, from, j & 31), 0);
+                    const uint8_t *const src = from4 + i * (kChunk * kKv4Row);
+                    copy16(to_k + at, src);
+                    copy16(to_v + at, src + 32);
+                    copy4(to_scales + at, from_scales + i * (kChunk * kKv4Scales));
+                } else {
+                    place(j);
+                    entry = table_entry(j + 1);
+                    there[st] = __ballot_sync(0xFFFFFFFFu, from >= 0) & 0xFFFFu;
+                    const int64_t row = __shfl_sync(0xFFFFFFFFu, max(from, (int64_t)0), row_of);
+                    const uint8_t *const src = from4 + (row - row_of) * kKv4Row;
+                    copy16(to_k + at, src);
+                    copy16(to_v + at, src + 32);
+                    copy4(to_scales + at, a.scales + row * kKv4Scales + 2 * (lane & 1));
+                }
+            };
+            const uint8_t *const own = s_ring + warp * (kRing * kChunkBytes);
+            const uint8_t *const k_from = own + 32 * g + 8 * c, *const v_from = own + kChunkV + 32 * c + 4 * g;
+            const uint8_t *const scale_from = own + kChunkScales + 8 * (lane & 15);
+#pragma unroll
+            for (int j = 0; j < kRing - 1; ++j) {
+                if (j < count)
+                    issue(j, j);
+                copy_commit();
+            }
+            for (int j0 = 0; j0 < count; j0 += kRing) {
+#pragma unroll
+                for (int i = 0; i < kRing; ++i) {
+                    const int j = j0 + i;
+                    if (j >= count)
+                        break;
+                    copy_wait<kRing - 2>();
+                    __syncwarp();
+                    // (into the stage of chunk j - 1, which every lane has read)
+                    if (j + kRing - 1 < count)
+                        issue(j + kRing - 1, (i + kRing - 1) % kRing);
+                    copy_commit();
+                    Chunk now;
+                    const uint32_t at = i * kChunkBytes;
+                    now.scale = *reinterpret_cast<const uint2 *>(scale_from + at);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        now.k[e] = *reinterpret_cast<const uint2 *>(k_from + at + 256u * e);
+                    // (`lost` is of the 32 that the chunk issued last is one of)
+                    const uint32_t gone = ((min(j + kRing - 1, count - 1) ^ j) & ~31) != 0 ? lost_before : lost;
+                    now.at = !kRuns ? (int32_t)there[i] : (gone >> (j & 31)) & 1u ? -1 : 0;
+                    work(j, now, [&](int e) { return *reinterpret_cast<const volatile uint32_t *>(v_from + at + 128u * e); });
+                }
+            }
+            copy_wait<0>();
+        }
         constexpr int kBuffers = kAhead<kTiles> + 1;
         Chunk ring[kBuffers];
+        const int streamed = kShared<kTiles> ? 0 : count;       // straight into registers
 #pragma unroll
         for (int i = 0; i < kAhead<kTiles>; ++i)
-            if (i < count)
+            if (i < streamed)
                 load(i, ring[i]);
-        for (int j = 0; j < count; j += kBuffers) {
+        for (int j = 0; j < streamed; j += kBuffers) {
 #pragma unroll
             for (int i = 0; i < kBuffers; ++i) {
-                if (j + i >= count)
+                if (j + i >= streamed)
                     break;
-                if (j + i + kAhead<kTiles> < count)
+                if (j + i + kAhead<kTiles> < streamed)
                     load(j + i + kAhead<kTiles>, ring[(i + kAhead<kTiles>) % kBuffers]);
-                work(j + i, ring[i]);
+                work(j + i, ring[i], [&](int e) { return ring[i].v[e]; });
             }
         }
 
@@ -419,8 +520,12 @@ size_t workspace_of(Variant v, int num_sms) {
 template <int kTiles, bool kRuns, bool kWindow>
 cudaError_t launch_tiles(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
+    static bool configured[64] = {};
+    cudaError_t e = kShared<kTiles> ? allow_smem(k11_attention<kTiles, kRuns, kWindow>, kSmem<kTiles>, configured) : cudaSuccess;
+    if (e != cudaSuccess)
+        return e;
     *why = "attention launch";
-    const cudaError_t e = launch_pdl(k11_attention<kTiles, kRuns, kWindow>, dim3((unsigned)ctas), dim3(kThreads), 0, stream, 1, a);
+    e = launch_pdl(k11_attention<kTiles, kRuns, kWindow>, dim3((unsigned)ctas), dim3(kThreads), kSmem<kTiles>, stream, 1, a);
     return e != cudaSuccess ? e : launch_join<8 * kTiles, kWindow, true>(a, ctas, stream, why);
 }
 

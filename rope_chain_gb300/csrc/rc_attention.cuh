@@ -570,7 +570,7 @@ inline int plan(Args &a, int64_t unit_rows, bool wide, int most)
     // the nodes.
     int64_t keys = (int64_t)a.table_width * a.block_size;
     if (a.window > 0)
-        keys = std::min<int64_t>(keys, ((int64_t)(a.sinks + kKeyTile - 1) / kKeyTile + 1) * kKeyTile + a.window + a.rows);
+        keys = std::min<int64_t>(keys, (((int64_t)a.sinks + kKeyTile - 1) / kKeyTile + 1) * kKeyTile + a.window + a.rows);
     // Units of at most so many tiles are not worth a cut and a join: one token over
     // 300 keys 6.9 us (cut 11.2), 30 single tokens over 450 to 900 15.0 (19.2); a
     // tile of many rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of
