@@ -20,19 +20,17 @@
 // for the products with V) and the output.  No value is infinite or NaN, so what a row
 // does not see stays away by a weight of 0.
 //
-// Every warp streams its own 16 of a tile's 128 keys from the cache into registers,
-// kAhead chunks ahead, with a running maximum, sum and output of its own; the warps'
-// parts are joined at a unit's end.
-// Measured: 64 tokens over 4100 to 8200 keys (8 query heads a KV head, 229 MB) 77 us,
-// 3.0 TB/s (tree attention over bf16 reads 3.6 times as much); one token over 131071 keys
+// Every warp streams its own 16 of a tile's 128 keys from the cache, into registers
+// kAhead chunks ahead or through a ring in shared memory, with a running maximum, sum and
+// output of its own; the warps' parts are joined at a unit's end.
+// Measured: 64 tokens over 4100 to 8200 keys (8 query heads a KV head, 229 MB) 74 us,
+// 3.1 TB/s (tree attention over bf16 reads 3.6 times as much); one token over 131071 keys
 // (75 MB) 29 us with the join; 32 trees of 2 over 4000 to 8000 52, 16 of 4 47; one token
-// over 500 keys 6.5.  From L2 alone the first takes 74, so it is not memory that bounds
-// it: 206 instructions of a warp per chunk, 111 of them on the integer pipe, at 2.3 an
-// SM's cycle, and some 20 us of starts, changes of unit and the join.  Tried and no
-// faster: chunks in pairs (80), through shared memory with more warps (80 to 91; with two
-// blocks an SM 74, but 56 where 256 tokens over 350 to 700 keys take 52), four-warp blocks
-// (85 to 96), shifts as products on the other pipe (79 to 81), the scores' products in 8
-// bits (80).
+// over 500 keys 6.5.  Memory does not bound it (with every block in L2 the first took 74 of
+// then 77): some 210 instructions of a warp per chunk, half of them on the integer pipe, at
+// 2.3 an SM's cycle, and some 20 us of starts, changes of unit and the join.  Tried and no
+// faster: chunks in pairs (80), three blocks an SM (80 to 93), four-warp blocks (85 to 96),
+// shifts as products on the other pipe (79 to 81), the scores' products in 8 bits (80).
 #include "rc_attention.cuh"
 #include "rc_kv4.cuh"
 #include "rc_tcgen05.cuh"
@@ -83,15 +81,17 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int kLeft> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
-// With two row tiles the chunks come through a ring in shared memory instead, which
-// leaves the registers for two blocks an SM (32 trees of 2 over 4000 to 8000 keys: 52 us
-// for 58).  There a chunk is the K of its rows, 32 bytes each; their V, the rows in the
+// kShared: the chunks come through a ring in shared memory instead.  With two row tiles
+// that leaves the registers for two blocks an SM (32 trees of 2 over 4000 to 8000 keys: 52
+// us for 58); with one it is better over long contexts (64 tokens over 4100 to 8200 keys:
+// 74 for 77), not over short ones (256 tokens over 350 to 700: 56 for 52).  There a
+// chunk is the K of its rows, 32 bytes each; their V, the rows in the
 // order 0 2 4 6 1 3 5 7, so that what a warp reads at once lies in all banks; their
 // scales.
-template <int kTiles> constexpr bool kShared = kTiles == 2;
 constexpr int kRing = 4;               // stages
 constexpr uint32_t kChunkV = 512, kChunkScales = 1024, kChunkBytes = 1024 + 128;
-template <int kTiles> constexpr uint32_t kSmem = kShared<kTiles> ? kWarps * kRing * kChunkBytes : 0;
+template <bool kShared> constexpr uint32_t kSmem = kShared ? kWarps * kRing * kChunkBytes : 0;
+constexpr int64_t kLongContext = 2048; // keys that a block table must have room for
 
 // Chunks in flight beside the one that is worked on (64 tokens over 4100 to 8200 keys: 82
 // us with two, 78 with three), and CTAs on an SM (three, at 80 registers a thread: 93 us).
@@ -100,7 +100,7 @@ template <int kTiles> constexpr int kPerSm = kTiles <= 2 ? 2 : 1;
 
 // kTiles: tiles of eight rows.  kRuns: blocks hold a multiple of 16 keys, so a chunk
 // is 1 KiB in a row.
-template <int kTiles, bool kRuns, bool kWindow>
+template <int kTiles, bool kShared, bool kRuns, bool kWindow>
 __global__ void __launch_bounds__(kThreads, kPerSm<kTiles>)
 k11_attention(const __grid_constant__ Args a)
 {
@@ -329,7 +329,7 @@ k11_attention(const __grid_constant__ Args a)
                     mma16816(o[m][n], vf, pf[m][0], pf[m][1]);
             }
         };
-        if constexpr (kShared<kTiles>) {
+        if constexpr (kShared) {
             const uint32_t ring = smem_u32(s_ring) + (uint32_t)warp * (kRing * kChunkBytes);
             const int row_of = lane >> 1, half = 16 * (lane & 1);
             const uint32_t to_k = ring + 16u * lane;
@@ -405,7 +405,7 @@ k11_attention(const __grid_constant__ Args a)
         }
         constexpr int kBuffers = kAhead<kTiles> + 1;
         Chunk ring[kBuffers];
-        const int streamed = kShared<kTiles> ? 0 : count;       // straight into registers
+        const int streamed = kShared ? 0 : count;       // straight into registers
 #pragma unroll
         for (int i = 0; i < kAhead<kTiles>; ++i)
             if (i < streamed)
@@ -517,15 +517,15 @@ size_t workspace_of(Variant v, int num_sms) {
     return 2 * (size_t)ctas_of(v, num_sms) * floats * sizeof(float);
 }
 
-template <int kTiles, bool kRuns, bool kWindow>
+template <int kTiles, bool kShared, bool kRuns, bool kWindow>
 cudaError_t launch_tiles(const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     static bool configured[64] = {};
-    cudaError_t e = kShared<kTiles> ? allow_smem(k11_attention<kTiles, kRuns, kWindow>, kSmem<kTiles>, configured) : cudaSuccess;
+    cudaError_t e = kShared ? allow_smem(k11_attention<kTiles, kShared, kRuns, kWindow>, kSmem<kShared>, configured) : cudaSuccess;
     if (e != cudaSuccess)
         return e;
     *why = "attention launch";
-    e = launch_pdl(k11_attention<kTiles, kRuns, kWindow>, dim3((unsigned)ctas), dim3(kThreads), kSmem<kTiles>, stream, 1, a);
+    e = launch_pdl(k11_attention<kTiles, kShared, kRuns, kWindow>, dim3((unsigned)ctas), dim3(kThreads), kSmem<kShared>, stream, 1, a);
     return e != cudaSuccess ? e : launch_join<8 * kTiles, kWindow, true>(a, ctas, stream, why);
 }
 
@@ -533,9 +533,12 @@ template <bool kRuns, bool kWindow>
 cudaError_t launch_variant(Variant v, const Args &a, int ctas, cudaStream_t stream, const char **why)
 {
     switch (v) {
-    case kRows8: return launch_tiles<1, kRuns, kWindow>(a, ctas, stream, why);
-    case kRows16: return launch_tiles<2, kRuns, kWindow>(a, ctas, stream, why);
-    default: return launch_tiles<4, kRuns, kWindow>(a, ctas, stream, why);
+    case kRows8:
+        return (int64_t)a.table_width * a.block_size >= kLongContext
+                   ? launch_tiles<1, true, kRuns, kWindow>(a, ctas, stream, why)
+                   : launch_tiles<1, false, kRuns, kWindow>(a, ctas, stream, why);
+    case kRows16: return launch_tiles<2, true, kRuns, kWindow>(a, ctas, stream, why);
+    default: return launch_tiles<4, false, kRuns, kWindow>(a, ctas, stream, why);
     }
 }
 
