@@ -1030,6 +1030,11 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 if (lane == 0)
                     mbar_arrive_local(s_free0 + 8u * t);
                 if ((kWindow ? some_partly_seen(a, s, p0, kKeyTile) : p0 + kKeyTile > ctx) || bads != 0u) {
+                    // of the four lanes of a row each finds 32 of the keys
+                    uint32_t own[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        own[e] = seen32<kWindow>(a, s, node[e], p0 + 32 * (lane & 3), kWindow ? begin[e] : 0);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t out = 0u;              // keys of blocks out of range
@@ -1039,7 +1044,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const uint32_t see =
-                                (seen32<kWindow>(a, s, node[e], p0 + 32 * c, kWindow ? begin[e] : 0) & ~out) >> (2 * (lane & 3));
+                                (__shfl_sync(0xFFFFFFFFu, own[e], (lane & 28) | c) & ~out) >> (2 * (lane & 3));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
 #pragma unroll
