@@ -566,6 +566,14 @@ constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
     return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
+// One lane of a warp whose lanes are all here; the compiler knows it for one (the
+// products' operands otherwise go through a loop over lanes: 8 trees of 64 tokens over a
+// window of 8192 102 us, so 100).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
 // D[tmem] (+)= A[smem] x B[smem], and with A in TMEM
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alow, uint32_t blow, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
@@ -897,7 +905,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 break;
             }
     } else if (warp >= kMmaWarp) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int t = warp - kMmaWarp;
             constexpr uint32_t idesc_s = make_idesc(128, kKeyTile, false), idesc_o = make_idesc(128, kHeadDim, true);
             const uint32_t tS = tmem + 256u * t, tP = tS + kPCol, tO = tS + kOCol;

@@ -20,6 +20,7 @@ struct Args : TreeAttentionLaunch {
     int32_t min_tiles;                 // fewest key tiles a CTA is given
     bool whole;                        // units are not cut
     int32_t change;                    // going to another unit, in key tiles' time
+    int32_t join;                      // and joining parts; 0: units are cut in any case
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -127,6 +128,7 @@ __device__ __forceinline__ int32_t most_of(const Args &a, int64_t tiles, int64_t
 template <int kRows, int kThreads, bool kParts, bool kWindow>
 __device__ Place locate(const Args &a, int c, int ctas) {
     __shared__ int64_t warp_tiles[kParts ? kThreads / 32 : 1], warp_units[kParts ? kThreads / 32 : 1];
+    __shared__ int32_t warp_longest[kParts ? kThreads / 32 : 1];
     __shared__ int64_t warp_sum[kThreads / 32];
     __shared__ int64_t found_off;
     __shared__ int32_t found_b;
@@ -139,12 +141,15 @@ __device__ Place locate(const Args &a, int c, int ctas) {
     p.most = a.whole ? INT32_MAX : 0;
     if (kParts && !a.whole && a.partial != nullptr) {
         int64_t tiles = 0, units = 0;
+        int32_t longest = 0;
         for (int b = b0; b < b1; ++b) {
             const SeqOf<kWindow> s = seq_of<kWindow>(a, b);
-            const int n = row_tiles<kRows>(a, s) * a.kv_heads;
+            const int n = row_tiles<kRows>(a, s) * a.kv_heads, kt = key_tiles(s);
             units += n;
-            tiles += (int64_t)n * key_tiles(s);
+            tiles += (int64_t)n * kt;
+            longest = max(longest, n > 0 ? kt : 0);
         }
+        longest = __reduce_max_sync(0xFFFFFFFFu, longest);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             tiles += __shfl_xor_sync(0xFFFFFFFFu, tiles, o);
@@ -154,15 +159,20 @@ __device__ Place locate(const Args &a, int c, int ctas) {
             if (lane == 0) {
                 warp_tiles[kParts ? warp : 0] = tiles;
                 warp_units[kParts ? warp : 0] = units;
+                warp_longest[kParts ? warp : 0] = longest;
             }
             __syncthreads();
             tiles = units = 0;
             for (int w = 0; w < kThreads / 32; ++w) {
                 tiles += warp_tiles[kParts ? w : 0];
                 units += warp_units[kParts ? w : 0];
+                longest = max(longest, warp_longest[kParts ? w : 0]);
             }
         }
         p.most = most_of(a, tiles, units, ctas);
+        if (p.most == 0 && a.join > 0 &&
+            quotient(units + ctas - 1, ctas) * longest * ctas <= tiles + a.change * units + (int64_t)a.join * ctas)
+            p.most = INT32_MAX;
     }
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b)
@@ -593,6 +603,12 @@ inline int plan(Args &a, int64_t unit_rows, bool wide, int most)
     // the small kernel, with few tiles a CTA, the ranges had better begin with the
     // units.
     a.change = wide || units * tiles >= 8 * ctas ? 6 : 0;
+    // Units that come out even are not cut where the longest of their rounds takes no
+    // more than the cut and some tiles' time for the join (in 4 bits a tile takes
+    // longer): 8 trees of 64 over a window of 1024 28.7 us, cut 38.3, of 8192 97.4, 100;
+    // 32 of 16 over 1024 in 4 bits 39.5, 47.9.  (Calls that have neither keep their cuts
+    // and with them the last bit of their results.)
+    a.join = a.cache4 != nullptr ? 4 : (a.window > 0 ? 6 : 0);
     return ctas;
 }
 
