@@ -499,15 +499,16 @@ template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 // single warp loads both, as an eleventh warp would cost the SM its second CTA:
 // 16 trees of 16 over 8192 keys take 73 us, with two loaders 84.
 //
-//
 // kFour: over a cache in 4 bits the loaders make bf16 numbers of the rows in shared
 // memory, in place of the boxes: 32 elements and their scale to a lane.  That is some
 // 1000 instructions a tile, more than one warp (or two for two row tiles) issues beside
 // the softmax: 16 trees of 16 over a window of 6000 keys 103 us with one loader, with two
-// 79; 8 trees of 64 over 32768 keys 538 with two, with four 380 (bf16: 69 and 278).  The
-// loaders cost the softmax warps registers, 80 a thread instead of 96.
+// 79, with three, as many as fit at 80 registers a thread, 68; 8 trees of 64 over 32768
+// keys 538 with two, with four 380 (bf16: 69 and 278).  The loaders cost the softmax warps
+// registers, 80 a thread instead of 96.  A branch between a loader's boxes keeps it from
+// working on several at once: 380 us would be 460.
 constexpr int kTileBoxes = 16;         // of eight keys
-template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 2 : 4) : kQ;
+template <int kQ, bool kFour> constexpr int kLoaders = kFour ? (kQ == 1 ? 3 : 4) : kQ;
 template <int kQ, bool kFour> constexpr int kWideThreads = 32 * (kSoftmaxWarps<kQ> + kQ + kLoaders<kQ, kFour>);
 template <int kQ> constexpr int kWideStages = kQ == 1 ? 3 : 5;
 template <int kQ> constexpr uint32_t kTmemCols = 256u * kQ;        // per row tile: S 128, P 64, O 64 columns
@@ -630,11 +631,6 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void loaded8(float *r) {
     asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]));
 }
-__device__ __forceinline__ uint2 ld_shared_v2(uint32_t at) {
-    uint2 x;
-    asm volatile("ld.volatile.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at) : "memory");
-    return x;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -691,7 +687,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
     // by piece modulo 8: a row tile is never more than kStages + 1 pieces ahead
     // of another, whose products free its stages
     __shared__ uint32_t s_tmem, s_skip, s_bad[kStages], s_unfinite[8];
-    __shared__ __align__(8) uint16_t s_gone[kFour ? kStages : 1][4];  // kFour: of each loader's boxes
+    __shared__ __align__(16) uint16_t s_gone[kFour ? kStages : 1][8];  // kFour: such of each loader
     static_assert(kStages + 1 < 8, "pieces in flight");
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kStages, q_ready0 = empty0 + 8u * kStages;
     const uint32_t s_full0 = q_ready0 + 8u * kQ, s_free0 = s_full0 + 8u * kQ, p_ready0 = s_free0 + 8u * kQ;
@@ -713,8 +709,8 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         }
         for (int i = 0; i < 8; ++i)
             s_unfinite[i] = 0u;
-        for (int i = 0; kFour && i < 4 * kStages; ++i)
-            s_gone[i / 4][i % 4] = 0;
+        for (int i = 0; kFour && i < 8 * kStages; ++i)
+            s_gone[i / 8][i % 8] = 0;
         // one decision for the CTA: a raised fault skips the work
         s_skip = *reinterpret_cast<volatile unsigned int *>(&g_attention_faults);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -755,16 +751,17 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         in_memory(u);
     }
     if (kFour && warp >= kLoadWarp) {
-        // A tile's 16 boxes of eight keys, kOwn to a warp.  Lane 4r + q has key r of a box
+        // A tile's 16 boxes of eight keys, kOwn to a warp (with three warps two boxes are
+        // done twice, as a branch around them would part their arithmetic).  Lane 4r + q has key r of a box
         // and of its 64 bytes the q-th 16, K's two halves and V's two: a group of 32
         // elements with one scale.  A box's registers are loaded again, for the next
         // kGroup boxes, as soon as they are used.  In a word the elements come apart as
         // (i, i + 4): the heads' elements are in that order in shared memory, Q's too, and
         // O's columns are put back at the end.  V's lanes take their words in the order
         // 2 3 0 1, so that the eight lanes of a store's phase write to all banks.
-        constexpr int kOwn = kTileBoxes / kLoaders<kQ, kFour>, kGroup = kOwn < 8 ? kOwn : 8, kRounds = kOwn / kGroup;
+        constexpr int kWarps = kLoaders<kQ, kFour>, kOwn = 2 * ((kTileBoxes / 2 + kWarps - 1) / kWarps);
         constexpr int kAtOnce = 32 / kOwn;              // tiles whose boxes are looked up at once, a lane each
-        const int first_box = (warp - kLoadWarp) * kOwn, r = lane >> 2, q = lane & 3;
+        const int first_box = min((warp - kLoadWarp) * kOwn, kTileBoxes - kOwn), r = lane >> 2, q = lane & 3;
         const uint32_t first_word = (q & 2) ? 2u : 0u;
         // where this lane's words of box 0 go: word i, chunk 4 (q % 2) + i of the row
         const uint32_t row_at = sK + (q >> 1) * kTileBytes + (uint32_t)(8 * first_box + r) * 128u;
@@ -778,20 +775,22 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         bool fine = true;
         while (fine && walk.next(a, u)) {
             const SeqOf<kWindow> &s = u.s;
-            uint2 word[kGroup][2];
-            uint32_t scale[kGroup];
+            uint2 word[kOwn][2];
+            uint32_t scale[kOwn];
             // this lane's box, of tile j + lane / kOwn: its table entry, then the number of
             // its eight rows in the cache (negative: none)
             auto key_of = [&](int j) { return tile_at(s, u.k0 + j + lane / kOwn) * kKeyTile + (first_box + lane % kOwn) * 8; };
+            const bool has_box = lane < kAtOnce * kOwn;
             auto look_up = [&](int j) -> int {
                 const int p = key_of(j);
-                return j + lane / kOwn < u.count && p < s.keys ? block_of(a, u.b, p) : 0;
+                return has_box && j + lane / kOwn < u.count && p < s.keys ? block_of(a, u.b, p) : 0;
             };
             auto place = [&](int j, int blk) -> int32_t {
                 const int p = key_of(j);
-                const bool mine = j + lane / kOwn < u.count && p < s.keys && some_seen(a, s, p, 8);
+                const bool mine = has_box && j + lane / kOwn < u.count && p < s.keys && some_seen(a, s, p, 8);
                 const bool lost = mine && (blk < 0 || blk >= a.num_blocks);
-                if (lost && u.unit == 0 && a.err != nullptr && first_needed(a, s, p, min(8, s.keys - p)))
+                if (lost && u.unit == 0 && a.err != nullptr && first_box + lane % kOwn >= (warp - kLoadWarp) * kOwn &&
+                    first_needed(a, s, p, min(8, s.keys - p)))
                     atomicAdd(a.err, 1);
                 if (!mine || lost)
                     return lost ? -1 : -2;              // (-2: hidden by the rows' masks anyway)
@@ -811,9 +810,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
             uint32_t gone_next = gone;
             int next_lane = 0;                          // of the boxes that are loaded next
 #pragma unroll
-            for (int k = 0; k < kGroup; ++k)
+            for (int k = 0; k < kOwn; ++k)
                 load(at, next_lane + k, k);
-            next_lane += kGroup;
+            next_lane += kOwn;
             for (int j = 0; j < u.count; ++j, ++n) {
                 const uint32_t st = n % kStages;
                 if (j % kAtOnce == 0)
@@ -823,30 +822,28 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 if (!fine)
                     break;
                 if (lane == 0)
-                    s_gone[kFour ? st : 0][warp - kLoadWarp] = (uint16_t)(gone >> (j % kAtOnce * kOwn) & ((1u << kOwn) - 1u));
+                    s_gone[kFour ? st : 0][warp - kLoadWarp] =
+                        (uint16_t)((gone >> (j % kAtOnce * kOwn) & ((1u << kOwn) - 1u)) << first_box);
                 const uint32_t to = st * (2 * kTileBytes);
-#pragma unroll
-                for (int h = 0; h < kRounds; ++h) {
-                    if (next_lane == kAtOnce * kOwn) {  // the next boxes are those of tile j + 1
-                        next_lane = 0;
-                        at = place(j + 1, blk);
-                        blk = look_up(j + 1 + kAtOnce);
-                        gone_next = __ballot_sync(0xFFFFFFFFu, at == -1);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        const uint32_t sc = kv4_scales(scale[k] * 0x10001u), off = kv4_offsets(sc);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t w = c & 1 ? word[k][c >> 1].y : word[k][c >> 1].x;
-                            st_shared_v4(chunk_at[c] + to + 1024u * (h * kGroup + k),
-                                         make_uint4(fma_bf16x2(kv4_pair(w, 0), sc, off), fma_bf16x2(kv4_pair(w, 1), sc, off),
-                                                    fma_bf16x2(kv4_pair(w, 2), sc, off), fma_bf16x2(kv4_pair(w, 3), sc, off)));
-                        }
-                        load(at, next_lane + k, k);     // (past the last tile: row 0)
-                    }
-                    next_lane += kGroup;
+                if (next_lane == kAtOnce * kOwn) {      // the next boxes are those of tile j + 1
+                    next_lane = 0;
+                    at = place(j + 1, blk);
+                    blk = look_up(j + 1 + kAtOnce);
+                    gone_next = __ballot_sync(0xFFFFFFFFu, at == -1);
                 }
+#pragma unroll
+                for (int k = 0; k < kOwn; ++k) {
+                    const uint32_t sc = kv4_scales(scale[k] * 0x10001u), off = kv4_offsets(sc);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t w = c & 1 ? word[k][c >> 1].y : word[k][c >> 1].x;
+                        st_shared_v4(chunk_at[c] + to + 1024u * k,
+                                     make_uint4(fma_bf16x2(kv4_pair(w, 0), sc, off), fma_bf16x2(kv4_pair(w, 1), sc, off),
+                                                fma_bf16x2(kv4_pair(w, 2), sc, off), fma_bf16x2(kv4_pair(w, 3), sc, off)));
+                    }
+                    load(at, next_lane + k, k);         // (past the last tile: row 0)
+                }
+                next_lane += kOwn;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
@@ -1015,13 +1012,9 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
                 const uint32_t st = n % kStages;
                 uint32_t bads;                          // boxes without keys
                 if constexpr (kFour) {
-                    constexpr int kWarps4 = kLoaders<kQ, kFour>, kOwn = kTileBoxes / kWarps4;
-                    const uint2 gone = ld_shared_v2(smem_u32(s_gone[st]));
-                    bads = gone.x & 0xFFFFu;
-                    if constexpr (kWarps4 > 1)
-                        bads |= gone.x >> 16 << kOwn;
-                    if constexpr (kWarps4 > 2)
-                        bads |= (gone.y & 0xFFFFu) << 2 * kOwn | gone.y >> 16 << 3 * kOwn;
+                    const uint4 gone = ld_shared_v4(smem_u32(s_gone[st]));
+                    bads = gone.x | gone.y | gone.z | gone.w;
+                    bads = (bads | bads >> 16) & 0xFFFFu;
                 } else {
                     bads = *reinterpret_cast<volatile uint32_t *>(&s_bad[st]);
                 }
