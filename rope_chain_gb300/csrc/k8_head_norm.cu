@@ -11,9 +11,9 @@
 // there the work of an element must stay small, so a lane takes 16 bytes or two times
 // 16 of a head, up to eight heads one after another, whose table columns and weights it
 // loads once, and FP32 arithmetic goes in pairs.  Measured, 16384 tokens of 32 + 8 heads
-// of 128: bf16 halves 52 us forward (6.4 TB/s) and 88 backward (5.7), pairs 53 and 90,
-// FP32 halves 100 and 156; one head at a time straight into registers 67 and 107.
-// Heads of 96 leave four lanes of 16 idle (49 and 94 us for 40 of them).
+// of 128: bf16 halves 53 us forward (6.4 TB/s) and 85 backward (5.9), pairs 53 and 85,
+// FP32 halves 100 and 155; one head at a time straight into registers 67 and 107.
+// Heads of 96 leave four lanes of 16 idle (49 and 88 us for 40 of them).
 #include "rc_paged.cuh"
 #include "rc_tcgen05.cuh"
 
@@ -162,79 +162,85 @@ struct NormArgs : HeadNormLaunch {
     int32_t blocks;                      // of a kind (gradient)
 };
 
-// A head's units of kVec elements (HALVES: kVec of each half; past rot_dim kVec) go
-// to consecutive lanes, kU to a lane.  In FP32 a unit is kPairs pairs (p, q): the
-// pairs that turn, or two elements that do not.
+// A head's units of kVec elements (HALVES: kVec of each half, and past rot_dim kVec of
+// each half of the rest, whose first may be one longer) go to consecutive lanes, kU to a
+// lane.  In FP32 a unit is kPairs pairs (p, q): the pairs that turn, or two elements that
+// do not (12000 x 16 heads of 64 in BF16, 32 elements of which turn, 10.6 us and the
+// gradient 19.8; with one run to a unit of the rest 19.0 and 34.8).
 template <typename T, bool kHalves, int kVec, int kU> struct Lane {
     static constexpr bool kOne = kVec * sizeof(T) == 16;
     static constexpr int kParts = kHalves ? 2 : 1;          // runs of kVec elements of a unit
     static constexpr int kPairs = kHalves ? kVec : kVec / 2;
     using Raw = Run<T, kVec>[kU][kParts];
 
-    // the unit's first element, or -1 past the last unit; whether it is turned
-    static __device__ __forceinline__ int place(const NormArgs &a, int i, bool &rot) {
-        const int u = (threadIdx.x & (a.lanes - 1)) + i * a.lanes;
-        const int rotated = kHalves ? a.rot / (2 * kVec) : a.rot / kVec;
-        rot = u < rotated;
-        const int at = rot ? u * kVec : a.rot + (u - rotated) * kVec;
-        return at < a.width ? at : -1;
-    }
+    // Of each unit of the lane: its first element (turned: below rot), or -1 past the last
+    // unit; HALVES: how far behind it its second run is, 0 without one.
+    struct Spots {
+        int at[kU], by[kU];
+        __device__ __forceinline__ explicit Spots(const NormArgs &a) {
+            const int turned = a.rot / (2 * kVec), rest = (a.width - a.rot) / kVec, units = (rest + 1) / 2;
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+                const int u = (threadIdx.x & (a.lanes - 1)) + i * a.lanes, v = u - turned;
+                at[i] = !kHalves || v < 0 ? u * kVec : a.rot + v * kVec;
+                if (kHalves ? v >= units : at[i] >= a.width)
+                    at[i] = -1;
+                by[i] = !kHalves ? 0 : (v < 0 ? a.rot / 2 : (v + units < rest ? units * kVec : 0));
+            }
+        }
+    };
     // what a lane has of the head at `head` (NULL: zeros)
-    static __device__ __forceinline__ void load(const NormArgs &a, const T *head, Raw &v) {
+    static __device__ __forceinline__ void load(const Spots &spot, const T *head, Raw &v) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
-            bool rot;
-            const int at = place(a, i, rot);
+            const int at = spot.at[i], by = spot.by[i];
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
                 v[i][p].clear();
             if (head != nullptr && at >= 0) {
                 v[i][0].template get<kOne>(head + at);
-                if (kHalves && rot)
-                    v[i][kParts - 1].template get<kOne>(head + at + a.rot / 2);
+                if (kHalves && by != 0)
+                    v[i][kParts - 1].template get<kOne>(head + at + by);
             }
         }
     }
     // The same through shared memory (16-byte accesses): copied there ahead, into the
     // lane's own places from `to` on, kThreads * 16 bytes apart, and read by it alone.
     static constexpr uint32_t kBytes = kU * kParts * kThreads * 16;
-    static __device__ __forceinline__ void copy(const NormArgs &a, const T *head, uint32_t to) {
+    static __device__ __forceinline__ void copy(const Spots &spot, const T *head, uint32_t to) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
-            bool rot;
-            const int at = place(a, i, rot);
+            const int at = spot.at[i], by = spot.by[i];
             if (head == nullptr || at < 0)
                 continue;
             copy16(to + (i * kParts) * (kThreads * 16), head + at);
-            if (kHalves && rot)
-                copy16(to + (i * kParts + 1) * (kThreads * 16), head + at + a.rot / 2);
+            if (kHalves && by != 0)
+                copy16(to + (i * kParts + 1) * (kThreads * 16), head + at + by);
         }
     }
-    static __device__ __forceinline__ void copied(const NormArgs &a, bool there, uint32_t from, Raw &v) {
+    static __device__ __forceinline__ void copied(const Spots &spot, bool there, uint32_t from, Raw &v) {
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
-            bool rot;
-            const int at = place(a, i, rot);
+            const int at = spot.at[i], by = spot.by[i];
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 v[i][p].clear();
-                if (there && at >= 0 && (p == 0 || rot))
+                if (there && at >= 0 && (p == 0 || by != 0))
                     v[i][p].from_shared(from + (i * kParts + p) * (kThreads * 16));
             }
         }
     }
-    static __device__ __forceinline__ void store(const NormArgs &a, T *head, int i, const float (&p)[kPairs], const float (&q)[kPairs]) {
-        bool rot;
-        const int at = place(a, i, rot);
+    static __device__ __forceinline__ void store(const Spots &spot, T *head, int i, const float (&p)[kPairs], const float (&q)[kPairs]) {
+        const int at = spot.at[i], by = spot.by[i];
         if (at < 0)
             return;
         Run<T, kVec> o;
         if constexpr (kHalves) {
             o.set(p);
             o.template put<kOne>(head + at);
-            if (rot) {
+            if (by != 0) {
                 o.set(q);
-                o.template put<kOne>(head + at + a.rot / 2);
+                o.template put<kOne>(head + at + by);
             }
         } else {
             float both[kVec];
@@ -255,23 +261,21 @@ template <typename T, bool kHalves, int kVec, int kU> struct Lane {
         }
     }
     // the table's columns of unit i (1 and 0 where it is not turned)
-    static __device__ __forceinline__ void table(const NormArgs &a, int64_t pos, bool bad, int i, float (&c)[kPairs], float (&s)[kPairs]) {
-        bool rot;
-        const int at = place(a, i, rot);
+    static __device__ __forceinline__ void table(const NormArgs &a, const Spots &spot, int64_t pos, bool bad, int i, float (&c)[kPairs], float (&s)[kPairs]) {
+        const int at = spot.at[i], by = spot.by[i];
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
             c[j] = 1.0f;
             s[j] = 0.0f;
         }
-        if (at >= 0 && rot && !bad) {
+        if (at >= 0 && at < a.rot && !bad) {
             const int64_t from = pos * a.rot + (kHalves ? at : at / 2);
             values<kPairs, kOne>(a.table, a.table_f32 != 0, from, c);
             values<kPairs, kOne>(a.table, a.table_f32 != 0, from + a.rot / 2, s);
         }
     }
-    static __device__ __forceinline__ void weights(const NormArgs &a, int kind, int i, float (&p)[kPairs], float (&q)[kPairs]) {
-        bool rot;
-        const int at = place(a, i, rot);
+    static __device__ __forceinline__ void weights(const NormArgs &a, const Spots &spot, int kind, int i, float (&p)[kPairs], float (&q)[kPairs]) {
+        const int at = spot.at[i], by = spot.by[i];
 #pragma unroll
         for (int j = 0; j < kPairs; ++j)
             p[j] = q[j] = 1.0f;
@@ -279,8 +283,8 @@ template <typename T, bool kHalves, int kVec, int kU> struct Lane {
             return;
         if constexpr (kHalves) {
             values<kPairs, kOne>(a.weight[kind], a.weight_f32 != 0, at, p);
-            if (rot)
-                values<kPairs, kOne>(a.weight[kind], a.weight_f32 != 0, at + a.rot / 2, q);
+            if (by != 0)
+                values<kPairs, kOne>(a.weight[kind], a.weight_f32 != 0, at + by, q);
         } else {
             float both[kVec];
             values<kVec, kOne>(a.weight[kind], a.weight_f32 != 0, at, both);
@@ -358,6 +362,7 @@ k8_head_norm(const __grid_constant__ NormArgs a)
 {
     using L = Lane<T, kHalves, kVec, kU>;
     constexpr int kP = L::kPairs;
+    const typename L::Spots spot(a);
     extern __shared__ __align__(16) uint8_t s_ring[];
     pdl_trigger();
     pdl_wait();
@@ -373,11 +378,11 @@ k8_head_norm(const __grid_constant__ NormArgs a)
     if constexpr (kRing) {
 #pragma unroll
         for (int h = 0; h < kStages - 1; ++h) {
-            L::copy(a, h < heads ? src + h * a.x_head_stride : nullptr, ring + h * L::kBytes);
+            L::copy(spot, h < heads ? src + h * a.x_head_stride : nullptr, ring + h * L::kBytes);
             copy_commit();
         }
     } else {
-        L::load(a, heads > 0 ? src : nullptr, v);
+        L::load(spot, heads > 0 ? src : nullptr, v);
     }
     const int64_t pos = __ldg(a.positions + it.t);
     const bool bad = pos < 0 || pos >= a.max_position;
@@ -387,8 +392,8 @@ k8_head_norm(const __grid_constant__ NormArgs a)
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
         float wp[kP], wq[kP];
-        L::table(a, pos, bad, i, pp[i], pq[i]);
-        L::weights(a, it.kind, i, wp, wq);
+        L::table(a, spot, pos, bad, i, pp[i], pq[i]);
+        L::weights(a, spot, it.kind, i, wp, wq);
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
             const float c = pp[i][j], s = pq[i][j];
@@ -402,7 +407,7 @@ k8_head_norm(const __grid_constant__ NormArgs a)
     for (int h = 0; h < (kRing ? a.per : 1); ++h) {
         if constexpr (kRing) {
             copy_wait<kStages - 2>();
-            L::copied(a, h < heads, ring + st * L::kBytes, v);
+            L::copied(spot, h < heads, ring + st * L::kBytes, v);
         }
         float p[kU][kP], q[kU][kP], squares[kP];
 #pragma unroll
@@ -418,7 +423,7 @@ k8_head_norm(const __grid_constant__ NormArgs a)
         if constexpr (kRing) {
             // into the place of the head before, long read
             const int next = h + kStages - 1;
-            L::copy(a, next < heads ? src + next * a.x_head_stride : nullptr, ring + ((st + kStages - 1) % kStages) * L::kBytes);
+            L::copy(spot, next < heads ? src + next * a.x_head_stride : nullptr, ring + ((st + kStages - 1) % kStages) * L::kBytes);
             copy_commit();
             st = st + 1 == kStages ? 0 : st + 1;
         }
@@ -440,7 +445,7 @@ k8_head_norm(const __grid_constant__ NormArgs a)
             add_product(y, q[i], pq[i]);
             times(z, qp[i]);
             add_product(z, q[i], qq[i]);
-            L::store(a, head, i, y, z);
+            L::store(spot, head, i, y, z);
         }
     }
 }
@@ -460,6 +465,7 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
 {
     using L = Lane<T, kHalves, kVec, kU>;
     constexpr int kP = L::kPairs;
+    const typename L::Spots spot(a);
     extern __shared__ __align__(16) uint8_t s_ring[];
     __shared__ float s_sum[kThreads / 32][kMaxNormDim];
     pdl_trigger();
@@ -471,7 +477,7 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
     float wp[kU][kP], wq[kU][kP], dp[kU][kP], dq[kU][kP];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-        L::weights(a, kind, i, wp[i], wq[i]);
+        L::weights(a, spot, kind, i, wp[i], wq[i]);
 #pragma unroll
         for (int j = 0; j < kP; ++j)
             dp[i][j] = dq[i][j] = 0.0f;
@@ -493,8 +499,8 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
             }
         }
         const bool there = h_ahead < heads_ahead;
-        L::copy(a, there ? x_ahead : nullptr, ring + (2 * st) * L::kBytes);
-        L::copy(a, there ? dy_ahead : nullptr, ring + (2 * st + 1) * L::kBytes);
+        L::copy(spot, there ? x_ahead : nullptr, ring + (2 * st) * L::kBytes);
+        L::copy(spot, there ? dy_ahead : nullptr, ring + (2 * st + 1) * L::kBytes);
         copy_commit();
         x_ahead += a.x_head_stride;
         dy_ahead += a.dy_head_stride;
@@ -525,16 +531,16 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
         float c[kU][kP], s[kU][kP];
 #pragma unroll
         for (int i = 0; i < kU; ++i)
-            L::table(a, pos, bad, i, c[i], s[i]);
+            L::table(a, spot, pos, bad, i, c[i], s[i]);
         for (int h = 0; h < a.per; ++h) {
             typename L::Raw v, d;
             if constexpr (kRing) {
                 copy_wait<kStages - 2>();
-                L::copied(a, h < heads, ring + (2 * st) * L::kBytes, v);
-                L::copied(a, h < heads, ring + (2 * st + 1) * L::kBytes, d);
+                L::copied(spot, h < heads, ring + (2 * st) * L::kBytes, v);
+                L::copied(spot, h < heads, ring + (2 * st + 1) * L::kBytes, d);
             } else {
-                L::load(a, h < heads ? src + h * a.x_head_stride : nullptr, v);
-                L::load(a, h < heads ? dsrc + h * a.dy_head_stride : nullptr, d);
+                L::load(spot, h < heads ? src + h * a.x_head_stride : nullptr, v);
+                L::load(spot, h < heads ? dsrc + h * a.dy_head_stride : nullptr, d);
             }
             float p[kU][kP], q[kU][kP], g[kU][kP], k[kU][kP], squares[kP], dots[kP];   // x, the gradient of n w
 #pragma unroll
@@ -591,7 +597,7 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
                 add_product(k[i], q[i], m);
                 scale(g[i], r);
                 scale(k[i], r);
-                L::store(a, head, i, g[i], k[i]);
+                L::store(spot, head, i, g[i], k[i]);
             }
         }
     }
@@ -601,8 +607,7 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-        bool rot;
-        const int at = L::place(a, i, rot);
+        const int at = spot.at[i], by = spot.by[i];
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
             float x = dp[i][j], y = dq[i][j];
@@ -612,8 +617,8 @@ k8_head_norm_grad(const __grid_constant__ NormArgs a)
             }
             if (at >= 0 && lane < a.lanes) {
                 s_sum[warp][kHalves ? at + j : at + 2 * j] = x;
-                if (!kHalves || rot)
-                    s_sum[warp][kHalves ? at + a.rot / 2 + j : at + 2 * j + 1] = y;
+                if (!kHalves || by != 0)
+                    s_sum[warp][kHalves ? at + by + j : at + 2 * j + 1] = y;
             }
         }
     }
@@ -715,15 +720,16 @@ cudaError_t launch_type(const HeadNormLaunch &a, bool wide, int num_sms, cudaStr
 {
     constexpr int kWide = 16 / (int)sizeof(T), kNarrow = kHalves ? 1 : 2;
     const int vec = wide ? kWide : kNarrow;
-    const int units = (kHalves ? a.rot / (2 * vec) : a.rot / vec) + (a.width - a.rot) / vec;
+    const int units = kHalves ? a.rot / (2 * vec) + ((a.width - a.rot) / vec + 1) / 2 : a.width / vec;
     // Several heads an item, whose table columns and weights are read once, where
     // there is work to fill the GPU that way.
     const int64_t threads = a.T * a.heads * units;
     const int most = (int)std::min<int64_t>(8, std::max<int64_t>(1, threads / ((int64_t)num_sms * 2048)));
-    if (!wide)                              // up to 511 units of an element or two
-        return launch_kind<T, kHalves, kNarrow, 16, false>(a, units, 1, num_sms, stream);
-    if (units > 64)                         // up to 128
-        return launch_kind<T, kHalves, kWide, 4, false>(a, units, 1, num_sms, stream);
+    if (!wide)                              // up to 256 units of two elements
+        return launch_kind<T, kHalves, kNarrow, 8, false>(a, units, 1, num_sms, stream);
+    if constexpr (!kHalves)
+        if (units > 64)                     // up to 128
+            return launch_kind<T, kHalves, kWide, 4, false>(a, units, 1, num_sms, stream);
     if (units > 32 || (most > 1 && !kHalves && a.dy != nullptr && units > 1))    // (the gradient in pairs: two units a lane)
         return most > 1 ? launch_kind<T, kHalves, kWide, 2, true>(a, units, most, num_sms, stream)
                         : launch_kind<T, kHalves, kWide, 2, false>(a, units, 1, num_sms, stream);

@@ -146,6 +146,16 @@ def test_types_of_tables_and_weights(dtype, table, weight, layout, d):
     c.check_grad(*c.grad())
 
 
+@pytest.mark.parametrize("d,rot", [(40, 16), (72, 32), (88, 16), (96, 32), (128, 32), (104, 96), (504, 16), (33, 10), (511, 2), (66, 64)])
+@pytest.mark.parametrize("T,heads", [(3, 5), (4000, 12)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rest_of_a_head_in_even_and_odd_parts(d, rot, T, heads, dtype):
+    """Halves, of whose rest the two runs of a lane are of the same length or the first is longer."""
+    c = Case(T if d < 256 else T // 8 + 1, heads, d, rot, dtype, HALVES, weight=dtype, q_heads=heads - 4)
+    c.check_forward(c.run())
+    c.check_grad(*c.grad())
+
+
 @pytest.mark.parametrize("q_heads", [0, 1, 5])
 @pytest.mark.parametrize("weight", [None, BF])
 def test_which_heads_take_which_weight(q_heads, weight):
