@@ -211,6 +211,22 @@ def test_many_units(counts, ctx, G, ws, four):
 
 
 @pytest.mark.parametrize("four", FORMATS)
+@pytest.mark.parametrize("counts,ctx,H", [
+    ([13] * 20, [2000] * 20, 8), ([13, 5] * 10, [2000 - 31 * i for i in range(20)], 8), ([40] * 10, [1700] * 10, 8),
+    ([13] * 40, [1500 + i for i in range(40)], 4), ([40, 0, 33] * 12, [1500 - 41 * i for i in range(36)], 4),
+    ([13] * 20 + [0] * 14, [2000] * 34, 8), ([13] * 24, [9000] + [700] * 23, 8)])
+def test_units_that_come_out_even(counts, ctx, H, four):
+    """More units of several tiles than a cut would be worth: the same with a workspace as without one."""
+    for window, sinks in ((700, 3), (1000, 130)):
+        case = Case(len(counts) + H, counts, ctx, H, 8, 16, four=four, window=window, sinks=sinks)
+        case.block_out(1, (ctx[1] - 5) // 16, -1)
+        for ws in (True, False):
+            out, lse, err = case.run(ws)
+            assert err == (counts[1] > 0)
+            case.check(out, lse)
+
+
+@pytest.mark.parametrize("four", FORMATS)
 def test_strided_output_and_rows_without_a_sequence(four):
     case = Case(21, [5, 6], [290, 33], 2, 4, 16, four=four, window=20, sinks=2, pad_rows=3)
     whole = torch.full((case.rows, 8 * 64 + 128), 3.0, dtype=BF, device=DEV)
