@@ -1,0 +1,86 @@
+"""rc_head_norm_rope and its gradients where much work goes through the kernels that
+copy heads ahead.
+
+Tolerance of a weight's gradient, a sum of N = tokens * heads products of n and g, with
+u = 2^-24: a product is off by (d / 2 + 16) u of |g n| (r, n and the turn of dy, as in
+test_gpu_head_norm), and what matters of the sum is how many additions lie one behind
+another.  At least 8 threads of every SM have each of its columns, so a thread adds some
+N / (8 SMs) of them, and half an item (8 heads) of it more; then 5 + 8 within a block, 2 SMs
+/ 32 + 32 over the blocks: (N / (8 SMs) + d / 2 + 96) u of sum |g n| in all.  So a head that
+is left out of the sum shows, which each test asserts of its own sizes."""
+import pytest
+import torch
+
+import rope_chain_gb300 as rc
+from tests.test_gpu_head_norm import BF, DEV, F32, HALVES, PAIRS, U, Case, turn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from rope_chain_gb300 import _build
+    _build.build()
+
+
+def check_weight_gradients(c, dq, dk):
+    """Returns, for each weight, the tolerances and the terms' sizes per column."""
+    x, dy = c.x.double(), c.dy.double()
+    n = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + c.eps)
+    g = turn(dy, c.table, c.pos, c.layout, back=True)
+    size = turn(dy.abs(), c.table, c.pos, c.layout, sizes=True)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    found = []
+    for got, weight, part in ((dq, c.qw, slice(0, c.q_heads)), (dk, c.kw, slice(c.q_heads, c.heads))):
+        if weight is None:
+            assert got is None
+            continue
+        ref = (g * n)[:, part].sum((0, 1))
+        deep = c.T * (part.stop - part.start) / (8 * sms) + c.d / 2 + 96
+        tol = deep * U * (size * n.abs())[:, part].sum((0, 1)) + 2.0 ** -133
+        err = (got.double() - ref).abs()
+        assert got.dtype == F32 and bool((err <= tol).all()), float((err - tol).max())
+        found.append((tol, ref, (g * n)[:, part]))
+    return found
+
+
+BUSY = [(3000, 40, 128, BF), (9000, 16, 64, BF), (2500, 33, 96, BF), (1500, 20, 256, F32), (900, 24, 512, BF), (2000, 17, 128, F32),
+        (4000, 12, 64, F32)]
+
+
+@pytest.mark.parametrize("T,heads,d,dtype", BUSY)
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+@pytest.mark.parametrize("rot", [64, 0])
+def test_weight_gradients_of_much_work(T, heads, d, dtype, layout, rot):
+    c = Case(T, heads, d, rot or d, dtype, layout, weight=dtype, q_heads=heads - 7)
+    _, dq, dk = c.grad()
+    for tol, ref, terms in check_weight_gradients(c, dq, dk):
+        # an eighth of the tokens (a warp's), or a 304th of them (a block's), would show in
+        # every other column at least
+        for lost in (terms[::8], terms[::304]):
+            assert float((lost.sum((0, 1)).abs() > 2 * tol).float().mean()) > 0.5
+
+
+@pytest.mark.parametrize("T,heads,d,dtype", BUSY[:4])
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+@pytest.mark.parametrize("where", ["last token", "last heads", "first heads", "one head of a token", "every 304th token"])
+def test_every_head_enters_the_weight_gradients(T, heads, d, dtype, layout, where):
+    """A gradient that is zero but for a few heads, at the ends of items, tokens, kinds and
+    the whole: what is left out changes the sums altogether."""
+    c = Case(T, heads, d, d, dtype, layout, weight=dtype, q_heads=heads - 7)
+    keep = torch.zeros(T, heads, 1, dtype=dtype, device=DEV)
+    if where == "last token":
+        keep[-1] = 1
+    elif where == "last heads":
+        keep[:, [c.q_heads - 1, heads - 1]] = 1
+    elif where == "first heads":
+        keep[:, [0, c.q_heads]] = 1
+    elif where == "one head of a token":
+        keep[T // 2, [c.q_heads // 2, c.q_heads + 3]] = 1
+    else:
+        keep[::304] = 1
+    c.dy.mul_(keep)
+    dx, dq, dk = c.grad()
+    c.check_grad(dx, dq, dk)
+    for tol, ref, _ in check_weight_gradients(c, dq, dk):
+        assert float((ref.abs() > 4 * tol).float().mean()) > 0.9
