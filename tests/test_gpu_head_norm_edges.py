@@ -84,3 +84,42 @@ def test_every_head_enters_the_weight_gradients(T, heads, d, dtype, layout, wher
     c.check_grad(dx, dq, dk)
     for tol, ref, _ in check_weight_gradients(c, dq, dk):
         assert float((ref.abs() > 4 * tol).float().mean()) > 0.9
+
+
+@pytest.mark.parametrize("T,heads,d,dtype", [(3000, 40, 128, BF), (9000, 16, 64, BF), (1500, 20, 256, F32), (2000, 18, 128, F32)])
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+@pytest.mark.parametrize("kw", [dict(extra=1024), dict(extra=64, order="heads"), dict()])
+def test_much_work_in_place_and_strided(T, heads, d, dtype, layout, kw):
+    """Columns of a projection's wider rows, or heads before tokens; the same bits as into
+    an output of its own, and nothing beside the columns is touched."""
+    def made():
+        return Case(T, heads, d, d if d < 256 else 64, dtype, layout, weight=dtype, q_heads=heads - 5, **kw)
+
+    def whole(t):                                        # the memory that a view lies in
+        return t.as_strided((t.untyped_storage().nbytes() // t.element_size(),), (1,), 0)
+
+    def beside(t):                                       # what of it is not the view's
+        outside = torch.ones_like(whole(t), dtype=torch.bool)
+        outside.as_strided(t.shape, t.stride(), t.storage_offset()).fill_(False)
+        return whole(t)[outside]
+    c = made()
+    want = c.run()
+    dx, dq, dk = c.grad()
+    c.check_forward(want)
+    c.check_grad(dx, dq, dk)
+    check_weight_gradients(c, dq, dk)
+    dense = Case(T, heads, d, c.rot, dtype, layout, weight=dtype, q_heads=heads - 5)
+    dense.x, dense.dy, dense.pos = c.x.contiguous(), c.dy.contiguous(), c.pos
+    dense.how = c.how
+    assert torch.equal(dense.run(), want) and all(torch.equal(a, b) for a, b in zip(dense.grad(), (dx, dq, dk)))
+    for over in ("dy", "x"):
+        other = made()
+        out = getattr(other, over)
+        rest = beside(out).clone()
+        got = other.grad(out=out)
+        assert torch.equal(out, dx) and torch.equal(got[1], dq) and torch.equal(got[2], dk)
+        assert torch.equal(beside(out), rest)
+    other = made()
+    rest = beside(other.x).clone()
+    assert torch.equal(other.run(out=other.x), want) and torch.equal(other.x, want)
+    assert torch.equal(beside(other.x), rest)
