@@ -1,11 +1,11 @@
 """rc_head_norm_rope and its gradients where much work goes through the kernels that
-copy heads ahead.
+copy heads ahead, and where single elements are infinite or NaN.
 
 Tolerance of a weight's gradient, a sum of N = tokens * heads products of n and g, with
 u = 2^-24: a product is off by (d / 2 + 16) u of |g n| (r, n and the turn of dy, as in
 test_gpu_head_norm), and what matters of the sum is how many additions lie one behind
 another.  At least 8 threads of every SM have each of its columns, so a thread adds some
-N / (8 SMs) of them, and half an item (8 heads) of it more; then 5 + 8 within a block, 2 SMs
+N / (8 SMs) of them, and up to an item (8 heads) more; then 5 + 8 within a block, 2 SMs
 / 32 + 32 over the blocks: (N / (8 SMs) + d / 2 + 96) u of sum |g n| in all.  So a head that
 is left out of the sum shows, which each test asserts of its own sizes."""
 import pytest
@@ -123,3 +123,64 @@ def test_much_work_in_place_and_strided(T, heads, d, dtype, layout, kw):
     rest = beside(other.x).clone()
     assert torch.equal(other.run(out=other.x), want) and torch.equal(other.x, want)
     assert torch.equal(beside(other.x), rest)
+
+
+UNFINITE = [float("inf"), float("-inf"), float("nan")]
+
+
+@pytest.mark.parametrize("T,heads,d,rot,dtype", [(5, 6, 64, 32, BF), (5, 6, 64, 32, F32), (6, 5, 66, 10, BF), (4, 4, 96, 32, F32), (3, 4, 512, 64, F32),
+                                                 (3000, 40, 128, 64, BF), (2000, 18, 128, 32, F32)])
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+def test_what_does_not_turn_keeps_infinities_to_itself(T, heads, d, rot, dtype, layout, at):
+    """An element past rot_dim meets no other but in its head's means: an infinite weight or
+    gradient of one column is seen in that column alone, of y and of the sums."""
+    c = Case(T, heads, d, rot, dtype, layout, weight=dtype, q_heads=heads - 3)
+    e = dict(first=rot, middle=(rot + d) // 2, last=d - 1)[at]
+    others = torch.arange(d, device=DEV) != e
+    y, (dx, dq, dk) = c.run(), c.grad()
+    for odd in UNFINITE:
+        for weight, part in ((c.qw, slice(0, c.q_heads)), (c.kw, slice(c.q_heads, heads))):
+            held = weight[e].clone()
+            weight[e] = odd
+            z = c.run()
+            weight[e] = held
+            assert not bool(torch.isfinite(z[:, part, e]).any())
+            assert torch.equal(z[..., others], y[..., others])
+        held = c.dy[T // 2, 0, e].clone()
+        c.dy[T // 2, 0, e] = odd
+        dx2, dq2, dk2 = c.grad()
+        c.dy[T // 2, 0, e] = held
+        assert torch.equal(dq2[others], dq[others]) and not bool(torch.isfinite(dq2[e])) and torch.equal(dk2, dk)
+        rows = torch.ones(T, heads, dtype=torch.bool, device=DEV)
+        rows[T // 2, 0] = False
+        assert torch.equal(dx2[rows], dx[rows])
+
+
+@pytest.mark.parametrize("T,heads,d,dtype", [(5, 6, 64, BF), (5, 6, 64, F32), (6, 5, 66, BF), (3000, 40, 128, BF), (2000, 18, 128, F32)])
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+def test_tokens_outside_the_table_keep_infinities_in_their_columns(T, heads, d, dtype, layout):
+    """Such a token is normed but not turned: no element of it meets another."""
+    c = Case(T, heads, d, d, dtype, layout, weight=dtype, q_heads=heads - 3)
+    t = T // 2
+    c.pos[t] = -1
+    y, (_, dq, dk) = c.run()[t].clone(), c.grad()
+    for e in (0, 1, d // 2, d - 1):
+        others = torch.arange(d, device=DEV) != e
+        for odd in UNFINITE:
+            held = c.qw[e].clone()
+            c.qw[e] = odd
+            z = c.run()[t]
+            c.qw[e] = held
+            assert not bool(torch.isfinite(z[: c.q_heads, e]).any())
+            assert torch.equal(z[:, others], y[:, others])
+            held = c.dy[t, 1, e].clone()
+            c.dy[t, 1, e] = odd
+            _, dq2, dk2 = c.grad()
+            c.dy[t, 1, e] = held
+            assert torch.equal(dq2[others], dq[others]) and not bool(torch.isfinite(dq2[e])) and torch.equal(dk2, dk)
+    # an infinite element of x makes its head's others zeros (x r w with r = 0), not NaN
+    c.x[t, 1, 3] = float("inf")
+    z = c.run()[t, 1]
+    others = torch.arange(d, device=DEV) != 3
+    assert bool((z[others] == 0).all()) and bool(torch.isnan(z[3]))
