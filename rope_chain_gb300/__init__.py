@@ -912,7 +912,8 @@ def head_norm_rope(x: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tens
     (bf16 or float32 [head_dim]; None: ones).  Rounded once; ``out`` may be x (in
     place).  autograd takes the gradients where x or a weight requires one, without
     ``out``; its backward pass may be captured into a graph once no eager graph of
-    the same leaves is alive (autograd would join streams that are not captured)."""
+    the same leaves is alive (autograd would join streams that are not captured).
+    Tangents of forward mode are refused, here as by the other calls."""
     y = (_draft_module or _draft()).head_norm_rope(x, positions, cos_sin, eps, q_weight, k_weight, q_heads, layout, out,
                                                    err, None if stream is None else stream.cuda_stream)
     if y is None:                        # something requires a gradient

@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Device.h>
@@ -81,8 +82,16 @@ void beside(const Tensor &t, at::Device device, const char *name) {
     TORCH_CHECK_VALUE(t.device() == device, name, " is on device ", t.device(), ", other operands on ", device);
 }
 
-// The calls record nothing for autograd (rope_apply does so in Python).
+// A tangent of forward mode (torch.autograd.forward_ad) is carried on by no call; it is
+// there under torch.no_grad() too, not in inference mode.
+void no_tangent(const Tensor &t, const char *name) {
+    TORCH_CHECK_VALUE(!t._fw_grad(0).defined() || !c10::AutogradState::get_tls_state().get_fw_grad_mode(), name,
+                      " has a tangent (forward-mode differentiation), which this call does not carry on");
+}
+
+// The calls record nothing for autograd (rope_apply and head_norm_rope do so in Python).
 void no_gradient(const Tensor &t, const char *name) {
+    no_tangent(t, name);
     TORCH_CHECK_VALUE(!t.requires_grad() || !at::GradMode::is_enabled(), name, " requires a gradient, which this call "
                       "does not give: detach it or call under torch.no_grad()");
 }
@@ -201,6 +210,7 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
                       "cos_sin must be a contiguous CUDA tensor [max_position, rot_dim]");
     beside(table, x.device(), "cos_sin");
     no_gradient(table, "cos_sin");
+    no_tangent(x, "x");
     if (args[5] == Py_None && x.requires_grad() && at::GradMode::is_enabled())
         Py_RETURN_NONE;                  // to be recorded: the caller does
     no_gradient(x, "x");
@@ -446,6 +456,7 @@ private:
                           " must be a contiguous CUDA tensor [head_dim]");
         params.weight_dtype = dtype_of(w, name);
         beside(w, x.device(), name);
+        no_tangent(w, name);
         return w.const_data_ptr();
     }
 };
@@ -466,6 +477,7 @@ PyObject *head_norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
     heads_view(x, "x");
     const int32_t type = dtype_of(x, "x");
     const NormOperands o(x, args + 1);
+    no_tangent(x, "x");
     if (at::GradMode::is_enabled() && (x.requires_grad() || wants_gradient(args[4]) || wants_gradient(args[5]))) {
         if (args[8] == Py_None)
             Py_RETURN_NONE;              // to be recorded: the caller does
