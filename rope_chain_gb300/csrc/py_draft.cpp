@@ -157,6 +157,23 @@ Tensor output(PyObject *o, const Tensor &t, const char *what) {
     return out;
 }
 
+// What a call wrote into tensors that were there before it shows as torch's own in-place
+// operations show it: a backward pass that has saved one of them finds it changed, and
+// raises, instead of taking other values.  (Counters and workspaces hold none.)
+void written(std::initializer_list<PyObject *> list) {
+    for (PyObject *o : list)
+        if (o != Py_None && !THPVariable_Unpack(o).is_inference())
+            THPVariable_Unpack(o).unsafeGetTensorImpl()->bump_version();
+}
+
+// The result of a call: `out`, once what was `given` to be written is marked; or an error.
+PyObject *result(rc_status s, const Tensor &out, std::initializer_list<PyObject *> given) {
+    if (s != RC_OK)
+        return raise_status(s);
+    written(given);
+    return THPVariable_Wrap(out);
+}
+
 // A new contiguous output like `t` where there is none yet (within an On).
 void made(Tensor &out, const Tensor &t) {
     if (!out.defined())
@@ -195,7 +212,7 @@ PyObject *rope_table(PyObject *, PyObject *const *args, Py_ssize_t n) {
                         at::TensorOptions(integer(args[9]) ? at::kFloat : at::kBFloat16).device(at::kCUDA));
     const rc_status s = rc_rope_table(out.data_ptr(), dtype_of(out, "out"), positions,
                                       narrow<int32_t>(rot_dim, "rot_dim"), number(args[2]), &sc, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    return result(s, out, {args[11]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -228,7 +245,7 @@ PyObject *rope_apply(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(x.size(2), "head_dim"), positions, table.const_data_ptr(), dtype_of(table, "cos_sin"),
         table.size(0), narrow<int32_t>(table.size(1), "rot_dim"), narrow<int32_t>(integer(args[3]), "layout"),
         inverse, out.data_ptr(), out.stride(0), out.stride(1), err, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    return result(s, out, {args[5]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -328,7 +345,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
         narrow<int32_t>(o.words, "words of tree_mask"), c.data, c.blocks, c.block_size, o.scale, o.outputs(),
         o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
+    return result(s, o.out, {args[7], args[8]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -348,7 +365,7 @@ PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
         narrow<int32_t>(o.words, "words of tree_mask"), c.data, c.blocks, c.block_size, window, sinks, o.scale,
         o.outputs(), o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
+    return result(s, o.out, {args[7], args[8]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -415,7 +432,7 @@ PyObject *logits_adjust(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                          narrow<int32_t>(vocab, "vocab"), row_start,
                                          narrow<int32_t>(seqs, "seqs"), &p, out.data_ptr(), out.stride(0), err,
                                          on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    return result(s, out, {args[14]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -496,7 +513,7 @@ PyObject *head_norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(x.size(2), "head_dim"), &o.params, o.positions, o.table->const_data_ptr(),
         dtype_of(*o.table, "cos_sin"), o.table->size(0), narrow<int32_t>(o.table->size(1), "rot_dim"), o.layout,
         out.data_ptr(), out.stride(0), out.stride(1), err, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    return result(s, out, {args[8]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -548,6 +565,7 @@ PyObject *head_norm_rope_grad(PyObject *, PyObject *const *args, Py_ssize_t n) {
         workspace.defined() ? workspace.data_ptr() : nullptr, workspace.defined() ? workspace.nbytes() : 0, err, on.stream());
     if (s != RC_OK)
         return raise_status(s);
+    written({args[10]});
     auto wrapped = [](bool is, Tensor &t) {
         if (is)
             return THPVariable_Wrap(t);
@@ -601,7 +619,7 @@ PyObject *kv4_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
         narrow<int32_t>(o.seqs, "seqs"), o.context_len, o.blocks(), o.table.stride(0), o.table_width(), o.tree_mask,
         narrow<int32_t>(o.words, "words of tree_mask"), c->cache4, c->scales, c->blocks, c->block_size, window, sinks,
         o.scale, o.outputs(), o.out.stride(0), o.lse, o.err, o.workspace, o.workspace_bytes, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(o.out) : raise_status(s);
+    return result(s, o.out, {args[8], args[9]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -629,6 +647,7 @@ PyObject *kv4_store(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                      c.heads, slots, c.cache4, c.scales, c.blocks, c.block_size, err, on.stream());
     if (s != RC_OK)
         return raise_status(s);
+    written({args[3], args[4]});
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -657,7 +676,7 @@ PyObject *kv4_load(PyObject *, PyObject *const *args, Py_ssize_t n) {
         out = at::empty({slot.size(0), c.heads, 128}, slot.options().dtype(at::kBFloat16));
     const rc_status s = rc_kv4_load(slots, slot.size(0), c.heads, c.cache4, c.scales, c.blocks, c.block_size,
                                     static_cast<uint16_t *>(out.data_ptr()), err, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(out) : raise_status(s);
+    return result(s, out, {args[3]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -716,7 +735,9 @@ PyObject *kv_compact(PyObject *, PyObject *const *args, Py_ssize_t n) {
         static_cast<const int32_t *>(table.const_data_ptr()), table.stride(0), narrow<int32_t>(table.size(1), "width of block_table"),
         context_len, row_start, narrow<int32_t>(seqs, "seqs"), 0x7FFFFFFF, static_cast<const int32_t *>(path.const_data_ptr()),
         path.stride(0), narrow<int32_t>(path.size(1), "width of path"), path_len, new_len.data_ptr<int32_t>(), err, on.stream());
-    return s == RC_OK ? THPVariable_Wrap(new_len) : raise_status(s);
+    for (Py_ssize_t i = 0; s == RC_OK && i < count; ++i)
+        written({PySequence_Fast_GET_ITEM(list.get(), i)});
+    return result(s, new_len, {args[6]});
     END_HANDLE_TH_ERRORS
 }
 
