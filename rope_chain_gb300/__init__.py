@@ -10,7 +10,8 @@ path: if the library is missing, every call raises.
     kv_store_from_projection(kv, H, positions, slots, cos_sin, caches, eps)
 
 and, for the tokens drafted over those caches: rope_table, rope_apply,
-tree_attention and logits_adjust.
+tree_attention and logits_adjust; around them head_norm_rope, window_attention,
+caches in 4 bits (kv4_store, kv4_load, kv4_attention) and kv_compact.
 """
 from __future__ import annotations
 
