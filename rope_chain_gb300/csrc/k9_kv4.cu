@@ -31,7 +31,6 @@ __device__ __forceinline__ uint32_t tamed(uint32_t half) {
 
 constexpr int kGroups = 4;             // of a row's head: K's two and V's two, a lane each
 
-template <int kItems>
 __global__ void __launch_bounds__(kThreads)
 k9_store(const __grid_constant__ Kv4StoreLaunch a)
 {
@@ -39,100 +38,86 @@ k9_store(const __grid_constant__ Kv4StoreLaunch a)
     pdl_wait();
     const int q = threadIdx.x & (kGroups - 1);
     const uint32_t items = (uint32_t)a.T * (uint32_t)a.heads;
-    const uint32_t first = blockIdx.x * (uint32_t)(kThreads / kGroups * kItems) + threadIdx.x / kGroups;
-    const uint16_t *const src = (q >= 2 ? a.v : a.k) + 32 * (q & 1);
-    const int64_t row_stride = q >= 2 ? a.v_row_stride : a.k_row_stride;
-    const int64_t head_stride = q >= 2 ? a.v_head_stride : a.k_head_stride;
-    uint4 x[kItems][4];
-    int64_t slot[kItems];
-    uint32_t head[kItems];
+    const uint32_t item = blockIdx.x * (uint32_t)(kThreads / kGroups) + threadIdx.x / kGroups;
+    const uint32_t t = item < items ? item / (uint32_t)a.heads : 0u, head = item - t * (uint32_t)a.heads;
+    uint32_t w[16];
+    int64_t slot = -1;
+    if (item < items) {
+        slot = __ldg(a.slots + t);
+        const uint16_t *const src = (q >= 2 ? a.v : a.k) + 32 * (q & 1);
+        const int64_t row_stride = q >= 2 ? a.v_row_stride : a.k_row_stride;
+        const int64_t head_stride = q >= 2 ? a.v_head_stride : a.k_head_stride;
+        const uint4 *from = reinterpret_cast<const uint4 *>(src + t * row_stride + head * head_stride);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t item = first + i * (kThreads / kGroups);
-        const uint32_t t = item < items ? item / (uint32_t)a.heads : 0u;
-        head[i] = item - t * (uint32_t)a.heads;
-        slot[i] = -1;
-        if (item < items) {
-            slot[i] = __ldg(a.slots + t);
-            const uint4 *from = reinterpret_cast<const uint4 *>(src + t * row_stride + head[i] * head_stride);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[i][j] = __ldg(from + j);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[i][j] = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+            const uint4 x = __ldg(from + j);
+            w[4 * j] = x.x;
+            w[4 * j + 1] = x.y;
+            w[4 * j + 2] = x.z;
+            w[4 * j + 3] = x.w;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            w[j] = 0u;
     }
+    auto largest = [&] {
+        uint32_t most[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        uint32_t w[16];
+        for (int j = 0; j < 16; ++j)
+            most[j & 1] = __vmaxu2(most[j & 1], w[j] & 0x7FFF7FFFu);
+        most[0] = __vmaxu2(most[0], most[1]);
+        return max(most[0] & 0xFFFFu, most[0] >> 16);
+    };
+    uint32_t most = largest();
+    const uint32_t odd = __ballot_sync(0xFFFFFFFFu, most >= 0x7F80u);
+    if (most > kMostValue) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[4 * j] = x[i][j].x;
-            w[4 * j + 1] = x[i][j].y;
-            w[4 * j + 2] = x[i][j].z;
-            w[4 * j + 3] = x[i][j].w;
+        for (int j = 0; j < 16; ++j)
+            w[j] = tamed(w[j] & 0xFFFFu) | tamed(w[j] >> 16) << 16;
+        most = largest();
+    }
+    // to four significant bits, ties to even
+    uint32_t bits = __float_as_uint(__fdiv_rn(__uint_as_float(most << 16), 7.0f));
+    bits = (bits + 0x7FFFFu + ((bits >> 20) & 1u)) & 0xFFF00000u;
+    if (bits < 0x0D800000u)                              // 2^-100
+        bits = 0u;
+    // 1 / scale, less 2^-14 of it: a quotient that lies between two whole numbers goes
+    // toward zero, any other is 2^-10 away from such a tie at least (eight bits over four)
+    const float per = bits == 0u ? 0.0f : __fmul_rn(__frcp_rn(__uint_as_float(bits)), 1.0f - 0x1p-14f);
+    // 1.5 * 2^23 + 8: the sum's unit is 1, so its bits are those of 1.5 * 2^23 plus 8 + the
+    // whole number; what 16 times and add leaves of the former is taken off
+    constexpr uint32_t kOnes = 0x11111111u * 0x4B400000u;
+    uint32_t word[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t sum = 0u;
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+            float lo = bf16_lo(w[4 * j + e]), hi = bf16_hi(w[4 * j + e]);
+            fma2_rn(lo, hi, per, per, 12582920.0f, 12582920.0f);
+            sum = sum * 16u + __float_as_uint(hi);
+            sum = sum * 16u + __float_as_uint(lo);
         }
-        auto largest = [&] {
-            uint32_t most[2] = {0u, 0u};
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                most[j & 1] = __vmaxu2(most[j & 1], w[j] & 0x7FFF7FFFu);
-            most[0] = __vmaxu2(most[0], most[1]);
-            return max(most[0] & 0xFFFFu, most[0] >> 16);
-        };
-        uint32_t most = largest();
-        const uint32_t odd = __ballot_sync(0xFFFFFFFFu, most >= 0x7F80u);
-        if (most > kMostValue) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                w[j] = tamed(w[j] & 0xFFFFu) | tamed(w[j] >> 16) << 16;
-            most = largest();
-        }
-        // to four significant bits, ties to even
-        uint32_t bits = __float_as_uint(__fdiv_rn(__uint_as_float(most << 16), 7.0f));
-        bits = (bits + 0x7FFFFu + ((bits >> 20) & 1u)) & 0xFFF00000u;
-        if (bits < 0x0D800000u)                          // 2^-100
-            bits = 0u;
-        // 1 / scale, less 2^-14 of it: a quotient that lies between two whole
-        // numbers goes toward zero, any other is 2^-10 away from such a tie at least
-        // (eight bits over four)
-        const float per = bits == 0u ? 0.0f : __fmul_rn(__frcp_rn(__uint_as_float(bits)), 1.0f - 0x1p-14f);
-        // 1.5 * 2^23 + 8: the sum's unit is 1, so its bits are those of 1.5 * 2^23 plus
-        // 8 + the whole number; what 16 times and add leaves of the former is taken off
-        constexpr uint32_t kOnes = 0x11111111u * 0x4B400000u;
-        uint32_t word[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t sum = 0u;
-#pragma unroll
-            for (int e = 3; e >= 0; --e) {
-                float lo = bf16_lo(w[4 * j + e]), hi = bf16_hi(w[4 * j + e]);
-                fma2_rn(lo, hi, per, per, 12582920.0f, 12582920.0f);
-                sum = sum * 16u + __float_as_uint(hi);
-                sum = sum * 16u + __float_as_uint(lo);
-            }
-            word[j] = sum - kOnes;
-        }
-        // the row's four scales in one lane
-        const uint32_t two = (bits >> 16) | (__shfl_down_sync(0xFFFFFFFFu, bits, 1) & 0xFFFF0000u);
-        const uint32_t far = __shfl_down_sync(0xFFFFFFFFu, two, 2);
-        if (slot[i] < 0)
-            continue;
-        if (slot[i] >= a.capacity) {
-            if (q == 0 && head[i] == 0 && a.err != nullptr)
-                atomicAdd(a.err, 1);
-            continue;
-        }
-        const uint32_t s = (uint32_t)slot[i], blk = s / (uint32_t)a.block_size;      // capacity < 2^31
-        const int64_t row = ((int64_t)blk * a.heads + head[i]) * a.block_size + (s - blk * (uint32_t)a.block_size);
-        reinterpret_cast<uint4 *>(a.cache4)[row * kGroups + q] = make_uint4(word[0], word[1], word[2], word[3]);
-        if (q == 0) {
-            *reinterpret_cast<uint2 *>(a.scales + row * kKv4Scales) = make_uint2(two, far);
-            if (((odd >> (threadIdx.x & 28)) & 15u) != 0u && a.err != nullptr)
-                atomicAdd(a.err, 1);
-        }
+        word[j] = sum - kOnes;
+    }
+    // the row's four scales in one lane
+    const uint32_t two = (bits >> 16) | (__shfl_down_sync(0xFFFFFFFFu, bits, 1) & 0xFFFF0000u);
+    const uint32_t far = __shfl_down_sync(0xFFFFFFFFu, two, 2);
+    if (slot < 0)
+        return;
+    if (slot >= a.capacity) {
+        if (q == 0 && head == 0 && a.err != nullptr)
+            atomicAdd(a.err, 1);
+        return;
+    }
+    const uint32_t s = (uint32_t)slot, blk = s / (uint32_t)a.block_size;         // capacity < 2^31
+    const int64_t row = ((int64_t)blk * a.heads + head) * a.block_size + (s - blk * (uint32_t)a.block_size);
+    reinterpret_cast<uint4 *>(a.cache4)[row * kGroups + q] = make_uint4(word[0], word[1], word[2], word[3]);
+    if (q == 0) {
+        *reinterpret_cast<uint2 *>(a.scales + row * kKv4Scales) = make_uint2(two, far);
+        if (((odd >> (threadIdx.x & 28)) & 15u) != 0u && a.err != nullptr)
+            atomicAdd(a.err, 1);
     }
 }
 
@@ -197,29 +182,29 @@ k9_load(const __grid_constant__ Kv4LoadLaunch a)
     }
 }
 
-// Several rows a thread where they fill the GPU; else one, for latency.
-template <int kMany, typename Launch>
-cudaError_t launch_rows(void (*one)(Launch), void (*many)(Launch), int lanes, const Launch &a, int num_sms, cudaStream_t stream)
+// Four rows a thread where they fill the GPU; else one, for latency.
+template <bool kWhole> cudaError_t launch_load(const Kv4LoadLaunch &a, int num_sms, cudaStream_t stream)
 {
-    const int rows = kThreads / lanes;
+    constexpr int kRows = kThreads / kLanes, kMany = 4;
     const int64_t items = a.T * a.heads;
-    const bool more = items >= (int64_t)num_sms * 8 * rows * kMany;
-    const int64_t per = rows * (more ? kMany : 1);
-    return launch_pdl(more ? many : one, dim3((unsigned)((items + per - 1) / per)), dim3(kThreads), 0, stream, 1, a);
+    const bool more = items >= (int64_t)num_sms * 8 * kRows * kMany;
+    const int64_t per = kRows * (more ? kMany : 1);
+    return launch_pdl(more ? k9_load<kMany, kWhole> : k9_load<1, kWhole>, dim3((unsigned)((items + per - 1) / per)), dim3(kThreads), 0,
+                      stream, 1, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_store(const Kv4StoreLaunch &a, int num_sms, cudaStream_t stream)
+cudaError_t launch_kv4_store(const Kv4StoreLaunch &a, cudaStream_t stream)
 {
-    return launch_rows<1>(k9_store<1>, k9_store<1>, kGroups, a, num_sms, stream);
+    constexpr int kRows = kThreads / kGroups;
+    return launch_pdl(k9_store, dim3((unsigned)((a.T * a.heads + kRows - 1) / kRows)), dim3(kThreads), 0, stream, 1, a);
 }
 
 cudaError_t launch_kv4_load(const Kv4LoadLaunch &a, int num_sms, cudaStream_t stream)
 {
-    if (reinterpret_cast<uintptr_t>(a.out) % 32 != 0)
-        return launch_rows<4>(k9_load<1, false>, k9_load<4, false>, kLanes, a, num_sms, stream);
-    return launch_rows<4>(k9_load<1, true>, k9_load<4, true>, kLanes, a, num_sms, stream);
+    return reinterpret_cast<uintptr_t>(a.out) % 32 != 0 ? launch_load<false>(a, num_sms, stream)
+                                                        : launch_load<true>(a, num_sms, stream);
 }
 
 }  // namespace rc

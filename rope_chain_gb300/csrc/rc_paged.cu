@@ -296,10 +296,7 @@ rc_status rc_kv4_store(const uint16_t *k, int64_t k_row_stride, int64_t k_head_s
     a.heads = num_kv_heads;
     a.block_size = block_size;
     a.err = err;
-    const int sms = num_sms_current();
-    if (sms <= 0)
-        return fail(RC_ERR_CUDA, "%s: no current CUDA device", fn);
-    const cudaError_t e = launch_kv4_store(a, sms, stream);
+    const cudaError_t e = launch_kv4_store(a, stream);
     return e == cudaSuccess ? ok() : cuda_fail(e, "rc_kv4_store launch");
 }
 

@@ -67,7 +67,7 @@ struct Kv4LoadLaunch {
     uint16_t *out;                   // bf16 [T, heads, 128]
     int32_t *err;
 };
-cudaError_t launch_kv4_store(const Kv4StoreLaunch &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv4_store(const Kv4StoreLaunch &a, cudaStream_t stream);
 cudaError_t launch_kv4_load(const Kv4LoadLaunch &a, int num_sms, cudaStream_t stream);
 
 // Accepted nodes' rows moved to follow the context.
