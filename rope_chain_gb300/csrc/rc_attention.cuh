@@ -12,12 +12,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kKeyTile = 128;          // keys per step of a CTA
+// Fewest key tiles a CTA is given (3 trees of 13 over 1500 keys, in equal ranges: 15.3 us
+// with two, 19.9 with four, 18.3 with one).
+constexpr int32_t kMinTiles = 2;
 constexpr float kGrow = 8.0f;          // log2: growth of a row's maximum at which its output is rescaled
 
 struct Args : TreeAttentionLaunch {
     float scale_log2;                  // scale * log2 e
     float grow;                        // kGrow / scale_log2: in scores before that factor
-    int32_t min_tiles;                 // fewest key tiles a CTA is given
     bool whole;                        // units are not cut
     int32_t change;                    // going to another unit, in key tiles' time
     int32_t join;                      // and joining parts; 0: units are cut in any case
@@ -114,7 +116,7 @@ __device__ __forceinline__ int32_t most_of(const Args &a, int64_t tiles, int64_t
     if (units >= ctas)
         return 0;
     const int32_t room = ctas - (int32_t)units;
-    const int64_t most = max((int64_t)a.min_tiles, quotient(tiles + room - 1, room));
+    const int64_t most = max((int64_t)kMinTiles, quotient(tiles + room - 1, room));
     return most <= a.change + 2 || most * ctas <= tiles + a.change * units ? (int32_t)min(most, (int64_t)INT32_MAX) : 0;
 }
 
@@ -199,7 +201,7 @@ __device__ Place locate(const Args &a, int c, int ctas) {
             p.total += warp_sum[w];
         }
     }
-    p.used = (int32_t)max((int64_t)1, min((int64_t)ctas, p.most > 0 ? p.total : quotient(p.total, a.min_tiles)));
+    p.used = (int32_t)max((int64_t)1, min((int64_t)ctas, p.most > 0 ? p.total : quotient(p.total, kMinTiles)));
     p.each = quotient(p.total, p.used);
     p.rest = (int32_t)(p.total - p.each * p.used);               // rest * c < used^2 < 2^32
     p.lo = c < p.used ? p.begin_of(c) : p.total;
@@ -567,13 +569,10 @@ cudaError_t launch_join(const Args &a, int ctas, cudaStream_t stream, const char
                       stream, 1, a);
 }
 
-// How a call is cut (Args' min_tiles, whole, change, partial), for units of
+// How a call is cut (Args' whole, change, join, partial), for units of
 // `unit_rows` rows and at most `most` CTAs at once; returns the CTAs.
 inline int plan(Args &a, int64_t unit_rows, bool wide, int most)
 {
-    // (3 trees of 13 over 1500 keys, in equal ranges: 15.3 us with two tiles a CTA at
-    // least, 19.9 with four, 18.3 with one)
-    a.min_tiles = 2;
     const int64_t units = (a.rows * a.group / unit_rows + a.seqs) * a.kv_heads;      // at most
     // The key tiles of a unit that the block table, and the window, let be: that of
     // the first keys, those of the window, which may begin and end inside one, and of
@@ -596,7 +595,7 @@ inline int plan(Args &a, int64_t unit_rows, bool wide, int most)
     }
     // as many CTAs as fill the GPU, or as the block table lets have work
     const int64_t tiles = std::max<int64_t>(1, (keys + kKeyTile - 1) / kKeyTile);
-    const int ctas = (int)std::min<int64_t>(most, std::max<int64_t>(1, a.whole ? units : units * tiles / a.min_tiles));
+    const int ctas = (int)std::min<int64_t>(most, std::max<int64_t>(1, a.whole ? units : units * tiles / kMinTiles));
     // A CTA that goes from one unit to another loses some 10 us while the cache is
     // streamed, six key tiles' time; counted as such, 64 sequences of 1025 to 2050
     // keys take 43 us instead of 46, 16 trees of 16 over 8192 71.2, 74.5.  In
