@@ -84,14 +84,15 @@ template <int kLeft> __device__ __forceinline__ void copy_wait() {
 // kShared: the chunks come through a ring in shared memory instead.  With two row tiles
 // that leaves the registers for two blocks an SM (32 trees of 2 over 4000 to 8000 keys: 52
 // us for 58); with one it is better over long contexts (64 tokens over 4100 to 8200 keys:
-// 74 for 77), not over short ones (256 tokens over 350 to 700: 56 for 52).  There a
+// 74 for 77), not over short ones (256 tokens over 350 to 700: 56 for 52; 64 tokens over a
+// window of 512 of 8192 keys 29.5 for 22.4, of 2048 39.2 for 40.3).  There a
 // chunk is the K of its rows, 32 bytes each; their V, the rows in the
 // order 0 2 4 6 1 3 5 7, so that what a warp reads at once lies in all banks; their
 // scales.
 constexpr int kRing = 4;               // stages
 constexpr uint32_t kChunkV = 512, kChunkScales = 1024, kChunkBytes = 1024 + 128;
 template <bool kShared> constexpr uint32_t kSmem = kShared ? kWarps * kRing * kChunkBytes : 0;
-constexpr int64_t kLongContext = 2048; // keys that a block table must have room for
+constexpr int64_t kLongContext = 2048; // keys that the block table and the window must let be
 
 // Chunks in flight beside the one that is worked on (64 tokens over 4100 to 8200 keys: 82
 // us with two, 78 with three), and CTAs on an SM (three, at 80 registers a thread: 93 us).
@@ -534,7 +535,7 @@ cudaError_t launch_variant(Variant v, const Args &a, int ctas, cudaStream_t stre
 {
     switch (v) {
     case kRows8:
-        return (int64_t)a.table_width * a.block_size >= kLongContext
+        return most_keys(a) >= kLongContext
                    ? launch_tiles<1, true, kRuns, kWindow>(a, ctas, stream, why)
                    : launch_tiles<1, false, kRuns, kWindow>(a, ctas, stream, why);
     case kRows16: return launch_tiles<2, true, kRuns, kWindow>(a, ctas, stream, why);

@@ -569,19 +569,24 @@ cudaError_t launch_join(const Args &a, int ctas, cudaStream_t stream, const char
                       stream, 1, a);
 }
 
+// The keys of a unit that the block table, and the window, let be, at most: that of the
+// first keys, those of the window, which may begin and end inside a tile, and of the
+// nodes, of which a mask names so many (an estimate: others cost time only).
+inline int64_t most_keys(const TreeAttentionLaunch &a)
+{
+    const int64_t keys = (int64_t)a.table_width * a.block_size;
+    if (a.window == 0)
+        return keys;
+    const int64_t nodes = a.tree_mask != nullptr ? std::min<int64_t>(a.rows, 64 * (int64_t)a.mask_words) : a.rows;
+    return std::min<int64_t>(keys, (((int64_t)a.sinks + kKeyTile - 1) / kKeyTile + 1) * kKeyTile + a.window + nodes);
+}
+
 // How a call is cut (Args' whole, change, join, partial), for units of
 // `unit_rows` rows and at most `most` CTAs at once; returns the CTAs.
 inline int plan(Args &a, int64_t unit_rows, bool wide, int most)
 {
     const int64_t units = (a.rows * a.group / unit_rows + a.seqs) * a.kv_heads;      // at most
-    // The key tiles of a unit that the block table, and the window, let be: that of
-    // the first keys, those of the window, which may begin and end inside one, and of
-    // the nodes, of which a mask names so many (an estimate: others cost time only).
-    int64_t keys = (int64_t)a.table_width * a.block_size;
-    if (a.window > 0) {
-        const int64_t nodes = a.tree_mask != nullptr ? std::min<int64_t>(a.rows, 64 * (int64_t)a.mask_words) : a.rows;
-        keys = std::min<int64_t>(keys, (((int64_t)a.sinks + kKeyTile - 1) / kKeyTile + 1) * kKeyTile + a.window + nodes);
-    }
+    const int64_t keys = most_keys(a);
     // Units of at most so many tiles are not worth a cut and a join: one token over
     // 300 keys 6.9 us (cut 11.2), 30 single tokens over 450 to 900 15.0 (19.2); a
     // tile of many rows takes longer, 16 trees of 16 over 480 15.7 (23.2), but 3 of
