@@ -495,9 +495,14 @@ k11_attention(const __grid_constant__ Args a)
 
 // By the average rows of a unit; any kernel is right for any unit.  From 33 rows on
 // the products are the bound, and k5_wide takes the call (blocks of a multiple of 8
-// keys; other block sizes stay here): 16 trees of 16 over a window of 6000 keys, 128 rows
-// a unit, 79 us, in tiles of 32 rows here 170; at 32 rows (16 trees of 4 over 4000 to 8000
-// keys) 47 here.
+// keys; other block sizes stay here).  8 sequences over 4096 keys, and 32, us:
+//   up to 8 rows    one tile: 14.4 and 31.8 at 8 rows, two tiles 16.6 and 39.5; at 16 17.2 and 42.9
+//   up to 16        two: 17.3 and 40.9 at 16, four 23.1 and 60.2
+//   up to 32        four: 25.1 and 64.0 at 32, two 25.9 and 70.0, k5_wide<1> 31.4 and 88.0; at
+//                   24 23.9 and 62.1, two 21.9 and 55.0
+//   up to 128       k5_wide<1>: 31.5 and 87.8 at 40 rows, four 31.2 and 89.7; at 128 33.8 and
+//                   90.3, k5_wide<2> 39.0 and 120
+//   beyond          k5_wide<2>: 40.0 and 122 at 160, k5_wide<1> 50.1 and 160
 enum Variant { kRows8, kRows16, kRows32, kRows128, kRows256 };
 Variant variant_for(int64_t rows, int32_t seqs, int32_t group, int32_t block_size) {
     const int64_t mean = (rows + seqs - 1) / seqs * group;

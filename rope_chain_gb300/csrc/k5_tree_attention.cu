@@ -477,13 +477,13 @@ k5_small(const __grid_constant__ Args a)
 // cycle), the products as many at full rate; products of 64 columns (O) run at
 // about half of it, 1536 in all.
 // Measured: 8 trees of 64 tokens over 32768 keys (64 query and 8 KV heads, 273
-// GFLOP) 290 to 307 us by the box, 0.89 to 0.94 PFLOP/s, 2700 cycles per 256 x 128
-// (in blocks of 16 keys; 273 us in blocks of 128): the steps of the two row tiles,
-// products, softmax and weights, one after the other; tensor pipe 42 %, issue slots
-// 60 %.  16 trees of 16 over 8192 keys (273 MB) 71 us, 3.8 TB/s: 44 us at 6.2 TB/s
+// GFLOP) 274 us, 1.0 PFLOP/s, some 2500 cycles per 256 x 128
+// (in blocks of 16 keys; 264 us in blocks of 128): the steps of the two row tiles,
+// products, softmax and weights, one after the other; tensor pipe 43 %, issue slots
+// 64 %.  16 trees of 16 over 8192 keys (273 MB) 69.5 us, 3.9 TB/s: 44 us at 6.2 TB/s
 // between a start of 9 us (launch, lengths, Q, first tile) and changes of unit and
-// the join of 18.  Two CTAs an SM leave kQ = 1 96 registers a thread, of which it
-// spills 51 (204 bytes stored, 572 loaded); kQ = 2 spills three.
+// the join of 17.  Two CTAs an SM leave kQ = 1 96 registers a thread, of which it
+// spills 51 (204 bytes stored, 676 loaded; with a window one); kQ = 2 spills one.
 // Key tiles that hold drafted keys, the end, or a window's begin, take a masked path; there the
 // V rows past the end are zeroed and what is infinite or NaN in a drafted one
 // is taken out (see add_unfinite).  Every wait is bounded; on timeout a sticky
@@ -494,17 +494,18 @@ enum : unsigned { kFaultLoad = 1u, kFaultMma = 2u, kFaultSoftmax = 4u, kFaultDra
 constexpr uint32_t kTileBytes = kKeyTile * kHeadDim * 2;           // K or V of a step, Q of a tile: 16 KiB
 template <int kQ> constexpr int kSoftmaxWarps = 8 * kQ;
 // A warp's boxes are issued one by one, at some 130 cycles each.  With two row
-// tiles one warp loads K and another V: 293 us instead of 323 for 8 trees of 64
-// tokens over 32768 keys (512 rows a KV head, blocks of 16).  With one row tile a
-// single warp loads both, as an eleventh warp would cost the SM its second CTA:
-// 16 trees of 16 over 8192 keys take 73 us, with two loaders 84.
+// tiles one warp loads K and another V: 274 us instead of 323 for 8 trees of 64
+// tokens over 32768 keys (512 rows a KV head, blocks of 16; of 128 264 either way).
+// With one row tile a single warp loads both, as an eleventh warp would leave 88
+// registers a thread for two CTAs an SM: 16 trees of 16 over 8192 keys take 70 us,
+// with two loaders 76.
 //
 // kFour: over a cache in 4 bits the loaders make bf16 numbers of the rows in shared
 // memory, in place of the boxes: 32 elements and their scale to a lane.  That is some
 // 1000 instructions a tile, more than one warp (or two for two row tiles) issues beside
 // the softmax: 16 trees of 16 over a window of 6000 keys 103 us with one loader, with two
 // 79, with three, as many as fit at 80 registers a thread, 68; 8 trees of 64 over 32768
-// keys 538 with two, with four 380 (bf16: 69 and 278).  The loaders cost the softmax warps
+// keys 538 with two, with four 380 (bf16: 65 and 274).  The loaders cost the softmax warps
 // registers, 80 a thread instead of 96.  A branch between a loader's boxes keeps it from
 // working on several at once: 380 us would be 460.
 constexpr int kTileBoxes = 16;         // of eight keys
@@ -517,9 +518,10 @@ template <int kQ> constexpr size_t kWideSmem = kQ * kTileBytes + kWideStages<kQ>
 
 // Keeps x in local memory: what is read at a piece's ends only would otherwise
 // crowd the scores out of the registers.  Used with two row tiles (8 trees of 64
-// tokens over 32768 keys in blocks of 128: 273 us, without 291; in blocks of 16,
-// where the loads bound, 293 either way), not with one (16 trees of 16 over 8192
-// keys: 73 us, with it 76).
+// tokens over 32768 keys: 274 us, without 288; in blocks of 128 265 and 288), with a
+// window (8 trees of 64 over one of 8192 98 and 100 us, with one row tile 64 and 63) and
+// in 4 bits, not with one row tile over bf16 (16 trees of 16 over 8192 keys: 69.7 us,
+// with it 70.4).
 template <typename T> __device__ __forceinline__ void in_memory(T &x) { asm volatile("" ::"l"(&x) : "memory"); }
 
 // The slow half of a wait: up to kWaitNs from its first look at the timer, or
@@ -755,7 +757,7 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
         // done twice, as a branch around them would part their arithmetic).  Lane 4r + q has key r of a box
         // and of its 64 bytes the q-th 16, K's two halves and V's two: a group of 32
         // elements with one scale.  A box's registers are loaded again, for the next
-        // kGroup boxes, as soon as they are used.  In a word the elements come apart as
+        // kOwn boxes, as soon as they are used.  In a word the elements come apart as
         // (i, i + 4): the heads' elements are in that order in shared memory, Q's too, and
         // O's columns are put back at the end.  V's lanes take their words in the order
         // 2 3 0 1, so that the eight lanes of a store's phase write to all banks.
@@ -1242,12 +1244,12 @@ k5_wide(const __grid_constant__ CUtensorMap map, const __grid_constant__ Args a,
 // Which kernel takes a call, by the average rows of a unit (only the totals are
 // known on the host; any kernel is right for any unit).  8 sequences over 4096
 // keys, us:
-//   up to 16 rows   k5_small<1>: 21.2 at 16 rows, k5_small<2> 23.5
-//   up to 32        k5_small<2>: 26.5 at 32, k5_wide<1> 29.6; at 40 31.3 and 29.5
-//   up to 128       k5_wide<1>: 32.5 at 128, k5_wide<2> 38.5; at 160 44.1 and 40.1
-//   beyond          k5_wide<2>: two row tiles share each key tile
-// Batches that mix them: 63 single tokens and a tree of 64 over 2000 keys 57 us (64
-// single tokens 51, the tree alone 25).
+//   up to 16 rows   k5_small<1>: 16.8 at 16 rows, k5_small<2> 20.3
+//   up to 32        k5_small<2>: 23.0 at 32, k5_wide<1> 25.3; at 40 28.5 and 25.6
+//   up to 128       k5_wide<1>: 28.7 at 128, k5_wide<2> 35.1; at 160 39.9 and 36.3
+//   beyond          k5_wide<2>
+// Batches that mix them: 63 single tokens and a tree of 64 over 2000 keys 56 us (64
+// single tokens 51, the tree alone 24).
 // The wide kernel's TMA boxes need blocks of a multiple of 8 keys; other block
 // sizes stay with k5_small<2>.
 enum Variant { kSmall16, kSmall32, kWide128, kWide256 };

@@ -11,9 +11,9 @@
 // there the work of an element must stay small, so a lane takes 16 bytes or two times
 // 16 of a head, up to eight heads one after another, whose table columns and weights it
 // loads once, and FP32 arithmetic goes in pairs.  Measured, 16384 tokens of 32 + 8 heads
-// of 128: bf16 halves 53 us forward (6.4 TB/s) and 85 backward (5.9), pairs 53 and 85,
+// of 128: bf16 halves 53 us forward (6.4 TB/s) and 86 backward (5.9), pairs 53 and 86,
 // FP32 halves 100 and 155; one head at a time straight into registers 67 and 107.
-// Heads of 96 leave four lanes of 16 idle (49 and 88 us for 40 of them).
+// Heads of 96 leave four lanes of 16 idle (49 and 90 us for 40 of them).
 #include "rc_paged.cuh"
 #include "rc_tcgen05.cuh"
 
